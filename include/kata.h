@@ -268,6 +268,123 @@ kata_status kata_bwd_chunked(const kata_problem* pr, const void* q, const void* 
                              const void* v, const void* dO, void* dq, void* dk, void* dv,
                              void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- Linear attention with one decay per head --------------------------------------------
+ * Causal, without a denominator; per head h with decay g = exp(log_decay[h]) and per sequence
+ *     S_t = g S_{t-1} + k_t v_t^T  (dk x dv),     o_t = scale q_t S_t,
+ * S_{-1} being the initial state (zero where none is given).  Chunks of 64 tokens run on MFMA
+ * (fp32 problems on the fp32 MFMA); every sum and the state are fp32.  bf16 problems round the
+ * weights of the pairs and the state to bf16 where they are operands of a product; the terms of
+ * a final state (or of the gradient of the initial state) that is asked for are not rounded.
+ * A row reaches only what the recurrence lets it reach, infinities and NaN included.
+ *
+ *   n_seq, T: packed == 0: n_seq sequences of T tokens, tensors [n_seq][T][H][width].
+ *          packed == 1: the sequences lie one behind the other in T rows, tensors
+ *          [1][T][H][width]; sequence i is the rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (device
+ *          int32 [n_seq + 1], ascending, within [0, T]; values outside are clamped, so that no
+ *          content is read or written out of bounds).  A sequence may be empty: its final state
+ *          is its initial state.
+ *   H, dk, dv: heads, width of q and k, width of v: at most 128, rows of whole 16 bytes.
+ *   zero_tail: packed: 0 leaves the output rows behind cu_seqlens[n_seq] as they are, 1 zeroes
+ *          them.
+ *   dtype: of q, k, v, o, dO and the gradients.  States are fp32 [n_seq][H][dk][dv], contiguous.
+ *   log_decay: device fp32 [H], any value; -inf is a decay of zero.  It has no gradient.
+ *   sq, sk, sv, so, sdo: element strides of (b, t, h); those of an input may be zero (a broadcast
+ *          axis).  Rows are 16-byte aligned.  An output overlaps no input and no other output. */
+typedef struct {
+  int32_t n_seq, H, T, dk, dv;
+  int32_t packed;
+  int32_t zero_tail;
+  int32_t dtype;
+  float scale;
+  int64_t sq[3], sk[3], sv[3], so[3], sdo[3];
+} kata_decay_problem;
+
+/* Bytes of device workspace kata_fwd_decay needs (0: none, or an invalid problem). */
+size_t kata_fwd_decay_workspace_size(const kata_decay_problem* pr);
+
+/* Chunked forward.  initial_state, final_state: nullable; they may be the same array.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE (256-byte aligned), DEVICE. */
+kata_status kata_fwd_decay(const kata_decay_problem* pr, const void* q, const void* k,
+                           const void* v, const float* log_decay, const int32_t* cu_seqlens,
+                           const float* initial_state, void* o, float* final_state,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+size_t kata_bwd_decay_workspace_size(const kata_decay_problem* pr);
+
+/* Gradients of sum(dO * o) + sum(dfinal_state * final_state) in q, k, v and, where dinitial_state
+ * is not NULL, the initial state:
+ *     dq_t = scale (g^(t+1) S_{-1} dO_t + sum_{s<=t} g^(t-s) (dO_t . v_s) k_s)
+ *     dk_s = g^(T-1-s) dS v_s + scale sum_{t>=s} g^(t-s) (dO_t . v_s) q_t
+ *     dv_s = g^(T-1-s) dS^T k_s + scale sum_{t>=s} g^(t-s) (q_t . k_s) dO_t
+ *     dS_{-1} = g^T dS + scale sum_t g^(t+1) q_t dO_t^T
+ * initial_state and dfinal_state: nullable (zero).  dq, dk, dv: contiguous [B][T][H][width] of
+ * the problem's dtype. */
+kata_status kata_bwd_decay(const kata_decay_problem* pr, const void* q, const void* k,
+                           const void* v, const void* dO, const float* log_decay,
+                           const int32_t* cu_seqlens, const float* initial_state,
+                           const float* dfinal_state, void* dq, void* dk, void* dv,
+                           float* dinitial_state, void* workspace, size_t ws_bytes, void* stream);
+
+/* Recurrent form: advances state [n_seq][H][dk][dv], in place, over the T tokens one at a time
+ * (T = 1 is one decode step) in fp32 and writes o.  packed must be 0.  Calls that share a state
+ * must be ordered on one stream. */
+kata_status kata_decode_decay(const kata_decay_problem* pr, const void* q, const void* k,
+                              const void* v, const float* log_decay, float* state, void* o,
+                              void* stream);
+
+/* ---- Rotary positions ----------------------------------------------------------------------
+ * The first `rot` coordinates of every head form rot / 2 pairs (a, b): coordinates (i, i + rot / 2),
+ * or with interleaved (2 i, 2 i + 1).  At position x pair i becomes
+ *     m (a cos(x r_i) - b sin(x r_i)),  m (a sin(x r_i) + b cos(x r_i)),
+ * with the angle negated where inverse is set (the gradient); coordinates from rot on are copied.
+ * Angles are formed in fp64, so far positions keep their phase.
+ *   q [B][T][H][D] and, unless Hk = 0, k [B][T][Hk][D], the last axis contiguous; D <= 1024, rot
+ *   even.  Rows of whole, aligned 16-byte vectors (in the half layout rot / 2 too) take 16-byte
+ *   accesses, others go element by element.  An output may be its own input (in place) but must
+ *   not overlap inputs otherwise.
+ *   rates: device fp64 [rot / 2], radians a token.  magnitude: m.
+ *   positions: device int32 or (pos64) int64 with element strides pos_b, pos_t (zero: broadcast), or
+ *   NULL: token t has position offset + t. */
+typedef struct {
+  int32_t B, T, H, Hk, D, rot;
+  int32_t dtype;
+  int32_t interleaved, inverse;
+  int32_t pos64;
+  float magnitude;
+  int64_t pos_b, pos_t, offset;
+  int64_t sq[3], sk[3], soq[3], sok[3];
+} kata_rotary_problem;
+
+kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void* k,
+                        const double* rates, const void* positions, void* out_q, void* out_k,
+                        void* stream);
+
+/* ---- Layer norm ----------------------------------------------------------------------------
+ *     hat = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  y = hat weight + bias
+ * over rows of N elements, rows sx (sdy, sy, sdx) elements apart, statistics and sums in fp32.
+ * weight, bias: [N] of w_dtype (fp32, or bf16 with bf16 rows), nullable: ones, zeros. */
+typedef struct {
+  int64_t rows;
+  int32_t N;
+  int32_t dtype, w_dtype;
+  float eps;
+  int64_t sx, sdy, sy, sdx;
+} kata_norm_problem;
+
+/* mean, rstd: fp32 [rows] for the backward pass, or both NULL.  y may be x. */
+kata_status kata_fwd_layer_norm(const kata_norm_problem* pr, const void* x, const void* weight,
+                                const void* bias, void* y, float* mean, float* rstd, void* stream);
+
+size_t kata_bwd_layer_norm_workspace_size(const kata_norm_problem* pr);
+
+/* Gradients of sum(dy * y): dx, and dweight, dbias [N] of w_dtype summed over the rows in a fixed
+ * order.  Each of the three is nullable; without dweight and dbias no workspace is needed.
+ * dx may be dy. */
+kata_status kata_bwd_layer_norm(const kata_norm_problem* pr, const void* dy, const void* x,
+                                const void* weight, const float* mean, const float* rstd, void* dx,
+                                void* dweight, void* dbias, void* workspace, size_t ws_bytes,
+                                void* stream);
+
 /* Static text for a status code. */
 const char* kata_status_string(kata_status s);
 

@@ -14,6 +14,12 @@ path: if libkata.so is missing, or a call fails, an exception is raised.
     state = recurrent_state(k, v)               # (S, Z) after the given tokens (prefill)
     o = decode(q, k, v, state)                  # advance the state token by token
 
+and the parts of a layer without the denominator (layer.py):
+
+    o = parallel_decay_attn(q, k, v, log_decay) # linear attention with one decay per head
+    q, k = rotary(q, k, rates)                  # rotary positions
+    y = layer_norm(x, weight, bias)
+
 q, k: (B, T, H, p); v: (B, T, H, dv) -- the layout of the pages' kernel call -- with the last
 dimension contiguous; any (b, t, h) strides that keep rows 16-byte aligned are accepted
 (e.g. a head-major (B, H, T, D) tensor passed as .transpose(1, 2)).
@@ -30,6 +36,9 @@ __all__ = [
     "chunk_state_scan", "scan_workspace_size", "bwd", "bwd_workspace_size",
     "recurrent_state", "recurrent_state_workspace_size", "decode", "state_shape",
     "timing_begin", "timing_end", "library_path", "KERNEL_KINDS",
+    "fwd_decay", "bwd_decay", "decode_decay", "decay_state_shape", "decay_workspace_size",
+    "parallel_decay_attn", "rotary_rates", "rotary", "layer_norm", "fwd_layer_norm",
+    "bwd_layer_norm", "layer_norm_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -104,6 +113,7 @@ def _lib():
             "kata_last_error": (ctypes.c_char_p, []),
             "kata_timing_begin": (I32, []),
             "kata_timing_end": (I32, [ctypes.POINTER(_Times)]),
+            **layer._signatures(),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -384,7 +394,8 @@ class _KataAttn(torch.autograd.Function):
         return dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), None, None, None, None
 
 
-def parallel_kata_attn(q, k, v, num_groups=1, form="auto", chunk=64, eps=1e-6):
+def parallel_kata_attn(q, k, v, num_groups=1, form="auto", chunk=64, eps=1e-6, rotary=None,
+                       positions=None, interleaved=False):
     """Causal KATA attention as a differentiable op: (B, T, H, D) -> (B, T, H, d_v), the
     output in the inputs' dtype, named and laid out like the KATA README's kernel call
     (num_groups: the KATA-Mg factor count g).
@@ -392,7 +403,11 @@ def parallel_kata_attn(q, k, v, num_groups=1, form="auto", chunk=64, eps=1e-6):
     form: "chunked" (exact O(T) chunked-state forward; T a multiple of chunk), "quadratic"
     (flash-style O(T^2)), or "auto" (chunked where T is a multiple of chunk, else quadratic).
     Under autograd the backward runs bwd (chunked where T is a multiple of chunk, else flash);
-    its fp32 gradients are handed back in the inputs' dtype."""
+    its fp32 gradients are handed back in the inputs' dtype.
+    rotary: (rates, magnitude) of rotary_rates: q and k are turned by their positions first (see
+    rotary(); positions and interleaved are its arguments)."""
+    if rotary is not None:
+        q, k = layer.turn(q, k, rotary, positions, 0, interleaved)
     if form == "auto":
         form = "chunked" if q.shape[1] % chunk == 0 else "quadratic"
     if form not in ("chunked", "quadratic"):
@@ -409,3 +424,9 @@ def timing_end():
     t = _Times()
     _check(_lib().kata_timing_end(ctypes.byref(t)), "kata_timing_end")
     return {name: (int(t.launches[i]), float(t.total_ms[i])) for i, name in enumerate(KERNEL_KINDS)}
+
+
+from . import layer  # noqa: E402  (needs the helpers above)
+from .layer import (  # noqa: E402
+    bwd_decay, bwd_layer_norm, decay_state_shape, decay_workspace_size, decode_decay, fwd_decay,
+    fwd_layer_norm, layer_norm, layer_norm_workspace_size, parallel_decay_attn, rotary, rotary_rates)

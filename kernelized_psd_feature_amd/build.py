@@ -21,7 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkata.so")
 
 SOURCES = ["kata_api.cpp", "plan.cpp", "generic.hip", "scan.hip", "bwd.hip", "fast.hip", "fast32.hip",
-           "quadratic.hip", "decode.hip", "bwd_chunked.hip"]
+           "quadratic.hip", "decode.hip", "bwd_chunked.hip", "decay.hip", "rotary.hip",
+           "layer_norm.hip", "layer_plan.cpp", "layer_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -11,6 +11,7 @@
 #include <string>
 #include <vector>
 
+#include "api.h"
 #include "device.h"
 #include "kata.h"
 #include "plan.h"
@@ -47,17 +48,30 @@ using kata::Form;
 
 thread_local std::string g_last_error;
 
-kata_status set_error(kata_status s, const std::string& why) {
+}  // namespace
+
+kata_status kata::set_error(kata_status s, const std::string& why) {
   g_last_error = why;
   return s;
 }
+
+void kata::clear_error(void) { g_last_error.clear(); }
+
+namespace {
+
+using kata::check_device;
+using kata::launch_status;
+using kata::set_error;
+using kata::Timed;
 
 // ---- device check: the code objects in this library are built for gfx950 only ----------
 constexpr int kMaxDevices = 64;
 std::mutex g_dev_mutex;
 int g_dev_state[kMaxDevices];   // 0 unknown, 1 gfx950, -1 other
 
-kata_status check_device(void) {
+}  // namespace
+
+kata_status kata::check_device(void) {
   int dev = -1;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess || dev < 0 || dev >= kMaxDevices)
@@ -76,6 +90,8 @@ kata_status check_device(void) {
   if (g_dev_state[dev] < 0) return set_error(KATA_ERR_DEVICE, "device is not a gfx950");
   return KATA_OK;
 }
+
+namespace {
 
 // ---- optional per-kernel timing ----------------------------------------------------
 struct TimingRec {
@@ -103,42 +119,33 @@ thread_local TimingState g_timing;
 // stamp its events with their own dispatch timestamps.
 thread_local kata::LaunchTiming* g_scope = nullptr;
 
-// One timing record per scope when timing is on: the span from the start of the scope's first
-// kernel to the end of its last (no record if it launched nothing).
-struct Timed {
-  int kind;
-  kata::LaunchTiming lt;
-  kata::LaunchTiming* prev = nullptr;
-  bool open = false;
-  Timed(int kind_, hipStream_t) : kind(kind_) {
-    if (!g_timing.on) return;
-    lt.start = g_timing.get();
-    lt.stop = g_timing.get();
-    if (lt.start && lt.stop) {
-      prev = g_scope;
-      g_scope = &lt;
-      open = true;
-    } else {
-      if (lt.start) g_timing.pool.push_back(lt.start);
-      if (lt.stop) g_timing.pool.push_back(lt.stop);
-      lt.start = lt.stop = nullptr;
-    }
-  }
-  ~Timed() {
-    if (!open) return;
-    g_scope = prev;
-    if (lt.used) {
-      g_timing.recs.push_back({kind, lt.start, lt.stop});
-    } else {
-      g_timing.pool.push_back(lt.start);
-      g_timing.pool.push_back(lt.stop);
-    }
-  }
-  Timed(const Timed&) = delete;
-  Timed& operator=(const Timed&) = delete;
-};
-
 }  // namespace
+
+kata::Timed::Timed(int kind_, hipStream_t) : kind(kind_) {
+  if (!g_timing.on) return;
+  lt.start = g_timing.get();
+  lt.stop = g_timing.get();
+  if (lt.start && lt.stop) {
+    prev = g_scope;
+    g_scope = &lt;
+    open = true;
+  } else {
+    if (lt.start) g_timing.pool.push_back(lt.start);
+    if (lt.stop) g_timing.pool.push_back(lt.stop);
+    lt.start = lt.stop = nullptr;
+  }
+}
+
+kata::Timed::~Timed() {
+  if (!open) return;
+  g_scope = prev;
+  if (lt.used) {
+    g_timing.recs.push_back({kind, lt.start, lt.stop});
+  } else {
+    g_timing.pool.push_back(lt.start);
+    g_timing.pool.push_back(lt.stop);
+  }
+}
 
 namespace kata {
 LaunchTiming* launch_timing() { return g_scope; }
@@ -159,6 +166,11 @@ hipError_t ensure_dynamic_lds(const void* kernel, int bytes) {
   e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == hipSuccess) done.push_back({kernel, dev, bytes});
   return e;
+}
+
+kata_status launch_status(hipError_t e, const char* what) {
+  if (e == hipSuccess) return KATA_OK;
+  return set_error(KATA_ERR_DEVICE, std::string(what) + ": " + hipGetErrorString(e));
 }
 }  // namespace kata
 
@@ -185,10 +197,6 @@ kata::DevProblem to_dev(const kata_problem* pr) {
   return d;
 }
 
-kata_status launch_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return KATA_OK;
-  return set_error(KATA_ERR_DEVICE, std::string(what) + ": " + hipGetErrorString(e));
-}
 
 kata_status check_forward_args(const kata_problem* pr, Form f, const void* q, const void* k,
                                const void* v, const void* o, const float* den) {

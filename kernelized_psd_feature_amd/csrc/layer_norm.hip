@@ -1,0 +1,360 @@
+// Layer norm over the last axis, forward and backward, gfx950.
+//
+//   hat = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  y = hat w + b
+//   dx = rstd (t - sum(t) / N - hat sum(t hat) / N),  t = dy w
+//   dw = sum over rows of dy hat,  db = sum over rows of dy
+//
+// A row stays in the registers of R lanes (K vectors of V elements each) between its statistics
+// and its result, so every element is read once and written once; the variance is the second
+// pass over those registers, of differences from the mean.  All sums are fp32.  A workgroup
+// walks over many rows: w and b are read once, and the backward pass keeps its sums of dw and
+// db in registers over its rows, adds them up across its lanes and leaves one partial row pair, which a
+// second kernel adds in block order (no atomics: the same result every time).
+// Bound: HBM.  Rows wider than the widest register form go through the loop kernels, which read
+// a row again for each pass (from the L2 cache where it fits).
+#include "device.h"
+#include "layer.h"
+#include "mfma_util.h"
+
+namespace kata {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(float (&x)[V], const T* p) {
+  if constexpr (V == 1) {
+    x[0] = to_f32(p[0]);
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    if constexpr (sizeof(T) == 2) {
+      x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
+      x[4] = bf_lo(u.z); x[5] = bf_hi(u.z); x[6] = bf_lo(u.w); x[7] = bf_hi(u.w);
+    } else {
+      x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+      x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
+  if constexpr (V == 1) {
+    p[0] = from_f32<T>(x[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(p) = uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                         pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+  } else {
+    *reinterpret_cast<float4*>(p) = float4{x[0], x[1], x[2], x[3]};
+  }
+}
+
+__device__ __forceinline__ float param(const void* p, int bf16, int i, float none) {
+  if (!p) return none;
+  return bf16 ? (float)reinterpret_cast<const __bf16*>(p)[i] : reinterpret_cast<const float*>(p)[i];
+}
+
+// Sum over the R lanes of a row, in every one of them.  R = 256: over the workgroup, through
+// `sh` (4 floats; every thread calls it, twice in a row with two buffers).
+template <int R>
+__device__ __forceinline__ float row_sum(float x, float* sh) {
+#pragma unroll
+  for (int m = (R < 64 ? R : 64) / 2; m >= 1; m >>= 1) x += __shfl_xor(x, m);
+  if constexpr (R == 256) {
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = (sh[0] + sh[1]) + (sh[2] + sh[3]);
+    __syncthreads();
+  }
+  return x;
+}
+
+template <typename T, int V, int R, int K>
+__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs A) {
+  __shared__ float sh[4];
+  constexpr int RPB = kThreads / R;                 // rows at a time
+  const int l = threadIdx.x % R, N = A.N;
+  float w[K][V], b[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int r = 0; r < V; ++r) {
+      const int c = (k * R + l) * V + r;
+      w[k][r] = c < N ? param(A.w, A.w_bf16, c, 1.f) : 0.f;
+      b[k][r] = c < N ? param(A.b, A.w_bf16, c, 0.f) : 0.f;
+    }
+  const float n = (float)N;
+  // R = 256: one row at a time, so all threads leave the loop together
+  for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / R; row < A.rows;
+       row += (long long)gridDim.x * RPB) {
+    const T* px = reinterpret_cast<const T*>(A.x) + row * A.sx;
+    float x[K][V], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * R + l) * V;
+#pragma unroll
+      for (int r = 0; r < V; ++r) x[k][r] = 0.f;
+      if (c < N) load_vec<T, V>(x[k], px + c);
+#pragma unroll
+      for (int r = 0; r < V; ++r) sum += x[k][r];
+    }
+    const float mean = row_sum<R>(sum, sh) / n;   // a division: a constant row has its value as mean
+    float sq = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int r = 0; r < V; ++r) {
+        x[k][r] = (k * R + l) * V < N ? x[k][r] - mean : 0.f;
+        sq = fmaf(x[k][r], x[k][r], sq);
+      }
+    const float rstd = 1.f / sqrtf(row_sum<R>(sq, sh) / n + A.eps);
+    T* py = reinterpret_cast<T*>(A.y) + row * A.sy;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * R + l) * V;
+#pragma unroll
+      for (int r = 0; r < V; ++r) x[k][r] = fmaf(x[k][r] * rstd, w[k][r], b[k][r]);
+      if (c < N) store_vec<T, V>(py + c, x[k]);
+    }
+    if (l == 0 && A.mean) {
+      A.mean[row] = mean;
+      A.rstd[row] = rstd;
+    }
+  }
+}
+
+template <typename T, int V, int R, int K>
+__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs A) {
+  constexpr int RPB = kThreads / R, W = R < 64 ? R : 64;
+  __shared__ float sh[4];
+  __shared__ float cross[R == 256 ? 1 : 4 * W * V];
+  const int tid = threadIdx.x, l = tid % R, N = A.N;
+  float w[K][V], gw[K][V], gb[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int r = 0; r < V; ++r) {
+      const int c = (k * R + l) * V + r;
+      w[k][r] = c < N ? param(A.w, A.w_bf16, c, 1.f) : 0.f;
+      gw[k][r] = gb[k][r] = 0.f;
+    }
+  const float n = (float)N;
+  for (long long row = (long long)blockIdx.x * RPB + tid / R; row < A.rows;
+       row += (long long)gridDim.x * RPB) {
+    const T* px = reinterpret_cast<const T*>(A.x) + row * A.sx;
+    const T* pg = reinterpret_cast<const T*>(A.dy) + row * A.sdy;
+    const float mean = A.mean[row], rstd = A.rstd[row];
+    float hat[K][V], t[K][V], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * R + l) * V;
+#pragma unroll
+      for (int r = 0; r < V; ++r) hat[k][r] = t[k][r] = 0.f;
+      if (c < N) {
+        load_vec<T, V>(hat[k], px + c);
+        load_vec<T, V>(t[k], pg + c);
+#pragma unroll
+        for (int r = 0; r < V; ++r) hat[k][r] = (hat[k][r] - mean) * rstd;
+      }
+#pragma unroll
+      for (int r = 0; r < V; ++r) {
+        gw[k][r] = fmaf(t[k][r], hat[k][r], gw[k][r]);
+        gb[k][r] += t[k][r];
+        t[k][r] *= w[k][r];
+        s1 += t[k][r];
+        s2 = fmaf(t[k][r], hat[k][r], s2);
+      }
+    }
+    s1 = row_sum<R>(s1, sh) / n;
+    s2 = row_sum<R>(s2, sh) / n;
+    if (A.dx) {
+      T* pd = reinterpret_cast<T*>(A.dx) + row * A.sdx;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = (k * R + l) * V;
+#pragma unroll
+        for (int r = 0; r < V; ++r) t[k][r] = (t[k][r] - s1 - hat[k][r] * s2) * rstd;
+        if (c < N) store_vec<T, V>(pd + c, t[k]);
+      }
+    }
+  }
+  if (!A.part) return;
+  float* part = A.part + (long long)blockIdx.x * 2 * N;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float y[V];
+#pragma unroll
+      for (int r = 0; r < V; ++r) y[r] = which ? gb[k][r] : gw[k][r];
+      if constexpr (R < 256) {                      // add up the rows taken side by side
+#pragma unroll
+        for (int r = 0; r < V; ++r)
+#pragma unroll
+          for (int m = R; m < 64; m <<= 1) y[r] += __shfl_xor(y[r], m);
+        __syncthreads();
+        if ((tid & 63) < W)
+#pragma unroll
+          for (int r = 0; r < V; ++r) cross[((tid >> 6) * W + (tid & 63)) * V + r] = y[r];
+        __syncthreads();
+        if (tid < W)
+#pragma unroll
+          for (int r = 0; r < V; ++r)
+            y[r] = (cross[tid * V + r] + cross[(W + tid) * V + r]) +
+                   (cross[(2 * W + tid) * V + r] + cross[(3 * W + tid) * V + r]);
+      }
+      if (R == 256 || tid < W)
+#pragma unroll
+        for (int r = 0; r < V; ++r) {
+          const int c = (k * R + l) * V + r;
+          if (c < N) part[(long long)which * N + c] = y[r];
+        }
+    }
+}
+
+// dw and db from the blocks' partial sums: 64 columns of a workgroup, 16 slices of the blocks,
+// added in order.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs A) {
+  __shared__ float sh[16][64];
+  const int lane = threadIdx.x & 63, s = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  const int which = blockIdx.y, per = (A.blocks + 15) / 16;
+  float sum = 0.f;
+  if (c < A.N)
+    for (int i = s * per; i < min(A.blocks, (s + 1) * per); ++i)
+      sum += A.part[((long long)i * 2 + which) * A.N + c];
+  sh[s][lane] = sum;
+  __syncthreads();
+  if (s == 0 && c < A.N) {
+    for (int i = 1; i < 16; ++i) sum += sh[i][lane];
+    void* out = which ? A.db : A.dw;
+    if (!out) return;
+    if (A.w_bf16) reinterpret_cast<__bf16*>(out)[c] = (__bf16)sum;
+    else reinterpret_cast<float*>(out)[c] = sum;
+  }
+}
+
+// ---- rows of any width ------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_fwd_loop_kernel(NormArgs A) {
+  __shared__ float sh[4];
+  const int N = A.N;
+  const float n = (float)N;
+  for (long long row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    const T* px = reinterpret_cast<const T*>(A.x) + row * A.sx;
+    T* py = reinterpret_cast<T*>(A.y) + row * A.sy;
+    float sum = 0.f, sq = 0.f;
+    for (int c = threadIdx.x; c < N; c += kThreads) sum += to_f32(px[c]);
+    const float mean = row_sum<256>(sum, sh) / n;
+    for (int c = threadIdx.x; c < N; c += kThreads) {
+      const float d = to_f32(px[c]) - mean;
+      sq = fmaf(d, d, sq);
+    }
+    const float rstd = 1.f / sqrtf(row_sum<256>(sq, sh) / n + A.eps);
+    for (int c = threadIdx.x; c < N; c += kThreads)
+      py[c] = from_f32<T>(fmaf((to_f32(px[c]) - mean) * rstd, param(A.w, A.w_bf16, c, 1.f),
+                               param(A.b, A.w_bf16, c, 0.f)));
+    if (threadIdx.x == 0 && A.mean) {
+      A.mean[row] = mean;
+      A.rstd[row] = rstd;
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_dx_loop_kernel(NormArgs A) {
+  __shared__ float sh[4];
+  const int N = A.N;
+  const float n = (float)N;
+  for (long long row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    const T* px = reinterpret_cast<const T*>(A.x) + row * A.sx;
+    const T* pg = reinterpret_cast<const T*>(A.dy) + row * A.sdy;
+    T* pd = reinterpret_cast<T*>(A.dx) + row * A.sdx;
+    const float mean = A.mean[row], rstd = A.rstd[row];
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x; c < N; c += kThreads) {
+      const float t = to_f32(pg[c]) * param(A.w, A.w_bf16, c, 1.f);
+      s1 += t;
+      s2 = fmaf(t, (to_f32(px[c]) - mean) * rstd, s2);
+    }
+    s1 = row_sum<256>(s1, sh) / n;
+    s2 = row_sum<256>(s2, sh) / n;
+    for (int c = threadIdx.x; c < N; c += kThreads) {
+      const float t = to_f32(pg[c]) * param(A.w, A.w_bf16, c, 1.f);
+      pd[c] = from_f32<T>((t - s1 - (to_f32(px[c]) - mean) * rstd * s2) * rstd);
+    }
+  }
+}
+
+// Partial sums of dw and db: a column a thread, the rows of block y.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_dw_loop_kernel(NormArgs A) {
+  const int c = blockIdx.x * kThreads + threadIdx.x;
+  if (c >= A.N) return;
+  float gw = 0.f, gb = 0.f;
+  for (long long row = blockIdx.y; row < A.rows; row += gridDim.y) {
+    const float g = to_f32(reinterpret_cast<const T*>(A.dy)[row * A.sdy + c]);
+    const float x = to_f32(reinterpret_cast<const T*>(A.x)[row * A.sx + c]);
+    gw = fmaf(g, (x - A.mean[row]) * A.rstd[row], gw);
+    gb += g;
+  }
+  float* part = A.part + (long long)blockIdx.y * 2 * A.N + c;
+  part[0] = gw;
+  part[A.N] = gb;
+}
+
+template <typename T, int V, bool kBwd>
+bool launch_rows(NormArgs& a, hipStream_t st) {
+  const int nv = a.N / V;
+  auto run = [&](auto fwd, auto bwd, int rpb) {
+    const long long want = (a.rows + rpb - 1) / rpb;
+    const int most = kBwd ? kNormBlocks : 2 * kNormBlocks;
+    a.blocks = (int)(want < most ? want : most);
+    launch_kernel(kBwd ? bwd : fwd, dim3(a.blocks), kThreads, 0, st, a);
+    return true;
+  };
+#define KATA_NORM(R_, K_)                                                                       \
+  if (nv <= R_ * K_)                                                                            \
+    return run(norm_fwd_kernel<T, V, R_, K_>, norm_bwd_kernel<T, V, R_, K_>, kThreads / R_);
+  KATA_NORM(8, 1) KATA_NORM(16, 1) KATA_NORM(32, 1) KATA_NORM(64, 1) KATA_NORM(64, 2)
+  KATA_NORM(64, 4) KATA_NORM(256, 2) KATA_NORM(256, 4)
+#undef KATA_NORM
+  return false;
+}
+
+template <typename T>
+hipError_t fwd_t(NormArgs& a, bool vec, hipStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec ? launch_rows<T, V, false>(a, st) : launch_rows<T, 1, false>(a, st)) return hipGetLastError();
+  launch_kernel(norm_fwd_loop_kernel<T>, dim3((unsigned)(a.rows < 2048 ? a.rows : 2048)), kThreads, 0, st, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t bwd_t(NormArgs& a, bool vec, hipStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  if (!(vec ? launch_rows<T, V, true>(a, st) : launch_rows<T, 1, true>(a, st))) {
+    // dw and db first: dx may overwrite dy
+    a.blocks = (int)(a.rows < 64 ? a.rows : 64);
+    if (a.part)
+      launch_kernel(norm_dw_loop_kernel<T>, dim3((a.N + kThreads - 1) / kThreads, a.blocks), kThreads, 0, st, a);
+    if (a.dx)
+      launch_kernel(norm_dx_loop_kernel<T>, dim3((unsigned)(a.rows < 2048 ? a.rows : 2048)), kThreads, 0, st, a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.part) return e;
+  launch_kernel(norm_sum_kernel, dim3((a.N + 63) / 64, 2), 1024, 0, st, a);
+  return hipGetLastError();
+}
+
+// 16-byte accesses need rows of whole vectors.
+bool vectors(const NormArgs& a, bool bf16, bool aligned) { return aligned && a.N % (bf16 ? 8 : 4) == 0; }
+
+}  // namespace
+
+hipError_t launch_norm_fwd(NormArgs& a, bool bf16, bool aligned, hipStream_t st) {
+  return bf16 ? fwd_t<__bf16>(a, vectors(a, bf16, aligned), st) : fwd_t<float>(a, vectors(a, bf16, aligned), st);
+}
+hipError_t launch_norm_bwd(NormArgs& a, bool bf16, bool aligned, hipStream_t st) {
+  return bf16 ? bwd_t<__bf16>(a, vectors(a, bf16, aligned), st) : bwd_t<float>(a, vectors(a, bf16, aligned), st);
+}
+
+}  // namespace kata
