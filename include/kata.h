@@ -289,7 +289,7 @@ kata_status kata_bwd_chunked(const kata_problem* pr, const void* q, const void* 
  *   dtype: of q, k, v, o, dO and the gradients.  States are fp32 [n_seq][H][dk][dv], contiguous.
  *   log_decay: device fp32 [H], any value; -inf is a decay of zero.  It has no gradient.
  *   sq, sk, sv, so, sdo: element strides of (b, t, h); those of an input may be zero (a broadcast
- *          axis).  Rows are 16-byte aligned.  An output overlaps no input and no other output. */
+ *          axis), that of an axis of one entry is not looked at.  Rows are 16-byte aligned.  An output overlaps no input and no other output. */
 typedef struct {
   int32_t n_seq, H, T, dk, dv;
   int32_t packed;

@@ -201,9 +201,9 @@ struct Tiles {
   }
 };
 
-// Value weights of the state's update, x = w v: for bf16 as one term (rounded, half a step of
-// bf16, like every operand of the products) or as three that add up to the fp32 product, which
-// a state that the caller keeps is worth; fp32 as it is.
+// Value weights of the state's update, x = w v, as SPLIT bf16 terms that add up to it: two (2^-17 of
+// x: one rounded term puts the outputs 1.7 times as far off the exact ones as their own
+// rounding), or three, the whole fp32 product, for a state that the caller keeps; fp32 as it is.
 template <int SPLIT>
 __device__ __forceinline__ void weigh(const bf16x8& v, const float (&w)[8], bf16x8 (&out)[SPLIT]) {
 #pragma unroll
@@ -659,9 +659,9 @@ hipError_t launch_decay_chunks(DecayArgs& a, bool bf16, bool exact_state, bool s
   if (!bf16) return launch_chunks_d<float, 1, 1>(a, dk, state_pass, st);
   if (cols == 128)
     return exact_state ? launch_chunks_d<__bf16, 2, 3>(a, dk, state_pass, st)
-                       : launch_chunks_d<__bf16, 2, 1>(a, dk, state_pass, st);
+                       : launch_chunks_d<__bf16, 2, 2>(a, dk, state_pass, st);
   return exact_state ? launch_chunks_d<__bf16, 1, 3>(a, dk, state_pass, st)
-                     : launch_chunks_d<__bf16, 1, 1>(a, dk, state_pass, st);
+                     : launch_chunks_d<__bf16, 1, 2>(a, dk, state_pass, st);
 }
 
 hipError_t launch_decay_scan(const DecayArgs& a, hipStream_t st) {

@@ -20,6 +20,7 @@ using kata::Timed;
 
 namespace {
 
+// Strides for the kernels; an axis of one entry is never stepped along.
 void copy3(long long (&to)[3], const int64_t from[3]) {
   for (int i = 0; i < 3; ++i) to[i] = from[i];
 }
@@ -44,8 +45,9 @@ kata_status check_decay(const kata_decay_problem* pr, bool backward, const Named
   kata_status s = kata::validate_decay(pr, backward, &why);
   if (s != KATA_OK) return set_error(s, why);
   const size_t es = kata::elem_size(pr->dtype);
+  const int64_t sizes[3] = {pr->packed ? 1 : pr->n_seq, pr->T, pr->H};
   for (int i = 0; i < n; ++i)
-    if ((s = kata::validate_rows(ts[i].p, ts[i].st, es, ts[i].name, &why)) != KATA_OK)
+    if ((s = kata::validate_rows(ts[i].p, ts[i].st, sizes, es, ts[i].name, &why)) != KATA_OK)
       return set_error(s, why);
   if (!log_decay) return set_error(KATA_ERR_INVALID_ARGUMENT, "log_decay is null");
   if (pr->packed && !cu) return set_error(KATA_ERR_INVALID_ARGUMENT, "cu_seqlens is null");

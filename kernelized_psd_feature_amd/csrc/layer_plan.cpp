@@ -23,7 +23,7 @@ kata_status check_strides(const char* name, const int64_t st[3], const int64_t s
   const int64_t kMax = int64_t(1) << 60;
   int64_t extent = width;
   for (int a = 0; a < 3; ++a) {
-    const int64_t s = st[a];
+    const int64_t s = sizes[a] > 1 ? st[a] : 0;
     if (s < 0) return fail(why, KATA_ERR_INVALID_ARGUMENT, std::string(name) + ": negative stride");
     if (sizes[a] > 1 && s < width && (output || s != 0))
       return fail(why, KATA_ERR_INVALID_ARGUMENT,
@@ -38,9 +38,11 @@ kata_status check_strides(const char* name, const int64_t st[3], const int64_t s
 
 }  // namespace
 
-kata_status validate_rows(const void* p, const int64_t st[3], size_t esize, const char* name,
-                          std::string* why) {
-  return validate_tensor(p, st, esize, name, why);
+kata_status validate_rows(const void* p, const int64_t st[3], const int64_t sizes[3], size_t esize,
+                          const char* name, std::string* why) {
+  int64_t used[3];
+  for (int a = 0; a < 3; ++a) used[a] = sizes[a] > 1 ? st[a] : 0;
+  return validate_tensor(p, used, esize, name, why);
 }
 
 kata_status validate_decay(const kata_decay_problem* pr, bool backward, std::string* why) {

@@ -23,9 +23,10 @@ struct DecayPlan {
 };
 
 kata_status validate_decay(const kata_decay_problem* pr, bool backward, std::string* why);
-// A tensor's pointer and (b, t, h) strides: 16-byte aligned rows.
-kata_status validate_rows(const void* p, const int64_t st[3], size_t esize, const char* name,
-                          std::string* why);
+// A tensor's pointer and (b, t, h) strides: 16-byte aligned rows.  The stride of an axis of one
+// entry means nothing.
+kata_status validate_rows(const void* p, const int64_t st[3], const int64_t sizes[3], size_t esize,
+                          const char* name, std::string* why);
 // pr must have passed validate_decay.
 DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles);
 

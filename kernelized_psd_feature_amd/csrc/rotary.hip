@@ -126,11 +126,14 @@ hipError_t launch_t(RotaryArgs& a, bool interleaved, hipStream_t st) {
   const int half = a.rot / 2;
   const int NR = interleaved ? a.rot / (V == 1 ? 2 : V) : half / V;
   const int per = (a.H + a.Hk) * (NR + (a.D - a.rot) / V);
-  // about four items a thread, the cosines of the block within 32 KB
+  // about four items a thread, fewer where that leaves CUs without a workgroup, and the cosines of
+  // the block within 32 KB
+  const long long tokens = (long long)a.B * a.T;
   a.TT = 4 * kThreads / per;
+  if (a.TT > tokens / 512) a.TT = (int)(tokens / 512);
   if (a.TT > 4096 / (half ? half : 1)) a.TT = 4096 / half;
   if (a.TT < 1) a.TT = 1;
-  const long long blocks = ((long long)a.B * a.T + a.TT - 1) / a.TT;
+  const long long blocks = (tokens + a.TT - 1) / a.TT;
   const size_t lds = sizeof(float2) * a.TT * half;
   if (interleaved)
     launch_kernel(rotary_kernel<T, V, true>, dim3((unsigned)blocks), kThreads, lds, st, a);

@@ -13,7 +13,9 @@ The last one and layer_norm are differentiable by torch autograd.
 """
 
 import ctypes
+import functools
 import math
+import struct
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -42,35 +44,78 @@ class _NormProblem(ctypes.Structure):
                 ("sx", _I64), ("sdy", _I64), ("sy", _I64), ("sdx", _I64)]
 
 
+# The same layouts for struct.pack: a call of a few microseconds is mostly spent in its arguments.
+_DECAY = struct.Struct("8if15q")
+_ROTARY = struct.Struct("10if15q")
+_NORM = struct.Struct("q3if4q")
+assert (_DECAY.size, _ROTARY.size, _NORM.size) == tuple(
+    ctypes.sizeof(x) for x in (_DecayProblem, _RotaryProblem, _NormProblem))
+
+
 def _signatures():
-    VP, SZ = ctypes.c_void_p, ctypes.c_size_t
-    D, R, N = (ctypes.POINTER(x) for x in (_DecayProblem, _RotaryProblem, _NormProblem))
+    VP, SZ = ctypes.c_void_p, ctypes.c_size_t   # a problem is passed by its address
     return {
-        "kata_fwd_decay_workspace_size": (SZ, [D]),
-        "kata_fwd_decay": (_I32, [D] + [VP] * 9 + [SZ, VP]),
-        "kata_bwd_decay_workspace_size": (SZ, [D]),
-        "kata_bwd_decay": (_I32, [D] + [VP] * 13 + [SZ, VP]),
-        "kata_decode_decay": (_I32, [D] + [VP] * 7),
-        "kata_rotary": (_I32, [R] + [VP] * 7),
-        "kata_fwd_layer_norm": (_I32, [N] + [VP] * 7),
-        "kata_bwd_layer_norm_workspace_size": (SZ, [N]),
-        "kata_bwd_layer_norm": (_I32, [N] + [VP] * 9 + [SZ, VP]),
+        "kata_fwd_decay_workspace_size": (SZ, [VP]),
+        "kata_fwd_decay": (_I32, [VP] * 10 + [SZ, VP]),
+        "kata_bwd_decay_workspace_size": (SZ, [VP]),
+        "kata_bwd_decay": (_I32, [VP] * 14 + [SZ, VP]),
+        "kata_decode_decay": (_I32, [VP] * 8),
+        "kata_rotary": (_I32, [VP] * 8),
+        "kata_fwd_layer_norm": (_I32, [VP] * 8),
+        "kata_bwd_layer_norm_workspace_size": (SZ, [VP]),
+        "kata_bwd_layer_norm": (_I32, [VP] * 10 + [SZ, VP]),
     }
 
 
-def _strides(x, name):
-    """Element strides of the (b, t, h) axes; an axis of one entry counts as zero."""
-    if x.dim() != 4:
-        raise ValueError(f"{name} must be 4-D (B, T, H, D)")
-    if x.shape[3] > 1 and x.stride(3) != 1:
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(name, device, *args):
+    """One entry point on the device's current stream."""
+    fn = getattr(_k._LIB or _k._lib(), name)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device.index))
+    if status:
+        _k._check(status, name)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_size(name, problem):
+    return int(getattr(_k._lib(), name)(problem))
+
+
+def _ptr(x):
+    return None if x is None else x.data_ptr()
+
+
+def _rows_ok(x, name):
+    if x.stride(-1) != 1 and x.shape[-1] > 1:
         raise ValueError(f"{name}: last dimension must be contiguous")
-    return tuple(x.stride(i) if x.shape[i] > 1 else 0 for i in range(3))
+    return x.stride()[:3]
 
 
-def _on(device, **tensors):
-    for name, x in tensors.items():
+def _same_device(device, *named):
+    for name, x in named:
         if x is not None and x.device != device:
             raise ValueError(f"{name} must be on {device}")
+
+
+def _empty(x):
+    """A new contiguous tensor like x."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+_DTYPES = {torch.float32: _k.KATA_F32, torch.bfloat16: _k.KATA_BF16}
+
+
+def _dtype(dt):
+    code = _DTYPES.get(dt)
+    return _k._dtype_code(dt) if code is None else code
 
 
 def _workspace(need, given, device):
@@ -87,33 +132,33 @@ def _bytes(x):
 
 # ---- linear attention with one decay per head -------------------------------------------------
 
-def _decay_problem(q, k, v, log_decay, scale, cu_seqlens, o=None, dO=None):
+def _decay_problem(q, k, v, log_decay, scale, cu_seqlens, o=None, dO=None, zero_tail=0):
+    """The packed kata_decay_problem of a call, its arguments checked."""
+    device, dtype, shape, vs = q.device, q.dtype, q.shape, v.shape
     if not q.is_cuda:
         raise ValueError("q must be a GPU tensor")
-    for name, x in (("q", q), ("k", k), ("v", v)):
-        if x.dim() != 4:
-            raise ValueError(f"{name} must be 4-D (B, T, H, D)")
-    if k.shape != q.shape or v.shape[:3] != q.shape[:3] or k.dtype != q.dtype or v.dtype != q.dtype:
+    if len(shape) != 4 or len(vs) != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be 4-D (B, T, H, D)")
+    if k.shape != shape or vs[:3] != shape[:3] or k.dtype != dtype or v.dtype != dtype:
         raise ValueError("q, k, v must share (B, T, H) and dtype; q and k share dk")
-    B, T, H, dk = q.shape
+    B, T, H, dk = shape
+    dv = vs[3]
     if log_decay.shape != (H,) or log_decay.dtype != torch.float32 or not log_decay.is_contiguous():
         raise ValueError("log_decay must be a contiguous fp32 tensor of shape (H,)")
-    _on(q.device, k=k, v=v, log_decay=log_decay, cu_seqlens=cu_seqlens, out=o, dO=dO)
-    pr = _DecayProblem()
-    pr.n_seq, pr.H, pr.T, pr.dk, pr.dv = B, H, T, dk, v.shape[3]
+    _same_device(device, ("k", k), ("v", v), ("log_decay", log_decay), ("cu_seqlens", cu_seqlens),
+                 ("out", o), ("dO", dO))
+    n, packed = B, 0
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.dtype != torch.int32 \
                 or not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be a contiguous int32 tensor of n + 1 >= 2 offsets")
         if B != 1:
             raise ValueError("packed sequences lie in one batch row: B must be 1")
-        pr.packed, pr.n_seq = 1, cu_seqlens.numel() - 1
-    pr.dtype, pr.scale = _k._dtype_code(q.dtype), scale
-    pr.sq[:], pr.sk[:], pr.sv[:] = _strides(q, "q"), _strides(k, "k"), _strides(v, "v")
-    pr.so[:] = _strides(o, "out") if o is not None else (T * H * pr.dv, H * pr.dv, pr.dv)
-    if dO is not None:
-        pr.sdo[:] = _strides(dO, "dO")
-    return pr
+        n, packed = cu_seqlens.numel() - 1, 1
+    so = _rows_ok(o, "out") if o is not None else (T * H * dv, H * dv, dv)
+    sdo = _rows_ok(dO, "dO") if dO is not None else so
+    return _DECAY.pack(n, H, T, dk, dv, packed, zero_tail, _dtype(dtype), scale, *_rows_ok(q, "q"),
+                       *_rows_ok(k, "k"), *_rows_ok(v, "v"), *so, *sdo)
 
 
 def decay_state_shape(q, v, cu_seqlens=None):
@@ -130,11 +175,11 @@ def _state(x, shape, device, name):
     return x
 
 
-def _out_like(v, out, name="out"):
+def _out_like(v, out):
     if out is None:
-        return torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        return _empty(v)
     if out.shape != v.shape or out.dtype != v.dtype or out.device != v.device:
-        raise ValueError(f"{name} must match v's shape, dtype and device")
+        raise ValueError("out must match v's shape, dtype and device")
     return out
 
 
@@ -149,31 +194,24 @@ def fwd_decay(q, k, v, log_decay, scale=1.0, initial_state=None, return_state=Fa
     initial_state, and the final state with return_state: fp32 (n, H, dk, dv).
     workspace: uint8, decay_workspace_size() bytes (allocated here otherwise)."""
     o = _out_like(v, out)
-    pr = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, o=o)
-    shape = decay_state_shape(q, v, cu_seqlens)
-    _state(initial_state, shape, q.device, "initial_state")
-    final = torch.empty(shape, dtype=torch.float32, device=q.device) if return_state else None
+    pr = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, o=o, zero_tail=1 if out is None else 0)
+    shape, device = decay_state_shape(q, v, cu_seqlens), q.device
+    _state(initial_state, shape, device, "initial_state")
+    final = torch.empty(shape, dtype=torch.float32, device=device) if return_state else None
     if q.shape[0] * q.shape[1] == 0:
         if final is not None:
             final.copy_(initial_state) if initial_state is not None else final.zero_()
     elif q.shape[2]:
-        pr.zero_tail = 1 if out is None else 0
-        lib = _k._lib()
-        ws = _workspace(int(lib.kata_fwd_decay_workspace_size(ctypes.byref(pr))), workspace, q.device)
-        p = _k._ptr
-        with torch.cuda.device(q.device):
-            _k._check(lib.kata_fwd_decay(ctypes.byref(pr), p(q), p(k), p(v), p(log_decay),
-                                         p(cu_seqlens), p(initial_state), p(o), p(final), p(ws),
-                                         _bytes(ws), _k._stream(q.device)), "kata_fwd_decay")
+        ws = _workspace(_workspace_size("kata_fwd_decay_workspace_size", pr), workspace, device)
+        _run("kata_fwd_decay", device, pr, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+             _ptr(cu_seqlens), _ptr(initial_state), o.data_ptr(), _ptr(final), _ptr(ws), _bytes(ws))
     return (o, final) if return_state else o
 
 
 def decay_workspace_size(q, k, v, log_decay, cu_seqlens=None, backward=False):
     """Bytes of workspace fwd_decay (or bwd_decay) needs."""
-    pr = _decay_problem(q, k, v, log_decay, 1.0, cu_seqlens)
-    lib = _k._lib()
-    fn = lib.kata_bwd_decay_workspace_size if backward else lib.kata_fwd_decay_workspace_size
-    return int(fn(ctypes.byref(pr)))
+    return _workspace_size(f"kata_{'bwd' if backward else 'fwd'}_decay_workspace_size",
+                           _decay_problem(q, k, v, log_decay, 1.0, cu_seqlens))
 
 
 def bwd_decay(q, k, v, dO, log_decay, scale=1.0, initial_state=None, dfinal_state=None,
@@ -183,25 +221,20 @@ def bwd_decay(q, k, v, dO, log_decay, scale=1.0, initial_state=None, dfinal_stat
     the last packed sequence get zeros."""
     if dO.shape != v.shape or dO.dtype != q.dtype:
         raise ValueError("dO must match v's shape and q's dtype")
-    pr = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, dO=dO)
-    pr.zero_tail = 1
-    shape = decay_state_shape(q, v, cu_seqlens)
-    _state(initial_state, shape, q.device, "initial_state")
-    _state(dfinal_state, shape, q.device, "dfinal_state")
-    dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
-    dinit = torch.empty(shape, dtype=torch.float32, device=q.device) if initial_state is not None else None
+    pr = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, dO=dO, zero_tail=1)
+    shape, device = decay_state_shape(q, v, cu_seqlens), q.device
+    _state(initial_state, shape, device, "initial_state")
+    _state(dfinal_state, shape, device, "dfinal_state")
+    dq, dk, dv = _empty(q), _empty(k), _empty(v)
+    dinit = torch.empty(shape, dtype=torch.float32, device=device) if initial_state is not None else None
     if q.shape[0] * q.shape[1] == 0:
         if dinit is not None:
             dinit.copy_(dfinal_state) if dfinal_state is not None else dinit.zero_()
     elif q.shape[2]:
-        lib = _k._lib()
-        ws = _workspace(int(lib.kata_bwd_decay_workspace_size(ctypes.byref(pr))), workspace, q.device)
-        p = _k._ptr
-        with torch.cuda.device(q.device):
-            _k._check(lib.kata_bwd_decay(ctypes.byref(pr), p(q), p(k), p(v), p(dO), p(log_decay),
-                                         p(cu_seqlens), p(initial_state), p(dfinal_state), p(dq), p(dk),
-                                         p(dv), p(dinit), p(ws), _bytes(ws), _k._stream(q.device)),
-                      "kata_bwd_decay")
+        ws = _workspace(_workspace_size("kata_bwd_decay_workspace_size", pr), workspace, device)
+        _run("kata_bwd_decay", device, pr, q.data_ptr(), k.data_ptr(), v.data_ptr(), dO.data_ptr(),
+             log_decay.data_ptr(), _ptr(cu_seqlens), _ptr(initial_state), _ptr(dfinal_state),
+             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dinit), _ptr(ws), _bytes(ws))
     return dq, dk, dv, dinit
 
 
@@ -213,12 +246,9 @@ def decode_decay(q, k, v, log_decay, state, scale=1.0, out=None):
     if state is None:
         raise ValueError("decode_decay needs a state")
     _state(state, decay_state_shape(q, v), q.device, "state")
-    if q.shape[0] * q.shape[1] * q.shape[2]:
-        p = _k._ptr
-        with torch.cuda.device(q.device):
-            _k._check(_k._lib().kata_decode_decay(ctypes.byref(pr), p(q), p(k), p(v), p(log_decay),
-                                                  p(state), p(o), _k._stream(q.device)),
-                      "kata_decode_decay")
+    if v.numel():
+        _run("kata_decode_decay", q.device, pr, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             log_decay.data_ptr(), state.data_ptr(), o.data_ptr())
     return o
 
 
@@ -278,44 +308,44 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
     B, T, H, D = q.shape
     if 2 * rates.numel() > D:
         raise ValueError("rates turn more coordinates than a head has")
-    ins = [q] if k is None else [q, k]
-    outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in ins] if out is None else \
-        [out] if torch.is_tensor(out) else list(out)
-    if len(outs) != len(ins):
-        raise ValueError("out must hold an output for each input")
-    for x, y in zip(ins, outs):
-        if y.shape != x.shape or y.dtype != x.dtype:
-            raise ValueError("out must match the inputs' shapes and dtype")
-        _on(q.device, k=x, out=y)
-    _on(q.device, rates=rates, positions=positions)
-    pr = _RotaryProblem()
-    pr.B, pr.T, pr.H, pr.Hk, pr.D, pr.rot = B, T, H, 0 if k is None else k.shape[2], D, 2 * rates.numel()
-    pr.dtype, pr.interleaved, pr.inverse = _k._dtype_code(q.dtype), int(interleaved), int(inverse)
-    pr.magnitude, pr.offset = magnitude, offset
+    device = q.device
+    if out is None:
+        oq, ok = _empty(q), None if k is None else _empty(k)
+    else:
+        outs = (out,) if torch.is_tensor(out) else tuple(out)
+        if len(outs) != (1 if k is None else 2):
+            raise ValueError("out must hold an output for each input")
+        oq, ok = (*outs, None)[:2]
+        for x, y in ((q, oq), (k, ok)):
+            if x is not None and (y.shape != x.shape or y.dtype != x.dtype):
+                raise ValueError("out must match the inputs' shapes and dtype")
+    _same_device(device, ("k", k), ("rates", rates), ("positions", positions), ("out", oq), ("out", ok))
+    pos64 = pos_b = pos_t = 0
     if positions is not None:
         if positions.dtype not in (torch.int32, torch.int64):
             raise ValueError("positions must be int32 or int64")
         try:
-            at = positions.expand(B, T)
+            at = positions if positions.shape == (B, T) else positions.expand(B, T)
         except RuntimeError:
             raise ValueError("positions must broadcast to (B, T)") from None
-        pr.pos64, pr.pos_b, pr.pos_t = int(positions.dtype == torch.int64), at.stride(0), at.stride(1)
-    pr.sq[:], pr.soq[:] = _strides(q, "q"), _strides(outs[0], "out")
-    if k is not None:
-        pr.sk[:], pr.sok[:] = _strides(k, "k"), _strides(outs[1], "out")
-    if B * T * H * D and not (k is not None and k.shape[2] == 0):
-        p = _k._ptr
-        with torch.cuda.device(q.device):
-            _k._check(_k._lib().kata_rotary(ctypes.byref(pr), p(q), p(k), p(rates), p(positions),
-                                            p(outs[0]), p(outs[1]) if k is not None else None,
-                                            _k._stream(q.device)), "kata_rotary")
-    return outs[0] if k is None else tuple(outs)
+        pos64, (pos_b, pos_t) = int(positions.dtype == torch.int64), at.stride()
+    Hk = 0 if k is None else k.shape[2]
+    sq, soq = _rows_ok(q, "q"), _rows_ok(oq, "out")
+    sk, sok = (sq, soq) if k is None else (_rows_ok(k, "k"), _rows_ok(ok, "out"))
+    if B * T * H * D and (k is None or Hk):
+        pr = _ROTARY.pack(B, T, H, Hk, D, 2 * rates.numel(), _dtype(q.dtype), int(interleaved), int(inverse),
+                          pos64, magnitude, pos_b, pos_t, offset, *sq, *sk, *soq, *sok)
+        _run("kata_rotary", device, pr, q.data_ptr(), _ptr(k), rates.data_ptr(), _ptr(positions),
+             oq.data_ptr(), _ptr(ok))
+    return oq if k is None else (oq, ok)
 
 
 # ---- layer norm --------------------------------------------------------------------------------
 
 def _rows(x):
     """x as (rows, N) with one row stride, copied only where its axes do not collapse."""
+    if x.dim() == 2 and (x.shape[1] == 1 or x.stride(1) == 1):
+        return x
     try:
         y = x.view(-1, x.shape[-1])
     except RuntimeError:
@@ -323,94 +353,80 @@ def _rows(x):
     return y if y.shape[1] == 1 or y.stride(1) == 1 else y.contiguous()
 
 
-def _norm_problem(x, weight, bias, eps):
+def _check_norm(x, weight, bias):
+    """The weights' dtype code, the arguments checked."""
     if not x.is_cuda:
         raise ValueError("x must be a GPU tensor")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x needs a last axis of at least one element")
-    N = x.shape[-1]
-    dt = None
+    dt, want = None, (x.shape[-1],)
     for name, p in (("weight", weight), ("bias", bias)):
         if p is None:
             continue
-        if p.shape != (N,) or not p.is_contiguous():
+        if p.shape != want or not p.is_contiguous():
             raise ValueError(f"{name} must be a contiguous vector of the last axis's length")
         if dt is not None and p.dtype != dt:
             raise ValueError("weight and bias must share their dtype")
         dt = p.dtype
-    _on(x.device, weight=weight, bias=bias)
-    pr = _NormProblem()
-    pr.N, pr.eps = N, eps
-    pr.dtype = _k._dtype_code(x.dtype)
-    pr.w_dtype = _k._dtype_code(dt) if dt is not None else _k.KATA_F32
-    return pr
-
-
-def _row_stride(x2):
-    return x2.stride(0) if x2.shape[0] > 1 else x2.shape[1]
+    _same_device(x.device, ("weight", weight), ("bias", bias))
+    return _k.KATA_F32 if dt is None else _dtype(dt)
 
 
 def fwd_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, return_stats=False):
     """Layer norm over the last axis of x (bf16 or fp32, any leading axes); weight and bias (N,) in
     fp32, or bf16 for bf16 rows.  With return_stats also the rows' mean and 1 / sqrt(var + eps), fp32
     of x's leading shape, for bwd_layer_norm.  out may be x."""
-    pr = _norm_problem(x, weight, bias, eps)
+    wt = _check_norm(x, weight, bias)
     if out is not None and (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device):
         raise ValueError("out must match x's shape, dtype and device")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if return_stats else None
-                  for _ in range(2))
+    y = _empty(x) if out is None else out
+    device, mean, rstd = x.device, None, None
+    if return_stats:
+        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=device) for _ in range(2))
     if x.numel():
-        x2 = _rows(x)
+        x2, N = _rows(x), x.shape[-1]
         try:
-            y2 = y.view(-1, pr.N)
+            y2 = y.view(-1, N)
         except RuntimeError:
             raise ValueError("out's leading axes must collapse into one") from None
-        if pr.N > 1 and y2.stride(1) != 1:
+        if N > 1 and y2.stride(1) != 1:
             raise ValueError("out: last dimension must be contiguous")
-        pr.rows, pr.sx, pr.sy = x2.shape[0], _row_stride(x2), _row_stride(y2)
-        pr.sdy = pr.sdx = pr.N
-        p = _k._ptr
-        with torch.cuda.device(x.device):
-            _k._check(_k._lib().kata_fwd_layer_norm(ctypes.byref(pr), p(x2), p(weight), p(bias), p(y2),
-                                                    p(mean), p(rstd), _k._stream(x.device)),
-                      "kata_fwd_layer_norm")
+        pr = _NORM.pack(x2.shape[0], N, _dtype(x.dtype), wt, eps, x2.stride(0), N, y2.stride(0), N)
+        _run("kata_fwd_layer_norm", device, pr, x2.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(),
+             _ptr(mean), _ptr(rstd))
     return (y, mean, rstd) if return_stats else y
 
 
 def layer_norm_workspace_size(x, weight=None):
     """Bytes of workspace bwd_layer_norm needs for the gradients of the weight and the bias."""
-    pr = _norm_problem(x, weight, None, 0.0)
-    pr.rows = x.numel() // pr.N
-    pr.sx = pr.sy = pr.sdy = pr.sdx = pr.N
-    return int(_k._lib().kata_bwd_layer_norm_workspace_size(ctypes.byref(pr)))
+    wt, N = _check_norm(x, weight, None), x.shape[-1]
+    return _workspace_size("kata_bwd_layer_norm_workspace_size",
+                           _NORM.pack(x.numel() // N, N, _dtype(x.dtype), wt, 0.0, N, N, N, N))
 
 
 def bwd_layer_norm(dy, x, weight, mean, rstd, params=True, workspace=None):
     """Gradients (dx, dweight, dbias) of sum(dy * y), mean and rstd as fwd_layer_norm returned them.
     dweight and dbias have the weight's dtype (fp32 without one), summed over the rows in a fixed
     order; None with params=False."""
-    pr = _norm_problem(x, weight, None, 0.0)
+    wt = _check_norm(x, weight, None)
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must match x's shape and dtype")
     for name, s in (("mean", mean), ("rstd", rstd)):
         if s.shape != x.shape[:-1] or s.dtype != torch.float32 or not s.is_contiguous():
             raise ValueError(f"{name} must be a contiguous fp32 tensor of x's leading shape")
-    _on(x.device, dy=dy, mean=mean, rstd=rstd)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dt = weight.dtype if weight is not None else torch.float32
-    dw, db = (torch.empty(pr.N, dtype=dt, device=x.device) if params else None for _ in range(2))
+    device, N, dw, db = x.device, x.shape[-1], None, None
+    _same_device(device, ("dy", dy), ("mean", mean), ("rstd", rstd))
+    dx = _empty(x)
+    if params:
+        dt = weight.dtype if weight is not None else torch.float32
+        dw, db = (torch.empty(N, dtype=dt, device=device) for _ in range(2))
     if x.numel():
         x2, g2 = _rows(x), _rows(dy)
-        pr.rows, pr.sx, pr.sdy = x2.shape[0], _row_stride(x2), _row_stride(g2)
-        pr.sy = pr.sdx = pr.N
-        lib, p = _k._lib(), _k._ptr
-        ws = _workspace(int(lib.kata_bwd_layer_norm_workspace_size(ctypes.byref(pr))) if params else 0,
-                        workspace, x.device)
-        with torch.cuda.device(x.device):
-            _k._check(lib.kata_bwd_layer_norm(ctypes.byref(pr), p(g2), p(x2), p(weight), p(mean), p(rstd),
-                                              p(dx), p(dw), p(db), p(ws), _bytes(ws),
-                                              _k._stream(x.device)), "kata_bwd_layer_norm")
+        pr = _NORM.pack(x2.shape[0], N, _dtype(x.dtype), wt, 0.0, x2.stride(0), g2.stride(0), N, N)
+        ws = _workspace(_workspace_size("kata_bwd_layer_norm_workspace_size", pr) if params else 0,
+                        workspace, device)
+        _run("kata_bwd_layer_norm", device, pr, g2.data_ptr(), x2.data_ptr(), _ptr(weight), mean.data_ptr(),
+             rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), _bytes(ws))
     elif params:
         dw.zero_(), db.zero_()
     return dx, dw, db
