@@ -5,6 +5,8 @@
 
 namespace kata {
 
+constexpr int kDecayColumns = 64;         // value columns of a block of the chunk kernels
+
 // One recurrence over the tokens of every sequence, in the role's own time order (rev: last
 // token first):
 //     out_t = out_scale ( g^t a_t . E + kv_scale sum_{s<=t} g^(t-s) (a_t . b_s) c_s )
@@ -34,17 +36,16 @@ struct DecayArgs {
   int n_seg;                              // batch form: segments of a sequence
   int n_slots;                            // segment slots over all sequences
   int nvb;                                // value-column blocks
+  int scan;                               // a state pass and a scan run before the walk, and write fin
 };
 
-// exact_state: the terms of the state are added without rounding a factor to bf16.
-// state_pass: only the sums over each sequence's segments but its last, into role.states.
+// exact_state: the terms of fin are added without rounding a factor to bf16.
+// state_pass: only the sums over each sequence's segments, into role.states (the last one's where
+// fin is wanted).
 hipError_t launch_decay_chunks(DecayArgs& a, bool bf16, bool exact_state, bool state_pass,
                                hipStream_t st);
-// The segments' sums in role.states become their entry states.
+// The segments' sums in role.states become their entry states, and fin is written.
 hipError_t launch_decay_scan(const DecayArgs& a, hipStream_t st);
-// Value columns of one block of the chunk kernels, for the widest role.
-int decay_block_columns(bool bf16, int dk, int dv);
-
 hipError_t launch_decay_decode(bool bf16, int B, int T, int H, int dk, int dv,
                                const long long sq[3], const long long sk[3],
                                const long long sv[3], const long long so[3], const void* q,

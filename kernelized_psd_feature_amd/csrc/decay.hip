@@ -13,15 +13,23 @@
 // one segment and the walk runs alone.
 //
 // Layout (256 threads, four waves; tiles are 16 x 16, K steps 32 wide; fragment conventions as in
-// mfma_util.h with K slot r of lane group g being index 8 g + r of the step):
-//   - scores: wave w computes rows 16 w .. of P (transposed, K as the first operand, so that a
-//     lane ends with four neighbouring keys of one row), weights them, and leaves them in LDS;
-//   - the value columns are split over the waves, 16 NT each: a wave keeps the whole state of
-//     its columns in registers, and the state's accumulators are the operand of the readout
-//     without any exchange.  For that, row 4 g + b of state tile 2 m + a is dk index
-//     32 m + 8 g + 4 a + b: slots 0..7 of lane group g are then indices 8 g .. 8 g + 7 of step m,
-//     the order of a plain 16-byte read of a q row;
-//   - outputs are computed transposed (columns x rows), so a lane stores four neighbouring ones.
+// mfma_util.h).  Both operands of a product enumerate its K step in one order, of two: "straight"
+// (slot r of lane group g is index 8 g + r) or "split" (slots 0..3 are 4 g + r, slots 4..7 are
+// 16 + 4 g + r - 4, the order in which two accumulator tiles hold their rows).
+//   - scores (straight over dk): wave w computes rows 16 w .. of P, transposed, K as the first
+//     operand, so that a lane ends with four neighbouring keys of one row, weights them, and
+//     leaves them in LDS;
+//   - the value columns are split over the waves, 16 each: a wave keeps the whole state of its
+//     columns in registers, and the state's accumulators are the operand of the readout (split
+//     over dk) without any exchange;
+//   - products over keys are split: the transposing reads of V and K^T then take rows 0..7 of 16
+//     at a time, which the row strides below spread over the banks;
+//   - outputs are computed transposed (columns x rows), so a lane stores four neighbouring ones;
+//     they are stored while the next chunk is staged, so that the wait for its loads does not
+//     wait for stores just issued;
+//   - a chunk is straight code: the chunk that may end early is a second copy of it, every wave
+//     computes all four score tiles, and the state is read out and added to before the wait for the
+//     other waves' weights, so the compiler overlaps the products' reads.
 // fp32 problems run the same code with eight fp32 MFMAs (K = 4) for one K step.
 #include <type_traits>
 
@@ -60,7 +68,7 @@ __device__ __forceinline__ f32x4 mma(const f32x8& a, const f32x8& b, f32x4 c) {
   return c;
 }
 
-// Slots 0..7 from eight neighbouring elements.
+// Straight slots of a row: eight neighbouring elements.
 __device__ __forceinline__ bf16x8 row_frag(const __bf16* p) {
   return __builtin_bit_cast(bf16x8, ld16(p));
 }
@@ -68,25 +76,39 @@ __device__ __forceinline__ f32x8 row_frag(const float* p) {
   const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
-
-// Slots 0..7 from eight rows of one column: lane i of a 16-lane group g gets rows 8 g .. 8 g + 7
-// of column cs (i / 4) + i % 4, p pointing at row 0 of column 0 (LD: elements of a row).
-template <int LD, int CS>
+// Rows that are read in split slots are kept so that these are neighbours: run u of four elements
+// of every 32 (0..7) lies at place 2 (u % 4) + u / 4, and row_frag reads split slots.  (As two 8-byte
+// reads 16 elements apart, which the compiler makes one instruction, they met each bank twice.)
+__device__ __forceinline__ constexpr int split_place(int col) {
+  return (col & ~31) + 8 * ((col >> 2) & 3) + 4 * ((col >> 4) & 1) + (col & 3);
+}
+// Straight slots 8 g .. 8 g + 7 of 32 columns of such a row.
+__device__ __forceinline__ bf16x8 straight_frag(const __bf16* p, int g) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p + split_place(8 * g));
+  const uint2 b = *reinterpret_cast<const uint2*>(p + split_place(8 * g + 4));
+  return __builtin_bit_cast(bf16x8, uint4{a.x, a.y, b.x, b.y});
+}
+__device__ __forceinline__ f32x8 straight_frag(const float* p, int g) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p + split_place(8 * g));
+  const f32x4 b = *reinterpret_cast<const f32x4*>(p + split_place(8 * g + 4));
+  return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+// Split slots of column i, i the lane's place in its group of 16, of 32 rows of LD elements at p.
+// bf16 by the transposing read (v_frag in mfma_util.h).
+template <int LD>
 __device__ __forceinline__ bf16x8 column_frag(const __bf16* p, int lane) {
-  const int g = lane >> 4, j = lane & 15;
-  const __bf16* at = p + (8 * g + (j >> 2)) * LD + CS * (j & 3);
+  const __bf16* at = p + (4 * (lane >> 4) + ((lane & 15) >> 2)) * LD + 4 * (lane & 3);
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * LD));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 16 * LD));
   const uint2 ul = __builtin_bit_cast(uint2, lo), uh = __builtin_bit_cast(uint2, hi);
   return __builtin_bit_cast(bf16x8, uint4{ul.x, ul.y, uh.x, uh.y});
 }
-template <int LD, int CS>
+template <int LD>
 __device__ __forceinline__ f32x8 column_frag(const float* p, int lane) {
-  const int g = lane >> 4, i = lane & 15;
-  const float* at = p + 8 * g * LD + CS * (i >> 2) + (i & 3);
+  const float* at = p + 4 * (lane >> 4) * LD + (lane & 15);
   f32x8 x;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) x[r] = at[r * LD];
+  for (int r = 0; r < 8; ++r) x[r] = at[(16 * (r / 4) + r % 4) * LD];
   return x;
 }
 
@@ -98,18 +120,31 @@ __device__ __forceinline__ f32x8 pack_frag(const f32x4& a, const f32x4& b, float
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-__device__ __forceinline__ bool has_nonfinite(const bf16x8& x) {
-  return nonfinite_bf16x8(__builtin_bit_cast(uint4, x)) != 0u;
+// Adds 0 x to t for every element: t becomes nan where one is an infinity or nan.
+__device__ __forceinline__ float poison(const bf16x8& x, float t) {
+  const uint4 u = __builtin_bit_cast(uint4, x);
+  typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+  const b2 z = __builtin_bit_cast(b2, 0u);
+  t = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, u.x), z, t, false);
+  t = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, u.y), z, t, false);
+  t = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, u.z), z, t, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, u.w), z, t, false);
 }
-__device__ __forceinline__ bool has_nonfinite(const f32x8& x) {
-  bool bad = false;
+__device__ __forceinline__ float poison(const f32x8& x, float t) {
 #pragma unroll
-  for (int r = 0; r < 8; ++r) bad |= !(fabsf(x[r]) < __builtin_inff());
-  return bad;
+  for (int r = 0; r < 8; ++r) t = fmaf(x[r], 0.f, t);
+  return t;
 }
 
+// Four neighbouring elements as they are stored.
+template <typename T>
+using Quad = std::conditional_t<sizeof(T) == 2, uint2, f32x4>;
+__device__ __forceinline__ uint2 quad(const f32x4& x, __bf16) {
+  return uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+}
+__device__ __forceinline__ f32x4 quad(const f32x4& x, float) { return x; }
 __device__ __forceinline__ void store4(__bf16* p, const f32x4& x) {
-  *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+  *reinterpret_cast<uint2*>(p) = quad(x, __bf16());
 }
 __device__ __forceinline__ void store4(float* p, const f32x4& x) {
   *reinterpret_cast<f32x4*>(p) = x;
@@ -167,55 +202,97 @@ __device__ __forceinline__ bool find_segment(const DecayArgs& A, int slot, int* 
 // W / (4 V) 16-byte vectors a thread.
 template <typename T, int W>
 struct Stage {
-  static constexpr int V = Elem<T>::V, PER = W / V, N = kC * PER / kThreads;
-  static_assert(N >= 1, "a vector a thread");
+  static constexpr int V = Elem<T>::V, PER = W / V, N = kC * PER / kThreads, kRows = kThreads / PER;
+  static_assert(N >= 1 && kC % kRows == 0, "whole rows a step");
+  const T* p;                             // the thread's first vector of the next chunk
   uint4 x[N];
-  // row 0 at p, rows st elements apart (negative in reversed time)
-  __device__ __forceinline__ void load(const T* p, long long st, int n, int width) {
+  // row 0 at base, rows st elements apart (negative in reversed time)
+  __device__ __forceinline__ Stage(const T* base, long long st)
+      : p(base + (long long)(threadIdx.x / PER) * st + (threadIdx.x % PER) * V) {}
+  __device__ __forceinline__ void fetch(long long st) {             // 64 whole rows
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const uint4*>(p + i * kRows * st);
+    p += kC * st;
+  }
+  __device__ __forceinline__ void fetch(long long st, int n, int width) {
+    const int row = threadIdx.x / PER, col = (threadIdx.x % PER) * V;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int idx = threadIdx.x + kThreads * i, row = idx / PER, col = (idx % PER) * V;
       x[i] = uint4{0u, 0u, 0u, 0u};
-      if (row < n && col < width) x[i] = *reinterpret_cast<const uint4*>(p + row * st + col);
+      if (row + i * kRows < n && col < width) x[i] = *reinterpret_cast<const uint4*>(p + i * kRows * st);
     }
+    p += kC * st;
   }
   template <int LD>
   __device__ __forceinline__ void put(T* tile) const {
+    T* at = tile + threadIdx.x / PER * LD + (threadIdx.x % PER) * V;
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(at + i * kRows * LD) = x[i];
+  }
+  // the rows' runs of four elements at their split places
+  template <int LD>
+  __device__ __forceinline__ void put_split(T* tile) const {
+    const int col = (threadIdx.x % PER) * V;
+    T* at = tile + threadIdx.x / PER * LD;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int idx = threadIdx.x + kThreads * i, row = idx / PER, col = (idx % PER) * V;
-      *reinterpret_cast<uint4*>(tile + row * LD + col) = x[i];
+      if constexpr (V == 8) {
+        *reinterpret_cast<uint2*>(at + i * kRows * LD + split_place(col)) = uint2{x[i].x, x[i].y};
+        *reinterpret_cast<uint2*>(at + i * kRows * LD + split_place(col + 4)) = uint2{x[i].z, x[i].w};
+      } else {
+        *reinterpret_cast<uint4*>(at + i * kRows * LD + split_place(col)) = x[i];
+      }
     }
   }
 };
 
-template <typename T, int DK, int NT>
+// Row strides of the LDS tiles, in elements.  bf16 (64 banks of 4 bytes, s the stride in words): a
+// read of one 16-byte vector of 16 rows is free of conflicts for s = 4 odd mod 64, the transposing
+// reads of 16 bytes of 8 rows for s = 8 odd, and nearly for s = 36.  K is read both ways: s = 36 at
+// 64 columns, and at 128, where the padding to 36 mod 64 would not fit, s = 72 for the more
+// frequent transposed ones.
+template <typename T, int DK>
 struct Tiles {
-  static constexpr int V = Elem<T>::V;
-  static constexpr int DV = 64 * NT;                // value columns of a block
-  static constexpr int LK = DK + V, LV = DV + V, LP = kC + V;   // row strides: one vector of padding
-  static constexpr int kState = kC * (LK + LV), kWalk = kState + kC * (LK + LP);
+  static constexpr bool kBf = sizeof(T) == 2;
+  static constexpr int DV = kDecayColumns;
+  static constexpr int LQ = DK + 16 / sizeof(T), LK = kBf && DK == 128 ? DK + 16 : LQ;
+  static constexpr int LV = DV + (kBf ? 16 : 4), LP = kC + 16 / sizeof(T);
+  // Two buffers of the operands' tiles where two workgroups a CU still fit: the next chunk is staged
+  // while this one is computed, for one barrier and one exposed LDS write less a chunk.
+  static constexpr int kBuffers = kBf && DK <= 64 ? 2 : 1;
+  static constexpr int stage(bool state_pass) { return kC * (LK + LV + (state_pass ? 0 : LQ)); }
   static constexpr int kHead = 288;                 // an int, then the powers g^0 .. g^64
   static constexpr int bytes(bool state_pass) {
-    return kHead + (state_pass ? kState : kWalk) * (int)sizeof(T);
+    return kHead + (kBuffers * stage(state_pass) + (state_pass ? 0 : kC * LP)) * (int)sizeof(T);
+  }
+  // workgroups a CU the registers are held to (256 threads: as many waves a SIMD)
+  static constexpr int occupancy(bool state_pass) {
+    return !kBf ? (DK == 128 ? 1 : 2) : DK == 128 ? (state_pass ? 3 : 2) : state_pass ? 4 : 2;
   }
 };
 
 // Value weights of the state's update, x = w v, as SPLIT bf16 terms that add up to it: two (2^-17 of
 // x: one rounded term puts the outputs 1.7 times as far off the exact ones as their own
 // rounding), or three, the whole fp32 product, for a state that the caller keeps; fp32 as it is.
+// An infinity among the values makes the later terms, and the state's entries, nan.
 template <int SPLIT>
 __device__ __forceinline__ void weigh(const bf16x8& v, const float (&w)[8], bf16x8 (&out)[SPLIT]) {
+  const uint4 u = __builtin_bit_cast(uint4, v);
+  const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+  uint32_t o[SPLIT][4];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    float x = w[r] * (float)v[r];
+  for (int r = 0; r < 4; ++r) {
+    float x = w[2 * r] * bf_lo(in[r]), y = w[2 * r + 1] * bf_hi(in[r]);
 #pragma unroll
     for (int k = 0; k < SPLIT; ++k) {
-      const __bf16 y = (__bf16)x;
-      out[k][r] = y;
-      x = fabsf((float)y) < __builtin_inff() ? x - (float)y : 0.f;   // inf and nan: once
+      o[k][r] = pack_bf16x2(x, y);
+      x -= bf_lo(o[k][r]);
+      y -= bf_hi(o[k][r]);
     }
   }
+#pragma unroll
+  for (int k = 0; k < SPLIT; ++k)
+    out[k] = __builtin_bit_cast(bf16x8, uint4{o[k][0], o[k][1], o[k][2], o[k][3]});
 }
 template <int SPLIT>
 __device__ __forceinline__ void weigh(const f32x8& v, const float (&w)[8], f32x8 (&out)[SPLIT]) {
@@ -223,20 +300,25 @@ __device__ __forceinline__ void weigh(const f32x8& v, const float (&w)[8], f32x8
   for (int r = 0; r < 8; ++r) out[0][r] = w[r] * v[r];
 }
 
-template <typename T, int DK, int NT, int SPLIT, bool kStatePass>
-__global__ __launch_bounds__(kThreads) void decay_chunks_kernel(DecayArgs A) {
-  using TL = Tiles<T, DK, NT>;
+template <typename T, int DK, int SPLIT, bool kStatePass>
+__global__ __launch_bounds__(kThreads, (Tiles<T, DK>::occupancy(kStatePass))) void decay_chunks_kernel(
+    DecayArgs A) {
+  using TL = Tiles<T, DK>;
   using frag = typename Elem<T>::frag;
-  constexpr int LK = TL::LK, LV = TL::LV, LP = TL::LP, DV = TL::DV, M = DK / 32, NS = DK / 16;
+  constexpr int DV = TL::DV, M = DK / 32, NS = DK / 16, LQ = TL::LQ, LK = TL::LK, LV = TL::LV, LP = TL::LP;
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const pw = reinterpret_cast<float*>(lds) + 4;
-  T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
-  T* const sV = sK + kC * LK;
-  T* const sQ = sV + kC * LV;                       // walk only
-  T* const sP = sQ + kC * LK;
+  constexpr bool kTwo = TL::kBuffers == 2;
+  constexpr int kStage = TL::stage(kStatePass);
+  T* const sP = reinterpret_cast<T*>(lds + TL::kHead);             // walk only
+  T* sK = sP + (kStatePass ? 0 : kC * LP);
+  T* sV = sK + kC * LK;
+  T* sQ = sV + kC * LV;                             // walk only
+  int other = kStage;                               // from this chunk's tiles to the next one's
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, l16 = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // The value blocks and roles of one (slot, head) read the same rows: their workgroups get ids
   // congruent mod 8, one XCD.
   const long long x = blockIdx.x;
@@ -265,7 +347,7 @@ __global__ __launch_bounds__(kThreads) void decay_chunks_kernel(DecayArgs A) {
   const long long SE = (long long)R.dk * R.dv, st_off = ((long long)s.seq * A.H + h) * SE;
   const int rs = R.init_trans ? 1 : R.dv, cs = R.init_trans ? R.dk : 1;   // strides of init
   if (s.seg >= n_seg) {
-    if (!kStatePass && s.len == 0 && s.seg == 0 && R.fin)          // an empty sequence
+    if (!kStatePass && !A.scan && s.len == 0 && s.seg == 0 && R.fin)          // an empty sequence
       for (int i = tid; i < R.dk * DV; i += kThreads) {
         const int r = i / DV, c = c0 + i % DV;
         if (c < R.dv)
@@ -275,224 +357,241 @@ __global__ __launch_bounds__(kThreads) void decay_chunks_kernel(DecayArgs A) {
     return;
   }
   const bool last_seg = s.seg == n_seg - 1;
-  if (kStatePass && last_seg) return;
+  if (kStatePass && last_seg && !R.fin) return;     // enters no entry state
   const int first = s.seg * L, behind = min(first + L, n_chunks);
+
+  // rows in the role's time order: row i of the sequence is start + i, or its mirror image
+  const int dir = R.rev ? -1 : 1, dk = R.dk, dv = R.dv;
+  const long long t0 = (R.rev ? s.start + s.len - 1 : s.start) + (long long)dir * kC * first;
+  const long long sta = dir * R.sa[1], stb = dir * R.sb[1], stc = dir * R.sc[1], sto = dir * R.so[1];
+  Stage<T, DK> ra(reinterpret_cast<const T*>(R.a) + s.b * R.sa[0] + t0 * R.sa[1] + h * R.sa[2], sta);
+  Stage<T, DK> rb(reinterpret_cast<const T*>(R.b) + s.b * R.sb[0] + t0 * R.sb[1] + h * R.sb[2], stb);
+  Stage<T, DV> rc(reinterpret_cast<const T*>(R.c) + s.b * R.sc[0] + t0 * R.sc[1] + h * R.sc[2] + c0, stc);
+  const int wc = 16 * w;                            // the wave's columns in the block
+  const bool whole_rows = dk == DK && dv - c0 >= DV;
+  const bool live_col = c0 + wc + 4 * g < dv;
+  T* po = out + (t0 + (long long)dir * l16) * R.so[1] + wc + 4 * g;   // the lane's first output
+
+  auto fetch = [&](int n) {
+    if (n == kC && whole_rows) {                    // uniform
+      if constexpr (!kStatePass) ra.fetch(sta);
+      rb.fetch(stb);
+      rc.fetch(stc);
+    } else {
+      if constexpr (!kStatePass) ra.fetch(sta, n, dk);
+      rb.fetch(stb, n, dk);
+      rc.fetch(stc, n, dv - c0);
+    }
+  };
+  const int n_last = min(kC, s.len - kC * (behind - 1));   // rows of the segment's last chunk
+  fetch(behind - first > 1 ? kC : n_last);
 
   if (tid <= kC) pw[tid] = decay_power(log2_decay(A.log_decay[h]), tid);
   __syncthreads();
-  const int wc = 16 * NT * w;                       // the wave's columns in the block
 
-  // rows in the role's time order: row i of the sequence is start + i, or its mirror image
-  const int dir = R.rev ? -1 : 1, t0 = R.rev ? s.start + s.len - 1 : s.start;
-  const long long sta = dir * R.sa[1], stb = dir * R.sb[1], stc = dir * R.sc[1], sto = dir * R.so[1];
-  const T* const pa = reinterpret_cast<const T*>(R.a) + s.b * R.sa[0] + t0 * R.sa[1] + h * R.sa[2];
-  const T* const pb = reinterpret_cast<const T*>(R.b) + s.b * R.sb[0] + t0 * R.sb[1] + h * R.sb[2];
-  const T* const pc = reinterpret_cast<const T*>(R.c) + s.b * R.sc[0] + t0 * R.sc[1] + h * R.sc[2] + c0;
-  T* const po = out + t0 * R.so[1];
-
-  // state tiles: S[i][n] lane holds row 32 (i / 2) + 8 g + 4 (i % 2) + r, column wc + 16 n + l16
-  f32x4 S[NS][NT];
-  const bool from_scan = n_seg > 1;
-  bool has_state = !kStatePass && (from_scan || R.init);
+  // state tiles: S[i] lane holds rows 16 i + 4 g + r of column wc + l16
+  f32x4 S[NS];
   {
+    const bool from_scan = n_seg > 1;
     const float* src = from_scan ? R.states + ((long long)slot * A.H + h) * SE : R.init + st_off;
-    const int r1 = from_scan ? R.dv : rs, q1 = from_scan ? 1 : cs;
+    const int r1 = from_scan ? dv : rs, q1 = from_scan ? 1 : cs;
     const float f = from_scan || R.rev ? 1.f : pw[1];
+    const int col = c0 + wc + l16;
+    const bool any = !kStatePass && (from_scan || R.init) && col < dv;
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
+    for (int i = 0; i < NS; ++i) {
+      S[i] = zero4();
+      const int row = 16 * i + 4 * g;
+      if (any)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        S[i][n] = zero4();
-        const int row = 32 * (i / 2) + 8 * g + 4 * (i % 2), col = c0 + wc + 16 * n + l16;
-        if (has_state && col < R.dv)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (row + r < R.dk) S[i][n][r] = f * src[(long long)(row + r) * r1 + (long long)col * q1];
-      }
+        for (int r = 0; r < 4; ++r)
+          if (row + r < dk) S[i][r] = f * src[(long long)(row + r) * r1 + (long long)col * q1];
+    }
   }
 
-  // powers: dec[j][r] of (row, key) = (16 w + l16, 16 j + 4 g + r), rowp[i] of row 16 i + l16,
-  // vw[m][r] of key 32 m + 8 g + r
-  float dec[4][4], rowp[4], vw[2][8];
+  // powers: dec[j][r] of (row, key) = (16 w + l16, 16 j + 4 g + r), rowp[i] of row 16 i + l16, vw[m][r]
+  // of the key in slot r of the m-th 32
+  const float g16 = pw[16];
+  float dec[4][4], row0 = 0.f, vw[2][8];
   if constexpr (!kStatePass) {
+    row0 = pw[l16] * R.out_scale;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      rowp[j] = pw[16 * j + l16] * R.out_scale;
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         dec[j][r] = pw[max(16 * (w - j) + l16 - 4 * g - r, 0)] * (R.out_scale * R.kv_scale);
-    }
-    // keys of the K step that no score tile of this wave covers
-    if (!(w & 1)) store4(sP + (16 * w + l16) * LP + 16 * (w + 1) + 4 * g, zero4());
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int r = 0; r < 8; ++r) vw[m][r] = pw[kC - 32 * m - 8 * g - r] * R.kv_scale;
+    for (int r = 0; r < 8; ++r) vw[m][r] = pw[kC - 32 * m - 16 * (r / 4) - 4 * g - r % 4] * R.kv_scale;
   float whole = pw[kC];
 
-  Stage<T, DK> ra, rb;
-  Stage<T, DV> rc;
-  auto fetch = [&](int c) {
-    const int n = min(kC, s.len - kC * c);
-    if constexpr (!kStatePass) ra.load(pa + (long long)kC * c * sta, sta, n, R.dk);
-    rb.load(pb + (long long)kC * c * stb, stb, n, R.dk);
-    rc.load(pc + (long long)kC * c * stc, stc, n, R.dv - c0);
+  Quad<T> O[4];                                     // outputs of the last chunk
+  auto store = [&](int rows) {
+    if (live_col)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (16 * i + l16 < rows) *reinterpret_cast<Quad<T>*>(po + 16 * i * sto) = O[i];
+    po += kC * sto;
   };
-  fetch(first);
-  for (int c = first; c < behind; ++c) {
-    const int n = min(kC, s.len - kC * c);
-    __syncthreads();                                // the last chunk's tiles have been read
-    rb.template put<LK>(sK);
-    rc.template put<LV>(sV);
-    if constexpr (!kStatePass) ra.template put<LK>(sQ);
-    if (c + 1 < behind) fetch(c + 1);
-    __syncthreads();
 
-    f32x4 O[4][NT];
+  auto stage = [&](int to) {
+    rb.template put<LK>(sK + to);
+    rc.template put<LV>(sV + to);
+    if constexpr (!kStatePass) ra.template put_split<LQ>(sQ + to);
+  };
+  if constexpr (kTwo) {
+    stage(0);
+    if (behind - first > 1) fetch(behind - first > 2 ? kC : n_last);
+  }
+
+  // one chunk, its rows on their way (or, with two buffers, staged and the next one's on their
+  // way); kLast: the segment's last one, n_last rows
+  auto chunk = [&](int c, auto last) {
+    constexpr bool kLast = decltype(last)::value;
+    // rows of the chunk after the next one to be staged
+    const int n_next = c + (kTwo ? 3 : 2) < behind ? kC : n_last;
+    __syncthreads();                                // the last chunk's tiles have been read
+    if constexpr (!kTwo) {
+      stage(0);
+      if constexpr (!kStatePass)
+        if (c > first) store(kC);
+      if constexpr (kStatePass && !kLast) fetch(n_next);
+      __syncthreads();
+    } else if constexpr (!kStatePass) {
+      if (c > first) store(kC);
+    }
+
+    f32x4 o[4];
     if constexpr (!kStatePass) {
       frag qf[M];
+      f32x4 p[4];
 #pragma unroll
-      for (int m = 0; m < M; ++m) qf[m] = row_frag(sQ + (16 * w + l16) * LK + 32 * m + 8 * g);
+      for (int m = 0; m < M; ++m) qf[m] = straight_frag(sQ + (16 * w + l16) * LQ + 32 * m, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = zero4();
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          p[j] = mma(row_frag(sK + (16 * j + l16) * LK + 32 * m + 8 * g), qf[m], p[j]);
+      // weights, zero by selection where the key is later (bf16: rounded, an operand)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j > w) continue;                        // uniform in the wave
-        f32x4 p = zero4();
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-          p = mma(row_frag(sK + (16 * j + l16) * LK + 32 * m + 8 * g), qf[m], p);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          p[r] *= dec[j][r];
-          if (j == w && 4 * g + r > l16) p[r] = 0.f;   // select, never multiply
-        }
-        // bf16: the weights are an operand of the next product
-        store4(sP + (16 * w + l16) * LP + 16 * j + 4 * g, p);
+        for (int r = 0; r < 4; ++r)
+          p[j][r] = 16 * j + 4 * g + r > 16 * w + l16 ? 0.f : p[j][r] * dec[j][r];
+        store4(sP + (16 * w + l16) * LP + split_place(16 * j + 4 * g), p[j]);
       }
       // readout of the entry state (bf16: rounded as an operand, the sum itself stays fp32)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) o[i] = zero4();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) O[i][nt] = zero4();
-      if (has_state) {
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-          frag sf[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) sf[nt] = pack_frag(S[2 * m][nt], S[2 * m + 1][nt], T());
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const frag qr = row_frag(sQ + (16 * i + l16) * LK + 32 * m + 8 * g);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) O[i][nt] = mma(sf[nt], qr, O[i][nt]);
-          }
-        }
+      for (int m = 0; m < M; ++m) {
+        const frag sf = pack_frag(S[2 * m], S[2 * m + 1], T());
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) O[i][nt] *= rowp[i];
+          o[i] = mma(sf, row_frag(sQ + (16 * i + l16) * LQ + 32 * m + 8 * g), o[i]);
       }
-      __syncthreads();                              // the weights are there
+      float f = row0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[i] *= f;
+        f *= g16;
+      }
     }
 
-    const bool ends = last_seg && c + 1 == behind;
-    const bool update = kStatePass || c + 1 < behind || (ends && R.fin);
-    if (ends && update) {
-      // the state behind token n - 1 (reversed: its product with g, the gradient of the initial
-      // state); keys behind n are zero rows
-      const int e = n - (R.rev ? 0 : 1);
+    if constexpr (kTwo && !kLast) {                 // the next chunk into the other buffer
+      stage(other);
+      if (c + 2 < behind) fetch(n_next);
+    }
+
+    frag vf[2];                                     // the wave's values, 32 keys each
+#pragma unroll
+    for (int m = 0; m < 2; ++m) vf[m] = column_frag<LV>(sV + 32 * m * LV + wc, lane);
+    if (kLast && last_seg) {
+      // The state behind the last token, n_last - 1 (reversed: its product with g, the gradient of
+      // the initial state).  Keys behind it are zero rows.
+      const int e = n_last - (R.rev ? 0 : 1);
       whole = pw[e];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-          vw[m][r] = pw[max(e - 32 * m - 8 * g - r, 0)] * R.kv_scale;
+          vw[m][r] = pw[max(e - 32 * m - 16 * (r / 4) - 4 * g - r % 4, 0)] * R.kv_scale;
     }
-    if (update)
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
+    for (int i = 0; i < NS; ++i) S[i] *= whole;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) S[i][nt] *= whole;
-
+    for (int m = 0; m < 2; ++m) {
+      frag vx[SPLIT];
+      weigh<SPLIT>(vf[m], vw[m], vx);
+      frag kf[NS];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {                   // 32 keys
-      frag vf[NT];
+      for (int i = 0; i < NS; ++i) kf[i] = column_frag<LK>(sK + 32 * m * LK + 16 * i, lane);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) vf[nt] = column_frag<LV, 4>(sV + 32 * m * LV + wc + 16 * nt, lane);
-      if constexpr (!kStatePass) {
-        bool bad = false;
+      for (int k = 0; k < SPLIT; ++k)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) bad |= has_nonfinite(vf[nt]);
-        if (!__any(bad)) {
-#pragma unroll
-          for (int i = 2 * m; i < 4; ++i) {
-            const frag pf = row_frag(sP + (16 * i + l16) * LP + 32 * m + 8 * g);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) O[i][nt] = mma(vf[nt], pf, O[i][nt]);
-          }
-        } else {
-          // An infinity or nan among the values: in the product above a masked weight of zero
-          // would still meet it and leave nan in earlier rows, so the pairs are added one by one.
-#pragma unroll
-          for (int i = 2 * m; i < 4; ++i)
-#pragma unroll 1
-            for (int key = 32 * m; key < min(32 * m + 32, 16 * i + 16); ++key) {
-              if (key > 16 * i + l16) continue;
-              const float p = to_f32(sP[(16 * i + l16) * LP + key]);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  O[i][nt][r] += p * to_f32(sV[key * LV + wc + 16 * nt + 4 * g + r]);
-            }
-        }
-      }
-      if (update) {
-        frag vx[NT][SPLIT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) weigh<SPLIT>(vf[nt], vw[m], vx[nt]);
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const frag kf = column_frag<LK, 8>(sK + 32 * m * LK + 32 * (i / 2) + 4 * (i % 2), lane);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < SPLIT; ++k) S[i][nt] = mma(kf, vx[nt][k], S[i][nt]);
-        }
-      }
+        for (int i = 0; i < NS; ++i) S[i] = mma(kf[i], vx[k], S[i]);
     }
-    has_state = true;
 
     if constexpr (!kStatePass) {
+      const float sick = poison(vf[1], poison(vf[0], 0.f));
+      // The loads are issued late: early ones, a whole chunk ahead of their use, measured slower
+      // (131k tokens: 276 us for 252), as many in flight as there are then cost more than they hide.
+      if constexpr (!kLast && !kTwo) fetch(n_next);
+      __syncthreads();                              // the weights are there
+      if (!__any(sick != sick)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int row = 16 * i + l16, col = wc + 16 * nt + 4 * g;
-          if (row < n && c0 + col < R.dv) store4(po + (long long)(kC * c + row) * sto + col, O[i][nt]);
-        }
+          for (int i = 2 * m; i < 4; ++i)
+            o[i] = mma(vf[m], row_frag(sP + (16 * i + l16) * LP + 32 * m + 8 * g), o[i]);
+      } else {
+        // An infinity or nan among the values: in the product above a masked weight of zero
+        // would still meet it and leave nan in earlier rows, so the pairs are added one by one.
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+          for (int key = 0; key < 16 * i + 16; ++key) {
+            if (key > 16 * i + l16) continue;
+            const float p = to_f32(sP[(16 * i + l16) * LP + split_place(key)]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[i][r] += p * to_f32(sV[key * LV + wc + 4 * g + r]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) O[i] = quad(o[i], T());
     }
-  }
+    if constexpr (kTwo && !kLast) {
+      sK += other;
+      sV += other;
+      sQ += other;
+      other = -other;
+    }
+  };
+  for (int c = first; c < behind - 1; ++c) chunk(c, std::false_type());
+  chunk(behind - 1, std::true_type());
+  if constexpr (!kStatePass) store(n_last);
 
   float* dst = kStatePass ? R.states + ((long long)slot * A.H + h) * SE
-               : last_seg && R.fin ? R.fin + st_off : nullptr;
-  if (!dst) return;
+               : last_seg && R.fin && !A.scan ? R.fin + st_off : nullptr;
+  const int col = c0 + wc + l16;
+  if (!dst || col >= dv) return;
 #pragma unroll
   for (int i = 0; i < NS; ++i)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = 32 * (i / 2) + 8 * g + 4 * (i % 2), col = c0 + wc + 16 * nt + l16;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (row + r < R.dk && col < R.dv) dst[(long long)(row + r) * R.dv + col] = S[i][nt][r];
-    }
+    for (int r = 0; r < 4; ++r)
+      if (16 * i + 4 * g + r < dk) dst[(long long)(16 * i + 4 * g + r) * dv + col] = S[i][r];
 }
 
 // ---- scan ------------------------------------------------------------------------------------
 // Per (sequence, head, role) and element, over the segments in order: the sum U_j of segment j is
-// replaced by the entry state E_j, E_{j+1} = g^SL E_j + U_j.  One thread has four neighbouring
-// elements; the loads of four segments are in flight together.  Bound: HBM (or the Infinity Cache
-// that the state pass has just written), one read and one write of the segment states.
+// replaced by the entry state E_j, E_{j+1} = g^SL E_j + U_j; the last sum, over the n tokens that the
+// segment has, completes the final state, g^(n-1) E + U (reversed: g^n E + U).  One thread has four
+// neighbouring elements; the loads of four segments are in flight together.  Bound: HBM (or the
+// Infinity Cache that the state pass has just written), one read and one write of the states.
 __global__ __launch_bounds__(kThreads) void decay_scan_kernel(DecayArgs A) {
   const int SE = A.role[0].dk * A.role[0].dv, nb = (SE / 4 + kThreads - 1) / kThreads;
   long long x = blockIdx.x;
@@ -509,37 +608,41 @@ __global__ __launch_bounds__(kThreads) void decay_scan_kernel(DecayArgs A) {
     len = max(cu_at(A, seq + 1) - first, 0);
   }
   const int n = (len + SL - 1) / SL;
-  if (n < 2 || e4 >= SE) return;
+  if ((n < 2 && !R.fin) || e4 >= SE) return;
   const double lg = log2_decay(A.log_decay[h]);
   const float f = decay_power(lg, SL);
+  const long long st_off = ((long long)seq * A.H + h) * SE;
   float4 e = {0.f, 0.f, 0.f, 0.f};
   if (R.init) {
-    const float* p = R.init + ((long long)seq * A.H + h) * SE;
-    const float f0 = R.rev ? 1.f : decay_power(lg, 1);
+    const float f0 = R.rev || len == 0 ? 1.f : decay_power(lg, 1);
     float y[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = (e4 + r) / R.dv, j = (e4 + r) % R.dv;
-      y[r] = f0 * p[R.init_trans ? j * R.dk + i : e4 + r];
+      y[r] = f0 * R.init[st_off + (R.init_trans ? j * R.dk + i : e4 + r)];
     }
     e = float4{y[0], y[1], y[2], y[3]};
   }
   float* p = R.states + ((long long)slot * A.H + h) * SE + e4;
   const long long step = (long long)A.H * SE;
+  const int sums = R.fin ? n : n - 1;
   for (int j = 0; j < n; j += 4) {
     float4 u[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       u[r] = float4{0.f, 0.f, 0.f, 0.f};
-      if (j + r < n - 1) u[r] = *reinterpret_cast<const float4*>(p + (j + r) * step);
+      if (j + r < sums) u[r] = *reinterpret_cast<const float4*>(p + (j + r) * step);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      if (j + r < n) *reinterpret_cast<float4*>(p + (j + r) * step) = e;
-      e.x = fmaf(f, e.x, u[r].x); e.y = fmaf(f, e.y, u[r].y);
-      e.z = fmaf(f, e.z, u[r].z); e.w = fmaf(f, e.w, u[r].w);
+      if (j + r >= n) break;
+      *reinterpret_cast<float4*>(p + (j + r) * step) = e;
+      const float fj = j + r < n - 1 ? f : decay_power(lg, len - (n - 1) * SL - (R.rev ? 0 : 1));
+      e.x = fmaf(fj, e.x, u[r].x); e.y = fmaf(fj, e.y, u[r].y);
+      e.z = fmaf(fj, e.z, u[r].z); e.w = fmaf(fj, e.w, u[r].w);
     }
   }
+  if (R.fin) *reinterpret_cast<float4*>(R.fin + st_off + e4) = e;
 }
 
 // ---- recurrent form ------------------------------------------------------------------------
@@ -620,7 +723,7 @@ __global__ __launch_bounds__(kThreads) void decay_decode_kernel(
   }
 }
 
-template <typename T, int DK, int NT, int SPLIT>
+template <typename T, int DK, int SPLIT>
 hipError_t launch_chunks_t(const DecayArgs& a, bool state_pass, hipStream_t st) {
   const long long units = (long long)a.n_slots * a.H;
   const long long blocks = (units + 7) / 8 * 8 * a.nvb * a.n_roles;
@@ -630,22 +733,20 @@ hipError_t launch_chunks_t(const DecayArgs& a, bool state_pass, hipStream_t st) 
     launch_kernel(kernel, dim3((unsigned)blocks), kThreads, bytes, st, a);
     return hipGetLastError();
   };
-  using TL = Tiles<T, DK, NT>;
-  return state_pass ? run(decay_chunks_kernel<T, DK, NT, SPLIT, true>, TL::bytes(true))
-                    : run(decay_chunks_kernel<T, DK, NT, SPLIT, false>, TL::bytes(false));
+  using TL = Tiles<T, DK>;
+  return state_pass ? run(decay_chunks_kernel<T, DK, SPLIT, true>, TL::bytes(true))
+                    : run(decay_chunks_kernel<T, DK, SPLIT, false>, TL::bytes(false));
 }
 
-template <typename T, int NT, int SPLIT>
+template <typename T, int SPLIT>
 hipError_t launch_chunks_d(const DecayArgs& a, int dk, bool state_pass, hipStream_t st) {
-  if (dk <= 32) return launch_chunks_t<T, 32, NT, SPLIT>(a, state_pass, st);
-  if (dk <= 64) return launch_chunks_t<T, 64, NT, SPLIT>(a, state_pass, st);
-  if (dk <= 128) return launch_chunks_t<T, 128, NT, SPLIT>(a, state_pass, st);
+  if (dk <= 32) return launch_chunks_t<T, 32, SPLIT>(a, state_pass, st);
+  if (dk <= 64) return launch_chunks_t<T, 64, SPLIT>(a, state_pass, st);
+  if (dk <= 128) return launch_chunks_t<T, 128, SPLIT>(a, state_pass, st);
   return hipErrorInvalidValue;
 }
 
 }  // namespace
-
-int decay_block_columns(bool bf16, int dk, int dv) { return bf16 && dv > 64 ? 128 : 64; }
 
 hipError_t launch_decay_chunks(DecayArgs& a, bool bf16, bool exact_state, bool state_pass,
                                hipStream_t st) {
@@ -654,14 +755,11 @@ hipError_t launch_decay_chunks(DecayArgs& a, bool bf16, bool exact_state, bool s
     dk = dk > a.role[r].dk ? dk : a.role[r].dk;
     dv = dv > a.role[r].dv ? dv : a.role[r].dv;
   }
-  const int cols = decay_block_columns(bf16, dk, dv);
-  a.nvb = (dv + cols - 1) / cols;
-  if (!bf16) return launch_chunks_d<float, 1, 1>(a, dk, state_pass, st);
-  if (cols == 128)
-    return exact_state ? launch_chunks_d<__bf16, 2, 3>(a, dk, state_pass, st)
-                       : launch_chunks_d<__bf16, 2, 2>(a, dk, state_pass, st);
-  return exact_state ? launch_chunks_d<__bf16, 1, 3>(a, dk, state_pass, st)
-                     : launch_chunks_d<__bf16, 1, 2>(a, dk, state_pass, st);
+  a.nvb = (dv + kDecayColumns - 1) / kDecayColumns;
+  if (!bf16) return launch_chunks_d<float, 1>(a, dk, state_pass, st);
+  // a state that the caller keeps gets the exact terms, in the pass that computes it
+  return exact_state && state_pass == (a.scan != 0) ? launch_chunks_d<__bf16, 3>(a, dk, state_pass, st)
+                                                    : launch_chunks_d<__bf16, 2>(a, dk, state_pass, st);
 }
 
 hipError_t launch_decay_scan(const DecayArgs& a, hipStream_t st) {

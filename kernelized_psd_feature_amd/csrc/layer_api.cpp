@@ -76,6 +76,7 @@ kata::DecayArgs decay_args(const kata_decay_problem* pr, const kata::DecayPlan& 
   a.L = p.L;
   a.n_seg = p.n_seg;
   a.n_slots = p.n_slots;
+  a.scan = p.scan;
   return a;
 }
 
@@ -139,7 +140,6 @@ kata_status kata_fwd_decay(const kata_decay_problem* pr, const void* q, const vo
   r.states = static_cast<float*>(workspace);
   r.dk = pr->dk; r.dv = pr->dv;
   r.out_scale = pr->scale; r.kv_scale = 1.f;
-  // a state that the caller keeps gets the exact terms
   return run_decay(a, p, pr->dtype == KATA_BF16, final_state != nullptr,
                    reinterpret_cast<hipStream_t>(stream), "decayed attention");
 }

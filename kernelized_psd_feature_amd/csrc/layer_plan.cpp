@@ -78,8 +78,8 @@ DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles) {
   constexpr int64_t kTarget = 512;
   DecayPlan p;
   const int64_t chunks = (int64_t(pr->T) + kDecayChunk - 1) / kDecayChunk;
-  const int cols = pr->dtype == KATA_BF16 && std::max(pr->dk, pr->dv) > 64 ? 128 : 64;
-  const int64_t blocks = int64_t(pr->H) * ((std::max(pr->dk, pr->dv) + cols - 1) / cols) * n_roles;
+  const int wide = n_roles > 1 ? std::max(pr->dk, pr->dv) : pr->dv;
+  const int64_t blocks = int64_t(pr->H) * ((wide + 63) / 64) * n_roles;   // 64 value columns each
   // segments that a sequence (packed: all tokens together) is cut into to fill the card
   const int64_t want = std::max<int64_t>(1, kTarget / (pr->packed ? blocks : blocks * pr->n_seq));
   int64_t L = std::max<int64_t>(std::min<int64_t>(chunks, 4), (chunks + want - 1) / want);
