@@ -5,8 +5,6 @@
 
 namespace kata {
 
-constexpr int kDecayColumns = 64;         // value columns of a block of the chunk kernels
-
 // One recurrence over the tokens of every sequence, in the role's own time order (rev: last
 // token first):
 //     out_t = out_scale ( g^t a_t . E + kv_scale sum_{s<=t} g^(t-s) (a_t . b_s) c_s )

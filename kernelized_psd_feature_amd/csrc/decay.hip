@@ -42,7 +42,7 @@ namespace kata {
 namespace {
 
 constexpr int kC = 64;                    // tokens of a chunk
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;             // of the scan and decode kernels
 
 typedef __attribute__((__vector_size__(8 * sizeof(float)))) float f32x8;
 
@@ -200,9 +200,9 @@ __device__ __forceinline__ bool find_segment(const DecayArgs& A, int slot, int* 
 // ---- staging -------------------------------------------------------------------------------
 // A chunk of one operand: 64 rows of W columns (those behind `width` and the rows behind n zero),
 // W / (4 V) 16-byte vectors a thread.
-template <typename T, int W>
+template <typename T, int W, int kThr>
 struct Stage {
-  static constexpr int V = Elem<T>::V, PER = W / V, N = kC * PER / kThreads, kRows = kThreads / PER;
+  static constexpr int V = Elem<T>::V, PER = W / V, N = kC * PER / kThr, kRows = kThr / PER;
   static_assert(N >= 1 && kC % kRows == 0, "whole rows a step");
   const T* p;                             // the thread's first vector of the next chunk
   uint4 x[N];
@@ -251,23 +251,23 @@ struct Stage {
 // reads of 16 bytes of 8 rows for s = 8 odd, and nearly for s = 36.  K is read both ways: s = 36 at
 // 64 columns, and at 128, where the padding to 36 mod 64 would not fit, s = 72 for the more
 // frequent transposed ones.
-template <typename T, int DK>
+template <typename T, int DK, int W>
 struct Tiles {
   static constexpr bool kBf = sizeof(T) == 2;
-  static constexpr int DV = kDecayColumns;
+  static constexpr int DV = 16 * W;                 // value columns of a block
   static constexpr int LQ = DK + 16 / sizeof(T), LK = kBf && DK == 128 ? DK + 16 : LQ;
   static constexpr int LV = DV + (kBf ? 16 : 4), LP = kC + 16 / sizeof(T);
-  // Two buffers of the operands' tiles where two workgroups a CU still fit: the next chunk is staged
+  // Two buffers of the operands' tiles where eight waves a CU still fit: the next chunk is staged
   // while this one is computed, for one barrier and one exposed LDS write less a chunk.
-  static constexpr int kBuffers = kBf && DK <= 64 ? 2 : 1;
+  static constexpr int kBuffers = kBf && (DK <= 64 || W == 8) ? 2 : 1;
   static constexpr int stage(bool state_pass) { return kC * (LK + LV + (state_pass ? 0 : LQ)); }
   static constexpr int kHead = 288;                 // an int, then the powers g^0 .. g^64
   static constexpr int bytes(bool state_pass) {
     return kHead + (kBuffers * stage(state_pass) + (state_pass ? 0 : kC * LP)) * (int)sizeof(T);
   }
-  // workgroups a CU the registers are held to (256 threads: as many waves a SIMD)
+  // waves a SIMD that the registers are held to (the launch bound counts workgroups a CU)
   static constexpr int occupancy(bool state_pass) {
-    return !kBf ? (DK == 128 ? 1 : 2) : DK == 128 ? (state_pass ? 3 : 2) : state_pass ? 4 : 2;
+    return (!kBf ? (DK == 128 ? 1 : 2) : !state_pass ? 2 : W == 8 ? 4 : DK == 128 ? 3 : 4) * 4 / W;
   }
 };
 
@@ -300,10 +300,11 @@ __device__ __forceinline__ void weigh(const f32x8& v, const float (&w)[8], f32x8
   for (int r = 0; r < 8; ++r) out[0][r] = w[r] * v[r];
 }
 
-template <typename T, int DK, int SPLIT, bool kStatePass>
-__global__ __launch_bounds__(kThreads, (Tiles<T, DK>::occupancy(kStatePass))) void decay_chunks_kernel(
+template <typename T, int DK, int W, int SPLIT, bool kStatePass>
+__global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) void decay_chunks_kernel(
     DecayArgs A) {
-  using TL = Tiles<T, DK>;
+  using TL = Tiles<T, DK, W>;
+  constexpr int kThr = 64 * W;
   using frag = typename Elem<T>::frag;
   constexpr int DV = TL::DV, M = DK / 32, NS = DK / 16, LQ = TL::LQ, LK = TL::LK, LV = TL::LV, LP = TL::LP;
   extern __shared__ __align__(16) char lds[];
@@ -339,7 +340,7 @@ __global__ __launch_bounds__(kThreads, (Tiles<T, DK>::occupancy(kStatePass))) vo
     if (kStatePass || !A.zero_tail) return;
     const int per_row = min(DV, R.dv - c0) / 4, r0 = kC * L * s.seg;
     const long long todo = (long long)min(kC * L, s.len - r0) * per_row;
-    for (long long i = tid; i < todo; i += kThreads)
+    for (long long i = tid; i < todo; i += kThr)
       store4(out + (s.start + r0 + i / per_row) * R.so[1] + i % per_row * 4, zero4());
     return;
   }
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(kThreads, (Tiles<T, DK>::occupancy(kStatePass))) vo
   const int rs = R.init_trans ? 1 : R.dv, cs = R.init_trans ? R.dk : 1;   // strides of init
   if (s.seg >= n_seg) {
     if (!kStatePass && !A.scan && s.len == 0 && s.seg == 0 && R.fin)          // an empty sequence
-      for (int i = tid; i < R.dk * DV; i += kThreads) {
+      for (int i = tid; i < R.dk * DV; i += kThr) {
         const int r = i / DV, c = c0 + i % DV;
         if (c < R.dv)
           R.fin[st_off + (long long)r * R.dv + c] =
@@ -364,9 +365,9 @@ __global__ __launch_bounds__(kThreads, (Tiles<T, DK>::occupancy(kStatePass))) vo
   const int dir = R.rev ? -1 : 1, dk = R.dk, dv = R.dv;
   const long long t0 = (R.rev ? s.start + s.len - 1 : s.start) + (long long)dir * kC * first;
   const long long sta = dir * R.sa[1], stb = dir * R.sb[1], stc = dir * R.sc[1], sto = dir * R.so[1];
-  Stage<T, DK> ra(reinterpret_cast<const T*>(R.a) + s.b * R.sa[0] + t0 * R.sa[1] + h * R.sa[2], sta);
-  Stage<T, DK> rb(reinterpret_cast<const T*>(R.b) + s.b * R.sb[0] + t0 * R.sb[1] + h * R.sb[2], stb);
-  Stage<T, DV> rc(reinterpret_cast<const T*>(R.c) + s.b * R.sc[0] + t0 * R.sc[1] + h * R.sc[2] + c0, stc);
+  Stage<T, DK, kThr> ra(reinterpret_cast<const T*>(R.a) + s.b * R.sa[0] + t0 * R.sa[1] + h * R.sa[2], sta);
+  Stage<T, DK, kThr> rb(reinterpret_cast<const T*>(R.b) + s.b * R.sb[0] + t0 * R.sb[1] + h * R.sb[2], stb);
+  Stage<T, DV, kThr> rc(reinterpret_cast<const T*>(R.c) + s.b * R.sc[0] + t0 * R.sc[1] + h * R.sc[2] + c0, stc);
   const int wc = 16 * w;                            // the wave's columns in the block
   const bool whole_rows = dk == DK && dv - c0 >= DV;
   const bool live_col = c0 + wc + 4 * g < dv;
@@ -409,17 +410,20 @@ __global__ __launch_bounds__(kThreads, (Tiles<T, DK>::occupancy(kStatePass))) vo
     }
   }
 
-  // powers: dec[j][r] of (row, key) = (16 w + l16, 16 j + 4 g + r), rowp[i] of row 16 i + l16, vw[m][r]
-  // of the key in slot r of the m-th 32
+  // scores: the wave's row tile, and its J key tiles from j0 on
+  constexpr int J = 16 / W;
+  const int rt = w & 3, j0 = J * (w >> 2);
+  // powers: dec[j][r] of (row, key) = (16 rt + l16, 16 (j0 + j) + 4 g + r), row0 of row l16, vw[m][r] of
+  // the key in slot r of the m-th 32
   const float g16 = pw[16];
-  float dec[4][4], row0 = 0.f, vw[2][8];
+  float dec[J][4], row0 = 0.f, vw[2][8];
   if constexpr (!kStatePass) {
     row0 = pw[l16] * R.out_scale;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        dec[j][r] = pw[max(16 * (w - j) + l16 - 4 * g - r, 0)] * (R.out_scale * R.kv_scale);
+        dec[j][r] = pw[max(16 * (rt - j0 - j) + l16 - 4 * g - r, 0)] * (R.out_scale * R.kv_scale);
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -466,23 +470,23 @@ __global__ __launch_bounds__(kThreads, (Tiles<T, DK>::occupancy(kStatePass))) vo
     f32x4 o[4];
     if constexpr (!kStatePass) {
       frag qf[M];
-      f32x4 p[4];
+      f32x4 p[J];
 #pragma unroll
-      for (int m = 0; m < M; ++m) qf[m] = straight_frag(sQ + (16 * w + l16) * LQ + 32 * m, g);
+      for (int m = 0; m < M; ++m) qf[m] = straight_frag(sQ + (16 * rt + l16) * LQ + 32 * m, g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = zero4();
+      for (int j = 0; j < J; ++j) p[j] = zero4();
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          p[j] = mma(row_frag(sK + (16 * j + l16) * LK + 32 * m + 8 * g), qf[m], p[j]);
+        for (int j = 0; j < J; ++j)
+          p[j] = mma(row_frag(sK + (16 * (j0 + j) + l16) * LK + 32 * m + 8 * g), qf[m], p[j]);
       // weights, zero by selection where the key is later (bf16: rounded, an operand)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          p[j][r] = 16 * j + 4 * g + r > 16 * w + l16 ? 0.f : p[j][r] * dec[j][r];
-        store4(sP + (16 * w + l16) * LP + split_place(16 * j + 4 * g), p[j]);
+          p[j][r] = 16 * (j0 + j) + 4 * g + r > 16 * rt + l16 ? 0.f : p[j][r] * dec[j][r];
+        store4(sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g), p[j]);
       }
       // readout of the entry state (bf16: rounded as an operand, the sum itself stays fp32)
 #pragma unroll
@@ -723,26 +727,27 @@ __global__ __launch_bounds__(kThreads) void decay_decode_kernel(
   }
 }
 
-template <typename T, int DK, int SPLIT>
+template <typename T, int DK, int W, int SPLIT>
 hipError_t launch_chunks_t(const DecayArgs& a, bool state_pass, hipStream_t st) {
   const long long units = (long long)a.n_slots * a.H;
   const long long blocks = (units + 7) / 8 * 8 * a.nvb * a.n_roles;
   auto run = [&](auto kernel, int bytes) {
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes);
     if (e != hipSuccess) return e;
-    launch_kernel(kernel, dim3((unsigned)blocks), kThreads, bytes, st, a);
+    launch_kernel(kernel, dim3((unsigned)blocks), 64 * W, bytes, st, a);
     return hipGetLastError();
   };
-  using TL = Tiles<T, DK>;
-  return state_pass ? run(decay_chunks_kernel<T, DK, SPLIT, true>, TL::bytes(true))
-                    : run(decay_chunks_kernel<T, DK, SPLIT, false>, TL::bytes(false));
+  using TL = Tiles<T, DK, W>;
+  return state_pass ? run(decay_chunks_kernel<T, DK, W, SPLIT, true>, TL::bytes(true))
+                    : run(decay_chunks_kernel<T, DK, W, SPLIT, false>, TL::bytes(false));
 }
 
-template <typename T, int SPLIT>
+template <typename T, int W, int SPLIT>
 hipError_t launch_chunks_d(const DecayArgs& a, int dk, bool state_pass, hipStream_t st) {
-  if (dk <= 32) return launch_chunks_t<T, 32, SPLIT>(a, state_pass, st);
-  if (dk <= 64) return launch_chunks_t<T, 64, SPLIT>(a, state_pass, st);
-  if (dk <= 128) return launch_chunks_t<T, 128, SPLIT>(a, state_pass, st);
+  if constexpr (W == 4)                             // eight waves stage rows of 64 columns at least
+    if (dk <= 32) return launch_chunks_t<T, 32, W, SPLIT>(a, state_pass, st);
+  if (dk <= 64) return launch_chunks_t<T, 64, W, SPLIT>(a, state_pass, st);
+  if (dk <= 128) return launch_chunks_t<T, 128, W, SPLIT>(a, state_pass, st);
   return hipErrorInvalidValue;
 }
 
@@ -755,11 +760,16 @@ hipError_t launch_decay_chunks(DecayArgs& a, bool bf16, bool exact_state, bool s
     dk = dk > a.role[r].dk ? dk : a.role[r].dk;
     dv = dv > a.role[r].dv ? dv : a.role[r].dv;
   }
-  a.nvb = (dv + kDecayColumns - 1) / kDecayColumns;
-  if (!bf16) return launch_chunks_d<float, 1>(a, dk, state_pass, st);
+  const int cols = decay_columns(bf16, dv);
+  a.nvb = (dv + cols - 1) / cols;
+  if (!bf16) return launch_chunks_d<float, 4, 1>(a, dk, state_pass, st);
   // a state that the caller keeps gets the exact terms, in the pass that computes it
-  return exact_state && state_pass == (a.scan != 0) ? launch_chunks_d<__bf16, 3>(a, dk, state_pass, st)
-                                                    : launch_chunks_d<__bf16, 2>(a, dk, state_pass, st);
+  const bool exact = exact_state && state_pass == (a.scan != 0);
+  if (cols == 128)
+    return exact ? launch_chunks_d<__bf16, 8, 3>(a, dk, state_pass, st)
+                 : launch_chunks_d<__bf16, 8, 2>(a, dk, state_pass, st);
+  return exact ? launch_chunks_d<__bf16, 4, 3>(a, dk, state_pass, st)
+               : launch_chunks_d<__bf16, 4, 2>(a, dk, state_pass, st);
 }
 
 hipError_t launch_decay_scan(const DecayArgs& a, hipStream_t st) {

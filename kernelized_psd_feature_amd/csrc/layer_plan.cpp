@@ -74,14 +74,17 @@ kata_status validate_decay(const kata_decay_problem* pr, bool backward, std::str
 }
 
 DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles) {
-  // workgroups that the card holds at once, two a CU
-  constexpr int64_t kTarget = 512;
   DecayPlan p;
   const int64_t chunks = (int64_t(pr->T) + kDecayChunk - 1) / kDecayChunk;
   const int wide = n_roles > 1 ? std::max(pr->dk, pr->dv) : pr->dv;
-  const int64_t blocks = int64_t(pr->H) * ((wide + 63) / 64) * n_roles;   // 64 value columns each
+  const int cols = decay_columns(pr->dtype == KATA_BF16, wide);
+  // Workgroups that the card holds at once: two of four waves a CU, or one of eight.  Half as many
+  // leave it idle (8 x 4096 x 16 heads of width 64: 93 us for 82), twice as many add segment states
+  // and their scan (103 us).
+  const int64_t target = cols == 128 ? 256 : 512;
+  const int64_t blocks = int64_t(pr->H) * ((wide + cols - 1) / cols) * n_roles;
   // segments that a sequence (packed: all tokens together) is cut into to fill the card
-  const int64_t want = std::max<int64_t>(1, kTarget / (pr->packed ? blocks : blocks * pr->n_seq));
+  const int64_t want = std::max<int64_t>(1, target / (pr->packed ? blocks : blocks * pr->n_seq));
   int64_t L = std::max<int64_t>(std::min<int64_t>(chunks, 4), (chunks + want - 1) / want);
   p.L = int(L);
   const int64_t SL = L * kDecayChunk;
