@@ -322,12 +322,10 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // The value blocks and roles of one (slot, head) read the same rows: their workgroups get ids
   // congruent mod 8, one XCD.
-  const long long x = blockIdx.x;
-  const int per = A.nvb * A.n_roles;
-  const long long unit = x / (8LL * per) * 8 + x % 8;
-  const int sub = int(x / 8 % per);
-  if (unit >= (long long)A.n_slots * A.H) return;
-  const int slot = int(unit / A.H), h = int(unit % A.H);
+  const unsigned x = blockIdx.x, per = A.nvb * A.n_roles, y = x / 8 / per, unit = 8 * y + x % 8;
+  const int sub = int(x / 8 - y * per);
+  if (unit >= (unsigned)A.n_slots * (unsigned)A.H) return;
+  const int slot = int(unit / (unsigned)A.H), h = int(unit - (unsigned)slot * (unsigned)A.H);
   const DecayRole& R = A.role[sub % A.n_roles];
   const int c0 = sub / A.n_roles * DV;              // first value column
   if (c0 >= R.dv) return;
@@ -387,28 +385,28 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   const int n_last = min(kC, s.len - kC * (behind - 1));   // rows of the segment's last chunk
   fetch(behind - first > 1 ? kC : n_last);
 
-  if (tid <= kC) pw[tid] = decay_power(log2_decay(A.log_decay[h]), tid);
-  __syncthreads();
-
   // state tiles: S[i] lane holds rows 16 i + 4 g + r of column wc + l16
   f32x4 S[NS];
+  const bool from_scan = n_seg > 1, has_state = !kStatePass && (from_scan || R.init);
   {
-    const bool from_scan = n_seg > 1;
     const float* src = from_scan ? R.states + ((long long)slot * A.H + h) * SE : R.init + st_off;
-    const int r1 = from_scan ? dv : rs, q1 = from_scan ? 1 : cs;
-    const float f = from_scan || R.rev ? 1.f : pw[1];
-    const int col = c0 + wc + l16;
-    const bool any = !kStatePass && (from_scan || R.init) && col < dv;
+    const int r1 = from_scan ? dv : rs, q1 = from_scan ? 1 : cs, col = c0 + wc + l16;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       S[i] = zero4();
       const int row = 16 * i + 4 * g;
-      if (any)
+      if (has_state && col < dv)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (row + r < dk) S[i][r] = f * src[(long long)(row + r) * r1 + (long long)col * q1];
+          if (row + r < dk) S[i][r] = src[(long long)(row + r) * r1 + (long long)col * q1];
     }
   }
+  // (after the loads above are on their way)
+  if (tid <= kC) pw[tid] = decay_power(log2_decay(A.log_decay[h]), tid);
+  __syncthreads();
+  if (has_state && !from_scan && !R.rev)            // a given state is decayed to the first token
+#pragma unroll
+    for (int i = 0; i < NS; ++i) S[i] *= pw[1];
 
   // scores: the wave's row tile, and its J key tiles from j0 on
   constexpr int J = 16 / W;
@@ -598,13 +596,13 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
 // Infinity Cache that the state pass has just written), one read and one write of the states.
 __global__ __launch_bounds__(kThreads) void decay_scan_kernel(DecayArgs A) {
   const int SE = A.role[0].dk * A.role[0].dv, nb = (SE / 4 + kThreads - 1) / kThreads;
-  long long x = blockIdx.x;
-  const int e4 = 4 * (int(x % nb) * kThreads + threadIdx.x);
-  x /= nb;
-  const int h = int(x % A.H);
-  x /= A.H;
-  const DecayRole& R = A.role[x % A.n_roles];
-  const int seq = int(x / A.n_roles), SL = kC * A.L;
+  unsigned x = blockIdx.x;
+  const int e4 = 4 * (int(x % (unsigned)nb) * kThreads + threadIdx.x);
+  x /= (unsigned)nb;
+  const int h = int(x % (unsigned)A.H);
+  x /= (unsigned)A.H;
+  const DecayRole& R = A.role[x % (unsigned)A.n_roles];
+  const int seq = int(x / (unsigned)A.n_roles), SL = kC * A.L;
   int slot = seq * A.n_seg, len = A.T;
   if (A.packed) {
     const int first = cu_at(A, seq);

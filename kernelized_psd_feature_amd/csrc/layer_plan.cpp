@@ -85,7 +85,13 @@ DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles) {
   const int64_t blocks = int64_t(pr->H) * ((wide + cols - 1) / cols) * n_roles;
   // segments that a sequence (packed: all tokens together) is cut into to fill the card
   const int64_t want = std::max<int64_t>(1, target / (pr->packed ? blocks : blocks * pr->n_seq));
-  int64_t L = std::max<int64_t>(std::min<int64_t>(chunks, 4), (chunks + want - 1) / want);
+  // Short sequences stay whole, and a segment has a few chunks at least: the state pass and the scan
+  // cost two launches.  512 tokens of 16 bf16 heads: 20 us whole, 24 in segments of 3; 1024: 25 in
+  // segments of 3, 28 of 4, 34 of 8.  A chunk in fp32 takes three times as long (512 tokens of 4
+  // heads: 25 us in segments of 1, 46 whole).
+  const bool bf16 = pr->dtype == KATA_BF16;
+  const int64_t L = chunks <= (bf16 ? 8 : 2) ? chunks
+                    : std::max<int64_t>(bf16 ? 3 : 1, (chunks + want - 1) / want);
   p.L = int(L);
   const int64_t SL = L * kDecayChunk;
   p.n_seg = int((chunks + L - 1) / L);

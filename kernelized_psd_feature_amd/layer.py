@@ -72,14 +72,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _run(name, device, *args):
     """One entry point on the device's current stream."""
-    fn = getattr(_k._LIB or _k._lib(), name)
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, _raw_stream(device.index))
+    fn, index = getattr(_k._LIB or _k._lib(), name), device.index
+    if _current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(device.index))
+            status = fn(*args, _raw_stream(index))
     if status:
         _k._check(status, name)
 
@@ -107,7 +110,7 @@ def _same_device(device, *named):
 
 def _empty(x):
     """A new contiguous tensor like x."""
-    return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 _DTYPES = {torch.float32: _k.KATA_F32, torch.bfloat16: _k.KATA_BF16}
@@ -134,31 +137,41 @@ def _bytes(x):
 
 def _decay_problem(q, k, v, log_decay, scale, cu_seqlens, o=None, dO=None, zero_tail=0):
     """The packed kata_decay_problem of a call, its arguments checked."""
-    device, dtype, shape, vs = q.device, q.dtype, q.shape, v.shape
+    device, dtype, shape = q.device, q.dtype, q.shape
     if not q.is_cuda:
         raise ValueError("q must be a GPU tensor")
-    if len(shape) != 4 or len(vs) != 4 or k.dim() != 4:
+    if len(shape) != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be 4-D (B, T, H, D)")
-    if k.shape != shape or vs[:3] != shape[:3] or k.dtype != dtype or v.dtype != dtype:
-        raise ValueError("q, k, v must share (B, T, H) and dtype; q and k share dk")
     B, T, H, dk = shape
-    dv = vs[3]
+    dv = v.shape[3]
+    if k.shape != shape or v.shape != (B, T, H, dv) or k.dtype != dtype or v.dtype != dtype:
+        raise ValueError("q, k, v must share (B, T, H) and dtype; q and k share dk")
     if log_decay.shape != (H,) or log_decay.dtype != torch.float32 or not log_decay.is_contiguous():
         raise ValueError("log_decay must be a contiguous fp32 tensor of shape (H,)")
-    _same_device(device, ("k", k), ("v", v), ("log_decay", log_decay), ("cu_seqlens", cu_seqlens),
-                 ("out", o), ("dO", dO))
+    if k.device != device or v.device != device or log_decay.device != device \
+            or (o is not None and o.device != device):
+        raise ValueError(f"k, v, log_decay and out must be on {device}")
     n, packed = B, 0
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.dtype != torch.int32 \
-                or not cu_seqlens.is_contiguous():
-            raise ValueError("cu_seqlens must be a contiguous int32 tensor of n + 1 >= 2 offsets")
+                or not cu_seqlens.is_contiguous() or cu_seqlens.device != device:
+            raise ValueError(f"cu_seqlens must be a contiguous int32 tensor of n + 1 >= 2 offsets on {device}")
         if B != 1:
             raise ValueError("packed sequences lie in one batch row: B must be 1")
         n, packed = cu_seqlens.numel() - 1, 1
-    so = _rows_ok(o, "out") if o is not None else (T * H * dv, H * dv, dv)
-    sdo = _rows_ok(dO, "dO") if dO is not None else so
-    return _DECAY.pack(n, H, T, dk, dv, packed, zero_tail, _dtype(dtype), scale, *_rows_ok(q, "q"),
-                       *_rows_ok(k, "k"), *_rows_ok(v, "v"), *so, *sdo)
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    so = (T * H * dv, H * dv, dv, 1) if o is None else o.stride()
+    sdo = so
+    if dO is not None:
+        sdo = dO.stride()
+        if dO.device != device:
+            raise ValueError(f"dO must be on {device}")
+    if not sq[3] == sk[3] == sv[3] == so[3] == sdo[3] == 1:
+        for name, x in (("q", q), ("k", k), ("v", v), ("out", o), ("dO", dO)):
+            if x is not None:
+                _rows_ok(x, name)
+    return _DECAY.pack(n, H, T, dk, dv, packed, zero_tail, _dtype(dtype), scale, *sq[:3], *sk[:3], *sv[:3],
+                       *so[:3], *sdo[:3])
 
 
 def decay_state_shape(q, v, cu_seqlens=None):
@@ -169,7 +182,7 @@ def decay_state_shape(q, v, cu_seqlens=None):
 
 
 def _state(x, shape, device, name):
-    if x is not None and (tuple(x.shape) != shape or x.dtype != torch.float32 or not x.is_contiguous()
+    if x is not None and (x.shape != shape or x.dtype != torch.float32 or not x.is_contiguous()
                           or x.device != device):
         raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {shape} on {device}")
     return x
