@@ -136,6 +136,13 @@ __device__ __forceinline__ float poison(const f32x8& x, float t) {
   return t;
 }
 
+// LDS reads above this line in the source stay above it, and what uses them below.  fp32 fragments
+// are twice as large: there the compiler keeps its own order.
+template <typename T>
+__device__ __forceinline__ void reads_above() {
+  if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+}
+
 // Four neighbouring elements as they are stored.
 template <typename T>
 using Quad = std::conditional_t<sizeof(T) == 2, uint2, f32x4>;
@@ -467,35 +474,61 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
 
     f32x4 o[4];
     if constexpr (!kStatePass) {
-      frag qf[M];
+      // Reads are issued in batches, ahead of the work that hides them (reads_above): left alone, the
+      // compiler waits for nearly every read before its product, 4400 cycles a chunk for one
+      // workgroup a CU.
+      frag qf[M], kr[M][J], qr[4];
       f32x4 p[J];
 #pragma unroll
-      for (int m = 0; m < M; ++m) qf[m] = straight_frag(sQ + (16 * rt + l16) * LQ + 32 * m, g);
+      for (int m = 0; m < M; ++m) {
+        qf[m] = straight_frag(sQ + (16 * rt + l16) * LQ + 32 * m, g);
+#pragma unroll
+        for (int j = 0; j < J; ++j) kr[m][j] = row_frag(sK + (16 * (j0 + j) + l16) * LK + 32 * m + 8 * g);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qr[i] = row_frag(sQ + (16 * i + l16) * LQ + 8 * g);
+      reads_above<T>();
 #pragma unroll
       for (int j = 0; j < J; ++j) p[j] = zero4();
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-          p[j] = mma(row_frag(sK + (16 * (j0 + j) + l16) * LK + 32 * m + 8 * g), qf[m], p[j]);
-      // weights, zero by selection where the key is later (bf16: rounded, an operand)
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          p[j][r] = 16 * (j0 + j) + 4 * g + r > 16 * rt + l16 ? 0.f : p[j][r] * dec[j][r];
-        store4(sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g), p[j]);
-      }
+        for (int j = 0; j < J; ++j) p[j] = mma(kr[m][j], qf[m], p[j]);
       // readout of the entry state (bf16: rounded as an operand, the sum itself stays fp32)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = zero4();
 #pragma unroll
       for (int m = 0; m < M; ++m) {
+        frag next[4];
+        if (m + 1 < M)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) next[i] = row_frag(sQ + (16 * i + l16) * LQ + 32 * (m + 1) + 8 * g);
+        reads_above<T>();
+        if (m == 0) {
+          // weights, zero by selection where the key is later (bf16: rounded, an operand)
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              p[j][r] = 16 * (j0 + j) + 4 * g + r > 16 * rt + l16 ? 0.f : p[j][r] * dec[j][r];
+            store4(sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g), p[j]);
+          }
+        }
         const frag sf = pack_frag(S[2 * m], S[2 * m + 1], T());
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = mma(sf, row_frag(sQ + (16 * i + l16) * LQ + 32 * m + 8 * g), o[i]);
+        for (int i = 0; i < 4; ++i) o[i] = mma(sf, qr[i], o[i]);
+        if (m + 1 < M)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qr[i] = next[i];
       }
+    }
+    frag vf[2], kf[NS];                             // the wave's values, 32 keys each; K^T of 32 keys
+#pragma unroll
+    for (int m = 0; m < 2; ++m) vf[m] = column_frag<LV>(sV + 32 * m * LV + wc, lane);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) kf[i] = column_frag<LK>(sK + 16 * i, lane);
+    reads_above<T>();
+    if constexpr (!kStatePass) {
       float f = row0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -509,9 +542,6 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
       if (c + 2 < behind) fetch(n_next);
     }
 
-    frag vf[2];                                     // the wave's values, 32 keys each
-#pragma unroll
-    for (int m = 0; m < 2; ++m) vf[m] = column_frag<LV>(sV + 32 * m * LV + wc, lane);
     if (kLast && last_seg) {
       // The state behind the last token, n_last - 1 (reversed: its product with g, the gradient of
       // the initial state).  Keys behind it are zero rows.
@@ -527,15 +557,19 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
     for (int i = 0; i < NS; ++i) S[i] *= whole;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      frag vx[SPLIT];
-      weigh<SPLIT>(vf[m], vw[m], vx);
-      frag kf[NS];
+      frag vx[SPLIT], next[NS];
+      if (m == 0)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) kf[i] = column_frag<LK>(sK + 32 * m * LK + 16 * i, lane);
+        for (int i = 0; i < NS; ++i) next[i] = column_frag<LK>(sK + 32 * LK + 16 * i, lane);
+      reads_above<T>();
+      weigh<SPLIT>(vf[m], vw[m], vx);
 #pragma unroll
       for (int k = 0; k < SPLIT; ++k)
 #pragma unroll
         for (int i = 0; i < NS; ++i) S[i] = mma(kf[i], vx[k], S[i]);
+      if (m == 0)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) kf[i] = next[i];
     }
 
     if constexpr (!kStatePass) {
@@ -543,13 +577,19 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
       // The loads are issued late: early ones, a whole chunk ahead of their use, measured slower
       // (131k tokens: 276 us for 252), as many in flight as there are then cost more than they hide.
       if constexpr (!kLast && !kTwo) fetch(n_next);
+      const bool bad = __any(sick != sick);
       __syncthreads();                              // the weights are there
-      if (!__any(sick != sick)) {
+      frag pf[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 2 * m; i < 4; ++i) pf[m][i] = row_frag(sP + (16 * i + l16) * LP + 32 * m + 8 * g);
+      reads_above<T>();
+      if (!bad) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int i = 2 * m; i < 4; ++i)
-            o[i] = mma(vf[m], row_frag(sP + (16 * i + l16) * LP + 32 * m + 8 * g), o[i]);
+          for (int i = 2 * m; i < 4; ++i) o[i] = mma(vf[m], pf[m][i], o[i]);
       } else {
         // An infinity or nan among the values: in the product above a masked weight of zero
         // would still meet it and leave nan in earlier rows, so the pairs are added one by one.
