@@ -284,8 +284,8 @@ kata_status kata_bwd_chunked(const kata_problem* pr, const void* q, const void* 
  *          content is read or written out of bounds).  A sequence may be empty: its final state
  *          is its initial state.
  *   H, dk, dv: heads, width of q and k, width of v: at most 128, rows of whole 16 bytes.
- *   zero_tail: packed: 0 leaves the output rows behind cu_seqlens[n_seq] as they are, 1 zeroes
- *          them.
+ *   zero_tail: packed: 0 leaves the output rows that belong to no sequence (before cu_seqlens[0] or
+ *          from cu_seqlens[n_seq] on) as they are, 1 zeroes them.
  *   dtype: of q, k, v, o, dO and the gradients.  States are fp32 [n_seq][H][dk][dv], contiguous.
  *   log_decay: device fp32 [H], any value; -inf is a decay of zero.  It has no gradient.
  *   sq, sk, sv, so, sdo: element strides of (b, t, h); those of an input may be zero (a broadcast

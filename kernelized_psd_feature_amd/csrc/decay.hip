@@ -341,14 +341,16 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   if (!find_segment(A, slot, sh, s)) return;
   const int L = A.L;
   T* const out = reinterpret_cast<T*>(R.out) + s.b * R.so[0] + h * R.so[2] + c0;
+  const int per_row = min(DV, R.dv - c0) / 4;
+  auto clear = [&](int from, int rows) {            // the block's columns of `rows` output rows
+    for (long long i = tid; i < (long long)rows * per_row; i += kThr)
+      store4(out + (from + i / per_row) * R.so[1] + i % per_row * 4, zero4());
+  };
   if (s.seq == A.n_seq) {                           // rows behind the last sequence
-    if (kStatePass || !A.zero_tail) return;
-    const int per_row = min(DV, R.dv - c0) / 4, r0 = kC * L * s.seg;
-    const long long todo = (long long)min(kC * L, s.len - r0) * per_row;
-    for (long long i = tid; i < todo; i += kThr)
-      store4(out + (s.start + r0 + i / per_row) * R.so[1] + i % per_row * 4, zero4());
+    if (!kStatePass && A.zero_tail) clear(s.start + kC * L * s.seg, min(kC * L, s.len - kC * L * s.seg));
     return;
   }
+  if (!kStatePass && A.packed && A.zero_tail && s.seq == 0 && s.seg == 0) clear(0, s.start);   // before the first
   const int n_chunks = (s.len + kC - 1) / kC, n_seg = (n_chunks + L - 1) / L;
   const long long SE = (long long)R.dk * R.dv, st_off = ((long long)s.seq * A.H + h) * SE;
   const int rs = R.init_trans ? 1 : R.dv, cs = R.init_trans ? R.dk : 1;   // strides of init

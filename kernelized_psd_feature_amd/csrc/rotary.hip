@@ -53,14 +53,13 @@ template <typename T, int V, bool IL>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs A) {
   extern __shared__ float2 cs[];                    // [tokens of the block][rot / 2]
   const int half = A.rot / 2, tid = threadIdx.x;
-  const long long first = (long long)blockIdx.x * A.TT, total = (long long)A.B * A.T;
-  const int tokens = (int)min((long long)A.TT, total - first);
+  const unsigned first = blockIdx.x * (unsigned)A.TT, total = (unsigned)A.B * (unsigned)A.T;   // < 2^31
+  const int tokens = (int)min((unsigned)A.TT, total - first);
   for (int i = tid; i < tokens * half; i += kThreads) {
-    const long long token = first + i / half;
-    const long long b = token / A.T, t = token % A.T;
-    long long pos = A.offset + t;
+    const unsigned token = first + i / half, b = token / (unsigned)A.T, t = token - b * (unsigned)A.T;
+    long long pos = A.offset + (long long)t;
     if (A.positions) {
-      const long long at = b * A.pos_b + t * A.pos_t;
+      const long long at = (long long)b * A.pos_b + (long long)t * A.pos_t;
       pos = A.pos64 ? reinterpret_cast<const long long*>(A.positions)[at]
                     : (long long)reinterpret_cast<const int*>(A.positions)[at];
     }
@@ -77,8 +76,8 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs A) {
   for (int i = tid; i < tokens * per; i += kThreads) {
     const int tt = i / per, y = i % per, it = y % NI;
     int h = y / NI;
-    const long long token = first + tt;
-    const int b = int(token / A.T), t = int(token % A.T);
+    const unsigned token = first + tt;
+    const int b = int(token / (unsigned)A.T), t = int(token - (unsigned)b * (unsigned)A.T);
     const bool is_k = h >= A.H;
     h -= is_k ? A.H : 0;
     const T* src = reinterpret_cast<const T*>(is_k ? A.k : A.q) + row_off(is_k ? A.sk : A.sq, b, t, h);
@@ -131,7 +130,7 @@ hipError_t launch_t(RotaryArgs& a, bool interleaved, hipStream_t st) {
   const long long tokens = (long long)a.B * a.T;
   a.TT = 4 * kThreads / per;
   if (a.TT > tokens / 512) a.TT = (int)(tokens / 512);
-  if (a.TT > 4096 / (half ? half : 1)) a.TT = 4096 / half;
+  if (a.TT * half > 4096) a.TT = 4096 / half;
   if (a.TT < 1) a.TT = 1;
   const long long blocks = (tokens + a.TT - 1) / a.TT;
   const size_t lds = sizeof(float2) * a.TT * half;

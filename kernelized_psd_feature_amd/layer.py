@@ -124,8 +124,8 @@ def _dtype(dt):
 def _workspace(need, given, device):
     if given is None:
         return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    if given.device != device:
-        raise ValueError(f"workspace must be on {device}")
+    if given.device != device or not given.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
     return given
 
 
@@ -202,8 +202,8 @@ def fwd_decay(q, k, v, log_decay, scale=1.0, initial_state=None, return_state=Fa
 
     q, k (B, T, H, dk), v (B, T, H, dv), bf16 or fp32, widths up to 128 with rows of whole 16 bytes,
     any (b, t, h) strides (broadcast axes too); o has the inputs' dtype.  log_decay: fp32 (H,).
-    cu_seqlens: int32 (n + 1,) offsets of n sequences packed into B = 1; rows behind the last one
-    are zero in a new output and left as they are in `out`.
+    cu_seqlens: int32 (n + 1,) offsets of n sequences packed into B = 1; rows of no sequence are zero
+    in a new output and left as they are in `out`.
     initial_state, and the final state with return_state: fp32 (n, H, dk, dv).
     workspace: uint8, decay_workspace_size() bytes (allocated here otherwise)."""
     o = _out_like(v, out)
@@ -230,8 +230,8 @@ def decay_workspace_size(q, k, v, log_decay, cu_seqlens=None, backward=False):
 def bwd_decay(q, k, v, dO, log_decay, scale=1.0, initial_state=None, dfinal_state=None,
               cu_seqlens=None, workspace=None):
     """Gradients (dq, dk, dv, dinitial_state) of sum(dO * o) + sum(dfinal_state * final_state), the
-    first three in the inputs' dtype, the last one fp32 (None without an initial_state).  Rows behind
-    the last packed sequence get zeros."""
+    first three in the inputs' dtype, the last one fp32 (None without an initial_state).  Rows of no
+    packed sequence get zeros."""
     if dO.shape != v.shape or dO.dtype != q.dtype:
         raise ValueError("dO must match v's shape and q's dtype")
     pr = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, dO=dO, zero_tail=1)

@@ -203,6 +203,12 @@ def test_decay_packed_first_rows_before_the_first_sequence_are_left_alone():
     K.fwd_decay(q, k, v, _decays(1), cu_seqlens=torch.tensor([10, 80], dtype=torch.int32, device=DEV), out=out)
     assert (out[:, :10] == 3.0).all() and (out[:, 80:] == 3.0).all()
     _check_decay(q[:, 10:80], k[:, 10:80], v[:, 10:80], _decays(1), 1.0, o=out[:, 10:80])
+    for cu in ([10, 80], [10, 10, 80], [100, 100], [64, 70]):        # and zero in a new output
+        new = K.fwd_decay(q, k, v, _decays(1), cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV))
+        assert not new[:, :cu[0]].any() and not new[:, cu[-1]:].any()
+    out[:, :10], out[:, 80:] = 0, 0
+    new = K.fwd_decay(q, k, v, _decays(1), cu_seqlens=torch.tensor([10, 10, 80], dtype=torch.int32, device=DEV))
+    assert torch.equal(new, out)                     # an empty sequence in front changes nothing
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -350,6 +356,8 @@ def test_decay_refusals():
                 lambda: K.bwd_decay(q, k, v, v.float(), ld), lambda: K.bwd_decay(q, k, v, v[:, :4], ld),
                 lambda: K.decode_decay(q, k, v, ld, torch.zeros(1, 2, 64, 64, device=DEV, dtype=BF)),
                 lambda: K.decode_decay(q, k, v, ld, None),
+                lambda: K.fwd_decay(*[_randn(1, 1, 999, 1, 64)] * 3, ld[:1], workspace=torch.empty(
+                    1, dtype=torch.uint8, device=DEV).expand(1 << 30)),
                 lambda: K.parallel_decay_attn(q, k, v, ld.clone().requires_grad_()),
                 lambda: K.parallel_decay_attn(q, k, v, ld, cu_seqlens=cu, rotary=K.rotary_rates(64)),
                 lambda: K.parallel_decay_attn(q, k, v, ld, norm=(torch.ones(32, device=DEV), None))):
