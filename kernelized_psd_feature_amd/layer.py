@@ -311,17 +311,17 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
     q (B, T, H, D) and k (B, T, Hk, D) (or None), bf16 or fp32; positions: int32 or int64, broadcastable
     to (B, T), or None: offset + t.  inverse negates the angles: the gradient.  out: outputs of q (and
     k), which may be q and k themselves.  Returns the turned q, or the pair."""
+    device, dtype, shape = q.device, q.dtype, q.shape
     if not q.is_cuda:
         raise ValueError("q must be a GPU tensor")
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or
-                                           k.shape[3] != q.shape[3] or k.dtype != q.dtype)):
-        raise ValueError("q and k must be 4-D (B, T, H, D) and share B, T, D and dtype")
-    if rates.dim() != 1 or rates.dtype != torch.float64 or not rates.is_contiguous():
-        raise ValueError("rates must be a contiguous fp64 vector")
-    B, T, H, D = q.shape
-    if 2 * rates.numel() > D:
+    if len(shape) != 4:
+        raise ValueError("q and k must be 4-D (B, T, H, D)")
+    B, T, H, D = shape
+    n = rates.numel()
+    if rates.dim() != 1 or rates.dtype != torch.float64 or not rates.is_contiguous() or rates.device != device:
+        raise ValueError(f"rates must be a contiguous fp64 vector on {device}")
+    if 2 * n > D:
         raise ValueError("rates turn more coordinates than a head has")
-    device = q.device
     if out is None:
         oq, ok = _empty(q), None if k is None else _empty(k)
     else:
@@ -330,26 +330,32 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
             raise ValueError("out must hold an output for each input")
         oq, ok = (*outs, None)[:2]
         for x, y in ((q, oq), (k, ok)):
-            if x is not None and (y.shape != x.shape or y.dtype != x.dtype):
-                raise ValueError("out must match the inputs' shapes and dtype")
-    _same_device(device, ("k", k), ("rates", rates), ("positions", positions), ("out", oq), ("out", ok))
+            if x is not None and (y.shape != x.shape or y.dtype != dtype or y.device != device):
+                raise ValueError("out must match the inputs' shapes, dtype and device")
+    sq, soq, Hk, pk, pok = q.stride(), oq.stride(), 0, None, None
+    sk, sok = sq, soq
+    if k is not None:
+        if k.dim() != 4 or k.shape != (B, T, k.shape[2], D) or k.dtype != dtype or k.device != device:
+            raise ValueError("q and k must be 4-D (B, T, H, D) and share B, T, D, dtype and device")
+        Hk, sk, sok, pk, pok = k.shape[2], k.stride(), ok.stride(), k.data_ptr(), ok.data_ptr()
+    if not sq[3] == sk[3] == soq[3] == sok[3] == 1:
+        for name, x in (("q", q), ("k", k), ("out", oq), ("out", ok)):
+            if x is not None:
+                _rows_ok(x, name)
     pos64 = pos_b = pos_t = 0
+    at = None
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise ValueError("positions must be int32 or int64")
+        if positions.dtype not in (torch.int32, torch.int64) or positions.device != device:
+            raise ValueError(f"positions must be int32 or int64 on {device}")
         try:
-            at = positions if positions.shape == (B, T) else positions.expand(B, T)
+            x = positions if positions.shape == (B, T) else positions.expand(B, T)
         except RuntimeError:
             raise ValueError("positions must broadcast to (B, T)") from None
-        pos64, (pos_b, pos_t) = int(positions.dtype == torch.int64), at.stride()
-    Hk = 0 if k is None else k.shape[2]
-    sq, soq = _rows_ok(q, "q"), _rows_ok(oq, "out")
-    sk, sok = (sq, soq) if k is None else (_rows_ok(k, "k"), _rows_ok(ok, "out"))
+        pos64, (pos_b, pos_t), at = int(positions.dtype == torch.int64), x.stride(), positions.data_ptr()
     if B * T * H * D and (k is None or Hk):
-        pr = _ROTARY.pack(B, T, H, Hk, D, 2 * rates.numel(), _dtype(q.dtype), int(interleaved), int(inverse),
-                          pos64, magnitude, pos_b, pos_t, offset, *sq, *sk, *soq, *sok)
-        _run("kata_rotary", device, pr, q.data_ptr(), _ptr(k), rates.data_ptr(), _ptr(positions),
-             oq.data_ptr(), _ptr(ok))
+        pr = _ROTARY.pack(B, T, H, Hk, D, 2 * n, _dtype(dtype), 1 if interleaved else 0, 1 if inverse else 0,
+                          pos64, magnitude, pos_b, pos_t, offset, *sq[:3], *sk[:3], *soq[:3], *sok[:3])
+        _run("kata_rotary", device, pr, q.data_ptr(), pk, rates.data_ptr(), at, oq.data_ptr(), pok)
     return oq if k is None else (oq, ok)
 
 
@@ -370,18 +376,19 @@ def _check_norm(x, weight, bias):
     """The weights' dtype code, the arguments checked."""
     if not x.is_cuda:
         raise ValueError("x must be a GPU tensor")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape, device, dt = x.shape, x.device, None
+    if not shape or shape[-1] < 1:
         raise ValueError("x needs a last axis of at least one element")
-    dt, want = None, (x.shape[-1],)
-    for name, p in (("weight", weight), ("bias", bias)):
-        if p is None:
-            continue
-        if p.shape != want or not p.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous vector of the last axis's length")
-        if dt is not None and p.dtype != dt:
+    if weight is not None:
+        dt = weight.dtype
+        if weight.shape != shape[-1:] or not weight.is_contiguous() or weight.device != device:
+            raise ValueError(f"weight must be a contiguous vector of the last axis's length on {device}")
+    if bias is not None:
+        if bias.shape != shape[-1:] or not bias.is_contiguous() or bias.device != device:
+            raise ValueError(f"bias must be a contiguous vector of the last axis's length on {device}")
+        if dt is not None and bias.dtype != dt:
             raise ValueError("weight and bias must share their dtype")
-        dt = p.dtype
-    _same_device(x.device, ("weight", weight), ("bias", bias))
+        dt = bias.dtype
     return _k.KATA_F32 if dt is None else _dtype(dt)
 
 
@@ -390,21 +397,26 @@ def fwd_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, return_stats=F
     fp32, or bf16 for bf16 rows.  With return_stats also the rows' mean and 1 / sqrt(var + eps), fp32
     of x's leading shape, for bwd_layer_norm.  out may be x."""
     wt = _check_norm(x, weight, bias)
-    if out is not None and (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device):
-        raise ValueError("out must match x's shape, dtype and device")
-    y = _empty(x) if out is None else out
-    device, mean, rstd = x.device, None, None
-    if return_stats:
-        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=device) for _ in range(2))
-    if x.numel():
-        x2, N = _rows(x), x.shape[-1]
+    device, dtype, shape, N, mean, rstd = x.device, x.dtype, x.shape, x.shape[-1], None, None
+    if out is None:
+        y = _empty(x)
+        y2_stride = N
+    else:
+        y = out
+        if out.shape != shape or out.dtype != dtype or out.device != device:
+            raise ValueError("out must match x's shape, dtype and device")
         try:
             y2 = y.view(-1, N)
         except RuntimeError:
             raise ValueError("out's leading axes must collapse into one") from None
         if N > 1 and y2.stride(1) != 1:
             raise ValueError("out: last dimension must be contiguous")
-        pr = _NORM.pack(x2.shape[0], N, _dtype(x.dtype), wt, eps, x2.stride(0), N, y2.stride(0), N)
+        y2_stride = y2.stride(0)
+    if return_stats:
+        mean, rstd = (torch.empty(shape[:-1], dtype=torch.float32, device=device) for _ in range(2))
+    if y.numel():
+        x2 = _rows(x)
+        pr = _NORM.pack(x2.shape[0], N, _dtype(dtype), wt, eps, x2.stride(0), N, y2_stride, N)
         _run("kata_fwd_layer_norm", device, pr, x2.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(),
              _ptr(mean), _ptr(rstd))
     return (y, mean, rstd) if return_stats else y
