@@ -150,6 +150,9 @@ __device__ __forceinline__ uint2 quad(const f32x4& x, __bf16) {
   return uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
 }
 __device__ __forceinline__ f32x4 quad(const f32x4& x, float) { return x; }
+__device__ __forceinline__ f32x4 unquad(const uint2& u) {
+  return f32x4{bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y)};
+}
 __device__ __forceinline__ void store4(__bf16* p, const f32x4& x) {
   *reinterpret_cast<uint2*>(p) = quad(x, __bf16());
 }
@@ -269,8 +272,14 @@ struct Tiles {
   static constexpr int kBuffers = kBf && (DK <= 64 || W == 8) ? 2 : 1;
   static constexpr int stage(bool state_pass) { return kC * (LK + LV + (state_pass ? 0 : LQ)); }
   static constexpr int kHead = 288;                 // an int, then the powers g^0 .. g^64
+  // Terms of a score weight.  The rounding of one weight moves a whole row of outputs alike.  Over
+  // many rows that adds a factor of sqrt(2) to the outputs' own rounding, but a short sequence has
+  // few weights and their errors do not average out (two tokens: 1.5 times and more; one: up to
+  // 2.5), so up to kFine tokens what the rounding left is a second operand.  For all sequences that
+  // would cost 3 to 7% of the walk (8 x 4096 backward: 195 us for 189; width 128: 763 for 712).
+  static constexpr int kTerms = kBf ? 2 : 1, kFine = 512;
   static constexpr int bytes(bool state_pass) {
-    return kHead + (kBuffers * stage(state_pass) + (state_pass ? 0 : kC * LP)) * (int)sizeof(T);
+    return kHead + (kBuffers * stage(state_pass) + (state_pass ? 0 : kTerms * kC * LP)) * (int)sizeof(T);
   }
   // waves a SIMD that the registers are held to (the launch bound counts workgroups a CU)
   static constexpr int occupancy(bool state_pass) {
@@ -320,7 +329,7 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   constexpr bool kTwo = TL::kBuffers == 2;
   constexpr int kStage = TL::stage(kStatePass);
   T* const sP = reinterpret_cast<T*>(lds + TL::kHead);             // walk only
-  T* sK = sP + (kStatePass ? 0 : kC * LP);
+  T* sK = sP + (kStatePass ? 0 : TL::kTerms * kC * LP);
   T* sV = sK + kC * LK;
   T* sQ = sV + kC * LV;                             // walk only
   int other = kStage;                               // from this chunk's tiles to the next one's
@@ -367,6 +376,7 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   const bool last_seg = s.seg == n_seg - 1;
   if (kStatePass && last_seg && !R.fin) return;     // enters no entry state
   const int first = s.seg * L, behind = min(first + L, n_chunks);
+  const bool fine = __builtin_amdgcn_readfirstlane(s.len) <= TL::kFine;
 
   // rows in the role's time order: row i of the sequence is start + i, or its mirror image
   const int dir = R.rev ? -1 : 1, dk = R.dk, dv = R.dv;
@@ -507,13 +517,18 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
           for (int i = 0; i < 4; ++i) next[i] = row_frag(sQ + (16 * i + l16) * LQ + 32 * (m + 1) + 8 * g);
         reads_above<T>();
         if (m == 0) {
-          // weights, zero by selection where the key is later (bf16: rounded, an operand)
+          // weights, zero by selection where the key is later (bf16: rounded, an operand; fine: and
+          // what that left, as a second one)
 #pragma unroll
           for (int j = 0; j < J; ++j) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
               p[j][r] = 16 * (j0 + j) + 4 * g + r > 16 * rt + l16 ? 0.f : p[j][r] * dec[j][r];
-            store4(sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g), p[j]);
+            T* const at = sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g);
+            const Quad<T> hi = quad(p[j], T());
+            *reinterpret_cast<Quad<T>*>(at) = hi;
+            if constexpr (TL::kTerms == 2)
+              if (fine) store4(at + kC * LP, p[j] - unquad(hi));
           }
         }
         const frag sf = pack_frag(S[2 * m], S[2 * m + 1], T());
@@ -581,17 +596,21 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
       if constexpr (!kLast && !kTwo) fetch(n_next);
       const bool bad = __any(sick != sick);
       __syncthreads();                              // the weights are there
-      frag pf[2][4];
+      auto weighted = [&](const T* sp) {              // o += weights at sp x values
+        frag pf[2][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 2 * m; i < 4; ++i) pf[m][i] = row_frag(sP + (16 * i + l16) * LP + 32 * m + 8 * g);
-      reads_above<T>();
-      if (!bad) {
+          for (int i = 2 * m; i < 4; ++i) pf[m][i] = row_frag(sp + (16 * i + l16) * LP + 32 * m + 8 * g);
+        reads_above<T>();
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int i = 2 * m; i < 4; ++i) o[i] = mma(vf[m], pf[m][i], o[i]);
+      };
+      if (!bad) {
+        weighted(sP);
+        if (TL::kTerms == 2 && fine) weighted(sP + kC * LP);
       } else {
         // An infinity or nan among the values: in the product above a masked weight of zero
         // would still meet it and leave nan in earlier rows, so the pairs are added one by one.
@@ -600,7 +619,9 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
 #pragma unroll 1
           for (int key = 0; key < 16 * i + 16; ++key) {
             if (key > 16 * i + l16) continue;
-            const float p = to_f32(sP[(16 * i + l16) * LP + split_place(key)]);
+            const int at = (16 * i + l16) * LP + split_place(key);
+            float p = to_f32(sP[at]);
+            if (TL::kTerms == 2 && fine) p += to_f32(sP[kC * LP + at]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[i][r] += p * to_f32(sV[key * LV + wc + 4 * g + r]);
           }
@@ -709,7 +730,7 @@ __device__ __forceinline__ f32x4 load4<float>(const float* p) {
 template <>
 __device__ __forceinline__ f32x4 load4<__bf16>(const __bf16* p) {
   const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return f32x4{bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y)};
+  return unquad(u);
 }
 
 template <typename T, int LC, int RI>

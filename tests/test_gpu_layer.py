@@ -158,6 +158,30 @@ def test_decay_of_any_strength(dtype, ld):
     _check_decay(q, k, v, decays, 1.0, S0=S0, dO=g, dS=dS, o=o, S=S, grads=grads)
 
 
+@pytest.mark.parametrize("dk,dv", [(32, 32), (64, 64), (128, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("T", [1, 2, 3, 8, 64])
+def test_decay_of_few_tokens_keeps_its_weights(T, dk, dv):
+    """One chunk without an entry state: a weight's two bf16 terms leave 2^-16 of it, so the outputs and
+    gradients are off by little more than their own rounding."""
+    B, H, scale = 2, 3, dk ** -0.5
+    q, k = _randn(1, B, T, H, dk, dtype=BF), _randn(2, B, T, H, dk, dtype=BF)
+    v, dO = _randn(3, B, T, H, dv, dtype=BF), _randn(4, B, T, H, dv, dtype=BF)
+    ld = _decays(H)
+    o = K.fwd_decay(q, k, v, ld, scale=scale)
+    grads = K.bwd_decay(q, k, v, dO, ld, scale=scale)
+    few = (2 * T + 128 + 64) * 2.0 ** -24 + 5 * 2.0 ** -21 + 1.02 * 2.0 ** -16
+    for b in range(B):
+        for h in range(H):
+            a, g = [_np(x)[b, :, h] for x in (q, k, v)], _np(dO)[b, :, h]
+            ab = [np.abs(x) for x in a]
+            nld = _np(ld)[h]
+            refs = (L.decay_closed(*a, nld, scale, None)[0], *L.decay_backward(*a, g, nld, scale, None, None)[:3])
+            sizes = (L.decay_closed(*ab, nld, scale, None)[0],
+                     *L.decay_backward(*ab, np.abs(g), nld, scale, None, None)[:3])
+            for name, got, r, z in zip(("o", "dq", "dk", "dv"), (o, *grads), refs, sizes):
+                _inside(got[b, :, h], r, few * z + U[BF] * 1.01 * np.abs(r), f"{name} batch {b} head {h}")
+
+
 @pytest.mark.parametrize("lengths", [[1], [0], [0, 0, 5, 0], [64, 64, 64], [1, 0, 77, 512, 130, 1, 63],
                                      [700, 3], [5] * 30, [256, 1, 255, 257]])
 @pytest.mark.parametrize("dtype", [BF, F32])
