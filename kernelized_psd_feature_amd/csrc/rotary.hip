@@ -9,7 +9,10 @@
 // bits: in fp32 an angle of 10^5 is known to 0.004 only.  All heads of q and k share the angles of
 // a token, so a workgroup takes a few tokens, leaves their rot / 2 cosines and sines in LDS, and
 // then streams every head through 16-byte accesses.  One launch for q and k.
-// Bound: HBM, each element read and written once.
+// Bound: HBM, each element read and written once: 131072 tokens of 16 + 16 bf16 heads of width 64 in
+// 194 us, 5.5 TB/s.
+#include <type_traits>
+
 #include "device.h"
 #include "layer.h"
 #include "mfma_util.h"
@@ -19,34 +22,29 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// V neighbouring elements: one of 16 bytes, or V = 1.
 template <typename T, int V>
-struct Vec {
-  float x[V];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (V == 1) {
-      x[0] = to_f32(p[0]);
-    } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      if constexpr (sizeof(T) == 2) {
-        x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
-        x[4] = bf_lo(u.z); x[5] = bf_hi(u.z); x[6] = bf_lo(u.w); x[7] = bf_hi(u.w);
-      } else {
-        x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-        x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
-      }
-    }
-  }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (V == 1) {
-      p[0] = from_f32<T>(x[0]);
-    } else if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4*>(p) = uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
-    } else {
-      *reinterpret_cast<float4*>(p) = float4{x[0], x[1], x[2], x[3]};
-    }
-  }
-};
+using Raw = std::conditional_t<V == 1, T, uint4>;
+
+template <typename T>
+__device__ __forceinline__ void unpack(const T& u, float (&x)[1]) { x[0] = to_f32(u); }
+__device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
+  x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
+  x[4] = bf_lo(u.z); x[5] = bf_hi(u.z); x[6] = bf_lo(u.w); x[7] = bf_hi(u.w);
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&x)[4]) {
+  x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+  x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+}
+template <typename T>
+__device__ __forceinline__ void put(T* p, const float (&x)[1]) { p[0] = from_f32<T>(x[0]); }
+__device__ __forceinline__ void put(__bf16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+}
+__device__ __forceinline__ void put(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = float4{x[0], x[1], x[2], x[3]};
+}
 
 // V elements of a vector (1: element by element), IL: pairs of neighbours.
 template <typename T, int V, bool IL>
@@ -73,49 +71,45 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs A) {
   // items of a head: NR that turn (V pairs in halves; V / 2 or one of neighbours), NC that are copied
   const int NR = IL ? A.rot / (V == 1 ? 2 : V) : half / V, NC = (A.D - A.rot) / V, NI = NR + NC;
   const int heads = A.H + A.Hk, per = heads * NI;
+  constexpr bool kTwo = !IL || V == 1;              // a pair's second half is a load of its own
+  const int second = IL ? 1 : half;
   for (int i = tid; i < tokens * per; i += kThreads) {
-    const int tt = i / per, y = i % per, it = y % NI;
-    int h = y / NI;
+    const int tt = i / per, y = i - tt * per, hh = y / NI, it = y - hh * NI;
     const unsigned token = first + tt;
     const int b = int(token / (unsigned)A.T), t = int(token - (unsigned)b * (unsigned)A.T);
-    const bool is_k = h >= A.H;
-    h -= is_k ? A.H : 0;
-    const T* src = reinterpret_cast<const T*>(is_k ? A.k : A.q) + row_off(is_k ? A.sk : A.sq, b, t, h);
-    T* dst = reinterpret_cast<T*>(is_k ? A.ok : A.oq) + row_off(is_k ? A.sok : A.soq, b, t, h);
-    if (it >= NR) {
-      const int e = A.rot + (it - NR) * V;
-      Vec<T, V> x;
-      x.load(src + e);
-      x.store(dst + e);
-    } else if constexpr (!IL) {
-      const int e = it * V;
-      Vec<T, V> a, c, ya, yc;
-      a.load(src + e);
-      c.load(src + half + e);
+    const bool is_k = hh >= A.H, turns = it < NR;
+    const int h = hh - (is_k ? A.H : 0);
+    const int e = !turns ? A.rot + (it - NR) * V : kTwo && IL ? 2 * it : it * V;
+    const T* src = reinterpret_cast<const T*>(is_k ? A.k : A.q) + row_off(is_k ? A.sk : A.sq, b, t, h) + e;
+    T* dst = reinterpret_cast<T*>(is_k ? A.ok : A.oq) + row_off(is_k ? A.sok : A.soq, b, t, h) + e;
+    const float2* w = cs + tt * half + (IL ? e / 2 : e);
+    // Both loads are issued before the branch (a copy's second one repeats the first); the empty asm
+    // keeps the compiler from moving the second one into it, behind the wait for the first (194 us
+    // for 207 at 131072 tokens).
+    const Raw<T, V> u = *reinterpret_cast<const Raw<T, V>*>(src);
+    Raw<T, V> v = u;
+    if constexpr (kTwo) v = *reinterpret_cast<const Raw<T, V>*>(src + (turns ? second : 0));
+    if constexpr (kTwo && V > 1) asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+    float x[V], z[V], p[V], s[V];
+    unpack(u, x);
+    if (!turns) {
+      *reinterpret_cast<Raw<T, V>*>(dst) = u;
+    } else if constexpr (kTwo) {
+      unpack(v, z);
 #pragma unroll
       for (int r = 0; r < V; ++r) {
-        const float2 w = cs[tt * half + e + r];
-        ya.x[r] = a.x[r] * w.x - c.x[r] * w.y;
-        yc.x[r] = a.x[r] * w.y + c.x[r] * w.x;
+        p[r] = x[r] * w[r].x - z[r] * w[r].y;
+        s[r] = x[r] * w[r].y + z[r] * w[r].x;
       }
-      ya.store(dst + e);
-      yc.store(dst + half + e);
-    } else if constexpr (V == 1) {
-      const float a = to_f32(src[2 * it]), c = to_f32(src[2 * it + 1]);
-      const float2 w = cs[tt * half + it];
-      dst[2 * it] = from_f32<T>(a * w.x - c * w.y);
-      dst[2 * it + 1] = from_f32<T>(a * w.y + c * w.x);
+      put(dst, p);
+      put(dst + second, s);
     } else {
-      const int e = it * V;
-      Vec<T, V> x, z;
-      x.load(src + e);
 #pragma unroll
       for (int r = 0; r < V; r += 2) {
-        const float2 w = cs[tt * half + (e + r) / 2];
-        z.x[r] = x.x[r] * w.x - x.x[r + 1] * w.y;
-        z.x[r + 1] = x.x[r] * w.y + x.x[r + 1] * w.x;
+        p[r] = x[r] * w[r / 2].x - x[r + 1] * w[r / 2].y;
+        p[r + 1] = x[r] * w[r / 2].y + x[r + 1] * w[r / 2].x;
       }
-      z.store(dst + e);
+      put(dst, p);
     }
   }
 }
@@ -125,10 +119,12 @@ hipError_t launch_t(RotaryArgs& a, bool interleaved, hipStream_t st) {
   const int half = a.rot / 2;
   const int NR = interleaved ? a.rot / (V == 1 ? 2 : V) : half / V;
   const int per = (a.H + a.Hk) * (NR + (a.D - a.rot) / V);
-  // about four items a thread, fewer where that leaves CUs without a workgroup, and the cosines of
-  // the block within 32 KB
+  // About four vector loads a thread (an item of halves has two), fewer where that leaves CUs without
+  // a workgroup, and the cosines of the block within 32 KB.  131072 tokens, 16 + 16 bf16 heads of
+  // width 64, halves: two items 194 us, one 190, four 203, six 210; neighbours: four items 190, one
+  // 243, two 197, six 196.  8 x 4096 tokens, halves: 40.4, 40.3, 42.7, 43.8.
   const long long tokens = (long long)a.B * a.T;
-  a.TT = 4 * kThreads / per;
+  a.TT = (interleaved ? 4 : 2) * kThreads / per;
   if (a.TT > tokens / 512) a.TT = (int)(tokens / 512);
   if (a.TT * half > 4096) a.TT = 4096 / half;
   if (a.TT < 1) a.TT = 1;
