@@ -34,7 +34,8 @@ struct DecayArgs {
   int n_seg;                              // batch form: segments of a sequence
   int n_slots;                            // segment slots over all sequences
   int nvb;                                // value-column blocks
-  int scan;                               // a state pass and a scan run before the walk, and write fin
+  int scan;                               // a state pass runs before the walk, and then the scan, which writes fin
+  int join;                               // with scan: no scan kernel, the walk adds the sums itself and writes fin
 };
 
 // exact_state: the terms of fin are added without rounding a factor to bf16.

@@ -364,7 +364,7 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   const long long SE = (long long)R.dk * R.dv, st_off = ((long long)s.seq * A.H + h) * SE;
   const int rs = R.init_trans ? 1 : R.dv, cs = R.init_trans ? R.dk : 1;   // strides of init
   if (s.seg >= n_seg) {
-    if (!kStatePass && !A.scan && s.len == 0 && s.seg == 0 && R.fin)          // an empty sequence
+    if (!kStatePass && (!A.scan || A.join) && s.len == 0 && s.seg == 0 && R.fin)          // an empty sequence
       for (int i = tid; i < R.dk * DV; i += kThr) {
         const int r = i / DV, c = c0 + i % DV;
         if (c < R.dv)
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
 
   // state tiles: S[i] lane holds rows 16 i + 4 g + r of column wc + l16
   f32x4 S[NS];
-  const bool from_scan = n_seg > 1, has_state = !kStatePass && (from_scan || R.init);
+  const bool from_scan = n_seg > 1 && !A.join, has_state = !kStatePass && (from_scan || R.init);
   {
     const float* src = from_scan ? R.states + ((long long)slot * A.H + h) * SE : R.init + st_off;
     const int r1 = from_scan ? dv : rs, q1 = from_scan ? 1 : cs, col = c0 + wc + l16;
@@ -426,6 +426,45 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   if (has_state && !from_scan && !R.rev)            // a given state is decayed to the first token
 #pragma unroll
     for (int i = 0; i < NS; ++i) S[i] *= pw[1];
+  if constexpr (!kStatePass)
+    if (A.join && dv > c0 + wc) {
+      // The entry state from the sums of the segments before, as the scan adds them; with the own sum
+      // it becomes the final state.
+      constexpr int JB = NS > 4 ? 2 : 4;            // sums in flight
+      const double lg = log2_decay(A.log_decay[h]);
+      const float f = decay_power(lg, kC * L);
+      const float f_last = decay_power(lg, s.len - (n_seg - 1) * kC * L - (R.rev ? 0 : 1));
+      const int sums = s.seg + (last_seg && R.fin ? 1 : 0), col = c0 + wc + l16;
+      const bool live = col < dv;
+      const float* src = R.states + ((long long)(slot - s.seg) * A.H + h) * SE + 4 * g * dv + (live ? col : 0);
+      for (int j = 0; j < sums; j += JB) {
+        f32x4 u[JB][NS];
+#pragma unroll
+        for (int b = 0; b < JB; ++b) {
+          const float* at = src + (long long)min(j + b, sums - 1) * A.H * SE;
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[b][i][r] = 16 * i + 4 * g + r < dk ? at[(16 * i + r) * dv] : 0.f;
+        }
+#pragma unroll
+        for (int b = 0; b < JB; ++b) {
+          if (j + b < s.seg) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) S[i][r] = fmaf(f, S[i][r], u[b][i][r]);
+          } else if (j + b < sums && live) {
+            float* dst = R.fin + st_off + 4 * g * dv + col;
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (16 * i + 4 * g + r < dk) dst[(16 * i + r) * dv] = fmaf(f_last, S[i][r], u[b][i][r]);
+          }
+        }
+      }
+    }
 
   // scores: the wave's row tile, and its J key tiles from j0 on
   constexpr int J = 16 / W;

@@ -77,6 +77,7 @@ kata::DecayArgs decay_args(const kata_decay_problem* pr, const kata::DecayPlan& 
   a.n_seg = p.n_seg;
   a.n_slots = p.n_slots;
   a.scan = p.scan;
+  a.join = p.join;
   return a;
 }
 
@@ -90,18 +91,33 @@ kata_status check_grid(const kata_decay_problem* pr, const kata::DecayPlan& p, i
   return KATA_OK;
 }
 
+// Whether a final state is written where an initial state is read: its workgroups read the initial
+// state at different times then.
+bool states_overlap(const kata::DecayArgs& a) {
+  for (int i = 0; i < a.n_roles; ++i)
+    for (int j = 0; j < a.n_roles; ++j) {
+      const uintptr_t f = uintptr_t(a.role[i].fin), s = uintptr_t(a.role[j].init);
+      const uintptr_t n = uintptr_t(a.n_seq) * a.H * a.role[0].dk * a.role[0].dv * 4;
+      if (f && s && f < s + n && s < f + n) return true;
+    }
+  return false;
+}
+
 kata_status run_decay(kata::DecayArgs& a, const kata::DecayPlan& p, bool bf16, bool exact_state,
                       hipStream_t st, const char* what) {
   hipError_t e = hipSuccess;
+  if (a.join && states_overlap(a)) a.join = 0;
   if (p.scan) {
     {
       Timed t(KATA_K_CHUNK_STATE, st);
       e = kata::launch_decay_chunks(a, bf16, exact_state, true, st);
     }
     if (e != hipSuccess) return launch_status(e, what);
-    Timed t(KATA_K_SCAN, st);
-    e = kata::launch_decay_scan(a, st);
-    if (e != hipSuccess) return launch_status(e, what);
+    if (!a.join) {
+      Timed t(KATA_K_SCAN, st);
+      e = kata::launch_decay_scan(a, st);
+      if (e != hipSuccess) return launch_status(e, what);
+    }
   }
   Timed t(a.n_roles > 1 ? KATA_K_BWD : KATA_K_CHUNK_OUTPUT, st);
   return launch_status(kata::launch_decay_chunks(a, bf16, exact_state, false, st), what);

@@ -18,6 +18,7 @@ import pytest
 import torch
 
 import kernelized_psd_feature_amd as K
+from kernelized_psd_feature_amd import layer as KL
 from oracle import layer_oracle as L
 
 pytestmark = pytest.mark.gpu
@@ -350,6 +351,23 @@ def test_decay_state_in_place_and_continued_prompts():
         o, st = K.fwd_decay(q[:, a:b], k[:, a:b], v[:, a:b], ld, initial_state=st, return_state=True)
         outs.append(o)
     _check_decay(q, k, v, ld, 1.0, o=torch.cat(outs, 1), S=st)
+
+
+@pytest.mark.parametrize("T,H", [(64, 2), (700, 16), (2000, 16), (9000, 4)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decay_final_state_over_the_initial_one(dtype, T, H):
+    """The C entry takes one array for both states, whichever way the segments are joined."""
+    q, k, v = (_randn(i, 1, T, H, 64, dtype=dtype) for i in range(3))
+    cu = torch.tensor([0, T // 3, T], dtype=torch.int32, device=DEV)
+    ld, st = _decays(H), _randn(5, 2, H, 64, 64)
+    want_o, want = K.fwd_decay(q, k, v, ld, initial_state=st, cu_seqlens=cu, return_state=True)
+    o = torch.empty_like(q)
+    pr = KL._decay_problem(q, k, v, ld, 1.0, cu, o=o)
+    ws = torch.empty(max(256, K.decay_workspace_size(q, k, v, ld, cu_seqlens=cu)), dtype=torch.uint8, device=DEV)
+    KL._run("kata_fwd_decay", q.device, pr, q.data_ptr(), k.data_ptr(), v.data_ptr(), ld.data_ptr(), cu.data_ptr(),
+            st.data_ptr(), o.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel())
+    # the scan and the walk add a state's terms in the same order and precision
+    assert torch.equal(o, want_o) and torch.equal(st, want)
 
 
 def test_decay_large_offsets():
