@@ -330,7 +330,11 @@ bool launch_rows(NormArgs& a, hipStream_t st) {
   const int nv = a.N / V;
   auto run = [&](auto fwd, auto bwd, int rpb) {
     const long long want = (a.rows + rpb - 1) / rpb;
-    const int most = kBwd ? kNormBlocks : 2 * kNormBlocks;
+    // Backward: three workgroups a CU, as one or two leave less in flight and four more partial rows to
+    // add (32768 x 1024 bf16: 39.9 us; 1024 workgroups 41.3, 512 40.4, 256 60; 65536 x 512: 40.8, 40.9,
+    // 45.9, 76), two where their rows are few (4096 x 1024: 13.6 us with 512, 16.7 with 768, 18.6
+    // with 1024).
+    const int most = !kBwd ? 2048 : want < 4 * kNormBlocks ? 512 : kNormBlocks;
     a.blocks = (int)(want < most ? want : most);
     launch_kernel(kBwd ? bwd : fwd, dim3(a.blocks), kThreads, 0, st, a);
     return true;
