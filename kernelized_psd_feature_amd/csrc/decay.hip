@@ -336,12 +336,17 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // The value blocks and roles of one (slot, head) read the same rows: their workgroups get ids
-  // congruent mod 8, one XCD.
+  // The value blocks and roles of one (slot, head) read the same rows, and its other segments write
+  // the sums that it adds up: their workgroups get ids congruent mod 8, one XCD.  Over the sequences
+  // the heads go round: with 16 heads an XCD would otherwise have two of them all along, whose rows
+  // lie 2 KB apart and meet few of its L2's channels (8 x 4096 backward: 173 us for 185, 4 x 16384
+  // walk: 113 for 121; round over the segments too: 173 and 124, and 2048 tokens 22.3 for 19.7).
   const unsigned x = blockIdx.x, per = A.nvb * A.n_roles, y = x / 8 / per, unit = 8 * y + x % 8;
   const int sub = int(x / 8 - y * per);
   if (unit >= (unsigned)A.n_slots * (unsigned)A.H) return;
-  const int slot = int(unit / (unsigned)A.H), h = int(unit - (unsigned)slot * (unsigned)A.H);
+  const int slot = int(unit / (unsigned)A.H);
+  const unsigned turn = A.packed ? 0u : (unsigned)slot / (unsigned)A.n_seg;
+  const int h = int((unit - (unsigned)slot * (unsigned)A.H + turn) % (unsigned)A.H);
   const DecayRole& R = A.role[sub % A.n_roles];
   const int c0 = sub / A.n_roles * DV;              // first value column
   if (c0 >= R.dv) return;
