@@ -30,6 +30,7 @@ struct DecayArgs {
   const int* cu;                          // packed: [n_seq + 1] first rows of the sequences
   int n_roles, n_seq, H, T;
   int packed, zero_tail;
+  int stream;                             // q, k and v are loaded past the caches
   int L;                                  // chunks of 64 tokens in a segment
   int n_seg;                              // batch form: segments of a sequence
   int n_slots;                            // segment slots over all sequences

@@ -219,9 +219,15 @@ struct Stage {
   // row 0 at base, rows st elements apart (negative in reversed time)
   __device__ __forceinline__ Stage(const T* base, long long st)
       : p(base + (long long)(threadIdx.x / PER) * st + (threadIdx.x % PER) * V) {}
-  __device__ __forceinline__ void fetch(long long st) {             // 64 whole rows
+  // 64 whole rows; kStream: nothing of them is kept in the caches
+  template <bool kStream>
+  __device__ __forceinline__ void fetch(long long st) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const uint4*>(p + i * kRows * st);
+    for (int i = 0; i < N; ++i) {
+      typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+      const u32x4* at = reinterpret_cast<const u32x4*>(p + i * kRows * st);
+      x[i] = __builtin_bit_cast(uint4, kStream ? __builtin_nontemporal_load(at) : *at);
+    }
     p += kC * st;
   }
   __device__ __forceinline__ void fetch(long long st, int n, int width) {
@@ -396,10 +402,17 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   T* po = out + (t0 + (long long)dir * l16) * R.so[1] + wc + 4 * g;   // the lane's first output
 
   auto fetch = [&](int n) {
-    if (n == kC && whole_rows) {                    // uniform
-      if constexpr (!kStatePass) ra.fetch(sta);
-      rb.fetch(stb);
-      rc.fetch(stc);
+    if (n == kC && whole_rows && A.stream) {        // uniform
+      // (the empty asm keeps the compiler from joining the two branches' loads, as plain ones)
+      asm volatile("" ::: "memory");
+      if constexpr (!kStatePass) ra.template fetch<true>(sta);
+      rb.template fetch<true>(stb);
+      rc.template fetch<true>(stc);
+      asm volatile("" ::: "memory");
+    } else if (n == kC && whole_rows) {
+      if constexpr (!kStatePass) ra.template fetch<false>(sta);
+      rb.template fetch<false>(stb);
+      rc.template fetch<false>(stc);
     } else {
       if constexpr (!kStatePass) ra.fetch(sta, n, dk);
       rb.fetch(stb, n, dk);

@@ -78,6 +78,7 @@ kata::DecayArgs decay_args(const kata_decay_problem* pr, const kata::DecayPlan& 
   a.n_slots = p.n_slots;
   a.scan = p.scan;
   a.join = p.join;
+  a.stream = p.stream;
   return a;
 }
 

@@ -19,6 +19,7 @@ struct DecayPlan {
   int n_seg = 1;                          // batch form: segments of a sequence
   int n_slots = 1;                        // segment slots over all sequences
   int scan = 0;                           // 1: a state pass and a scan run before the walk
+  int stream = 0;                         // 1: q, k and v are loaded past the caches
   int join = 0;                           // 1: the walk does the scan's work itself
   size_t role_bytes = 0;                  // workspace of one role's segment states
 };
