@@ -34,7 +34,7 @@ struct DecayArgs {
   int L;                                  // chunks of 64 tokens in a segment
   int n_seg;                              // batch form: segments of a sequence
   int n_slots;                            // segment slots over all sequences
-  int nvb;                                // value-column blocks
+  int blocks;                             // value-column blocks, those of all roles
   int scan;                               // a state pass runs before the walk, and then the scan, which writes fin
   int join;                               // with scan: no scan kernel, the walk adds the sums itself and writes fin
 };

@@ -347,15 +347,22 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   // the heads go round: with 16 heads an XCD would otherwise have two of them all along, whose rows
   // lie 2 KB apart and meet few of its L2's channels (8 x 4096 backward: 173 us for 185, 4 x 16384
   // walk: 113 for 121; round over the segments too: 173 and 124, and 2048 tokens 22.3 for 19.7).
-  const unsigned x = blockIdx.x, per = A.nvb * A.n_roles, y = x / 8 / per, unit = 8 * y + x % 8;
-  const int sub = int(x / 8 - y * per);
+  const unsigned x = blockIdx.x, per = A.blocks, y = x / 8 / per, unit = 8 * y + x % 8;
+  int sub = int(x / 8 - y * per), role = 0;
   if (unit >= (unsigned)A.n_slots * (unsigned)A.H) return;
   const int slot = int(unit / (unsigned)A.H);
   const unsigned turn = A.packed ? 0u : (unsigned)slot / (unsigned)A.n_seg;
   const int h = int((unit - (unsigned)slot * (unsigned)A.H + turn) % (unsigned)A.H);
-  const DecayRole& R = A.role[sub % A.n_roles];
-  const int c0 = sub / A.n_roles * DV;              // first value column
-  if (c0 >= R.dv) return;
+  // The roles' blocks one after the other, none without columns: a workgroup that only leaves still
+  // takes its turn in the order in which they are dealt out (2 x 1001 fp32, 3 heads of 72 and 40:
+  // backward 68 us with one such of six).
+  if (A.n_roles > 1) {
+    const int n0 = (A.role[0].dv + DV - 1) / DV, n1 = n0 + (A.role[1].dv + DV - 1) / DV;
+    role = (sub >= n0) + (sub >= n1);
+    sub -= sub >= n1 ? n1 : sub >= n0 ? n0 : 0;
+  }
+  const DecayRole& R = A.role[role];
+  const int c0 = sub * DV;                          // first value column
 
   Segment s;
   if (!find_segment(A, slot, sh, s)) return;
@@ -848,7 +855,7 @@ __global__ __launch_bounds__(kThreads) void decay_decode_kernel(
 template <typename T, int DK, int W, int SPLIT>
 hipError_t launch_chunks_t(const DecayArgs& a, bool state_pass, hipStream_t st) {
   const long long units = (long long)a.n_slots * a.H;
-  const long long blocks = (units + 7) / 8 * 8 * a.nvb * a.n_roles;
+  const long long blocks = (units + 7) / 8 * 8 * a.blocks;
   auto run = [&](auto kernel, int bytes) {
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes);
     if (e != hipSuccess) return e;
@@ -879,7 +886,8 @@ hipError_t launch_decay_chunks(DecayArgs& a, bool bf16, bool exact_state, bool s
     dv = dv > a.role[r].dv ? dv : a.role[r].dv;
   }
   const int cols = decay_columns(bf16, dv);
-  a.nvb = (dv + cols - 1) / cols;
+  a.blocks = 0;
+  for (int r = 0; r < a.n_roles; ++r) a.blocks += (a.role[r].dv + cols - 1) / cols;
   if (!bf16) return launch_chunks_d<float, 4, 1>(a, dk, state_pass, st);
   // a state that the caller keeps gets the exact terms, in the pass that computes it
   const bool exact = exact_state && state_pass == (a.scan != 0);

@@ -78,15 +78,18 @@ DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles) {
   const int64_t chunks = (int64_t(pr->T) + kDecayChunk - 1) / kDecayChunk;
   const int wide = n_roles > 1 ? std::max(pr->dk, pr->dv) : pr->dv;
   const int cols = decay_columns(pr->dtype == KATA_BF16, wide);
-  // Workgroups that the card holds at once: two of four waves a CU, or one of eight.  Half as many
-  // leave it idle (8 x 4096 x 16 heads of width 64: 93 us for 82), twice as many add segment states
-  // and their scan (103 us).
-  const int64_t target = cols == 128 ? 256 : 512;
-  const int64_t blocks = int64_t(pr->H) * ((wide + cols - 1) / cols) * n_roles;
+  // Workgroups that the card holds at once: two of four waves a CU, or one of eight, or of four that
+  // keep an fp32 state of more than 64 rows (2 x 1001, 3 heads of 128: 55 us backward, 74 with 512
+  // of them, 83 with 128).  Half as many leave it idle (8 x 4096, 16 bf16 heads of width 64: 93 us
+  // for 82), twice as many add segment states and their scan (103 us).
+  const bool deep = pr->dtype == KATA_F32 && (n_roles > 1 ? wide : pr->dk) > 64;
+  const int64_t target = cols == 128 || deep ? 256 : 512;
+  const auto col_blocks = [&](int width) { return int64_t((width + cols - 1) / cols); };
+  const int64_t blocks = pr->H * (n_roles > 1 ? 2 * col_blocks(pr->dk) + col_blocks(pr->dv) : col_blocks(pr->dv));
   // segments that a sequence (packed: all tokens together) is cut into to fill the card
   const int64_t want = std::max<int64_t>(1, target / (pr->packed ? blocks : blocks * pr->n_seq));
-  // Short sequences stay whole, and a segment has a few chunks at least: the state pass and the scan
-  // cost two launches.  512 tokens of 16 bf16 heads: 20 us whole, 24 in segments of 3; 1024: 25 in
+  // Short sequences stay whole, and a segment has a few chunks at least: the state pass costs a launch,
+  // and the scan another.  512 tokens of 16 bf16 heads: 20 us whole, 24 in segments of 3; 1024: 25 in
   // segments of 3, 28 of 4, 34 of 8.  A chunk in fp32 takes three times as long (512 tokens of 4
   // heads: 25 us in segments of 1, 46 whole).
   const bool bf16 = pr->dtype == KATA_BF16;
