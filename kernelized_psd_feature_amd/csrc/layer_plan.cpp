@@ -109,8 +109,8 @@ DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles) {
   // (64 x 1024: 107, 121; 131072 tokens: 320 to 340, 375), 448 MB 144, 146, 384 MB 140, 137, 256 MB
   // 83, 75.  The gradients' three roles share what they read, and take it through the cache (32 x
   // 2048: 278 us, 308 past it; with only the operands of one role past it 289).
-  const int64_t rows = int64_t(pr->T) * (pr->packed ? 1 : pr->n_seq) * pr->H;
-  p.stream = n_roles == 1 && rows * 2 * (pr->dk + pr->dv) * (bf16 ? 2 : 4) > int64_t(384) << 20;
+  const double rows = double(pr->T) * (pr->packed ? 1 : pr->n_seq) * pr->H;
+  p.stream = n_roles == 1 && rows * 2 * (pr->dk + pr->dv) * (bf16 ? 2 : 4) > 384 * 1048576.;
   const size_t states = size_t(p.n_slots) * pr->H * pr->dk * pr->dv * 4;
   p.role_bytes = p.scan ? (states + 255) & ~size_t(255) : 0;
   return p;
