@@ -381,6 +381,26 @@ def test_decay_large_offsets():
     assert torch.equal(K.fwd_decay(x, x, x, ld), K.fwd_decay(*[x.contiguous()] * 3, ld))
 
 
+@pytest.mark.parametrize("T,dk,dv", [(2200, 64, 64), (2600, 64, 64), (2600, 128, 40), (2600, 40, 128)])
+def test_decay_segments_joined_by_the_walk_and_by_the_scan(T, dk, dv):
+    # 12 and 14 segments of three chunks, with all states
+    q, k, v, g = (_randn(i, 1, T, 1, d, dtype=BF) for i, d in ((1, dk), (2, dk), (3, dv), (4, dv)))
+    S0, dS, ld = _randn(5, 1, 1, dk, dv), _randn(6, 1, 1, dk, dv), _decays(1, "-0.004")
+    o, S = K.fwd_decay(q, k, v, ld, scale=0.125, initial_state=S0, return_state=True)
+    grads = K.bwd_decay(q, k, v, g, ld, scale=0.125, initial_state=S0, dfinal_state=dS)
+    _check_decay(q, k, v, ld, 0.125, S0=S0, dO=g, dS=dS, o=o, S=S, grads=grads)
+
+
+@pytest.mark.parametrize("dtype,B,H", [(BF, 64, 32), (F32, 64, 16)])
+def test_decay_of_operands_larger_than_the_caches(dtype, B, H):
+    # loaded past the caches; half of the sequences are not, and get the same results
+    q, k, v = (_randn(i, B, 500, H, 64, dtype=dtype) for i in range(3))
+    ld = _decays(H)
+    o = K.fwd_decay(q, k, v, ld)
+    for part in (slice(0, B // 2), slice(B // 2, B)):
+        assert torch.equal(o[part], K.fwd_decay(q[part], k[part], v[part], ld))
+
+
 def test_decay_refusals():
     q, k, v = (_randn(i, 1, 8, 2, 64, dtype=BF) for i in range(3))
     ld = _decays(2)
