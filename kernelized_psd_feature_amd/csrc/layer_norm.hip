@@ -10,7 +10,9 @@
 // walks over many rows: w and b are read once, and the backward pass keeps its sums of dw and
 // db in registers over its rows, adds them up across its lanes and leaves one partial row pair, which a
 // second kernel adds in block order (no atomics: the same result every time).
-// Bound: HBM.  Rows wider than the widest register form go through the loop kernels, which read
+// Bound: HBM.  32768 x 1024 bf16, calls in a row: forward 24 us (5.6 TB/s, part of it from the Infinity
+// Cache; 30 us and 4.4 TB/s for rows that are not there), backward 39 us and 5 us of sums (5.2 TB/s).
+// 512 x 1024: 3.3 us forward, latency.  Rows wider than the widest register form go through the loop kernels, which read
 // a row again for each pass (from the L2 cache where it fits).
 #include "device.h"
 #include "layer.h"
