@@ -339,9 +339,9 @@ kata_status kata_decode_decay(const kata_decay_problem* pr, const void* q, const
  * with the angle negated where inverse is set (the gradient); coordinates from rot on are copied.
  * Angles are formed in fp64, so far positions keep their phase.
  *   q [B][T][H][D] and, unless Hk = 0, k [B][T][Hk][D], the last axis contiguous; D <= 1024, rot
- *   even.  Rows of whole, aligned 16-byte vectors (in the half layout rot / 2 too) take 16-byte
- *   accesses, others go element by element.  An output may be its own input (in place) but must
- *   not overlap inputs otherwise.
+ *   even.  Rows of any alignment; those of whole, aligned 16-byte vectors (in the half layout rot / 2
+ *   too) are the fastest.  An output may be its own input (in place) but must not overlap inputs
+ *   otherwise.
  *   rates: device fp64 [rot / 2], radians a token.  magnitude: m.
  *   positions: device int32 or (pos64) int64 with element strides pos_b, pos_t (zero: broadcast), or
  *   NULL: token t has position offset + t. */

@@ -12,8 +12,11 @@
 // second kernel adds in block order (no atomics: the same result every time).
 // Bound: HBM.  32768 x 1024 bf16, calls in a row: forward 24 us (5.6 TB/s, part of it from the Infinity
 // Cache; 30 us and 4.4 TB/s for rows that are not there), backward 39 us and 5 us of sums (5.2 TB/s).
-// 512 x 1024: 3.3 us forward, latency.  Rows wider than the widest register form go through the loop kernels, which read
-// a row again for each pass (from the L2 cache where it fits).
+// 512 x 1024: 3.3 us forward, latency.  Rows that are not whole, aligned vectors take unaligned 16-byte
+// accesses and single elements at their end (kEdge; 8192 x 4097: 33 and 101 us, element by element 63
+// and 110; 16384 x 2047: 38 and 66, 65 and 142).  Rows wider than the widest register form (8192
+// elements) go through the loop kernels, which read a row again for each pass (from the L2 cache
+// where it fits).
 #include "device.h"
 #include "layer.h"
 #include "mfma_util.h"
@@ -23,31 +26,46 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(float (&x)[V], const T* p) {
-  if constexpr (V == 1) {
-    x[0] = to_f32(p[0]);
+// The 16 bytes of V elements; kEdge: at any element, which this card's global memory allows.
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Unaligned {
+  u32x4 u;
+};
+
+// V elements from column c on; kEdge: rows of any length and alignment, zeros behind N.
+template <typename T, int V, bool kEdge>
+__device__ __forceinline__ void load_vec(float (&x)[V], const T* p, int c, int N) {
+  if (kEdge && c + V > N) {
+#pragma unroll
+    for (int r = 0; r < V; ++r) x[r] = c + r < N ? to_f32(p[c + r]) : 0.f;
+    return;
+  }
+  const u32x4 u = kEdge ? reinterpret_cast<const Unaligned<T>*>(p + c)->u
+                        : *reinterpret_cast<const u32x4*>(p + c);
+  if constexpr (sizeof(T) == 2) {
+    x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
+    x[4] = bf_lo(u.z); x[5] = bf_hi(u.z); x[6] = bf_lo(u.w); x[7] = bf_hi(u.w);
   } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    if constexpr (sizeof(T) == 2) {
-      x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
-      x[4] = bf_lo(u.z); x[5] = bf_hi(u.z); x[6] = bf_lo(u.w); x[7] = bf_hi(u.w);
-    } else {
-      x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-      x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
-    }
+    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
   }
 }
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
-  if constexpr (V == 1) {
-    p[0] = from_f32<T>(x[0]);
-  } else if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) = uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                         pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
-  } else {
-    *reinterpret_cast<float4*>(p) = float4{x[0], x[1], x[2], x[3]};
+template <typename T, int V, bool kEdge>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[V], int c, int N) {
+  if (kEdge && c + V > N) {
+#pragma unroll
+    for (int r = 0; r < V; ++r)
+      if (c + r < N) p[c + r] = from_f32<T>(x[r]);
+    return;
   }
+  u32x4 u;
+  if constexpr (sizeof(T) == 2)
+    u = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+  else
+    u = u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+  if (kEdge) reinterpret_cast<Unaligned<T>*>(p + c)->u = u;
+  else *reinterpret_cast<u32x4*>(p + c) = u;
 }
 
 __device__ __forceinline__ float param(const void* p, int bf16, int i, float none) {
@@ -56,13 +74,15 @@ __device__ __forceinline__ float param(const void* p, int bf16, int i, float non
 }
 
 // V neighbouring parameters from column c on; `none` where there are none or behind N.
-template <int V>
+template <int V, bool kEdge>
 __device__ __forceinline__ void load_params(float (&x)[V], const void* p, int bf16, int c, int N, float none) {
 #pragma unroll
   for (int r = 0; r < V; ++r) x[r] = none;
   if (!p || c >= N) return;
-  if constexpr (V == 1) {
-    x[0] = param(p, bf16, c, none);
+  if (kEdge && c + V > N) {
+#pragma unroll
+    for (int r = 0; r < V; ++r)
+      if (c + r < N) x[r] = param(p, bf16, c + r, none);
   } else if (bf16) {
     const __bf16* b = reinterpret_cast<const __bf16*>(p) + c;
 #pragma unroll
@@ -89,7 +109,7 @@ __device__ __forceinline__ float row_sum(float x, float* sh) {
   return x;
 }
 
-template <typename T, int V, int R, int K>
+template <typename T, int V, int R, int K, bool kEdge>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs A) {
   __shared__ float sh[4];
   constexpr int RPB = kThreads / R;                 // rows at a time
@@ -97,8 +117,8 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs A) {
   float w[K][V], b[K][V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    load_params<V>(w[k], A.w, A.w_bf16, (k * R + l) * V, N, 1.f);
-    load_params<V>(b[k], A.b, A.w_bf16, (k * R + l) * V, N, 0.f);
+    load_params<V, kEdge>(w[k], A.w, A.w_bf16, (k * R + l) * V, N, 1.f);
+    load_params<V, kEdge>(b[k], A.b, A.w_bf16, (k * R + l) * V, N, 0.f);
   }
   const float n = (float)N;
   // R = 256: one row at a time, so all threads leave the loop together
@@ -111,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs A) {
       const int c = (k * R + l) * V;
 #pragma unroll
       for (int r = 0; r < V; ++r) x[k][r] = 0.f;
-      if (c < N) load_vec<T, V>(x[k], px + c);
+      if (c < N) load_vec<T, V, kEdge>(x[k], px, c, N);
 #pragma unroll
       for (int r = 0; r < V; ++r) sum += x[k][r];
     }
@@ -121,7 +141,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs A) {
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int r = 0; r < V; ++r) {
-        x[k][r] = (k * R + l) * V < N ? x[k][r] - mean : 0.f;
+        x[k][r] = (k * R + l) * V + (kEdge ? r : 0) < N ? x[k][r] - mean : 0.f;
         sq = fmaf(x[k][r], x[k][r], sq);
       }
     const float rstd = 1.f / sqrtf(row_sum<R>(sq, sh) / n + A.eps);
@@ -131,7 +151,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs A) {
       const int c = (k * R + l) * V;
 #pragma unroll
       for (int r = 0; r < V; ++r) x[k][r] = fmaf(x[k][r] * rstd, w[k][r], b[k][r]);
-      if (c < N) store_vec<T, V>(py + c, x[k]);
+      if (c < N) store_vec<T, V, kEdge>(py, x[k], c, N);
     }
     if (l == 0 && A.mean) {
       A.mean[row] = mean;
@@ -140,7 +160,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs A) {
   }
 }
 
-template <typename T, int V, int R, int K>
+template <typename T, int V, int R, int K, bool kEdge>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs A) {
   constexpr int RPB = kThreads / R, W = R < 64 ? R : 64;
   __shared__ float sh[4];
@@ -149,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs A) {
   float w[K][V], gw[K][V], gb[K][V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    load_params<V>(w[k], A.w, A.w_bf16, (k * R + l) * V, N, 1.f);
+    load_params<V, kEdge>(w[k], A.w, A.w_bf16, (k * R + l) * V, N, 1.f);
 #pragma unroll
     for (int r = 0; r < V; ++r) gw[k][r] = gb[k][r] = 0.f;
   }
@@ -166,10 +186,10 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs A) {
 #pragma unroll
       for (int r = 0; r < V; ++r) hat[k][r] = t[k][r] = 0.f;
       if (c < N) {
-        load_vec<T, V>(hat[k], px + c);
-        load_vec<T, V>(t[k], pg + c);
+        load_vec<T, V, kEdge>(hat[k], px, c, N);
+        load_vec<T, V, kEdge>(t[k], pg, c, N);
 #pragma unroll
-        for (int r = 0; r < V; ++r) hat[k][r] = (hat[k][r] - mean) * rstd;
+        for (int r = 0; r < V; ++r) hat[k][r] = !kEdge || c + r < N ? (hat[k][r] - mean) * rstd : 0.f;
       }
 #pragma unroll
       for (int r = 0; r < V; ++r) {
@@ -189,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs A) {
         const int c = (k * R + l) * V;
 #pragma unroll
         for (int r = 0; r < V; ++r) t[k][r] = (t[k][r] - s1 - hat[k][r] * s2) * rstd;
-        if (c < N) store_vec<T, V>(pd + c, t[k]);
+        if (c < N) store_vec<T, V, kEdge>(pd, t[k], c, N);
       }
     }
   }
@@ -327,41 +347,41 @@ __global__ __launch_bounds__(kThreads) void norm_dw_loop_kernel(NormArgs A) {
   part[A.N] = gb;
 }
 
-template <typename T, int V, bool kBwd>
+template <typename T, bool kEdge, bool kBwd>
 bool launch_rows(NormArgs& a, hipStream_t st) {
-  const int nv = a.N / V;
-  auto run = [&](auto fwd, auto bwd, int rpb) {
+  constexpr int V = 16 / sizeof(T);
+  const int nv = (a.N + V - 1) / V;
+  auto run = [&](auto fwd, auto bwd, int rpb, int held) {
     const long long want = (a.rows + rpb - 1) / rpb;
     // Backward: three workgroups a CU, as one or two leave less in flight and four more partial rows to
     // add (32768 x 1024 bf16: 39.9 us; 1024 workgroups 41.3, 512 40.4, 256 60; 65536 x 512: 40.8, 40.9,
     // 45.9, 76), two where their rows are few (4096 x 1024: 13.6 us with 512, 16.7 with 768, 18.6
-    // with 1024).
-    const int most = !kBwd ? 2048 : want < 4 * kNormBlocks ? 512 : kNormBlocks;
+    // with 1024) and where no more fit (32 elements a thread in registers).
+    const int most = !kBwd ? 2048 : want < 4 * kNormBlocks || held >= 32 ? 512 : kNormBlocks;
     a.blocks = (int)(want < most ? want : most);
     launch_kernel(kBwd ? bwd : fwd, dim3(a.blocks), kThreads, 0, st, a);
     return true;
   };
 #define KATA_NORM(R_, K_)                                                                       \
   if (nv <= R_ * K_)                                                                            \
-    return run(norm_fwd_kernel<T, V, R_, K_>, norm_bwd_kernel<T, V, R_, K_>, kThreads / R_);
+    return run(norm_fwd_kernel<T, V, R_, K_, kEdge>, norm_bwd_kernel<T, V, R_, K_, kEdge>, kThreads / R_, K_ * V);
   KATA_NORM(8, 1) KATA_NORM(16, 1) KATA_NORM(32, 1) KATA_NORM(64, 1) KATA_NORM(64, 2)
-  KATA_NORM(64, 4) KATA_NORM(256, 2) KATA_NORM(256, 4)
+  KATA_NORM(64, 3) KATA_NORM(64, 4) KATA_NORM(256, 2) KATA_NORM(256, 3) KATA_NORM(256, 4)
+  if constexpr (V == 4) KATA_NORM(256, 8)           // 32 elements a thread, as of bf16 rows
 #undef KATA_NORM
   return false;
 }
 
 template <typename T>
-hipError_t fwd_t(NormArgs& a, bool vec, hipStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  if (vec ? launch_rows<T, V, false>(a, st) : launch_rows<T, 1, false>(a, st)) return hipGetLastError();
+hipError_t fwd_t(NormArgs& a, bool whole, hipStream_t st) {
+  if (whole ? launch_rows<T, false, false>(a, st) : launch_rows<T, true, false>(a, st)) return hipGetLastError();
   launch_kernel(norm_fwd_loop_kernel<T>, dim3((unsigned)(a.rows < 2048 ? a.rows : 2048)), kThreads, 0, st, a);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t bwd_t(NormArgs& a, bool vec, hipStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  if (!(vec ? launch_rows<T, V, true>(a, st) : launch_rows<T, 1, true>(a, st))) {
+hipError_t bwd_t(NormArgs& a, bool whole, hipStream_t st) {
+  if (!(whole ? launch_rows<T, false, true>(a, st) : launch_rows<T, true, true>(a, st))) {
     // dw and db first: dx may overwrite dy
     a.blocks = (int)(a.rows < 64 ? a.rows : 64);
     if (a.part)
@@ -375,7 +395,7 @@ hipError_t bwd_t(NormArgs& a, bool vec, hipStream_t st) {
   return hipGetLastError();
 }
 
-// 16-byte accesses need rows of whole vectors.
+// Rows of whole, aligned vectors.
 bool vectors(const NormArgs& a, bool bf16, bool aligned) { return aligned && a.N % (bf16 ? 8 : 4) == 0; }
 
 }  // namespace
