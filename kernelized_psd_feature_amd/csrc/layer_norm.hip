@@ -73,6 +73,12 @@ __device__ __forceinline__ float param(const void* p, int bf16, int i, float non
   return bf16 ? (float)reinterpret_cast<const __bf16*>(p)[i] : reinterpret_cast<const float*>(p)[i];
 }
 
+__device__ __forceinline__ void store_param(void* p, int bf16, int i, float x) {
+  if (!p) return;
+  if (bf16) reinterpret_cast<__bf16*>(p)[i] = (__bf16)x;
+  else reinterpret_cast<float*>(p)[i] = x;
+}
+
 // V neighbouring parameters from column c on; `none` where there are none or behind N.
 template <int V, bool kEdge>
 __device__ __forceinline__ void load_params(float (&x)[V], const void* p, int bf16, int c, int N, float none) {
@@ -242,7 +248,10 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs A) {
 #pragma unroll
         for (int r = 0; r < V; ++r) {
           const int c = (k * R + l) * V + r;
-          if (c < N) part[(long long)which * N + c] = y[r];
+          if (c < N) {
+            if (gridDim.x > 1) part[(long long)which * N + c] = y[r];
+            else store_param(which ? A.db : A.dw, A.w_bf16, c, y[r]);
+          }
         }
     }
 }
@@ -271,10 +280,7 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs A) {
   __syncthreads();
   if (s == 0 && c < A.N) {
     for (int i = 1; i < 32; ++i) sum += sh[i][col];
-    void* out = which ? A.db : A.dw;
-    if (!out) return;
-    if (A.w_bf16) reinterpret_cast<__bf16*>(out)[c] = (__bf16)sum;
-    else reinterpret_cast<float*>(out)[c] = sum;
+    store_param(which ? A.db : A.dw, A.w_bf16, c, sum);
   }
 }
 
@@ -358,7 +364,9 @@ bool launch_rows(NormArgs& a, hipStream_t st) {
     // 45.9, 76), two where their rows are few (4096 x 1024: 13.6 us with 512, 16.7 with 768, 18.6
     // with 1024) and where no more fit (32 elements a thread in registers).
     const int most = !kBwd ? 2048 : want < 4 * kNormBlocks || held >= 32 ? 512 : kNormBlocks;
-    a.blocks = (int)(want < most ? want : most);
+    // A few rows: one workgroup, whose sums are the gradients, instead of a second kernel (8 x 1024, two
+    // turns: 7.6 us for 8.1 and a launch less; four turns: 9.8).
+    a.blocks = kBwd && want <= 2 ? 1 : (int)(want < most ? want : most);
     launch_kernel(kBwd ? bwd : fwd, dim3(a.blocks), kThreads, 0, st, a);
     return true;
   };
@@ -381,7 +389,8 @@ hipError_t fwd_t(NormArgs& a, bool whole, hipStream_t st) {
 
 template <typename T>
 hipError_t bwd_t(NormArgs& a, bool whole, hipStream_t st) {
-  if (!(whole ? launch_rows<T, false, true>(a, st) : launch_rows<T, true, true>(a, st))) {
+  const bool rows = whole ? launch_rows<T, false, true>(a, st) : launch_rows<T, true, true>(a, st);
+  if (!rows) {
     // dw and db first: dx may overwrite dy
     a.blocks = (int)(a.rows < 64 ? a.rows : 64);
     if (a.part)
@@ -390,7 +399,7 @@ hipError_t bwd_t(NormArgs& a, bool whole, hipStream_t st) {
       launch_kernel(norm_dx_loop_kernel<T>, dim3((unsigned)(a.rows < 2048 ? a.rows : 2048)), kThreads, 0, st, a);
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.part) return e;
+  if (e != hipSuccess || !a.part || (rows && a.blocks == 1)) return e;
   launch_kernel(norm_sum_kernel, dim3((a.N + 31) / 32, 2), 1024, 0, st, a);
   return hipGetLastError();
 }
