@@ -214,17 +214,26 @@ __device__ __forceinline__ bool find_segment(const DecayArgs& A, int slot, int* 
 }
 
 // ---- staging -------------------------------------------------------------------------------
-// A chunk of one operand: 64 rows of W columns (those behind `width` and the rows behind n zero),
-// W / (4 V) 16-byte vectors a thread.
+// A chunk of one operand: 64 rows of W columns, W / (4 V) 16-byte vectors a thread (the rows behind n
+// zero).  A thread behind the operand's `width` columns reads the row's first vector again and
+// writes it behind the tile's columns, into the row's padding: no load or write depends on the
+// width, and the tile's columns behind the width keep the zeros that they start with (4 x 8192, 8 bf16
+// heads of 72: 81 us, backward 251; with loads under a mask 96 and 334).
 template <typename T, int W, int kThr>
 struct Stage {
   static constexpr int V = Elem<T>::V, PER = W / V, N = kC * PER / kThr, kRows = kThr / PER;
   static_assert(N >= 1 && kC % kRows == 0, "whole rows a step");
   const T* p;                             // the thread's first vector of the next chunk
+  int to, to2;                            // its columns in the tile; in split order of each half
   uint4 x[N];
   // row 0 at base, rows st elements apart (negative in reversed time)
-  __device__ __forceinline__ Stage(const T* base, long long st)
-      : p(base + (long long)(threadIdx.x / PER) * st + (threadIdx.x % PER) * V) {}
+  __device__ __forceinline__ Stage(const T* base, long long st, int width, bool split) {
+    const int col = (threadIdx.x % PER) * V;
+    const bool live = col < width;
+    p = base + (long long)(threadIdx.x / PER) * st + (live ? col : 0);
+    to = !live ? W : split ? split_place(col) : col;
+    to2 = !live ? W + 4 : split_place(col + 4);
+  }
   // 64 whole rows; kStream: nothing of them is kept in the caches
   template <bool kStream>
   __device__ __forceinline__ void fetch(long long st) {
@@ -236,33 +245,34 @@ struct Stage {
     }
     p += kC * st;
   }
-  __device__ __forceinline__ void fetch(long long st, int n, int width) {
-    const int row = threadIdx.x / PER, col = (threadIdx.x % PER) * V;
+  __device__ __forceinline__ void fetch(long long st, int n) {
+    const int row = threadIdx.x / PER;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       x[i] = uint4{0u, 0u, 0u, 0u};
-      if (row + i * kRows < n && col < width) x[i] = *reinterpret_cast<const uint4*>(p + i * kRows * st);
+      if (row + i * kRows < n) x[i] = *reinterpret_cast<const uint4*>(p + i * kRows * st);
     }
     p += kC * st;
   }
   template <int LD>
   __device__ __forceinline__ void put(T* tile) const {
-    T* at = tile + threadIdx.x / PER * LD + (threadIdx.x % PER) * V;
+    static_assert(LD - W >= V, "padding for a vector");
+    T* at = tile + threadIdx.x / PER * LD + to;
 #pragma unroll
     for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(at + i * kRows * LD) = x[i];
   }
   // the rows' runs of four elements at their split places
   template <int LD>
   __device__ __forceinline__ void put_split(T* tile) const {
-    const int col = (threadIdx.x % PER) * V;
+    static_assert(LD - W >= V, "padding for a vector");
     T* at = tile + threadIdx.x / PER * LD;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if constexpr (V == 8) {
-        *reinterpret_cast<uint2*>(at + i * kRows * LD + split_place(col)) = uint2{x[i].x, x[i].y};
-        *reinterpret_cast<uint2*>(at + i * kRows * LD + split_place(col + 4)) = uint2{x[i].z, x[i].w};
+        *reinterpret_cast<uint2*>(at + i * kRows * LD + to) = uint2{x[i].x, x[i].y};
+        *reinterpret_cast<uint2*>(at + i * kRows * LD + to2) = uint2{x[i].z, x[i].w};
       } else {
-        *reinterpret_cast<uint4*>(at + i * kRows * LD + split_place(col)) = x[i];
+        *reinterpret_cast<uint4*>(at + i * kRows * LD + to) = x[i];
       }
     }
   }
@@ -406,30 +416,29 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   const int dir = R.rev ? -1 : 1, dk = R.dk, dv = R.dv;
   const long long t0 = (R.rev ? s.start + s.len - 1 : s.start) + (long long)dir * kC * first;
   const long long sta = dir * R.sa[1], stb = dir * R.sb[1], stc = dir * R.sc[1], sto = dir * R.so[1];
-  Stage<T, DK, kThr> ra(reinterpret_cast<const T*>(R.a) + s.b * R.sa[0] + t0 * R.sa[1] + h * R.sa[2], sta);
-  Stage<T, DK, kThr> rb(reinterpret_cast<const T*>(R.b) + s.b * R.sb[0] + t0 * R.sb[1] + h * R.sb[2], stb);
-  Stage<T, DV, kThr> rc(reinterpret_cast<const T*>(R.c) + s.b * R.sc[0] + t0 * R.sc[1] + h * R.sc[2] + c0, stc);
+  Stage<T, DK, kThr> ra(reinterpret_cast<const T*>(R.a) + s.b * R.sa[0] + t0 * R.sa[1] + h * R.sa[2], sta, dk, true);
+  Stage<T, DK, kThr> rb(reinterpret_cast<const T*>(R.b) + s.b * R.sb[0] + t0 * R.sb[1] + h * R.sb[2], stb, dk, false);
+  Stage<T, DV, kThr> rc(reinterpret_cast<const T*>(R.c) + s.b * R.sc[0] + t0 * R.sc[1] + h * R.sc[2] + c0, stc, dv - c0, false);
   const int wc = 16 * w;                            // the wave's columns in the block
-  const bool whole_rows = dk == DK && dv - c0 >= DV;
   const bool live_col = c0 + wc + 4 * g < dv;
   T* po = out + (t0 + (long long)dir * l16) * R.so[1] + wc + 4 * g;   // the lane's first output
 
   auto fetch = [&](int n) {
-    if (n == kC && whole_rows && A.stream) {        // uniform
+    if (n < kC) {                                   // uniform
+      if constexpr (!kStatePass) ra.fetch(sta, n);
+      rb.fetch(stb, n);
+      rc.fetch(stc, n);
+    } else if (A.stream) {
       // (the empty asm keeps the compiler from joining the two branches' loads, as plain ones)
       asm volatile("" ::: "memory");
       if constexpr (!kStatePass) ra.template fetch<true>(sta);
       rb.template fetch<true>(stb);
       rc.template fetch<true>(stc);
       asm volatile("" ::: "memory");
-    } else if (n == kC && whole_rows) {
+    } else {
       if constexpr (!kStatePass) ra.template fetch<false>(sta);
       rb.template fetch<false>(stb);
       rc.template fetch<false>(stc);
-    } else {
-      if constexpr (!kStatePass) ra.fetch(sta, n, dk);
-      rb.fetch(stb, n, dk);
-      rc.fetch(stc, n, dv - c0);
     }
   };
   const int n_last = min(kC, s.len - kC * (behind - 1));   // rows of the segment's last chunk
@@ -452,6 +461,10 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
     }
   }
   // (after the loads above are on their way)
+  if (dk < DK || dv - c0 < DV) {                    // columns that no operand has: zeros all along
+    uint4* const z = reinterpret_cast<uint4*>(sK);
+    for (int i = tid; i < TL::kBuffers * kStage * (int)sizeof(T) / 16; i += kThr) z[i] = uint4{0u, 0u, 0u, 0u};
+  }
   if (tid <= kC) pw[tid] = decay_power(log2_decay(A.log_decay[h]), tid);
   __syncthreads();
   if (has_state && !from_scan && !R.rev)            // a given state is decayed to the first token
