@@ -204,7 +204,8 @@ def fwd_decay(q, k, v, log_decay, scale=1.0, initial_state=None, return_state=Fa
     any (b, t, h) strides (broadcast axes too); o has the inputs' dtype.  log_decay: fp32 (H,).
     cu_seqlens: int32 (n + 1,) offsets of n sequences packed into B = 1; rows of no sequence are zero
     in a new output and left as they are in `out`.
-    initial_state, and the final state with return_state: fp32 (n, H, dk, dv).
+    initial_state, and the final state with return_state: fp32 (n, H, dk, dv); a state that is returned
+    has its terms added exactly, so bf16 outputs may differ from a call without it by a rounding.
     workspace: uint8, decay_workspace_size() bytes (allocated here otherwise)."""
     o = _out_like(v, out)
     pr = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, o=o, zero_tail=1 if out is None else 0)
