@@ -446,7 +446,10 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
 
   // state tiles: S[i] lane holds rows 16 i + 4 g + r of column wc + l16
   f32x4 S[NS];
-  const bool from_scan = n_seg > 1 && !A.join, has_state = !kStatePass && (from_scan || R.init);
+  // The scan has left every entry state in its slot, and may have put the final state of a sequence of one
+  // segment where its initial one was.
+  const bool from_scan = A.scan && !A.join && (n_seg > 1 || (R.init && R.fin));
+  const bool has_state = !kStatePass && (from_scan || R.init);
   {
     const float* src = from_scan ? R.states + ((long long)slot * A.H + h) * SE : R.init + st_off;
     const int r1 = from_scan ? dv : rs, q1 = from_scan ? 1 : cs, col = c0 + wc + l16;

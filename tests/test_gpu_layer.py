@@ -370,6 +370,29 @@ def test_decay_final_state_over_the_initial_one(dtype, T, H):
     assert torch.equal(o, want_o) and torch.equal(st, want)
 
 
+@pytest.mark.parametrize("lengths,H", [([100, 2000], 16), ([1, 0, 77, 2000], 16), ([2000, 64], 16),
+                                       ([1, 0, 77, 512, 130, 1303], 16), ([9000, 30, 0, 1], 4)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decay_one_array_for_both_states_of_short_and_long_sequences(dtype, lengths, H):
+    """Sequences of one segment in a call whose longer ones are joined by the scan: it writes their final
+    states before the walk needs the initial ones."""
+    T, n = sum(lengths), len(lengths)
+    q, k, v = (_randn(i, 1, T, H, 64, dtype=dtype) for i in range(3))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device=DEV)
+    ld, S0 = _decays(H), _randn(5, n, H, 64, 64)
+    want_o, want = K.fwd_decay(q, k, v, ld, initial_state=S0, cu_seqlens=cu, return_state=True)
+    st, o = S0.clone(), torch.empty_like(q)
+    pr = KL._decay_problem(q, k, v, ld, 1.0, cu, o=o)
+    ws = torch.empty(K.decay_workspace_size(q, k, v, ld, cu_seqlens=cu), dtype=torch.uint8, device=DEV)
+    assert ws.numel()                                # the long sequences have segments
+    KL._run("kata_fwd_decay", q.device, pr, q.data_ptr(), k.data_ptr(), v.data_ptr(), ld.data_ptr(), cu.data_ptr(),
+            st.data_ptr(), o.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel())
+    assert torch.equal(st, want) and torch.equal(o, want_o)
+    heads = [0, H - 1]                               # the strongest and the weakest decay
+    part = [x[:, :, heads] for x in (q, k, v)]
+    _check_decay(*part, ld[heads], 1.0, lengths, S0=S0[:, heads], o=o[:, :, heads], S=st[:, heads])
+
+
 def test_decay_large_offsets():
     # rows beyond 2^31 elements: head-major views of one big buffer, the last rows of each head used
     T, H, d = 9_000_000, 4, 64                       # 2.3e9 bf16 elements
