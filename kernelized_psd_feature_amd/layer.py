@@ -97,7 +97,7 @@ def _ptr(x):
 
 
 def _rows_ok(x, name):
-    if x.stride(-1) != 1 and x.shape[-1] > 1:
+    if x.stride(-1) != 1 and x.shape[-1] > 1 and x.numel():
         raise ValueError(f"{name}: last dimension must be contiguous")
     return x.stride()[:3]
 
@@ -353,10 +353,13 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
         except RuntimeError:
             raise ValueError("positions must broadcast to (B, T)") from None
         pos64, (pos_b, pos_t), at = int(positions.dtype == torch.int64), x.stride(), positions.data_ptr()
-    if B * T * H * D and (k is None or Hk):
+    pq, poq = q.data_ptr(), oq.data_ptr()
+    if H == 0 and Hk:                                # only k has heads: its turn is a call of one tensor
+        H, sq, soq, pq, poq, Hk = Hk, sk, sok, pk, pok, 0
+    if B * T * H * D:
         pr = _ROTARY.pack(B, T, H, Hk, D, 2 * n, _dtype(dtype), 1 if interleaved else 0, 1 if inverse else 0,
                           pos64, magnitude, pos_b, pos_t, offset, *sq[:3], *sk[:3], *soq[:3], *sok[:3])
-        _run("kata_rotary", device, pr, q.data_ptr(), pk, rates.data_ptr(), at, oq.data_ptr(), pok)
+        _run("kata_rotary", device, pr, pq, pk, rates.data_ptr(), at, poq, pok)
     return oq if k is None else (oq, ok)
 
 

@@ -494,6 +494,25 @@ def test_rotary(dtype, B, T, H, Hk, D, rot, interleaved, inverse):
     assert torch.equal(off[0], row[0])
 
 
+@pytest.mark.parametrize("H,Hk", [(2, 0), (0, 2), (0, 0)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rotary_without_heads_on_one_side(dtype, H, Hk):
+    q, k = _randn(1, 2, 5, H, 16, dtype=dtype), _randn(2, 2, 5, Hk, 16, dtype=dtype)
+    rates, m = K.rotary_rates(16)
+    want = [K.rotary(x, None, rates, offset=7) if x.numel() else x for x in (q, k)]
+    outs = torch.zeros_like(q), torch.zeros_like(k)
+    got = K.rotary(q, k, rates, offset=7, out=outs)
+    assert got[0] is outs[0] and got[1] is outs[1]
+    for got in (got, K.rotary(q, k, rates, offset=7)):
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    leaves = q.clone().requires_grad_(), k.clone().requires_grad_()
+    a, b = KL.turn(*leaves, (rates, m), offset=7)
+    grads = torch.autograd.grad(a.sum() + b.sum(), leaves)
+    for x, g in zip((q, k), grads):
+        ones = torch.ones_like(x)
+        assert torch.equal(g, K.rotary(ones, None, rates, offset=7, inverse=True) if x.numel() else x)
+
+
 def test_rotary_strides_and_alignment():
     fused = _randn(1, 2, 7, 3, 200, dtype=BF)
     rates, m = K.rotary_rates(64)
