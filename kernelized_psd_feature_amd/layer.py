@@ -547,8 +547,9 @@ def parallel_decay_attn(q, k, v, log_decay, scale=1.0, initial_state=None, retur
     o, final = got if return_state else (got, None)
     if norm is not None:
         weight, bias, eps = (*norm, 1e-5)[:3]
-        n = weight.numel() if weight is not None else v.shape[3]
-        if n not in (v.shape[3], v.shape[2] * v.shape[3]):
+        H, dv = v.shape[2:]
+        n = weight.numel() if weight is not None else dv
+        if n < 1 or n not in (dv, H * dv):
             raise ValueError("the norm's weight must have dv or H * dv elements")
-        o = layer_norm(o.reshape(*o.shape[:2], -1, n), weight, bias, eps).reshape(v.shape)
+        o = layer_norm(o.reshape(*o.shape[:2], H * dv // n, n), weight, bias, eps).reshape(v.shape)
     return (o, final) if return_state else o

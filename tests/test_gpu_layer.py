@@ -745,6 +745,25 @@ def test_autograd_of_a_layer(packed):
         _inside(x, r.numpy(), 512 * 2.0 ** -24 * float(r.abs().max()), name)
 
 
+@pytest.mark.parametrize("B,T,H", [(0, 5, 2), (2, 0, 2), (0, 0, 2), (2, 5, 0)])
+@pytest.mark.parametrize("over", ["head", "token", "none", "no norm"])
+def test_a_layer_of_an_empty_batch(B, T, H, over):
+    d = 32
+    leaves = [torch.empty(B, T, H, d, device=DEV, requires_grad=True) for _ in range(3)]
+    n = H * d if over == "token" else d
+    w, b = (torch.ones(n, device=DEV, requires_grad=True) for _ in range(2))
+    norm = {"none": (None, None), "no norm": None}.get(over, (w, b))
+    run = lambda: K.parallel_decay_attn(*leaves, torch.zeros(H, device=DEV), rotary=K.rotary_rates(d), norm=norm)  # noqa: E731
+    if n == 0:                                       # a norm over nothing
+        with pytest.raises(ValueError):
+            run()
+        return
+    o = run()
+    assert o.shape == (B, T, H, d)
+    grads = torch.autograd.grad(o.sum(), leaves + ([w, b] if over in ("head", "token") else []))
+    assert all(g.shape == x.shape for g, x in zip(grads, leaves)) and not any(g.any() for g in grads[3:])
+
+
 def test_shared_heads_and_unused_outputs_under_autograd():
     B, T, H, d = 1, 70, 4, 64
     q, k, v, ld = _randn(1, B, T, H, d), _randn(2, B, T, 1, d), _randn(3, B, T, 1, d), _decays(H)
