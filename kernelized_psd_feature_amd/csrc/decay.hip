@@ -363,7 +363,7 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   // the heads go round: with 16 heads an XCD would otherwise have two of them all along, whose rows
   // lie 2 KB apart and meet few of its L2's channels (8 x 4096 backward: 173 us for 185, 4 x 16384
   // walk: 113 for 121; round over the segments too: 173 and 124, and 2048 tokens 22.3 for 19.7).
-  const unsigned x = blockIdx.x, per = A.blocks, y = x / 8 / per, unit = 8 * y + x % 8;
+  const unsigned x = block_number(), per = A.blocks, y = x / 8 / per, unit = 8 * y + x % 8;
   int sub = int(x / 8 - y * per), role = 0;
   if (unit >= (unsigned)A.n_slots * (unsigned)A.H) return;
   const int slot = int(unit / (unsigned)A.H);
@@ -746,13 +746,13 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
 // 64, 8.4 MB in and out, 7.4 us (9.3 with four loads in flight).
 __global__ __launch_bounds__(kThreads) void decay_scan_kernel(DecayArgs A) {
   const int SE = A.role[0].dk * A.role[0].dv, nb = (SE / 4 + kThreads - 1) / kThreads;
-  unsigned x = blockIdx.x;
+  unsigned x = blockIdx.x;                         // sequences: blockIdx.y, at most 65535
   const int e4 = 4 * (int(x % (unsigned)nb) * kThreads + threadIdx.x);
   x /= (unsigned)nb;
   const int h = int(x % (unsigned)A.H);
   x /= (unsigned)A.H;
-  const DecayRole& R = A.role[x % (unsigned)A.n_roles];
-  const int seq = int(x / (unsigned)A.n_roles), SL = kC * A.L;
+  const DecayRole& R = A.role[x];
+  const int seq = blockIdx.y, SL = kC * A.L;
   int slot = seq * A.n_seg, len = A.T;
   if (A.packed) {
     const int first = cu_at(A, seq);
@@ -884,7 +884,7 @@ hipError_t launch_chunks_t(const DecayArgs& a, bool state_pass, hipStream_t st) 
   auto run = [&](auto kernel, int bytes) {
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes);
     if (e != hipSuccess) return e;
-    launch_kernel(kernel, dim3((unsigned)blocks), 64 * W, bytes, st, a);
+    launch_kernel(kernel, grid_rows(blocks), 64 * W, bytes, st, a);
     return hipGetLastError();
   };
   using TL = Tiles<T, DK, W>;
@@ -925,8 +925,7 @@ hipError_t launch_decay_chunks(DecayArgs& a, bool bf16, bool exact_state, bool s
 
 hipError_t launch_decay_scan(const DecayArgs& a, hipStream_t st) {
   const int SE = a.role[0].dk * a.role[0].dv, nb = (SE / 4 + kThreads - 1) / kThreads;
-  const long long blocks = (long long)nb * a.H * a.n_roles * a.n_seq;
-  launch_kernel(decay_scan_kernel, dim3((unsigned)blocks), kThreads, 0, st, a);
+  launch_kernel(decay_scan_kernel, dim3(nb * a.H * a.n_roles, a.n_seq), kThreads, 0, st, a);
   return hipGetLastError();
 }
 

@@ -34,6 +34,19 @@ inline void launch_kernel(F kernel, dim3 grid, dim3 block, size_t shmem, hipStre
   }
 }
 
+// ---- many workgroups -------------------------------------------------------------------
+// A grid axis holds fewer than 2^32 work-items (hardware and runtime; more are cut off modulo 2^32
+// without an error), that is 2^22 workgroups of up to 1023 threads.  `blocks` workgroups (below 2^31)
+// as rows of so many; block_number() counts through them in the order in which they are dispatched,
+// and those behind `blocks` have nothing to do.  2^22 is a multiple of 8, so that numbers congruent
+// mod 8 stay on one XCD.
+constexpr unsigned kGridRow = 1u << 22;
+inline dim3 grid_rows(long long blocks) {
+  return blocks <= (long long)kGridRow ? dim3((unsigned)blocks)
+                                       : dim3(kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+__device__ __forceinline__ unsigned block_number() { return blockIdx.x + blockIdx.y * kGridRow; }
+
 // Raises a kernel's dynamic-LDS limit to `bytes` on the current device, once per (kernel,
 // device) in the process -- the attribute stays set -- so that launches after the first pay a
 // table lookup, not a runtime call.  Returns the runtime's error if setting it fails.

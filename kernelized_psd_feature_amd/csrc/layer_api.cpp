@@ -82,12 +82,9 @@ kata::DecayArgs decay_args(const kata_decay_problem* pr, const kata::DecayPlan& 
   return a;
 }
 
-// Grids are one-dimensional with fewer than 2^31 workgroups.
-kata_status check_grid(const kata_decay_problem* pr, const kata::DecayPlan& p, int n_roles) {
-  const int64_t most = (int64_t(1) << 31) - 1;
-  const int64_t chunks = (int64_t(p.n_slots) * pr->H + 7) / 8 * 8 * 2 * n_roles;
-  const int64_t scan = int64_t(16) * pr->H * n_roles * pr->n_seq;
-  if (chunks > most || (p.scan && scan > most))
+// The kernels number their workgroups in 32 bits (grid_rows in device.h takes fewer than 2^31).
+kata_status check_grid(const kata::DecayPlan& p) {
+  if (p.groups >= int64_t(1) << 31)
     return set_error(KATA_ERR_UNSUPPORTED, "too many sequences and heads for one launch");
   return KATA_OK;
 }
@@ -146,7 +143,7 @@ kata_status kata_fwd_decay(const kata_decay_problem* pr, const void* q, const vo
   if ((s = need_aligned(final_state, 16, "final_state")) != KATA_OK) return s;
   const kata::DecayPlan p = kata::plan_decay(pr, 1);
   if ((s = check_workspace(workspace, ws_bytes, p.role_bytes)) != KATA_OK) return s;
-  if ((s = check_grid(pr, p, 1)) != KATA_OK) return s;
+  if ((s = check_grid(p)) != KATA_OK) return s;
   if ((s = check_device()) != KATA_OK) return s;
   kata::DecayArgs a = decay_args(pr, p, log_decay, cu_seqlens, 1);
   kata::DecayRole& r = a.role[0];
@@ -184,7 +181,7 @@ kata_status kata_bwd_decay(const kata_decay_problem* pr, const void* q, const vo
   if ((s = need_aligned(dinitial_state, 16, "dinitial_state")) != KATA_OK) return s;
   const kata::DecayPlan p = kata::plan_decay(pr, 3);
   if ((s = check_workspace(workspace, ws_bytes, 3 * p.role_bytes)) != KATA_OK) return s;
-  if ((s = check_grid(pr, p, 3)) != KATA_OK) return s;
+  if ((s = check_grid(p)) != KATA_OK) return s;
   if ((s = check_device()) != KATA_OK) return s;
   kata::DecayArgs a = decay_args(pr, p, log_decay, cu_seqlens, 3);
   char* ws = static_cast<char*>(workspace);

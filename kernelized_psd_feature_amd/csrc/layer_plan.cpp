@@ -99,6 +99,8 @@ DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles) {
   const int64_t SL = L * kDecayChunk;
   p.n_seg = int((chunks + L - 1) / L);
   p.n_slots = pr->packed ? decay_slot_count(pr->T, pr->n_seq, int(SL)) : pr->n_seq * p.n_seg;
+  // as the kernel deals them out: slots and heads in eights, `blocks / H` column blocks each
+  p.groups = (int64_t(p.n_slots) * pr->H + 7) / 8 * 8 * (blocks / pr->H);
   p.scan = p.n_seg > 1;
   // With few segments each walk adds up the sums before its own, for one launch less.  8 x 4096, 16 bf16
   // heads (4 segments): 76 us, 81 with the scan; 2 x 16384 backward (6): 207, 214; 2048 (11): 20.3,

@@ -21,6 +21,7 @@ struct DecayPlan {
   int scan = 0;                           // 1: a state pass and a scan run before the walk
   int stream = 0;                         // 1: q, k and v are loaded past the caches
   int join = 0;                           // 1: the walk does the scan's work itself
+  int64_t groups = 1;                     // workgroups of a chunk launch
   size_t role_bytes = 0;                  // workspace of one role's segment states
 };
 

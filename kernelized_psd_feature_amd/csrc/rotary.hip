@@ -57,7 +57,8 @@ template <typename T, bool IL, bool kEdge>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs A) {
   extern __shared__ float2 cs[];                    // [tokens of the block][rot / 2]
   const int half = A.rot / 2, tid = threadIdx.x;
-  const unsigned first = blockIdx.x * (unsigned)A.TT, total = (unsigned)A.B * (unsigned)A.T;   // < 2^31
+  const unsigned first = block_number() * (unsigned)A.TT, total = (unsigned)A.B * (unsigned)A.T;   // < 2^31
+  if (first >= total) return;                       // behind the last of several grid rows
   const int tokens = (int)min((unsigned)A.TT, total - first);
   for (int i = tid; i < tokens * half; i += kThreads) {
     const unsigned token = first + i / half, b = token / (unsigned)A.T, t = token - b * (unsigned)A.T;
@@ -168,9 +169,9 @@ hipError_t launch_t(RotaryArgs& a, bool interleaved, hipStream_t st) {
   const long long blocks = (tokens + a.TT - 1) / a.TT;
   const size_t lds = sizeof(float2) * a.TT * half;
   if (interleaved)
-    launch_kernel(rotary_kernel<T, true, kEdge>, dim3((unsigned)blocks), kThreads, lds, st, a);
+    launch_kernel(rotary_kernel<T, true, kEdge>, grid_rows(blocks), kThreads, lds, st, a);
   else
-    launch_kernel(rotary_kernel<T, false, kEdge>, dim3((unsigned)blocks), kThreads, lds, st, a);
+    launch_kernel(rotary_kernel<T, false, kEdge>, grid_rows(blocks), kThreads, lds, st, a);
   return hipGetLastError();
 }
 

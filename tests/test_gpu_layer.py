@@ -424,6 +424,18 @@ def test_decay_of_operands_larger_than_the_caches(dtype, B, H):
         assert torch.equal(o[part], K.fwd_decay(q[part], k[part], v[part], ld))
 
 
+def test_decay_of_more_workgroups_than_a_grid_axis_has():
+    # 65535 one-token sequences of 260 heads: 17 million workgroups of 256 threads, over 2^32 work-items,
+    # which one grid axis cuts off.  The sequences share their inputs, so every output row is the first one's.
+    n, H, d = 65535, 260, 8
+    q, k, v = (_randn(i, 1, 1, H, d, dtype=BF).expand(n, 1, H, d) for i in range(3))
+    ld = _decays(H)
+    o = K.fwd_decay(q, k, v, ld, scale=0.5)
+    one = K.fwd_decay(q[:1], k[:1], v[:1], ld, scale=0.5)
+    assert torch.equal(o, one.expand(n, 1, H, d))
+    _check_decay(q[:1], k[:1], v[:1], ld, 0.5, o=one)
+
+
 def test_decay_refusals():
     q, k, v = (_randn(i, 1, 8, 2, 64, dtype=BF) for i in range(3))
     ld = _decays(2)
@@ -534,6 +546,19 @@ def test_rotary_negative_and_far_positions():
     ref = L.rotary(_np(x), _np(pos), _np(rates))
     # an angle of 2^31 is known to 2^31 2^-52 in fp64, on both sides
     _inside(K.rotary(x, None, rates, positions=pos), ref, 2.0 ** -19 * np.abs(_np(x)).sum(-1, keepdims=True), "far")
+
+
+def test_rotary_of_more_workgroups_than_a_grid_axis_has():
+    # a workgroup a token, 16.8 million of them; every token is the same one at another position
+    T, H = (1 << 24) + 20000, 257
+    q = _randn(1, 1, 1, H, 2, dtype=BF).expand(1, T, H, 2)
+    rates, m = K.rotary_rates(2, base=100.0)
+    out = torch.full((1, T, H, 2), float("nan"), dtype=BF, device=DEV)
+    K.rotary(q, None, rates * 1e-3, out=out)
+    for at in range(0, T, 1 << 21):
+        assert not torch.isnan(out[:, at:at + (1 << 21)]).any(), at
+    for at in (0, 19000, 1 << 22, (1 << 23) - 7, (1 << 24) - 500, T - 1000):
+        assert torch.equal(out[:, at:at + 1000], K.rotary(q[:, :1000], None, rates * 1e-3, offset=at)[:, :T - at]), at
 
 
 def test_rotary_refusals():

@@ -107,6 +107,15 @@ def test_decode_and_backward_refusals():
     assert call(f[:12], need - 1) == WORKSPACE
 
 
+@pytest.mark.parametrize("n_seq,H,dtype,d", [
+    (65535, 65535, 1, 8), (65535, 40000, 1, 8), (65535, 20000, 0, 128),   # two blocks of columns
+])
+def test_decay_refuses_more_workgroups_than_it_can_number(n_seq, H, dtype, d):
+    pr = _decay(n_seq=n_seq, H=H, T=1, dk=d, dv=d, dtype=dtype)
+    assert _fwd(pr) == UNSUPPORTED
+    assert b"one launch" in K._lib().kata_last_error()
+
+
 def _rot(B=2, T=3, H=4, Hk=2, D=16, rot=16, dtype=1):
     pr = KL._RotaryProblem()
     pr.B, pr.T, pr.H, pr.Hk, pr.D, pr.rot, pr.dtype, pr.magnitude = B, T, H, Hk, D, rot, dtype, 1.0
