@@ -282,8 +282,10 @@ kata_status kata_bwd_chunked(const kata_problem* pr, const void* q, const void* 
  *          [1][T][H][width]; sequence i is the rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (device
  *          int32 [n_seq + 1], ascending, within [0, T]; values outside are clamped, so that no
  *          content is read or written out of bounds).  A sequence may be empty: its final state
- *          is its initial state.
- *   H, dk, dv: heads, width of q and k, width of v: at most 128, rows of whole 16 bytes.
+ *          is its initial state.  T is at most 2^26; n_seq at most 65535 in the chunked forms, any
+ *          number in the recurrent one.
+ *   H, dk, dv: heads, at most 65535; width of q and k, width of v: at most 128, rows of whole 16
+ *          bytes.
  *   zero_tail: packed: 0 leaves the output rows that belong to no sequence (before cu_seqlens[0] or
  *          from cu_seqlens[n_seq] on) as they are, 1 zeroes them.
  *   dtype: of q, k, v, o, dO and the gradients.  States are fp32 [n_seq][H][dk][dv], contiguous.

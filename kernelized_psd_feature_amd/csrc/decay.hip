@@ -939,13 +939,18 @@ hipError_t launch_decay_decode(bool bf16, int B, int T, int H, int dk, int dv,
   for (int i = 0; i < 3; ++i) {
     a.sq[i] = sq[i]; a.sk[i] = sk[i]; a.sv[i] = sv[i]; a.so[i] = so[i];
   }
-  constexpr int LC = 16;
-  const dim3 grid((dv + 4 * LC - 1) / (4 * LC), H, B);
+  constexpr int LC = 16, kMost = 65535;             // sequences that a grid axis holds
   auto run = [&](auto t, auto ri) {
     using T_ = decltype(t);
-    launch_kernel(decay_decode_kernel<T_, LC, decltype(ri)::value>, grid, kThreads, 0, st, a,
-                  (const T_*)q, (const T_*)k, (const T_*)v, log_decay, state, (T_*)o);
-    return hipGetLastError();
+    hipError_t e = hipSuccess;
+    for (long long b = 0; b < B && e == hipSuccess; b += kMost) {
+      const dim3 grid((dv + 4 * LC - 1) / (4 * LC), H, (unsigned)(B - b < kMost ? B - b : kMost));
+      launch_kernel(decay_decode_kernel<T_, LC, decltype(ri)::value>, grid, kThreads, 0, st, a,
+                    (const T_*)q + b * sq[0], (const T_*)k + b * sk[0], (const T_*)v + b * sv[0], log_decay,
+                    state + b * H * dk * dv, (T_*)o + b * so[0]);
+      e = hipGetLastError();
+    }
+    return e;
   };
   auto rows = [&](auto t) {
     if (dk <= 32) return run(t, std::integral_constant<int, 2>());

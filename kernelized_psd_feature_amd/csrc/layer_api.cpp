@@ -38,11 +38,13 @@ struct Named {
   const char* name;
 };
 
-// Problem, tensors, decays and offsets of the chunked forms.
-kata_status check_decay(const kata_decay_problem* pr, bool backward, const Named* ts, int n,
+// Problem, tensors, decays and offsets.
+enum class Form { forward, backward, tokens };
+kata_status check_decay(const kata_decay_problem* pr, Form form, const Named* ts, int n,
                         const float* log_decay, const int32_t* cu) {
   std::string why;
-  kata_status s = kata::validate_decay(pr, backward, &why);
+  kata_status s = form == Form::tokens ? kata::validate_decay_decode(pr, &why)
+                                       : kata::validate_decay(pr, form == Form::backward, &why);
   if (s != KATA_OK) return set_error(s, why);
   const size_t es = kata::elem_size(pr->dtype);
   const int64_t sizes[3] = {pr->packed ? 1 : pr->n_seq, pr->T, pr->H};
@@ -137,7 +139,7 @@ kata_status kata_fwd_decay(const kata_decay_problem* pr, const void* q, const vo
   clear_error();
   if (!pr) return set_error(KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
   const Named ts[] = {{q, pr->sq, "q"}, {k, pr->sk, "k"}, {v, pr->sv, "v"}, {o, pr->so, "o"}};
-  kata_status s = check_decay(pr, false, ts, 4, log_decay, cu_seqlens);
+  kata_status s = check_decay(pr, Form::forward, ts, 4, log_decay, cu_seqlens);
   if (s != KATA_OK) return s;
   if ((s = need_aligned(initial_state, 16, "initial_state")) != KATA_OK) return s;
   if ((s = need_aligned(final_state, 16, "final_state")) != KATA_OK) return s;
@@ -174,7 +176,7 @@ kata_status kata_bwd_decay(const kata_decay_problem* pr, const void* q, const vo
   const int64_t gk[3] = {T * H * pr->dk, H * pr->dk, pr->dk}, gv[3] = {T * H * pr->dv, H * pr->dv, pr->dv};
   const Named ts[] = {{q, pr->sq, "q"},  {k, pr->sk, "k"}, {v, pr->sv, "v"}, {dO, pr->sdo, "dO"},
                       {dq, gk, "dq"},    {dk, gk, "dk"},   {dv, gv, "dv"}};
-  kata_status s = check_decay(pr, true, ts, 7, log_decay, cu_seqlens);
+  kata_status s = check_decay(pr, Form::backward, ts, 7, log_decay, cu_seqlens);
   if (s != KATA_OK) return s;
   if ((s = need_aligned(initial_state, 16, "initial_state")) != KATA_OK) return s;
   if ((s = need_aligned(dfinal_state, 16, "dfinal_state")) != KATA_OK) return s;
@@ -223,8 +225,7 @@ kata_status kata_decode_decay(const kata_decay_problem* pr, const void* q, const
   clear_error();
   if (!pr) return set_error(KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
   const Named ts[] = {{q, pr->sq, "q"}, {k, pr->sk, "k"}, {v, pr->sv, "v"}, {o, pr->so, "o"}};
-  if (pr->packed) return set_error(KATA_ERR_INVALID_ARGUMENT, "decode takes no packed sequences");
-  kata_status s = check_decay(pr, false, ts, 4, log_decay, nullptr);
+  kata_status s = check_decay(pr, Form::tokens, ts, 4, log_decay, nullptr);
   if (s != KATA_OK) return s;
   if (!state) return set_error(KATA_ERR_INVALID_ARGUMENT, "state is null");
   if ((s = need_aligned(state, 16, "state")) != KATA_OK) return s;

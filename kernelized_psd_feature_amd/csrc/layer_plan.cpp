@@ -36,21 +36,13 @@ kata_status check_strides(const char* name, const int64_t st[3], const int64_t s
   return KATA_OK;
 }
 
-}  // namespace
-
-kata_status validate_rows(const void* p, const int64_t st[3], const int64_t sizes[3], size_t esize,
-                          const char* name, std::string* why) {
-  int64_t used[3];
-  for (int a = 0; a < 3; ++a) used[a] = sizes[a] > 1 ? st[a] : 0;
-  return validate_tensor(p, used, esize, name, why);
-}
-
-kata_status validate_decay(const kata_decay_problem* pr, bool backward, std::string* why) {
+// most: sequences that the form takes.
+kata_status check_decay_problem(const kata_decay_problem* pr, int most, bool backward, std::string* why) {
   if (!pr) return fail(why, KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
   if (pr->n_seq < 1 || pr->H < 1 || pr->T < 1)
     return fail(why, KATA_ERR_INVALID_ARGUMENT, "n_seq, H and T must be >= 1");
   if (pr->T > kMaxT) return fail(why, KATA_ERR_UNSUPPORTED, "T exceeds 2^26");
-  if (pr->n_seq > 65535 || pr->H > 65535)
+  if (pr->n_seq > most || pr->H > kDecayMaxHeads)
     return fail(why, KATA_ERR_UNSUPPORTED, "n_seq or H exceeds 65535");
   if (pr->dtype != KATA_F32 && pr->dtype != KATA_BF16)
     return fail(why, KATA_ERR_INVALID_ARGUMENT, "dtype must be fp32 or bf16");
@@ -71,6 +63,25 @@ kata_status validate_decay(const kata_decay_problem* pr, bool backward, std::str
   if (backward) return check_strides("dO", pr->sdo, sizes, pr->dv, false, why);
   if ((s = check_strides("o", pr->so, sizes, pr->dv, true, why)) != KATA_OK) return s;
   return KATA_OK;
+}
+
+}  // namespace
+
+kata_status validate_rows(const void* p, const int64_t st[3], const int64_t sizes[3], size_t esize,
+                          const char* name, std::string* why) {
+  int64_t used[3];
+  for (int a = 0; a < 3; ++a) used[a] = sizes[a] > 1 ? st[a] : 0;
+  return validate_tensor(p, used, esize, name, why);
+}
+
+kata_status validate_decay(const kata_decay_problem* pr, bool backward, std::string* why) {
+  return check_decay_problem(pr, kDecayMaxSeqs, backward, why);
+}
+
+kata_status validate_decay_decode(const kata_decay_problem* pr, std::string* why) {
+  const kata_status s = check_decay_problem(pr, INT32_MAX, false, why);
+  if (s == KATA_OK && pr->packed) return fail(why, KATA_ERR_INVALID_ARGUMENT, "decode takes no packed sequences");
+  return s;
 }
 
 DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles) {

@@ -12,6 +12,8 @@ namespace kata {
 
 constexpr int kDecayChunk = 64;           // tokens of a chunk
 constexpr int kDecayMaxWidth = 128;       // dk and dv
+constexpr int kDecayMaxHeads = 65535;
+constexpr int kDecayMaxSeqs = 65535;      // of the chunked forms
 
 // Segments of the chunked form (see decay.hip).
 struct DecayPlan {
@@ -26,6 +28,7 @@ struct DecayPlan {
 };
 
 kata_status validate_decay(const kata_decay_problem* pr, bool backward, std::string* why);
+kata_status validate_decay_decode(const kata_decay_problem* pr, std::string* why);
 // A tensor's pointer and (b, t, h) strides: 16-byte aligned rows.  The stride of an axis of one
 // entry means nothing.
 kata_status validate_rows(const void* p, const int64_t st[3], const int64_t sizes[3], size_t esize,

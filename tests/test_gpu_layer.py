@@ -280,6 +280,27 @@ def test_decay_decode(dtype, shape, T):
             _inside(st[b, h], rS, few * bS, f"state {b} {h}")
 
 
+@pytest.mark.parametrize("B,H,dk,dv", [(65536, 1, 16, 16), (70001, 2, 16, 24)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decay_decode_of_more_sequences_than_a_grid_axis_has(dtype, B, H, dk, dv):
+    q, k, v = (_randn(i, B, 1, H, d, dtype=dtype) for i, d in ((1, dk), (2, dk), (3, dv)))
+    st, ld = _randn(4, B, H, dk, dv), _decays(H)
+    parts = [(slice(0, 40000), st[:40000].clone()), (slice(40000, B), st[40000:].clone())]
+    S0 = st.clone()
+    o = K.decode_decay(q, k, v, ld, st, scale=0.5)
+    for rows, s in parts:
+        assert torch.equal(o[rows], K.decode_decay(q[rows], k[rows], v[rows], ld, s, scale=0.5))
+        assert torch.equal(st[rows], s)
+    for b in (0, 65534, 65535, B - 1):
+        for h in range(H):
+            a = [_np(x[b, :, h]) for x in (q, k, v)]
+            ro, rS = L.decay_recurrent(*a, _np(ld)[h], 0.5, _np(S0[b, h]))
+            bo, bS = L.decay_closed(*[np.abs(x) for x in a], _np(ld)[h], 0.5, np.abs(_np(S0[b, h])))
+            few = (2 + dk + 16) * 2.0 ** -23         # as in test_decay_decode
+            _inside(o[b, :, h], ro, few * bo + U[dtype] * 1.01 * np.abs(ro), f"o {b} {h}")
+            _inside(st[b, h], rS, few * bS, f"state {b} {h}")
+
+
 def test_decay_decode_with_decays_zero_and_one():
     q, k, v = (_randn(i, 2, 3, 2, 64) for i in range(3))
     st = _randn(4, 2, 2, 64, 64)

@@ -116,6 +116,15 @@ def test_decay_refuses_more_workgroups_than_it_can_number(n_seq, H, dtype, d):
     assert b"one launch" in K._lib().kata_last_error()
 
 
+def test_decode_takes_any_number_of_sequences():
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real: nothing may be launched on them")
+    f, pr = _fake(6), _decay(n_seq=1 << 20, H=1, T=1, dk=16, dv=16)
+    assert K._lib().kata_decode_decay(ctypes.byref(pr), *f, None) == DEVICE
+    pr.H = 65536
+    assert K._lib().kata_decode_decay(ctypes.byref(pr), *f, None) == UNSUPPORTED
+
+
 def _rot(B=2, T=3, H=4, Hk=2, D=16, rot=16, dtype=1):
     pr = KL._RotaryProblem()
     pr.B, pr.T, pr.H, pr.Hk, pr.D, pr.rot, pr.dtype, pr.magnitude = B, T, H, Hk, D, rot, dtype, 1.0
