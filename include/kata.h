@@ -273,8 +273,9 @@ kata_status kata_bwd_chunked(const kata_problem* pr, const void* q, const void* 
  *     S_t = g S_{t-1} + k_t v_t^T  (dk x dv),     o_t = scale q_t S_t,
  * S_{-1} being the initial state (zero where none is given).  Chunks of 64 tokens run on MFMA
  * (fp32 problems on the fp32 MFMA); every sum and the state are fp32.  bf16 problems round the
- * weights of the pairs and the state to bf16 where they are operands of a product; the terms of
- * a final state (or of the gradient of the initial state) that is asked for are not rounded.
+ * state to bf16 where it is an operand of a product, and so the weights of the pairs, to two bf16
+ * terms in the first 512 rows (in dk and dv: the last ones) and where g^2 < 3/4, else to one; the
+ * terms of a final state (or of the gradient of the initial state) that is asked for are not rounded.
  * A row reaches only what the recurrence lets it reach, infinities and NaN included.
  *
  *   n_seq, T: packed == 0: n_seq sequences of T tokens, tensors [n_seq][T][H][width].

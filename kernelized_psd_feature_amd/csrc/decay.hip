@@ -294,12 +294,18 @@ struct Tiles {
   static constexpr int kBuffers = kBf && (DK <= 64 || W == 8) ? 2 : 1;
   static constexpr int stage(bool state_pass) { return kC * (LK + LV + (state_pass ? 0 : LQ)); }
   static constexpr int kHead = 288;                 // an int, then the powers g^0 .. g^64
-  // Terms of a score weight.  The rounding of one weight moves a whole row of outputs alike.  Over
-  // many rows that adds a factor of sqrt(2) to the outputs' own rounding, but a short sequence has
-  // few weights and their errors do not average out (two tokens: 1.5 times and more; one: up to
-  // 2.5), so up to kFine tokens what the rounding left is a second operand.  For all sequences that
-  // would cost 3 to 7% of the walk (8 x 4096 backward: 195 us for 189; width 128: 763 for 712).
-  static constexpr int kTerms = kBf ? 2 : 1, kFine = 512;
+  // Terms of a score weight.  The rounding of one weight moves a whole row of outputs alike, and a row
+  // with few weights does not average that out.  A row's rms error over its own rounding, by the weights
+  // that it has in effect, n = sum g^2(t-s) <= 1 / (1 - g^2) (64 columns, computed in 64 bits with the
+  // operands rounded): 1.4 in the mean whatever n is, but in one row of 100
+  //     n = 1: 2.6   1.6: 2.5   2.5: 2.2   4 to 17: 2.0 to 2.2   above 100: 1.9
+  // A second term, of what the rounding left, makes it 1.0 in the first chunk; behind it the entry
+  // state's rounding joins: 1.0 below n = 4, 1.2 at 34, 1.35 above 100, where it hardly helps any more.
+  // So two terms for the first rows of a sequence, which costs nothing measurable, and for all rows of
+  // a head of n < 4, g^2 < 3/4; one such head of 16 costs the walk 3% (8 x 4096 forward and backward:
+  // 265 us, 272; 4 x 4096 of width 128: 272, 282), since all wait for its workgroups.
+  static constexpr int kTerms = kBf ? 2 : 1, kFineRows = 512;
+  static constexpr float kFineDecay = -0.1438f;         // log(3/4) / 2
   static constexpr int bytes(bool state_pass) {
     return kHead + (kBuffers * stage(state_pass) + (state_pass ? 0 : kTerms * kC * LP)) * (int)sizeof(T);
   }
@@ -410,7 +416,7 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   const bool last_seg = s.seg == n_seg - 1;
   if (kStatePass && last_seg && !R.fin) return;     // enters no entry state
   const int first = s.seg * L, behind = min(first + L, n_chunks);
-  const bool fine = __builtin_amdgcn_readfirstlane(s.len) <= TL::kFine;
+  const int fine_before = A.log_decay[h] < TL::kFineDecay ? n_chunks : TL::kFineRows / kC;   // chunks
 
   // rows in the role's time order: row i of the sequence is start + i, or its mirror image
   const int dir = R.rev ? -1 : 1, dk = R.dk, dv = R.dv;
@@ -557,6 +563,7 @@ __global__ __launch_bounds__(64 * W, (Tiles<T, DK, W>::occupancy(kStatePass))) v
   // way); kLast: the segment's last one, n_last rows
   auto chunk = [&](int c, auto last) {
     constexpr bool kLast = decltype(last)::value;
+    const bool fine = c < fine_before;              // uniform
     // rows of the chunk after the next one to be staged
     const int n_next = c + (kTwo ? 3 : 2) < behind ? kC : n_last;
     __syncthreads();                                // the last chunk's tiles have been read

@@ -206,6 +206,10 @@ def fwd_decay(q, k, v, log_decay, scale=1.0, initial_state=None, return_state=Fa
     in a new output and left as they are in `out`.
     initial_state, and the final state with return_state: fp32 (n, H, dk, dv); a state that is returned
     has its terms added exactly, so bf16 outputs may differ from a call without it by a rounding.
+    Sums and states are fp32.  bf16 operands of a product are rounded: the state that a chunk of 64
+    tokens starts from, and the weight of a pair of tokens behind the first 512 rows of a sequence where
+    exp(2 log_decay) >= 3/4; with the output's own rounding that is a relative error of 1.7e-3 to
+    2.3e-3.  fp32 inputs have none of these roundings.
     workspace: uint8, decay_workspace_size() bytes (allocated here otherwise)."""
     o = _out_like(v, out)
     pr = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, o=o, zero_tail=1 if out is None else 0)
@@ -232,7 +236,8 @@ def bwd_decay(q, k, v, dO, log_decay, scale=1.0, initial_state=None, dfinal_stat
               cu_seqlens=None, workspace=None):
     """Gradients (dq, dk, dv, dinitial_state) of sum(dO * o) + sum(dfinal_state * final_state), the
     first three in the inputs' dtype, the last one fp32 (None without an initial_state).  Rows of no
-    packed sequence get zeros."""
+    packed sequence get zeros.  bf16 operands are rounded as in fwd_decay; for dk and dv the first rows
+    are a sequence's last ones."""
     if dO.shape != v.shape or dO.dtype != q.dtype:
         raise ValueError("dO must match v's shape and q's dtype")
     pr = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, dO=dO, zero_tail=1)
