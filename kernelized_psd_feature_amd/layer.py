@@ -19,6 +19,7 @@ import struct
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version as _written   # tensors that a kernel has written
 
 import kernelized_psd_feature_amd as _k
 
@@ -223,6 +224,8 @@ def fwd_decay(q, k, v, log_decay, scale=1.0, initial_state=None, return_state=Fa
         ws = _workspace(_workspace_size("kata_fwd_decay_workspace_size", pr), workspace, device)
         _run("kata_fwd_decay", device, pr, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
              _ptr(cu_seqlens), _ptr(initial_state), o.data_ptr(), _ptr(final), _ptr(ws), _bytes(ws))
+    if out is not None:
+        _written(out)
     return (o, final) if return_state else o
 
 
@@ -268,6 +271,7 @@ def decode_decay(q, k, v, log_decay, state, scale=1.0, out=None):
     if v.numel():
         _run("kata_decode_decay", q.device, pr, q.data_ptr(), k.data_ptr(), v.data_ptr(),
              log_decay.data_ptr(), state.data_ptr(), o.data_ptr())
+    _written(state if out is None else (state, out))
     return o
 
 
@@ -365,6 +369,8 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
         pr = _ROTARY.pack(B, T, H, Hk, D, 2 * n, _dtype(dtype), 1 if interleaved else 0, 1 if inverse else 0,
                           pos64, magnitude, pos_b, pos_t, offset, *sq[:3], *sk[:3], *soq[:3], *sok[:3])
         _run("kata_rotary", device, pr, pq, pk, rates.data_ptr(), at, poq, pok)
+    if out is not None:
+        _written(outs)
     return oq if k is None else (oq, ok)
 
 
@@ -428,6 +434,8 @@ def fwd_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, return_stats=F
         pr = _NORM.pack(x2.shape[0], N, _dtype(dtype), wt, eps, x2.stride(0), N, y2_stride, N)
         _run("kata_fwd_layer_norm", device, pr, x2.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(),
              _ptr(mean), _ptr(rstd))
+    if out is not None:
+        _written(out)
     return (y, mean, rstd) if return_stats else y
 
 

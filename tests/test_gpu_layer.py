@@ -924,6 +924,37 @@ def test_kata_attention_with_rotary():
     assert torch.equal(K.parallel_kata_attn(q, k, v, rotary=table), K.parallel_kata_attn(a, b, v))
 
 
+def test_tensors_written_in_place_tell_autograd():
+    q, k, v = (_randn(i, 2, 3, 2, 64) for i in range(3))
+    ld, (rates, _) = _decays(2), K.rotary_rates(64)
+    st = _randn(4, 2, 2, 64, 64)
+    o, a, b, y = (torch.empty_like(q) for _ in range(4))
+    for call, written in ((lambda: K.decode_decay(q, k, v, ld, st), [st]),
+                          (lambda: K.decode_decay(q, k, v, ld, st, out=o), [st, o]),
+                          (lambda: K.fwd_decay(q, k, v, ld, out=o), [o]),
+                          (lambda: K.rotary(q, k, rates, out=(a, b)), [a, b]),
+                          (lambda: K.rotary(q, None, rates, out=a), [a]),
+                          (lambda: K.fwd_layer_norm(q, out=y), [y])):
+        reads = q._version, k._version, v._version, ld._version
+        before = [x._version for x in written]
+        call()
+        assert all(x._version > n for x, n in zip(written, before))
+        assert reads == (q._version, k._version, v._version, ld._version)
+    # a state that a backward pass still needs, advanced by a token
+    leaf = q.clone().requires_grad_()
+    loss = K.parallel_decay_attn(leaf, k, v, ld, initial_state=st).sum()
+    K.decode_decay(q, k, v, ld, st)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    with torch.inference_mode():                     # whose tensors have no counters
+        s = st.clone()
+        K.decode_decay(q, k, v, ld, s, out=torch.empty_like(v))
+        K.rotary(q, k, rates, out=(torch.empty_like(q), torch.empty_like(k)))
+        K.fwd_layer_norm(q, out=torch.empty_like(q))
+    K.decode_decay(q, k, v, ld, st)
+    assert torch.equal(s, st)
+
+
 def test_side_stream():
     s = torch.cuda.Stream()
     q, k, v = (_randn(i, 1, 1000, 2, 64, dtype=BF) for i in range(3))
