@@ -411,7 +411,9 @@ typedef enum {
   KATA_K_BWD = 4,
   KATA_K_DECODE = 5,
   KATA_K_STATE_SUM = 6,
-  KATA_K_COUNT = 7
+  KATA_K_ROTARY = 7,
+  KATA_K_NORM = 8,        /* layer norm, forward or backward */
+  KATA_K_COUNT = 9
 } kata_kernel_kind;
 
 typedef struct {

@@ -48,7 +48,7 @@ _LIB = None
 KATA_F32, KATA_BF16 = 0, 1
 NOALLOC_SCRATCH_BYTES = 64 << 20     # KATA_NOALLOC_SCRATCH_BYTES of include/kata.h
 KERNEL_KINDS = ("quadratic", "chunk_state", "scan", "chunk_output", "bwd", "decode",
-                "state_sum")
+                "state_sum", "rotary", "norm")
 
 
 class KataError(RuntimeError):
@@ -77,7 +77,8 @@ class _ChunkedPlan(ctypes.Structure):
 
 
 class _Times(ctypes.Structure):
-    _fields_ = [("launches", ctypes.c_int64 * 7), ("total_ms", ctypes.c_double * 7)]
+    _fields_ = [("launches", ctypes.c_int64 * len(KERNEL_KINDS)),
+                ("total_ms", ctypes.c_double * len(KERNEL_KINDS))]
 
 
 def library_path():

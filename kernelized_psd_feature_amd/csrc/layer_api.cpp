@@ -274,8 +274,9 @@ kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void
   a.B = pr->B; a.T = pr->T; a.H = pr->H; a.Hk = pr->Hk; a.D = pr->D; a.rot = pr->rot;
   a.pos64 = pr->pos64; a.inverse = pr->inverse;
   a.magnitude = pr->magnitude;
-  return launch_status(kata::launch_rotary(a, pr->dtype == KATA_BF16, aligned, pr->interleaved != 0,
-                                           reinterpret_cast<hipStream_t>(stream)),
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  Timed t(KATA_K_ROTARY, st);
+  return launch_status(kata::launch_rotary(a, pr->dtype == KATA_BF16, aligned, pr->interleaved != 0, st),
                        "rotary positions");
 }
 
@@ -305,8 +306,9 @@ kata_status kata_fwd_layer_norm(const kata_norm_problem* pr, const void* x, cons
   a.N = pr->N; a.w_bf16 = pr->w_dtype == KATA_BF16; a.eps = pr->eps;
   const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % 16) == 0 &&
                        (pr->rows == 1 || ((pr->sx | pr->sy) * (int64_t)es) % 16 == 0);
-  return launch_status(kata::launch_norm_fwd(a, pr->dtype == KATA_BF16, aligned,
-                                             reinterpret_cast<hipStream_t>(stream)), "layer norm");
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  Timed t(KATA_K_NORM, st);
+  return launch_status(kata::launch_norm_fwd(a, pr->dtype == KATA_BF16, aligned, st), "layer norm");
 }
 
 size_t kata_bwd_layer_norm_workspace_size(const kata_norm_problem* pr) {
@@ -345,8 +347,9 @@ kata_status kata_bwd_layer_norm(const kata_norm_problem* pr, const void* dy, con
   const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dy) |
                          reinterpret_cast<uintptr_t>(dx)) % 16) == 0 &&
                        (pr->rows == 1 || ((pr->sx | pr->sdy | pr->sdx) * (int64_t)es) % 16 == 0);
-  return launch_status(kata::launch_norm_bwd(a, pr->dtype == KATA_BF16, aligned,
-                                             reinterpret_cast<hipStream_t>(stream)), "layer norm backward");
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  Timed t(KATA_K_NORM, st);
+  return launch_status(kata::launch_norm_bwd(a, pr->dtype == KATA_BF16, aligned, st), "layer norm backward");
 }
 
 }  // extern "C"

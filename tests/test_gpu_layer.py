@@ -955,6 +955,26 @@ def test_tensors_written_in_place_tell_autograd():
     assert torch.equal(s, st)
 
 
+def test_timing_records_every_kernel_of_a_layer():
+    q, k, v, g = (_randn(i, 1, 900, 2, 64, dtype=BF) for i in range(4))
+    ld, (rates, _) = _decays(2), K.rotary_rates(64)
+    w = torch.ones(64, device=DEV)
+    K.fwd_decay(q, k, v, ld)
+    K.timing_begin()
+    K.rotary(q, k, rates)
+    o = K.fwd_decay(q, k, v, ld)
+    y, mean, rstd = K.fwd_layer_norm(o, w, return_stats=True)
+    K.bwd_layer_norm(g, o, w, mean, rstd)
+    K.bwd_decay(q, k, v, g, ld)
+    t = K.timing_end()
+    assert set(t) == set(K.KERNEL_KINDS)
+    assert t["rotary"][0] == 1 and t["norm"][0] == 2 and t["chunk_output"][0] == 1 and t["bwd"][0] == 1
+    assert all(ms > 0 for n, ms in t.values() if n)
+    K.rotary(q, k, rates)                            # recording has stopped
+    K.timing_begin()
+    assert not any(n for n, _ in K.timing_end().values())
+
+
 def test_side_stream():
     s = torch.cuda.Stream()
     q, k, v = (_randn(i, 1, 1000, 2, 64, dtype=BF) for i in range(3))
