@@ -476,6 +476,13 @@ def bwd_layer_norm(dy, x, weight, mean, rstd, params=True, workspace=None):
 
 # ---- autograd ----------------------------------------------------------------------------------
 
+def _dense(x):
+    """A gradient as the kernels read it: contiguous, on a 16-byte boundary (a concatenation's gradient
+    comes as a view at any element)."""
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 class _Decay(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, log_decay, scale, initial_state, cu_seqlens, return_state):
@@ -489,10 +496,10 @@ class _Decay(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dO, dfinal=None):
         q, k, v, log_decay, initial_state, cu_seqlens = ctx.saved_tensors
-        dO = torch.zeros_like(v, memory_format=torch.contiguous_format) if dO is None else dO.contiguous()
+        dO = torch.zeros_like(v, memory_format=torch.contiguous_format) if dO is None else _dense(dO)
         dq, dk, dv, dinit = bwd_decay(q, k, v, dO, log_decay, scale=ctx.scale,
                                       initial_state=initial_state, cu_seqlens=cu_seqlens,
-                                      dfinal_state=None if dfinal is None else dfinal.contiguous())
+                                      dfinal_state=None if dfinal is None else _dense(dfinal))
         return dq, dk, dv, None, None, dinit, None, None
 
 

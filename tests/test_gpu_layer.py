@@ -917,6 +917,21 @@ def test_shared_heads_and_unused_outputs_under_autograd():
     _inside(sk[0, :, 0], ref, 2.0 ** -16 * np.abs(_np(v)).sum(), "dk of the state")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradients_that_arrive_at_any_alignment(dtype):
+    # the gradient of a concatenation is a view at the place that its input had: contiguous, but not
+    # on a 16-byte boundary
+    q, k, v = (_randn(i, 1, 70, 2, 64, dtype=dtype) for i in range(3))
+    ld, S0 = _decays(2), _randn(4, 1, 2, 64, 64)
+    lead, c, cs = torch.zeros(1, dtype=dtype, device=DEV), _randn(5, 1 + v.numel(), dtype=dtype), _randn(6, 1 + S0.numel())
+    leaves = [x.clone().requires_grad_() for x in (q, k, v, S0)]
+    o, S = K.parallel_decay_attn(*leaves[:3], ld, initial_state=leaves[3], return_state=True)
+    loss = (torch.cat([lead, o.flatten()]) * c).sum() + (torch.cat([lead.float(), S.flatten()]) * cs).sum()
+    got = torch.autograd.grad(loss, leaves)
+    want = K.bwd_decay(q, k, v, c[1:].clone().view_as(v), ld, initial_state=S0, dfinal_state=cs[1:].clone().view_as(S0))
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_kata_attention_with_rotary():
     q, k, v = (_randn(i, 1, 128, 2, d, dtype=BF) for i, d in ((1, 16), (2, 16), (3, 64)))
     table = K.rotary_rates(16)
