@@ -364,7 +364,9 @@ kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void
 
 /* ---- Layer norm ----------------------------------------------------------------------------
  *     hat = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  y = hat weight + bias
- * over rows of N elements, rows sx (sdy, sy, sdx) elements apart, statistics and sums in fp32.
+ * over rows of N elements, statistics and sums in fp32.  sx, sy, sdy, sdx: elements from a row of x, y,
+ * dy, dx to the next, N at least (those of x and dy may be zero: the same row).  The forward pass looks
+ * at sx and sy; a backward problem has all four, sy being its forward pass's.
  * weight, bias: [N] of w_dtype (fp32, or bf16 with bf16 rows), nullable: ones, zeros. */
 typedef struct {
   int64_t rows;

@@ -280,16 +280,16 @@ kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void
                        "rotary positions");
 }
 
-static kata_status check_norm(const kata_norm_problem* pr) {
+static kata_status check_norm(const kata_norm_problem* pr, bool backward) {
   std::string why;
-  kata_status s = kata::validate_norm(pr, &why);
+  kata_status s = kata::validate_norm(pr, backward, &why);
   return s == KATA_OK ? s : set_error(s, why);
 }
 
 kata_status kata_fwd_layer_norm(const kata_norm_problem* pr, const void* x, const void* weight,
                                 const void* bias, void* y, float* mean, float* rstd, void* stream) {
   clear_error();
-  kata_status s = check_norm(pr);
+  kata_status s = check_norm(pr, false);
   if (s != KATA_OK) return s;
   if (!x || !y) return set_error(KATA_ERR_INVALID_ARGUMENT, "x or y is null");
   if (!mean != !rstd) return set_error(KATA_ERR_INVALID_ARGUMENT, "mean and rstd go together");
@@ -312,7 +312,7 @@ kata_status kata_fwd_layer_norm(const kata_norm_problem* pr, const void* x, cons
 }
 
 size_t kata_bwd_layer_norm_workspace_size(const kata_norm_problem* pr) {
-  return kata::validate_norm(pr, nullptr) == KATA_OK ? kata::norm_workspace_bytes(pr) : 0;
+  return kata::validate_norm(pr, true, nullptr) == KATA_OK ? kata::norm_workspace_bytes(pr) : 0;
 }
 
 kata_status kata_bwd_layer_norm(const kata_norm_problem* pr, const void* dy, const void* x,
@@ -320,7 +320,7 @@ kata_status kata_bwd_layer_norm(const kata_norm_problem* pr, const void* dy, con
                                 void* dweight, void* dbias, void* workspace, size_t ws_bytes,
                                 void* stream) {
   clear_error();
-  kata_status s = check_norm(pr);
+  kata_status s = check_norm(pr, true);
   if (s != KATA_OK) return s;
   if (!dy || !x || !mean || !rstd)
     return set_error(KATA_ERR_INVALID_ARGUMENT, "dy, x, mean or rstd is null");

@@ -154,7 +154,7 @@ kata_status validate_rotary(const kata_rotary_problem* pr, std::string* why) {
   return check_strides("out k", pr->sok, sizes_k, pr->D, true, why);
 }
 
-kata_status validate_norm(const kata_norm_problem* pr, std::string* why) {
+kata_status validate_norm(const kata_norm_problem* pr, bool backward, std::string* why) {
   if (!pr) return fail(why, KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
   if (pr->rows < 1 || pr->N < 1) return fail(why, KATA_ERR_INVALID_ARGUMENT, "rows and N must be >= 1");
   if (pr->N > 1 << 24 || pr->rows > int64_t(1) << 40)
@@ -165,12 +165,12 @@ kata_status validate_norm(const kata_norm_problem* pr, std::string* why) {
     return fail(why, KATA_ERR_INVALID_ARGUMENT, "weights must be fp32, or bf16 with bf16 rows");
   if (!std::isfinite(pr->eps) || pr->eps < 0.f)
     return fail(why, KATA_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
-  const int64_t strides[4] = {pr->sx, pr->sdy, pr->sy, pr->sdx};
-  const char* names[4] = {"x", "dy", "y", "dx"};
-  for (int i = 0; i < 4; ++i) {
+  const int64_t strides[4] = {pr->sx, pr->sy, pr->sdy, pr->sdx};
+  const char* names[4] = {"x", "y", "dy", "dx"};
+  for (int i = 0; i < (backward ? 4 : 2); ++i) {
     const int64_t s = strides[i];
     if (s < 0) return fail(why, KATA_ERR_INVALID_ARGUMENT, std::string(names[i]) + ": negative stride");
-    if (pr->rows > 1 && s < pr->N && (i >= 2 || s != 0))
+    if (pr->rows > 1 && s < pr->N && (i % 2 || s != 0))   // an input may repeat its row
       return fail(why, KATA_ERR_INVALID_ARGUMENT,
                   std::string(names[i]) + ": stride smaller than the row length");
     if (pr->rows > 1 && s > (int64_t(1) << 60) / pr->rows)

@@ -37,7 +37,8 @@ kata_status validate_rows(const void* p, const int64_t st[3], const int64_t size
 DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles);
 
 kata_status validate_rotary(const kata_rotary_problem* pr, std::string* why);
-kata_status validate_norm(const kata_norm_problem* pr, std::string* why);
+// The strides of the gradients' rows count in the backward pass only.
+kata_status validate_norm(const kata_norm_problem* pr, bool backward, std::string* why);
 size_t norm_workspace_bytes(const kata_norm_problem* pr);
 
 }  // namespace kata

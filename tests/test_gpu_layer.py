@@ -786,6 +786,13 @@ def test_layer_norm_strides_in_place_and_empty():
     assert torch.isfinite(y[[0, 3]]).all() and not torch.isfinite(y[1]).any()
 
 
+def test_layer_norm_forward_needs_no_strides_of_gradients():
+    x, y = _randn(1, 5, 64), torch.empty(5, 64, device=DEV)
+    pr = KL._NORM.pack(5, 64, KL._dtype(F32), KL._dtype(F32), 1e-5, 64, 0, 64, 0)
+    KL._run("kata_fwd_layer_norm", x.device, pr, x.data_ptr(), None, None, y.data_ptr(), None, None)
+    assert torch.equal(y, K.fwd_layer_norm(x))
+
+
 def test_layer_norm_refusals():
     x, w = _randn(1, 4, 64, dtype=BF), torch.ones(64, device=DEV)
     mean = torch.zeros(4, device=DEV)
