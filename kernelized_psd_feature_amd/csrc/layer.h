@@ -30,7 +30,4 @@ struct NormArgs {
 };
 hipError_t launch_norm_fwd(NormArgs& a, bool bf16, bool aligned, hipStream_t st);
 hipError_t launch_norm_bwd(NormArgs& a, bool bf16, bool aligned, hipStream_t st);
-// Workgroups whose partial sums of dw and db the backward pass keeps.
-constexpr int kNormBlocks = 768;
-
 }  // namespace kata

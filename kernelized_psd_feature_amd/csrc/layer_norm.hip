@@ -19,6 +19,7 @@
 // where it fits).
 #include "device.h"
 #include "layer.h"
+#include "layer_plan.h"
 #include "mfma_util.h"
 
 namespace kata {
@@ -356,6 +357,7 @@ __global__ __launch_bounds__(kThreads) void norm_dw_loop_kernel(NormArgs A) {
 template <typename T, bool kEdge, bool kBwd>
 bool launch_rows(NormArgs& a, hipStream_t st) {
   constexpr int V = 16 / sizeof(T);
+  if (a.N > kNormInRegisters) return false;
   const int nv = (a.N + V - 1) / V;
   auto run = [&](auto fwd, auto bwd, int rpb, int held) {
     const long long want = (a.rows + rpb - 1) / rpb;
@@ -377,6 +379,7 @@ bool launch_rows(NormArgs& a, hipStream_t st) {
   KATA_NORM(64, 3) KATA_NORM(64, 4) KATA_NORM(256, 2) KATA_NORM(256, 3) KATA_NORM(256, 4)
   if constexpr (V == 4) KATA_NORM(256, 8)           // 32 elements a thread, as of bf16 rows
 #undef KATA_NORM
+  static_assert(kNormInRegisters == 256 * (V == 4 ? 8 : 4) * V, "the widest of them");
   return false;
 }
 
@@ -392,7 +395,7 @@ hipError_t bwd_t(NormArgs& a, bool whole, hipStream_t st) {
   const bool rows = whole ? launch_rows<T, false, true>(a, st) : launch_rows<T, true, true>(a, st);
   if (!rows) {
     // dw and db first: dx may overwrite dy
-    a.blocks = (int)(a.rows < 64 ? a.rows : 64);
+    a.blocks = (int)(a.rows < kNormLoopBlocks ? a.rows : kNormLoopBlocks);
     if (a.part)
       launch_kernel(norm_dw_loop_kernel<T>, dim3((a.N + kThreads - 1) / kThreads, a.blocks), kThreads, 0, st, a);
     if (a.dx)

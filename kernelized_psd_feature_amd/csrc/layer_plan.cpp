@@ -181,8 +181,8 @@ kata_status validate_norm(const kata_norm_problem* pr, bool backward, std::strin
 }
 
 size_t norm_workspace_bytes(const kata_norm_problem* pr) {
-  // one pair of partial rows a workgroup, at most 768 of them (kNormBlocks)
-  const int64_t blocks = std::min<int64_t>(pr->rows, 768);
+  // one pair of partial rows a workgroup
+  const int64_t blocks = std::min<int64_t>(pr->rows, pr->N > kNormInRegisters ? kNormLoopBlocks : kNormBlocks);
   return (size_t(blocks) * 2 * pr->N * 4 + 255) & ~size_t(255);
 }
 

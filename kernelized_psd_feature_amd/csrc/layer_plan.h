@@ -39,6 +39,9 @@ DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles);
 kata_status validate_rotary(const kata_rotary_problem* pr, std::string* why);
 // The strides of the gradients' rows count in the backward pass only.
 kata_status validate_norm(const kata_norm_problem* pr, bool backward, std::string* why);
+// Workgroups whose partial sums of dw and db the backward pass keeps at most: of rows in registers, and
+// of wider ones than kNormInRegisters elements (layer_norm.hip).
+constexpr int kNormBlocks = 768, kNormLoopBlocks = 64, kNormInRegisters = 8192;
 size_t norm_workspace_bytes(const kata_norm_problem* pr);
 
 }  // namespace kata

@@ -761,6 +761,22 @@ def test_layer_norm_many_rows(N):
     _inside(db, rdb, 256 * 2.0 ** -24 * np.abs(ndy).sum(0), "db")
 
 
+@pytest.mark.parametrize("N", [8192, 8193, 8200])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_layer_norm_gradients_stay_inside_their_workspace(dtype, N):
+    # more rows than workgroups keep sums of; the bytes behind the workspace are left alone
+    rows = 900
+    x, dy = _randn(1, rows, N, dtype=dtype), _randn(2, rows, N, dtype=dtype)
+    _, mean, rstd = K.fwd_layer_norm(x, return_stats=True)
+    need = K.layer_norm_workspace_size(x)
+    ws = torch.full((need + 4096,), 171, dtype=torch.uint8, device=DEV)
+    dx, dw, db = K.bwd_layer_norm(dy, x, None, mean, rstd, workspace=ws[:need])
+    assert (ws[need:] == 171).all()
+    hat = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    _inside(dw, _np((dy.double() * hat).sum(0)), _np((rows + 64) * 2.0 ** -23 * (dy.double() * hat).abs().sum(0)), "dw")
+    _inside(db, _np(dy.double().sum(0)), _np((rows + 64) * 2.0 ** -24 * dy.double().abs().sum(0)), "db")
+
+
 def test_layer_norm_strides_in_place_and_empty():
     big = _randn(1, 6, 5, 200, dtype=BF)
     for lo in (0, 8, 3):

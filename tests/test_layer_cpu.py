@@ -203,6 +203,17 @@ def test_norm_refuses_bad_pointers():
     assert call(f[:6]) == INVALID
 
 
+@pytest.mark.parametrize("rows", [1, 63, 64, 65, 1 << 20])
+@pytest.mark.parametrize("N,most", [(1024, 768), (8192, 768), (8193, 64), (1 << 20, 64)])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_norm_workspace_holds_the_partial_rows_that_there_are(dtype, N, most, rows):
+    # a pair of fp32 rows a workgroup, in whole 256 bytes: of wide rows there are 64 workgroups
+    pr = _norm(rows=rows, N=N, dtype=dtype)
+    need = min(rows, most) * 2 * N * 4
+    got = K._lib().kata_bwd_layer_norm_workspace_size(ctypes.byref(pr))
+    assert need <= got < need + 256
+
+
 def test_the_binding_refuses_cpu_tensors_and_bad_rates():
     q = torch.zeros(1, 4, 2, 16)
     with pytest.raises(ValueError):
