@@ -1,6 +1,8 @@
 import os
 import sys
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
@@ -8,3 +10,18 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU and the built HIP library")
+
+
+# Calls that pass every check with addresses that are not real: without a GPU they end at the device
+# check, with one they would be launched.
+_FAKE_ADDRESSES = ("test_decay_accepts_broadcast_inputs", "test_scan_reports_log_depth")
+
+
+def pytest_collection_modifyitems(items):
+    found = [x for x in items if x.name.split("[")[0] in _FAKE_ADDRESSES]
+    if found:
+        import torch
+
+        if torch.cuda.device_count():
+            for x in found:
+                x.add_marker(pytest.mark.skip(reason="a GPU is present: nothing may be launched on fake addresses"))
