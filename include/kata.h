@@ -302,7 +302,10 @@ typedef struct {
   int64_t sq[3], sk[3], sv[3], so[3], sdo[3];
 } kata_decay_problem;
 
-/* Bytes of device workspace kata_fwd_decay needs (0: none, or an invalid problem). */
+/* Bytes of device workspace kata_fwd_decay needs (0: none, or an invalid problem): a state a segment,
+ * where sequences are cut into segments; packed, a state a sequence and one more for every segment
+ * that T rows have, as the offsets are known on the device only.  The backward pass needs three times
+ * as many. */
 size_t kata_fwd_decay_workspace_size(const kata_decay_problem* pr);
 
 /* Chunked forward.  initial_state, final_state: nullable; they may be the same array.
@@ -341,8 +344,8 @@ kata_status kata_decode_decay(const kata_decay_problem* pr, const void* q, const
  *     m (a cos(x r_i) - b sin(x r_i)),  m (a sin(x r_i) + b cos(x r_i)),
  * with the angle negated where inverse is set (the gradient); coordinates from rot on are copied.
  * Angles are formed in fp64, so far positions keep their phase.
- *   q [B][T][H][D] and, unless Hk = 0, k [B][T][Hk][D], the last axis contiguous; D <= 1024, rot
- *   even.  Rows of any alignment; those of whole, aligned 16-byte vectors (in the half layout rot / 2
+ *   q [B][T][H][D] and, unless Hk = 0, k [B][T][Hk][D], the last axis contiguous; D <= 1024, H and
+ *   Hk <= 4096, B T < 2^31, rot even.  Rows of any alignment; those of whole, aligned 16-byte vectors (in the half layout rot / 2
  *   too) are the fastest.  An output may be its own input (in place) but must not overlap inputs
  *   otherwise.
  *   rates: device fp64 [rot / 2], radians a token.  magnitude: m.
@@ -367,7 +370,7 @@ kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void
  * over rows of N elements, statistics and sums in fp32.  sx, sy, sdy, sdx: elements from a row of x, y,
  * dy, dx to the next, N at least (those of x and dy may be zero: the same row).  The forward pass looks
  * at sx and sy; a backward problem has all four, sy being its forward pass's.
- * weight, bias: [N] of w_dtype (fp32, or bf16 with bf16 rows), nullable: ones, zeros. */
+ * N is at most 2^24.  weight, bias: [N] of w_dtype (fp32, or bf16 with bf16 rows), nullable: ones, zeros. */
 typedef struct {
   int64_t rows;
   int32_t N;

@@ -12,11 +12,15 @@
 // itself), and the walk runs the chunks of each segment from its entry state.  With enough
 // sequences, heads and value blocks a sequence is one segment and the walk runs alone.
 //
-// Bound: HBM, and with segments k and v are read twice; the gradients by a chunk's chain of
-// products, LDS exchanges and two barriers (their roles read 9 tensors where 4 are distinct, through
-// the caches).  Measured, 16 bf16 heads: 131072 tokens of width 64, state pass 103 us (5.2 TB/s), scan
-// 7, walk 240 (4.5 TB/s); 4 x 16384 of width 128, 130 (4.1), 240 (4.5); 32 x 2048 of width 64, the walk
-// alone 118 us (4.5 TB/s); 8 x 4096, forward 20 + 54 us, backward 173 (805 MB, 470 MB distinct).
+// Bound.  State pass: HBM (k and v, which the walk reads again).  Walk: a chunk's chain of products, LDS
+// exchanges and barriers more than memory.  A token takes as long at 8 x 4096, whether the operands
+// are in the Infinity Cache (54 us) or not (59), as at 131072 (242); the waves stand ready and do not
+// issue for 42% of their cycles, wait for memory, LDS or a barrier for 30%, and the MFMA units are
+// busy for 13%.  The gradients likewise (their roles read 9 tensors where 4 are distinct, through the
+// caches).  Measured by kernel over three sets of inputs in turn, 16 bf16 heads: 131072 tokens of
+// width 64, state pass 101 to 110 us (5.1 TB/s), scan 8, walk 242 to 246 (4.4); 4 x 16384 of width 128,
+// 145 to 149 (3.7), 9, 258 to 264 (4.1); 8 x 4096 of width 64, 28 and 59 (with the inputs in the
+// cache 20 and 54), backward 178 to 182 (805 MB, 470 MB distinct); 32 x 2048, the walk alone, 118.
 //
 // Layout (four waves, or eight for value blocks of 128 columns; tiles are 16 x 16, K steps 32 wide;
 // fragment conventions as in mfma_util.h).  Both operands of a product enumerate its K step in one
@@ -280,9 +284,10 @@ struct Stage {
 
 // Row strides of the LDS tiles, in elements.  bf16 (64 banks of 4 bytes, s the stride in words): a
 // read of one 16-byte vector of 16 rows is free of conflicts for s = 4 odd mod 64, the transposing
-// reads of 16 bytes of 8 rows for s = 8 odd, and nearly for s = 36.  K is read both ways: s = 36 at
-// 64 columns, and at 128, where the padding to 36 mod 64 would not fit, s = 72 for the more
-// frequent transposed ones.
+// reads of 16 bytes of 8 rows for s = 8 odd.  K is read both ways.  At 64 columns s = 36, for the
+// former: conflicts are 31% of the LDS cycles of the state pass, which reads K transposed only, and
+// 42% of the walk's.  At 128, where the padding to 36 mod 64 would not fit, s = 72, for the more
+// frequent transposed reads: none in the state pass, 34% in the walk.
 template <typename T, int DK, int W>
 struct Tiles {
   static constexpr bool kBf = sizeof(T) == 2;

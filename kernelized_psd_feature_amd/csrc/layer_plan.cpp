@@ -118,8 +118,8 @@ DecayPlan plan_decay(const kata_decay_problem* pr, int n_roles) {
   // 20.7, backward 27.3, 31.1; 4096 (22): 28.9, 28.6; 8192 (32): 40.4, 36.4.
   p.join = p.scan && p.n_seg <= 12;
   // Operands that do not stay in the Infinity Cache (256 MB) until the walk reads them again are loaded
-  // past it; q, k, v and o together, 16 bf16 heads of width 64: 512 MB 149 us, 158 through the cache
-  // (64 x 1024: 107, 121; 131072 tokens: 320 to 340, 375), 448 MB 144, 146, 384 MB 140, 137, 256 MB
+  // past it; three sets of inputs in turn, q, k, v and o together, 16 bf16 heads of width 64: 512 MB 149 us, 158 through the cache
+  // (64 x 1024: 107, 121; 131072 tokens: 337, 375), 448 MB 144, 146, 384 MB 140, 137, 256 MB
   // 83, 75.  The gradients' three roles share what they read, and take it through the cache (32 x
   // 2048: 278 us, 308 past it; with only the operands of one role past it 289).
   const double rows = double(pr->T) * (pr->packed ? 1 : pr->n_seq) * pr->H;

@@ -204,7 +204,7 @@ def fwd_decay(q, k, v, log_decay, scale=1.0, initial_state=None, return_state=Fa
     q, k (B, T, H, dk), v (B, T, H, dv), bf16 or fp32, widths up to 128 with rows of whole 16 bytes,
     any (b, t, h) strides (broadcast axes too); o has the inputs' dtype.  log_decay: fp32 (H,).
     cu_seqlens: int32 (n + 1,) offsets of n sequences packed into B = 1; rows of no sequence are zero
-    in a new output and left as they are in `out`.
+    in a new output and left as they are in `out`, which must not overlap an input.
     initial_state, and the final state with return_state: fp32 (n, H, dk, dv); a state that is returned
     has its terms added exactly, so bf16 outputs may differ from a call without it by a rounding.
     Sums and states are fp32.  bf16 operands of a product are rounded: the state that a chunk of 64
@@ -320,7 +320,7 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
 
     q (B, T, H, D) and k (B, T, Hk, D) (or None), bf16 or fp32; positions: int32 or int64, broadcastable
     to (B, T), or None: offset + t.  inverse negates the angles: the gradient.  out: outputs of q (and
-    k), which may be q and k themselves.  Returns the turned q, or the pair."""
+    k), which may be q and k themselves and overlap neither otherwise.  Returns the turned q, or the pair."""
     device, dtype, shape = q.device, q.dtype, q.shape
     if not q.is_cuda:
         raise ValueError("q must be a GPU tensor")
