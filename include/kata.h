@@ -308,7 +308,8 @@ typedef struct {
  * as many. */
 size_t kata_fwd_decay_workspace_size(const kata_decay_problem* pr);
 
-/* Chunked forward.  initial_state, final_state: nullable; they may be the same array.
+/* Chunked forward.  initial_state, final_state: nullable; they may be the same array, and overlap in
+ * no other way.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE (256-byte aligned), DEVICE. */
 kata_status kata_fwd_decay(const kata_decay_problem* pr, const void* q, const void* k,
                            const void* v, const float* log_decay, const int32_t* cu_seqlens,
@@ -323,7 +324,7 @@ size_t kata_bwd_decay_workspace_size(const kata_decay_problem* pr);
  *     dk_s = g^(T-1-s) dS v_s + scale sum_{t>=s} g^(t-s) (dO_t . v_s) q_t
  *     dv_s = g^(T-1-s) dS^T k_s + scale sum_{t>=s} g^(t-s) (q_t . k_s) dO_t
  *     dS_{-1} = g^T dS + scale sum_t g^(t+1) q_t dO_t^T
- * initial_state and dfinal_state: nullable (zero).  dq, dk, dv: contiguous [B][T][H][width] of
+ * initial_state and dfinal_state: nullable (zero); dinitial_state overlaps neither.  dq, dk, dv: contiguous [B][T][H][width] of
  * the problem's dtype. */
 kata_status kata_bwd_decay(const kata_decay_problem* pr, const void* q, const void* k,
                            const void* v, const void* dO, const float* log_decay,

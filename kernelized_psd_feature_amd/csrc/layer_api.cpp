@@ -91,22 +91,16 @@ kata_status check_grid(const kata::DecayPlan& p) {
   return KATA_OK;
 }
 
-// Whether a final state is written where an initial state is read: its workgroups read the initial
-// state at different times then.
-bool states_overlap(const kata::DecayArgs& a) {
-  for (int i = 0; i < a.n_roles; ++i)
-    for (int j = 0; j < a.n_roles; ++j) {
-      const uintptr_t f = uintptr_t(a.role[i].fin), s = uintptr_t(a.role[j].init);
-      const uintptr_t n = uintptr_t(a.n_seq) * a.H * a.role[0].dk * a.role[0].dv * 4;
-      if (f && s && f < s + n && s < f + n) return true;
-    }
-  return false;
+// Whether states are written where others are read.
+bool states_overlap(const kata_decay_problem* pr, const float* written, const float* read) {
+  const uintptr_t w = uintptr_t(written), r = uintptr_t(read);
+  const uintptr_t n = uintptr_t(pr->n_seq) * pr->H * pr->dk * pr->dv * 4;
+  return w && r && w < r + n && r < w + n;
 }
 
 kata_status run_decay(kata::DecayArgs& a, const kata::DecayPlan& p, bool bf16, bool exact_state,
                       hipStream_t st, const char* what) {
   hipError_t e = hipSuccess;
-  if (a.join && states_overlap(a)) a.join = 0;
   if (p.scan) {
     {
       Timed t(KATA_K_CHUNK_STATE, st);
@@ -146,6 +140,8 @@ kata_status kata_fwd_decay(const kata_decay_problem* pr, const void* q, const vo
   const kata::DecayPlan p = kata::plan_decay(pr, 1);
   if ((s = check_workspace(workspace, ws_bytes, p.role_bytes)) != KATA_OK) return s;
   if ((s = check_grid(p)) != KATA_OK) return s;
+  if (final_state != initial_state && states_overlap(pr, final_state, initial_state))
+    return set_error(KATA_ERR_INVALID_ARGUMENT, "final_state overlaps initial_state without being it");
   if ((s = check_device()) != KATA_OK) return s;
   kata::DecayArgs a = decay_args(pr, p, log_decay, cu_seqlens, 1);
   kata::DecayRole& r = a.role[0];
@@ -153,6 +149,9 @@ kata_status kata_fwd_decay(const kata_decay_problem* pr, const void* q, const vo
   copy3(r.sa, pr->sq); copy3(r.sb, pr->sk); copy3(r.sc, pr->sv); copy3(r.so, pr->so);
   r.init = initial_state;
   r.fin = final_state;
+  // one array: the walk's workgroups would read a sequence's initial state at different times, the scan
+  // reads it once
+  if (initial_state && initial_state == final_state) a.join = 0;
   r.states = static_cast<float*>(workspace);
   r.dk = pr->dk; r.dv = pr->dv;
   r.out_scale = pr->scale; r.kv_scale = 1.f;
@@ -184,6 +183,8 @@ kata_status kata_bwd_decay(const kata_decay_problem* pr, const void* q, const vo
   const kata::DecayPlan p = kata::plan_decay(pr, 3);
   if ((s = check_workspace(workspace, ws_bytes, 3 * p.role_bytes)) != KATA_OK) return s;
   if ((s = check_grid(p)) != KATA_OK) return s;
+  if (states_overlap(pr, dinitial_state, initial_state) || states_overlap(pr, dinitial_state, dfinal_state))
+    return set_error(KATA_ERR_INVALID_ARGUMENT, "dinitial_state overlaps initial_state or dfinal_state");
   if ((s = check_device()) != KATA_OK) return s;
   kata::DecayArgs a = decay_args(pr, p, log_decay, cu_seqlens, 3);
   char* ws = static_cast<char*>(workspace);

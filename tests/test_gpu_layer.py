@@ -148,6 +148,19 @@ def test_decay_backward(dtype, shape, states):
     assert all(x is y or torch.equal(x, y) for x, y in zip(grads, again))
 
 
+@pytest.mark.parametrize("T,dk,dv", [(1, 4, 4), (70, 12, 20), (300, 100, 68), (513, 36, 124), (700, 4, 128), (260, 128, 4)])
+def test_decay_fp32_widths_of_odd_vectors(T, dk, dv):
+    # rows of four fp32 elements and odd multiples of it, which bf16 does not have
+    B, H = 2, 2
+    q, k, v, g = (_randn(i, B, T, H, d) for i, d in ((1, dk), (2, dk), (3, dv), (4, dv)))
+    S0, dS, ld = _randn(5, B, H, dk, dv), _randn(6, B, H, dk, dv), _decays(H)
+    o, S = K.fwd_decay(q, k, v, ld, initial_state=S0, return_state=True)
+    grads = K.bwd_decay(q, k, v, g, ld, initial_state=S0, dfinal_state=dS)
+    _check_decay(q, k, v, ld, 1.0, S0=S0, dO=g, dS=dS, o=o, S=S, grads=grads)
+    st = S0.clone()
+    _check_decay(q, k, v, ld, 1.0, S0=S0, o=K.decode_decay(q, k, v, ld, st), S=st)
+
+
 @pytest.mark.parametrize("ld", ["0.0", "-1e-4", "-3.0", "-40.0", "-inf", "0.02"])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_decay_of_any_strength(dtype, ld):

@@ -116,6 +116,25 @@ def test_decay_refuses_more_workgroups_than_it_can_number(n_seq, H, dtype, d):
     assert b"one launch" in K._lib().kata_last_error()
 
 
+def test_decay_refuses_states_that_overlap():
+    size = 2 * 2 * 64 * 64 * 4
+    s0 = _fake(9)[5].value
+    for by in (-size + 16, -16, 16, size - 16):      # the same array at another place
+        assert _fwd(_decay(), sT=ctypes.c_void_p(s0 + by)) == INVALID
+        assert b"overlaps" in K._lib().kata_last_error()
+    if not torch.cuda.is_available():                # (made-up addresses: nothing may be launched on them)
+        for by in (-size, 0, size):
+            assert _fwd(_decay(), sT=ctypes.c_void_p(s0 + by)) == DEVICE
+    lib, f, pr = K._lib(), _fake(14), _decay()
+    need = lib.kata_bwd_decay_workspace_size(ctypes.byref(pr))
+    for i in (6, 7):                                 # initial_state, dfinal_state
+        for by in (-16, 0, size - 16):
+            a = list(f[:12])
+            a[11] = ctypes.c_void_p(f[i].value + by)
+            assert lib.kata_bwd_decay(ctypes.byref(pr), *a, f[13], need, None) == INVALID
+            assert b"overlaps" in lib.kata_last_error()
+
+
 def test_decode_takes_any_number_of_sequences():
     if torch.cuda.is_available():
         pytest.skip("the addresses are not real: nothing may be launched on them")
