@@ -202,7 +202,7 @@ def fwd_decay(q, k, v, log_decay, scale=1.0, initial_state=None, return_state=Fa
     """o_t = scale q_t S_t with S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T, in chunks (MFMA).
 
     q, k (B, T, H, dk), v (B, T, H, dv), bf16 or fp32, widths up to 128 with rows of whole 16 bytes,
-    any (b, t, h) strides (broadcast axes too); o has the inputs' dtype.  log_decay: fp32 (H,).
+    any (b, t, h) strides that keep rows apart, or zero (broadcast axes); o has the inputs' dtype.  log_decay: fp32 (H,).
     cu_seqlens: int32 (n + 1,) offsets of n sequences packed into B = 1; rows of no sequence are zero
     in a new output and left as they are in `out`, which must not overlap an input.
     initial_state, and the final state with return_state: fp32 (n, H, dk, dv); a state that is returned
@@ -377,14 +377,18 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
 # ---- layer norm --------------------------------------------------------------------------------
 
 def _rows(x):
-    """x as (rows, N) with one row stride, copied only where its axes do not collapse."""
-    if x.dim() == 2 and (x.shape[1] == 1 or x.stride(1) == 1):
-        return x
-    try:
-        y = x.view(-1, x.shape[-1])
-    except RuntimeError:
-        y = x.contiguous().view(-1, x.shape[-1])
-    return y if y.shape[1] == 1 or y.stride(1) == 1 else y.contiguous()
+    """x as (rows, N) with one row stride, copied only where its axes do not collapse or its rows overlap
+    (windows of one array)."""
+    N = x.shape[-1]
+    if x.dim() == 2:
+        y = x
+    else:
+        try:
+            y = x.view(-1, N)
+        except RuntimeError:
+            return x.contiguous().view(-1, N)
+    step, one = y.stride()
+    return y if (one == 1 or N == 1) and (step >= N or step == 0 or y.shape[0] == 1) else y.contiguous()
 
 
 def _check_norm(x, weight, bias):

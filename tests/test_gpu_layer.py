@@ -822,6 +822,18 @@ def test_layer_norm_forward_needs_no_strides_of_gradients():
     assert torch.equal(y, K.fwd_layer_norm(x))
 
 
+@pytest.mark.parametrize("step", [1, 3, 64])
+def test_layer_norm_of_windows_that_overlap(step):
+    base = _randn(1, 2, 200)
+    x = base.unfold(1, 64, step)                     # (2, windows, 64), rows `step` elements apart
+    dy = _randn(2, 2, 200).unfold(1, 64, step)
+    y, mean, rstd = K.fwd_layer_norm(x, return_stats=True)
+    assert torch.equal(y, K.fwd_layer_norm(x.contiguous()))
+    got, want = K.bwd_layer_norm(dy, x, None, mean, rstd), K.bwd_layer_norm(dy.contiguous(), x.contiguous(), None, mean, rstd)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(K.fwd_layer_norm(x[0]), y[0]) and torch.equal(K.fwd_layer_norm(x[0, :1]), y[0, :1])
+
+
 def test_layer_norm_refusals():
     x, w = _randn(1, 4, 64, dtype=BF), torch.ones(64, device=DEV)
     mean = torch.zeros(4, device=DEV)
