@@ -394,6 +394,64 @@ kata_status kata_bwd_layer_norm(const kata_norm_problem* pr, const void* dy, con
                                 void* dweight, void* dbias, void* workspace, size_t ws_bytes,
                                 void* stream);
 
+/* ---- Gated delta rule ------------------------------------------------------------------------
+ * Causal, a state that is corrected rather than only added to; per head, with g_t = exp(log_decay_t) and
+ * b_t = beta_t, and per sequence
+ *     S_t = g_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T  (dk x dv),     o_t = scale S_t^T q_t,
+ * S_{-1} being the initial state (zero where none is given).  Keys of unit length (kata_qk_norm) and b_t in
+ * [0, 2] keep it stable; other values are computed as they are.  Chunks of 64 tokens run on MFMA (fp32
+ * problems on the fp32 MFMA).  Sums, inverses and states are fp32; in bf16 problems an operand that comes
+ * out of them (state, inverse, correction, weight) is kept in two bf16 terms, hi + lo, which hold 2^-18 of it.
+ * A token reaches only later ones, infinities and NaN included: from one on, the columns that it
+ * reaches are NaN.  Gradients of sequences with such values are not defined.
+ *
+ *   n_seq, T, packed, zero_tail, dtype: as in kata_decay_problem, n_seq at most 65535 in the chunked forms.
+ *   H: heads of v, beta, log_decay, o and the states; Hk: heads of q and k, a divisor of H: value head h
+ *          uses head h / (H / Hk).  At most 65535.
+ *   dk, dv: width of q and k, width of v: at most 128, rows of whole 16 bytes.
+ *   beta: [b][t][H] of dtype; log_decay: fp32 [b][t][H], or NULL (no decay); below -256 taken as -256, a decay
+ *          of zero in fp32.
+ *   sq .. sdo: element strides of (b, t, h) of q, k, v, o and dO, as in kata_decay_problem; sbeta, sdecay:
+ *          of beta and log_decay, any that are not negative. */
+typedef struct {
+  int32_t n_seq, H, Hk, T, dk, dv;
+  int32_t packed;
+  int32_t zero_tail;
+  int32_t dtype;
+  float scale;
+  int64_t sq[3], sk[3], sv[3], so[3], sdo[3], sbeta[3], sdecay[3];
+} kata_delta_problem;
+
+/* Bytes of device workspace kata_fwd_delta needs (0 for an invalid problem): 13.6 KB for a chunk of 64 tokens
+ * and head, and where sequences are cut into segments, a state and a transition (dk x dk) a segment. */
+size_t kata_fwd_delta_workspace_size(const kata_delta_problem* pr);
+
+/* Chunked forward.  initial_state, final_state: fp32 [n_seq][H][dk][dv], nullable; they do not overlap.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE (256-byte aligned), DEVICE. */
+kata_status kata_fwd_delta(const kata_delta_problem* pr, const void* q, const void* k, const void* v,
+                           const void* beta, const float* log_decay, const int32_t* cu_seqlens,
+                           const float* initial_state, void* o, float* final_state, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+size_t kata_bwd_delta_workspace_size(const kata_delta_problem* pr);
+
+/* Gradients of sum(dO * o) + sum(dfinal_state * final_state) in q, k [B][T][Hk][dk] (summed over the value
+ * heads that share them), v [B][T][H][dv], beta [B][T][H] of dtype, and log_decay fp32 [B][T][H]
+ * (dlog_decay NULL: not wanted), all contiguous, and where dinitial_state is not NULL, the initial state.
+ * Rows of no sequence get zeros.  initial_state and dfinal_state: nullable (zero); dinitial_state overlaps
+ * neither. */
+kata_status kata_bwd_delta(const kata_delta_problem* pr, const void* q, const void* k, const void* v,
+                           const void* beta, const float* log_decay, const void* dO, const int32_t* cu_seqlens,
+                           const float* initial_state, const float* dfinal_state, void* dq, void* dk, void* dv,
+                           void* dbeta, float* dlog_decay, float* dinitial_state, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* Recurrent form: advances state [n_seq][H][dk][dv], in place, over the T tokens one at a time (T = 1 is one
+ * decode step) in fp32 and writes o.  packed must be 0.  Calls that share a state must be ordered on one
+ * stream. */
+kata_status kata_decode_delta(const kata_delta_problem* pr, const void* q, const void* k, const void* v,
+                              const void* beta, const float* log_decay, float* state, void* o, void* stream);
+
 /* Static text for a status code. */
 const char* kata_status_string(kata_status s);
 

@@ -39,6 +39,7 @@ __all__ = [
     "fwd_decay", "bwd_decay", "decode_decay", "decay_state_shape", "decay_workspace_size",
     "parallel_decay_attn", "rotary_rates", "rotary", "layer_norm", "fwd_layer_norm",
     "bwd_layer_norm", "layer_norm_workspace_size",
+    "fwd_delta", "bwd_delta", "decode_delta", "delta_state_shape", "delta_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -114,7 +115,7 @@ def _lib():
             "kata_last_error": (ctypes.c_char_p, []),
             "kata_timing_begin": (I32, []),
             "kata_timing_end": (I32, [ctypes.POINTER(_Times)]),
-            **layer._signatures(),
+            **layer._signatures(), **delta._signatures(),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -431,3 +432,6 @@ from . import layer  # noqa: E402  (needs the helpers above)
 from .layer import (  # noqa: E402
     bwd_decay, bwd_layer_norm, decay_state_shape, decay_workspace_size, decode_decay, fwd_decay,
     fwd_layer_norm, layer_norm, layer_norm_workspace_size, parallel_decay_attn, rotary, rotary_rates)
+from . import delta  # noqa: E402
+from .delta import (  # noqa: E402
+    bwd_delta, decode_delta, delta_state_shape, delta_workspace_size, fwd_delta)

@@ -1,0 +1,746 @@
+// Gated delta rule, gfx950: chunked form and recurrent form.
+//
+//   S_t = g_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// Chunk of 64 tokens with entry state S (the state behind the token before it), c_i the sum of the log
+// decays of its tokens 0 .. i, y_i = exp(c_i):
+//   A_ij = b_i exp(c_i - c_j) (k_i . k_j) for j < i, else 0
+//   U = (I + A)^-1 diag(b) (V - diag(y) K S)
+//   o = scale (diag(y) Q S + P U),  P_ij = exp(c_i - c_j) (q_i . k_j) for j <= i
+//   S <- y_63 S + sum_j exp(c_63 - c_j) k_j u_j^T
+// The inverses need no state: the first pass forms them for all chunks at once (delta_prep_kernel).
+// The walk then runs the chunks of a sequence one after the other; everything in it that depends on S
+// belongs to single columns of the values, so a wave takes 16 of them and passes S, X = b (V - y K S) and U
+// from product to product in registers.
+//
+// A chunk maps S to M S + N.  Where sequences and heads do not fill the card, a sequence is cut into
+// segments of L chunks: a pass over each of them gives its N (the recurrence from a state of zero) and its
+// M (the recurrence from the unit matrix, without values), delta_join_kernel turns them into entry states,
+// and the walk runs the segments side by side.
+#include <type_traits>
+
+#include "delta.h"
+#include "delta_tiles.h"
+#include "device.h"
+#include "mfma_util.h"
+
+namespace kata {
+namespace {
+
+constexpr int kThreads = 256;             // of the kernels other than the walk
+
+// ---- inverses --------------------------------------------------------------------------------
+// One workgroup for a chunk and head.  A wave forms a strip of 16 rows of A (fp32 sums on MFMA); the four
+// blocks on the diagonal are inverted by substitution, 16 lanes a block, a column each; below them
+// T_ij = -D_i sum_{j <= k < i} A_ik T_kj, a wave a block column, on the fp32 MFMA.
+template <typename T, int DK>
+struct PrepTiles {
+  static constexpr int LK = DK + 16 / (int)sizeof(T), LA = kC + 4, LD = 20;
+  static constexpr int kHead = 16 + kC * 8 + kC * 4;                   // an int, c, beta
+  static constexpr int kKeys = kC * LK * (int)sizeof(T), kInv = kC * LA * 4;
+  static constexpr int kFirst = kKeys > kInv ? kKeys : kInv;           // the keys, then the inverse
+  static constexpr int bytes = kHead + kFirst + kC * LA * 4 + kC * LD * 4;
+};
+
+template <typename T, int DK>
+__global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int backward) {
+  using TL = PrepTiles<T, DK>;
+  using frag = typename Elem<T>::frag;
+  constexpr int M = DK / 32, LK = TL::LK, LA = TL::LA, LD = TL::LD;
+  extern __shared__ __align__(16) char lds[];
+  int* const sh = reinterpret_cast<int*>(lds);
+  double* const sc = reinterpret_cast<double*>(lds + 16);
+  float* const sb = reinterpret_cast<float*>(lds + 16 + kC * 8);
+  T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
+  float* const sT = reinterpret_cast<float*>(lds + TL::kHead);
+  float* const sA = reinterpret_cast<float*>(lds + TL::kHead + TL::kFirst);
+  float* const sD = sA + kC * LA;
+
+  const DeltaMap& m = A.m;
+  const unsigned unit = block_number();
+  if (unit >= (unsigned)m.c_slots * (unsigned)m.H) return;
+  const int slot = int(unit / (unsigned)m.H), h = int(unit - (unsigned)slot * (unsigned)m.H);
+  DeltaPart s;
+  if (!find_part(m, slot, 1, m.n_chunks, m.c_slots, sh, s) || s.seq == m.n_seq) return;
+  const int row0 = s.start + kC * s.part, n = min(kC, s.len - kC * s.part);
+  if (n <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  Stage<T, DK, kThreads> rk(reinterpret_cast<const T*>(A.k) + s.b * A.sk[0] + row0 * A.sk[1] + (h / (m.H / m.Hk)) * A.sk[2],
+                            A.sk[1], m.dk, true);
+  fetch_rows(rk, A.sk[1], n);
+  if (m.dk < DK)
+    for (int i = tid; i < kC * LK * (int)sizeof(T) / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sK)[i] = uint4{0u, 0u, 0u, 0u};
+  if (w == 0) {
+    float ld = 0.f, b = 0.f;
+    if (lane < n) {
+      b = to_f32(reinterpret_cast<const T*>(A.beta)[row_off(A.sb, s.b, row0 + lane, h)]);
+      if (A.log_decay) ld = A.log_decay[row_off(A.sl, s.b, row0 + lane, h)];
+      if (ld < -256.f) ld = -256.f;                 // exp of it is zero in fp32; sums of 64 stay finite
+      // U / b is wanted there: a factor of 1e-30 is as good as none, and can be taken out again
+      if (backward && fabsf(b) < 1e-30f) b = copysignf(1e-30f, b);
+    }
+    double c = ld;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double up = __shfl_up(c, d);
+      if (lane >= d) c += up;
+    }
+    const double all = __shfl(c, 63);
+    sc[lane] = c;
+    sb[lane] = b;
+    float* vec = A.vec + (long long)unit * kDeltaVec;
+    vec[lane] = exp64(c);
+    vec[kC + lane] = exp64(all - c);
+    vec[2 * kC + lane] = b;
+    reinterpret_cast<double*>(vec + 3 * kC)[lane] = c;
+  }
+  if (m.dk < DK) __syncthreads();
+  rk.template put_split<LK>(sK);
+  __syncthreads();
+
+  // A: rows 16 w + 4 g + r, columns 16 j + l16
+  frag ka[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) ka[i] = row_frag(sK + (16 * w + l16) * LK + 32 * i + 8 * g);
+  for (int j = 0; j <= w; ++j) {                    // uniform
+    f32x4 acc = zero4();
+#pragma unroll
+    for (int i = 0; i < M; ++i) acc = mma(ka[i], row_frag(sK + (16 * j + l16) * LK + 32 * i + 8 * g), acc);
+    const int col = 16 * j + l16;
+    const double cj = sc[col];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * w + 4 * g + r;
+      sA[row * LA + col] = col < row ? sb[row] * exp64(sc[row] - cj) * acc[r] : 0.f;
+    }
+  }
+  __syncthreads();
+  if (w == 0) {                                     // block g, column l16: x = e - A x
+    float x[16];
+    const float* a = sA + 16 * g * LA + 16 * g;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float y = i == l16 ? 1.f : 0.f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) y = fmaf(-a[i * LA + j], x[j], y);
+      x[i] = y;
+      sD[(16 * g + i) * LD + l16] = y;
+    }
+  }
+  __syncthreads();
+  {                                                 // block column w
+    f32x4 t[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) t[0][r] = sD[(16 * w + 4 * g + r) * LD + l16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                   // block row w + i
+      if (w + i > 3) break;                         // uniform
+      const int bi = w + i;
+      if (i > 0) {
+        f32x4 acc = zero4();
+#pragma unroll
+        for (int k = 0; k < i; ++k) {
+          const f32x4 a = *reinterpret_cast<const f32x4*>(sA + (16 * bi + l16) * LA + 16 * (w + k) + 4 * g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], t[k][r], acc, 0, 0, 0);
+        }
+        const f32x4 d = *reinterpret_cast<const f32x4*>(sD + (16 * bi + l16) * LD + 4 * g);
+        t[i] = zero4();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(-d[r], acc[r], t[i], 0, 0, 0);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sT[(16 * bi + 4 * g + r) * LA + 16 * w + l16] = t[i][r];
+    }
+  }
+  __syncthreads();
+  // as operands: lane's row l16 (of the transpose: column) of a tile, split slots of the other index
+  for (int f = w; f < (backward ? 2 : 1) * kInvFrags; f += 4) {
+    const bool trans = f >= kInvFrags;
+    const int x = trans ? f - kInvFrags : f;
+    const int it = trans ? (x < 4 ? x >> 1 : x - 2) : (x < 2 ? x : 1 + (x >> 1));
+    const int ms = trans ? (x < 4 ? x & 1 : 1) : (x < 2 ? 0 : x & 1);
+    f32x4 p[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int other = 2 * ms + half;              // block of the K step
+      if (!trans) {
+        p[half] = other > it ? zero4()
+                             : *reinterpret_cast<const f32x4*>(sT + (16 * it + l16) * LA + 16 * other + 4 * g);
+      } else {
+        p[half] = zero4();
+        if (other >= it)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[half][r] = sT[(16 * other + 4 * g + r) * LA + 16 * it + l16];
+      }
+    }
+    Op<T> op;
+    split_terms(p[0], p[1], op);
+    T* dst = reinterpret_cast<T*>(trans ? A.inv_t : A.inv) + (long long)unit * kInvElems<T>;
+#pragma unroll
+    for (int t = 0; t < kTerms<T>; ++t)
+      *reinterpret_cast<frag*>(dst + ((x * kTerms<T> + t) * 64 + lane) * 8) = op.t[t];
+  }
+}
+
+// ---- the walk ----------------------------------------------------------------------------------
+enum class Walk { output, states, sums };
+
+template <typename T, int DK, int W, bool kOut>
+struct WalkTiles {
+  static constexpr bool kBf = sizeof(T) == 2;
+  static constexpr int DV = 16 * W;
+  static constexpr int LK = DK + 16 / (int)sizeof(T), LV = DV + (kBf ? 16 : 4), LP = kC + 16 / (int)sizeof(T);
+  static constexpr int kHead = 16 + kDeltaVec * 4;
+  static constexpr int kTiles = kC * (LK * (kOut ? 2 : 1) + LV);
+  static constexpr int bytes = kHead + (kTiles + (kOut ? kTerms<T> * kC * LP : 0)) * (int)sizeof(T);
+};
+
+// kWhat: outputs and the final state; or (backward) the states before the chunks; or, of the segments,
+// sums and transitions (blocks of columns behind those of the values).
+template <typename T, int DK, int W, Walk kWhat>
+__global__ __launch_bounds__(64 * W) void delta_walk_kernel(DeltaArgs A, int blocks, int backward) {
+  constexpr bool kOut = kWhat == Walk::output, kSums = kWhat == Walk::sums;
+  using TL = WalkTiles<T, DK, W, kOut>;
+  using frag = typename Elem<T>::frag;
+  constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
+  extern __shared__ __align__(16) char lds[];
+  int* const sh = reinterpret_cast<int*>(lds);
+  float* const vec = reinterpret_cast<float*>(lds + 16);
+  const double* const sc = reinterpret_cast<const double*>(vec + 3 * kC);
+  T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
+  T* const sV = sK + kC * LK;
+  T* const sQ = sV + kC * LV;
+  T* const sP = sQ + kC * LK;
+
+  const DeltaMap& m = A.m;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // the blocks of one (segment, head) read the same rows: ids congruent mod 8, one XCD
+  const unsigned x = block_number(), per = blocks, y = x / 8 / per, unit = 8 * y + x % 8;
+  int sub = int(x / 8 - y * per);
+  if (unit >= (unsigned)m.n_slots * (unsigned)m.H) return;
+  const int slot = int(unit / (unsigned)m.H), h = int(unit - (unsigned)slot * (unsigned)m.H);
+  const int v_blocks = (m.dv + DV - 1) / DV;
+  const bool unit_matrix = kSums && sub >= v_blocks;                   // columns of the transition
+  if (unit_matrix) sub -= v_blocks;
+  const int c0 = sub * DV, cols = unit_matrix ? m.dk : m.dv;
+
+  DeltaPart s;
+  if (!find_part(m, slot, m.L, m.n_seg, m.n_slots, sh, s)) return;
+  const int L = m.L;
+  T* const out = kOut ? reinterpret_cast<T*>(A.o) + s.b * A.so[0] + h * A.so[2] + c0 : nullptr;
+  if constexpr (kOut) {
+    const int per_row = min(DV, m.dv - c0) / 4;
+    auto clear = [&](int from, int rows) {          // the block's columns of `rows` output rows
+      for (long long i = tid; i < (long long)rows * per_row; i += kThr)
+        store4(out + (from + i / per_row) * A.so[1] + i % per_row * 4, zero4());
+    };
+    if (s.seq == m.n_seq) {                         // rows behind the last sequence
+      if (A.zero_tail) clear(s.start + kC * L * s.part, min(kC * L, s.len - kC * L * s.part));
+      return;
+    }
+    if (m.packed && A.zero_tail && s.seq == 0 && s.part == 0) clear(0, s.start);   // before the first
+  }
+  if (s.seq == m.n_seq) return;
+  const int n_chunks = (s.len + kC - 1) / kC, n_seg = (n_chunks + L - 1) / L;
+  const long long SE = (long long)m.dk * m.dv, st_off = ((long long)s.seq * m.H + h) * SE;
+  if (s.part >= n_seg) {
+    if (kOut && s.len == 0 && s.part == 0 && A.fin)  // an empty sequence
+      for (int i = tid; i < m.dk * DV; i += kThr) {
+        const int r = i / DV, c = c0 + i % DV;
+        if (c < m.dv) A.fin[st_off + (long long)r * m.dv + c] = A.init ? A.init[st_off + (long long)r * m.dv + c] : 0.f;
+      }
+    return;
+  }
+  const bool last_seg = s.part == n_seg - 1;
+  if constexpr (kSums) {
+    // the sum of the last segment enters no entry state; a transition is used where a state comes in
+    // from before, or in reversed time from behind
+    if (!unit_matrix && last_seg) return;
+    const bool from_before = !last_seg && (s.part > 0 || A.init);
+    const bool from_behind = backward && s.part > 0 && (!last_seg || A.dfin);
+    if (unit_matrix && !from_before && !from_behind) return;
+  }
+  const int first = s.part * L, behind = min(first + L, n_chunks);
+  const long long row0 = s.start + (long long)kC * first;
+  const int hk = h / (m.H / m.Hk);
+  Stage<T, DK, kThr> rk(reinterpret_cast<const T*>(A.k) + s.b * A.sk[0] + row0 * A.sk[1] + hk * A.sk[2], A.sk[1], m.dk, true);
+  Stage<T, DK, kThr> rq(reinterpret_cast<const T*>(kOut ? A.q : A.k) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2], A.sq[1], m.dk, true);
+  Stage<T, DV, kThr> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + (unit_matrix ? 0 : c0),
+                        A.sv[1], m.dv - (unit_matrix ? 0 : c0), false);
+  const int n_last = min(kC, s.len - kC * (behind - 1));
+  uint4 vec_next;
+  const long long chunk0 = (long long)(s.c_slot + first) * m.H + h;    // [c_slots][H]
+  auto fetch = [&](int c) {
+    const int n = c == behind - 1 ? n_last : kC;
+    fetch_rows(rk, A.sk[1], n);
+    if constexpr (kOut) fetch_rows(rq, A.sq[1], n);
+    if (!unit_matrix) fetch_rows(rv, A.sv[1], n);
+    if (tid < kDeltaVec / 4)
+      vec_next = reinterpret_cast<const uint4*>(A.vec + (chunk0 + (long long)(c - first) * m.H) * kDeltaVec)[tid];
+  };
+  Op<T> inv[kInvFrags];
+  auto fetch_inv = [&](int c) {
+    const T* at = reinterpret_cast<const T*>(A.inv) + (chunk0 + (long long)(c - first) * m.H) * kInvElems<T>;
+#pragma unroll
+    for (int f = 0; f < kInvFrags; ++f) load_inv<T>(at, f, lane, inv[f]);
+  };
+  fetch(first);
+  fetch_inv(first);
+
+  // state tiles: S[i] lane holds rows 16 i + 4 g + r of column c0 + wc + l16
+  const int wc = 16 * w, col = c0 + wc + l16;
+  f32x4 S[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    S[i] = zero4();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * g + r;
+      if (kSums) {
+        if (unit_matrix && row == col) S[i][r] = 1.f;
+      } else if (row < m.dk && col < m.dv) {
+        if (s.part > 0) S[i][r] = A.sums[((long long)slot * m.H + h) * SE + (long long)row * m.dv + col];
+        else if (A.init) S[i][r] = A.init[st_off + (long long)row * m.dv + col];
+      }
+    }
+  }
+  if (m.dk < DK || m.dv - c0 < DV || unit_matrix) { // columns that no operand has: zeros all along
+    uint4* const z = reinterpret_cast<uint4*>(sK);
+    for (int i = tid; i < TL::kTiles * (int)sizeof(T) / 16; i += kThr) z[i] = uint4{0u, 0u, 0u, 0u};
+  }
+  const bool live_col = c0 + wc + 4 * g < m.dv;
+  T* po = kOut ? out + (row0 + l16) * A.so[1] + wc + 4 * g : nullptr;
+
+  for (int c = first; c < behind; ++c) {
+    const int n = c == behind - 1 ? n_last : kC;
+    __syncthreads();                                // the last chunk's tiles have been read
+    rk.template put_split<LK>(sK);
+    if constexpr (kOut) rq.template put_split<LK>(sQ);
+    if (!unit_matrix) rv.template put<LV>(sV);
+    if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
+    if (c + 1 < behind) fetch(c + 1);
+    __syncthreads();
+
+    if (kWhat == Walk::states && 16 * (c0 / 16 + w) < (m.dv + 15) / 16 * 16) {
+      float* dst = A.cstates + ((chunk0 + (long long)(c - first) * m.H) * ((m.dv + 15) / 16) + c0 / 16 + w) * (DK * 16) + lane * 4;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(dst + i * 256) = S[i];
+    }
+    Op<T> sf[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
+    f32x4 X[4], U[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      X[it] = zero4();
+#pragma unroll
+      for (int i = 0; i < M; ++i) X[it] = mul<T>(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], X[it]);
+    }
+    if constexpr (kOut) {                           // P, the wave's strip of rows
+      constexpr int J = 16 / W;
+      const int rt = w & 3, j0 = J * (w >> 2);
+      frag qf[M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) qf[i] = row_frag(sQ + (16 * rt + l16) * LK + 32 * i + 8 * g);
+      const double ci = sc[16 * rt + l16];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        f32x4 p = zero4();
+        if (j0 + j <= rt) {                         // uniform
+#pragma unroll
+          for (int i = 0; i < M; ++i) p = mma(row_frag(sK + (16 * (j0 + j) + l16) * LK + 32 * i + 8 * g), qf[i], p);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = 16 * (j0 + j) + 4 * g + r;
+            p[r] = key > 16 * rt + l16 ? 0.f : p[r] * (exp64(ci - sc[key]) * A.scale);
+          }
+        }
+        T* const at = sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g);
+        const Quad<T> hi = quad(p, T());
+        *reinterpret_cast<Quad<T>*>(at) = hi;
+        if constexpr (kTerms<T> == 2) store4(at + kC * LP, p - unquad(hi));
+      }
+    }
+    frag vf[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
+    float sick = 0.f;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
+      const f32x4 bv = *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);
+      X[it] = bv * (half_of(vf[it >> 1], it & 1) - yv * X[it]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sick = fmaf(X[it][r], 0.f, sick);
+    }
+    // An infinity or nan in row j: in the products below a zero of a later column would still meet it and
+    // leave nan in earlier rows.  From row j on the column's outputs and its state are nan; the rows before
+    // it are computed without.
+    int ill = kC;                                   // the column's first such row
+    if (__any(sick != sick)) {
+#pragma unroll
+      for (int it = 3; it >= 0; --it)
+#pragma unroll
+        for (int r = 3; r >= 0; --r)
+          if (!(fabsf(X[it][r]) < __builtin_huge_valf())) ill = 16 * it + 4 * g + r;
+      ill = min(ill, __shfl_xor(ill, 16));
+      ill = min(ill, __shfl_xor(ill, 32));
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * it + 4 * g + r >= ill) X[it][r] = 0.f;
+    }
+    {
+      Op<T> xf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_terms(X[2 * i], X[2 * i + 1], xf[i]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        U[it] = zero4();
+#pragma unroll
+        for (int i = 0; i <= it >> 1; ++i) U[it] = mul<T>(inv[inv_frag(it, i)], xf[i], U[it]);
+      }
+    }
+    const bool any_ill = __any(ill < kC);
+    if (any_ill) {                                  // (rows of an inverse may be nan from a key on)
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * it + 4 * g + r >= ill) U[it][r] = 0.f;
+    }
+    if (c + 1 < behind) fetch_inv(c + 1);
+    f32x4 o[4];
+    if constexpr (kOut) {
+      Op<T> uf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
+      __syncthreads();                              // P is there
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        o[it] = zero4();
+#pragma unroll
+        for (int i = 0; i < M; ++i) o[it] = mul<T>(sf[i], row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g), o[it]);
+        o[it] *= vec[16 * it + l16] * A.scale;
+#pragma unroll
+        for (int i = 0; i <= it >> 1; ++i) {
+          Op<T> pf;
+#pragma unroll
+          for (int t = 0; t < kTerms<T>; ++t)
+            pf.t[t] = row_frag(sP + (t * kC + 16 * it + l16) * LP + 32 * i + 8 * g);
+          o[it] = mul<T>(uf[i], pf, o[it]);
+        }
+      }
+      if (any_ill) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = __shfl(ill, 4 * g + r);
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+            if (16 * it + l16 >= at) o[it][r] = __builtin_nanf("");
+        }
+      }
+      if (live_col)
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+          if (16 * it + l16 < n) *reinterpret_cast<Quad<T>*>(po + 16 * it * A.so[1]) = quad(o[it], T());
+      po += kC * A.so[1];
+    }
+    {
+      const float whole = vec[kC - 1];
+      Op<T> uf[2];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) U[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        S[i] *= whole;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) S[i] = mul<T>(split_column_frag<LK>(sK + 32 * j * LK, i, lane), uf[j], S[i]);
+      }
+      if (any_ill && ill < kC)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) S[i] = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+    }
+  }
+
+  float* dst = kSums ? (unit_matrix ? A.trans + ((long long)slot * m.H + h) * m.dk * m.dk
+                                    : A.sums + ((long long)slot * m.H + h) * SE)
+               : kOut && last_seg && A.fin ? A.fin + st_off : nullptr;
+  if (!dst || col >= cols) return;
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (16 * i + 4 * g + r < m.dk) dst[(long long)(16 * i + 4 * g + r) * cols + col] = S[i][r];
+}
+
+// ---- joining segments ---------------------------------------------------------------------------
+// Per (sequence, head) and 64 columns, over the segments in order: E_{j+1} = M_j E_j + N_j; the sum in slot
+// j is replaced by the entry state E_j.  Backward also in reversed time: D_{j-1} = M_j^T D_j + N'_j, the
+// sum in slot j replaced by D_j, the gradient of the state behind the segment.  fp32 MFMA.
+template <int DK>
+__global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int blocks) {
+  constexpr int M = DK / 32, NS = DK / 16;
+  const DeltaMap& m = A.m;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15, w = tid >> 6;
+  unsigned x = blockIdx.x;                          // sequences: blockIdx.y
+  const int sub = int(x % (unsigned)blocks);
+  x /= (unsigned)blocks;
+  const int h = int(x % (unsigned)m.H);
+  const bool rev = x / (unsigned)m.H;
+  const int seq = blockIdx.y, SL = kC * m.L;
+  int slot = seq * m.n_seg, len = m.T;
+  if (m.packed) {
+    const int first = cu_at(m, seq);
+    slot = decay_first_slot(first, seq, SL);
+    len = max(cu_at(m, seq + 1) - first, 0);
+  }
+  const int n = (len + SL - 1) / SL;
+  const int col = 64 * sub + 16 * w + l16;
+  if (n < 2 || 64 * sub + 16 * w >= m.dv) return;
+  const long long SE = (long long)m.dk * m.dv, ME = (long long)m.dk * m.dk;
+  float* const sums = rev ? A.rsums : A.sums;
+  const float* given = rev ? A.dfin : A.init;
+  const bool live = col < m.dv;
+  f32x4 S[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * g + r;
+      S[i][r] = given && live && row < m.dk ? given[((long long)seq * m.H + h) * SE + (long long)row * m.dv + col] : 0.f;
+    }
+  for (int j = 0; j < n; ++j) {
+    const int seg = rev ? n - 1 - j : j;
+    const long long at = (long long)(slot + seg) * m.H + h;
+    float* const here = sums + at * SE;
+    const float* const tr = A.trans + at * ME;
+    f32x4 N[NS];
+    const bool more = j + 1 < n;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + 4 * g + r;
+        N[i][r] = 0.f;
+        if (live && row < m.dk) {
+          if (more) N[i][r] = here[(long long)row * m.dv + col];
+          here[(long long)row * m.dv + col] = S[i][r];
+        }
+      }
+    if (!more) break;
+    if (j > 0 || given)                             // else S is zero, and the transition is not there
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+          f32x8 a;
+          const int row = 16 * i + l16;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int q = 32 * k + 16 * (r / 4) + 4 * g + r % 4;
+            a[r] = row < m.dk && q < m.dk ? tr[rev ? (long long)q * m.dk + row : (long long)row * m.dk + q] : 0.f;
+          }
+          N[i] = mma(a, pack_frag(S[2 * k], S[2 * k + 1], float()), N[i]);
+        }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) S[i] = N[i];
+  }
+}
+
+// ---- recurrent form ------------------------------------------------------------------------
+// One workgroup per (column block, head, sequence) keeps its part of the state in registers over the call's
+// tokens: thread (row group, lane group) has 4 neighbouring columns of the rows row group + RG i.  Both
+// products with the state are taken of the one before the token, in one pass over the rows:
+//   a = S^T k, z = S^T q, u = b (v - g a), o = scale (g z + (q . k) u), S <- g S + k u^T.
+struct TokenArgs {
+  int T, H, share, dk, dv;
+  long long sq[3], sk[3], sv[3], so[3], sb[3], sl[3];
+  float scale;
+};
+
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load4(const __bf16* p) { return unquad(*reinterpret_cast<const uint2*>(p)); }
+
+template <typename T, int LC, int RI>
+__global__ __launch_bounds__(kThreads) void delta_decode_kernel(
+    TokenArgs A, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+    const T* __restrict__ beta, const float* __restrict__ log_decay, float* __restrict__ state, T* __restrict__ o) {
+  constexpr int RG = kThreads / LC;
+  __shared__ f32x4 part[2][4][2][LC];
+  __shared__ float dots[2][4];
+  const int tid = threadIdx.x, rg = tid / LC, col = 4 * (blockIdx.x * LC + tid % LC);
+  const int h = blockIdx.y, b = blockIdx.z, w = tid >> 6, hk = h / A.share;
+  const bool live = col < A.dv;
+  float* st = state + ((long long)b * A.H + h) * A.dk * A.dv + col;
+  f32x4 S[RI];
+#pragma unroll
+  for (int i = 0; i < RI; ++i) {
+    const int row = rg + RG * i;
+    S[i] = zero4();
+    if (live && row < A.dk) S[i] = load4(st + row * A.dv);
+  }
+  for (int t = 0; t < A.T; ++t) {
+    const T* qt = q + row_off(A.sq, b, t, hk);
+    const T* kt = k + row_off(A.sk, b, t, hk);
+    const f32x4 vt = live ? load4(v + row_off(A.sv, b, t, h) + col) : zero4();
+    const float bt = to_f32(beta[row_off(A.sb, b, t, h)]);
+    const float gt = log_decay ? expf(log_decay[row_off(A.sl, b, t, h)]) : 1.f;
+    f32x4 a = zero4(), z = zero4();
+    float kr[RI], qk = 0.f;
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      const int row = rg + RG * i;
+      kr[i] = 0.f;
+      if (row < A.dk) {
+        kr[i] = to_f32(kt[row]);
+        const float qr = to_f32(qt[row]);
+        qk = fmaf(qr, kr[i], qk);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          a[r] = fmaf(kr[i], S[i][r], a[r]);
+          z[r] = fmaf(qr, S[i][r], z[r]);
+        }
+      }
+    }
+#pragma unroll
+    for (int s = LC; s < 64; s <<= 1) {
+      qk += __shfl_xor(qk, s);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        a[r] += __shfl_xor(a[r], s);
+        z[r] += __shfl_xor(z[r], s);
+      }
+    }
+    const int p = t & 1;                            // two buffers: one barrier a token
+    if ((tid & 63) < LC) {
+      part[p][w][0][tid % LC] = a;
+      part[p][w][1][tid % LC] = z;
+      if ((tid & 63) == 0) dots[p][w] = qk;
+    }
+    __syncthreads();
+    a = part[p][0][0][tid % LC] + part[p][1][0][tid % LC] + part[p][2][0][tid % LC] + part[p][3][0][tid % LC];
+    const f32x4 u = bt * (vt - gt * a);
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = fmaf(kr[i], u[r], gt * S[i][r]);
+    if (tid < LC && live) {
+      z = part[p][0][1][tid] + part[p][1][1][tid] + part[p][2][1][tid] + part[p][3][1][tid];
+      qk = dots[p][0] + dots[p][1] + dots[p][2] + dots[p][3];
+      store4(o + row_off(A.so, b, t, h) + col, A.scale * (gt * z + qk * u));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RI; ++i) {
+    const int row = rg + RG * i;
+    if (live && row < A.dk) *reinterpret_cast<f32x4*>(st + row * A.dv) = S[i];
+  }
+}
+
+template <typename F>
+hipError_t with_lds(F kernel, int bytes) {
+  return ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes);
+}
+
+template <typename T, int DK>
+hipError_t launch_prep_t(const DeltaArgs& a, bool backward, hipStream_t st) {
+  using TL = PrepTiles<T, DK>;
+  hipError_t e = with_lds(delta_prep_kernel<T, DK>, TL::bytes);
+  if (e != hipSuccess) return e;
+  launch_kernel(delta_prep_kernel<T, DK>, grid_rows((long long)a.m.c_slots * a.m.H), kThreads, TL::bytes, st, a,
+                backward ? 1 : 0);
+  return hipGetLastError();
+}
+
+template <typename T, int DK, int W, Walk kWhat>
+hipError_t launch_walk_t(const DeltaArgs& a, bool backward, hipStream_t st) {
+  using TL = WalkTiles<T, DK, W, kWhat == Walk::output>;
+  hipError_t e = with_lds(delta_walk_kernel<T, DK, W, kWhat>, TL::bytes);
+  if (e != hipSuccess) return e;
+  const int blocks = (a.m.dv + 16 * W - 1) / (16 * W) + (kWhat == Walk::sums ? (a.m.dk + 16 * W - 1) / (16 * W) : 0);
+  const long long units = (long long)a.m.n_slots * a.m.H;
+  launch_kernel(delta_walk_kernel<T, DK, W, kWhat>, grid_rows((units + 7) / 8 * 8 * blocks), 64 * W, TL::bytes, st, a,
+                blocks, backward ? 1 : 0);
+  return hipGetLastError();
+}
+
+template <Walk kWhat>
+hipError_t launch_walk_d(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st) {
+  const int dk = a.m.dk;
+  if (!bf16) return dk <= 32 ? launch_walk_t<float, 32, 4, kWhat>(a, backward, st)
+                  : dk <= 64 ? launch_walk_t<float, 64, 4, kWhat>(a, backward, st)
+                             : launch_walk_t<float, 128, 4, kWhat>(a, backward, st);
+  if (decay_columns(true, a.m.dv) == 128)
+    return dk <= 64 ? launch_walk_t<__bf16, 64, 8, kWhat>(a, backward, st)
+                    : launch_walk_t<__bf16, 128, 8, kWhat>(a, backward, st);
+  return dk <= 32 ? launch_walk_t<__bf16, 32, 4, kWhat>(a, backward, st)
+         : dk <= 64 ? launch_walk_t<__bf16, 64, 4, kWhat>(a, backward, st)
+                    : launch_walk_t<__bf16, 128, 4, kWhat>(a, backward, st);
+}
+
+}  // namespace
+
+hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st) {
+  const int dk = a.m.dk;
+  if (bf16) return dk <= 32 ? launch_prep_t<__bf16, 32>(a, backward, st)
+                 : dk <= 64 ? launch_prep_t<__bf16, 64>(a, backward, st) : launch_prep_t<__bf16, 128>(a, backward, st);
+  return dk <= 32 ? launch_prep_t<float, 32>(a, backward, st)
+         : dk <= 64 ? launch_prep_t<float, 64>(a, backward, st) : launch_prep_t<float, 128>(a, backward, st);
+}
+
+hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st) {
+  return launch_walk_d<Walk::sums>(a, bf16, backward, st);
+}
+
+hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, hipStream_t st) {
+  return launch_walk_d<Walk::output>(a, bf16, false, st);
+}
+
+hipError_t launch_delta_join(const DeltaArgs& a, bool backward, hipStream_t st) {
+  const int blocks = (a.m.dv + 63) / 64;
+  const dim3 grid(blocks * a.m.H * (backward ? 2 : 1), a.m.n_seq);
+  if (a.m.dk <= 32) launch_kernel(delta_join_kernel<32>, grid, kThreads, 0, st, a, blocks);
+  else if (a.m.dk <= 64) launch_kernel(delta_join_kernel<64>, grid, kThreads, 0, st, a, blocks);
+  else launch_kernel(delta_join_kernel<128>, grid, kThreads, 0, st, a, blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_decode(const DeltaArgs& x, bool bf16, float* state, hipStream_t st) {
+  const DeltaMap& m = x.m;
+  TokenArgs a;
+  a.T = m.T; a.H = m.H; a.share = m.H / m.Hk; a.dk = m.dk; a.dv = m.dv; a.scale = x.scale;
+  for (int i = 0; i < 3; ++i) {
+    a.sq[i] = x.sq[i]; a.sk[i] = x.sk[i]; a.sv[i] = x.sv[i]; a.so[i] = x.so[i]; a.sb[i] = x.sb[i]; a.sl[i] = x.sl[i];
+  }
+  constexpr int LC = 16, kMost = 65535;             // sequences that a grid axis holds
+  auto run = [&](auto t, auto ri) {
+    using T_ = decltype(t);
+    hipError_t e = hipSuccess;
+    for (long long b = 0; b < m.n_seq && e == hipSuccess; b += kMost) {
+      const dim3 grid((m.dv + 4 * LC - 1) / (4 * LC), m.H, (unsigned)(m.n_seq - b < kMost ? m.n_seq - b : kMost));
+      launch_kernel(delta_decode_kernel<T_, LC, decltype(ri)::value>, grid, kThreads, 0, st, a,
+                    (const T_*)x.q + b * a.sq[0], (const T_*)x.k + b * a.sk[0], (const T_*)x.v + b * a.sv[0],
+                    (const T_*)x.beta + b * a.sb[0], x.log_decay ? x.log_decay + b * a.sl[0] : nullptr,
+                    state + b * m.H * m.dk * m.dv, (T_*)x.o + b * a.so[0]);
+      e = hipGetLastError();
+    }
+    return e;
+  };
+  auto rows = [&](auto t) {
+    if (m.dk <= 32) return run(t, std::integral_constant<int, 2>());
+    if (m.dk <= 64) return run(t, std::integral_constant<int, 4>());
+    return run(t, std::integral_constant<int, 8>());
+  };
+  return bf16 ? rows(__bf16()) : rows(float());
+}
+
+}  // namespace kata

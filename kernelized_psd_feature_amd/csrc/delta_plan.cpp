@@ -1,0 +1,110 @@
+// Host-side argument validation and launch planning of the gated delta rule (pure C++, no HIP).
+#include "delta_plan.h"
+
+#include <algorithm>
+#include <cmath>
+
+#include "decay_slots.h"
+#include "layer_plan.h"
+#include "plan.h"
+
+namespace kata {
+
+namespace {
+
+kata_status fail(std::string* why, kata_status s, const std::string& msg) {
+  if (why) *why = msg;
+  return s;
+}
+
+// most: sequences that the form takes.
+kata_status check_delta_problem(const kata_delta_problem* pr, int most, bool backward, std::string* why) {
+  if (!pr) return fail(why, KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
+  if (pr->n_seq < 1 || pr->H < 1 || pr->Hk < 1 || pr->T < 1)
+    return fail(why, KATA_ERR_INVALID_ARGUMENT, "n_seq, H, Hk and T must be >= 1");
+  if (pr->T > kMaxT) return fail(why, KATA_ERR_UNSUPPORTED, "T exceeds 2^26");
+  if (pr->n_seq > most || pr->H > kDecayMaxHeads)
+    return fail(why, KATA_ERR_UNSUPPORTED, "n_seq or H exceeds 65535");
+  if (pr->H % pr->Hk) return fail(why, KATA_ERR_INVALID_ARGUMENT, "H must be a multiple of Hk");
+  if (pr->dtype != KATA_F32 && pr->dtype != KATA_BF16)
+    return fail(why, KATA_ERR_INVALID_ARGUMENT, "dtype must be fp32 or bf16");
+  if (pr->packed != 0 && pr->packed != 1)
+    return fail(why, KATA_ERR_INVALID_ARGUMENT, "packed must be 0 or 1");
+  if (pr->dk < 1 || pr->dv < 1)
+    return fail(why, KATA_ERR_INVALID_ARGUMENT, "dk and dv must be >= 1");
+  const int V = pr->dtype == KATA_BF16 ? 8 : 4;
+  if (pr->dk > kDecayMaxWidth || pr->dv > kDecayMaxWidth || pr->dk % V || pr->dv % V)
+    return fail(why, KATA_ERR_UNSUPPORTED,
+                "dk and dv must be at most 128 and a multiple of 16 bytes");
+  if (!std::isfinite(pr->scale)) return fail(why, KATA_ERR_INVALID_ARGUMENT, "scale must be finite");
+  const int64_t B = pr->packed ? 1 : pr->n_seq;
+  const int64_t sizes[3] = {B, pr->T, pr->H}, shared[3] = {B, pr->T, pr->Hk};
+  kata_status s;
+  if ((s = check_strides("q", pr->sq, shared, pr->dk, false, why)) != KATA_OK) return s;
+  if ((s = check_strides("k", pr->sk, shared, pr->dk, false, why)) != KATA_OK) return s;
+  if ((s = check_strides("v", pr->sv, sizes, pr->dv, false, why)) != KATA_OK) return s;
+  if ((s = check_strides("beta", pr->sbeta, sizes, 1, false, why)) != KATA_OK) return s;
+  if ((s = check_strides("log_decay", pr->sdecay, sizes, 1, false, why)) != KATA_OK) return s;
+  if (backward) return check_strides("dO", pr->sdo, sizes, pr->dv, false, why);
+  return check_strides("o", pr->so, sizes, pr->dv, true, why);
+}
+
+constexpr size_t kVecBytes = 1280, kInvBytes = 12288;   // of a chunk and head (delta_tiles.h)
+
+}  // namespace
+
+kata_status validate_delta(const kata_delta_problem* pr, bool backward, std::string* why) {
+  return check_delta_problem(pr, kDecayMaxSeqs, backward, why);
+}
+
+kata_status validate_delta_decode(const kata_delta_problem* pr, std::string* why) {
+  const kata_status s = check_delta_problem(pr, INT32_MAX, false, why);
+  if (s == KATA_OK && pr->packed) return fail(why, KATA_ERR_INVALID_ARGUMENT, "decode takes no packed sequences");
+  return s;
+}
+
+DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
+  DeltaPlan p;
+  const bool bf16 = pr->dtype == KATA_BF16;
+  const int64_t chunks = (int64_t(pr->T) + kDecayChunk - 1) / kDecayChunk;
+  const int cols = decay_columns(bf16, pr->dv);
+  const int64_t v_blocks = (pr->dv + cols - 1) / cols, k_blocks = (pr->dk + cols - 1) / cols;
+  // segments that a sequence (packed: all tokens together) is cut into to fill the card
+  const int64_t units = pr->H * v_blocks * (backward ? 2 : 1) * (pr->packed ? 1 : pr->n_seq);
+  const int64_t want = std::max<int64_t>(1, 512 / units);
+  const int64_t L = chunks <= 8 ? chunks : std::max<int64_t>(4, (chunks + want - 1) / want);
+  p.L = int(L);
+  p.n_chunks = int(chunks);
+  const int64_t SL = L * kDecayChunk;
+  p.n_seg = int((chunks + L - 1) / L);
+  p.n_slots = pr->packed ? decay_slot_count(pr->T, pr->n_seq, int(SL)) : pr->n_seq * p.n_seg;
+  p.c_slots = pr->packed ? decay_slot_count(pr->T, pr->n_seq, kDecayChunk) : int(std::min<int64_t>(pr->n_seq * chunks, INT32_MAX));
+  const int64_t H = pr->H;
+  p.groups = std::max<int64_t>((pr->packed ? int64_t(p.c_slots) : pr->n_seq * chunks) * H,
+                               (int64_t(p.n_slots) * H + 7) / 8 * 8 * (2 * v_blocks + k_blocks));
+  size_t at = 0;
+  const auto part = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) & ~size_t(255);
+    return here;
+  };
+  const size_t c = size_t(p.c_slots) * H, s = size_t(p.n_slots) * H, state = size_t(pr->dk) * pr->dv * 4;
+  p.vec = part(c * kVecBytes);
+  p.inv = part(c * kInvBytes);
+  if (p.n_seg > 1) {
+    p.sums = part(s * state);
+    p.trans = part(s * pr->dk * pr->dk * 4);
+  }
+  if (backward) {
+    if (p.n_seg > 1) p.rsums = part(s * state);
+    p.inv_t = part(c * kInvBytes);
+    const size_t DK = pr->dk <= 32 ? 32 : pr->dk <= 64 ? 64 : 128;
+    const size_t chunk_state = DK * 16 * ((pr->dv + 15) / 16) * 4;
+    p.cstates = part(c * chunk_state);
+    p.rstates = part(c * chunk_state);
+  }
+  p.bytes = at;
+  return p;
+}
+
+}  // namespace kata

@@ -16,26 +16,6 @@ kata_status fail(std::string* why, kata_status s, const std::string& msg) {
   return s;
 }
 
-// Strides of a [B][T][H][width] tensor: none negative, the addressed extent below 2^60 elements.
-// An input may repeat its rows (a stride of zero, a broadcast axis); an output may not.
-kata_status check_strides(const char* name, const int64_t st[3], const int64_t sizes[3], int64_t width,
-                          bool output, std::string* why) {
-  const int64_t kMax = int64_t(1) << 60;
-  int64_t extent = width;
-  for (int a = 0; a < 3; ++a) {
-    const int64_t s = sizes[a] > 1 ? st[a] : 0;
-    if (s < 0) return fail(why, KATA_ERR_INVALID_ARGUMENT, std::string(name) + ": negative stride");
-    if (sizes[a] > 1 && s < width && (output || s != 0))
-      return fail(why, KATA_ERR_INVALID_ARGUMENT,
-                  std::string(name) + ": stride smaller than the row length");
-    if (sizes[a] > 1 && s > (kMax - extent) / (sizes[a] - 1))
-      return fail(why, KATA_ERR_INVALID_ARGUMENT,
-                  std::string(name) + ": strides address more than 2^60 elements");
-    if (sizes[a] > 1) extent += (sizes[a] - 1) * s;
-  }
-  return KATA_OK;
-}
-
 // most: sequences that the form takes.
 kata_status check_decay_problem(const kata_decay_problem* pr, int most, bool backward, std::string* why) {
   if (!pr) return fail(why, KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
@@ -66,6 +46,24 @@ kata_status check_decay_problem(const kata_decay_problem* pr, int most, bool bac
 }
 
 }  // namespace
+
+kata_status check_strides(const char* name, const int64_t st[3], const int64_t sizes[3], int64_t width,
+                          bool output, std::string* why) {
+  const int64_t kMax = int64_t(1) << 60;
+  int64_t extent = width;
+  for (int a = 0; a < 3; ++a) {
+    const int64_t s = sizes[a] > 1 ? st[a] : 0;
+    if (s < 0) return fail(why, KATA_ERR_INVALID_ARGUMENT, std::string(name) + ": negative stride");
+    if (sizes[a] > 1 && s < width && (output || s != 0))
+      return fail(why, KATA_ERR_INVALID_ARGUMENT,
+                  std::string(name) + ": stride smaller than the row length");
+    if (sizes[a] > 1 && s > (kMax - extent) / (sizes[a] - 1))
+      return fail(why, KATA_ERR_INVALID_ARGUMENT,
+                  std::string(name) + ": strides address more than 2^60 elements");
+    if (sizes[a] > 1) extent += (sizes[a] - 1) * s;
+  }
+  return KATA_OK;
+}
 
 kata_status validate_rows(const void* p, const int64_t st[3], const int64_t sizes[3], size_t esize,
                           const char* name, std::string* why) {

@@ -27,6 +27,10 @@ struct DecayPlan {
   size_t role_bytes = 0;                  // workspace of one role's segment states
 };
 
+// Strides of a [B][T][H][width] tensor: none negative, the addressed extent below 2^60 elements.
+// An input may repeat its rows (a stride of zero, a broadcast axis); an output may not.
+kata_status check_strides(const char* name, const int64_t st[3], const int64_t sizes[3], int64_t width,
+                          bool output, std::string* why);
 kata_status validate_decay(const kata_decay_problem* pr, bool backward, std::string* why);
 kata_status validate_decay_decode(const kata_decay_problem* pr, std::string* why);
 // A tensor's pointer and (b, t, h) strides: 16-byte aligned rows.  The stride of an axis of one
