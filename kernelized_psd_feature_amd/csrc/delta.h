@@ -48,8 +48,10 @@ hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, bool backward, h
 // The sums become entry states.
 hipError_t launch_delta_join(const DeltaArgs& a, bool backward, hipStream_t st);
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, hipStream_t st);
-// Backward: the states before and the gradients of the states behind every chunk.
-hipError_t launch_delta_bwd_walk(const DeltaArgs& a, bool bf16, hipStream_t st);
+// Backward: the states before every chunk (cstates); in reversed time the gradients of the states behind
+// them (rstates), or of the segments the sums (rsums); and then the gradients.
+hipError_t launch_delta_states(const DeltaArgs& a, bool bf16, hipStream_t st);
+hipError_t launch_delta_reverse(const DeltaArgs& a, bool bf16, bool sums, hipStream_t st);
 hipError_t launch_delta_grads(const DeltaArgs& a, bool bf16, hipStream_t st);
 hipError_t launch_delta_decode(const DeltaArgs& a, bool bf16, float* state, hipStream_t st);
 

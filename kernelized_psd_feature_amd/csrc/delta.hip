@@ -705,6 +705,10 @@ hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, hipStream_t st) {
   return launch_walk_d<Walk::output>(a, bf16, false, st);
 }
 
+hipError_t launch_delta_states(const DeltaArgs& a, bool bf16, hipStream_t st) {
+  return launch_walk_d<Walk::states>(a, bf16, true, st);
+}
+
 hipError_t launch_delta_join(const DeltaArgs& a, bool backward, hipStream_t st) {
   const int blocks = (a.m.dv + 63) / 64;
   const dim3 grid(blocks * a.m.H * (backward ? 2 : 1), a.m.n_seq);

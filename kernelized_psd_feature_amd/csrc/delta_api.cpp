@@ -112,6 +112,7 @@ kata_status run_before(const kata::DeltaArgs& a, bool bf16, bool backward, hipSt
     Timed t(KATA_K_CHUNK_STATE, st);
     hipError_t e = kata::launch_delta_prep(a, bf16, backward, st);
     if (e == hipSuccess && a.m.n_seg > 1) e = kata::launch_delta_segments(a, bf16, backward, st);
+    if (e == hipSuccess && a.m.n_seg > 1 && backward) e = kata::launch_delta_reverse(a, bf16, true, st);
     if (e != hipSuccess) return launch_status(e, what);
   }
   if (a.m.n_seg < 2) return KATA_OK;
@@ -155,6 +156,54 @@ kata_status kata_fwd_delta(const kata_delta_problem* pr, const void* q, const vo
   if ((s = run_before(a, bf16, false, st, "gated delta rule")) != KATA_OK) return s;
   Timed t(KATA_K_CHUNK_OUTPUT, st);
   return launch_status(kata::launch_delta_walk(a, bf16, st), "gated delta rule");
+}
+
+size_t kata_bwd_delta_workspace_size(const kata_delta_problem* pr) {
+  if (kata::validate_delta(pr, true, nullptr) != KATA_OK) return 0;
+  return kata::plan_delta(pr, true).bytes;
+}
+
+kata_status kata_bwd_delta(const kata_delta_problem* pr, const void* q, const void* k, const void* v,
+                           const void* beta, const float* log_decay, const void* dO, const int32_t* cu_seqlens,
+                           const float* initial_state, const float* dfinal_state, void* dq, void* dk, void* dv,
+                           void* dbeta, float* dlog_decay, float* dinitial_state, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  clear_error();
+  if (!pr) return set_error(KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
+  const int64_t T = pr->T, H = pr->H, Hk = pr->Hk;
+  const int64_t gk[3] = {T * Hk * pr->dk, Hk * pr->dk, pr->dk}, gv[3] = {T * H * pr->dv, H * pr->dv, pr->dv};
+  const Named ts[] = {{q, pr->sq, "q", 1}, {k, pr->sk, "k", 1}, {v, pr->sv, "v", 0}, {dO, pr->sdo, "dO", 0},
+                      {dq, gk, "dq", 1},   {dk, gk, "dk", 1},   {dv, gv, "dv", 0}};
+  kata_status s = check_delta(pr, Form::backward, ts, 7, beta, log_decay, cu_seqlens);
+  if (s != KATA_OK) return s;
+  if (!dbeta) return set_error(KATA_ERR_INVALID_ARGUMENT, "dbeta is null");
+  if ((s = need_aligned(dbeta, kata::elem_size(pr->dtype), "dbeta")) != KATA_OK) return s;
+  if ((s = need_aligned(dlog_decay, 4, "dlog_decay")) != KATA_OK) return s;
+  if ((s = need_aligned(initial_state, 16, "initial_state")) != KATA_OK) return s;
+  if ((s = need_aligned(dfinal_state, 16, "dfinal_state")) != KATA_OK) return s;
+  if ((s = need_aligned(dinitial_state, 16, "dinitial_state")) != KATA_OK) return s;
+  const kata::DeltaPlan p = kata::plan_delta(pr, true);
+  if ((s = check_grid(p)) != KATA_OK) return s;
+  if ((s = check_workspace(workspace, ws_bytes, p.bytes)) != KATA_OK) return s;
+  if (states_overlap(pr, dinitial_state, initial_state) || states_overlap(pr, dinitial_state, dfinal_state))
+    return set_error(KATA_ERR_INVALID_ARGUMENT, "dinitial_state overlaps initial_state or dfinal_state");
+  if ((s = check_device()) != KATA_OK) return s;
+  kata::DeltaArgs a = delta_args(pr, q, k, v, beta, log_decay, cu_seqlens);
+  place(a, p, workspace);
+  a.dO = dO;
+  a.init = initial_state;
+  a.dfin = dfinal_state;
+  a.dinit = dinitial_state;
+  a.dq = dq; a.dk = dk; a.dv = dv; a.dbeta = dbeta; a.dlog = dlog_decay;
+  const bool bf16 = pr->dtype == KATA_BF16;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const char* what = "gated delta rule backward";
+  if ((s = run_before(a, bf16, true, st, what)) != KATA_OK) return s;
+  Timed t(KATA_K_BWD, st);
+  hipError_t e = kata::launch_delta_states(a, bf16, st);
+  if (e == hipSuccess) e = kata::launch_delta_reverse(a, bf16, false, st);
+  if (e == hipSuccess) e = kata::launch_delta_grads(a, bf16, st);
+  return launch_status(e, what);
 }
 
 kata_status kata_decode_delta(const kata_delta_problem* pr, const void* q, const void* k, const void* v,

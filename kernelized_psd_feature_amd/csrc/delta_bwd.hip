@@ -1,0 +1,682 @@
+// Gradients of the gated delta rule (delta.hip), gfx950.
+//
+// With the notation there, S the state before a chunk and D the gradient of the one behind it:
+//   Z = P^T dO scale + diag(exp(c_63 - c)) K D          (the gradient of U)
+//   X = (I + A)^-T Z,  dv = diag(b) X
+//   the gradient of S:  y_63 D + scale (diag(y) Q)^T dO - (diag(y) K)^T dv
+//   dbeta_i = X_i . U_i / b_i
+//   dlog_t = sum_{i >= t in the chunk} (dO_i . o_i - dv_i . v_i) + <D, S'>,  S' the state behind the chunk
+//   PO_ij = scale exp(c_i - c_j) (dO_i . u_j) for j <= i,  PV_ij = -exp(c_i - c_j) (dv_i . u_j) for j < i
+//   dq = scale diag(y) dO S^T + PO K
+//   dk = diag(exp(c_63 - c)) U D^T - diag(y) dv S^T + PO^T Q + PV^T K + PV K
+// (the second last line but two: what S_t loses or gains from token t on is known from its products with
+// the gradients, d<dS_t, S_t> = dv_t . v_t - dO_t . o_t.)
+//
+// S and D of every chunk come from two walks like the forward pass's, one of them in reversed time, which
+// keep nothing else; all the rest is then computed for all chunks at once (delta_grads_kernel).
+#include <type_traits>
+
+#include "delta.h"
+#include "delta_tiles.h"
+#include "device.h"
+#include "mfma_util.h"
+
+namespace kata {
+namespace {
+
+constexpr int kThreads = 256;             // of the gradients' kernel
+
+// A strip of P for one wave: row tile rt, J key tiles from j0 on, times `scale`; zero by selection where the
+// key is later.  Rows of split places, the second term kC rows behind.
+template <typename T, int DK, int LK, int LP, int J>
+__device__ __forceinline__ void put_scores(T* sP, const T* sQ, const T* sK, const double* sc, int rt, int j0, int lane,
+                                           float scale) {
+  constexpr int M = DK / 32;
+  const int g = lane >> 4, l16 = lane & 15;
+  typename Elem<T>::frag qf[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) qf[i] = row_frag(sQ + (16 * rt + l16) * LK + 32 * i + 8 * g);
+  const double ci = sc[16 * rt + l16];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    f32x4 p = zero4();
+    if (j0 + j <= rt) {                             // uniform
+#pragma unroll
+      for (int i = 0; i < M; ++i) p = mma(row_frag(sK + (16 * (j0 + j) + l16) * LK + 32 * i + 8 * g), qf[i], p);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int key = 16 * (j0 + j) + 4 * g + r;
+        p[r] = key > 16 * rt + l16 ? 0.f : p[r] * (exp64(ci - sc[key]) * scale);
+      }
+    }
+    T* const at = sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g);
+    const Quad<T> hi = quad(p, T());
+    *reinterpret_cast<Quad<T>*>(at) = hi;
+    if constexpr (kTerms<T> == 2) store4(at + kC * LP, p - unquad(hi));
+  }
+}
+
+// ---- the walk in reversed time ------------------------------------------------------------------
+template <typename T, int DK, int W>
+struct ReverseTiles {
+  static constexpr bool kBf = sizeof(T) == 2;
+  static constexpr int DV = 16 * W;
+  static constexpr int LK = DK + 16 / (int)sizeof(T), LV = DV + (kBf ? 16 : 4), LP = kC + 16 / (int)sizeof(T);
+  static constexpr int kHead = 16 + kDeltaVec * 4;
+  static constexpr int kTiles = kC * (2 * LK + LV);
+  static constexpr int bytes = kHead + (kTiles + kTerms<T> * kC * LP) * (int)sizeof(T);
+};
+
+// kSums: of the segments, from a gradient of zero behind them.
+template <typename T, int DK, int W, bool kSums>
+__global__ __launch_bounds__(64 * W) void delta_reverse_kernel(DeltaArgs A, int blocks) {
+  using TL = ReverseTiles<T, DK, W>;
+  using frag = typename Elem<T>::frag;
+  constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
+  extern __shared__ __align__(16) char lds[];
+  int* const sh = reinterpret_cast<int*>(lds);
+  float* const vec = reinterpret_cast<float*>(lds + 16);
+  const double* const sc = reinterpret_cast<const double*>(vec + 3 * kC);
+  T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
+  T* const sQ = sK + kC * LK;
+  T* const sO = sQ + kC * LK;
+  T* const sP = sO + kC * LV;
+
+  const DeltaMap& m = A.m;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned x = block_number(), per = blocks, y = x / 8 / per, unit = 8 * y + x % 8;
+  const int sub = int(x / 8 - y * per);
+  if (unit >= (unsigned)m.n_slots * (unsigned)m.H) return;
+  const int slot = int(unit / (unsigned)m.H), h = int(unit - (unsigned)slot * (unsigned)m.H);
+  const int c0 = sub * DV;
+  DeltaPart s;
+  if (!find_part(m, slot, m.L, m.n_seg, m.n_slots, sh, s) || s.seq == m.n_seq) return;
+  const int L = m.L, n_chunks = (s.len + kC - 1) / kC, n_seg = (n_chunks + L - 1) / L;
+  const long long SE = (long long)m.dk * m.dv, st_off = ((long long)s.seq * m.H + h) * SE;
+  if (s.part >= n_seg) {
+    if (!kSums && s.len == 0 && s.part == 0 && A.dinit)   // an empty sequence
+      for (int i = tid; i < m.dk * DV; i += kThr) {
+        const int r = i / DV, c = c0 + i % DV;
+        if (c < m.dv) A.dinit[st_off + (long long)r * m.dv + c] = A.dfin ? A.dfin[st_off + (long long)r * m.dv + c] : 0.f;
+      }
+    return;
+  }
+  if (kSums && s.part == 0) return;                 // enters no other segment
+  const bool last_seg = s.part == n_seg - 1;
+  const int first = s.part * L, behind = min(first + L, n_chunks);
+  const int n_last = min(kC, s.len - kC * (behind - 1));
+  const int hk = h / (m.H / m.Hk);
+  const long long row0 = s.start + (long long)kC * (behind - 1);
+  // (Stage steps to the next chunk by 64 rows; here the next one is the one before)
+  const T* pk = reinterpret_cast<const T*>(A.k) + s.b * A.sk[0] + row0 * A.sk[1] + hk * A.sk[2];
+  const T* pq = reinterpret_cast<const T*>(A.q) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2];
+  const T* px = reinterpret_cast<const T*>(A.dO) + s.b * A.sdo[0] + row0 * A.sdo[1] + h * A.sdo[2] + c0;
+  Stage<T, DK, kThr> rk(pk, A.sk[1], m.dk, true), rq(pq, A.sq[1], m.dk, true);
+  Stage<T, DV, kThr> ro(px, A.sdo[1], m.dv - c0, false);
+  uint4 vec_next;
+  const long long chunk0 = (long long)s.c_slot * m.H + h;              // [c_slots][H]
+  auto fetch = [&](int c) {
+    const int n = c == behind - 1 ? n_last : kC;
+    fetch_rows(rk, A.sk[1], n);
+    fetch_rows(rq, A.sq[1], n);
+    fetch_rows(ro, A.sdo[1], n);
+    rk.p -= 2 * kC * A.sk[1];
+    rq.p -= 2 * kC * A.sq[1];
+    ro.p -= 2 * kC * A.sdo[1];
+    if (tid < kDeltaVec / 4)
+      vec_next = reinterpret_cast<const uint4*>(A.vec + (chunk0 + (long long)c * m.H) * kDeltaVec)[tid];
+  };
+  Op<T> inv[kInvFrags];
+  auto fetch_inv = [&](int c) {
+    const T* at = reinterpret_cast<const T*>(A.inv_t) + (chunk0 + (long long)c * m.H) * kInvElems<T>;
+#pragma unroll
+    for (int f = 0; f < kInvFrags; ++f) load_inv<T>(at, f, lane, inv[f]);
+  };
+  fetch(behind - 1);
+  fetch_inv(behind - 1);
+
+  const int wc = 16 * w, col = c0 + wc + l16;
+  f32x4 D[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    D[i] = zero4();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * g + r;
+      if (!kSums && row < m.dk && col < m.dv) {
+        if (!last_seg) D[i][r] = A.rsums[((long long)slot * m.H + h) * SE + (long long)row * m.dv + col];
+        else if (A.dfin) D[i][r] = A.dfin[st_off + (long long)row * m.dv + col];
+      }
+    }
+  }
+  if (m.dk < DK || m.dv - c0 < DV) {
+    uint4* const z = reinterpret_cast<uint4*>(sK);
+    for (int i = tid; i < TL::kTiles * (int)sizeof(T) / 16; i += kThr) z[i] = uint4{0u, 0u, 0u, 0u};
+  }
+  for (int c = behind - 1; c >= first; --c) {
+    __syncthreads();                                // the last chunk's tiles have been read
+    rk.template put_split<LK>(sK);
+    rq.template put_split<LK>(sQ);
+    ro.template put<LV>(sO);
+    if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
+    if (c > first) fetch(c - 1);
+    __syncthreads();
+    if (!kSums && c0 / 16 + w < (m.dv + 15) / 16) {
+      float* dst = A.rstates + ((chunk0 + (long long)c * m.H) * ((m.dv + 15) / 16) + c0 / 16 + w) * (DK * 16) + lane * 4;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(dst + i * 256) = D[i];
+    }
+    put_scores<T, DK, LK, LP, 16 / W>(sP, sQ, sK, sc, w & 3, 16 / W * (w >> 2), lane, A.scale);
+    Op<T> df[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) split_terms(D[2 * i], D[2 * i + 1], df[i]);
+    f32x4 Z[4], X[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      Z[it] = zero4();
+#pragma unroll
+      for (int i = 0; i < M; ++i) Z[it] = mul<T>(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), df[i], Z[it]);
+      Z[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
+    }
+    frag of[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) of[i] = column_frag<LV>(sO + 32 * i * LV + wc, lane);
+    __syncthreads();                                // P is there
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int i = it >> 1; i < 2; ++i) {
+        Op<T> pf;
+#pragma unroll
+        for (int t = 0; t < kTerms<T>; ++t) pf.t[t] = split_column_frag<LP>(sP + (t * kC + 32 * i) * LP, it, lane);
+        Z[it] = mul<T>(pf, of[i], Z[it]);
+      }
+    Op<T> zf[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) split_terms(Z[2 * i], Z[2 * i + 1], zf[i]);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      X[it] = zero4();
+#pragma unroll
+      for (int i = it >> 1; i < 2; ++i) X[it] = mul<T>(inv[inv_t_frag(it, i)], zf[i], X[it]);
+    }
+    if (c > first) fetch_inv(c - 1);
+    Op<T> kw[2], qw[2];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
+      X[it] *= -yv * *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);
+      Z[it] = half_of(of[it >> 1], it & 1) * yv * A.scale;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      split_terms(X[2 * i], X[2 * i + 1], kw[i]);
+      split_terms(Z[2 * i], Z[2 * i + 1], qw[i]);
+    }
+    const float whole = vec[kC - 1];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      D[i] *= whole;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        D[i] = mul<T>(split_column_frag<LK>(sQ + 32 * j * LK, i, lane), qw[j], D[i]);
+        D[i] = mul<T>(split_column_frag<LK>(sK + 32 * j * LK, i, lane), kw[j], D[i]);
+      }
+    }
+  }
+  float* dst = kSums ? A.rsums + ((long long)slot * m.H + h) * SE : first == 0 && A.dinit ? A.dinit + st_off : nullptr;
+  if (!dst || col >= m.dv) return;
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (16 * i + 4 * g + r < m.dk) dst[(long long)(16 * i + 4 * g + r) * m.dv + col] = D[i][r];
+}
+
+// ---- the gradients ------------------------------------------------------------------------------
+// One workgroup of four waves for a chunk and a head of q and k, over the value heads that share it and
+// blocks of 64 value columns.  As in the walks a wave has 16 columns of S, D, U, X and dv; then these go
+// through LDS, [column][token] and [column][row of the state], and a wave has 16 tokens of dq and dk.
+template <typename T, int DK>
+struct GradTiles {
+  static constexpr bool kBf = sizeof(T) == 2;
+  static constexpr int PAD = 16 / (int)sizeof(T);
+  static constexpr int LK = DK + PAD, LO = 64 + PAD, LV = 64 + (kBf ? 16 : 4), LP = kC + PAD, LS = DK + PAD;
+  static constexpr int kHead = 16 + kDeltaVec * 4 + 2 * 4 * kC * 4 + 16;   // an int, vec, dots, sums of the waves
+  static constexpr int kStateTile = 64 * LS, kPair = 2 * 64 * LP;
+  // scores, then (bf16) the second terms of U and dv, or (fp32) the state, then PO and PV
+  static constexpr int kA = kBf || kPair > kStateTile ? kPair : kStateTile;
+  static constexpr int bytes = kHead + (kC * (2 * LK + LO) + kA + kPair + (kBf ? kStateTile : 0)) * (int)sizeof(T);
+  static_assert(64 * LV <= kPair, "V lies where U and dv come");
+};
+
+__device__ __forceinline__ float sum16(float x) {   // over the 16 lanes of a group
+#pragma unroll
+  for (int s = 1; s < 16; s <<= 1) x += __shfl_xor(x, s);
+  return x;
+}
+
+template <typename T, int DK>
+__global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void delta_grads_kernel(DeltaArgs A) {
+  using TL = GradTiles<T, DK>;
+  using frag = typename Elem<T>::frag;
+  constexpr int M = DK / 32, NS = DK / 16, LK = TL::LK, LO = TL::LO, LV = TL::LV, LP = TL::LP, LS = TL::LS;
+  constexpr bool kBf = TL::kBf;
+  extern __shared__ __align__(16) char lds[];
+  int* const sh = reinterpret_cast<int*>(lds);
+  float* const vec = reinterpret_cast<float*>(lds + 16);
+  const double* const sc = reinterpret_cast<const double*>(vec + 3 * kC);
+  float* const sE = vec + kDeltaVec;                // [4][64] dO . o - dv . v, then [4][64] X . U
+  float* const sF = sE + 2 * 4 * kC;                // [4] <D, S'>
+  T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
+  T* const sQ = sK + kC * LK;
+  T* const sO = sQ + kC * LK;
+  T* const sA = sO + kC * LO;
+  T* const sU = sA + TL::kA;                        // V, then U and dv
+  T* const sZ = sU + 64 * LP;
+  T* const sS = kBf ? sZ + 64 * LP : sA;
+
+  const DeltaMap& m = A.m;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned unit = block_number();
+  if (unit >= (unsigned)m.c_slots * (unsigned)m.Hk) return;
+  const int slot = int(unit / (unsigned)m.Hk), hk = int(unit - (unsigned)slot * (unsigned)m.Hk);
+  const int share = m.H / m.Hk;
+  DeltaPart s;
+  if (!find_part(m, slot, 1, m.n_chunks, m.c_slots, sh, s)) return;
+
+  T* const gq = reinterpret_cast<T*>(A.dq) + ((long long)s.b * m.T * m.Hk + hk) * m.dk;   // row stride Hk dk
+  T* const gk = reinterpret_cast<T*>(A.dk) + ((long long)s.b * m.T * m.Hk + hk) * m.dk;
+  const long long lead = (long long)s.b * m.T * m.H + hk * share;      // of [b][t][H], the first shared head
+  auto clear = [&](int from, int rows) {
+    for (long long i = tid; i < (long long)rows * (m.dk / 4); i += kThreads) {
+      const long long at = (from + i / (m.dk / 4)) * m.Hk * m.dk + i % (m.dk / 4) * 4;
+      store4(gq + at, zero4());
+      store4(gk + at, zero4());
+    }
+    const int per = share * m.dv / 4;
+    for (long long i = tid; i < (long long)rows * per; i += kThreads)
+      store4(reinterpret_cast<T*>(A.dv) + (lead + (from + i / per) * m.H) * m.dv + i % per * 4, zero4());
+    for (long long i = tid; i < (long long)rows * share; i += kThreads) {
+      const long long at = lead + (from + i / share) * m.H + i % share;
+      reinterpret_cast<T*>(A.dbeta)[at] = T(0.f);
+      if (A.dlog) A.dlog[at] = 0.f;
+    }
+  };
+  const int n = min(kC, s.len - kC * s.part);
+  if (s.seq == m.n_seq) {                           // rows behind the last sequence
+    if (n > 0) clear(s.start + kC * s.part, n);
+    return;
+  }
+  if (m.packed && s.seq == 0 && s.part == 0) clear(0, s.start);        // before the first
+  if (n <= 0) return;
+  const long long row0 = s.start + (long long)kC * s.part;
+  const int ct = (m.dv + 15) / 16, v_blocks = (m.dv + 63) / 64;
+
+  // tiles' columns that no operand has: zeros all along (V's place is written over: cleared each time)
+  if (m.dk < DK || m.dv % 64)
+    for (int i = tid; i < kC * (2 * LK + LO) * (int)sizeof(T) / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sK)[i] = uint4{0u, 0u, 0u, 0u};
+  {
+    Stage<T, DK, kThreads> rk(reinterpret_cast<const T*>(A.k) + s.b * A.sk[0] + row0 * A.sk[1] + hk * A.sk[2], A.sk[1], m.dk, true);
+    Stage<T, DK, kThreads> rq(reinterpret_cast<const T*>(A.q) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2], A.sq[1], m.dk, true);
+    fetch_rows(rk, A.sk[1], n);
+    fetch_rows(rq, A.sq[1], n);
+    if (m.dk < DK || m.dv % 64) __syncthreads();
+    rk.template put_split<LK>(sK);
+    rq.template put_split<LK>(sQ);
+  }
+
+  f32x4 dqa[NS], dka[NS];                           // [row 16 i + 4 g + r][token 16 w + l16]
+#pragma unroll
+  for (int i = 0; i < NS; ++i) dqa[i] = dka[i] = zero4();
+
+  for (int hh = 0; hh < share; ++hh) {
+    const int h = hk * share + hh;
+    const long long cs = (long long)slot * m.H + h;                    // [c_slots][H]
+    f32x4 WO[4], WV[4], e[4], db[4];
+    float frob = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) WO[i] = WV[i] = e[i] = db[i] = zero4();
+    for (int vb = 0; vb < v_blocks; ++vb) {
+      const int c0 = 64 * vb;
+      Stage<T, 64, kThreads> ro(reinterpret_cast<const T*>(A.dO) + s.b * A.sdo[0] + row0 * A.sdo[1] + h * A.sdo[2] + c0,
+                                A.sdo[1], m.dv - c0, true);
+      Stage<T, 64, kThreads> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + c0,
+                                A.sv[1], m.dv - c0, false);
+      fetch_rows(ro, A.sdo[1], n);
+      fetch_rows(rv, A.sv[1], n);
+      f32x4 S[NS], D[NS];
+      const bool live_tile = 4 * vb + w < ct;       // uniform
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        S[i] = D[i] = zero4();
+        if (live_tile) {
+          const long long at = (cs * ct + 4 * vb + w) * (DK * 16) + i * 256 + lane * 4;
+          S[i] = *reinterpret_cast<const f32x4*>(A.cstates + at);
+          D[i] = *reinterpret_cast<const f32x4*>(A.rstates + at);
+        }
+      }
+      __syncthreads();                              // the last block's and head's tiles have been read
+      if (vb == 0 && tid < kDeltaVec / 4)
+        reinterpret_cast<uint4*>(vec)[tid] = reinterpret_cast<const uint4*>(A.vec + cs * kDeltaVec)[tid];
+      if (m.dv - c0 < 64) {
+        for (int i = tid; i < 64 * LV * (int)sizeof(T) / 16; i += kThreads)
+          reinterpret_cast<uint4*>(sU)[i] = uint4{0u, 0u, 0u, 0u};
+        if (vb > 0)
+          for (int i = tid; i < kC * LO * (int)sizeof(T) / 16; i += kThreads)
+            reinterpret_cast<uint4*>(sO)[i] = uint4{0u, 0u, 0u, 0u};
+        __syncthreads();
+      }
+      ro.template put_split<LO>(sO);
+      rv.template put<LV>(sU);
+      __syncthreads();
+
+      // a wave's 16 columns
+      put_scores<T, DK, LK, LP, 4>(sA, sQ, sK, sc, w, 0, lane, A.scale);
+      const int wc = 16 * w;
+      f32x4 U[4], X[4], V[4];
+      {
+        Op<T> sf[M], df[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          split_terms(S[2 * i], S[2 * i + 1], sf[i]);
+          split_terms(D[2 * i], D[2 * i + 1], df[i]);
+        }
+        frag of[2], vf[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vf[i] = column_frag<LV>(sU + 32 * i * LV + wc, lane);
+          of[i] = split_column_frag<LO>(sO + 32 * i * LO, w, lane);
+        }
+        const T* inv = reinterpret_cast<const T*>(A.inv) + cs * kInvElems<T>;
+        const T* inv_t = reinterpret_cast<const T*>(A.inv_t) + cs * kInvElems<T>;
+        f32x4 Z[4], o[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          X[it] = Z[it] = o[it] = zero4();
+#pragma unroll
+          for (int i = 0; i < M; ++i) {
+            const frag kf = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
+            X[it] = mul<T>(kf, sf[i], X[it]);
+            Z[it] = mul<T>(kf, df[i], Z[it]);
+            o[it] = mul<T>(row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], o[it]);
+          }
+          const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
+          V[it] = half_of(vf[it >> 1], it & 1);
+          X[it] = *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g) * (V[it] - yv * X[it]);
+          Z[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
+          o[it] *= yv * A.scale;
+        }
+        Op<T> xf[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_terms(X[2 * i], X[2 * i + 1], xf[i]);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          U[it] = zero4();
+#pragma unroll
+          for (int i = 0; i <= it >> 1; ++i) {
+            Op<T> a;
+            load_inv<T>(inv, inv_frag(it, i), lane, a);
+            U[it] = mul<T>(a, xf[i], U[it]);
+          }
+        }
+        // <D, S'>, S' = y_63 S + K^T diag(exp(c_63 - c)) U
+        {
+          float f = 0.f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f = fmaf(S[i][r], D[i][r], f);
+          frob = fmaf(vec[kC - 1], f, frob);
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) frob = fmaf(U[it][r], Z[it][r], frob);
+        }
+        Op<T> uf[2], zf[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
+        __syncthreads();                            // P is there, and V has been read
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            Op<T> pf;
+            if (i <= it >> 1) {
+#pragma unroll
+              for (int t = 0; t < kTerms<T>; ++t) pf.t[t] = row_frag(sA + (t * kC + 16 * it + l16) * LP + 32 * i + 8 * g);
+              o[it] = mul<T>(pf, uf[i], o[it]);
+            }
+            if (i >= it >> 1) {
+#pragma unroll
+              for (int t = 0; t < kTerms<T>; ++t) pf.t[t] = split_column_frag<LP>(sA + (t * kC + 32 * i) * LP, it, lane);
+              Z[it] = mul<T>(pf, of[i], Z[it]);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_terms(Z[2 * i], Z[2 * i + 1], zf[i]);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          X[it] = zero4();
+#pragma unroll
+          for (int i = it >> 1; i < 2; ++i) {
+            Op<T> a;
+            load_inv<T>(inv_t, inv_t_frag(it, i), lane, a);
+            X[it] = mul<T>(a, zf[i], X[it]);
+          }
+          db[it] += X[it] * U[it];
+          X[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
+          e[it] += o[it] * half_of(of[it >> 1], it & 1) - X[it] * V[it];
+        }
+      }
+      // U, dv and the state through LDS
+      T* const mine = sU + (wc + l16) * LP + 4 * g;
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const Quad<T> u = quad(U[it], T()), z = quad(X[it], T());
+        *reinterpret_cast<Quad<T>*>(mine + 16 * it) = u;
+        *reinterpret_cast<Quad<T>*>(mine + (sZ - sU) + 16 * it) = z;
+        if constexpr (kBf) {
+          U[it] -= unquad(u);
+          X[it] -= unquad(z);
+        }
+      }
+      __syncthreads();                              // P has been read
+      if constexpr (kBf)
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          store4(sA + (wc + l16) * LP + 4 * g + 16 * it, U[it]);
+          store4(sA + (64 + wc + l16) * LP + 4 * g + 16 * it, X[it]);
+        }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) store4(sS + (wc + l16) * LS + 16 * i + 4 * g, S[i]);
+      __syncthreads();
+
+      // a wave's 16 tokens
+      frag ur[2], zr[2];
+      {
+        Op<T> zt[2], ot[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          zt[i].t[0] = zr[i] = column_frag<LP>(sZ + 32 * i * LP + 16 * w, lane);
+          if constexpr (kBf) zt[i].t[1] = column_frag<LP>(sA + (64 + 32 * i) * LP + 16 * w, lane);
+          ot[i].t[0] = row_frag(sO + (16 * w + l16) * LO + 32 * i + 8 * g);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j <= w)                               // uniform
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              Op<T> ut;
+              ut.t[0] = column_frag<LP>(sU + 32 * i * LP + 16 * j, lane);
+              if constexpr (kBf) ut.t[1] = column_frag<LP>(sA + 32 * i * LP + 16 * j, lane);
+              WO[j] = mul<T>(ut, ot[i].t[0], WO[j]);
+              WV[j] = mul<T>(ut, zt[i], WV[j]);
+              if (j == w) ur[i] = ut.t[0];
+            }
+        const float yr = vec[16 * w + l16], yo = yr * A.scale;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          f32x4 a = zero4(), b = zero4();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const frag st = column_frag<LS>(sS + 32 * j * LS + 16 * i, lane);
+            a = mma(st, ot[j].t[0], a);
+            b = mma(st, zr[j], b);
+          }
+          dqa[i] += a * yo;
+          dka[i] -= b * yr;
+        }
+        // dv: tokens 16 w + l16, columns 32 i + 16 half + 4 g
+        if (16 * w + l16 < n) {
+          T* const dst = reinterpret_cast<T*>(A.dv) + ((lead + hh) + (row0 + 16 * w + l16) * m.H) * m.dv + c0 + 4 * g;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              if (c0 + 32 * i + 16 * half + 4 * g < m.dv) store4(dst + 32 * i + 16 * half, half_of(zr[i], half));
+        }
+      }
+      __syncthreads();                              // S has been read
+#pragma unroll
+      for (int i = 0; i < NS; ++i) store4(sS + (wc + l16) * LS + 16 * i + 4 * g, D[i]);
+      __syncthreads();
+      const float left = vec[kC + 16 * w + l16];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        f32x4 a = zero4();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) a = mma(column_frag<LS>(sS + 32 * j * LS + 16 * i, lane), ur[j], a);
+        dka[i] += a * left;
+      }
+    }
+    // dots: over a wave's 16 columns, then over the waves
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float a = sum16(e[it][r]), b = sum16(db[it][r]);
+        if (l16 == 0) {
+          sE[w * kC + 16 * it + 4 * g + r] = a;
+          sE[(4 + w) * kC + 16 * it + 4 * g + r] = b;
+        }
+      }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
+    if (lane == 0) sF[w] = frob;
+    __syncthreads();                                // (the second terms and D have been read, too)
+    // PO and PV, the wave's strip of rows
+    {
+      const double ci = sc[16 * w + l16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f32x4 po = zero4(), pv = zero4();
+        if (j <= w)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = 16 * j + 4 * g + r, row = 16 * w + l16;
+            const float x = exp64(ci - sc[key]);
+            po[r] = key > row ? 0.f : WO[j][r] * (x * A.scale);
+            pv[r] = key >= row ? 0.f : -WV[j][r] * x;
+          }
+        T* const at = sA + (16 * w + l16) * LP + split_place(16 * j + 4 * g);
+        store4(at, po);
+        store4(at + kC * LP, pv);
+      }
+    }
+    if (w == 0) {
+      const long long at = lead + hh + (row0 + lane) * m.H;
+      const float b = sE[4 * kC + lane] + sE[5 * kC + lane] + sE[6 * kC + lane] + sE[7 * kC + lane];
+      if (lane < n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(b / vec[2 * kC + lane]);
+      if (A.dlog) {
+        double x = (double)sE[lane] + sE[kC + lane] + sE[2 * kC + lane] + sE[3 * kC + lane];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const double up = __shfl_down(x, d);
+          if (lane + d < 64) x += up;
+        }
+        x += (double)sF[0] + sF[1] + sF[2] + sF[3];
+        // a decay of nothing, and one of zero (in fp32), have no gradient
+        const bool none = (s.part == 0 && lane == 0 && !A.init) || sc[lane] - (lane ? sc[lane - 1] : 0.0) < -104.0;
+        if (lane < n) A.dlog[at] = none ? 0.f : (float)x;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const frag kt = split_column_frag<LK>(sK + 32 * j * LK, i, lane);
+        if (j <= w >> 1) {                          // uniform
+          dqa[i] = mma(kt, row_frag(sA + (16 * w + l16) * LP + 32 * j + 8 * g), dqa[i]);
+          dka[i] = mma(kt, row_frag(sA + (kC + 16 * w + l16) * LP + 32 * j + 8 * g), dka[i]);
+        }
+        if (j >= w >> 1) {
+          dka[i] = mma(split_column_frag<LK>(sQ + 32 * j * LK, i, lane), split_column_frag<LP>(sA + 32 * j * LP, w, lane), dka[i]);
+          dka[i] = mma(kt, split_column_frag<LP>(sA + (kC + 32 * j) * LP, w, lane), dka[i]);
+        }
+      }
+  }
+  if (16 * w + l16 < n) {
+    const long long at = (row0 + 16 * w + l16) * m.Hk * m.dk + 4 * g;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (16 * i + 4 * g < m.dk) {
+        store4(gq + at + 16 * i, dqa[i]);
+        store4(gk + at + 16 * i, dka[i]);
+      }
+  }
+}
+
+template <typename T, int DK, int W, bool kSums>
+hipError_t launch_reverse_t(const DeltaArgs& a, hipStream_t st) {
+  using TL = ReverseTiles<T, DK, W>;
+  const auto kernel = delta_reverse_kernel<T, DK, W, kSums>;
+  hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), TL::bytes);
+  if (e != hipSuccess) return e;
+  const int blocks = (a.m.dv + 16 * W - 1) / (16 * W);
+  const long long units = (long long)a.m.n_slots * a.m.H;
+  launch_kernel(kernel, grid_rows((units + 7) / 8 * 8 * blocks), 64 * W, TL::bytes, st, a, blocks);
+  return hipGetLastError();
+}
+
+template <bool kSums>
+hipError_t launch_reverse_d(const DeltaArgs& a, bool bf16, hipStream_t st) {
+  const int dk = a.m.dk;
+  if (!bf16) return dk <= 32 ? launch_reverse_t<float, 32, 4, kSums>(a, st)
+                  : dk <= 64 ? launch_reverse_t<float, 64, 4, kSums>(a, st) : launch_reverse_t<float, 128, 4, kSums>(a, st);
+  if (decay_columns(true, a.m.dv) == 128)
+    return dk <= 64 ? launch_reverse_t<__bf16, 64, 8, kSums>(a, st) : launch_reverse_t<__bf16, 128, 8, kSums>(a, st);
+  return dk <= 32 ? launch_reverse_t<__bf16, 32, 4, kSums>(a, st)
+         : dk <= 64 ? launch_reverse_t<__bf16, 64, 4, kSums>(a, st) : launch_reverse_t<__bf16, 128, 4, kSums>(a, st);
+}
+
+template <typename T, int DK>
+hipError_t launch_grads_t(const DeltaArgs& a, hipStream_t st) {
+  using TL = GradTiles<T, DK>;
+  const auto kernel = delta_grads_kernel<T, DK>;
+  hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), TL::bytes);
+  if (e != hipSuccess) return e;
+  launch_kernel(kernel, grid_rows((long long)a.m.c_slots * a.m.Hk), kThreads, TL::bytes, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_reverse(const DeltaArgs& a, bool bf16, bool sums, hipStream_t st) {
+  return sums ? launch_reverse_d<true>(a, bf16, st) : launch_reverse_d<false>(a, bf16, st);
+}
+
+hipError_t launch_delta_grads(const DeltaArgs& a, bool bf16, hipStream_t st) {
+  const int dk = a.m.dk;
+  if (bf16) return dk <= 32 ? launch_grads_t<__bf16, 32>(a, st)
+                 : dk <= 64 ? launch_grads_t<__bf16, 64>(a, st) : launch_grads_t<__bf16, 128>(a, st);
+  return dk <= 32 ? launch_grads_t<float, 32>(a, st)
+         : dk <= 64 ? launch_grads_t<float, 64>(a, st) : launch_grads_t<float, 128>(a, st);
+}
+
+}  // namespace kata

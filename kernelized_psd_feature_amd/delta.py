@@ -38,6 +38,8 @@ def _signatures():
     return {
         "kata_fwd_delta_workspace_size": (SZ, [VP]),
         "kata_fwd_delta": (_I32, [VP] * 11 + [SZ, VP]),
+        "kata_bwd_delta_workspace_size": (SZ, [VP]),
+        "kata_bwd_delta": (_I32, [VP] * 17 + [SZ, VP]),
         "kata_decode_delta": (_I32, [VP] * 9),
     }
 
