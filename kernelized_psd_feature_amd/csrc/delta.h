@@ -27,8 +27,7 @@ struct DeltaArgs {
   int zero_tail;
   // workspace
   float* vec;                             // [c_slots][H][kDeltaVec]
-  void* inv;                              // [c_slots][H] inverses, as operands (delta_tiles.h)
-  void* inv_t;                            // their transposes; null in a forward pass
+  float* inv;                             // [c_slots][H][kInvFloats] inverses
   float* sums;                            // [n_slots][H][dk][dv] sums of the segments, then their entry states
   float* trans;                           // [n_slots][H][dk][dk] transitions of the segments
   float* rsums;                           // backward: [n_slots][H][dk][dv], the same of the gradient of the state

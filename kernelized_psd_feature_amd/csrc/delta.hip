@@ -36,10 +36,9 @@ constexpr int kThreads = 256;             // of the kernels other than the walk
 template <typename T, int DK>
 struct PrepTiles {
   static constexpr int LK = DK + 16 / (int)sizeof(T), LA = kC + 4, LD = 20;
-  static constexpr int kHead = 16 + kC * 8 + kC * 4;                   // an int, c, beta
-  static constexpr int kKeys = kC * LK * (int)sizeof(T), kInv = kC * LA * 4;
-  static constexpr int kFirst = kKeys > kInv ? kKeys : kInv;           // the keys, then the inverse
-  static constexpr int bytes = kHead + kFirst + kC * LA * 4 + kC * LD * 4;
+  static constexpr int kHead = 16 + 3 * kC * 4;                        // an int, c in two floats, beta
+  static constexpr int kKeys = kC * LK * (int)sizeof(T);
+  static constexpr int bytes = kHead + kKeys + kC * LA * 4 + kC * LD * 4;
 };
 
 template <typename T, int DK>
@@ -49,11 +48,10 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
   constexpr int M = DK / 32, LK = TL::LK, LA = TL::LA, LD = TL::LD;
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
-  double* const sc = reinterpret_cast<double*>(lds + 16);
-  float* const sb = reinterpret_cast<float*>(lds + 16 + kC * 8);
+  float* const sc = reinterpret_cast<float*>(lds + 16);
+  float* const sb = sc + 2 * kC;
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
-  float* const sT = reinterpret_cast<float*>(lds + TL::kHead);
-  float* const sA = reinterpret_cast<float*>(lds + TL::kHead + TL::kFirst);
+  float* const sA = reinterpret_cast<float*>(lds + TL::kHead + TL::kKeys);
   float* const sD = sA + kC * LA;
 
   const DeltaMap& m = A.m;
@@ -73,29 +71,32 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
   if (m.dk < DK)
     for (int i = tid; i < kC * LK * (int)sizeof(T) / 16; i += kThreads)
       reinterpret_cast<uint4*>(sK)[i] = uint4{0u, 0u, 0u, 0u};
+  float* const vec = A.vec + (long long)unit * kDeltaVec;
   if (w == 0) {
     float ld = 0.f, b = 0.f;
     if (lane < n) {
       b = to_f32(reinterpret_cast<const T*>(A.beta)[row_off(A.sb, s.b, row0 + lane, h)]);
       if (A.log_decay) ld = A.log_decay[row_off(A.sl, s.b, row0 + lane, h)];
       if (ld < -256.f) ld = -256.f;                 // exp of it is zero in fp32; sums of 64 stay finite
-      // U / b is wanted there: a factor of 1e-30 is as good as none, and can be taken out again
-      if (backward && fabsf(b) < 1e-30f) b = copysignf(1e-30f, b);
+      // X U / b^2 is wanted there: a factor of 1e-15 is as good as none, and can be taken out again
+      if (backward && fabsf(b) < 1e-15f) b = copysignf(1e-15f, b);
     }
-    double c = ld;
+    double c = ld * 1.4426950408889634;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const double up = __shfl_up(c, d);
       if (lane >= d) c += up;
     }
-    const double all = __shfl(c, 63);
-    sc[lane] = c;
+    const double left = __shfl(c, 63) - c;
+    const float hi = (float)c, lo = hi - hi == 0.f ? (float)(c - hi) : hi;
+    sc[lane] = hi;
+    sc[kC + lane] = lo;
     sb[lane] = b;
-    float* vec = A.vec + (long long)unit * kDeltaVec;
-    vec[lane] = exp64(c);
-    vec[kC + lane] = exp64(all - c);
+    vec[lane] = exp2_diff(hi, lo, 0.f, 0.f);
+    vec[kC + lane] = exp2_diff((float)left, (float)(left - (float)left), 0.f, 0.f);
     vec[2 * kC + lane] = b;
-    reinterpret_cast<double*>(vec + 3 * kC)[lane] = c;
+    vec[3 * kC + lane] = hi;
+    vec[4 * kC + lane] = lo;
   }
   if (m.dk < DK) __syncthreads();
   rk.template put_split<LK>(sK);
@@ -105,18 +106,34 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
   frag ka[M];
 #pragma unroll
   for (int i = 0; i < M; ++i) ka[i] = row_frag(sK + (16 * w + l16) * LK + 32 * i + 8 * g);
+  f32x4 sick = zero4();
   for (int j = 0; j <= w; ++j) {                    // uniform
     f32x4 acc = zero4();
 #pragma unroll
     for (int i = 0; i < M; ++i) acc = mma(ka[i], row_frag(sK + (16 * j + l16) * LK + 32 * i + 8 * g), acc);
     const int col = 16 * j + l16;
-    const double cj = sc[col];
+    const float hj = sc[col], lj = sc[kC + col];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * w + 4 * g + r;
-      sA[row * LA + col] = col < row ? sb[row] * exp64(sc[row] - cj) * acc[r] : 0.f;
+      const float a = col < row ? sb[row] * exp2_diff(sc[row], sc[kC + row], hj, lj) * acc[r] : 0.f;
+      sick[r] = fmaf(a, 0.f, sick[r]);
+      sA[row * LA + col] = a;
     }
   }
+  // A row with an infinity or nan would leave nan in earlier rows of the inverse: it is taken as zeros, and
+  // its beta as nan, which makes the row's correction nan in the walk.
+  if (__any(sick[0] + sick[1] + sick[2] + sick[3] != 0.f))
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) sick[r] += __shfl_xor(sick[r], d);
+      if (sick[r] != 0.f) {
+        const int row = 16 * w + 4 * g + r;
+        for (int j = 0; j <= w; ++j) sA[row * LA + 16 * j + l16] = 0.f;
+        if (l16 == 0) vec[2 * kC + row] = __builtin_nanf("");
+      }
+    }
   __syncthreads();
   if (w == 0) {                                     // block g, column l16: x = e - A x
     float x[16];
@@ -131,90 +148,67 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
     }
   }
   __syncthreads();
-  {                                                 // block column w
-    f32x4 t[4];
+  // block column w
+  float* const inv = A.inv + (long long)unit * kInvFloats;
+  f32x4 t[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) t[0][r] = sD[(16 * w + 4 * g + r) * LD + l16];
+  for (int r = 0; r < 4; ++r) t[0][r] = sD[(16 * w + 4 * g + r) * LD + l16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {                   // block row w + i
-      if (w + i > 3) break;                         // uniform
-      const int bi = w + i;
-      if (i > 0) {
-        f32x4 acc = zero4();
+  for (int i = 0; i < 4; ++i) {                     // block row w + i
+    if (w + i > 3) break;                           // uniform
+    const int bi = w + i;
+    if (i > 0) {
+      f32x4 acc = zero4();
 #pragma unroll
-        for (int k = 0; k < i; ++k) {
-          const f32x4 a = *reinterpret_cast<const f32x4*>(sA + (16 * bi + l16) * LA + 16 * (w + k) + 4 * g);
+      for (int k = 0; k < i; ++k) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(sA + (16 * bi + l16) * LA + 16 * (w + k) + 4 * g);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], t[k][r], acc, 0, 0, 0);
-        }
-        const f32x4 d = *reinterpret_cast<const f32x4*>(sD + (16 * bi + l16) * LD + 4 * g);
-        t[i] = zero4();
-#pragma unroll
-        for (int r = 0; r < 4; ++r) t[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(-d[r], acc[r], t[i], 0, 0, 0);
+        for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], t[k][r], acc, 0, 0, 0);
       }
+      const f32x4 d = *reinterpret_cast<const f32x4*>(sD + (16 * bi + l16) * LD + 4 * g);
+      t[i] = zero4();
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sT[(16 * bi + 4 * g + r) * LA + 16 * w + l16] = t[i][r];
+      for (int r = 0; r < 4; ++r) t[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(-d[r], acc[r], t[i], 0, 0, 0);
     }
-  }
-  __syncthreads();
-  // as operands: lane's row l16 (of the transpose: column) of a tile, split slots of the other index
-  for (int f = w; f < (backward ? 2 : 1) * kInvFrags; f += 4) {
-    const bool trans = f >= kInvFrags;
-    const int x = trans ? f - kInvFrags : f;
-    const int it = trans ? (x < 4 ? x >> 1 : x - 2) : (x < 2 ? x : 1 + (x >> 1));
-    const int ms = trans ? (x < 4 ? x & 1 : 1) : (x < 2 ? 0 : x & 1);
-    f32x4 p[2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int other = 2 * ms + half;              // block of the K step
-      if (!trans) {
-        p[half] = other > it ? zero4()
-                             : *reinterpret_cast<const f32x4*>(sT + (16 * it + l16) * LA + 16 * other + 4 * g);
-      } else {
-        p[half] = zero4();
-        if (other >= it)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) p[half][r] = sT[(16 * other + 4 * g + r) * LA + 16 * it + l16];
-      }
-    }
-    Op<T> op;
-    split_terms(p[0], p[1], op);
-    T* dst = reinterpret_cast<T*>(trans ? A.inv_t : A.inv) + (long long)unit * kInvElems<T>;
-#pragma unroll
-    for (int t = 0; t < kTerms<T>; ++t)
-      *reinterpret_cast<frag*>(dst + ((x * kTerms<T> + t) * 64 + lane) * 8) = op.t[t];
+    for (int r = 0; r < 4; ++r) inv[(bi * (bi + 1) / 2 + w) * 256 + (4 * g + r) * 16 + l16] = t[i][r];
   }
 }
 
 // ---- the walk ----------------------------------------------------------------------------------
 enum class Walk { output, states, sums };
 
-template <typename T, int DK, int W, bool kOut>
+template <typename T, int DK, int W, int NT, bool kOut>
 struct WalkTiles {
   static constexpr bool kBf = sizeof(T) == 2;
   static constexpr int DV = 16 * W;
   static constexpr int LK = DK + 16 / (int)sizeof(T), LV = DV + (kBf ? 16 : 4), LP = kC + 16 / (int)sizeof(T);
   static constexpr int kHead = 16 + kDeltaVec * 4;
   static constexpr int kTiles = kC * (LK * (kOut ? 2 : 1) + LV);
-  static constexpr int bytes = kHead + (kTiles + (kOut ? kTerms<T> * kC * LP : 0)) * (int)sizeof(T);
+  static constexpr int kPO = kBf ? 2 : 1;           // terms of the outputs' operands
+  static constexpr int bytes = kHead + (kTiles + (NT + (kOut ? kPO : 0)) * kC * LP) * (int)sizeof(T);
+  // waves a SIMD that the registers are held to (the launch bound counts workgroups a CU)
+  static constexpr int occupancy = !kBf && DK == 128 ? 1 : 8 / W;
 };
 
 // kWhat: outputs and the final state; or (backward) the states before the chunks; or, of the segments,
-// sums and transitions (blocks of columns behind those of the values).
-template <typename T, int DK, int W, Walk kWhat>
-__global__ __launch_bounds__(64 * W) void delta_walk_kernel(DeltaArgs A, int blocks, int backward) {
+// sums and transitions (blocks of columns behind those of the values).  NT: terms of the recurrence's operands.
+template <typename T, int DK, int W, int NT, Walk kWhat>
+__global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::output>::occupancy)) void delta_walk_kernel(
+    DeltaArgs A, int blocks, int backward) {
   constexpr bool kOut = kWhat == Walk::output, kSums = kWhat == Walk::sums;
-  using TL = WalkTiles<T, DK, W, kOut>;
+  using TL = WalkTiles<T, DK, W, NT, kOut>;
   using frag = typename Elem<T>::frag;
   constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
+  constexpr int PO = TL::kPO, J = 16 / W;           // terms of the outputs' operands; key tiles of a wave's part of P
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
-  const double* const sc = reinterpret_cast<const double*>(vec + 3 * kC);
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
   T* const sV = sK + kC * LK;
   T* const sQ = sV + kC * LV;
-  T* const sP = sQ + kC * LK;
+  T* const sT = sK + TL::kTiles;
+  T* const sP = sT + NT * kC * LP;
 
   const DeltaMap& m = A.m;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
@@ -272,172 +266,227 @@ __global__ __launch_bounds__(64 * W) void delta_walk_kernel(DeltaArgs A, int blo
   Stage<T, DK, kThr> rq(reinterpret_cast<const T*>(kOut ? A.q : A.k) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2], A.sq[1], m.dk, true);
   Stage<T, DV, kThr> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + (unit_matrix ? 0 : c0),
                         A.sv[1], m.dv - (unit_matrix ? 0 : c0), false);
+  StageInv<T, NT, LP, kThr> ri;
   const int n_last = min(kC, s.len - kC * (behind - 1));
   uint4 vec_next;
   const long long chunk0 = (long long)(s.c_slot + first) * m.H + h;    // [c_slots][H]
+  const float* p_inv = A.inv + chunk0 * kInvFloats;
+  const float* p_vec = A.vec + chunk0 * kDeltaVec;
   auto fetch = [&](int c) {
     const int n = c == behind - 1 ? n_last : kC;
     fetch_rows(rk, A.sk[1], n);
     if constexpr (kOut) fetch_rows(rq, A.sq[1], n);
     if (!unit_matrix) fetch_rows(rv, A.sv[1], n);
-    if (tid < kDeltaVec / 4)
-      vec_next = reinterpret_cast<const uint4*>(A.vec + (chunk0 + (long long)(c - first) * m.H) * kDeltaVec)[tid];
-  };
-  Op<T> inv[kInvFrags];
-  auto fetch_inv = [&](int c) {
-    const T* at = reinterpret_cast<const T*>(A.inv) + (chunk0 + (long long)(c - first) * m.H) * kInvElems<T>;
-#pragma unroll
-    for (int f = 0; f < kInvFrags; ++f) load_inv<T>(at, f, lane, inv[f]);
+    ri.fetch(p_inv);
+    if (tid < kDeltaVec / 4) vec_next = reinterpret_cast<const uint4*>(p_vec)[tid];
+    p_inv += (long long)m.H * kInvFloats;
+    p_vec += (long long)m.H * kDeltaVec;
   };
   fetch(first);
-  fetch_inv(first);
 
   // state tiles: S[i] lane holds rows 16 i + 4 g + r of column c0 + wc + l16
   const int wc = 16 * w, col = c0 + wc + l16;
   f32x4 S[NS];
+  {
+    const float* given = kSums ? nullptr : s.part > 0 ? A.sums + ((long long)slot * m.H + h) * SE : A.init ? A.init + st_off : nullptr;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    S[i] = zero4();
+    for (int i = 0; i < NS; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * i + 4 * g + r;
-      if (kSums) {
-        if (unit_matrix && row == col) S[i][r] = 1.f;
-      } else if (row < m.dk && col < m.dv) {
-        if (s.part > 0) S[i][r] = A.sums[((long long)slot * m.H + h) * SE + (long long)row * m.dv + col];
-        else if (A.init) S[i][r] = A.init[st_off + (long long)row * m.dv + col];
-      }
-    }
+      for (int r = 0; r < 4; ++r) S[i][r] = kSums && unit_matrix && 16 * i + 4 * g + r == col ? 1.f : 0.f;
+    if (given) load_state(S, given, m.dk, m.dv, col, g);               // uniform
   }
   if (m.dk < DK || m.dv - c0 < DV || unit_matrix) { // columns that no operand has: zeros all along
     uint4* const z = reinterpret_cast<uint4*>(sK);
     for (int i = tid; i < TL::kTiles * (int)sizeof(T) / 16; i += kThr) z[i] = uint4{0u, 0u, 0u, 0u};
   }
+  ri.zeros(sT);
+  const int rt = w & 3, j0 = J * (w >> 2);          // the wave's rows and first key tile of P
   const bool live_col = c0 + wc + 4 * g < m.dv;
   T* po = kOut ? out + (row0 + l16) * A.so[1] + wc + 4 * g : nullptr;
+  const int ct = (m.dv + 15) / 16;
+  float* p_state = nullptr;
+  if (kWhat == Walk::states && c0 / 16 + w < ct) p_state = A.cstates + (chunk0 * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
 
+#pragma unroll 1
   for (int c = first; c < behind; ++c) {
-    const int n = c == behind - 1 ? n_last : kC;
     __syncthreads();                                // the last chunk's tiles have been read
     rk.template put_split<LK>(sK);
     if constexpr (kOut) rq.template put_split<LK>(sQ);
     if (!unit_matrix) rv.template put<LV>(sV);
+    ri.put(sT);
     if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
     if (c + 1 < behind) fetch(c + 1);
     __syncthreads();
 
-    if (kWhat == Walk::states && 16 * (c0 / 16 + w) < (m.dv + 15) / 16 * 16) {
-      float* dst = A.cstates + ((chunk0 + (long long)(c - first) * m.H) * ((m.dv + 15) / 16) + c0 / 16 + w) * (DK * 16) + lane * 4;
+    if (kWhat == Walk::states && p_state) {         // uniform
 #pragma unroll
-      for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(dst + i * 256) = S[i];
+      for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(p_state + i * 256) = S[i];
+      p_state += (long long)m.H * ct * (DK * 16);
     }
-    Op<T> sf[M];
+    // LDS reads are issued in batches, ahead of the work that hides them (reads_above): left alone, the compiler
+    // waits for nearly every read before its product.
+    f32x4 X[4], U[4], o[4];
+    Op<T, NT> inv[6];                               // (row tile, K step): (0, 0), (1, 0), (2, 0), (2, 1), (3, 0), (3, 1)
+    auto read_inv = [&](int from, int to) {         // planes
 #pragma unroll
-    for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
-    f32x4 X[4], U[4];
+      for (int f = 0; f < 6; ++f)
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      X[it] = zero4();
+        for (int t = 0; t < NT; ++t)
+          if (t >= from && t < to)
+            inv[f].t[t] = row_frag(sT + t * kC * LP + (16 * (f < 2 ? f : 1 + f / 2) + l16) * LP + (f < 2 ? 0 : 32 * (f & 1)) + 8 * g);
+    };
+    constexpr int kEarly = M > 2 ? 0 : NT > 2 ? 2 : NT;                // planes that there are registers for
+    frag vf[2];
+    {
+      frag kr[4][M], qr[M];
 #pragma unroll
-      for (int i = 0; i < M; ++i) X[it] = mul<T>(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], X[it]);
-    }
-    if constexpr (kOut) {                           // P, the wave's strip of rows
-      constexpr int J = 16 / W;
-      const int rt = w & 3, j0 = J * (w >> 2);
-      frag qf[M];
+      for (int it = 0; it < 4; ++it)
 #pragma unroll
-      for (int i = 0; i < M; ++i) qf[i] = row_frag(sQ + (16 * rt + l16) * LK + 32 * i + 8 * g);
-      const double ci = sc[16 * rt + l16];
+        for (int i = 0; i < M; ++i) kr[it][i] = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
+      if constexpr (kOut)
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        f32x4 p = zero4();
-        if (j0 + j <= rt) {                         // uniform
+        for (int i = 0; i < M; ++i) qr[i] = row_frag(sQ + (16 * rt + l16) * LK + 32 * i + 8 * g);
+      reads_above<T>();
+      Op<T, NT> sf[M];
 #pragma unroll
-          for (int i = 0; i < M; ++i) p = mma(row_frag(sK + (16 * (j0 + j) + l16) * LK + 32 * i + 8 * g), qf[i], p);
+      for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int key = 16 * (j0 + j) + 4 * g + r;
-            p[r] = key > 16 * rt + l16 ? 0.f : p[r] * (exp64(ci - sc[key]) * A.scale);
-          }
+      for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
+      read_inv(0, kEarly);
+      reads_above<T>();
+#pragma unroll
+      for (int it = 0; it < 4; ++it) X[it] = zero4();
+#pragma unroll
+      for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int it = 0; it < 4; ++it) X[it] = mul(kr[it][i], sf[i], X[it]);
+      if constexpr (kOut) {
+        f32x4 p[J];                                 // P transposed: the wave's rows, J key tiles
+#pragma unroll
+        for (int j = 0; j < J; ++j) p[j] = zero4();
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+          for (int j = 0; j < J; ++j) p[j] = mma(W == 8 && j0 ? kr[(j + J) & 3][i] : kr[j][i], qr[i], p[j]);
+        frag qo[4][2];
+        auto read_q = [&](int i) {
+#pragma unroll
+          for (int it = 0; it < 4; ++it) qo[it][i & 1] = row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g);
+        };
+        read_q(0);
+        reads_above<T>();
+        put_weights<T, LP, J, PO>(sP, p, vec + 3 * kC, rt, j0, lane, A.scale);
+        // bf16: with two terms of the state, of P and of U an output has no error but its own rounding
+#pragma unroll
+        for (int it = 0; it < 4; ++it) o[it] = zero4();
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          if (i + 1 < M) read_q(i + 1);
+          reads_above<T>();
+#pragma unroll
+          for (int t = PO - 1; t >= 0; --t)
+#pragma unroll
+            for (int it = 0; it < 4; ++it) o[it] = mma(sf[i].t[t], qo[it][i & 1], o[it]);
         }
-        T* const at = sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g);
-        const Quad<T> hi = quad(p, T());
-        *reinterpret_cast<Quad<T>*>(at) = hi;
-        if constexpr (kTerms<T> == 2) store4(at + kC * LP, p - unquad(hi));
+#pragma unroll
+        for (int it = 0; it < 4; ++it) o[it] *= vec[16 * it + l16] * A.scale;
       }
     }
-    frag vf[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
-    float sick = 0.f;
+    if constexpr (kEarly == 0) read_inv(0, NT > 2 ? 2 : NT);
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
       const f32x4 bv = *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);
       X[it] = bv * (half_of(vf[it >> 1], it & 1) - yv * X[it]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sick = fmaf(X[it][r], 0.f, sick);
     }
-    // An infinity or nan in row j: in the products below a zero of a later column would still meet it and
-    // leave nan in earlier rows.  From row j on the column's outputs and its state are nan; the rows before
-    // it are computed without.
-    int ill = kC;                                   // the column's first such row
-    if (__any(sick != sick)) {
+    if constexpr (NT > 2) read_inv(2, NT);
+    frag kt[2][NS];                                 // K transposed, 32 keys each
+    auto read_kt = [&](int j) {
 #pragma unroll
-      for (int it = 3; it >= 0; --it)
-#pragma unroll
-        for (int r = 3; r >= 0; --r)
-          if (!(fabsf(X[it][r]) < __builtin_huge_valf())) ill = 16 * it + 4 * g + r;
-      ill = min(ill, __shfl_xor(ill, 16));
-      ill = min(ill, __shfl_xor(ill, 32));
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * it + 4 * g + r >= ill) X[it][r] = 0.f;
-    }
-    {
-      Op<T> xf[2];
+      for (int i = 0; i < NS; ++i) kt[j][i] = split_column_frag<LK>(sK + 32 * j * LK, i, lane);
+    };
+    if constexpr (M <= 2) read_kt(0);
+    reads_above<T>();
+    auto correct = [&] {
+      Op<T, NT> xf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_terms(X[2 * i], X[2 * i + 1], xf[i]);
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        U[it] = zero4();
-#pragma unroll
-        for (int i = 0; i <= it >> 1; ++i) U[it] = mul<T>(inv[inv_frag(it, i)], xf[i], U[it]);
-      }
-    }
-    const bool any_ill = __any(ill < kC);
-    if (any_ill) {                                  // (rows of an inverse may be nan from a key on)
+      U[0] = mul(inv[0], xf[0], zero4());
+      U[1] = mul(inv[1], xf[0], zero4());
+      U[2] = mul(inv[2], xf[0], zero4());
+      U[3] = mul(inv[4], xf[0], zero4());
+      U[2] = mul(inv[3], xf[1], U[2]);
+      U[3] = mul(inv[5], xf[1], U[3]);
+      float sick = 0.f;
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * it + 4 * g + r >= ill) U[it][r] = 0.f;
+        for (int r = 0; r < 4; ++r) sick = fmaf(U[it][r], 0.f, sick);
+      return sick != 0.f;
+    };
+    // An infinity or nan in row j: in products a zero of a later column would still meet it and leave nan in
+    // earlier rows.  From row j on the column's outputs and its state are nan; the rows before it are
+    // computed without.
+    int ill = kC;                                   // the column's first such row
+    const bool any_ill = __any(correct());
+    if (any_ill) {
+      auto look = [&](f32x4 (&x)[4]) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!(fabsf(x[it][r]) < __builtin_huge_valf())) ill = min(ill, 16 * it + 4 * g + r);
+        ill = min(ill, __shfl_xor(ill, 16));
+        ill = min(ill, __shfl_xor(ill, 32));
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (16 * it + 4 * g + r >= ill) x[it][r] = 0.f;
+      };
+      look(X);
+      read_inv(0, NT);
+      correct();
+      look(U);
     }
-    if (c + 1 < behind) fetch_inv(c + 1);
-    f32x4 o[4];
+    {
+      const float whole = vec[kC - 1];
+      f32x4 u[4];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) u[it] = U[it] * *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
+      if constexpr (M > 2) read_kt(0);
+      read_kt(1);
+      reads_above<T>();
+      Op<T, NT> uf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_terms(u[2 * i], u[2 * i + 1], uf[i]);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) S[i] *= whole;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) S[i] = mul(kt[j][i], uf[j], S[i]);
+      if (any_ill && ill < kC)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) S[i] = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+    }
     if constexpr (kOut) {
-      Op<T> uf[2];
+      __syncthreads();                              // P is there
+      Op<T, PO> pf[6];
+#pragma unroll
+      for (int f = 0; f < 6; ++f)
+        pf[f] = row_op<PO>(sP + (16 * (f < 2 ? f : 1 + f / 2) + l16) * LP + (f < 2 ? 0 : 32 * (f & 1)) + 8 * g, kC * LP);
+      reads_above<T>();
+      Op<T, PO> uf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
-      __syncthreads();                              // P is there
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        o[it] = zero4();
-#pragma unroll
-        for (int i = 0; i < M; ++i) o[it] = mul<T>(sf[i], row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g), o[it]);
-        o[it] *= vec[16 * it + l16] * A.scale;
-#pragma unroll
-        for (int i = 0; i <= it >> 1; ++i) {
-          Op<T> pf;
-#pragma unroll
-          for (int t = 0; t < kTerms<T>; ++t)
-            pf.t[t] = row_frag(sP + (t * kC + 16 * it + l16) * LP + 32 * i + 8 * g);
-          o[it] = mul<T>(uf[i], pf, o[it]);
-        }
-      }
-      if (any_ill) {
+      o[0] = mul(uf[0], pf[0], o[0]);
+      o[1] = mul(uf[0], pf[1], o[1]);
+      o[2] = mul(uf[0], pf[2], o[2]);
+      o[3] = mul(uf[0], pf[4], o[3]);
+      o[2] = mul(uf[1], pf[3], o[2]);
+      o[3] = mul(uf[1], pf[5], o[3]);
+      if (any_ill)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int at = __shfl(ill, 4 * g + r);
@@ -445,29 +494,13 @@ __global__ __launch_bounds__(64 * W) void delta_walk_kernel(DeltaArgs A, int blo
           for (int it = 0; it < 4; ++it)
             if (16 * it + l16 >= at) o[it][r] = __builtin_nanf("");
         }
-      }
-      if (live_col)
+      if (live_col) {
+        const int n = c == behind - 1 ? n_last : kC;
 #pragma unroll
         for (int it = 0; it < 4; ++it)
           if (16 * it + l16 < n) *reinterpret_cast<Quad<T>*>(po + 16 * it * A.so[1]) = quad(o[it], T());
-      po += kC * A.so[1];
-    }
-    {
-      const float whole = vec[kC - 1];
-      Op<T> uf[2];
-#pragma unroll
-      for (int it = 0; it < 4; ++it) U[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        S[i] *= whole;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) S[i] = mul<T>(split_column_frag<LK>(sK + 32 * j * LK, i, lane), uf[j], S[i]);
       }
-      if (any_ill && ill < kC)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) S[i] = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+      po += kC * A.so[1];
     }
   }
 
@@ -479,18 +512,21 @@ __global__ __launch_bounds__(64 * W) void delta_walk_kernel(DeltaArgs A, int blo
   for (int i = 0; i < NS; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (16 * i + 4 * g + r < m.dk) dst[(long long)(16 * i + 4 * g + r) * cols + col] = S[i][r];
+      if (16 * i + 4 * g + r < m.dk) dst[(16 * i + 4 * g + r) * cols + col] = S[i][r];
 }
 
 // ---- joining segments ---------------------------------------------------------------------------
-// Per (sequence, head) and 64 columns, over the segments in order: E_{j+1} = M_j E_j + N_j; the sum in slot
+// Per (sequence, head) and 16 columns, over the segments in order: E_{j+1} = M_j E_j + N_j; the sum in slot
 // j is replaced by the entry state E_j.  Backward also in reversed time: D_{j-1} = M_j^T D_j + N'_j, the
-// sum in slot j replaced by D_j, the gradient of the state behind the segment.  fp32 MFMA.
+// sum in slot j replaced by D_j, the gradient of the state behind the segment.  On the fp32 MFMA; the rows are
+// split over the waves, which pass the state through LDS, and the next transition is loaded meanwhile.
 template <int DK>
 __global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int blocks) {
-  constexpr int M = DK / 32, NS = DK / 16;
+  constexpr int M = DK / 32, NS = DK / 16, R = (NS + 3) / 4, LS = DK + 4;
+  __shared__ __align__(16) float sS[2][16 * LS];
   const DeltaMap& m = A.m;
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15, w = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   unsigned x = blockIdx.x;                          // sequences: blockIdx.y
   const int sub = int(x % (unsigned)blocks);
   x /= (unsigned)blocks;
@@ -504,55 +540,76 @@ __global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int b
     len = max(cu_at(m, seq + 1) - first, 0);
   }
   const int n = (len + SL - 1) / SL;
-  const int col = 64 * sub + 16 * w + l16;
-  if (n < 2 || 64 * sub + 16 * w >= m.dv) return;
-  const long long SE = (long long)m.dk * m.dv, ME = (long long)m.dk * m.dk;
+  if (n < 2) return;
+  const int col = 16 * sub + l16, SE = m.dk * m.dv, ME = m.dk * m.dk;
   float* const sums = rev ? A.rsums : A.sums;
   const float* given = rev ? A.dfin : A.init;
   const bool live = col < m.dv;
-  f32x4 S[NS];
-#pragma unroll
-  for (int i = 0; i < NS; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * i + 4 * g + r;
-      S[i][r] = given && live && row < m.dk ? given[((long long)seq * m.H + h) * SE + (long long)row * m.dv + col] : 0.f;
-    }
-  for (int j = 0; j < n; ++j) {
-    const int seg = rev ? n - 1 - j : j;
-    const long long at = (long long)(slot + seg) * m.H + h;
-    float* const here = sums + at * SE;
+  const int rs = rev ? 1 : m.dk, cs = rev ? m.dk : 1;                  // strides of the transition's rows and columns
+  f32x4 S[R], N[R];
+  f32x8 a[R][M];
+  auto fetch = [&](int j) {
+    const long long at = (long long)(slot + (rev ? n - 1 - j : j)) * m.H + h;
+    const float* const here = sums + at * SE;
     const float* const tr = A.trans + at * ME;
-    f32x4 N[NS];
-    const bool more = j + 1 < n;
+    const bool used = j > 0 || given;               // else the state is zero, and the transition is not there
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
+    for (int i = 0; i < R; ++i) {
+      const int tile = w * R + i, row = 16 * tile + l16;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * g + r;
-        N[i][r] = 0.f;
-        if (live && row < m.dk) {
-          if (more) N[i][r] = here[(long long)row * m.dv + col];
-          here[(long long)row * m.dv + col] = S[i][r];
-        }
+        const int y = 16 * tile + 4 * g + r;
+        N[i][r] = live && y < m.dk ? here[y * m.dv + col] : 0.f;
       }
-    if (!more) break;
-    if (j > 0 || given)                             // else S is zero, and the transition is not there
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
+      for (int k = 0; k < M; ++k)
 #pragma unroll
-        for (int k = 0; k < M; ++k) {
-          f32x8 a;
-          const int row = 16 * i + l16;
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const int q = 32 * k + 16 * (r / 4) + 4 * g + r % 4;
-            a[r] = row < m.dk && q < m.dk ? tr[rev ? (long long)q * m.dk + row : (long long)row * m.dk + q] : 0.f;
-          }
-          N[i] = mma(a, pack_frag(S[2 * k], S[2 * k + 1], float()), N[i]);
+        for (int r = 0; r < 8; ++r) {
+          const int q = 32 * k + 16 * (r / 4) + 4 * g + r % 4;
+          a[i][k][r] = used && row < m.dk && q < m.dk ? tr[row * rs + q * cs] : 0.f;
         }
+    }
+  };
+  fetch(0);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) S[i] = N[i];
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int y = 16 * (w * R + i) + 4 * g + r;
+      S[i][r] = given && live && y < m.dk ? given[((long long)seq * m.H + h) * SE + y * m.dv + col] : 0.f;
+    }
+  for (int j = 0; j < n; ++j) {
+    float* const here = sums + ((long long)(slot + (rev ? n - 1 - j : j)) * m.H + h) * SE;
+    float* const buf = sS[j & 1];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int tile = w * R + i;
+      if (tile < NS) *reinterpret_cast<f32x4*>(buf + l16 * LS + split_place(16 * tile + 4 * g)) = S[i];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int y = 16 * tile + 4 * g + r;
+        if (live && y < m.dk) here[y * m.dv + col] = S[i][r];
+      }
+    }
+    if (j + 1 >= n) break;
+    __syncthreads();
+    f32x4 odd[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) odd[i] = zero4();
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      const f32x8 b = row_frag(buf + l16 * LS + 32 * k + 8 * g);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int r = 0; r < 8; r += 2) {
+          N[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][k][r], b[r], N[i], 0, 0, 0);
+          odd[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][k][r + 1], b[r + 1], odd[i], 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) S[i] = N[i] + odd[i];
+    if (j + 2 < n) fetch(j + 1);
   }
 }
 
@@ -661,30 +718,38 @@ hipError_t launch_prep_t(const DeltaArgs& a, bool backward, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int DK, int W, Walk kWhat>
+template <typename T, int DK, int W, int NT, Walk kWhat>
 hipError_t launch_walk_t(const DeltaArgs& a, bool backward, hipStream_t st) {
-  using TL = WalkTiles<T, DK, W, kWhat == Walk::output>;
-  hipError_t e = with_lds(delta_walk_kernel<T, DK, W, kWhat>, TL::bytes);
+  using TL = WalkTiles<T, DK, W, NT, kWhat == Walk::output>;
+  hipError_t e = with_lds(delta_walk_kernel<T, DK, W, NT, kWhat>, TL::bytes);
   if (e != hipSuccess) return e;
   const int blocks = (a.m.dv + 16 * W - 1) / (16 * W) + (kWhat == Walk::sums ? (a.m.dk + 16 * W - 1) / (16 * W) : 0);
   const long long units = (long long)a.m.n_slots * a.m.H;
-  launch_kernel(delta_walk_kernel<T, DK, W, kWhat>, grid_rows((units + 7) / 8 * 8 * blocks), 64 * W, TL::bytes, st, a,
+  launch_kernel(delta_walk_kernel<T, DK, W, NT, kWhat>, grid_rows((units + 7) / 8 * 8 * blocks), 64 * W, TL::bytes, st, a,
                 blocks, backward ? 1 : 0);
   return hipGetLastError();
 }
 
-template <Walk kWhat>
-hipError_t launch_walk_d(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st) {
+template <Walk kWhat, int NT>
+hipError_t launch_walk_bf16(const DeltaArgs& a, bool backward, hipStream_t st) {
   const int dk = a.m.dk;
-  if (!bf16) return dk <= 32 ? launch_walk_t<float, 32, 4, kWhat>(a, backward, st)
-                  : dk <= 64 ? launch_walk_t<float, 64, 4, kWhat>(a, backward, st)
-                             : launch_walk_t<float, 128, 4, kWhat>(a, backward, st);
   if (decay_columns(true, a.m.dv) == 128)
-    return dk <= 64 ? launch_walk_t<__bf16, 64, 8, kWhat>(a, backward, st)
-                    : launch_walk_t<__bf16, 128, 8, kWhat>(a, backward, st);
-  return dk <= 32 ? launch_walk_t<__bf16, 32, 4, kWhat>(a, backward, st)
-         : dk <= 64 ? launch_walk_t<__bf16, 64, 4, kWhat>(a, backward, st)
-                    : launch_walk_t<__bf16, 128, 4, kWhat>(a, backward, st);
+    return dk <= 64 ? launch_walk_t<__bf16, 64, 8, NT, kWhat>(a, backward, st)
+                    : launch_walk_t<__bf16, 128, 8, NT, kWhat>(a, backward, st);
+  return dk <= 32 ? launch_walk_t<__bf16, 32, 4, NT, kWhat>(a, backward, st)
+         : dk <= 64 ? launch_walk_t<__bf16, 64, 4, NT, kWhat>(a, backward, st)
+                    : launch_walk_t<__bf16, 128, 4, NT, kWhat>(a, backward, st);
+}
+
+// fine: states that the caller keeps, or gradients, in three terms.
+template <Walk kWhat>
+hipError_t launch_walk_d(const DeltaArgs& a, bool bf16, bool fine, bool backward, hipStream_t st) {
+  const int dk = a.m.dk;
+  if (!bf16) return dk <= 32 ? launch_walk_t<float, 32, 4, 1, kWhat>(a, backward, st)
+                  : dk <= 64 ? launch_walk_t<float, 64, 4, 1, kWhat>(a, backward, st)
+                             : launch_walk_t<float, 128, 4, 1, kWhat>(a, backward, st);
+  if constexpr (kWhat == Walk::states) return launch_walk_bf16<kWhat, 3>(a, backward, st);
+  return fine ? launch_walk_bf16<kWhat, 3>(a, backward, st) : launch_walk_bf16<kWhat, 2>(a, backward, st);
 }
 
 }  // namespace
@@ -698,19 +763,19 @@ hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool backward, hipSt
 }
 
 hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st) {
-  return launch_walk_d<Walk::sums>(a, bf16, backward, st);
+  return launch_walk_d<Walk::sums>(a, bf16, backward || a.fin, backward, st);
 }
 
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, hipStream_t st) {
-  return launch_walk_d<Walk::output>(a, bf16, false, st);
+  return launch_walk_d<Walk::output>(a, bf16, a.fin != nullptr, false, st);
 }
 
 hipError_t launch_delta_states(const DeltaArgs& a, bool bf16, hipStream_t st) {
-  return launch_walk_d<Walk::states>(a, bf16, true, st);
+  return launch_walk_d<Walk::states>(a, bf16, true, true, st);
 }
 
 hipError_t launch_delta_join(const DeltaArgs& a, bool backward, hipStream_t st) {
-  const int blocks = (a.m.dv + 63) / 64;
+  const int blocks = (a.m.dv + 15) / 16;
   const dim3 grid(blocks * a.m.H * (backward ? 2 : 1), a.m.n_seq);
   if (a.m.dk <= 32) launch_kernel(delta_join_kernel<32>, grid, kThreads, 0, st, a, blocks);
   else if (a.m.dk <= 64) launch_kernel(delta_join_kernel<64>, grid, kThreads, 0, st, a, blocks);

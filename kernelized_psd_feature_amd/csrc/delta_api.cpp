@@ -97,8 +97,7 @@ void place(kata::DeltaArgs& a, const kata::DeltaPlan& p, void* workspace) {
   a.m.L = p.L; a.m.n_seg = p.n_seg; a.m.n_chunks = p.n_chunks;
   a.m.n_slots = p.n_slots; a.m.c_slots = p.c_slots;
   a.vec = reinterpret_cast<float*>(ws + p.vec);
-  a.inv = ws + p.inv;
-  a.inv_t = ws + p.inv_t;
+  a.inv = reinterpret_cast<float*>(ws + p.inv);
   a.sums = reinterpret_cast<float*>(ws + p.sums);
   a.trans = reinterpret_cast<float*>(ws + p.trans);
   a.rsums = reinterpret_cast<float*>(ws + p.rsums);

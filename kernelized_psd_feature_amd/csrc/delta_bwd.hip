@@ -26,36 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;             // of the gradients' kernel
 
-// A strip of P for one wave: row tile rt, J key tiles from j0 on, times `scale`; zero by selection where the
-// key is later.  Rows of split places, the second term kC rows behind.
-template <typename T, int DK, int LK, int LP, int J>
-__device__ __forceinline__ void put_scores(T* sP, const T* sQ, const T* sK, const double* sc, int rt, int j0, int lane,
-                                           float scale) {
-  constexpr int M = DK / 32;
-  const int g = lane >> 4, l16 = lane & 15;
-  typename Elem<T>::frag qf[M];
-#pragma unroll
-  for (int i = 0; i < M; ++i) qf[i] = row_frag(sQ + (16 * rt + l16) * LK + 32 * i + 8 * g);
-  const double ci = sc[16 * rt + l16];
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    f32x4 p = zero4();
-    if (j0 + j <= rt) {                             // uniform
-#pragma unroll
-      for (int i = 0; i < M; ++i) p = mma(row_frag(sK + (16 * (j0 + j) + l16) * LK + 32 * i + 8 * g), qf[i], p);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int key = 16 * (j0 + j) + 4 * g + r;
-        p[r] = key > 16 * rt + l16 ? 0.f : p[r] * (exp64(ci - sc[key]) * scale);
-      }
-    }
-    T* const at = sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g);
-    const Quad<T> hi = quad(p, T());
-    *reinterpret_cast<Quad<T>*>(at) = hi;
-    if constexpr (kTerms<T> == 2) store4(at + kC * LP, p - unquad(hi));
-  }
-}
-
 // ---- the walk in reversed time ------------------------------------------------------------------
 template <typename T, int DK, int W>
 struct ReverseTiles {
@@ -63,24 +33,27 @@ struct ReverseTiles {
   static constexpr int DV = 16 * W;
   static constexpr int LK = DK + 16 / (int)sizeof(T), LV = DV + (kBf ? 16 : 4), LP = kC + 16 / (int)sizeof(T);
   static constexpr int kHead = 16 + kDeltaVec * 4;
+  static constexpr int NT = kBf ? 3 : 1, NP = kBf ? 2 : 1;              // terms of the recurrence's operands, of P
   static constexpr int kTiles = kC * (2 * LK + LV);
-  static constexpr int bytes = kHead + (kTiles + kTerms<T> * kC * LP) * (int)sizeof(T);
+  static constexpr int bytes = kHead + (kTiles + (NT + NP) * kC * LP) * (int)sizeof(T);
+  static constexpr int occupancy = !kBf && DK == 128 ? 1 : 8 / W;
 };
 
 // kSums: of the segments, from a gradient of zero behind them.
 template <typename T, int DK, int W, bool kSums>
-__global__ __launch_bounds__(64 * W) void delta_reverse_kernel(DeltaArgs A, int blocks) {
+__global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void delta_reverse_kernel(DeltaArgs A, int blocks) {
   using TL = ReverseTiles<T, DK, W>;
   using frag = typename Elem<T>::frag;
   constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
+  constexpr int NT = TL::NT, NP = TL::NP;
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
-  const double* const sc = reinterpret_cast<const double*>(vec + 3 * kC);
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
   T* const sQ = sK + kC * LK;
   T* const sO = sQ + kC * LK;
-  T* const sP = sO + kC * LV;
+  T* const sT = sK + TL::kTiles;
+  T* const sP = sT + NT * kC * LP;
 
   const DeltaMap& m = A.m;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
@@ -114,6 +87,7 @@ __global__ __launch_bounds__(64 * W) void delta_reverse_kernel(DeltaArgs A, int 
   const T* px = reinterpret_cast<const T*>(A.dO) + s.b * A.sdo[0] + row0 * A.sdo[1] + h * A.sdo[2] + c0;
   Stage<T, DK, kThr> rk(pk, A.sk[1], m.dk, true), rq(pq, A.sq[1], m.dk, true);
   Stage<T, DV, kThr> ro(px, A.sdo[1], m.dv - c0, false);
+  StageInv<T, NT, LP, kThr> ri;
   uint4 vec_next;
   const long long chunk0 = (long long)s.c_slot * m.H + h;              // [c_slots][H]
   auto fetch = [&](int c) {
@@ -124,41 +98,30 @@ __global__ __launch_bounds__(64 * W) void delta_reverse_kernel(DeltaArgs A, int 
     rk.p -= 2 * kC * A.sk[1];
     rq.p -= 2 * kC * A.sq[1];
     ro.p -= 2 * kC * A.sdo[1];
+    ri.fetch(A.inv + (chunk0 + (long long)c * m.H) * kInvFloats);
     if (tid < kDeltaVec / 4)
       vec_next = reinterpret_cast<const uint4*>(A.vec + (chunk0 + (long long)c * m.H) * kDeltaVec)[tid];
   };
-  Op<T> inv[kInvFrags];
-  auto fetch_inv = [&](int c) {
-    const T* at = reinterpret_cast<const T*>(A.inv_t) + (chunk0 + (long long)c * m.H) * kInvElems<T>;
-#pragma unroll
-    for (int f = 0; f < kInvFrags; ++f) load_inv<T>(at, f, lane, inv[f]);
-  };
   fetch(behind - 1);
-  fetch_inv(behind - 1);
 
   const int wc = 16 * w, col = c0 + wc + l16;
+  const float* given = kSums ? nullptr : !last_seg ? A.rsums + ((long long)slot * m.H + h) * SE : A.dfin ? A.dfin + st_off : nullptr;
   f32x4 D[NS];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    D[i] = zero4();
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * i + 4 * g + r;
-      if (!kSums && row < m.dk && col < m.dv) {
-        if (!last_seg) D[i][r] = A.rsums[((long long)slot * m.H + h) * SE + (long long)row * m.dv + col];
-        else if (A.dfin) D[i][r] = A.dfin[st_off + (long long)row * m.dv + col];
-      }
-    }
-  }
+  for (int i = 0; i < NS; ++i) D[i] = zero4();
+  if (given) load_state(D, given, m.dk, m.dv, col, g);                 // uniform
   if (m.dk < DK || m.dv - c0 < DV) {
     uint4* const z = reinterpret_cast<uint4*>(sK);
     for (int i = tid; i < TL::kTiles * (int)sizeof(T) / 16; i += kThr) z[i] = uint4{0u, 0u, 0u, 0u};
   }
+  ri.zeros(sT);
+#pragma unroll 1
   for (int c = behind - 1; c >= first; --c) {
     __syncthreads();                                // the last chunk's tiles have been read
     rk.template put_split<LK>(sK);
     rq.template put_split<LK>(sQ);
     ro.template put<LV>(sO);
+    ri.put(sT);
     if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
     if (c > first) fetch(c - 1);
     __syncthreads();
@@ -167,8 +130,8 @@ __global__ __launch_bounds__(64 * W) void delta_reverse_kernel(DeltaArgs A, int 
 #pragma unroll
       for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(dst + i * 256) = D[i];
     }
-    put_scores<T, DK, LK, LP, 16 / W>(sP, sQ, sK, sc, w & 3, 16 / W * (w >> 2), lane, A.scale);
-    Op<T> df[M];
+    put_scores<T, DK, LK, LP, 16 / W, NP>(sP, sQ, sK, vec + 3 * kC, w & 3, 16 / W * (w >> 2), lane, A.scale);
+    Op<T, NT> df[M];
 #pragma unroll
     for (int i = 0; i < M; ++i) split_terms(D[2 * i], D[2 * i + 1], df[i]);
     f32x4 Z[4], X[4];
@@ -176,7 +139,7 @@ __global__ __launch_bounds__(64 * W) void delta_reverse_kernel(DeltaArgs A, int 
     for (int it = 0; it < 4; ++it) {
       Z[it] = zero4();
 #pragma unroll
-      for (int i = 0; i < M; ++i) Z[it] = mul<T>(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), df[i], Z[it]);
+      for (int i = 0; i < M; ++i) Z[it] = mul(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), df[i], Z[it]);
       Z[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
     }
     frag of[2];
@@ -186,23 +149,19 @@ __global__ __launch_bounds__(64 * W) void delta_reverse_kernel(DeltaArgs A, int 
 #pragma unroll
     for (int it = 0; it < 4; ++it)
 #pragma unroll
-      for (int i = it >> 1; i < 2; ++i) {
-        Op<T> pf;
-#pragma unroll
-        for (int t = 0; t < kTerms<T>; ++t) pf.t[t] = split_column_frag<LP>(sP + (t * kC + 32 * i) * LP, it, lane);
-        Z[it] = mul<T>(pf, of[i], Z[it]);
-      }
-    Op<T> zf[2];
+      for (int i = it >> 1; i < 2; ++i)
+        Z[it] = mul(split_column_op<NP, LP>(sP + 32 * i * LP, kC * LP, it, lane), of[i], Z[it]);
+    Op<T, NT> zf[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) split_terms(Z[2 * i], Z[2 * i + 1], zf[i]);
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       X[it] = zero4();
 #pragma unroll
-      for (int i = it >> 1; i < 2; ++i) X[it] = mul<T>(inv[inv_t_frag(it, i)], zf[i], X[it]);
+      for (int i = it >> 1; i < 2; ++i)
+        X[it] = mul(split_column_op<NT, LP>(sT + 32 * i * LP, kC * LP, it, lane), zf[i], X[it]);
     }
-    if (c > first) fetch_inv(c - 1);
-    Op<T> kw[2], qw[2];
+    Op<T, NT> kw[2], qw[2];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
@@ -220,8 +179,8 @@ __global__ __launch_bounds__(64 * W) void delta_reverse_kernel(DeltaArgs A, int 
       D[i] *= whole;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        D[i] = mul<T>(split_column_frag<LK>(sQ + 32 * j * LK, i, lane), qw[j], D[i]);
-        D[i] = mul<T>(split_column_frag<LK>(sK + 32 * j * LK, i, lane), kw[j], D[i]);
+        D[i] = mul(split_column_frag<LK>(sQ + 32 * j * LK, i, lane), qw[j], D[i]);
+        D[i] = mul(split_column_frag<LK>(sK + 32 * j * LK, i, lane), kw[j], D[i]);
       }
     }
   }
@@ -244,11 +203,12 @@ struct GradTiles {
   static constexpr int PAD = 16 / (int)sizeof(T);
   static constexpr int LK = DK + PAD, LO = 64 + PAD, LV = 64 + (kBf ? 16 : 4), LP = kC + PAD, LS = DK + PAD;
   static constexpr int kHead = 16 + kDeltaVec * 4 + 2 * 4 * kC * 4 + 16;   // an int, vec, dots, sums of the waves
+  static constexpr int NT = kBf ? 3 : 1, NP = kBf ? 2 : 1;              // terms of the recurrence's operands, of P
   static constexpr int kStateTile = 64 * LS, kPair = 2 * 64 * LP;
   // scores, then (bf16) the second terms of U and dv, or (fp32) the state, then PO and PV
   static constexpr int kA = kBf || kPair > kStateTile ? kPair : kStateTile;
-  static constexpr int bytes = kHead + (kC * (2 * LK + LO) + kA + kPair + (kBf ? kStateTile : 0)) * (int)sizeof(T);
-  static_assert(64 * LV <= kPair, "V lies where U and dv come");
+  static constexpr int bytes = kHead + (kC * (2 * LK + LO) + kA + kPair + (kBf ? kStateTile + NT * kC * LP : 0)) * (int)sizeof(T);
+  static_assert(64 * LV <= (kBf ? kPair : kPair / 2), "V lies where U (bf16: and dv) come, the inverse (fp32) where dv comes");
 };
 
 __device__ __forceinline__ float sum16(float x) {   // over the 16 lanes of a group
@@ -258,7 +218,7 @@ __device__ __forceinline__ float sum16(float x) {   // over the 16 lanes of a gr
 }
 
 template <typename T, int DK>
-__global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void delta_grads_kernel(DeltaArgs A) {
+__global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
   using TL = GradTiles<T, DK>;
   using frag = typename Elem<T>::frag;
   constexpr int M = DK / 32, NS = DK / 16, LK = TL::LK, LO = TL::LO, LV = TL::LV, LP = TL::LP, LS = TL::LS;
@@ -266,7 +226,8 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
-  const double* const sc = reinterpret_cast<const double*>(vec + 3 * kC);
+  const float* const sc = vec + 3 * kC;
+  constexpr int NT = TL::NT, NP = TL::NP;
   float* const sE = vec + kDeltaVec;                // [4][64] dO . o - dv . v, then [4][64] X . U
   float* const sF = sE + 2 * 4 * kC;                // [4] <D, S'>
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
@@ -276,6 +237,7 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
   T* const sU = sA + TL::kA;                        // V, then U and dv
   T* const sZ = sU + 64 * LP;
   T* const sS = kBf ? sZ + 64 * LP : sA;
+  T* const sT = kBf ? sS + TL::kStateTile : sZ;
 
   const DeltaMap& m = A.m;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
@@ -348,6 +310,8 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
                                 A.sv[1], m.dv - c0, false);
       fetch_rows(ro, A.sdo[1], n);
       fetch_rows(rv, A.sv[1], n);
+      StageInv<T, NT, LP, kThreads> ri;
+      ri.fetch(A.inv + cs * kInvFloats);
       f32x4 S[NS], D[NS];
       const bool live_tile = 4 * vb + w < ct;       // uniform
 #pragma unroll
@@ -372,14 +336,16 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
       }
       ro.template put_split<LO>(sO);
       rv.template put<LV>(sU);
+      ri.put(sT);
+      ri.zeros(sT);
       __syncthreads();
 
       // a wave's 16 columns
-      put_scores<T, DK, LK, LP, 4>(sA, sQ, sK, sc, w, 0, lane, A.scale);
+      put_scores<T, DK, LK, LP, 4, NP>(sA, sQ, sK, sc, w, 0, lane, A.scale);
       const int wc = 16 * w;
       f32x4 U[4], X[4], V[4];
       {
-        Op<T> sf[M], df[M];
+        Op<T, NT> sf[M], df[M];
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           split_terms(S[2 * i], S[2 * i + 1], sf[i]);
@@ -391,8 +357,6 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
           vf[i] = column_frag<LV>(sU + 32 * i * LV + wc, lane);
           of[i] = split_column_frag<LO>(sO + 32 * i * LO, w, lane);
         }
-        const T* inv = reinterpret_cast<const T*>(A.inv) + cs * kInvElems<T>;
-        const T* inv_t = reinterpret_cast<const T*>(A.inv_t) + cs * kInvElems<T>;
         f32x4 Z[4], o[4];
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -400,9 +364,9 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
 #pragma unroll
           for (int i = 0; i < M; ++i) {
             const frag kf = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
-            X[it] = mul<T>(kf, sf[i], X[it]);
-            Z[it] = mul<T>(kf, df[i], Z[it]);
-            o[it] = mul<T>(row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], o[it]);
+            X[it] = mul(kf, sf[i], X[it]);
+            Z[it] = mul(kf, df[i], Z[it]);
+            o[it] = mul(row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], o[it]);
           }
           const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
           V[it] = half_of(vf[it >> 1], it & 1);
@@ -410,18 +374,15 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
           Z[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
           o[it] *= yv * A.scale;
         }
-        Op<T> xf[2];
+        Op<T, NT> xf[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) split_terms(X[2 * i], X[2 * i + 1], xf[i]);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
           U[it] = zero4();
 #pragma unroll
-          for (int i = 0; i <= it >> 1; ++i) {
-            Op<T> a;
-            load_inv<T>(inv, inv_frag(it, i), lane, a);
-            U[it] = mul<T>(a, xf[i], U[it]);
-          }
+          for (int i = 0; i <= it >> 1; ++i)
+            U[it] = mul(row_op<NT>(sT + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), xf[i], U[it]);
         }
         // <D, S'>, S' = y_63 S + K^T diag(exp(c_63 - c)) U
         {
@@ -436,7 +397,7 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
 #pragma unroll
             for (int r = 0; r < 4; ++r) frob = fmaf(U[it][r], Z[it][r], frob);
         }
-        Op<T> uf[2], zf[2];
+        Op<T, NT> uf[2], zf[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
         __syncthreads();                            // P is there, and V has been read
@@ -444,17 +405,8 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
         for (int it = 0; it < 4; ++it) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            Op<T> pf;
-            if (i <= it >> 1) {
-#pragma unroll
-              for (int t = 0; t < kTerms<T>; ++t) pf.t[t] = row_frag(sA + (t * kC + 16 * it + l16) * LP + 32 * i + 8 * g);
-              o[it] = mul<T>(pf, uf[i], o[it]);
-            }
-            if (i >= it >> 1) {
-#pragma unroll
-              for (int t = 0; t < kTerms<T>; ++t) pf.t[t] = split_column_frag<LP>(sA + (t * kC + 32 * i) * LP, it, lane);
-              Z[it] = mul<T>(pf, of[i], Z[it]);
-            }
+            if (i <= it >> 1) o[it] = mul(row_op<NP>(sA + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), uf[i], o[it]);
+            if (i >= it >> 1) Z[it] = mul(split_column_op<NP, LP>(sA + 32 * i * LP, kC * LP, it, lane), of[i], Z[it]);
           }
         }
 #pragma unroll
@@ -463,17 +415,15 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
         for (int it = 0; it < 4; ++it) {
           X[it] = zero4();
 #pragma unroll
-          for (int i = it >> 1; i < 2; ++i) {
-            Op<T> a;
-            load_inv<T>(inv_t, inv_t_frag(it, i), lane, a);
-            X[it] = mul<T>(a, zf[i], X[it]);
-          }
+          for (int i = it >> 1; i < 2; ++i)
+            X[it] = mul(split_column_op<NT, LP>(sT + 32 * i * LP, kC * LP, it, lane), zf[i], X[it]);
           db[it] += X[it] * U[it];
           X[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
           e[it] += o[it] * half_of(of[it >> 1], it & 1) - X[it] * V[it];
         }
       }
       // U, dv and the state through LDS
+      __syncthreads();                              // P and (fp32) the inverse have been read
       T* const mine = sU + (wc + l16) * LP + 4 * g;
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
@@ -485,7 +435,6 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
           X[it] -= unquad(z);
         }
       }
-      __syncthreads();                              // P has been read
       if constexpr (kBf)
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -499,23 +448,25 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
       // a wave's 16 tokens
       frag ur[2], zr[2];
       {
-        Op<T> zt[2], ot[2];
+        constexpr int NW = kBf ? 2 : 1;             // terms of U and dv
+        Op<T, NW> zt[2];
+        frag ot[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           zt[i].t[0] = zr[i] = column_frag<LP>(sZ + 32 * i * LP + 16 * w, lane);
           if constexpr (kBf) zt[i].t[1] = column_frag<LP>(sA + (64 + 32 * i) * LP + 16 * w, lane);
-          ot[i].t[0] = row_frag(sO + (16 * w + l16) * LO + 32 * i + 8 * g);
+          ot[i] = row_frag(sO + (16 * w + l16) * LO + 32 * i + 8 * g);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (j <= w)                               // uniform
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              Op<T> ut;
+              Op<T, NW> ut;
               ut.t[0] = column_frag<LP>(sU + 32 * i * LP + 16 * j, lane);
               if constexpr (kBf) ut.t[1] = column_frag<LP>(sA + 32 * i * LP + 16 * j, lane);
-              WO[j] = mul<T>(ut, ot[i].t[0], WO[j]);
-              WV[j] = mul<T>(ut, zt[i], WV[j]);
+              WO[j] = mul(ut, ot[i], WO[j]);
+              WV[j] = mul(ut, zt[i], WV[j]);
               if (j == w) ur[i] = ut.t[0];
             }
         const float yr = vec[16 * w + l16], yo = yr * A.scale;
@@ -525,7 +476,7 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const frag st = column_frag<LS>(sS + 32 * j * LS + 16 * i, lane);
-            a = mma(st, ot[j].t[0], a);
+            a = mma(st, ot[j], a);
             b = mma(st, zr[j], b);
           }
           dqa[i] += a * yo;
@@ -571,7 +522,7 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
     __syncthreads();                                // (the second terms and D have been read, too)
     // PO and PV, the wave's strip of rows
     {
-      const double ci = sc[16 * w + l16];
+      const float hi = sc[16 * w + l16], lo = sc[kC + 16 * w + l16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f32x4 po = zero4(), pv = zero4();
@@ -579,7 +530,7 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int key = 16 * j + 4 * g + r, row = 16 * w + l16;
-            const float x = exp64(ci - sc[key]);
+            const float x = exp2_diff(hi, lo, sc[key], sc[kC + key]);
             po[r] = key > row ? 0.f : WO[j][r] * (x * A.scale);
             pv[r] = key >= row ? 0.f : -WV[j][r] * x;
           }
@@ -601,7 +552,7 @@ __global__ __launch_bounds__(kThreads, DK == 128 || sizeof(T) == 4 ? 1 : 2) void
         }
         x += (double)sF[0] + sF[1] + sF[2] + sF[3];
         // a decay of nothing, and one of zero (in fp32), have no gradient
-        const bool none = (s.part == 0 && lane == 0 && !A.init) || sc[lane] - (lane ? sc[lane - 1] : 0.0) < -104.0;
+        const bool none = (s.part == 0 && lane == 0 && !A.init) || sc[lane] - (lane ? sc[lane - 1] : 0.f) < -150.f;
         if (lane < n) A.dlog[at] = none ? 0.f : (float)x;
       }
     }

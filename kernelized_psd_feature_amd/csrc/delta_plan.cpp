@@ -49,7 +49,7 @@ kata_status check_delta_problem(const kata_delta_problem* pr, int most, bool bac
   return check_strides("o", pr->so, sizes, pr->dv, true, why);
 }
 
-constexpr size_t kVecBytes = 1280, kInvBytes = 12288;   // of a chunk and head (delta_tiles.h)
+constexpr size_t kVecBytes = 1280, kInvBytes = 10240;   // of a chunk and head (delta_tiles.h)
 
 }  // namespace
 
@@ -97,7 +97,6 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
   }
   if (backward) {
     if (p.n_seg > 1) p.rsums = part(s * state);
-    p.inv_t = part(c * kInvBytes);
     const size_t DK = pr->dk <= 32 ? 32 : pr->dk <= 64 ? 64 : 128;
     const size_t chunk_state = DK * 16 * ((pr->dv + 15) / 16) * 4;
     p.cstates = part(c * chunk_state);

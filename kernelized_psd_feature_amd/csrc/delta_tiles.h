@@ -8,49 +8,74 @@
 
 namespace kata {
 
-// Floats that a chunk and head keep in the workspace: exp(c), exp(c_63 - c), beta and c itself (double)
-// of every token, c being the sum of the log decays from the chunk's first token on.
-constexpr int kDeltaVec = 3 * kC + 2 * kC;
+// What a chunk and head keep in the workspace.  Vectors: exp(c), exp(c_63 - c), beta, and c log2(e) as the sum
+// of two floats, of every token, c being the sum of the log decays from the chunk's first token on.
+// Inverse: its 16 x 16 blocks on and below the diagonal, by rows of blocks.
+constexpr int kDeltaVec = 5 * kC, kInvBlocks = 10, kInvFloats = kInvBlocks * 256;
 
-// bf16 operands that come out of fp32 sums are kept as two terms, hi + lo, which hold 2^-18 of the value:
-// the recurrence passes a rounding on from chunk to chunk, and states are fp32.  fp32: one term.
-template <typename T>
-constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
+// 2^(hi + lo) of the difference of two such sums
+__device__ __forceinline__ float exp2_diff(float hi, float lo, float hj, float lj) {
+  return __builtin_amdgcn_exp2f((hi - hj) + (lo - lj));
+}
 
-template <typename T>
+// bf16 operands that come out of fp32 sums are kept as N bf16 terms that add up to them: the recurrence passes
+// a rounding on from chunk to chunk, and states are fp32.  Two terms hold 2^-18 of a value, three 2^-27.
+// fp32: one.
+template <typename T, int N>
 struct Op {
-  typename Elem<T>::frag t[kTerms<T>];
+  typename Elem<T>::frag t[N];
 };
 
-__device__ __forceinline__ void split_terms(const f32x4& a, const f32x4& b, Op<__bf16>& out) {
-  const uint2 x = quad(a, __bf16()), y = quad(b, __bf16());
-  out.t[0] = __builtin_bit_cast(bf16x8, uint4{x.x, x.y, y.x, y.y});
-  out.t[1] = pack_frag(a - unquad(x), b - unquad(y), __bf16());
+template <int N>
+__device__ __forceinline__ void split_terms(f32x4 a, f32x4 b, Op<__bf16, N>& out) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint2 x = quad(a, __bf16()), y = quad(b, __bf16());
+    out.t[i] = __builtin_bit_cast(bf16x8, uint4{x.x, x.y, y.x, y.y});
+    if (i + 1 < N) {
+      a -= unquad(x);
+      b -= unquad(y);
+    }
+  }
 }
-__device__ __forceinline__ void split_terms(const f32x4& a, const f32x4& b, Op<float>& out) {
+__device__ __forceinline__ void split_terms(const f32x4& a, const f32x4& b, Op<float, 1>& out) {
   out.t[0] = pack_frag(a, b, float());
 }
 
-// c + a b with an exact a, and with both in terms (what two second terms give is left out)
-template <typename T>
-__device__ __forceinline__ f32x4 mul(const typename Elem<T>::frag& a, const Op<T>& b, f32x4 c) {
+// c + a b with an exact operand, and with both in terms (products of order max(N, K) and above are left out)
+template <typename F, typename T, int N>
+__device__ __forceinline__ f32x4 mul(const F& a, const Op<T, N>& b, f32x4 c) {
 #pragma unroll
-  for (int i = kTerms<T> - 1; i >= 0; --i) c = mma(a, b.t[i], c);
+  for (int i = N - 1; i >= 0; --i) c = mma(a, b.t[i], c);
   return c;
 }
-template <typename T>
-__device__ __forceinline__ f32x4 mul(const Op<T>& a, const typename Elem<T>::frag& b, f32x4 c) {
+template <typename F, typename T, int N>
+__device__ __forceinline__ f32x4 mul(const Op<T, N>& a, const F& b, f32x4 c) {
 #pragma unroll
-  for (int i = kTerms<T> - 1; i >= 0; --i) c = mma(a.t[i], b, c);
+  for (int i = N - 1; i >= 0; --i) c = mma(a.t[i], b, c);
   return c;
 }
-template <typename T>
-__device__ __forceinline__ f32x4 mul(const Op<T>& a, const Op<T>& b, f32x4 c) {
-  if constexpr (kTerms<T> == 2) {
-    c = mma(a.t[1], b.t[0], c);
-    c = mma(a.t[0], b.t[1], c);
+template <typename T, int N, int K>
+__device__ __forceinline__ f32x4 mul(const Op<T, N>& a, const Op<T, K>& b, f32x4 c) {
+  constexpr int most = N > K ? N : K;
+#pragma unroll
+  for (int order = most - 1; order >= 0; --order)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (order - i >= 0 && order - i < K) c = mma(a.t[i], b.t[order - i], c);
+  return c;
+}
+
+// Four neighbouring elements of a row as N planes of them, `plane` elements apart.
+template <int N, typename T>
+__device__ __forceinline__ void put_terms(T* at, int plane, f32x4 x) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const Quad<T> u = quad(x, T());
+    *reinterpret_cast<Quad<T>*>(at + i * plane) = u;
+    if constexpr (sizeof(T) == 2)
+      if (i + 1 < N) x -= unquad(u);
   }
-  return mma(a.t[0], b.t[0], c);
 }
 
 // Split slots of column i (the lane's place in its group of 16) of columns 16 tile .. of 32 rows of LD elements
@@ -80,25 +105,102 @@ __device__ __forceinline__ f32x4 half_of(const f32x8& x, int half) {
   return half ? f32x4{x[4], x[5], x[6], x[7]} : f32x4{x[0], x[1], x[2], x[3]};
 }
 
-// Operands of the inverse [row tile it][K step m] (its K step 32 m .. of the columns; of the transpose the rows)
-// that are not all zero, in the order in which the workspace holds them: kTerms planes of one fragment a lane.
-constexpr int kInvFrags = 6;
-__device__ __forceinline__ constexpr int inv_frag(int it, int m) { return it < 2 ? it : 2 * (it - 1) + m; }
-__device__ __forceinline__ constexpr int inv_t_frag(int it, int m) { return it < 2 ? 2 * it + m : 2 + it; }
-template <typename T>
-constexpr int kInvElems = kInvFrags * kTerms<T> * 64 * 8;
-
-template <typename T>
-__device__ __forceinline__ void load_inv(const T* base, int frag, int lane, Op<T>& out) {
+// The N planes of a row's or (rows in split places) a column tile's operand, planes `plane` elements apart.
+template <int N, typename T>
+__device__ __forceinline__ Op<T, N> row_op(const T* p, int plane) {
+  Op<T, N> x;
 #pragma unroll
-  for (int t = 0; t < kTerms<T>; ++t) out.t[t] = row_frag(base + ((frag * kTerms<T> + t) * 64 + lane) * 8);
+  for (int i = 0; i < N; ++i) x.t[i] = row_frag(p + i * plane);
+  return x;
+}
+template <int N, int LD, typename T>
+__device__ __forceinline__ Op<T, N> split_column_op(const T* p, int plane, int tile, int lane) {
+  Op<T, N> x;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x.t[i] = split_column_frag<LD>(p + i * plane, tile, lane);
+  return x;
 }
 
-// exp(x), the exponent held in 64 bits: its fp32 rounding would cost |x| 2^-24.
-__device__ __forceinline__ float exp64(double x) {
-  const double y = x * 1.4426950408889634;
-  const float hi = (float)y;
-  return exp2f(hi) * (1.f + 0.69314718f * (float)(y - hi));
+// The inverse of a chunk from the workspace into N planes [64][LD] of LDS, rows of split places.  zeros(): the
+// two blocks above the diagonal that share a K step with one below it, written once.
+template <typename T, int N, int LD, int kThr>
+struct StageInv {
+  static constexpr int kVecs = kInvFloats / 4, R = (kVecs + kThr - 1) / kThr;
+  f32x4 x[R];
+  __device__ __forceinline__ void fetch(const float* p) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int v = threadIdx.x + i * kThr;
+      if (kVecs % kThr == 0 || v < kVecs) x[i] = reinterpret_cast<const f32x4*>(p)[v];
+    }
+  }
+  __device__ __forceinline__ static void zeros(T* tile) {
+    for (int v = threadIdx.x; v < 128; v += kThr)
+      put_terms<N>(tile + (32 * (v >> 6) + ((v >> 2) & 15)) * LD + split_place(32 * (v >> 6) + 16 + 4 * (v & 3)), kC * LD, zero4());
+  }
+  __device__ __forceinline__ void put(T* tile) const {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int v = threadIdx.x + i * kThr, block = v >> 6, row = (v >> 2) & 15;
+      const int bi = (block >= 1) + (block >= 3) + (block >= 6), bj = block - bi * (bi + 1) / 2;
+      if (kVecs % kThr == 0 || v < kVecs)
+        put_terms<N>(tile + (16 * bi + row) * LD + split_place(16 * bj + 4 * (v & 3)), kC * LD, x[i]);
+    }
+  }
+};
+
+// Products q . k of a wave's strip (transposed: lane's row 16 rt + l16, keys 16 (j0 + j) + 4 g + r) become its part
+// of P, times `scale`; zero by selection where the key is later.  c: the logarithms' two floats.  Rows of
+// split places, N planes.
+template <typename T, int LP, int J, int N>
+__device__ __forceinline__ void put_weights(T* sP, f32x4 (&p)[J], const float* c, int rt, int j0, int lane, float scale) {
+  const int g = lane >> 4, l16 = lane & 15;
+  const float hi = c[16 * rt + l16], lo = c[kC + 16 * rt + l16];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    f32x4 x = zero4();
+    if (j0 + j <= rt) {                             // uniform
+      const f32x4 hj = *reinterpret_cast<const f32x4*>(c + 16 * (j0 + j) + 4 * g);
+      const f32x4 lj = *reinterpret_cast<const f32x4*>(c + kC + 16 * (j0 + j) + 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        x[r] = 16 * (j0 + j) + 4 * g + r > 16 * rt + l16 ? 0.f : p[j][r] * (exp2_diff(hi, lo, hj[r], lj[r]) * scale);
+    }
+    put_terms<N>(sP + (16 * rt + l16) * LP + split_place(16 * (j0 + j) + 4 * g), kC * LP, x);
+  }
+}
+template <typename T, int DK, int LK, int LP, int J, int N>
+__device__ __forceinline__ void put_scores(T* sP, const T* sQ, const T* sK, const float* c, int rt, int j0, int lane,
+                                           float scale) {
+  constexpr int M = DK / 32;
+  const int g = lane >> 4, l16 = lane & 15;
+  f32x4 p[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) p[j] = zero4();
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const auto q = row_frag(sQ + (16 * rt + l16) * LK + 32 * i + 8 * g);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (j0 + j <= rt) p[j] = mma(row_frag(sK + (16 * (j0 + j) + l16) * LK + 32 * i + 8 * g), q, p[j]);
+  }
+  put_weights<T, LP, J, N>(sP, p, c, rt, j0, lane, scale);
+}
+
+// State tiles of columns col (the lane's): S[i] has rows 16 i + 4 g + r; zeros behind the state's rows and columns.
+// (Loads from clamped places and a selection: under a condition each they cost the registers of as many branches.)
+template <int NS>
+__device__ __forceinline__ void load_state(f32x4 (&S)[NS], const float* p, int rows, int cols, int col, int g) {
+  const float* const at = p + min(col, cols - 1);
+  const bool live = col < cols;
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * g + r;
+      const float x = at[min(row, rows - 1) * cols];
+      S[i][r] = live && row < rows ? x : 0.f;
+    }
 }
 
 // ---- sequences -------------------------------------------------------------------------------
