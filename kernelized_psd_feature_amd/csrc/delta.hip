@@ -186,7 +186,8 @@ struct WalkTiles {
   static constexpr int kHead = 16 + kDeltaVec * 4;
   static constexpr int kTiles = kC * (LK * (kOut ? 2 : 1) + LV);
   static constexpr int kPO = kBf ? 2 : 1;           // terms of the outputs' operands
-  static constexpr int bytes = kHead + (kTiles + (NT + (kOut ? kPO : 0)) * kC * LP) * (int)sizeof(T);
+  static constexpr int NI = kBf ? 2 : 1;            // terms of the inverse
+  static constexpr int bytes = kHead + (kTiles + (NI + (kOut ? kPO : 0)) * kC * LP) * (int)sizeof(T);
   // waves a SIMD that the registers are held to (the launch bound counts workgroups a CU)
   static constexpr int occupancy = !kBf && DK == 128 ? 1 : 8 / W;
 };
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
   using TL = WalkTiles<T, DK, W, NT, kOut>;
   using frag = typename Elem<T>::frag;
   constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
-  constexpr int PO = TL::kPO, J = 16 / W;           // terms of the outputs' operands; key tiles of a wave's part of P
+  constexpr int NI = TL::NI, PO = TL::kPO, J = 16 / W;            // J: key tiles of a wave's part of P
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
@@ -208,7 +209,7 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
   T* const sV = sK + kC * LK;
   T* const sQ = sV + kC * LV;
   T* const sT = sK + TL::kTiles;
-  T* const sP = sT + NT * kC * LP;
+  T* const sP = sT + NI * kC * LP;
 
   const DeltaMap& m = A.m;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
   Stage<T, DK, kThr> rq(reinterpret_cast<const T*>(kOut ? A.q : A.k) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2], A.sq[1], m.dk, true);
   Stage<T, DV, kThr> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + (unit_matrix ? 0 : c0),
                         A.sv[1], m.dv - (unit_matrix ? 0 : c0), false);
-  StageInv<T, NT, LP, kThr> ri;
+  StageInv<T, NI, LP, kThr> ri;
   const int n_last = min(kC, s.len - kC * (behind - 1));
   uint4 vec_next;
   const long long chunk0 = (long long)(s.c_slot + first) * m.H + h;    // [c_slots][H]
@@ -307,6 +308,14 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
   float* p_state = nullptr;
   if (kWhat == Walk::states && c0 / 16 + w < ct) p_state = A.cstates + (chunk0 * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
 
+  Quad<T> O[4];                                     // outputs of the last chunk
+  auto store = [&](int rows) {
+    if (live_col)
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+        if (16 * it + l16 < rows) *reinterpret_cast<Quad<T>*>(po + 16 * it * A.so[1]) = O[it];
+    po += kC * A.so[1];
+  };
 #pragma unroll 1
   for (int c = first; c < behind; ++c) {
     __syncthreads();                                // the last chunk's tiles have been read
@@ -315,44 +324,61 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
     if (!unit_matrix) rv.template put<LV>(sV);
     ri.put(sT);
     if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
-    if (c + 1 < behind) fetch(c + 1);
-    __syncthreads();
-
+    // (stores before the next loads: the wait for these then does not wait for stores just issued)
     if (kWhat == Walk::states && p_state) {         // uniform
 #pragma unroll
       for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(p_state + i * 256) = S[i];
       p_state += (long long)m.H * ct * (DK * 16);
     }
+    if (kOut && c > first) store(kC);
+    if (c + 1 < behind) fetch(c + 1);
+    __syncthreads();
+
     // LDS reads are issued in batches, ahead of the work that hides them (reads_above): left alone, the compiler
     // waits for nearly every read before its product.
     f32x4 X[4], U[4], o[4];
-    Op<T, NT> inv[6];                               // (row tile, K step): (0, 0), (1, 0), (2, 0), (2, 1), (3, 0), (3, 1)
-    auto read_inv = [&](int from, int to) {         // planes
+    Op<T, NI> inv[6];                               // (row tile, K step): (0, 0), (1, 0), (2, 0), (2, 1), (3, 0), (3, 1)
+    auto read_inv = [&] {
 #pragma unroll
       for (int f = 0; f < 6; ++f)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (t >= from && t < to)
-            inv[f].t[t] = row_frag(sT + t * kC * LP + (16 * (f < 2 ? f : 1 + f / 2) + l16) * LP + (f < 2 ? 0 : 32 * (f & 1)) + 8 * g);
+        inv[f] = row_op<NI>(sT + (16 * (f < 2 ? f : 1 + f / 2) + l16) * LP + (f < 2 ? 0 : 32 * (f & 1)) + 8 * g, kC * LP);
     };
-    constexpr int kEarly = M > 2 ? 0 : NT > 2 ? 2 : NT;                // planes that there are registers for
     frag vf[2];
-    {
-      frag kr[4][M], qr[M];
+    if constexpr (kOut) {
+      Op<T, NT> sf[M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
+      // bf16: with two terms of the state, of P and of U an output has no error but its own rounding
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        X[it] = o[it] = zero4();
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          X[it] = mul(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], X[it]);
+          const frag q = row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g);
+#pragma unroll
+          for (int t = PO - 1; t >= 0; --t) o[it] = mma(sf[i].t[t], q, o[it]);
+        }
+        o[it] *= vec[16 * it + l16] * A.scale;
+      }
+      reads_above<T>();
+      put_scores<T, DK, LK, LP, J, PO>(sP, sQ, sK, vec + 3 * kC, rt, j0, lane, A.scale);
+      reads_above<T>();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
+    } else {
+      frag kr[4][M];
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
         for (int i = 0; i < M; ++i) kr[it][i] = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
-      if constexpr (kOut)
-#pragma unroll
-        for (int i = 0; i < M; ++i) qr[i] = row_frag(sQ + (16 * rt + l16) * LK + 32 * i + 8 * g);
       reads_above<T>();
       Op<T, NT> sf[M];
 #pragma unroll
       for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
-      read_inv(0, kEarly);
+      if constexpr (M <= 2) read_inv();
       reads_above<T>();
 #pragma unroll
       for (int it = 0; it < 4; ++it) X[it] = zero4();
@@ -360,52 +386,20 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
       for (int i = 0; i < M; ++i)
 #pragma unroll
         for (int it = 0; it < 4; ++it) X[it] = mul(kr[it][i], sf[i], X[it]);
-      if constexpr (kOut) {
-        f32x4 p[J];                                 // P transposed: the wave's rows, J key tiles
-#pragma unroll
-        for (int j = 0; j < J; ++j) p[j] = zero4();
-#pragma unroll
-        for (int i = 0; i < M; ++i)
-#pragma unroll
-          for (int j = 0; j < J; ++j) p[j] = mma(W == 8 && j0 ? kr[(j + J) & 3][i] : kr[j][i], qr[i], p[j]);
-        frag qo[4][2];
-        auto read_q = [&](int i) {
-#pragma unroll
-          for (int it = 0; it < 4; ++it) qo[it][i & 1] = row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g);
-        };
-        read_q(0);
-        reads_above<T>();
-        put_weights<T, LP, J, PO>(sP, p, vec + 3 * kC, rt, j0, lane, A.scale);
-        // bf16: with two terms of the state, of P and of U an output has no error but its own rounding
-#pragma unroll
-        for (int it = 0; it < 4; ++it) o[it] = zero4();
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
-          if (i + 1 < M) read_q(i + 1);
-          reads_above<T>();
-#pragma unroll
-          for (int t = PO - 1; t >= 0; --t)
-#pragma unroll
-            for (int it = 0; it < 4; ++it) o[it] = mma(sf[i].t[t], qo[it][i & 1], o[it]);
-        }
-#pragma unroll
-        for (int it = 0; it < 4; ++it) o[it] *= vec[16 * it + l16] * A.scale;
-      }
     }
-    if constexpr (kEarly == 0) read_inv(0, NT > 2 ? 2 : NT);
+    if constexpr (M > 2 || kOut) read_inv();
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
       const f32x4 bv = *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);
       X[it] = bv * (half_of(vf[it >> 1], it & 1) - yv * X[it]);
     }
-    if constexpr (NT > 2) read_inv(2, NT);
     frag kt[2][NS];                                 // K transposed, 32 keys each
     auto read_kt = [&](int j) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) kt[j][i] = split_column_frag<LK>(sK + 32 * j * LK, i, lane);
     };
-    if constexpr (M <= 2) read_kt(0);
+    if constexpr (M <= 2 && !kOut) read_kt(0);
     reads_above<T>();
     auto correct = [&] {
       Op<T, NT> xf[2];
@@ -445,7 +439,7 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
             if (16 * it + 4 * g + r >= ill) x[it][r] = 0.f;
       };
       look(X);
-      read_inv(0, NT);
+      read_inv();
       correct();
       look(U);
     }
@@ -454,7 +448,7 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
       f32x4 u[4];
 #pragma unroll
       for (int it = 0; it < 4; ++it) u[it] = U[it] * *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
-      if constexpr (M > 2) read_kt(0);
+      if constexpr (M > 2 || kOut) read_kt(0);
       read_kt(1);
       reads_above<T>();
       Op<T, NT> uf[2];
@@ -472,20 +466,14 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
     }
     if constexpr (kOut) {
       __syncthreads();                              // P is there
-      Op<T, PO> pf[6];
-#pragma unroll
-      for (int f = 0; f < 6; ++f)
-        pf[f] = row_op<PO>(sP + (16 * (f < 2 ? f : 1 + f / 2) + l16) * LP + (f < 2 ? 0 : 32 * (f & 1)) + 8 * g, kC * LP);
-      reads_above<T>();
       Op<T, PO> uf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
-      o[0] = mul(uf[0], pf[0], o[0]);
-      o[1] = mul(uf[0], pf[1], o[1]);
-      o[2] = mul(uf[0], pf[2], o[2]);
-      o[3] = mul(uf[0], pf[4], o[3]);
-      o[2] = mul(uf[1], pf[3], o[2]);
-      o[3] = mul(uf[1], pf[5], o[3]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int i = 0; i <= it >> 1; ++i)
+          o[it] = mul(uf[i], row_op<PO>(sP + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), o[it]);
       if (any_ill)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -494,15 +482,12 @@ __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::out
           for (int it = 0; it < 4; ++it)
             if (16 * it + l16 >= at) o[it][r] = __builtin_nanf("");
         }
-      if (live_col) {
-        const int n = c == behind - 1 ? n_last : kC;
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-          if (16 * it + l16 < n) *reinterpret_cast<Quad<T>*>(po + 16 * it * A.so[1]) = quad(o[it], T());
-      }
-      po += kC * A.so[1];
+      for (int it = 0; it < 4; ++it) O[it] = quad(o[it], T());
     }
   }
+
+  if constexpr (kOut) store(n_last);
 
   float* dst = kSums ? (unit_matrix ? A.trans + ((long long)slot * m.H + h) * m.dk * m.dk
                                     : A.sums + ((long long)slot * m.H + h) * SE)

@@ -33,9 +33,9 @@ struct ReverseTiles {
   static constexpr int DV = 16 * W;
   static constexpr int LK = DK + 16 / (int)sizeof(T), LV = DV + (kBf ? 16 : 4), LP = kC + 16 / (int)sizeof(T);
   static constexpr int kHead = 16 + kDeltaVec * 4;
-  static constexpr int NT = kBf ? 3 : 1, NP = kBf ? 2 : 1;              // terms of the recurrence's operands, of P
+  static constexpr int NT = kBf ? 3 : 1, NI = kBf ? 2 : 1, NP = NI;     // terms of the recurrence's operands, of the inverse, of P
   static constexpr int kTiles = kC * (2 * LK + LV);
-  static constexpr int bytes = kHead + (kTiles + (NT + NP) * kC * LP) * (int)sizeof(T);
+  static constexpr int bytes = kHead + (kTiles + (NI + NP) * kC * LP) * (int)sizeof(T);
   static constexpr int occupancy = !kBf && DK == 128 ? 1 : 8 / W;
 };
 
@@ -45,7 +45,7 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
   using TL = ReverseTiles<T, DK, W>;
   using frag = typename Elem<T>::frag;
   constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
-  constexpr int NT = TL::NT, NP = TL::NP;
+  constexpr int NT = TL::NT, NI = TL::NI, NP = TL::NP;
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
   T* const sQ = sK + kC * LK;
   T* const sO = sQ + kC * LK;
   T* const sT = sK + TL::kTiles;
-  T* const sP = sT + NT * kC * LP;
+  T* const sP = sT + NI * kC * LP;
 
   const DeltaMap& m = A.m;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
   const T* px = reinterpret_cast<const T*>(A.dO) + s.b * A.sdo[0] + row0 * A.sdo[1] + h * A.sdo[2] + c0;
   Stage<T, DK, kThr> rk(pk, A.sk[1], m.dk, true), rq(pq, A.sq[1], m.dk, true);
   Stage<T, DV, kThr> ro(px, A.sdo[1], m.dv - c0, false);
-  StageInv<T, NT, LP, kThr> ri;
+  StageInv<T, NI, LP, kThr> ri;
   uint4 vec_next;
   const long long chunk0 = (long long)s.c_slot * m.H + h;              // [c_slots][H]
   auto fetch = [&](int c) {
@@ -123,13 +123,13 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
     ro.template put<LV>(sO);
     ri.put(sT);
     if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
-    if (c > first) fetch(c - 1);
-    __syncthreads();
     if (!kSums && c0 / 16 + w < (m.dv + 15) / 16) {
       float* dst = A.rstates + ((chunk0 + (long long)c * m.H) * ((m.dv + 15) / 16) + c0 / 16 + w) * (DK * 16) + lane * 4;
 #pragma unroll
       for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(dst + i * 256) = D[i];
     }
+    if (c > first) fetch(c - 1);
+    __syncthreads();
     put_scores<T, DK, LK, LP, 16 / W, NP>(sP, sQ, sK, vec + 3 * kC, w & 3, 16 / W * (w >> 2), lane, A.scale);
     Op<T, NT> df[M];
 #pragma unroll
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
       X[it] = zero4();
 #pragma unroll
       for (int i = it >> 1; i < 2; ++i)
-        X[it] = mul(split_column_op<NT, LP>(sT + 32 * i * LP, kC * LP, it, lane), zf[i], X[it]);
+        X[it] = mul(split_column_op<NI, LP>(sT + 32 * i * LP, kC * LP, it, lane), zf[i], X[it]);
     }
     Op<T, NT> kw[2], qw[2];
 #pragma unroll
@@ -203,11 +203,11 @@ struct GradTiles {
   static constexpr int PAD = 16 / (int)sizeof(T);
   static constexpr int LK = DK + PAD, LO = 64 + PAD, LV = 64 + (kBf ? 16 : 4), LP = kC + PAD, LS = DK + PAD;
   static constexpr int kHead = 16 + kDeltaVec * 4 + 2 * 4 * kC * 4 + 16;   // an int, vec, dots, sums of the waves
-  static constexpr int NT = kBf ? 3 : 1, NP = kBf ? 2 : 1;              // terms of the recurrence's operands, of P
+  static constexpr int NT = kBf ? 3 : 1, NI = kBf ? 2 : 1, NP = NI;     // terms of the recurrence's operands, of the inverse, of P
   static constexpr int kStateTile = 64 * LS, kPair = 2 * 64 * LP;
   // scores, then (bf16) the second terms of U and dv, or (fp32) the state, then PO and PV
   static constexpr int kA = kBf || kPair > kStateTile ? kPair : kStateTile;
-  static constexpr int bytes = kHead + (kC * (2 * LK + LO) + kA + kPair + (kBf ? kStateTile + NT * kC * LP : 0)) * (int)sizeof(T);
+  static constexpr int bytes = kHead + (kC * (2 * LK + LO) + kA + kPair + (kBf ? kStateTile + NI * kC * LP : 0)) * (int)sizeof(T);
   static_assert(64 * LV <= (kBf ? kPair : kPair / 2), "V lies where U (bf16: and dv) come, the inverse (fp32) where dv comes");
 };
 
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
   const float* const sc = vec + 3 * kC;
-  constexpr int NT = TL::NT, NP = TL::NP;
+  constexpr int NT = TL::NT, NI = TL::NI, NP = TL::NP;
   float* const sE = vec + kDeltaVec;                // [4][64] dO . o - dv . v, then [4][64] X . U
   float* const sF = sE + 2 * 4 * kC;                // [4] <D, S'>
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
                                 A.sv[1], m.dv - c0, false);
       fetch_rows(ro, A.sdo[1], n);
       fetch_rows(rv, A.sv[1], n);
-      StageInv<T, NT, LP, kThreads> ri;
+      StageInv<T, NI, LP, kThreads> ri;
       ri.fetch(A.inv + cs * kInvFloats);
       f32x4 S[NS], D[NS];
       const bool live_tile = 4 * vb + w < ct;       // uniform
@@ -382,7 +382,7 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
           U[it] = zero4();
 #pragma unroll
           for (int i = 0; i <= it >> 1; ++i)
-            U[it] = mul(row_op<NT>(sT + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), xf[i], U[it]);
+            U[it] = mul(row_op<NI>(sT + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), xf[i], U[it]);
         }
         // <D, S'>, S' = y_63 S + K^T diag(exp(c_63 - c)) U
         {
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
           X[it] = zero4();
 #pragma unroll
           for (int i = it >> 1; i < 2; ++i)
-            X[it] = mul(split_column_op<NT, LP>(sT + 32 * i * LP, kC * LP, it, lane), zf[i], X[it]);
+            X[it] = mul(split_column_op<NI, LP>(sT + 32 * i * LP, kC * LP, it, lane), zf[i], X[it]);
           db[it] += X[it] * U[it];
           X[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
           e[it] += o[it] * half_of(of[it >> 1], it & 1) - X[it] * V[it];
