@@ -33,6 +33,7 @@ struct DeltaArgs {
   float* rsums;                           // backward: [n_slots][H][dk][dv], the same of the gradient of the state
   float* cstates;                         // backward: [c_slots][H][DK][DV] entry states of the chunks, in registers' order
   float* rstates;                         // backward: the gradient of the state behind each chunk
+  float* fstates;                         // backward with dfin: [n_seq][H], as cstates, the final states
   // states
   const float *init, *dfin;               // [n_seq][H][dk][dv] or null
   float *fin, *dinit;
@@ -42,15 +43,13 @@ struct DeltaArgs {
 };
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st);
-// The segments' sums and transitions; backward: of the state's gradient too.
-hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st);
-// The sums become entry states.
+// The segments' sums and transitions; their sums become entry states; the outputs.
+hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, hipStream_t st);
 hipError_t launch_delta_join(const DeltaArgs& a, bool backward, hipStream_t st);
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, hipStream_t st);
-// Backward: the states before every chunk (cstates); in reversed time the gradients of the states behind
-// them (rstates), or of the segments the sums (rsums); and then the gradients.
-hipError_t launch_delta_states(const DeltaArgs& a, bool bf16, hipStream_t st);
-hipError_t launch_delta_reverse(const DeltaArgs& a, bool bf16, bool sums, hipStream_t st);
+// Backward: the states before every chunk and the gradients of the states behind them (sums: the segments'
+// sums of both, and the transitions); then the gradients.
+hipError_t launch_delta_bwd_walk(const DeltaArgs& a, bool bf16, bool sums, hipStream_t st);
 hipError_t launch_delta_grads(const DeltaArgs& a, bool bf16, hipStream_t st);
 hipError_t launch_delta_decode(const DeltaArgs& a, bool bf16, float* state, hipStream_t st);
 

@@ -21,6 +21,7 @@
 
 #include "delta.h"
 #include "delta_tiles.h"
+#include "delta_walk.h"
 #include "device.h"
 #include "mfma_util.h"
 
@@ -35,24 +36,26 @@ constexpr int kThreads = 256;             // of the kernels other than the walk
 // T_ij = -D_i sum_{j <= k < i} A_ik T_kj, a wave a block column, on the fp32 MFMA.
 template <typename T, int DK>
 struct PrepTiles {
-  static constexpr int LK = DK + 16 / (int)sizeof(T), LA = kC + 4, LD = 20;
+  static constexpr int LK = DK + 16 / (int)sizeof(T), LD = 20;
   static constexpr int kHead = 16 + 3 * kC * 4;                        // an int, c in two floats, beta
-  static constexpr int kKeys = kC * LK * (int)sizeof(T);
-  static constexpr int bytes = kHead + kKeys + kC * LA * 4 + kC * LD * 4;
+  static constexpr int kKeys = kC * LK * (int)sizeof(T);               // then the diagonal's inverses
+  static constexpr int bytes = kHead + kKeys + kInvBlocks * 16 * LD * 4;
+  static_assert(kC * LD * 4 <= kKeys, "the inverses lie where the keys were");
 };
 
 template <typename T, int DK>
 __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int backward) {
   using TL = PrepTiles<T, DK>;
   using frag = typename Elem<T>::frag;
-  constexpr int M = DK / 32, LK = TL::LK, LA = TL::LA, LD = TL::LD;
+  constexpr int M = DK / 32, LK = TL::LK, LD = TL::LD;
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const sc = reinterpret_cast<float*>(lds + 16);
   float* const sb = sc + 2 * kC;
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
-  float* const sA = reinterpret_cast<float*>(lds + TL::kHead + TL::kKeys);
-  float* const sD = sA + kC * LA;
+  float* const sD = reinterpret_cast<float*>(lds + TL::kHead);
+  float* const sA = reinterpret_cast<float*>(lds + TL::kHead + TL::kKeys);   // blocks [16][LD], row by row of them
+  auto block = [&](int i, int j) { return sA + (i * (i + 1) / 2 + j) * 16 * LD; };
 
   const DeltaMap& m = A.m;
   const unsigned unit = block_number();
@@ -118,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
       const int row = 16 * w + 4 * g + r;
       const float a = col < row ? sb[row] * exp2_diff(sc[row], sc[kC + row], hj, lj) * acc[r] : 0.f;
       sick[r] = fmaf(a, 0.f, sick[r]);
-      sA[row * LA + col] = a;
+      block(w, j)[(4 * g + r) * LD + l16] = a;
     }
   }
   // A row with an infinity or nan would leave nan in earlier rows of the inverse: it is taken as zeros, and
@@ -129,20 +132,19 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
 #pragma unroll
       for (int d = 1; d < 16; d <<= 1) sick[r] += __shfl_xor(sick[r], d);
       if (sick[r] != 0.f) {
-        const int row = 16 * w + 4 * g + r;
-        for (int j = 0; j <= w; ++j) sA[row * LA + 16 * j + l16] = 0.f;
-        if (l16 == 0) vec[2 * kC + row] = __builtin_nanf("");
+        for (int j = 0; j <= w; ++j) block(w, j)[(4 * g + r) * LD + l16] = 0.f;
+        if (l16 == 0) vec[2 * kC + 16 * w + 4 * g + r] = __builtin_nanf("");
       }
     }
   __syncthreads();
   if (w == 0) {                                     // block g, column l16: x = e - A x
     float x[16];
-    const float* a = sA + 16 * g * LA + 16 * g;
+    const float* a = block(g, g);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float y = i == l16 ? 1.f : 0.f;
 #pragma unroll
-      for (int j = 0; j < i; ++j) y = fmaf(-a[i * LA + j], x[j], y);
+      for (int j = 0; j < i; ++j) y = fmaf(-a[i * LD + j], x[j], y);
       x[i] = y;
       sD[(16 * g + i) * LD + l16] = y;
     }
@@ -161,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
       f32x4 acc = zero4();
 #pragma unroll
       for (int k = 0; k < i; ++k) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(sA + (16 * bi + l16) * LA + 16 * (w + k) + 4 * g);
+        const f32x4 a = *reinterpret_cast<const f32x4*>(block(bi, w + k) + l16 * LD + 4 * g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], t[k][r], acc, 0, 0, 0);
       }
@@ -175,349 +177,25 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
   }
 }
 
-// ---- the walk ----------------------------------------------------------------------------------
-enum class Walk { output, states, sums };
-
-template <typename T, int DK, int W, int NT, bool kOut>
-struct WalkTiles {
-  static constexpr bool kBf = sizeof(T) == 2;
-  static constexpr int DV = 16 * W;
-  static constexpr int LK = DK + 16 / (int)sizeof(T), LV = DV + (kBf ? 16 : 4), LP = kC + 16 / (int)sizeof(T);
-  static constexpr int kHead = 16 + kDeltaVec * 4;
-  static constexpr int kTiles = kC * (LK * (kOut ? 2 : 1) + LV);
-  static constexpr int kPO = kBf ? 2 : 1;           // terms of the outputs' operands
-  static constexpr int NI = kBf ? 2 : 1;            // terms of the inverse
-  static constexpr int bytes = kHead + (kTiles + (NI + (kOut ? kPO : 0)) * kC * LP) * (int)sizeof(T);
-  // waves a SIMD that the registers are held to (the launch bound counts workgroups a CU)
-  static constexpr int occupancy = !kBf && DK == 128 ? 1 : 8 / W;
-};
-
-// kWhat: outputs and the final state; or (backward) the states before the chunks; or, of the segments,
-// sums and transitions (blocks of columns behind those of the values).  NT: terms of the recurrence's operands.
 template <typename T, int DK, int W, int NT, Walk kWhat>
 __global__ __launch_bounds__(64 * W, (WalkTiles<T, DK, W, NT, kWhat == Walk::output>::occupancy)) void delta_walk_kernel(
-    DeltaArgs A, int blocks, int backward) {
-  constexpr bool kOut = kWhat == Walk::output, kSums = kWhat == Walk::sums;
-  using TL = WalkTiles<T, DK, W, NT, kOut>;
-  using frag = typename Elem<T>::frag;
-  constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
-  constexpr int NI = TL::NI, PO = TL::kPO, J = 16 / W;            // J: key tiles of a wave's part of P
+    DeltaArgs A, int blocks) {
   extern __shared__ __align__(16) char lds[];
-  int* const sh = reinterpret_cast<int*>(lds);
-  float* const vec = reinterpret_cast<float*>(lds + 16);
-  T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
-  T* const sV = sK + kC * LK;
-  T* const sQ = sV + kC * LV;
-  T* const sT = sK + TL::kTiles;
-  T* const sP = sT + NI * kC * LP;
-
-  const DeltaMap& m = A.m;
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // the blocks of one (segment, head) read the same rows: ids congruent mod 8, one XCD
-  const unsigned x = block_number(), per = blocks, y = x / 8 / per, unit = 8 * y + x % 8;
-  int sub = int(x / 8 - y * per);
-  if (unit >= (unsigned)m.n_slots * (unsigned)m.H) return;
-  const int slot = int(unit / (unsigned)m.H), h = int(unit - (unsigned)slot * (unsigned)m.H);
-  const int v_blocks = (m.dv + DV - 1) / DV;
-  const bool unit_matrix = kSums && sub >= v_blocks;                   // columns of the transition
-  if (unit_matrix) sub -= v_blocks;
-  const int c0 = sub * DV, cols = unit_matrix ? m.dk : m.dv;
-
-  DeltaPart s;
-  if (!find_part(m, slot, m.L, m.n_seg, m.n_slots, sh, s)) return;
-  const int L = m.L;
-  T* const out = kOut ? reinterpret_cast<T*>(A.o) + s.b * A.so[0] + h * A.so[2] + c0 : nullptr;
-  if constexpr (kOut) {
-    const int per_row = min(DV, m.dv - c0) / 4;
-    auto clear = [&](int from, int rows) {          // the block's columns of `rows` output rows
-      for (long long i = tid; i < (long long)rows * per_row; i += kThr)
-        store4(out + (from + i / per_row) * A.so[1] + i % per_row * 4, zero4());
-    };
-    if (s.seq == m.n_seq) {                         // rows behind the last sequence
-      if (A.zero_tail) clear(s.start + kC * L * s.part, min(kC * L, s.len - kC * L * s.part));
-      return;
-    }
-    if (m.packed && A.zero_tail && s.seq == 0 && s.part == 0) clear(0, s.start);   // before the first
-  }
-  if (s.seq == m.n_seq) return;
-  const int n_chunks = (s.len + kC - 1) / kC, n_seg = (n_chunks + L - 1) / L;
-  const long long SE = (long long)m.dk * m.dv, st_off = ((long long)s.seq * m.H + h) * SE;
-  if (s.part >= n_seg) {
-    if (kOut && s.len == 0 && s.part == 0 && A.fin)  // an empty sequence
-      for (int i = tid; i < m.dk * DV; i += kThr) {
-        const int r = i / DV, c = c0 + i % DV;
-        if (c < m.dv) A.fin[st_off + (long long)r * m.dv + c] = A.init ? A.init[st_off + (long long)r * m.dv + c] : 0.f;
-      }
-    return;
-  }
-  const bool last_seg = s.part == n_seg - 1;
-  if constexpr (kSums) {
-    // the sum of the last segment enters no entry state; a transition is used where a state comes in
-    // from before, or in reversed time from behind
-    if (!unit_matrix && last_seg) return;
-    const bool from_before = !last_seg && (s.part > 0 || A.init);
-    const bool from_behind = backward && s.part > 0 && (!last_seg || A.dfin);
-    if (unit_matrix && !from_before && !from_behind) return;
-  }
-  const int first = s.part * L, behind = min(first + L, n_chunks);
-  const long long row0 = s.start + (long long)kC * first;
-  const int hk = h / (m.H / m.Hk);
-  Stage<T, DK, kThr> rk(reinterpret_cast<const T*>(A.k) + s.b * A.sk[0] + row0 * A.sk[1] + hk * A.sk[2], A.sk[1], m.dk, true);
-  Stage<T, DK, kThr> rq(reinterpret_cast<const T*>(kOut ? A.q : A.k) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2], A.sq[1], m.dk, true);
-  Stage<T, DV, kThr> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + (unit_matrix ? 0 : c0),
-                        A.sv[1], m.dv - (unit_matrix ? 0 : c0), false);
-  StageInv<T, NI, LP, kThr> ri;
-  const int n_last = min(kC, s.len - kC * (behind - 1));
-  uint4 vec_next;
-  const long long chunk0 = (long long)(s.c_slot + first) * m.H + h;    // [c_slots][H]
-  const float* p_inv = A.inv + chunk0 * kInvFloats;
-  const float* p_vec = A.vec + chunk0 * kDeltaVec;
-  auto fetch = [&](int c) {
-    const int n = c == behind - 1 ? n_last : kC;
-    fetch_rows(rk, A.sk[1], n);
-    if constexpr (kOut) fetch_rows(rq, A.sq[1], n);
-    if (!unit_matrix) fetch_rows(rv, A.sv[1], n);
-    ri.fetch(p_inv);
-    if (tid < kDeltaVec / 4) vec_next = reinterpret_cast<const uint4*>(p_vec)[tid];
-    p_inv += (long long)m.H * kInvFloats;
-    p_vec += (long long)m.H * kDeltaVec;
-  };
-  fetch(first);
-
-  // state tiles: S[i] lane holds rows 16 i + 4 g + r of column c0 + wc + l16
-  const int wc = 16 * w, col = c0 + wc + l16;
-  f32x4 S[NS];
-  {
-    const float* given = kSums ? nullptr : s.part > 0 ? A.sums + ((long long)slot * m.H + h) * SE : A.init ? A.init + st_off : nullptr;
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = kSums && unit_matrix && 16 * i + 4 * g + r == col ? 1.f : 0.f;
-    if (given) load_state(S, given, m.dk, m.dv, col, g);               // uniform
-  }
-  if (m.dk < DK || m.dv - c0 < DV || unit_matrix) { // columns that no operand has: zeros all along
-    uint4* const z = reinterpret_cast<uint4*>(sK);
-    for (int i = tid; i < TL::kTiles * (int)sizeof(T) / 16; i += kThr) z[i] = uint4{0u, 0u, 0u, 0u};
-  }
-  ri.zeros(sT);
-  const int rt = w & 3, j0 = J * (w >> 2);          // the wave's rows and first key tile of P
-  const bool live_col = c0 + wc + 4 * g < m.dv;
-  T* po = kOut ? out + (row0 + l16) * A.so[1] + wc + 4 * g : nullptr;
-  const int ct = (m.dv + 15) / 16;
-  float* p_state = nullptr;
-  if (kWhat == Walk::states && c0 / 16 + w < ct) p_state = A.cstates + (chunk0 * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
-
-  Quad<T> O[4];                                     // outputs of the last chunk
-  auto store = [&](int rows) {
-    if (live_col)
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-        if (16 * it + l16 < rows) *reinterpret_cast<Quad<T>*>(po + 16 * it * A.so[1]) = O[it];
-    po += kC * A.so[1];
-  };
-#pragma unroll 1
-  for (int c = first; c < behind; ++c) {
-    __syncthreads();                                // the last chunk's tiles have been read
-    rk.template put_split<LK>(sK);
-    if constexpr (kOut) rq.template put_split<LK>(sQ);
-    if (!unit_matrix) rv.template put<LV>(sV);
-    ri.put(sT);
-    if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
-    // (stores before the next loads: the wait for these then does not wait for stores just issued)
-    if (kWhat == Walk::states && p_state) {         // uniform
-#pragma unroll
-      for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(p_state + i * 256) = S[i];
-      p_state += (long long)m.H * ct * (DK * 16);
-    }
-    if (kOut && c > first) store(kC);
-    if (c + 1 < behind) fetch(c + 1);
-    __syncthreads();
-
-    // LDS reads are issued in batches, ahead of the work that hides them (reads_above): left alone, the compiler
-    // waits for nearly every read before its product.
-    f32x4 X[4], U[4], o[4];
-    Op<T, NI> inv[6];                               // (row tile, K step): (0, 0), (1, 0), (2, 0), (2, 1), (3, 0), (3, 1)
-    auto read_inv = [&] {
-#pragma unroll
-      for (int f = 0; f < 6; ++f)
-        inv[f] = row_op<NI>(sT + (16 * (f < 2 ? f : 1 + f / 2) + l16) * LP + (f < 2 ? 0 : 32 * (f & 1)) + 8 * g, kC * LP);
-    };
-    frag vf[2];
-    if constexpr (kOut) {
-      Op<T, NT> sf[M];
-#pragma unroll
-      for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
-      // bf16: with two terms of the state, of P and of U an output has no error but its own rounding
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        X[it] = o[it] = zero4();
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
-          X[it] = mul(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], X[it]);
-          const frag q = row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g);
-#pragma unroll
-          for (int t = PO - 1; t >= 0; --t) o[it] = mma(sf[i].t[t], q, o[it]);
-        }
-        o[it] *= vec[16 * it + l16] * A.scale;
-      }
-      reads_above<T>();
-      put_scores<T, DK, LK, LP, J, PO>(sP, sQ, sK, vec + 3 * kC, rt, j0, lane, A.scale);
-      reads_above<T>();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
-    } else {
-      frag kr[4][M];
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int i = 0; i < M; ++i) kr[it][i] = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
-      reads_above<T>();
-      Op<T, NT> sf[M];
-#pragma unroll
-      for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
-      if constexpr (M <= 2) read_inv();
-      reads_above<T>();
-#pragma unroll
-      for (int it = 0; it < 4; ++it) X[it] = zero4();
-#pragma unroll
-      for (int i = 0; i < M; ++i)
-#pragma unroll
-        for (int it = 0; it < 4; ++it) X[it] = mul(kr[it][i], sf[i], X[it]);
-    }
-    if constexpr (M > 2 || kOut) read_inv();
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
-      const f32x4 bv = *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);
-      X[it] = bv * (half_of(vf[it >> 1], it & 1) - yv * X[it]);
-    }
-    frag kt[2][NS];                                 // K transposed, 32 keys each
-    auto read_kt = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) kt[j][i] = split_column_frag<LK>(sK + 32 * j * LK, i, lane);
-    };
-    if constexpr (M <= 2 && !kOut) read_kt(0);
-    reads_above<T>();
-    auto correct = [&] {
-      Op<T, NT> xf[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) split_terms(X[2 * i], X[2 * i + 1], xf[i]);
-      U[0] = mul(inv[0], xf[0], zero4());
-      U[1] = mul(inv[1], xf[0], zero4());
-      U[2] = mul(inv[2], xf[0], zero4());
-      U[3] = mul(inv[4], xf[0], zero4());
-      U[2] = mul(inv[3], xf[1], U[2]);
-      U[3] = mul(inv[5], xf[1], U[3]);
-      float sick = 0.f;
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sick = fmaf(U[it][r], 0.f, sick);
-      return sick != 0.f;
-    };
-    // An infinity or nan in row j: in products a zero of a later column would still meet it and leave nan in
-    // earlier rows.  From row j on the column's outputs and its state are nan; the rows before it are
-    // computed without.
-    int ill = kC;                                   // the column's first such row
-    const bool any_ill = __any(correct());
-    if (any_ill) {
-      auto look = [&](f32x4 (&x)[4]) {
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (!(fabsf(x[it][r]) < __builtin_huge_valf())) ill = min(ill, 16 * it + 4 * g + r);
-        ill = min(ill, __shfl_xor(ill, 16));
-        ill = min(ill, __shfl_xor(ill, 32));
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (16 * it + 4 * g + r >= ill) x[it][r] = 0.f;
-      };
-      look(X);
-      read_inv();
-      correct();
-      look(U);
-    }
-    {
-      const float whole = vec[kC - 1];
-      f32x4 u[4];
-#pragma unroll
-      for (int it = 0; it < 4; ++it) u[it] = U[it] * *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
-      if constexpr (M > 2 || kOut) read_kt(0);
-      read_kt(1);
-      reads_above<T>();
-      Op<T, NT> uf[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) split_terms(u[2 * i], u[2 * i + 1], uf[i]);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) S[i] *= whole;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) S[i] = mul(kt[j][i], uf[j], S[i]);
-      if (any_ill && ill < kC)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) S[i] = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
-    }
-    if constexpr (kOut) {
-      __syncthreads();                              // P is there
-      Op<T, PO> uf[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int i = 0; i <= it >> 1; ++i)
-          o[it] = mul(uf[i], row_op<PO>(sP + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), o[it]);
-      if (any_ill)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = __shfl(ill, 4 * g + r);
-#pragma unroll
-          for (int it = 0; it < 4; ++it)
-            if (16 * it + l16 >= at) o[it][r] = __builtin_nanf("");
-        }
-#pragma unroll
-      for (int it = 0; it < 4; ++it) O[it] = quad(o[it], T());
-    }
-  }
-
-  if constexpr (kOut) store(n_last);
-
-  float* dst = kSums ? (unit_matrix ? A.trans + ((long long)slot * m.H + h) * m.dk * m.dk
-                                    : A.sums + ((long long)slot * m.H + h) * SE)
-               : kOut && last_seg && A.fin ? A.fin + st_off : nullptr;
-  if (!dst || col >= cols) return;
-#pragma unroll
-  for (int i = 0; i < NS; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (16 * i + 4 * g + r < m.dk) dst[(16 * i + 4 * g + r) * cols + col] = S[i][r];
+  const UnitBlock u = unit_block(blocks);
+  delta_walk<T, DK, W, NT, kWhat>(A, u.unit, u.sub, 0, lds);
 }
 
 // ---- joining segments ---------------------------------------------------------------------------
 // Per (sequence, head) and 16 columns, over the segments in order: E_{j+1} = M_j E_j + N_j; the sum in slot
 // j is replaced by the entry state E_j.  Backward also in reversed time: D_{j-1} = M_j^T D_j + N'_j, the
 // sum in slot j replaced by D_j, the gradient of the state behind the segment.  On the fp32 MFMA; the rows are
-// split over the waves, which pass the state through LDS, and the next transition is loaded meanwhile.
-template <int DK>
-__global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int blocks) {
-  constexpr int M = DK / 32, NS = DK / 16, R = (NS + 3) / 4, LS = DK + 4;
-  __shared__ __align__(16) float sS[2][16 * LS];
+// split over the waves, which pass the state through LDS, and kAhead steps' transitions are on their way.
+template <int DK, bool kRev>
+__device__ __forceinline__ void join(const DeltaArgs& A, int sub, int h, int seq, float (&sS)[2][16 * (DK + 4)]) {
+  constexpr int M = DK / 32, NS = DK / 16, R = (NS + 3) / 4, LS = DK + 4, kAhead = DK > 64 ? 2 : 4;
   const DeltaMap& m = A.m;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  unsigned x = blockIdx.x;                          // sequences: blockIdx.y
-  const int sub = int(x % (unsigned)blocks);
-  x /= (unsigned)blocks;
-  const int h = int(x % (unsigned)m.H);
-  const bool rev = x / (unsigned)m.H;
-  const int seq = blockIdx.y, SL = kC * m.L;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), SL = kC * m.L;
   int slot = seq * m.n_seg, len = m.T;
   if (m.packed) {
     const int first = cu_at(m, seq);
@@ -527,16 +205,16 @@ __global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int b
   const int n = (len + SL - 1) / SL;
   if (n < 2) return;
   const int col = 16 * sub + l16, SE = m.dk * m.dv, ME = m.dk * m.dk;
-  float* const sums = rev ? A.rsums : A.sums;
-  const float* given = rev ? A.dfin : A.init;
+  float* const sums = kRev ? A.rsums : A.sums;
+  const float* given = kRev ? A.dfin : A.init;
   const bool live = col < m.dv;
-  const int rs = rev ? 1 : m.dk, cs = rev ? m.dk : 1;                  // strides of the transition's rows and columns
-  f32x4 S[R], N[R];
-  f32x8 a[R][M];
-  auto fetch = [&](int j) {
-    const long long at = (long long)(slot + (rev ? n - 1 - j : j)) * m.H + h;
-    const float* const here = sums + at * SE;
-    const float* const tr = A.trans + at * ME;
+  auto place = [&](int j) { return (long long)(slot + (kRev ? n - 1 - j : j)) * m.H + h; };
+  f32x4 S[R], N[kAhead][R];
+  f32x8 a[kAhead][R][M];
+  auto fetch = [&](int j, int to) {                 // `to`: known where this is unrolled
+    if (j + 1 >= n) return;                         // the last segment's are not used
+    const float* const here = sums + place(j) * SE;
+    const float* const tr = A.trans + place(j) * ME;
     const bool used = j > 0 || given;               // else the state is zero, and the transition is not there
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -544,18 +222,28 @@ __global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int b
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int y = 16 * tile + 4 * g + r;
-        N[i][r] = live && y < m.dk ? here[y * m.dv + col] : 0.f;
+        N[to][i][r] = live && y < m.dk ? here[y * m.dv + col] : 0.f;
       }
 #pragma unroll
       for (int k = 0; k < M; ++k)
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int q = 32 * k + 16 * (r / 4) + 4 * g + r % 4;
-          a[i][k][r] = used && row < m.dk && q < m.dk ? tr[row * rs + q * cs] : 0.f;
+        for (int half = 0; half < 2; ++half) {
+          const int q = 32 * k + 16 * half + 4 * g; // widths are multiples of four
+          f32x4 x = zero4();
+          if (used && row < m.dk && q < m.dk) {
+            if constexpr (kRev)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) x[r] = tr[(q + r) * m.dk + row];
+            else
+              x = *reinterpret_cast<const f32x4*>(tr + row * m.dk + q);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) a[to][i][k][4 * half + r] = x[r];
         }
     }
   };
-  fetch(0);
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) fetch(j, j);
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -563,39 +251,54 @@ __global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int b
       const int y = 16 * (w * R + i) + 4 * g + r;
       S[i][r] = given && live && y < m.dk ? given[((long long)seq * m.H + h) * SE + y * m.dv + col] : 0.f;
     }
-  for (int j = 0; j < n; ++j) {
-    float* const here = sums + ((long long)(slot + (rev ? n - 1 - j : j)) * m.H + h) * SE;
-    float* const buf = sS[j & 1];
+  for (int j0 = 0; j0 < n; j0 += kAhead)
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int tile = w * R + i;
-      if (tile < NS) *reinterpret_cast<f32x4*>(buf + l16 * LS + split_place(16 * tile + 4 * g)) = S[i];
+    for (int s = 0; s < kAhead; ++s) {
+      const int j = j0 + s;
+      if (j >= n) break;                            // uniform
+      float* const here = sums + place(j) * SE;
+      float* const buf = sS[j & 1];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int y = 16 * tile + 4 * g + r;
-        if (live && y < m.dk) here[y * m.dv + col] = S[i][r];
-      }
-    }
-    if (j + 1 >= n) break;
-    __syncthreads();
-    f32x4 odd[R];
+      for (int i = 0; i < R; ++i) {
+        const int tile = w * R + i;
+        if (tile < NS) *reinterpret_cast<f32x4*>(buf + l16 * LS + split_place(16 * tile + 4 * g)) = S[i];
 #pragma unroll
-    for (int i = 0; i < R; ++i) odd[i] = zero4();
-#pragma unroll
-    for (int k = 0; k < M; ++k) {
-      const f32x8 b = row_frag(buf + l16 * LS + 32 * k + 8 * g);
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int r = 0; r < 8; r += 2) {
-          N[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][k][r], b[r], N[i], 0, 0, 0);
-          odd[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][k][r + 1], b[r + 1], odd[i], 0, 0, 0);
+        for (int r = 0; r < 4; ++r) {
+          const int y = 16 * tile + 4 * g + r;
+          if (live && y < m.dk) here[y * m.dv + col] = S[i][r];
         }
-    }
+      }
+      if (j + 1 >= n) break;
+      __syncthreads();
+      f32x4 odd[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) S[i] = N[i] + odd[i];
-    if (j + 2 < n) fetch(j + 1);
-  }
+      for (int i = 0; i < R; ++i) odd[i] = zero4();
+#pragma unroll
+      for (int k = 0; k < M; ++k) {
+        const f32x8 b = row_frag(buf + l16 * LS + 32 * k + 8 * g);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int r = 0; r < 8; r += 2) {
+            N[s][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s][i][k][r], b[r], N[s][i], 0, 0, 0);
+            odd[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s][i][k][r + 1], b[r + 1], odd[i], 0, 0, 0);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) S[i] = N[s][i] + odd[i];
+      fetch(j + kAhead, s);
+    }
+}
+
+template <int DK>
+__global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int blocks) {
+  __shared__ __align__(16) float sS[2][16 * (DK + 4)];
+  unsigned x = blockIdx.x;                          // sequences: blockIdx.y
+  const int sub = int(x % (unsigned)blocks);
+  x /= (unsigned)blocks;
+  const int h = int(x % (unsigned)A.m.H);
+  if (x / (unsigned)A.m.H) join<DK, true>(A, sub, h, blockIdx.y, sS);
+  else join<DK, false>(A, sub, h, blockIdx.y, sS);
 }
 
 // ---- recurrent form ------------------------------------------------------------------------
@@ -704,37 +407,33 @@ hipError_t launch_prep_t(const DeltaArgs& a, bool backward, hipStream_t st) {
 }
 
 template <typename T, int DK, int W, int NT, Walk kWhat>
-hipError_t launch_walk_t(const DeltaArgs& a, bool backward, hipStream_t st) {
+hipError_t launch_walk_t(const DeltaArgs& a, hipStream_t st) {
   using TL = WalkTiles<T, DK, W, NT, kWhat == Walk::output>;
   hipError_t e = with_lds(delta_walk_kernel<T, DK, W, NT, kWhat>, TL::bytes);
   if (e != hipSuccess) return e;
   const int blocks = (a.m.dv + 16 * W - 1) / (16 * W) + (kWhat == Walk::sums ? (a.m.dk + 16 * W - 1) / (16 * W) : 0);
   const long long units = (long long)a.m.n_slots * a.m.H;
   launch_kernel(delta_walk_kernel<T, DK, W, NT, kWhat>, grid_rows((units + 7) / 8 * 8 * blocks), 64 * W, TL::bytes, st, a,
-                blocks, backward ? 1 : 0);
+                blocks);
   return hipGetLastError();
 }
 
 template <Walk kWhat, int NT>
-hipError_t launch_walk_bf16(const DeltaArgs& a, bool backward, hipStream_t st) {
+hipError_t launch_walk_bf16(const DeltaArgs& a, hipStream_t st) {
   const int dk = a.m.dk;
   if (decay_columns(true, a.m.dv) == 128)
-    return dk <= 64 ? launch_walk_t<__bf16, 64, 8, NT, kWhat>(a, backward, st)
-                    : launch_walk_t<__bf16, 128, 8, NT, kWhat>(a, backward, st);
-  return dk <= 32 ? launch_walk_t<__bf16, 32, 4, NT, kWhat>(a, backward, st)
-         : dk <= 64 ? launch_walk_t<__bf16, 64, 4, NT, kWhat>(a, backward, st)
-                    : launch_walk_t<__bf16, 128, 4, NT, kWhat>(a, backward, st);
+    return dk <= 64 ? launch_walk_t<__bf16, 64, 8, NT, kWhat>(a, st) : launch_walk_t<__bf16, 128, 8, NT, kWhat>(a, st);
+  return dk <= 32 ? launch_walk_t<__bf16, 32, 4, NT, kWhat>(a, st)
+         : dk <= 64 ? launch_walk_t<__bf16, 64, 4, NT, kWhat>(a, st) : launch_walk_t<__bf16, 128, 4, NT, kWhat>(a, st);
 }
 
-// fine: states that the caller keeps, or gradients, in three terms.
+// States that the caller keeps are computed with three terms.
 template <Walk kWhat>
-hipError_t launch_walk_d(const DeltaArgs& a, bool bf16, bool fine, bool backward, hipStream_t st) {
+hipError_t launch_walk_d(const DeltaArgs& a, bool bf16, hipStream_t st) {
   const int dk = a.m.dk;
-  if (!bf16) return dk <= 32 ? launch_walk_t<float, 32, 4, 1, kWhat>(a, backward, st)
-                  : dk <= 64 ? launch_walk_t<float, 64, 4, 1, kWhat>(a, backward, st)
-                             : launch_walk_t<float, 128, 4, 1, kWhat>(a, backward, st);
-  if constexpr (kWhat == Walk::states) return launch_walk_bf16<kWhat, 3>(a, backward, st);
-  return fine ? launch_walk_bf16<kWhat, 3>(a, backward, st) : launch_walk_bf16<kWhat, 2>(a, backward, st);
+  if (!bf16) return dk <= 32 ? launch_walk_t<float, 32, 4, 1, kWhat>(a, st)
+                  : dk <= 64 ? launch_walk_t<float, 64, 4, 1, kWhat>(a, st) : launch_walk_t<float, 128, 4, 1, kWhat>(a, st);
+  return a.fin ? launch_walk_bf16<kWhat, 3>(a, st) : launch_walk_bf16<kWhat, 2>(a, st);
 }
 
 }  // namespace
@@ -747,16 +446,12 @@ hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool backward, hipSt
          : dk <= 64 ? launch_prep_t<float, 64>(a, backward, st) : launch_prep_t<float, 128>(a, backward, st);
 }
 
-hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st) {
-  return launch_walk_d<Walk::sums>(a, bf16, backward || a.fin, backward, st);
+hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, hipStream_t st) {
+  return launch_walk_d<Walk::sums>(a, bf16, st);
 }
 
 hipError_t launch_delta_walk(const DeltaArgs& a, bool bf16, hipStream_t st) {
-  return launch_walk_d<Walk::output>(a, bf16, a.fin != nullptr, false, st);
-}
-
-hipError_t launch_delta_states(const DeltaArgs& a, bool bf16, hipStream_t st) {
-  return launch_walk_d<Walk::states>(a, bf16, true, true, st);
+  return launch_walk_d<Walk::output>(a, bf16, st);
 }
 
 hipError_t launch_delta_join(const DeltaArgs& a, bool backward, hipStream_t st) {

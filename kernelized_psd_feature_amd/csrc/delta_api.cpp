@@ -103,6 +103,7 @@ void place(kata::DeltaArgs& a, const kata::DeltaPlan& p, void* workspace) {
   a.rsums = reinterpret_cast<float*>(ws + p.rsums);
   a.cstates = reinterpret_cast<float*>(ws + p.cstates);
   a.rstates = reinterpret_cast<float*>(ws + p.rstates);
+  a.fstates = reinterpret_cast<float*>(ws + p.fstates);
 }
 
 // Inverses, and the segments' entry states.
@@ -110,8 +111,8 @@ kata_status run_before(const kata::DeltaArgs& a, bool bf16, bool backward, hipSt
   {
     Timed t(KATA_K_CHUNK_STATE, st);
     hipError_t e = kata::launch_delta_prep(a, bf16, backward, st);
-    if (e == hipSuccess && a.m.n_seg > 1) e = kata::launch_delta_segments(a, bf16, backward, st);
-    if (e == hipSuccess && a.m.n_seg > 1 && backward) e = kata::launch_delta_reverse(a, bf16, true, st);
+    if (e == hipSuccess && a.m.n_seg > 1)
+      e = backward ? kata::launch_delta_bwd_walk(a, bf16, true, st) : kata::launch_delta_segments(a, bf16, st);
     if (e != hipSuccess) return launch_status(e, what);
   }
   if (a.m.n_seg < 2) return KATA_OK;
@@ -193,14 +194,14 @@ kata_status kata_bwd_delta(const kata_delta_problem* pr, const void* q, const vo
   a.init = initial_state;
   a.dfin = dfinal_state;
   a.dinit = dinitial_state;
+  if (!dfinal_state) a.fstates = nullptr;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dbeta = dbeta; a.dlog = dlog_decay;
   const bool bf16 = pr->dtype == KATA_BF16;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const char* what = "gated delta rule backward";
   if ((s = run_before(a, bf16, true, st, what)) != KATA_OK) return s;
   Timed t(KATA_K_BWD, st);
-  hipError_t e = kata::launch_delta_states(a, bf16, st);
-  if (e == hipSuccess) e = kata::launch_delta_reverse(a, bf16, false, st);
+  hipError_t e = kata::launch_delta_bwd_walk(a, bf16, false, st);
   if (e == hipSuccess) e = kata::launch_delta_grads(a, bf16, st);
   return launch_status(e, what);
 }

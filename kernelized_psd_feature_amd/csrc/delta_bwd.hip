@@ -18,13 +18,14 @@
 
 #include "delta.h"
 #include "delta_tiles.h"
+#include "delta_walk.h"
 #include "device.h"
 #include "mfma_util.h"
 
 namespace kata {
 namespace {
 
-constexpr int kThreads = 256;             // of the gradients' kernel
+constexpr int kThreads = 512;             // of the gradients' kernel
 
 // ---- the walk in reversed time ------------------------------------------------------------------
 template <typename T, int DK, int W>
@@ -36,17 +37,15 @@ struct ReverseTiles {
   static constexpr int NT = kBf ? 3 : 1, NI = kBf ? 2 : 1, NP = NI;     // terms of the recurrence's operands, of the inverse, of P
   static constexpr int kTiles = kC * (2 * LK + LV);
   static constexpr int bytes = kHead + (kTiles + (NI + NP) * kC * LP) * (int)sizeof(T);
-  static constexpr int occupancy = !kBf && DK == 128 ? 1 : 8 / W;
 };
 
 // kSums: of the segments, from a gradient of zero behind them.
 template <typename T, int DK, int W, bool kSums>
-__global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void delta_reverse_kernel(DeltaArgs A, int blocks) {
+__device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit, int sub, char* lds) {
   using TL = ReverseTiles<T, DK, W>;
   using frag = typename Elem<T>::frag;
   constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
   constexpr int NT = TL::NT, NI = TL::NI, NP = TL::NP;
-  extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
@@ -58,8 +57,6 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
   const DeltaMap& m = A.m;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const unsigned x = block_number(), per = blocks, y = x / 8 / per, unit = 8 * y + x % 8;
-  const int sub = int(x / 8 - y * per);
   if (unit >= (unsigned)m.n_slots * (unsigned)m.H) return;
   const int slot = int(unit / (unsigned)m.H), h = int(unit - (unsigned)slot * (unsigned)m.H);
   const int c0 = sub * DV;
@@ -130,38 +127,81 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
     }
     if (c > first) fetch(c - 1);
     __syncthreads();
-    put_scores<T, DK, LK, LP, 16 / W, NP>(sP, sQ, sK, vec + 3 * kC, w & 3, 16 / W * (w >> 2), lane, A.scale);
-    Op<T, NT> df[M];
-#pragma unroll
-    for (int i = 0; i < M; ++i) split_terms(D[2 * i], D[2 * i + 1], df[i]);
+    // reads in batches, as in the walk
     f32x4 Z[4], X[4];
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      Z[it] = zero4();
-#pragma unroll
-      for (int i = 0; i < M; ++i) Z[it] = mul(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), df[i], Z[it]);
-      Z[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
-    }
     frag of[2];
+    {
+      constexpr int J = 16 / W;
+      const int rt = w & 3, j0 = J * (w >> 2);
+      frag kr[4][M], qr[M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) qr[i] = row_frag(sQ + (16 * rt + l16) * LK + 32 * i + 8 * g);
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int i = 0; i < M; ++i) kr[it][i] = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
+      reads_above<T>();
+      f32x4 p[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) p[j] = zero4();
+#pragma unroll
+      for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) p[j] = mma(W == 8 && j0 ? kr[(j + J) & 3][i] : kr[j][i], qr[i], p[j]);
+      Op<T, NT> df[M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) split_terms(D[2 * i], D[2 * i + 1], df[i]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) Z[it] = zero4();
+#pragma unroll
+      for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int it = 0; it < 4; ++it) Z[it] = mul(kr[it][i], df[i], Z[it]);
+      put_weights<T, LP, J, NP>(sP, p, vec + 3 * kC, rt, j0, lane, A.scale);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) of[i] = column_frag<LV>(sO + 32 * i * LV + wc, lane);
+    Op<T, NI> inv[6];                               // (row tile, K step): (0, 0), (0, 1), (1, 0), (1, 1), (2, 1), (3, 1)
+#pragma unroll
+    for (int f = 0; f < 6; ++f)
+      inv[f] = split_column_op<NI, LP>(sT + 32 * (f < 4 ? f & 1 : 1) * LP, kC * LP, f < 4 ? f >> 1 : f - 2, lane);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) Z[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
     __syncthreads();                                // P is there
+    {
+      Op<T, NP> pf[6];
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
-#pragma unroll
-      for (int i = it >> 1; i < 2; ++i)
-        Z[it] = mul(split_column_op<NP, LP>(sP + 32 * i * LP, kC * LP, it, lane), of[i], Z[it]);
-    Op<T, NT> zf[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) split_terms(Z[2 * i], Z[2 * i + 1], zf[i]);
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      X[it] = zero4();
-#pragma unroll
-      for (int i = it >> 1; i < 2; ++i)
-        X[it] = mul(split_column_op<NI, LP>(sT + 32 * i * LP, kC * LP, it, lane), zf[i], X[it]);
+      for (int f = 0; f < 6; ++f)
+        pf[f] = split_column_op<NP, LP>(sP + 32 * (f < 4 ? f & 1 : 1) * LP, kC * LP, f < 4 ? f >> 1 : f - 2, lane);
+      reads_above<T>();
+      Z[0] = mul(pf[0], of[0], Z[0]);
+      Z[1] = mul(pf[2], of[0], Z[1]);
+      Z[2] = mul(pf[4], of[1], Z[2]);
+      Z[3] = mul(pf[5], of[1], Z[3]);
+      Z[0] = mul(pf[1], of[1], Z[0]);
+      Z[1] = mul(pf[3], of[1], Z[1]);
     }
-    Op<T, NT> kw[2], qw[2];
+    frag qt[2][NS];                                 // Q transposed, 32 tokens each, then K
+    auto read_t = [&](const T* tile, int j) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) qt[j][i] = split_column_frag<LK>(tile + 32 * j * LK, i, lane);
+    };
+    if constexpr (M <= 2) read_t(sQ, 0);
+    if constexpr (M <= 2) read_t(sQ, 1);
+    reads_above<T>();
+    {
+      Op<T, NT> zf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_terms(Z[2 * i], Z[2 * i + 1], zf[i]);
+      X[0] = mul(inv[0], zf[0], zero4());
+      X[1] = mul(inv[2], zf[0], zero4());
+      X[2] = mul(inv[4], zf[1], zero4());
+      X[3] = mul(inv[5], zf[1], zero4());
+      X[0] = mul(inv[1], zf[1], X[0]);
+      X[1] = mul(inv[3], zf[1], X[1]);
+    }
+    Op<T, NT> kw[2];
+    Op<T, NI> qw[2];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
@@ -175,14 +215,20 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
     }
     const float whole = vec[kC - 1];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      D[i] *= whole;
+    for (int i = 0; i < NS; ++i) D[i] *= whole;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        D[i] = mul(split_column_frag<LK>(sQ + 32 * j * LK, i, lane), qw[j], D[i]);
-        D[i] = mul(split_column_frag<LK>(sK + 32 * j * LK, i, lane), kw[j], D[i]);
-      }
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (M > 2) read_t(sQ, j);
+      reads_above<T>();
+#pragma unroll
+      for (int i = 0; i < NS; ++i) D[i] = mul(qt[j][i], qw[j], D[i]);
+      read_t(sK, j);
     }
+    reads_above<T>();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < NS; ++i) D[i] = mul(qt[j][i], kw[j], D[i]);
   }
   float* dst = kSums ? A.rsums + ((long long)slot * m.H + h) * SE : first == 0 && A.dinit ? A.dinit + st_off : nullptr;
   if (!dst || col >= m.dv) return;
@@ -193,21 +239,36 @@ __global__ __launch_bounds__(64 * W, (ReverseTiles<T, DK, W>::occupancy)) void d
       if (16 * i + 4 * g + r < m.dk) dst[(long long)(16 * i + 4 * g + r) * m.dv + col] = D[i][r];
 }
 
+// Both walks side by side.  kSums: sums and transitions of the segments.
+template <typename T, int DK, int W, bool kSums>
+constexpr int kBothBytes = WalkTiles<T, DK, W, 3, false>::bytes > ReverseTiles<T, DK, W>::bytes ? WalkTiles<T, DK, W, 3, false>::bytes
+                                                                                              : ReverseTiles<T, DK, W>::bytes;
+template <typename T, int DK, int W, bool kSums>
+__global__ __launch_bounds__(64 * W, sizeof(T) == 4 && DK == 128 ? 1 : 8 / W) void delta_both_kernel(DeltaArgs A, int blocks,
+                                                                                                  int forward) {
+  extern __shared__ __align__(16) char lds[];
+  const UnitBlock u = unit_block(blocks);
+  if (u.sub < forward) delta_walk<T, DK, W, sizeof(T) == 2 ? 3 : 1, kSums ? Walk::sums : Walk::states>(A, u.unit, u.sub, 1, lds);
+  else delta_reverse<T, DK, W, kSums>(A, u.unit, u.sub - forward, lds);
+}
+
 // ---- the gradients ------------------------------------------------------------------------------
-// One workgroup of four waves for a chunk and a head of q and k, over the value heads that share it and
-// blocks of 64 value columns.  As in the walks a wave has 16 columns of S, D, U, X and dv; then these go
-// through LDS, [column][token] and [column][row of the state], and a wave has 16 tokens of dq and dk.
+// One workgroup of eight waves for a chunk and a head of q and k, over the value heads that share it and
+// blocks of 64 value columns.  As in the walks a wave has 16 columns, four of them S, U and the outputs, the
+// others D, Z, X and dv; then these go through LDS, [column][token] and [column][row of the state], and a wave
+// has 16 tokens of dq and dk, half of the columns each.
 template <typename T, int DK>
 struct GradTiles {
   static constexpr bool kBf = sizeof(T) == 2;
   static constexpr int PAD = 16 / (int)sizeof(T);
   static constexpr int LK = DK + PAD, LO = 64 + PAD, LV = 64 + (kBf ? 16 : 4), LP = kC + PAD, LS = DK + PAD;
-  static constexpr int kHead = 16 + kDeltaVec * 4 + 2 * 4 * kC * 4 + 16;   // an int, vec, dots, sums of the waves
+  static constexpr int kHead = 16 + kDeltaVec * 4 + 9 * kC * 4 + 16;   // an int, vec, dots and sums of the waves
   static constexpr int NT = kBf ? 3 : 1, NI = kBf ? 2 : 1, NP = NI;     // terms of the recurrence's operands, of the inverse, of P
   static constexpr int kStateTile = 64 * LS, kPair = 2 * 64 * LP;
-  // scores, then (bf16) the second terms of U and dv, or (fp32) the state, then PO and PV
+  // scores, then (bf16) the second terms of U and dv, or (fp32) a state, then PO and PV
   static constexpr int kA = kBf || kPair > kStateTile ? kPair : kStateTile;
-  static constexpr int bytes = kHead + (kC * (2 * LK + LO) + kA + kPair + (kBf ? kStateTile + NI * kC * LP : 0)) * (int)sizeof(T);
+  // bf16: both states, and the inverse's terms
+  static constexpr int bytes = kHead + (kC * (2 * LK + LO) + kA + kPair + (kBf ? 2 * kStateTile + NI * kC * LP : 0)) * (int)sizeof(T);
   static_assert(64 * LV <= (kBf ? kPair : kPair / 2), "V lies where U (bf16: and dv) come, the inverse (fp32) where dv comes");
 };
 
@@ -221,15 +282,15 @@ template <typename T, int DK>
 __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
   using TL = GradTiles<T, DK>;
   using frag = typename Elem<T>::frag;
-  constexpr int M = DK / 32, NS = DK / 16, LK = TL::LK, LO = TL::LO, LV = TL::LV, LP = TL::LP, LS = TL::LS;
+  constexpr int M = DK / 32, NS = DK / 16, NH = NS / 2, LK = TL::LK, LO = TL::LO, LV = TL::LV, LP = TL::LP, LS = TL::LS;
+  constexpr int NT = TL::NT, NI = TL::NI, NP = TL::NP;
   constexpr bool kBf = TL::kBf;
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
   const float* const sc = vec + 3 * kC;
-  constexpr int NT = TL::NT, NI = TL::NI, NP = TL::NP;
-  float* const sE = vec + kDeltaVec;                // [4][64] dO . o - dv . v, then [4][64] X . U
-  float* const sF = sE + 2 * 4 * kC;                // [4] <D, S'>
+  float* const sE = vec + kDeltaVec;                // [8][64] dO . o, -dv . v; then [64] dv . U
+  float* const sF = sE + 9 * kC;                    // [4] <D, S'>
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
   T* const sQ = sK + kC * LK;
   T* const sO = sQ + kC * LK;
@@ -237,11 +298,21 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
   T* const sU = sA + TL::kA;                        // V, then U and dv
   T* const sZ = sU + 64 * LP;
   T* const sS = kBf ? sZ + 64 * LP : sA;
-  T* const sT = kBf ? sS + TL::kStateTile : sZ;
+  T* const sD = kBf ? sS + TL::kStateTile : sA;
+  T* const sT = kBf ? sD + TL::kStateTile : sZ;
 
   const DeltaMap& m = A.m;
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x;
+  int lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  // The places in LDS that a phase uses are computed there: kept from phase to phase they would cost a hundred
+  // registers, and scratch.
+  auto forget = [&] {
+    asm volatile("" : "+v"(lane));
+    g = lane >> 4;
+    l16 = lane & 15;
+  };
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
+  const bool first_half = wave < 4;
   const unsigned unit = block_number();
   if (unit >= (unsigned)m.c_slots * (unsigned)m.Hk) return;
   const int slot = int(unit / (unsigned)m.Hk), hk = int(unit - (unsigned)slot * (unsigned)m.Hk);
@@ -274,6 +345,7 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
   }
   if (m.packed && s.seq == 0 && s.part == 0) clear(0, s.start);        // before the first
   if (n <= 0) return;
+  const bool last = kC * (s.part + 1) >= s.len;
   const long long row0 = s.start + (long long)kC * s.part;
   const int ct = (m.dv + 15) / 16, v_blocks = (m.dv + 63) / 64;
 
@@ -291,19 +363,23 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
     rq.template put_split<LK>(sQ);
   }
 
-  f32x4 dqa[NS], dka[NS];                           // [row 16 i + 4 g + r][token 16 w + l16]
+  f32x4 dqa[NH], dka[NH];                           // [row 16 (i0 + i) + 4 g + r][token 16 w + l16]
+  const int i0 = first_half ? 0 : NH;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) dqa[i] = dka[i] = zero4();
+  for (int i = 0; i < NH; ++i) dqa[i] = dka[i] = zero4();
 
+#pragma unroll 1
   for (int hh = 0; hh < share; ++hh) {
     const int h = hk * share + hh;
     const long long cs = (long long)slot * m.H + h;                    // [c_slots][H]
-    f32x4 WO[4], WV[4], e[4], db[4];
+    f32x4 Wt[4], e[4];                              // the strip of dO U^T (second half: dv U^T), transposed
     float frob = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) WO[i] = WV[i] = e[i] = db[i] = zero4();
+    for (int i = 0; i < 4; ++i) Wt[i] = e[i] = zero4();
+#pragma unroll 1
     for (int vb = 0; vb < v_blocks; ++vb) {
       const int c0 = 64 * vb;
+      forget();
       Stage<T, 64, kThreads> ro(reinterpret_cast<const T*>(A.dO) + s.b * A.sdo[0] + row0 * A.sdo[1] + h * A.sdo[2] + c0,
                                 A.sdo[1], m.dv - c0, true);
       Stage<T, 64, kThreads> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + c0,
@@ -312,15 +388,24 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
       fetch_rows(rv, A.sv[1], n);
       StageInv<T, NI, LP, kThreads> ri;
       ri.fetch(A.inv + cs * kInvFloats);
-      f32x4 S[NS], D[NS];
+      f32x4 S[NS];                                  // (second half: D)
       const bool live_tile = 4 * vb + w < ct;       // uniform
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        S[i] = D[i] = zero4();
-        if (live_tile) {
-          const long long at = (cs * ct + 4 * vb + w) * (DK * 16) + i * 256 + lane * 4;
-          S[i] = *reinterpret_cast<const f32x4*>(A.cstates + at);
-          D[i] = *reinterpret_cast<const f32x4*>(A.rstates + at);
+      for (int i = 0; i < NS; ++i) S[i] = zero4();
+      if (live_tile) {
+        const long long tile = (cs * ct + 4 * vb + w) * (DK * 16) + lane * 4;
+        const float* const from = (first_half ? A.cstates : A.rstates) + tile;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) S[i] = *reinterpret_cast<const f32x4*>(from + i * 256);
+        if (!first_half && !(last && !A.fstates)) {  // (behind the last chunk without a gradient D is zero)
+          const float* const next = last ? A.fstates + (((long long)s.seq * m.H + h) * ct + 4 * vb + w) * (DK * 16) + lane * 4
+                                         : A.cstates + tile + (long long)m.H * ct * (DK * 16);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(next + i * 256);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) frob = fmaf(S[i][r], x[r], frob);
+          }
         }
       }
       __syncthreads();                              // the last block's and head's tiles have been read
@@ -340,122 +425,113 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
       ri.zeros(sT);
       __syncthreads();
 
-      // a wave's 16 columns
-      put_scores<T, DK, LK, LP, 4, NP>(sA, sQ, sK, sc, w, 0, lane, A.scale);
+      // a wave's 16 columns: x becomes U (X), y the outputs (Z)
+      put_scores<T, DK, LK, LP, 2, NP>(sA, sQ, sK, sc, w, first_half ? 0 : 2, lane, A.scale);
+      forget();
       const int wc = 16 * w;
-      f32x4 U[4], X[4], V[4];
+      f32x4 x[4], y[4];
+      frag of[2], vf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        vf[i] = column_frag<LV>(sU + 32 * i * LV + wc, lane);
+        of[i] = split_column_frag<LO>(sO + 32 * i * LO, w, lane);
+      }
       {
-        Op<T, NT> sf[M], df[M];
+        Op<T, NT> sf[M];
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-          split_terms(S[2 * i], S[2 * i + 1], sf[i]);
-          split_terms(D[2 * i], D[2 * i + 1], df[i]);
-        }
-        frag of[2], vf[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          vf[i] = column_frag<LV>(sU + 32 * i * LV + wc, lane);
-          of[i] = split_column_frag<LO>(sO + 32 * i * LO, w, lane);
-        }
-        f32x4 Z[4], o[4];
+        for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          X[it] = Z[it] = o[it] = zero4();
+          x[it] = y[it] = zero4();
 #pragma unroll
-          for (int i = 0; i < M; ++i) {
-            const frag kf = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
-            X[it] = mul(kf, sf[i], X[it]);
-            Z[it] = mul(kf, df[i], Z[it]);
-            o[it] = mul(row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], o[it]);
+          for (int i = 0; i < M; ++i) x[it] = mul(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], x[it]);
+        }
+        if (first_half)
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+#pragma unroll
+            for (int i = 0; i < M; ++i) y[it] = mul(row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], y[it]);
+            const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
+            y[it] *= yv * A.scale;
+            x[it] = *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g) * (half_of(vf[it >> 1], it & 1) - yv * x[it]);
           }
-          const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
-          V[it] = half_of(vf[it >> 1], it & 1);
-          X[it] = *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g) * (V[it] - yv * X[it]);
-          Z[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
-          o[it] *= yv * A.scale;
-        }
-        Op<T, NT> xf[2];
+        else
 #pragma unroll
-        for (int i = 0; i < 2; ++i) split_terms(X[2 * i], X[2 * i + 1], xf[i]);
+          for (int it = 0; it < 4; ++it) y[it] = x[it] * *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
+      }
+      reads_above<T>();
+      Op<T, NT> f[2];
+      if (first_half) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_terms(x[2 * i], x[2 * i + 1], f[i]);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          U[it] = zero4();
+          x[it] = zero4();
 #pragma unroll
           for (int i = 0; i <= it >> 1; ++i)
-            U[it] = mul(row_op<NI>(sT + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), xf[i], U[it]);
+            x[it] = mul(row_op<NI>(sT + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), f[i], x[it]);
         }
-        // <D, S'>, S' = y_63 S + K^T diag(exp(c_63 - c)) U
-        {
-          float f = 0.f;
 #pragma unroll
-          for (int i = 0; i < NS; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) f = fmaf(S[i][r], D[i][r], f);
-          frob = fmaf(vec[kC - 1], f, frob);
-#pragma unroll
-          for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) frob = fmaf(U[it][r], Z[it][r], frob);
-        }
-        Op<T, NT> uf[2], zf[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
-        __syncthreads();                            // P is there, and V has been read
+        for (int i = 0; i < 2; ++i) split_terms(x[2 * i], x[2 * i + 1], f[i]);
+      }
+      __syncthreads();                              // P is there
+      forget();
+      if (first_half) {
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (i <= it >> 1) o[it] = mul(row_op<NP>(sA + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), uf[i], o[it]);
-            if (i >= it >> 1) Z[it] = mul(split_column_op<NP, LP>(sA + 32 * i * LP, kC * LP, it, lane), of[i], Z[it]);
-          }
+          for (int i = 0; i <= it >> 1; ++i)
+            y[it] = mul(row_op<NP>(sA + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), f[i], y[it]);
+          e[it] += y[it] * half_of(of[it >> 1], it & 1);
         }
+      } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) split_terms(Z[2 * i], Z[2 * i + 1], zf[i]);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          X[it] = zero4();
+        for (int it = 0; it < 4; ++it)
 #pragma unroll
           for (int i = it >> 1; i < 2; ++i)
-            X[it] = mul(split_column_op<NI, LP>(sT + 32 * i * LP, kC * LP, it, lane), zf[i], X[it]);
-          db[it] += X[it] * U[it];
-          X[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
-          e[it] += o[it] * half_of(of[it >> 1], it & 1) - X[it] * V[it];
-        }
-      }
-      // U, dv and the state through LDS
-      __syncthreads();                              // P and (fp32) the inverse have been read
-      T* const mine = sU + (wc + l16) * LP + 4 * g;
+            y[it] = mul(split_column_op<NP, LP>(sA + 32 * i * LP, kC * LP, it, lane), of[i], y[it]);
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const Quad<T> u = quad(U[it], T()), z = quad(X[it], T());
-        *reinterpret_cast<Quad<T>*>(mine + 16 * it) = u;
-        *reinterpret_cast<Quad<T>*>(mine + (sZ - sU) + 16 * it) = z;
-        if constexpr (kBf) {
-          U[it] -= unquad(u);
-          X[it] -= unquad(z);
-        }
-      }
-      if constexpr (kBf)
+        for (int i = 0; i < 2; ++i) split_terms(y[2 * i], y[2 * i + 1], f[i]);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          store4(sA + (wc + l16) * LP + 4 * g + 16 * it, U[it]);
-          store4(sA + (64 + wc + l16) * LP + 4 * g + 16 * it, X[it]);
-        }
+          x[it] = zero4();
 #pragma unroll
-      for (int i = 0; i < NS; ++i) store4(sS + (wc + l16) * LS + 16 * i + 4 * g, S[i]);
+          for (int i = it >> 1; i < 2; ++i)
+            x[it] = mul(split_column_op<NI, LP>(sT + 32 * i * LP, kC * LP, it, lane), f[i], x[it]);
+          x[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
+          e[it] -= x[it] * half_of(vf[it >> 1], it & 1);
+        }
+      }
+      __syncthreads();                              // P, V and the inverse have been read
+      // U, dv and the states through LDS
+      forget();
+      {
+        T* const mine = (first_half ? sU : sZ) + (wc + l16) * LP + 4 * g;
+        T* const rest = sA + ((first_half ? 0 : 64) + wc + l16) * LP + 4 * g;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const Quad<T> u = quad(x[it], T());
+          *reinterpret_cast<Quad<T>*>(mine + 16 * it) = u;
+          if constexpr (kBf) store4(rest + 16 * it, x[it] - unquad(u));
+        }
+        if (kBf || first_half)
+#pragma unroll
+          for (int i = 0; i < NS; ++i) store4((first_half ? sS : sD) + (wc + l16) * LS + 16 * i + 4 * g, S[i]);
+      }
       __syncthreads();
 
       // a wave's 16 tokens
-      frag ur[2], zr[2];
+      forget();
+      frag ur[2], zr[2], ot[2];
       {
         constexpr int NW = kBf ? 2 : 1;             // terms of U and dv
         Op<T, NW> zt[2];
-        frag ot[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           zt[i].t[0] = zr[i] = column_frag<LP>(sZ + 32 * i * LP + 16 * w, lane);
           if constexpr (kBf) zt[i].t[1] = column_frag<LP>(sA + (64 + 32 * i) * LP + 16 * w, lane);
           ot[i] = row_frag(sO + (16 * w + l16) * LO + 32 * i + 8 * g);
+          ur[i] = column_frag<LP>(sU + 32 * i * LP + 16 * w, lane);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -465,86 +541,97 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
               Op<T, NW> ut;
               ut.t[0] = column_frag<LP>(sU + 32 * i * LP + 16 * j, lane);
               if constexpr (kBf) ut.t[1] = column_frag<LP>(sA + 32 * i * LP + 16 * j, lane);
-              WO[j] = mul(ut, ot[i], WO[j]);
-              WV[j] = mul(ut, zt[i], WV[j]);
-              if (j == w) ur[i] = ut.t[0];
+              if (first_half) Wt[j] = mul(ut, ot[i], Wt[j]);
+              else Wt[j] = mul(ut, zt[i], Wt[j]);
             }
+        forget();
         const float yr = vec[16 * w + l16], yo = yr * A.scale;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
+        for (int i = 0; i < NH; ++i) {
           f32x4 a = zero4(), b = zero4();
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const frag st = column_frag<LS>(sS + 32 * j * LS + 16 * i, lane);
+            const frag st = column_frag<LS>(sS + 32 * j * LS + 16 * (i0 + i), lane);
             a = mma(st, ot[j], a);
             b = mma(st, zr[j], b);
           }
           dqa[i] += a * yo;
           dka[i] -= b * yr;
         }
-        // dv: tokens 16 w + l16, columns 32 i + 16 half + 4 g
+        // dv: tokens 16 w + l16, columns 32 i + 16 half + 4 g, half of them each
         if (16 * w + l16 < n) {
           T* const dst = reinterpret_cast<T*>(A.dv) + ((lead + hh) + (row0 + 16 * w + l16) * m.H) * m.dv + c0 + 4 * g;
+          const int i = first_half ? 0 : 1;
+          const frag z = first_half ? zr[0] : zr[1];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              if (c0 + 32 * i + 16 * half + 4 * g < m.dv) store4(dst + 32 * i + 16 * half, half_of(zr[i], half));
+          for (int half = 0; half < 2; ++half)
+            if (c0 + 32 * i + 16 * half + 4 * g < m.dv) store4(dst + 32 * i + 16 * half, half_of(z, half));
         }
       }
-      __syncthreads();                              // S has been read
+      if constexpr (!kBf) {
+        __syncthreads();                            // S has been read
+        if (!first_half)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) store4(sS + (wc + l16) * LS + 16 * i + 4 * g, D[i]);
-      __syncthreads();
+          for (int i = 0; i < NS; ++i) store4(sD + (wc + l16) * LS + 16 * i + 4 * g, S[i]);
+        __syncthreads();
+      }
+      forget();
       const float left = vec[kC + 16 * w + l16];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
+      for (int i = 0; i < NH; ++i) {
         f32x4 a = zero4();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) a = mma(column_frag<LS>(sS + 32 * j * LS + 16 * i, lane), ur[j], a);
+        for (int j = 0; j < 2; ++j) a = mma(column_frag<LS>(sD + 32 * j * LS + 16 * (i0 + i), lane), ur[j], a);
         dka[i] += a * left;
       }
     }
     // dots: over a wave's 16 columns, then over the waves
+    forget();
 #pragma unroll
     for (int it = 0; it < 4; ++it)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float a = sum16(e[it][r]), b = sum16(db[it][r]);
-        if (l16 == 0) {
-          sE[w * kC + 16 * it + 4 * g + r] = a;
-          sE[(4 + w) * kC + 16 * it + 4 * g + r] = b;
-        }
+        const float a = sum16(e[it][r]);
+        if (l16 == 0) sE[wave * kC + 16 * it + 4 * g + r] = a;
       }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
-    if (lane == 0) sF[w] = frob;
+    if (lane == 0 && !first_half) sF[w] = frob;
+    if (!first_half) {                              // the diagonal of dv U^T
+      float d = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (j == w && 4 * g + r == l16) d = Wt[j][r];
+      if (l16 >> 2 == g) sE[8 * kC + 16 * w + l16] = d;
+    }
     __syncthreads();                                // (the second terms and D have been read, too)
-    // PO and PV, the wave's strip of rows
+    // PO or PV, the wave's strip of rows
     {
-      const float hi = sc[16 * w + l16], lo = sc[kC + 16 * w + l16];
+      const float hi = sc[16 * w + l16], lo = sc[kC + 16 * w + l16], factor = first_half ? A.scale : -1.f;
+      const int row = 16 * w + l16 + (first_half ? 1 : 0);             // the first key that it does not reach
+      T* const at = sA + ((first_half ? 0 : kC) + 16 * w + l16) * LP;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        f32x4 po = zero4(), pv = zero4();
+        f32x4 p = zero4();
         if (j <= w)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int key = 16 * j + 4 * g + r, row = 16 * w + l16;
-            const float x = exp2_diff(hi, lo, sc[key], sc[kC + key]);
-            po[r] = key > row ? 0.f : WO[j][r] * (x * A.scale);
-            pv[r] = key >= row ? 0.f : -WV[j][r] * x;
+            const int key = 16 * j + 4 * g + r;
+            p[r] = key >= row ? 0.f : Wt[j][r] * (exp2_diff(hi, lo, sc[key], sc[kC + key]) * factor);
           }
-        T* const at = sA + (16 * w + l16) * LP + split_place(16 * j + 4 * g);
-        store4(at, po);
-        store4(at + kC * LP, pv);
+        store4(at + split_place(16 * j + 4 * g), p);
       }
     }
-    if (w == 0) {
+    if (wave == 0) {
       const long long at = lead + hh + (row0 + lane) * m.H;
-      const float b = sE[4 * kC + lane] + sE[5 * kC + lane] + sE[6 * kC + lane] + sE[7 * kC + lane];
-      if (lane < n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(b / vec[2 * kC + lane]);
+      const float b = vec[2 * kC + lane];
+      if (lane < n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[8 * kC + lane] / (b * b));
       if (A.dlog) {
-        double x = (double)sE[lane] + sE[kC + lane] + sE[2 * kC + lane] + sE[3 * kC + lane];
+        double x = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x += (double)sE[i * kC + lane];
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
           const double up = __shfl_down(x, d);
@@ -558,16 +645,16 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
+    for (int i = 0; i < NH; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const frag kt = split_column_frag<LK>(sK + 32 * j * LK, i, lane);
+        const frag kt = split_column_frag<LK>(sK + 32 * j * LK, i0 + i, lane);
         if (j <= w >> 1) {                          // uniform
           dqa[i] = mma(kt, row_frag(sA + (16 * w + l16) * LP + 32 * j + 8 * g), dqa[i]);
           dka[i] = mma(kt, row_frag(sA + (kC + 16 * w + l16) * LP + 32 * j + 8 * g), dka[i]);
         }
         if (j >= w >> 1) {
-          dka[i] = mma(split_column_frag<LK>(sQ + 32 * j * LK, i, lane), split_column_frag<LP>(sA + 32 * j * LP, w, lane), dka[i]);
+          dka[i] = mma(split_column_frag<LK>(sQ + 32 * j * LK, i0 + i, lane), split_column_frag<LP>(sA + 32 * j * LP, w, lane), dka[i]);
           dka[i] = mma(kt, split_column_frag<LP>(sA + (kC + 32 * j) * LP, w, lane), dka[i]);
         }
       }
@@ -575,35 +662,35 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
   if (16 * w + l16 < n) {
     const long long at = (row0 + 16 * w + l16) * m.Hk * m.dk + 4 * g;
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (16 * i + 4 * g < m.dk) {
-        store4(gq + at + 16 * i, dqa[i]);
-        store4(gk + at + 16 * i, dka[i]);
+    for (int i = 0; i < NH; ++i)
+      if (16 * (i0 + i) + 4 * g < m.dk) {
+        store4(gq + at + 16 * (i0 + i), dqa[i]);
+        store4(gk + at + 16 * (i0 + i), dka[i]);
       }
   }
 }
 
 template <typename T, int DK, int W, bool kSums>
-hipError_t launch_reverse_t(const DeltaArgs& a, hipStream_t st) {
-  using TL = ReverseTiles<T, DK, W>;
-  const auto kernel = delta_reverse_kernel<T, DK, W, kSums>;
-  hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), TL::bytes);
+hipError_t launch_both_t(const DeltaArgs& a, hipStream_t st) {
+  constexpr int bytes = kBothBytes<T, DK, W, kSums>;
+  const auto kernel = delta_both_kernel<T, DK, W, kSums>;
+  hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
-  const int blocks = (a.m.dv + 16 * W - 1) / (16 * W);
+  const int v = (a.m.dv + 16 * W - 1) / (16 * W), forward = v + (kSums ? (a.m.dk + 16 * W - 1) / (16 * W) : 0);
   const long long units = (long long)a.m.n_slots * a.m.H;
-  launch_kernel(kernel, grid_rows((units + 7) / 8 * 8 * blocks), 64 * W, TL::bytes, st, a, blocks);
+  launch_kernel(kernel, grid_rows((units + 7) / 8 * 8 * (forward + v)), 64 * W, bytes, st, a, forward + v, forward);
   return hipGetLastError();
 }
 
 template <bool kSums>
-hipError_t launch_reverse_d(const DeltaArgs& a, bool bf16, hipStream_t st) {
+hipError_t launch_both_d(const DeltaArgs& a, bool bf16, hipStream_t st) {
   const int dk = a.m.dk;
-  if (!bf16) return dk <= 32 ? launch_reverse_t<float, 32, 4, kSums>(a, st)
-                  : dk <= 64 ? launch_reverse_t<float, 64, 4, kSums>(a, st) : launch_reverse_t<float, 128, 4, kSums>(a, st);
+  if (!bf16) return dk <= 32 ? launch_both_t<float, 32, 4, kSums>(a, st)
+                  : dk <= 64 ? launch_both_t<float, 64, 4, kSums>(a, st) : launch_both_t<float, 128, 4, kSums>(a, st);
   if (decay_columns(true, a.m.dv) == 128)
-    return dk <= 64 ? launch_reverse_t<__bf16, 64, 8, kSums>(a, st) : launch_reverse_t<__bf16, 128, 8, kSums>(a, st);
-  return dk <= 32 ? launch_reverse_t<__bf16, 32, 4, kSums>(a, st)
-         : dk <= 64 ? launch_reverse_t<__bf16, 64, 4, kSums>(a, st) : launch_reverse_t<__bf16, 128, 4, kSums>(a, st);
+    return dk <= 64 ? launch_both_t<__bf16, 64, 8, kSums>(a, st) : launch_both_t<__bf16, 128, 8, kSums>(a, st);
+  return dk <= 64 ? launch_both_t<__bf16, 64, 4, kSums>(a, st)
+                  : launch_both_t<__bf16, 128, 4, kSums>(a, st);
 }
 
 template <typename T, int DK>
@@ -618,14 +705,13 @@ hipError_t launch_grads_t(const DeltaArgs& a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_delta_reverse(const DeltaArgs& a, bool bf16, bool sums, hipStream_t st) {
-  return sums ? launch_reverse_d<true>(a, bf16, st) : launch_reverse_d<false>(a, bf16, st);
+hipError_t launch_delta_bwd_walk(const DeltaArgs& a, bool bf16, bool sums, hipStream_t st) {
+  return sums ? launch_both_d<true>(a, bf16, st) : launch_both_d<false>(a, bf16, st);
 }
 
 hipError_t launch_delta_grads(const DeltaArgs& a, bool bf16, hipStream_t st) {
   const int dk = a.m.dk;
-  if (bf16) return dk <= 32 ? launch_grads_t<__bf16, 32>(a, st)
-                 : dk <= 64 ? launch_grads_t<__bf16, 64>(a, st) : launch_grads_t<__bf16, 128>(a, st);
+  if (bf16) return dk <= 64 ? launch_grads_t<__bf16, 64>(a, st) : launch_grads_t<__bf16, 128>(a, st);
   return dk <= 32 ? launch_grads_t<float, 32>(a, st)
          : dk <= 64 ? launch_grads_t<float, 64>(a, st) : launch_grads_t<float, 128>(a, st);
 }

@@ -71,7 +71,7 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
   const int64_t v_blocks = (pr->dv + cols - 1) / cols, k_blocks = (pr->dk + cols - 1) / cols;
   // segments that a sequence (packed: all tokens together) is cut into to fill the card
   const int64_t units = pr->H * v_blocks * (backward ? 2 : 1) * (pr->packed ? 1 : pr->n_seq);
-  const int64_t want = std::max<int64_t>(1, 512 / units);
+  const int64_t want = std::max<int64_t>(1, (backward ? 256 : 512) / units);
   const int64_t L = chunks <= 8 ? chunks : std::max<int64_t>(4, (chunks + want - 1) / want);
   p.L = int(L);
   p.n_chunks = int(chunks);
@@ -81,7 +81,7 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
   p.c_slots = pr->packed ? decay_slot_count(pr->T, pr->n_seq, kDecayChunk) : int(std::min<int64_t>(pr->n_seq * chunks, INT32_MAX));
   const int64_t H = pr->H;
   p.groups = std::max<int64_t>((pr->packed ? int64_t(p.c_slots) : pr->n_seq * chunks) * H,
-                               (int64_t(p.n_slots) * H + 7) / 8 * 8 * (2 * v_blocks + k_blocks));
+                               (int64_t(p.n_slots) * H + 7) / 8 * 8 * (2 * v_blocks + k_blocks + 1));
   size_t at = 0;
   const auto part = [&](size_t bytes) {
     const size_t here = at;
@@ -97,10 +97,12 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
   }
   if (backward) {
     if (p.n_seg > 1) p.rsums = part(s * state);
-    const size_t DK = pr->dk <= 32 ? 32 : pr->dk <= 64 ? 64 : 128;
+    // (the state walks' tile: 32 rows have no bf16 form of the gradients' kernel)
+    const size_t DK = pr->dk <= 32 && !bf16 ? 32 : pr->dk <= 64 ? 64 : 128;
     const size_t chunk_state = DK * 16 * ((pr->dv + 15) / 16) * 4;
     p.cstates = part(c * chunk_state);
     p.rstates = part(c * chunk_state);
+    p.fstates = part(size_t(pr->n_seq) * H * chunk_state);
   }
   p.bytes = at;
   return p;

@@ -230,11 +230,22 @@ __device__ __forceinline__ bool find_part(const DeltaMap& m, int slot, int chunk
     if (lo <= slot && slot < hi) *sh = i;
   }
   __syncthreads();
-  const int i = *sh;
+  const int i = __builtin_amdgcn_readfirstlane(*sh);
   if (i < 0) return false;
   const int first = cu_at(m, i), end = i < m.n_seq ? cu_at(m, i + 1) : m.T;
   s = DeltaPart{i, 0, first, max(end - first, 0), slot - decay_first_slot(first, i, SL), decay_first_slot(first, i, kC)};
   return true;
+}
+
+// A workgroup's unit (segment and head) and block: the blocks of one unit read the same rows, so they get ids
+// congruent mod 8, one XCD.
+struct UnitBlock {
+  unsigned unit;
+  int sub;
+};
+__device__ __forceinline__ UnitBlock unit_block(int blocks) {
+  const unsigned x = block_number(), per = blocks, y = x / 8 / per;
+  return UnitBlock{8 * y + x % 8, int(x / 8 - y * per)};
 }
 
 // A chunk's rows of an operand as they are staged (Stage in tiles.h), n of them.
