@@ -366,6 +366,49 @@ kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void
                         const double* rates, const void* positions, void* out_q, void* out_k,
                         void* stream);
 
+/* The same with positions of several axes (time, height, width of images and video): pair i turns by the
+ * position of axis axes[i] (device int32 [rot / 2]; a value outside [0, n_axes) is taken as the nearest one
+ * inside).  positions may not be NULL; that of axis a lies pos_a elements behind that of axis a - 1. */
+kata_status kata_rotary_axes(const kata_rotary_problem* pr, const void* q, const void* k,
+                             const double* rates, const void* positions, const int32_t* axes,
+                             int32_t n_axes, int64_t pos_a, void* out_q, void* out_k, void* stream);
+
+/* ---- Norms of queries and keys --------------------------------------------------------------
+ * Every head of q and k, rows of D elements, divided by its size, times a weight, and turned by its
+ * position as in kata_rotary, in one pass:
+ *     z = x r w,  r = 1 / sqrt(sum(x^2) / n + eps),  n = D, or 1 with l2 (rows of unit length),
+ * and y = z with its first `rot` coordinates turned (rot = 0: none, and rates, positions and axes are not
+ * looked at).  Nothing is rounded between the norm and the turn; sums are fp32.
+ *   q [B][T][H][D], k [B][T][Hk][D] (Hk = 0: none), strides, rates, positions, axes (NULL: one axis):
+ *   as in kata_rotary and kata_rotary_axes; D <= 256.
+ *   q_weight, k_weight: [D] of w_dtype (fp32, or bf16 with bf16 rows), nullable: ones. */
+typedef struct {
+  int32_t B, T, H, Hk, D, rot;
+  int32_t dtype, w_dtype;
+  int32_t interleaved, l2;
+  int32_t pos64, n_axes;
+  float magnitude, eps;
+  int64_t pos_a, pos_b, pos_t, offset;
+  int64_t sq[3], sk[3], soq[3], sok[3], sdq[3], sdk[3];
+} kata_qk_norm_problem;
+
+/* An output may be its own input (in place) but must not overlap inputs otherwise. */
+kata_status kata_fwd_qk_norm(const kata_qk_norm_problem* pr, const void* q, const void* k,
+                             const void* q_weight, const void* k_weight, const double* rates,
+                             const void* positions, const int32_t* axes, void* out_q, void* out_k,
+                             void* stream);
+
+size_t kata_bwd_qk_norm_workspace_size(const kata_qk_norm_problem* pr);
+
+/* Gradients of sum(dq * out_q) + sum(dk * out_k) in q, k (dq_in, dk_in: strides soq, sok) and the weights
+ * (of w_dtype, summed over tokens and heads in a fixed order; each nullable, without both no workspace is
+ * needed).  sdq, sdk: strides of dq and dk. */
+kata_status kata_bwd_qk_norm(const kata_qk_norm_problem* pr, const void* dq, const void* dk, const void* q,
+                             const void* k, const void* q_weight, const void* k_weight,
+                             const double* rates, const void* positions, const int32_t* axes, void* dq_in,
+                             void* dk_in, void* dq_weight, void* dk_weight, void* workspace,
+                             size_t ws_bytes, void* stream);
+
 /* ---- Layer norm ----------------------------------------------------------------------------
  *     hat = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  y = hat weight + bias
  * over rows of N elements, statistics and sums in fp32.  sx, sy, sdy, sdx: elements from a row of x, y,

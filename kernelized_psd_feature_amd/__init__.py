@@ -20,6 +20,11 @@ and the parts of a layer without the denominator (layer.py):
     q, k = rotary(q, k, rates)                  # rotary positions
     y = layer_norm(x, weight, bias)
 
+and of one whose state is corrected (delta.py):
+
+    o = parallel_delta_attn(q, k, v, beta, log_decay, qk_norm="l2")   # gated delta rule
+    q, k = qk_norm(q, k, q_weight, k_weight, rates=rates)   # norm of every head, turned in the same pass
+
 q, k: (B, T, H, p); v: (B, T, H, dv) -- the layout of the pages' kernel call -- with the last
 dimension contiguous; any (b, t, h) strides that keep rows 16-byte aligned are accepted
 (e.g. a head-major (B, H, T, D) tensor passed as .transpose(1, 2)).
@@ -40,6 +45,7 @@ __all__ = [
     "parallel_decay_attn", "rotary_rates", "rotary", "layer_norm", "fwd_layer_norm",
     "bwd_layer_norm", "layer_norm_workspace_size",
     "fwd_delta", "bwd_delta", "decode_delta", "delta_state_shape", "delta_workspace_size",
+    "parallel_delta_attn", "qk_norm", "fwd_qk_norm", "bwd_qk_norm", "qk_norm_workspace_size", "rotary_axes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -431,7 +437,8 @@ def timing_end():
 from . import layer  # noqa: E402  (needs the helpers above)
 from .layer import (  # noqa: E402
     bwd_decay, bwd_layer_norm, decay_state_shape, decay_workspace_size, decode_decay, fwd_decay,
-    fwd_layer_norm, layer_norm, layer_norm_workspace_size, parallel_decay_attn, rotary, rotary_rates)
+    fwd_layer_norm, layer_norm, layer_norm_workspace_size, parallel_decay_attn, rotary, rotary_axes, rotary_rates)
 from . import delta  # noqa: E402
 from .delta import (  # noqa: E402
-    bwd_delta, decode_delta, delta_state_shape, delta_workspace_size, fwd_delta)
+    bwd_delta, bwd_qk_norm, decode_delta, delta_state_shape, delta_workspace_size, fwd_delta, fwd_qk_norm,
+    parallel_delta_attn, qk_norm, qk_norm_workspace_size)

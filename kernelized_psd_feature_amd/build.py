@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libkata.so")
 
 SOURCES = ["kata_api.cpp", "plan.cpp", "generic.hip", "scan.hip", "bwd.hip", "fast.hip", "fast32.hip",
            "quadratic.hip", "decode.hip", "bwd_chunked.hip", "decay.hip", "rotary.hip",
-           "layer_norm.hip", "layer_plan.cpp", "layer_api.cpp", "delta.hip", "delta_bwd.hip", "delta_plan.cpp", "delta_api.cpp"]
+           "layer_norm.hip", "layer_plan.cpp", "layer_api.cpp", "delta.hip", "delta_bwd.hip", "delta_plan.cpp", "delta_api.cpp",
+           "qk_norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -241,10 +241,9 @@ kata_status kata_decode_decay(const kata_decay_problem* pr, const void* q, const
                        "decayed attention decode");
 }
 
-kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void* k,
-                        const double* rates, const void* positions, void* out_q, void* out_k,
-                        void* stream) {
-  clear_error();
+static kata_status run_rotary(const kata_rotary_problem* pr, const void* q, const void* k,
+                              const double* rates, const void* positions, const int32_t* axes,
+                              int32_t n_axes, int64_t pos_a, void* out_q, void* out_k, void* stream) {
   std::string why;
   kata_status s = kata::validate_rotary(pr, &why);
   if (s != KATA_OK) return set_error(s, why);
@@ -270,6 +269,7 @@ kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void
   a.q = q; a.k = k; a.oq = out_q; a.ok = out_k;
   a.rates = rates;
   a.positions = positions;
+  a.axes = axes; a.n_axes = n_axes; a.pos_a = pos_a;
   a.pos_b = pr->pos_b; a.pos_t = pr->pos_t; a.offset = pr->offset;
   copy3(a.sq, pr->sq); copy3(a.sk, pr->sk); copy3(a.soq, pr->soq); copy3(a.sok, pr->sok);
   a.B = pr->B; a.T = pr->T; a.H = pr->H; a.Hk = pr->Hk; a.D = pr->D; a.rot = pr->rot;
@@ -279,6 +279,109 @@ kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void
   Timed t(KATA_K_ROTARY, st);
   return launch_status(kata::launch_rotary(a, pr->dtype == KATA_BF16, aligned, pr->interleaved != 0, st),
                        "rotary positions");
+}
+
+kata_status kata_rotary(const kata_rotary_problem* pr, const void* q, const void* k,
+                        const double* rates, const void* positions, void* out_q, void* out_k,
+                        void* stream) {
+  clear_error();
+  return run_rotary(pr, q, k, rates, positions, nullptr, 1, 0, out_q, out_k, stream);
+}
+
+// Positions of several axes.
+static kata_status check_axes(const void* positions, const int32_t* axes, int32_t n_axes, int64_t pos_a) {
+  if (!positions || !axes) return set_error(KATA_ERR_INVALID_ARGUMENT, "positions or axes is null");
+  if (n_axes < 1 || pos_a < 0)
+    return set_error(KATA_ERR_INVALID_ARGUMENT, "n_axes must be >= 1, the axes' stride not negative");
+  return need_aligned(axes, 4, "axes");
+}
+
+kata_status kata_rotary_axes(const kata_rotary_problem* pr, const void* q, const void* k,
+                             const double* rates, const void* positions, const int32_t* axes,
+                             int32_t n_axes, int64_t pos_a, void* out_q, void* out_k, void* stream) {
+  clear_error();
+  const kata_status s = check_axes(positions, axes, n_axes, pos_a);
+  return s != KATA_OK ? s : run_rotary(pr, q, k, rates, positions, axes, n_axes, pos_a, out_q, out_k, stream);
+}
+
+// dq, dk: null in the forward pass.
+static kata_status run_qk_norm(const kata_qk_norm_problem* pr, const void* dq, const void* dk, const void* q,
+                               const void* k, const void* q_weight, const void* k_weight, const double* rates,
+                               const void* positions, const int32_t* axes, void* out_q, void* out_k,
+                               void* dq_weight, void* dk_weight, float* part, hipStream_t st, const char* what) {
+  const bool backward = dq != nullptr;
+  if (!q || !out_q) return set_error(KATA_ERR_INVALID_ARGUMENT, "q or its output is null");
+  if (pr->Hk && (!k || !out_k || (backward && !dk)))
+    return set_error(KATA_ERR_INVALID_ARGUMENT, "k, its output or its gradient is null");
+  kata_status s;
+  if (pr->rot) {
+    if (!rates) return set_error(KATA_ERR_INVALID_ARGUMENT, "rates is null");
+    if (axes && (s = check_axes(positions, axes, pr->n_axes, pr->pos_a)) != KATA_OK) return s;
+    if ((s = need_aligned(rates, 8, "rates")) != KATA_OK) return s;
+    if ((s = need_aligned(positions, pr->pos64 ? 8 : 4, "positions")) != KATA_OK) return s;
+  }
+  const size_t es = kata::elem_size(pr->dtype), ew = kata::elem_size(pr->w_dtype);
+  const void* ptrs[6] = {q, out_q, dq, k, out_k, dk};
+  const int64_t* sts[6] = {pr->sq, pr->soq, pr->sdq, pr->sk, pr->sok, pr->sdk};
+  const char* names[6] = {"q", "out q", "dq", "k", "out k", "dk"};
+  bool aligned = true;
+  for (int i = 0; i < (pr->Hk ? 6 : 3); ++i) {
+    if (!ptrs[i]) continue;                         // gradients of a forward pass
+    if ((s = need_aligned(ptrs[i], es, names[i])) != KATA_OK) return s;
+    aligned &= reinterpret_cast<uintptr_t>(ptrs[i]) % 16 == 0;
+    const int64_t sizes[3] = {pr->B, pr->T, i < 3 ? pr->H : pr->Hk};
+    for (int j = 0; j < 3; ++j) aligned &= sizes[j] == 1 || sts[i][j] * (int64_t)es % 16 == 0;
+  }
+  const void* weights[4] = {q_weight, k_weight, dq_weight, dk_weight};
+  for (const void* w : weights)
+    if ((s = need_aligned(w, ew, "a weight or its gradient")) != KATA_OK) return s;
+  if ((s = check_device()) != KATA_OK) return s;
+  kata::QkNormArgs a{};
+  a.q = q; a.k = k; a.dq = dq; a.dk = dk; a.wq = q_weight; a.wk = k_weight;
+  a.oq = out_q; a.ok = out_k; a.dwq = dq_weight; a.dwk = dk_weight;
+  a.part = part;
+  a.rates = rates; a.positions = positions; a.axes = axes;
+  a.pos_a = pr->pos_a; a.pos_b = pr->pos_b; a.pos_t = pr->pos_t; a.offset = pr->offset;
+  copy3(a.sq, pr->sq); copy3(a.sk, pr->sk); copy3(a.soq, pr->soq); copy3(a.sok, pr->sok);
+  copy3(a.sdq, pr->sdq); copy3(a.sdk, pr->sdk);
+  a.B = pr->B; a.T = pr->T; a.H = pr->H; a.Hk = pr->Hk; a.D = pr->D; a.rot = pr->rot;
+  a.pos64 = pr->pos64; a.inverse = backward; a.n_axes = pr->n_axes; a.w_bf16 = pr->w_dtype == KATA_BF16;
+  a.magnitude = pr->magnitude; a.eps = pr->eps; a.count = pr->l2 ? 1.f : (float)pr->D;
+  Timed t(KATA_K_NORM, st);
+  return launch_status(kata::launch_qk_norm(a, pr->dtype == KATA_BF16, aligned, pr->interleaved != 0, backward, st), what);
+}
+
+kata_status kata_fwd_qk_norm(const kata_qk_norm_problem* pr, const void* q, const void* k,
+                             const void* q_weight, const void* k_weight, const double* rates,
+                             const void* positions, const int32_t* axes, void* out_q, void* out_k,
+                             void* stream) {
+  clear_error();
+  std::string why;
+  const kata_status s = kata::validate_qk_norm(pr, false, &why);
+  if (s != KATA_OK) return set_error(s, why);
+  return run_qk_norm(pr, nullptr, nullptr, q, k, q_weight, k_weight, rates, positions, axes, out_q, out_k, nullptr,
+                     nullptr, nullptr, reinterpret_cast<hipStream_t>(stream), "norm of queries and keys");
+}
+
+size_t kata_bwd_qk_norm_workspace_size(const kata_qk_norm_problem* pr) {
+  return kata::validate_qk_norm(pr, true, nullptr) == KATA_OK ? size_t(kata::kQkNormBlocks) * 2 * pr->D * 4 : 0;
+}
+
+kata_status kata_bwd_qk_norm(const kata_qk_norm_problem* pr, const void* dq, const void* dk, const void* q,
+                             const void* k, const void* q_weight, const void* k_weight,
+                             const double* rates, const void* positions, const int32_t* axes, void* dq_in,
+                             void* dk_in, void* dq_weight, void* dk_weight, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  clear_error();
+  std::string why;
+  kata_status s = kata::validate_qk_norm(pr, true, &why);
+  if (s != KATA_OK) return set_error(s, why);
+  if (!dq) return set_error(KATA_ERR_INVALID_ARGUMENT, "dq is null");
+  const bool sums = dq_weight || dk_weight;
+  if (sums && (s = check_workspace(workspace, ws_bytes, kata_bwd_qk_norm_workspace_size(pr))) != KATA_OK) return s;
+  return run_qk_norm(pr, dq, dk, q, k, q_weight, k_weight, rates, positions, axes, dq_in, dk_in, dq_weight, dk_weight,
+                     sums ? static_cast<float*>(workspace) : nullptr, reinterpret_cast<hipStream_t>(stream),
+                     "norm of queries and keys backward");
 }
 
 static kata_status check_norm(const kata_norm_problem* pr, bool backward) {

@@ -152,6 +152,29 @@ kata_status validate_rotary(const kata_rotary_problem* pr, std::string* why) {
   return check_strides("out k", pr->sok, sizes_k, pr->D, true, why);
 }
 
+kata_status validate_qk_norm(const kata_qk_norm_problem* pr, bool backward, std::string* why) {
+  if (!pr) return fail(why, KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
+  kata_rotary_problem r{};
+  r.B = pr->B; r.T = pr->T; r.H = pr->H; r.Hk = pr->Hk; r.D = pr->D; r.rot = pr->rot;
+  r.dtype = pr->dtype;
+  r.magnitude = pr->magnitude;
+  r.pos_b = pr->pos_b; r.pos_t = pr->pos_t;
+  std::copy_n(pr->sq, 3, r.sq); std::copy_n(pr->sk, 3, r.sk);
+  std::copy_n(pr->soq, 3, r.soq); std::copy_n(pr->sok, 3, r.sok);
+  kata_status s = validate_rotary(&r, why);
+  if (s != KATA_OK) return s;
+  if (pr->D > 256) return fail(why, KATA_ERR_UNSUPPORTED, "D exceeds 256");
+  if (pr->w_dtype != KATA_F32 && !(pr->w_dtype == KATA_BF16 && pr->dtype == KATA_BF16))
+    return fail(why, KATA_ERR_INVALID_ARGUMENT, "weights must be fp32, or bf16 with bf16 rows");
+  if (!std::isfinite(pr->eps) || pr->eps < 0.f)
+    return fail(why, KATA_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+  if (pr->pos_a < 0) return fail(why, KATA_ERR_INVALID_ARGUMENT, "negative stride of positions");
+  if (!backward) return KATA_OK;
+  const int64_t sizes[3] = {pr->B, pr->T, pr->H}, sizes_k[3] = {pr->B, pr->T, pr->Hk};
+  if ((s = check_strides("dq", pr->sdq, sizes, pr->D, false, why)) != KATA_OK) return s;
+  return pr->Hk ? check_strides("dk", pr->sdk, sizes_k, pr->D, false, why) : KATA_OK;
+}
+
 kata_status validate_norm(const kata_norm_problem* pr, bool backward, std::string* why) {
   if (!pr) return fail(why, KATA_ERR_INVALID_ARGUMENT, "problem pointer is null");
   if (pr->rows < 1 || pr->N < 1) return fail(why, KATA_ERR_INVALID_ARGUMENT, "rows and N must be >= 1");

@@ -46,6 +46,9 @@ kata_status validate_norm(const kata_norm_problem* pr, bool backward, std::strin
 // Workgroups whose partial sums of dw and db the backward pass keeps at most: of rows in registers, and
 // of wider ones than kNormInRegisters elements (layer_norm.hip).
 constexpr int kNormBlocks = 768, kNormLoopBlocks = 64, kNormInRegisters = 8192;
+// Workgroups whose partial sums of the weights' gradients kata_bwd_qk_norm keeps at most.
+constexpr int kQkNormBlocks = 1024;
+kata_status validate_qk_norm(const kata_qk_norm_problem* pr, bool backward, std::string* why);
 size_t norm_workspace_bytes(const kata_norm_problem* pr);
 
 }  // namespace kata

@@ -62,6 +62,7 @@ def _signatures():
         "kata_bwd_decay": (_I32, [VP] * 14 + [SZ, VP]),
         "kata_decode_decay": (_I32, [VP] * 8),
         "kata_rotary": (_I32, [VP] * 8),
+        "kata_rotary_axes": (_I32, [VP] * 6 + [_I32, _I64] + [VP] * 3),
         "kata_fwd_layer_norm": (_I32, [VP] * 8),
         "kata_bwd_layer_norm_workspace_size": (SZ, [VP]),
         "kata_bwd_layer_norm": (_I32, [VP] * 10 + [SZ, VP]),
@@ -313,13 +314,53 @@ def rotary_rates(dim, base=10000.0, scaling=None, factor=1.0, original_length=No
     return rates.to(device), magnitude
 
 
+def rotary_axes(sections, interleaved=False, device="cuda"):
+    """Which axis each pair of coordinates turns by, for positions with several axes: an int32 vector of
+    sum(sections) pairs, sections[a] of them for axis a, one section behind the other, or with interleaved
+    dealt out in turn while a section has some left."""
+    if not sections or any(n < 0 for n in sections):
+        raise ValueError("sections must be counts of pairs, one for each axis")
+    axes = [a for a, n in enumerate(sections) for _ in range(n)]
+    if interleaved:
+        axes = [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+    return torch.tensor(axes, dtype=torch.int32).to(device)
+
+
+def _positions(positions, axes, B, T, pairs, device):
+    """(pos64, axes, stride of the axes, of b, of t, address) of positions that broadcast to (B, T), or with
+    axes to (axes, B, T)."""
+    if positions is None:
+        if axes is not None:
+            raise ValueError("several axes need positions")
+        return 0, 1, 0, 0, 0, None
+    if positions.dtype not in (torch.int32, torch.int64) or positions.device != device:
+        raise ValueError(f"positions must be int32 or int64 on {device}")
+    pos64 = int(positions.dtype == torch.int64)
+    if axes is None:
+        try:
+            x = positions if positions.shape == (B, T) else positions.expand(B, T)
+        except RuntimeError:
+            raise ValueError("positions must broadcast to (B, T)") from None
+        return pos64, 1, 0, *x.stride(), positions.data_ptr()
+    if axes.shape != (pairs,) or axes.dtype != torch.int32 or not axes.is_contiguous() or axes.device != device:
+        raise ValueError(f"axes must be a contiguous int32 vector of an axis for each rate on {device}")
+    try:
+        x = positions.expand(positions.shape[0], B, T) if positions.dim() == 3 and positions.shape[0] else None
+    except RuntimeError:
+        x = None
+    if x is None:
+        raise ValueError("positions must broadcast to (axes, B, T)")
+    return pos64, x.shape[0], *x.stride(), positions.data_ptr()
+
+
 def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1.0, inverse=False,
-           out=None):
+           out=None, axes=None):
     """q and k turned by their positions in one launch: the first 2 * len(rates) coordinates of every
     head, as pairs (i, i + len(rates)), or neighbours with interleaved; the others are copied.
 
     q (B, T, H, D) and k (B, T, Hk, D) (or None), bf16 or fp32; positions: int32 or int64, broadcastable
-    to (B, T), or None: offset + t.  inverse negates the angles: the gradient.  out: outputs of q (and
+    to (B, T), or None: offset + t.  axes (rotary_axes): positions have several axes, (axes, B, T), and pair i
+    turns by that of axis axes[i].  inverse negates the angles: the gradient.  out: outputs of q (and
     k), which may be q and k themselves and overlap neither otherwise.  Returns the turned q, or the pair."""
     device, dtype, shape = q.device, q.dtype, q.shape
     if not q.is_cuda:
@@ -352,23 +393,17 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
         for name, x in (("q", q), ("k", k), ("out", oq), ("out", ok)):
             if x is not None:
                 _rows_ok(x, name)
-    pos64 = pos_b = pos_t = 0
-    at = None
-    if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64) or positions.device != device:
-            raise ValueError(f"positions must be int32 or int64 on {device}")
-        try:
-            x = positions if positions.shape == (B, T) else positions.expand(B, T)
-        except RuntimeError:
-            raise ValueError("positions must broadcast to (B, T)") from None
-        pos64, (pos_b, pos_t), at = int(positions.dtype == torch.int64), x.stride(), positions.data_ptr()
+    pos64, n_axes, pos_a, pos_b, pos_t, at = _positions(positions, axes, B, T, n, device)
     pq, poq = q.data_ptr(), oq.data_ptr()
     if H == 0 and Hk:                                # only k has heads: its turn is a call of one tensor
         H, sq, soq, pq, poq, Hk = Hk, sk, sok, pk, pok, 0
     if B * T * H * D:
         pr = _ROTARY.pack(B, T, H, Hk, D, 2 * n, _dtype(dtype), 1 if interleaved else 0, 1 if inverse else 0,
                           pos64, magnitude, pos_b, pos_t, offset, *sq[:3], *sk[:3], *soq[:3], *sok[:3])
-        _run("kata_rotary", device, pr, pq, pk, rates.data_ptr(), at, poq, pok)
+        if axes is None:
+            _run("kata_rotary", device, pr, pq, pk, rates.data_ptr(), at, poq, pok)
+        else:
+            _run("kata_rotary_axes", device, pr, pq, pk, rates.data_ptr(), at, axes.data_ptr(), n_axes, pos_a, poq, pok)
     if out is not None:
         _written(outs)
     return oq if k is None else (oq, ok)
@@ -509,19 +544,19 @@ class _Decay(torch.autograd.Function):
 
 class _Rotary(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, rates, positions, offset, interleaved, magnitude):
-        ctx.save_for_backward(rates, positions)
+    def forward(ctx, q, k, rates, positions, offset, interleaved, magnitude, axes):
+        ctx.save_for_backward(rates, positions, axes)
         ctx.cfg = (offset, interleaved, magnitude)
-        return rotary(q, k, rates, positions, offset, interleaved, magnitude)
+        return rotary(q, k, rates, positions, offset, interleaved, magnitude, axes=axes)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
-        rates, positions = ctx.saved_tensors
+        rates, positions, axes = ctx.saved_tensors
         offset, interleaved, magnitude = ctx.cfg
         dq, dk = rotary(dq.contiguous(), dk.contiguous(), rates, positions, offset, interleaved,
-                        magnitude, inverse=True)
-        return dq, dk, None, None, None, None, None
+                        magnitude, inverse=True, axes=axes)
+        return dq, dk, None, None, None, None, None, None
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -547,9 +582,21 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
 
 
 def turn(q, k, rotary_table, positions=None, offset=0, interleaved=False):
-    """rotary() under torch autograd; rotary_table: (rates, magnitude) as rotary_rates returns them."""
-    rates, magnitude = rotary_table
-    return _Rotary.apply(q, k, rates, positions, offset, interleaved, magnitude)
+    """rotary() under torch autograd; rotary_table: (rates, magnitude) as rotary_rates returns them, with
+    positions of several axes (rates, magnitude, axes)."""
+    rates, magnitude, axes = (*rotary_table, None)[:3]
+    return _Rotary.apply(q, k, rates, positions, offset, interleaved, magnitude, axes)
+
+
+def norm_heads(o, norm):
+    """Layer norm of (B, T, H, dv) outputs; norm: (weight, bias[, eps]), over each head for a weight of dv elements,
+    over all heads of a token for one of H dv."""
+    weight, bias, eps = (*norm, 1e-5)[:3]
+    H, dv = o.shape[2:]
+    n = weight.numel() if weight is not None else dv
+    if n < 1 or n not in (dv, H * dv):
+        raise ValueError("the norm's weight must have dv or H * dv elements")
+    return layer_norm(o.reshape(*o.shape[:2], H * dv // n, n), weight, bias, eps).reshape(o.shape)
 
 
 def parallel_decay_attn(q, k, v, log_decay, scale=1.0, initial_state=None, return_state=False,
@@ -570,10 +617,5 @@ def parallel_decay_attn(q, k, v, log_decay, scale=1.0, initial_state=None, retur
     got = _Decay.apply(q, k, v, log_decay, scale, initial_state, cu_seqlens, return_state)
     o, final = got if return_state else (got, None)
     if norm is not None:
-        weight, bias, eps = (*norm, 1e-5)[:3]
-        H, dv = v.shape[2:]
-        n = weight.numel() if weight is not None else dv
-        if n < 1 or n not in (dv, H * dv):
-            raise ValueError("the norm's weight must have dv or H * dv elements")
-        o = layer_norm(o.reshape(*o.shape[:2], H * dv // n, n), weight, bias, eps).reshape(v.shape)
+        o = norm_heads(o, norm)
     return (o, final) if return_state else o
