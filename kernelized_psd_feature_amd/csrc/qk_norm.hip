@@ -41,8 +41,17 @@ struct Lane {
       n[k] = max(0, min(V, (turns[k] ? turned : A.D) - e[k]));
     }
   }
-  // the item's elements, and (halves) their partners, zeros behind them
-  __device__ __forceinline__ void load(const T* row, int k, float (&x)[V], float (&z)[V]) const {
+  // the item's vector, and (halves) its partners' (both loads without a branch: a lane without an item, and an
+  // item without partners, repeat one); kEdge: whole vectors only
+  __device__ __forceinline__ void fetch(const T* row, int k, u32x4& u, u32x4& v) const {
+    const bool whole = n[k] == V;
+    if (kEdge && !whole) return;
+    const T* const at = row + (whole ? e[k] : 0);
+    u = get<T, kEdge>(at);
+    if (!IL) v = get<T, kEdge>(at + (whole && turns[k] ? half : 0));
+  }
+  // the elements and partners, zeros behind them
+  __device__ __forceinline__ void load(const T* row, int k, const u32x4& u, const u32x4& v, float (&x)[V], float (&z)[V]) const {
     if (kEdge && n[k] < V) {
 #pragma unroll
       for (int r = 0; r < V; ++r) {
@@ -51,9 +60,6 @@ struct Lane {
       }
       return;
     }
-    // (both loads without a branch: a lane without an item, and an item without partners, repeat one)
-    const T* const at = row + (n[k] ? e[k] : 0);
-    const u32x4 u = get<T, kEdge>(at), v = IL ? u : get<T, kEdge>(at + (turns[k] ? half : 0));
     unpack(u, x);
     unpack(v, z);
 #pragma unroll
@@ -99,16 +105,12 @@ struct Lane {
         }
     }
   }
-  // the weight's elements, ones without a weight
-  __device__ __forceinline__ void weight(const void* w, bool bf16, int k, float (&x)[V], float (&z)[V]) const {
-    auto at = [&](int i) { return bf16 ? to_f32(reinterpret_cast<const __bf16*>(w)[i]) : reinterpret_cast<const float*>(w)[i]; };
+  // the item's elements of a weight
+  __device__ __forceinline__ void weight(const float* w, int k, float (&x)[V], float (&z)[V]) const {
 #pragma unroll
     for (int r = 0; r < V; ++r) {
-      x[r] = z[r] = 1.f;
-      if (w && r < n[k]) {
-        x[r] = at(e[k] + r);
-        if (!IL && turns[k]) z[r] = at(e[k] + half + r);
-      }
+      x[r] = r < n[k] ? w[e[k] + r] : 1.f;
+      z[r] = !IL && turns[k] && r < n[k] ? w[e[k] + half + r] : 1.f;
     }
   }
 };
@@ -116,19 +118,22 @@ struct Lane {
 template <typename T, bool IL, bool kEdge, int K, bool kBackward>
 __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkNormArgs A) {
   using L = Lane<T, IL, kEdge, K>;
-  constexpr int V = L::V, U = kBackward || K > 1 ? 1 : 2;              // rows in flight
-  extern __shared__ __align__(16) float2 cs[];      // [tokens of the block][rot / 2], then (backward) the sums
+  constexpr int V = L::V;
+  extern __shared__ __align__(16) float2 cs[];      // [tokens of the block][rot / 2] and the weights; then (backward) the sums
   const int tid = threadIdx.x, G = kThreads / A.R, group = tid / A.R, half = A.rot / 2;
   const unsigned total = (unsigned)A.B * (unsigned)A.T;                // < 2^31
   const unsigned n_blocks = (total + A.TT - 1) / A.TT, mine = block_number();
   if (mine >= n_blocks) return;                     // behind the last of several grid rows
   const L lane(A, tid % A.R);
-  float w[2][K][2][V];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    lane.weight(A.wq, A.w_bf16, k, w[0][k][0], w[0][k][1]);
-    lane.weight(A.wk, A.w_bf16, k, w[1][k][0], w[1][k][1]);
+  // the weights as fp32 through LDS: a lane's elements of them one by one from memory, for each workgroup, cost a
+  // fifth of the pass
+  float* const sw = reinterpret_cast<float*>(cs + A.TT * half);        // [2][D]
+  for (int i = tid; i < 2 * A.D; i += kThreads) {
+    const void* const p = i < A.D ? A.wq : A.wk;
+    const int at = i < A.D ? i : i - A.D;
+    sw[i] = !p ? 1.f : A.w_bf16 ? to_f32(reinterpret_cast<const __bf16*>(p)[at]) : reinterpret_cast<const float*>(p)[at];
   }
+  float w[2][K][2][V];
   float sum[2][K][2][V];
   if constexpr (kBackward)
 #pragma unroll
@@ -138,84 +143,101 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkNormArgs A) {
   const int heads = A.H + A.Hk;
   const float inv_n = 1.f / A.count;
 
+  // A row on its way.  Forward its loads are issued before the angles are formed, or while the row before it is
+  // computed (8 x 4096, 16 and 8 heads of 64: 45 us for 49; backward the registers would cost more, 81 us for 69).
+  struct Row {
+    int tt;
+    bool live, is_k;
+    const T *src, *grad;
+    T* dst;
+    u32x4 x[K], z[K], dx[K], dz[K];
+  };
   // (forward: one turn of the loop)
   for (unsigned block = mine; block < n_blocks; block += kBackward ? (unsigned)A.blocks : n_blocks) {
     const unsigned first = block * (unsigned)A.TT;
     const int tokens = (int)min((unsigned)A.TT, total - first), rows = tokens * heads;
+    auto fetch = [&](int row, Row& R) {
+      R.live = row < rows;
+      const int y = R.live ? row : rows - 1;        // (others read the last row again)
+      R.tt = y / heads;
+      const int hh = y - R.tt * heads;
+      R.is_k = hh >= A.H;
+      const int h = hh - (R.is_k ? A.H : 0);
+      const unsigned token = first + R.tt;
+      const int b = int(token / (unsigned)A.T), t = int(token - (unsigned)b * (unsigned)A.T);
+      R.src = reinterpret_cast<const T*>(R.is_k ? A.k : A.q) + row_off(R.is_k ? A.sk : A.sq, b, t, h);
+      R.dst = reinterpret_cast<T*>(R.is_k ? A.ok : A.oq) + row_off(R.is_k ? A.sok : A.soq, b, t, h);
+#pragma unroll
+      for (int k = 0; k < K; ++k) lane.fetch(R.src, k, R.x[k], R.z[k]);
+      if constexpr (kBackward) {
+        R.grad = reinterpret_cast<const T*>(R.is_k ? A.dk : A.dq) + row_off(R.is_k ? A.sdk : A.sdq, b, t, h);
+#pragma unroll
+        for (int k = 0; k < K; ++k) lane.fetch(R.grad, k, R.dx[k], R.dz[k]);
+      }
+    };
+    Row next{};
+    if constexpr (!kBackward) fetch(group, next);
     if (kBackward && block != mine) __syncthreads();
     put_turns(A, cs, first, tokens, kThreads);
     __syncthreads();
-    for (int row0 = 0; row0 < rows; row0 += U * G) {
-      float x[U][K][V], z[U][K][V], dx[U][K][V], dz[U][K][V];
-      int tt[U];
-      bool live[U], is_k[U];
-      T* dst[U];
+    if (block == mine)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int row = row0 + u * G + group;
-        live[u] = row < rows;
-        const int y = live[u] ? row : rows - 1;     // (others read the last row again)
-        tt[u] = y / heads;
-        const int hh = y - tt[u] * heads;
-        is_k[u] = hh >= A.H;
-        const int h = hh - (is_k[u] ? A.H : 0);
-        const unsigned token = first + tt[u];
-        const int b = int(token / (unsigned)A.T), t = int(token - (unsigned)b * (unsigned)A.T);
-        const T* src = reinterpret_cast<const T*>(is_k[u] ? A.k : A.q) + row_off(is_k[u] ? A.sk : A.sq, b, t, h);
-        dst[u] = reinterpret_cast<T*>(is_k[u] ? A.ok : A.oq) + row_off(is_k[u] ? A.sok : A.soq, b, t, h);
+      for (int k = 0; k < K; ++k) {
+        lane.weight(sw, k, w[0][k][0], w[0][k][1]);
+        lane.weight(sw + A.D, k, w[1][k][0], w[1][k][1]);
+      }
+    for (int row0 = 0; row0 < rows; row0 += G) {
+      if constexpr (kBackward) fetch(row0 + group, next);
+      const Row row = next;
+      if constexpr (!kBackward)
+        if (row0 + G < rows) fetch(row0 + G + group, next);
+      const float2* at = cs + row.tt * half;
+      float x[K][V], z[K][V], dx[K][V], dz[K][V];
+      float ss = 0.f, st = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) lane.load(src, k, x[u][k], z[u][k]);
+      for (int k = 0; k < K; ++k) {
+        lane.load(row.src, k, row.x[k], row.z[k], x[k], z[k]);
         if constexpr (kBackward) {
-          const T* grad = reinterpret_cast<const T*>(is_k[u] ? A.dk : A.dq) + row_off(is_k[u] ? A.sdk : A.sdq, b, t, h);
+          lane.load(row.grad, k, row.dx[k], row.dz[k], dx[k], dz[k]);
+          lane.turn(at, k, dx[k], dz[k]);
+        }
 #pragma unroll
-          for (int k = 0; k < K; ++k) lane.load(grad, k, dx[u][k], dz[u][k]);
+        for (int r = 0; r < V; ++r) {
+          ss = fmaf(x[k][r], x[k][r], ss);
+          ss = fmaf(z[k][r], z[k][r], ss);
+          if constexpr (kBackward) {
+            st = fmaf(dx[k][r] * (row.is_k ? w[1][k][0][r] : w[0][k][0][r]), x[k][r], st);
+            st = fmaf(dz[k][r] * (row.is_k ? w[1][k][1][r] : w[0][k][1][r]), z[k][r], st);
+          }
         }
       }
+      for (int d = 1; d < A.R; d <<= 1) {
+        ss += __shfl_xor(ss, d);
+        if constexpr (kBackward) st += __shfl_xor(st, d);
+      }
+      const float r_ = 1.f / sqrtf(fmaf(ss, inv_n, A.eps)), c = r_ * r_ * st * inv_n;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float ss = 0.f, st = 0.f;
-        const float2* at = cs + tt[u] * half;
+      for (int k = 0; k < K; ++k) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if constexpr (kBackward) lane.turn(at, k, dx[u][k], dz[u][k]);
-#pragma unroll
-          for (int r = 0; r < V; ++r) {
-            ss = fmaf(x[u][k][r], x[u][k][r], ss);
-            ss = fmaf(z[u][k][r], z[u][k][r], ss);
-            if constexpr (kBackward) {
-              st = fmaf(dx[u][k][r] * (is_k[u] ? w[1][k][0][r] : w[0][k][0][r]), x[u][k][r], st);
-              st = fmaf(dz[u][k][r] * (is_k[u] ? w[1][k][1][r] : w[0][k][1][r]), z[u][k][r], st);
+        for (int r = 0; r < V; ++r) {
+          const float wx = row.is_k ? w[1][k][0][r] : w[0][k][0][r], wz = row.is_k ? w[1][k][1][r] : w[0][k][1][r];
+          if constexpr (kBackward) {
+            if (row.live) {
+              const float ax = dx[k][r] * (x[k][r] * r_), az = dz[k][r] * (z[k][r] * r_);
+              sum[0][k][0][r] += row.is_k ? 0.f : ax;
+              sum[0][k][1][r] += row.is_k ? 0.f : az;
+              sum[1][k][0][r] += row.is_k ? ax : 0.f;
+              sum[1][k][1][r] += row.is_k ? az : 0.f;
             }
+            x[k][r] = r_ * (dx[k][r] * wx - x[k][r] * c);
+            z[k][r] = r_ * (dz[k][r] * wz - z[k][r] * c);
+          } else {
+            x[k][r] *= r_ * wx;
+            z[k][r] *= r_ * wz;
           }
         }
-        for (int d = 1; d < A.R; d <<= 1) {
-          ss += __shfl_xor(ss, d);
-          if constexpr (kBackward) st += __shfl_xor(st, d);
-        }
-        const float r_ = 1.f / sqrtf(fmaf(ss, inv_n, A.eps)), c = r_ * r_ * st * inv_n;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-#pragma unroll
-          for (int r = 0; r < V; ++r) {
-            const float wx = is_k[u] ? w[1][k][0][r] : w[0][k][0][r], wz = is_k[u] ? w[1][k][1][r] : w[0][k][1][r];
-            if constexpr (kBackward) {
-              if (live[u]) {
-                const float ax = dx[u][k][r] * (x[u][k][r] * r_), az = dz[u][k][r] * (z[u][k][r] * r_);
-                sum[0][k][0][r] += is_k[u] ? 0.f : ax;
-                sum[0][k][1][r] += is_k[u] ? 0.f : az;
-                sum[1][k][0][r] += is_k[u] ? ax : 0.f;
-                sum[1][k][1][r] += is_k[u] ? az : 0.f;
-              }
-              x[u][k][r] = r_ * (dx[u][k][r] * wx - x[u][k][r] * c);
-              z[u][k][r] = r_ * (dz[u][k][r] * wz - z[u][k][r] * c);
-            } else {
-              x[u][k][r] *= r_ * wx;
-              z[u][k][r] *= r_ * wz;
-            }
-          }
-          if constexpr (!kBackward) lane.turn(at, k, x[u][k], z[u][k]);
-          if (live[u]) lane.store(dst[u], k, x[u][k], z[u][k]);
-        }
+        if constexpr (!kBackward) lane.turn(at, k, x[k], z[k]);
+        if (row.live) lane.store(row.dst, k, x[k], z[k]);
       }
     }
   }
@@ -243,18 +265,31 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkNormArgs A) {
   }
 }
 
-// Columns of the partial sums: four slices of the workgroups' rows, each in order, then the slices.
+// Sixteen columns of the partial sums: sixteen slices of the workgroups' rows, each in order with many loads on
+// their way, then the slices.
 __global__ __launch_bounds__(kThreads) void qk_norm_sum_kernel(QkNormArgs A) {
-  __shared__ float slice[4][64];
-  const int c = threadIdx.x & 63, s = threadIdx.x >> 6, i = blockIdx.x * 64 + c;
-  const int per = (A.blocks + 3) / 4, end = min(A.blocks, (s + 1) * per);
+  __shared__ float slice[16][17];
+  const int c = threadIdx.x & 15, s = threadIdx.x >> 4, i = blockIdx.x * 16 + c, n = 2 * A.D;
+  const int per = (A.blocks + 15) / 16, end = min(A.blocks, (s + 1) * per);
   float x = 0.f;
-  if (i < 2 * A.D)
-    for (int j = s * per; j < end; ++j) x += A.part[(size_t)j * 2 * A.D + i];
+  if (i < n) {
+    const float* p = A.part + (size_t)s * per * n + i;
+    int j = s * per;
+    for (; j + 16 <= end; j += 16, p += (size_t)16 * n) {
+      float y[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) y[r] = p[(size_t)r * n];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x += y[r];
+    }
+    for (; j < end; ++j, p += n) x += *p;
+  }
   slice[s][c] = x;
   __syncthreads();
-  if (s || i >= 2 * A.D) return;
-  x = (slice[0][c] + slice[1][c]) + (slice[2][c] + slice[3][c]);
+  if (s || i >= n) return;
+  x = 0.f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) x += slice[r][c];
   void* const to = i < A.D ? A.dwq : A.dwk;
   if (!to) return;
   const int at = i < A.D ? i : i - A.D;
@@ -271,13 +306,15 @@ hipError_t launch_t(QkNormArgs& a, bool backward, hipStream_t st) {
   while (a.R < items && a.R < 64) a.R *= 2;
   const int K = items > a.R ? 2 : 1;
   const long long tokens = (long long)a.B * a.T;
-  // Two rows a group of lanes, fewer where that leaves CUs without a workgroup, and the angles within 32 KB.
-  a.TT = 2 * (kThreads / a.R) / heads;
+  // Eight rows a group of lanes (backward four, of many such blocks in turn), fewer where that leaves CUs without a
+  // workgroup, and the angles within 32 KB.  131072 tokens, 16 + 16 bf16 heads of 64: 222 us, two rows 266, four
+  // 231, sixteen 222.
+  a.TT = (backward ? 4 : 8) * (kThreads / a.R) / heads;
   if (a.TT > tokens / 512) a.TT = (int)(tokens / 512);
   if (half && a.TT * half > 4096) a.TT = 4096 / half;
   if (a.TT < 1) a.TT = 1;
   const long long n_blocks = (tokens + a.TT - 1) / a.TT;
-  size_t lds = sizeof(float2) * a.TT * half;
+  size_t lds = sizeof(float2) * a.TT * half + sizeof(float) * 2 * a.D;
   constexpr bool kMore = kEdge && sizeof(T) == 4;    // more items than a wave has lanes: at most 66
   auto run = [&](auto kernel, dim3 grid) {
     launch_kernel(kernel, grid, kThreads, lds, st, a);
@@ -294,7 +331,7 @@ hipError_t launch_t(QkNormArgs& a, bool backward, hipStream_t st) {
   hipError_t e = K == 1 ? run(qk_norm_kernel<T, IL, kEdge, 1, true>, dim3(a.blocks))
                         : run(qk_norm_kernel<T, IL, kEdge, kMore ? 2 : 1, true>, dim3(a.blocks));
   if (e != hipSuccess || !a.part) return e;
-  launch_kernel(qk_norm_sum_kernel, dim3((2 * a.D + 63) / 64), kThreads, 0, st, a);
+  launch_kernel(qk_norm_sum_kernel, dim3((2 * a.D + 15) / 16), kThreads, 0, st, a);
   return hipGetLastError();
 }
 
