@@ -20,7 +20,8 @@ __device__ __forceinline__ float exp2_diff(float hi, float lo, float hj, float l
 
 // bf16 operands that come out of fp32 sums are kept as N bf16 terms that add up to them: the recurrence passes
 // a rounding on from chunk to chunk, and states are fp32.  Two terms hold 2^-18 of a value, three 2^-27.
-// fp32: one.
+// fp32: one.  The differences are of the rounded sums: contracted with the product that a sum ended with, they would
+// depend on what the compiler makes of the path to them, and so a column on its neighbours' infinities.
 template <typename T, int N>
 struct Op {
   typename Elem<T>::frag t[N];
@@ -28,6 +29,7 @@ struct Op {
 
 template <int N>
 __device__ __forceinline__ void split_terms(f32x4 a, f32x4 b, Op<__bf16, N>& out) {
+#pragma clang fp contract(off)
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const uint2 x = quad(a, __bf16()), y = quad(b, __bf16());
@@ -69,6 +71,7 @@ __device__ __forceinline__ f32x4 mul(const Op<T, N>& a, const Op<T, K>& b, f32x4
 // Four neighbouring elements of a row as N planes of them, `plane` elements apart.
 template <int N, typename T>
 __device__ __forceinline__ void put_terms(T* at, int plane, f32x4 x) {
+#pragma clang fp contract(off)
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const Quad<T> u = quad(x, T());

@@ -161,9 +161,9 @@ kata_status validate_qk_norm(const kata_qk_norm_problem* pr, bool backward, std:
   r.pos_b = pr->pos_b; r.pos_t = pr->pos_t;
   std::copy_n(pr->sq, 3, r.sq); std::copy_n(pr->sk, 3, r.sk);
   std::copy_n(pr->soq, 3, r.soq); std::copy_n(pr->sok, 3, r.sok);
+  if (pr->D > 256) return fail(why, KATA_ERR_UNSUPPORTED, "D exceeds 256");
   kata_status s = validate_rotary(&r, why);
   if (s != KATA_OK) return s;
-  if (pr->D > 256) return fail(why, KATA_ERR_UNSUPPORTED, "D exceeds 256");
   if (pr->w_dtype != KATA_F32 && !(pr->w_dtype == KATA_BF16 && pr->dtype == KATA_BF16))
     return fail(why, KATA_ERR_INVALID_ARGUMENT, "weights must be fp32, or bf16 with bf16 rows");
   if (!std::isfinite(pr->eps) || pr->eps < 0.f)
