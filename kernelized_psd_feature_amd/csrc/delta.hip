@@ -312,9 +312,6 @@ struct TokenArgs {
   float scale;
 };
 
-__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-__device__ __forceinline__ f32x4 load4(const __bf16* p) { return unquad(*reinterpret_cast<const uint2*>(p)); }
-
 template <typename T, int LC, int RI>
 __global__ __launch_bounds__(kThreads) void delta_decode_kernel(
     TokenArgs A, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,

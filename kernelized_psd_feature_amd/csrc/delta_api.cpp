@@ -103,6 +103,8 @@ void place(kata::DeltaArgs& a, const kata::DeltaPlan& p, void* workspace) {
   a.rsums = reinterpret_cast<float*>(ws + p.rsums);
   a.cstates = reinterpret_cast<float*>(ws + p.cstates);
   a.rstates = reinterpret_cast<float*>(ws + p.rstates);
+  a.u = reinterpret_cast<float*>(ws + p.u);
+  a.x = reinterpret_cast<float*>(ws + p.x);
   a.fstates = reinterpret_cast<float*>(ws + p.fstates);
 }
 

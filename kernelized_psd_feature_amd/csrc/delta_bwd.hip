@@ -9,11 +9,11 @@
 //   PO_ij = scale exp(c_i - c_j) (dO_i . u_j) for j <= i,  PV_ij = -exp(c_i - c_j) (dv_i . u_j) for j < i
 //   dq = scale diag(y) dO S^T + PO K
 //   dk = diag(exp(c_63 - c)) U D^T - diag(y) dv S^T + PO^T Q + PV^T K + PV K
-// (the second last line but two: what S_t loses or gains from token t on is known from its products with
-// the gradients, d<dS_t, S_t> = dv_t . v_t - dO_t . o_t.)
+// (dlog: what <D, S> changes by at a token is known from its products with the gradients, dv . v - dO . o; and
+// dO . o is q . dq, a head's part of it.)
 //
-// S and D of every chunk come from two walks like the forward pass's, one of them in reversed time, which
-// keep nothing else; all the rest is then computed for all chunks at once (delta_grads_kernel).
+// S and U, and D and dv, come from two walks like the forward pass's, one of them in reversed time, which keep
+// them for every chunk; all the rest is then computed for all chunks at once (delta_grads_kernel).
 #include <type_traits>
 
 #include "delta.h"
@@ -26,6 +26,7 @@ namespace kata {
 namespace {
 
 constexpr int kThreads = 512;             // of the gradients' kernel
+constexpr int kGradBlocks = 256;          // its workgroups, one a CU
 
 // ---- the walk in reversed time ------------------------------------------------------------------
 template <typename T, int DK, int W>
@@ -34,7 +35,7 @@ struct ReverseTiles {
   static constexpr int DV = 16 * W;
   static constexpr int LK = DK + 16 / (int)sizeof(T), LV = DV + (kBf ? 16 : 4), LP = kC + 16 / (int)sizeof(T);
   static constexpr int kHead = 16 + kDeltaVec * 4;
-  static constexpr int NT = kBf ? 3 : 1, NI = kBf ? 2 : 1, NP = NI;     // terms of the recurrence's operands, of the inverse, of P
+  static constexpr int NT = kBf ? 3 : 1, NI = kBf ? 2 : 1, NP = NT;     // terms of the recurrence's operands, of the inverse, of P
   static constexpr int kTiles = kC * (2 * LK + LV);
   static constexpr int bytes = kHead + (kTiles + (NI + NP) * kC * LP) * (int)sizeof(T);
 };
@@ -81,9 +82,9 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
   // (Stage steps to the next chunk by 64 rows; here the next one is the one before)
   const T* pk = reinterpret_cast<const T*>(A.k) + s.b * A.sk[0] + row0 * A.sk[1] + hk * A.sk[2];
   const T* pq = reinterpret_cast<const T*>(A.q) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2];
-  const T* px = reinterpret_cast<const T*>(A.dO) + s.b * A.sdo[0] + row0 * A.sdo[1] + h * A.sdo[2] + c0;
+  const T* po = reinterpret_cast<const T*>(A.dO) + s.b * A.sdo[0] + row0 * A.sdo[1] + h * A.sdo[2] + c0;
   Stage<T, DK, kThr> rk(pk, A.sk[1], m.dk, true), rq(pq, A.sq[1], m.dk, true);
-  Stage<T, DV, kThr> ro(px, A.sdo[1], m.dv - c0, false);
+  Stage<T, DV, kThr> ro(po, A.sdo[1], m.dv - c0, false);
   StageInv<T, NI, LP, kThr> ri;
   uint4 vec_next;
   const long long chunk0 = (long long)s.c_slot * m.H + h;              // [c_slots][H]
@@ -112,6 +113,8 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
     for (int i = tid; i < TL::kTiles * (int)sizeof(T) / 16; i += kThr) z[i] = uint4{0u, 0u, 0u, 0u};
   }
   ri.zeros(sT);
+  const int ct = (m.dv + 15) / 16;
+  const bool live_tile = c0 / 16 + w < ct;          // uniform
 #pragma unroll 1
   for (int c = behind - 1; c >= first; --c) {
     __syncthreads();                                // the last chunk's tiles have been read
@@ -120,8 +123,8 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
     ro.template put<LV>(sO);
     ri.put(sT);
     if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
-    if (!kSums && c0 / 16 + w < (m.dv + 15) / 16) {
-      float* dst = A.rstates + ((chunk0 + (long long)c * m.H) * ((m.dv + 15) / 16) + c0 / 16 + w) * (DK * 16) + lane * 4;
+    if (!kSums && live_tile) {
+      float* dst = A.rstates + ((chunk0 + (long long)c * m.H) * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
 #pragma unroll
       for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(dst + i * 256) = D[i];
     }
@@ -200,12 +203,14 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
       X[0] = mul(inv[1], zf[1], X[0]);
       X[1] = mul(inv[3], zf[1], X[1]);
     }
-    Op<T, NT> kw[2];
-    Op<T, NI> qw[2];
+    Op<T, NT> kw[2], qw[2];
+    float* const px = A.x + ((chunk0 + (long long)c * m.H) * ct + c0 / 16 + w) * 1024 + lane * 4;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
-      X[it] *= -yv * *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);
+      X[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
+      if (!kSums && live_tile) *reinterpret_cast<f32x4*>(px + it * 256) = X[it];
+      X[it] *= -yv;
       Z[it] = half_of(of[it >> 1], it & 1) * yv * A.scale;
     }
 #pragma unroll
@@ -254,52 +259,93 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 4 && DK == 128 ? 1 : 8 / W) vo
 
 // ---- the gradients ------------------------------------------------------------------------------
 // One workgroup of eight waves for a chunk and a head of q and k, over the value heads that share it and
-// blocks of 64 value columns.  As in the walks a wave has 16 columns, four of them S, U and the outputs, the
-// others D, Z, X and dv; then these go through LDS, [column][token] and [column][row of the state], and a wave
-// has 16 tokens of dq and dk, half of the columns each.
+// blocks of 64 value columns.  U, dv and the states, which the walks have left in tiles of 16 columns, go through
+// LDS, [column][token] and [column][row of the state]; a wave has 16 tokens, four of the waves P's gradient and
+// half of the columns of dq and dk, the others that of the system's matrix and the other half.
 template <typename T, int DK>
 struct GradTiles {
   static constexpr bool kBf = sizeof(T) == 2;
   static constexpr int PAD = 16 / (int)sizeof(T);
-  static constexpr int LK = DK + PAD, LO = 64 + PAD, LV = 64 + (kBf ? 16 : 4), LP = kC + PAD, LS = DK + PAD;
-  static constexpr int kHead = 16 + kDeltaVec * 4 + 9 * kC * 4 + 16;   // an int, vec, dots and sums of the waves
-  static constexpr int NT = kBf ? 3 : 1, NI = kBf ? 2 : 1, NP = NI;     // terms of the recurrence's operands, of the inverse, of P
-  static constexpr int kStateTile = 64 * LS, kPair = 2 * 64 * LP;
-  // scores, then (bf16) the second terms of U and dv, or (fp32) a state, then PO and PV
-  static constexpr int kA = kBf || kPair > kStateTile ? kPair : kStateTile;
-  // bf16: both states, and the inverse's terms
-  static constexpr int bytes = kHead + (kC * (2 * LK + LO) + kA + kPair + (kBf ? 2 * kStateTile + NI * kC * LP : 0)) * (int)sizeof(T);
-  static_assert(64 * LV <= (kBf ? kPair : kPair / 2), "V lies where U (bf16: and dv) come, the inverse (fp32) where dv comes");
+  static constexpr int LK = DK + PAD, LP = kC + PAD, LS = DK + PAD;
+  static constexpr int kHead = 16 + kDeltaVec * 4 + 3 * kC * 4 + 16;   // an int, vec, dots and sums of the waves
+  // Terms of U, dv, S and PO, and how many of them enter dk, as of D and PV.  The dots dO . o and dv . v cancel in
+  // dlog: with two terms it was off by 2e-6 to 1e-5 of its norm, with three by N3ERR.
+  static constexpr int N = kBf ? 3 : 1, N2 = kBf ? 2 : 1;
+  static constexpr int kPlane = 64 * LP, kState = 64 * LS;
+  // The next chunk's operands are loaded ahead, and D has a place of its own, where registers and LDS are there.
+  static constexpr bool kAhead = DK <= 64;
+  // K and Q; U and dv, then PO and PV; S (and D)
+  static constexpr int bytes = kHead + (2 * kC * LK + 2 * N * kPlane + (N + (kAhead ? N2 : 0)) * kState) * (int)sizeof(T);
 };
-
-__device__ __forceinline__ float sum16(float x) {   // over the 16 lanes of a group
+template <int K, typename T, int N>
+__device__ __forceinline__ Op<T, K> leading(const Op<T, N>& x) {
+  Op<T, K> y;
 #pragma unroll
-  for (int s = 1; s < 16; s <<= 1) x += __shfl_xor(x, s);
+  for (int i = 0; i < K; ++i) y.t[i] = x.t[i];
+  return y;
+}
+
+// A row's operand over 32 value columns from memory, zeros from column `width` on, and the same order of columns of 32
+// rows of LD elements: bf16 straight (one load of 16 bytes), fp32 split (two).
+__device__ __forceinline__ bf16x8 value_row(const __bf16* p, int width, int g) {
+  return 8 * g < width ? row_frag(p + 8 * g) : bf16x8{};
+}
+__device__ __forceinline__ f32x8 value_row(const float* p, int width, int g) {
+  const f32x4 a = 4 * g < width ? load4(p + 4 * g) : zero4(), b = 16 + 4 * g < width ? load4(p + 16 + 4 * g) : zero4();
+  return pack_frag(a, b, float());
+}
+__device__ __forceinline__ void store_row(__bf16* p, int width, int g, const bf16x8& x) {
+  if (8 * g < width) *reinterpret_cast<uint4*>(p + 8 * g) = __builtin_bit_cast(uint4, x);
+}
+__device__ __forceinline__ void store_row(float* p, int width, int g, const f32x8& x) {
+  if (4 * g < width) store4(p + 4 * g, half_of(x, 0));
+  if (16 + 4 * g < width) store4(p + 16 + 4 * g, half_of(x, 1));
+}
+template <int LD>
+__device__ __forceinline__ bf16x8 value_column(const __bf16* p, int lane) {
+  const __bf16* at = p + (8 * (lane >> 4) + ((lane & 15) >> 2)) * LD + 4 * (lane & 3);
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * LD));
+  const uint2 ul = __builtin_bit_cast(uint2, lo), uh = __builtin_bit_cast(uint2, hi);
+  return __builtin_bit_cast(bf16x8, uint4{ul.x, ul.y, uh.x, uh.y});
+}
+template <int LD>
+__device__ __forceinline__ f32x8 value_column(const float* p, int lane) {
+  return column_frag<LD>(p, lane);
+}
+template <int N, int LD, typename T>
+__device__ __forceinline__ Op<T, N> value_op(const T* p, int plane, int lane) {
+  Op<T, N> x;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x.t[i] = value_column<LD>(p + i * plane, lane);
   return x;
+}
+// the sum of the products of two operands' elements
+template <typename F>
+__device__ __forceinline__ float dot(const F& a, const F& b) {
+  const f32x4 x = half_of(a, 0) * half_of(b, 0) + half_of(a, 1) * half_of(b, 1);
+  return x[0] + x[1] + x[2] + x[3];
 }
 
 template <typename T, int DK>
-__global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
+__global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   using TL = GradTiles<T, DK>;
   using frag = typename Elem<T>::frag;
-  constexpr int M = DK / 32, NS = DK / 16, NH = NS / 2, LK = TL::LK, LO = TL::LO, LV = TL::LV, LP = TL::LP, LS = TL::LS;
-  constexpr int NT = TL::NT, NI = TL::NI, NP = TL::NP;
-  constexpr bool kBf = TL::kBf;
+  constexpr int NS = DK / 16, NH = NS / 2, LK = TL::LK, LP = TL::LP, LS = TL::LS, N = TL::N, N2 = TL::N2;
+  constexpr int PL = TL::kPlane, PS = TL::kState;
+  constexpr bool kAhead = TL::kAhead;
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
   const float* const sc = vec + 3 * kC;
-  float* const sE = vec + kDeltaVec;                // [8][64] dO . o, -dv . v; then [64] dv . U
-  float* const sF = sE + 9 * kC;                    // [4] <D, S'>
+  float* const sE = vec + kDeltaVec;                // [2][64] q . dq - dv . v in parts; then [64] dv . U
+  float* const sF = sE + 3 * kC;                    // [4] <D, S'>
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
   T* const sQ = sK + kC * LK;
-  T* const sO = sQ + kC * LK;
-  T* const sA = sO + kC * LO;
-  T* const sU = sA + TL::kA;                        // V, then U and dv
-  T* const sZ = sU + 64 * LP;
-  T* const sS = kBf ? sZ + 64 * LP : sA;
-  T* const sD = kBf ? sS + TL::kStateTile : sA;
-  T* const sT = kBf ? sD + TL::kStateTile : sZ;
+  T* const sU = sQ + kC * LK;                       // N planes each of U and dv, then of PO and (N2) PV
+  T* const sZ = sU + N * PL;
+  T* const sS = sZ + N * PL;                        // N planes of S, N2 of D
+  T* const sD = kAhead ? sS + N * PS : sS;
 
   const DeltaMap& m = A.m;
   const int tid = threadIdx.x;
@@ -313,21 +359,22 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
   };
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   const bool first_half = wave < 4;
-  const unsigned unit = block_number();
-  if (unit >= (unsigned)m.c_slots * (unsigned)m.Hk) return;
-  const int slot = int(unit / (unsigned)m.Hk), hk = int(unit - (unsigned)slot * (unsigned)m.Hk);
-  const int share = m.H / m.Hk;
-  DeltaPart s;
-  if (!find_part(m, slot, 1, m.n_chunks, m.c_slots, sh, s)) return;
+  const int share = m.H / m.Hk, ct = (m.dv + 15) / 16, v_blocks = (m.dv + 63) / 64;
+  const unsigned units = (unsigned)m.c_slots * (unsigned)m.Hk;
 
-  T* const gq = reinterpret_cast<T*>(A.dq) + ((long long)s.b * m.T * m.Hk + hk) * m.dk;   // row stride Hk dk
-  T* const gk = reinterpret_cast<T*>(A.dk) + ((long long)s.b * m.T * m.Hk + hk) * m.dk;
-  const long long lead = (long long)s.b * m.T * m.H + hk * share;      // of [b][t][H], the first shared head
-  auto clear = [&](int from, int rows) {
+  // where the workgroup is: a chunk and head of q and k, its `hh`th value head, its `vb`th block of columns
+  struct Place {
+    unsigned unit;
+    int slot, hk, hh, vb, n;
+    DeltaPart s;
+    long long row0;
+  };
+  auto clear = [&](const Place& p, int from, int rows) {
+    const long long at_k = (long long)p.s.b * m.T * m.Hk + p.hk, lead = (long long)p.s.b * m.T * m.H + p.hk * share;
     for (long long i = tid; i < (long long)rows * (m.dk / 4); i += kThreads) {
-      const long long at = (from + i / (m.dk / 4)) * m.Hk * m.dk + i % (m.dk / 4) * 4;
-      store4(gq + at, zero4());
-      store4(gk + at, zero4());
+      const long long at = (at_k + (from + i / (m.dk / 4)) * m.Hk) * m.dk + i % (m.dk / 4) * 4;
+      store4(reinterpret_cast<T*>(A.dq) + at, zero4());
+      store4(reinterpret_cast<T*>(A.dk) + at, zero4());
     }
     const int per = share * m.dv / 4;
     for (long long i = tid; i < (long long)rows * per; i += kThreads)
@@ -338,280 +385,220 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
       if (A.dlog) A.dlog[at] = 0.f;
     }
   };
-  const int n = min(kC, s.len - kC * s.part);
-  if (s.seq == m.n_seq) {                           // rows behind the last sequence
-    if (n > 0) clear(s.start + kC * s.part, n);
-    return;
-  }
-  if (m.packed && s.seq == 0 && s.part == 0) clear(0, s.start);        // before the first
-  if (n <= 0) return;
-  const bool last = kC * (s.part + 1) >= s.len;
-  const long long row0 = s.start + (long long)kC * s.part;
-  const int ct = (m.dv + 15) / 16, v_blocks = (m.dv + 63) / 64;
+  // The first unit from p.unit on that has tokens; those before it are zeros' rows, or nothing.
+  auto find = [&](Place& p) {
+    for (; p.unit < units; p.unit += gridDim.x) {
+      p.slot = int(p.unit / (unsigned)m.Hk);
+      p.hk = int(p.unit - (unsigned)p.slot * (unsigned)m.Hk);
+      p.hh = p.vb = 0;
+      if (m.packed) __syncthreads();                // the last answer has been read
+      if (!find_part(m, p.slot, 1, m.n_chunks, m.c_slots, sh, p.s)) continue;
+      p.n = min(kC, p.s.len - kC * p.s.part);
+      p.row0 = p.s.start + (long long)kC * p.s.part;
+      if (p.s.seq == m.n_seq) {                     // rows behind the last sequence
+        if (p.n > 0) clear(p, (int)p.row0, p.n);
+        continue;
+      }
+      if (m.packed && p.s.seq == 0 && p.s.part == 0) clear(p, 0, p.s.start);   // before the first
+      if (p.n > 0) return true;
+    }
+    return false;
+  };
 
-  // tiles' columns that no operand has: zeros all along (V's place is written over: cleared each time)
-  if (m.dk < DK || m.dv % 64)
-    for (int i = tid; i < kC * (2 * LK + LO) * (int)sizeof(T) / 16; i += kThreads)
+  // What is loaded for a place: a wave's 16 columns of U and S, or of dv, D and S' (the state behind the chunk); its 16
+  // tokens' dO and (half of the columns) v; all together the chunk's rows and vectors.
+  Stage<T, DK, kThreads> rk(nullptr, 0, m.dk, true), rq(nullptr, 0, m.dk, true);
+  f32x4 x[4], S[NS], Sn[kAhead ? NS : 1];
+  frag od[2], vd;
+  uint4 vec_next;
+  float frob_next = 0.f;
+  auto load = [&](const Place& p) {
+    const int h = p.hk * share + p.hh, c0 = 64 * p.vb, row = 16 * w + l16;
+    const long long cs = (long long)p.slot * m.H + h, tile = cs * ct + 4 * p.vb + w;
+    const bool last = kC * (p.s.part + 1) >= p.s.len, live_tile = 4 * p.vb + w < ct;   // uniform
+    if (p.hh == 0 && p.vb == 0) {
+      rk = Stage<T, DK, kThreads>(reinterpret_cast<const T*>(A.k) + p.s.b * A.sk[0] + p.row0 * A.sk[1] + p.hk * A.sk[2], A.sk[1],
+                                  m.dk, true);
+      rq = Stage<T, DK, kThreads>(reinterpret_cast<const T*>(A.q) + p.s.b * A.sq[0] + p.row0 * A.sq[1] + p.hk * A.sq[2], A.sq[1],
+                                  m.dk, true);
+      fetch_rows(rk, A.sk[1], p.n);
+      fetch_rows(rq, A.sq[1], p.n);
+    }
+    if (p.vb == 0 && tid < kDeltaVec / 4) vec_next = reinterpret_cast<const uint4*>(A.vec + cs * kDeltaVec)[tid];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = zero4();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) S[i] = zero4();
+    if (live_tile) {
+      const float* const fx = (first_half ? A.u : A.x) + tile * 1024 + lane * 4;
+      const float* const fs = (first_half ? A.cstates : A.rstates) + tile * (DK * 16) + lane * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = load4(fx + i * 256);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) S[i] = load4(fs + i * 256);
+    }
+    od[0] = od[1] = vd = frag{};
+    if (row < p.n) {
+      const T* const po = reinterpret_cast<const T*>(A.dO) + p.s.b * A.sdo[0] + (p.row0 + row) * A.sdo[1] + h * A.sdo[2] + c0;
+      const T* const pv = reinterpret_cast<const T*>(A.v) + p.s.b * A.sv[0] + (p.row0 + row) * A.sv[1] + h * A.sv[2] + c0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) od[i] = value_row(po + 32 * i, m.dv - c0 - 32 * i, g);
+      const int half = first_half ? 0 : 32;
+      vd = value_row(pv + half, m.dv - c0 - half, g);
+    }
+    // (behind the last chunk without a gradient D is zero)
+    const bool sum = live_tile && !first_half && !(last && !A.fstates);
+    const float* const next = last ? A.fstates + (((long long)p.s.seq * m.H + h) * ct + 4 * p.vb + w) * (DK * 16) + lane * 4
+                                   : A.cstates + (tile + (long long)m.H * ct) * (DK * 16) + lane * 4;
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) Sn[i] = sum ? load4(next + i * 256) : zero4();
+    } else {
+      frob_next = 0.f;
+      if (sum)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const f32x4 y = S[i] * load4(next + i * 256);
+          frob_next += y[0] + y[1] + y[2] + y[3];
+        }
+    }
+  };
+
+  Place now;
+  now.unit = blockIdx.x;
+  bool more = find(now);
+  if (!more) return;
+  if (m.dk < DK)                                    // columns that no operand has: zeros all along
+    for (int i = tid; i < 2 * kC * LK * (int)sizeof(T) / 16; i += kThreads)
       reinterpret_cast<uint4*>(sK)[i] = uint4{0u, 0u, 0u, 0u};
-  {
-    Stage<T, DK, kThreads> rk(reinterpret_cast<const T*>(A.k) + s.b * A.sk[0] + row0 * A.sk[1] + hk * A.sk[2], A.sk[1], m.dk, true);
-    Stage<T, DK, kThreads> rq(reinterpret_cast<const T*>(A.q) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2], A.sq[1], m.dk, true);
-    fetch_rows(rk, A.sk[1], n);
-    fetch_rows(rq, A.sq[1], n);
-    if (m.dk < DK || m.dv % 64) __syncthreads();
-    rk.template put_split<LK>(sK);
-    rq.template put_split<LK>(sQ);
-  }
+  if constexpr (kAhead) load(now);
 
   f32x4 dqa[NH], dka[NH];                           // [row 16 (i0 + i) + 4 g + r][token 16 w + l16]
+  f32x4 Wt[4], dqh[NH];                             // the strip of dO U^T (second half: dv U^T), transposed; the head's dq
+  float frob = 0.f, e = 0.f;
   const int i0 = first_half ? 0 : NH;
-#pragma unroll
-  for (int i = 0; i < NH; ++i) dqa[i] = dka[i] = zero4();
-
 #pragma unroll 1
-  for (int hh = 0; hh < share; ++hh) {
-    const int h = hk * share + hh;
-    const long long cs = (long long)slot * m.H + h;                    // [c_slots][H]
-    f32x4 Wt[4], e[4];                              // the strip of dO U^T (second half: dv U^T), transposed
-    float frob = 0.f;
+  while (more) {
+    if constexpr (!kAhead) load(now);
+    const int h = now.hk * share + now.hh, c0 = 64 * now.vb, row = 16 * w + l16;
+    const long long lead = ((long long)now.s.b * m.T + now.row0) * m.H + h;    // of [b][t][H]
+    const bool live_row = row < now.n;
+    if (now.vb == 0) {
+      frob = e = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) Wt[i] = e[i] = zero4();
-#pragma unroll 1
-    for (int vb = 0; vb < v_blocks; ++vb) {
-      const int c0 = 64 * vb;
-      forget();
-      Stage<T, 64, kThreads> ro(reinterpret_cast<const T*>(A.dO) + s.b * A.sdo[0] + row0 * A.sdo[1] + h * A.sdo[2] + c0,
-                                A.sdo[1], m.dv - c0, true);
-      Stage<T, 64, kThreads> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + c0,
-                                A.sv[1], m.dv - c0, false);
-      fetch_rows(ro, A.sdo[1], n);
-      fetch_rows(rv, A.sv[1], n);
-      StageInv<T, NI, LP, kThreads> ri;
-      ri.fetch(A.inv + cs * kInvFloats);
-      f32x4 S[NS];                                  // (second half: D)
-      const bool live_tile = 4 * vb + w < ct;       // uniform
+      for (int i = 0; i < 4; ++i) Wt[i] = zero4();
 #pragma unroll
-      for (int i = 0; i < NS; ++i) S[i] = zero4();
-      if (live_tile) {
-        const long long tile = (cs * ct + 4 * vb + w) * (DK * 16) + lane * 4;
-        const float* const from = (first_half ? A.cstates : A.rstates) + tile;
+      for (int i = 0; i < NH; ++i) dqh[i] = zero4();
+      if (now.hh == 0)
 #pragma unroll
-        for (int i = 0; i < NS; ++i) S[i] = *reinterpret_cast<const f32x4*>(from + i * 256);
-        if (!first_half && !(last && !A.fstates)) {  // (behind the last chunk without a gradient D is zero)
-          const float* const next = last ? A.fstates + (((long long)s.seq * m.H + h) * ct + 4 * vb + w) * (DK * 16) + lane * 4
-                                         : A.cstates + tile + (long long)m.H * ct * (DK * 16);
+        for (int i = 0; i < NH; ++i) dqa[i] = dka[i] = zero4();
+    }
+    forget();
+    __syncthreads();                                // the last block's tiles have been read
+    if (now.vb == 0 && tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
+    if (now.hh == 0 && now.vb == 0) {
+      rk.template put_split<LK>(sK);
+      rq.template put_split<LK>(sQ);
+    }
+    {
+      T* const at = (first_half ? sU : sZ) + row * LP + 4 * g;
 #pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(next + i * 256);
+      for (int i = 0; i < 4; ++i) put_terms<N>(at + 16 * i, PL, x[i]);
+    }
+    auto put_d = [&] {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) frob = fmaf(S[i][r], x[r], frob);
-          }
-        }
+      for (int i = 0; i < NS; ++i) put_terms<N2>(sD + (16 * w + l16) * LS + 16 * i + 4 * g, PS, S[i]);
+    };
+    if (first_half) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) put_terms<N>(sS + (16 * w + l16) * LS + 16 * i + 4 * g, PS, S[i]);
+    } else if constexpr (kAhead) {
+      put_d();
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const f32x4 y = S[i] * Sn[i];
+        frob += y[0] + y[1] + y[2] + y[3];
       }
-      __syncthreads();                              // the last block's and head's tiles have been read
-      if (vb == 0 && tid < kDeltaVec / 4)
-        reinterpret_cast<uint4*>(vec)[tid] = reinterpret_cast<const uint4*>(A.vec + cs * kDeltaVec)[tid];
-      if (m.dv - c0 < 64) {
-        for (int i = tid; i < 64 * LV * (int)sizeof(T) / 16; i += kThreads)
-          reinterpret_cast<uint4*>(sU)[i] = uint4{0u, 0u, 0u, 0u};
-        if (vb > 0)
-          for (int i = tid; i < kC * LO * (int)sizeof(T) / 16; i += kThreads)
-            reinterpret_cast<uint4*>(sO)[i] = uint4{0u, 0u, 0u, 0u};
-        __syncthreads();
+    }
+    frob += frob_next;
+    const frag oc[2] = {od[0], od[1]}, vc = vd;
+    Place next = now;
+    if (++next.vb == v_blocks) {
+      next.vb = 0;
+      if (++next.hh == share) {
+        next.unit += gridDim.x;
+        more = find(next);
       }
-      ro.template put_split<LO>(sO);
-      rv.template put<LV>(sU);
-      ri.put(sT);
-      ri.zeros(sT);
-      __syncthreads();
+    }
+    if constexpr (kAhead)
+      if (more) load(next);
+    __syncthreads();
 
-      // a wave's 16 columns: x becomes U (X), y the outputs (Z)
-      put_scores<T, DK, LK, LP, 2, NP>(sA, sQ, sK, sc, w, first_half ? 0 : 2, lane, A.scale);
-      forget();
-      const int wc = 16 * w;
-      f32x4 x[4], y[4];
-      frag of[2], vf[2];
+    // a wave's 16 tokens
+    forget();
+    Op<T, N> z[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        vf[i] = column_frag<LV>(sU + 32 * i * LV + wc, lane);
-        of[i] = split_column_frag<LO>(sO + 32 * i * LO, w, lane);
-      }
-      {
-        Op<T, NT> sf[M];
+    for (int i = 0; i < 2; ++i) z[i] = value_op<N, LP>(sZ + 32 * i * LP + 16 * w, PL, lane);
+    if (live_row) {                                 // dv, half of the columns each
+      T* const dst = reinterpret_cast<T*>(A.dv) + (lead + (long long)row * m.H) * m.dv + c0;
+      if (first_half) store_row(dst, m.dv - c0, g, z[0].t[0]);
+      else store_row(dst + 32, m.dv - c0 - 32, g, z[1].t[0]);
+    }
 #pragma unroll
-        for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
+    for (int t = 0; t < N; ++t) e -= first_half ? dot(z[0].t[t], vc) : dot(z[1].t[t], vc);
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          x[it] = y[it] = zero4();
-#pragma unroll
-          for (int i = 0; i < M; ++i) x[it] = mul(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], x[it]);
-        }
-        if (first_half)
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-#pragma unroll
-            for (int i = 0; i < M; ++i) y[it] = mul(row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], y[it]);
-            const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
-            y[it] *= yv * A.scale;
-            x[it] = *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g) * (half_of(vf[it >> 1], it & 1) - yv * x[it]);
-          }
-        else
-#pragma unroll
-          for (int it = 0; it < 4; ++it) y[it] = x[it] * *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
-      }
-      reads_above<T>();
-      Op<T, NT> f[2];
-      if (first_half) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) split_terms(x[2 * i], x[2 * i + 1], f[i]);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          x[it] = zero4();
-#pragma unroll
-          for (int i = 0; i <= it >> 1; ++i)
-            x[it] = mul(row_op<NI>(sT + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), f[i], x[it]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) split_terms(x[2 * i], x[2 * i + 1], f[i]);
-      }
-      __syncthreads();                              // P is there
-      forget();
-      if (first_half) {
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-#pragma unroll
-          for (int i = 0; i <= it >> 1; ++i)
-            y[it] = mul(row_op<NP>(sA + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), f[i], y[it]);
-          e[it] += y[it] * half_of(of[it >> 1], it & 1);
-        }
-      } else {
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-          for (int i = it >> 1; i < 2; ++i)
-            y[it] = mul(split_column_op<NP, LP>(sA + 32 * i * LP, kC * LP, it, lane), of[i], y[it]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) split_terms(y[2 * i], y[2 * i + 1], f[i]);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          x[it] = zero4();
-#pragma unroll
-          for (int i = it >> 1; i < 2; ++i)
-            x[it] = mul(split_column_op<NI, LP>(sT + 32 * i * LP, kC * LP, it, lane), f[i], x[it]);
-          x[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
-          e[it] -= x[it] * half_of(vf[it >> 1], it & 1);
-        }
-      }
-      __syncthreads();                              // P, V and the inverse have been read
-      // U, dv and the states through LDS
-      forget();
-      {
-        T* const mine = (first_half ? sU : sZ) + (wc + l16) * LP + 4 * g;
-        T* const rest = sA + ((first_half ? 0 : 64) + wc + l16) * LP + 4 * g;
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const Quad<T> u = quad(x[it], T());
-          *reinterpret_cast<Quad<T>*>(mine + 16 * it) = u;
-          if constexpr (kBf) store4(rest + 16 * it, x[it] - unquad(u));
-        }
-        if (kBf || first_half)
-#pragma unroll
-          for (int i = 0; i < NS; ++i) store4((first_half ? sS : sD) + (wc + l16) * LS + 16 * i + 4 * g, S[i]);
-      }
-      __syncthreads();
-
-      // a wave's 16 tokens
-      forget();
-      frag ur[2], zr[2], ot[2];
-      {
-        constexpr int NW = kBf ? 2 : 1;             // terms of U and dv
-        Op<T, NW> zt[2];
+    for (int j = 0; j < 4; ++j)
+      if (j <= w)                                   // uniform
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          zt[i].t[0] = zr[i] = column_frag<LP>(sZ + 32 * i * LP + 16 * w, lane);
-          if constexpr (kBf) zt[i].t[1] = column_frag<LP>(sA + (64 + 32 * i) * LP + 16 * w, lane);
-          ot[i] = row_frag(sO + (16 * w + l16) * LO + 32 * i + 8 * g);
-          ur[i] = column_frag<LP>(sU + 32 * i * LP + 16 * w, lane);
+          const T* const at = sU + 32 * i * LP + 16 * j;
+          if (first_half) Wt[j] = mul(value_op<N, LP>(at, PL, lane), oc[i], Wt[j]);
+          else Wt[j] = mul(value_op<N2, LP>(at, PL, lane), leading<N2>(z[i]), Wt[j]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j <= w)                               // uniform
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              Op<T, NW> ut;
-              ut.t[0] = column_frag<LP>(sU + 32 * i * LP + 16 * j, lane);
-              if constexpr (kBf) ut.t[1] = column_frag<LP>(sA + 32 * i * LP + 16 * j, lane);
-              if (first_half) Wt[j] = mul(ut, ot[i], Wt[j]);
-              else Wt[j] = mul(ut, zt[i], Wt[j]);
-            }
-        forget();
-        const float yr = vec[16 * w + l16], yo = yr * A.scale;
-#pragma unroll
-        for (int i = 0; i < NH; ++i) {
-          f32x4 a = zero4(), b = zero4();
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const frag st = column_frag<LS>(sS + 32 * j * LS + 16 * (i0 + i), lane);
-            a = mma(st, ot[j], a);
-            b = mma(st, zr[j], b);
-          }
-          dqa[i] += a * yo;
-          dka[i] -= b * yr;
-        }
-        // dv: tokens 16 w + l16, columns 32 i + 16 half + 4 g, half of them each
-        if (16 * w + l16 < n) {
-          T* const dst = reinterpret_cast<T*>(A.dv) + ((lead + hh) + (row0 + 16 * w + l16) * m.H) * m.dv + c0 + 4 * g;
-          const int i = first_half ? 0 : 1;
-          const frag z = first_half ? zr[0] : zr[1];
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            if (c0 + 32 * i + 16 * half + 4 * g < m.dv) store4(dst + 32 * i + 16 * half, half_of(z, half));
-        }
-      }
-      if constexpr (!kBf) {
-        __syncthreads();                            // S has been read
-        if (!first_half)
-#pragma unroll
-          for (int i = 0; i < NS; ++i) store4(sD + (wc + l16) * LS + 16 * i + 4 * g, S[i]);
-        __syncthreads();
-      }
-      forget();
-      const float left = vec[kC + 16 * w + l16];
+    forget();
+    {
+      const float yr = vec[16 * w + l16], yo = yr * A.scale;
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
-        f32x4 a = zero4();
+        f32x4 a = zero4(), b = zero4();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) a = mma(column_frag<LS>(sD + 32 * j * LS + 16 * (i0 + i), lane), ur[j], a);
-        dka[i] += a * left;
+        for (int j = 0; j < 2; ++j) {
+          const Op<T, N> st = value_op<N, LS>(sS + 32 * j * LS + 16 * (i0 + i), PS, lane);
+          a = mul(st, oc[j], a);
+          b = mul(leading<N2>(st), leading<N2>(z[j]), b);
+        }
+        dqh[i] += a * yo;
+        dka[i] -= b * yr;
       }
     }
-    // dots: over a wave's 16 columns, then over the waves
+    Op<T, N2> u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) u[i] = value_op<N2, LP>(sU + 32 * i * LP + 16 * w, PL, lane);
+    if constexpr (!kAhead) {
+      __syncthreads();                              // S has been read
+      if (!first_half) put_d();
+      __syncthreads();
+    }
     forget();
+    const float left = vec[kC + 16 * w + l16];
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int i = 0; i < NH; ++i) {
+      f32x4 a = zero4();
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float a = sum16(e[it][r]);
-        if (l16 == 0) sE[wave * kC + 16 * it + 4 * g + r] = a;
-      }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
-    if (lane == 0 && !first_half) sF[w] = frob;
-    if (!first_half) {                              // the diagonal of dv U^T
-      float d = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (j == w && 4 * g + r == l16) d = Wt[j][r];
-      if (l16 >> 2 == g) sE[8 * kC + 16 * w + l16] = d;
+      for (int j = 0; j < 2; ++j) a = mul(value_op<N2, LS>(sD + 32 * j * LS + 16 * (i0 + i), PS, lane), u[j], a);
+      dka[i] += a * left;
     }
-    __syncthreads();                                // (the second terms and D have been read, too)
+    if (now.vb + 1 < v_blocks) {
+      now = next;
+      continue;
+    }
+    if constexpr (kAhead) __syncthreads();          // U and dv have been read
     // PO or PV, the wave's strip of rows
+    forget();
     {
       const float hi = sc[16 * w + l16], lo = sc[kC + 16 * w + l16], factor = first_half ? A.scale : -1.f;
-      const int row = 16 * w + l16 + (first_half ? 1 : 0);             // the first key that it does not reach
-      T* const at = sA + ((first_half ? 0 : kC) + 16 * w + l16) * LP;
+      const int end = 16 * w + l16 + (first_half ? 1 : 0);             // the first key that it does not reach
+      T* const at = (first_half ? sU : sZ) + (16 * w + l16) * LP;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f32x4 p = zero4();
@@ -619,29 +606,23 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int key = 16 * j + 4 * g + r;
-            p[r] = key >= row ? 0.f : Wt[j][r] * (exp2_diff(hi, lo, sc[key], sc[kC + key]) * factor);
+            p[r] = key >= end ? 0.f : Wt[j][r] * (exp2_diff(hi, lo, sc[key], sc[kC + key]) * factor);
           }
-        store4(at + split_place(16 * j + 4 * g), p);
+        if (first_half) put_terms<N>(at + split_place(16 * j + 4 * g), PL, p);
+        else put_terms<N2>(at + split_place(16 * j + 4 * g), PL, p);
       }
     }
-    if (wave == 0) {
-      const long long at = lead + hh + (row0 + lane) * m.H;
-      const float b = vec[2 * kC + lane];
-      if (lane < n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[8 * kC + lane] / (b * b));
-      if (A.dlog) {
-        double x = 0.0;
+    if (!first_half) {                              // the diagonal of dv U^T
+      float d = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x += (double)sE[i * kC + lane];
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const double up = __shfl_down(x, d);
-          if (lane + d < 64) x += up;
-        }
-        x += (double)sF[0] + sF[1] + sF[2] + sF[3];
-        // a decay of nothing, and one of zero (in fp32), have no gradient
-        const bool none = (s.part == 0 && lane == 0 && !A.init) || sc[lane] - (lane ? sc[lane - 1] : 0.f) < -150.f;
-        if (lane < n) A.dlog[at] = none ? 0.f : (float)x;
-      }
+        for (int r = 0; r < 4; ++r)
+          if (j == w && 4 * g + r == l16) d = Wt[j][r];
+      if (l16 >> 2 == g) sE[2 * kC + 16 * w + l16] = d;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
+      if (lane == 0) sF[w] = frob;
     }
     __syncthreads();
 #pragma unroll
@@ -650,23 +631,53 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs A) {
       for (int j = 0; j < 2; ++j) {
         const frag kt = split_column_frag<LK>(sK + 32 * j * LK, i0 + i, lane);
         if (j <= w >> 1) {                          // uniform
-          dqa[i] = mma(kt, row_frag(sA + (16 * w + l16) * LP + 32 * j + 8 * g), dqa[i]);
-          dka[i] = mma(kt, row_frag(sA + (kC + 16 * w + l16) * LP + 32 * j + 8 * g), dka[i]);
+          dqh[i] = mul(kt, row_op<N>(sU + (16 * w + l16) * LP + 32 * j + 8 * g, PL), dqh[i]);
+          dka[i] = mul(kt, row_op<N2>(sZ + (16 * w + l16) * LP + 32 * j + 8 * g, PL), dka[i]);
         }
         if (j >= w >> 1) {
-          dka[i] = mma(split_column_frag<LK>(sQ + 32 * j * LK, i0 + i, lane), split_column_frag<LP>(sA + 32 * j * LP, w, lane), dka[i]);
-          dka[i] = mma(kt, split_column_frag<LP>(sA + (kC + 32 * j) * LP, w, lane), dka[i]);
+          dka[i] = mul(split_column_frag<LK>(sQ + 32 * j * LK, i0 + i, lane),
+                       split_column_op<N2, LP>(sU + 32 * j * LP, PL, w, lane), dka[i]);
+          dka[i] = mul(kt, split_column_op<N2, LP>(sZ + 32 * j * LP, PL, w, lane), dka[i]);
         }
       }
-  }
-  if (16 * w + l16 < n) {
-    const long long at = (row0 + 16 * w + l16) * m.Hk * m.dk + 4 * g;
+    // dO . o = q . dq of this head
 #pragma unroll
-    for (int i = 0; i < NH; ++i)
-      if (16 * (i0 + i) + 4 * g < m.dk) {
-        store4(gq + at + 16 * (i0 + i), dqa[i]);
-        store4(gk + at + 16 * (i0 + i), dka[i]);
+    for (int i = 0; i < NH; ++i) {
+      const f32x4 y = unquad(*reinterpret_cast<const Quad<T>*>(sQ + (16 * w + l16) * LK + split_place(16 * (i0 + i) + 4 * g))) * dqh[i];
+      e += y[0] + y[1] + y[2] + y[3];
+      dqa[i] += dqh[i];
+    }
+    e += __shfl_xor(e, 16);
+    e += __shfl_xor(e, 32);
+    if (lane < 16) sE[(first_half ? 0 : kC) + 16 * w + lane] = e;
+    __syncthreads();
+    if (wave == 0) {
+      const long long at = lead + (long long)lane * m.H;
+      const float b = vec[2 * kC + lane];
+      if (lane < now.n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[2 * kC + lane] / (b * b));
+      if (A.dlog) {
+        double y = (double)sE[lane] + sE[kC + lane];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const double up = __shfl_down(y, d);
+          if (lane + d < 64) y += up;
+        }
+        y += (double)sF[0] + sF[1] + sF[2] + sF[3];
+        // a decay of nothing, and one of zero (in fp32), have no gradient
+        const bool none = (now.s.part == 0 && lane == 0 && !A.init) || sc[lane] - (lane ? sc[lane - 1] : 0.f) < -150.f;
+        if (lane < now.n) A.dlog[at] = none ? 0.f : (float)y;
       }
+    }
+    if (now.hh + 1 == share && live_row) {
+      const long long at = (((long long)now.s.b * m.T + now.row0 + row) * m.Hk + now.hk) * m.dk + 4 * g;
+#pragma unroll
+      for (int i = 0; i < NH; ++i)
+        if (16 * (i0 + i) + 4 * g < m.dk) {
+          store4(reinterpret_cast<T*>(A.dq) + at + 16 * (i0 + i), dqa[i]);
+          store4(reinterpret_cast<T*>(A.dk) + at + 16 * (i0 + i), dka[i]);
+        }
+    }
+    now = next;
   }
 }
 
@@ -699,7 +710,8 @@ hipError_t launch_grads_t(const DeltaArgs& a, hipStream_t st) {
   const auto kernel = delta_grads_kernel<T, DK>;
   hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), TL::bytes);
   if (e != hipSuccess) return e;
-  launch_kernel(kernel, grid_rows((long long)a.m.c_slots * a.m.Hk), kThreads, TL::bytes, st, a);
+  const long long units = (long long)a.m.c_slots * a.m.Hk;
+  launch_kernel(kernel, dim3(unsigned(units < kGradBlocks ? units : kGradBlocks)), kThreads, TL::bytes, st, a);
   return hipGetLastError();
 }
 

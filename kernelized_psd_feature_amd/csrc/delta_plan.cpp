@@ -99,9 +99,11 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
     if (p.n_seg > 1) p.rsums = part(s * state);
     // (the state walks' tile: 32 rows have no bf16 form of the gradients' kernel)
     const size_t DK = pr->dk <= 32 && !bf16 ? 32 : pr->dk <= 64 ? 64 : 128;
-    const size_t chunk_state = DK * 16 * ((pr->dv + 15) / 16) * 4;
+    const size_t tiles = (pr->dv + 15) / 16, chunk_state = DK * 16 * tiles * 4, chunk_u = 64 * 16 * tiles * 4;
     p.cstates = part(c * chunk_state);
     p.rstates = part(c * chunk_state);
+    p.u = part(c * chunk_u);
+    p.x = part(c * chunk_u);
     p.fstates = part(size_t(pr->n_seq) * H * chunk_state);
   }
   p.bytes = at;

@@ -8,6 +8,10 @@
 
 namespace kata {
 
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load4(const __bf16* p) { return unquad(*reinterpret_cast<const uint2*>(p)); }
+__device__ __forceinline__ f32x4 unquad(const f32x4& x) { return x; }
+
 // What a chunk and head keep in the workspace.  Vectors: exp(c), exp(c_63 - c), beta, and c log2(e) as the sum
 // of two floats, of every token, c being the sum of the log decays from the chunk's first token on.
 // Inverse: its 16 x 16 blocks on and below the diagonal, by rows of blocks.

@@ -147,8 +147,11 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   const bool live_col = c0 + wc + 4 * g < m.dv;
   T* po = kOut ? out + (row0 + l16) * A.so[1] + wc + 4 * g : nullptr;
   const int ct = (m.dv + 15) / 16;
-  float* p_state = nullptr;
-  if (kWhat == Walk::states && c0 / 16 + w < ct) p_state = A.cstates + (chunk0 * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
+  float *p_state = nullptr, *p_u = nullptr;
+  if (kWhat == Walk::states && c0 / 16 + w < ct) {
+    p_state = A.cstates + (chunk0 * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
+    p_u = A.u + (chunk0 * ct + c0 / 16 + w) * 1024 + lane * 4;
+  }
 
   Quad<T> O[4];                                     // outputs of the last chunk
   auto store = [&](int rows) {
@@ -287,6 +290,11 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       read_inv();
       correct();
       look(U);
+    }
+    if (kWhat == Walk::states && p_u) {             // uniform
+#pragma unroll
+      for (int it = 0; it < 4; ++it) *reinterpret_cast<f32x4*>(p_u + it * 256) = U[it];
+      p_u += (long long)m.H * ct * 1024;
     }
     {
       const float whole = vec[kC - 1];

@@ -142,6 +142,8 @@ int main(int argc, char** argv) {
       }
       if (backward) {
         parts.push_back({p.cstates, c * chunk});
+        parts.push_back({p.u, c * 4096 * ((pr.dv + 15) / 16)});
+        parts.push_back({p.x, c * 4096 * ((pr.dv + 15) / 16)});
         parts.push_back({p.rstates, c * chunk});
         parts.push_back({p.fstates, (wide)pr.n_seq * pr.H * chunk});
       }
