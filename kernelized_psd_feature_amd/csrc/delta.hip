@@ -408,7 +408,7 @@ hipError_t launch_walk_t(const DeltaArgs& a, hipStream_t st) {
   using TL = WalkTiles<T, DK, W, NT, kWhat == Walk::output>;
   hipError_t e = with_lds(delta_walk_kernel<T, DK, W, NT, kWhat>, TL::bytes);
   if (e != hipSuccess) return e;
-  const int blocks = (a.m.dv + 16 * W - 1) / (16 * W) + (kWhat == Walk::sums ? (a.m.dk + 16 * W - 1) / (16 * W) : 0);
+  const int tiles = (a.m.dv + 15) / 16 + (kWhat == Walk::sums ? (a.m.dk + 15) / 16 : 0), blocks = (tiles + W - 1) / W;
   const long long units = (long long)a.m.n_slots * a.m.H;
   launch_kernel(delta_walk_kernel<T, DK, W, NT, kWhat>, grid_rows((units + 7) / 8 * 8 * blocks), 64 * W, TL::bytes, st, a,
                 blocks);
@@ -418,10 +418,15 @@ hipError_t launch_walk_t(const DeltaArgs& a, hipStream_t st) {
 template <Walk kWhat, int NT>
 hipError_t launch_walk_bf16(const DeltaArgs& a, hipStream_t st) {
   const int dk = a.m.dk;
-  if (decay_columns(true, a.m.dv) == 128)
+  if constexpr (kWhat == Walk::sums) {              // values and transition side by side
+    if (dk <= 32 && a.m.dv <= 32) return launch_walk_t<__bf16, 32, 4, NT, kWhat>(a, st);
     return dk <= 64 ? launch_walk_t<__bf16, 64, 8, NT, kWhat>(a, st) : launch_walk_t<__bf16, 128, 8, NT, kWhat>(a, st);
-  return dk <= 32 ? launch_walk_t<__bf16, 32, 4, NT, kWhat>(a, st)
-         : dk <= 64 ? launch_walk_t<__bf16, 64, 4, NT, kWhat>(a, st) : launch_walk_t<__bf16, 128, 4, NT, kWhat>(a, st);
+  } else {
+    if (decay_columns(true, a.m.dv) == 128)
+      return dk <= 64 ? launch_walk_t<__bf16, 64, 8, NT, kWhat>(a, st) : launch_walk_t<__bf16, 128, 8, NT, kWhat>(a, st);
+    return dk <= 32 ? launch_walk_t<__bf16, 32, 4, NT, kWhat>(a, st)
+           : dk <= 64 ? launch_walk_t<__bf16, 64, 4, NT, kWhat>(a, st) : launch_walk_t<__bf16, 128, 4, NT, kWhat>(a, st);
+  }
 }
 
 // States that the caller keeps are computed with three terms.

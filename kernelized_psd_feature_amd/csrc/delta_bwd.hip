@@ -687,7 +687,8 @@ hipError_t launch_both_t(const DeltaArgs& a, hipStream_t st) {
   const auto kernel = delta_both_kernel<T, DK, W, kSums>;
   hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
-  const int v = (a.m.dv + 16 * W - 1) / (16 * W), forward = v + (kSums ? (a.m.dk + 16 * W - 1) / (16 * W) : 0);
+  const int v = (a.m.dv + 16 * W - 1) / (16 * W);
+  const int forward = kSums ? ((a.m.dv + 15) / 16 + (a.m.dk + 15) / 16 + W - 1) / W : v;
   const long long units = (long long)a.m.n_slots * a.m.H;
   launch_kernel(kernel, grid_rows((units + 7) / 8 * 8 * (forward + v)), 64 * W, bytes, st, a, forward + v, forward);
   return hipGetLastError();

@@ -69,10 +69,21 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
   const int64_t chunks = (int64_t(pr->T) + kDecayChunk - 1) / kDecayChunk;
   const int cols = decay_columns(bf16, pr->dv);
   const int64_t v_blocks = (pr->dv + cols - 1) / cols, k_blocks = (pr->dk + cols - 1) / cols;
-  // segments that a sequence (packed: all tokens together) is cut into to fill the card
+  // Segments that a sequence (packed: all tokens together) is cut into to fill the card.  Of the bf16 walks of heads of
+  // up to 64 two workgroups fit on a CU, of the others one: 131072 tokens of 16 heads of 64 take 1040 us in 512
+  // segments and 1275 in 256, 4 x 16384 of 16 heads of 128 1278 in 256 and 1350 in 512.  Backward both directions
+  // run side by side; where whole sequences fill the CUs once they stay whole (8 x 4096, 16 heads of 64: 1025 us, cut
+  // in two 1164; 4 x 4096: cut into four 655, into two 729).
   const int64_t units = pr->H * v_blocks * (backward ? 2 : 1) * (pr->packed ? 1 : pr->n_seq);
-  const int64_t want = std::max<int64_t>(1, (backward ? 256 : 512) / units);
-  const int64_t L = chunks <= 8 ? chunks : std::max<int64_t>(4, (chunks + want - 1) / want);
+  const int64_t fill = bf16 && pr->dk <= 64 && pr->dv <= 64 && !(backward && units >= 256) ? 512 : 256;
+  const int64_t want = std::max<int64_t>(1, fill / units);
+  // A cut costs two more launches, and a step of the join for each segment: a sequence of up to six chunks stays whole
+  // (256 tokens 31 us, cut 38; 512 tokens 44 cut, 48 whole), and few chunks are cut into segments of about half their
+  // number's square root, four at most (1024 tokens: segments of 2 51 us, of 4 59; 2048: of 3 64, of 2 or 4 66;
+  // 4096: of 4 83, of 2 101).
+  int64_t least = 1;
+  while (least < 4 && 4 * least * least < chunks) ++least;
+  const int64_t L = chunks <= 6 ? chunks : std::max(least, (chunks + want - 1) / want);
   p.L = int(L);
   p.n_chunks = int(chunks);
   const int64_t SL = L * kDecayChunk;

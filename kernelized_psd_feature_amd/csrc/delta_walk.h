@@ -25,12 +25,12 @@ struct WalkTiles {
   static constexpr int NI = kBf ? 2 : 1;            // terms of the inverse
   static constexpr int bytes = kHead + (kTiles + (NI + (kOut ? kPO : 0)) * kC * LP) * (int)sizeof(T);
   // waves a SIMD that the registers are held to (the launch bound counts workgroups a CU)
-  static constexpr int occupancy = !kBf && DK == 128 ? 1 : 8 / W;
+  static constexpr int occupancy = !kBf && DK == 128 ? 1 : kBf && !kOut && W == 8 && DK == 64 ? 4 : 8 / W;
 };
 
 // kWhat: outputs and the final state; or (backward) the states before the chunks; or, of the segments,
 // sums and transitions (blocks of columns behind those of the values).  NT: terms of the recurrence's operands.
-// unit, sub: the segment and head, and which block of columns.
+// unit, sub: the segment and head, and which block of 16 W columns.
 template <typename T, int DK, int W, int NT, Walk kWhat>
 __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, int sub, int backward, char* lds) {
   constexpr bool kOut = kWhat == Walk::output, kSums = kWhat == Walk::sums;
@@ -38,6 +38,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   using frag = typename Elem<T>::frag;
   constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
   constexpr int NI = TL::NI, PO = TL::kPO, J = 16 / W;            // J: key tiles of a wave's part of P
+  constexpr bool kLean = sizeof(T) == 2 && kSums && W == 8 && DK == 64;
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
@@ -52,7 +53,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   // Wide heads: the places in LDS that a phase uses are computed there; kept from chunk to chunk they would cost
   // registers that are not there (a reload from scratch waits for the loads on their way, too).
   auto forget = [&] {
-    if constexpr (kOut && M > 2) {
+    if constexpr ((kOut && M > 2) || kLean) {
       asm volatile("" : "+v"(lane));
       g = lane >> 4;
       l16 = lane & 15;
@@ -61,10 +62,11 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (unit >= (unsigned)m.n_slots * (unsigned)m.H) return;
   const int slot = int(unit / (unsigned)m.H), h = int(unit - (unsigned)slot * (unsigned)m.H);
-  const int v_blocks = (m.dv + DV - 1) / DV;
-  const bool unit_matrix = kSums && sub >= v_blocks;                   // columns of the transition
-  if (unit_matrix) sub -= v_blocks;
-  const int c0 = sub * DV, cols = unit_matrix ? m.dk : m.dv;
+  const int ct = (m.dv + 15) / 16, c0 = sub * DV;
+  const bool values = c0 < m.dv;                    // uniform
+  // Sums: behind the tiles of the values' columns are those of the transition's, which start from the unit matrix
+  // and have no values.
+  const bool unit_matrix = kSums && sub * W + w >= ct;
 
   DeltaPart s;
   if (!find_part(m, slot, m.L, m.n_seg, m.n_slots, sh, s)) return;
@@ -97,18 +99,17 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   if constexpr (kSums) {
     // the sum of the last segment enters no entry state; a transition is used where a state comes in
     // from before, or in reversed time from behind
-    if (!unit_matrix && last_seg) return;
     const bool from_before = !last_seg && (s.part > 0 || A.init);
     const bool from_behind = backward && s.part > 0 && (!last_seg || A.dfin);
-    if (unit_matrix && !from_before && !from_behind) return;
+    if ((!values || last_seg) && (sub * W + W <= ct || (!from_before && !from_behind))) return;
   }
   const int first = s.part * L, behind = min(first + L, n_chunks);
   const long long row0 = s.start + (long long)kC * first;
   const int hk = h / (m.H / m.Hk);
   Stage<T, DK, kThr> rk(reinterpret_cast<const T*>(A.k) + s.b * A.sk[0] + row0 * A.sk[1] + hk * A.sk[2], A.sk[1], m.dk, true);
   Stage<T, DK, kThr> rq(reinterpret_cast<const T*>(kOut ? A.q : A.k) + s.b * A.sq[0] + row0 * A.sq[1] + hk * A.sq[2], A.sq[1], m.dk, true);
-  Stage<T, DV, kThr> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + (unit_matrix ? 0 : c0),
-                        A.sv[1], m.dv - (unit_matrix ? 0 : c0), false);
+  Stage<T, DV, kThr> rv(reinterpret_cast<const T*>(A.v) + s.b * A.sv[0] + row0 * A.sv[1] + h * A.sv[2] + (values ? c0 : 0),
+                        A.sv[1], m.dv - (values ? c0 : 0), false);
   StageInv<T, NI, LP, kThr> ri;
   const int n_last = min(kC, s.len - kC * (behind - 1));
   uint4 vec_next;
@@ -119,7 +120,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
     const int n = c == behind - 1 ? n_last : kC;
     fetch_rows(rk, A.sk[1], n);
     if constexpr (kOut) fetch_rows(rq, A.sq[1], n);
-    if (!unit_matrix) fetch_rows(rv, A.sv[1], n);
+    if (!kSums || values) fetch_rows(rv, A.sv[1], n);
     ri.fetch(p_inv);
     if (tid < kDeltaVec / 4) vec_next = reinterpret_cast<const uint4*>(p_vec)[tid];
     p_inv += (long long)m.H * kInvFloats;
@@ -128,7 +129,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   fetch(first);
 
   // state tiles: S[i] lane holds rows 16 i + 4 g + r of column c0 + wc + l16
-  const int wc = 16 * w, col = c0 + wc + l16;
+  const int wc = 16 * w, col = c0 + wc + l16 - (unit_matrix ? 16 * ct : 0), cols = unit_matrix ? m.dk : m.dv;
   f32x4 S[NS];
   {
     const float* given = kSums ? nullptr : s.part > 0 ? A.sums + ((long long)slot * m.H + h) * SE : A.init ? A.init + st_off : nullptr;
@@ -138,7 +139,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       for (int r = 0; r < 4; ++r) S[i][r] = kSums && unit_matrix && 16 * i + 4 * g + r == col ? 1.f : 0.f;
     if (given) load_state(S, given, m.dk, m.dv, col, g);               // uniform
   }
-  if (m.dk < DK || m.dv - c0 < DV || unit_matrix) { // columns that no operand has: zeros all along
+  if (m.dk < DK || m.dv - c0 < DV) {                // columns that no operand has: zeros all along
     uint4* const z = reinterpret_cast<uint4*>(sK);
     for (int i = tid; i < TL::kTiles * (int)sizeof(T) / 16; i += kThr) z[i] = uint4{0u, 0u, 0u, 0u};
   }
@@ -146,7 +147,6 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   const int rt = w & 3, j0 = J * (w >> 2);          // the wave's rows and first key tile of P
   const bool live_col = c0 + wc + 4 * g < m.dv;
   T* po = kOut ? out + (row0 + l16) * A.so[1] + wc + 4 * g : nullptr;
-  const int ct = (m.dv + 15) / 16;
   float *p_state = nullptr, *p_u = nullptr;
   if (kWhat == Walk::states && c0 / 16 + w < ct) {
     p_state = A.cstates + (chunk0 * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
@@ -166,7 +166,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
     __syncthreads();                                // the last chunk's tiles have been read
     rk.template put_split<LK>(sK);
     if constexpr (kOut) rq.template put_split<LK>(sQ);
-    if (!unit_matrix) rv.template put<LV>(sV);
+    if (!kSums || values) rv.template put<LV>(sV);
     ri.put(sT);
     if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
     // (stores before the next loads: the wait for these then does not wait for stores just issued)
@@ -215,24 +215,27 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
     } else {
       frag kr[4][M];
+      if constexpr (!kLean) {
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
         for (int i = 0; i < M; ++i) kr[it][i] = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
       reads_above<T>();
+      }
       Op<T, NT> sf[M];
 #pragma unroll
       for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
-      if constexpr (M <= 2) read_inv();
+      if constexpr (M <= 2 && !kLean) read_inv();
       reads_above<T>();
 #pragma unroll
       for (int it = 0; it < 4; ++it) X[it] = zero4();
 #pragma unroll
       for (int i = 0; i < M; ++i)
 #pragma unroll
-        for (int it = 0; it < 4; ++it) X[it] = mul(kr[it][i], sf[i], X[it]);
+        for (int it = 0; it < 4; ++it) X[it] = mul(kLean ? row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g) : kr[it][i], sf[i], X[it]);
+      if constexpr (kLean) reads_above<T>();
     }
     forget();
     if constexpr (M > 2 || kOut) read_inv();
@@ -247,18 +250,29 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
 #pragma unroll
       for (int i = 0; i < NS; ++i) kt[j][i] = split_column_frag<LK>(sK + 32 * j * LK, i, lane);
     };
-    if constexpr (M <= 2 && !kOut) read_kt(0);
+    if constexpr (M <= 2 && !kOut && !kLean) read_kt(0);
     reads_above<T>();
     auto correct = [&] {
       Op<T, NT> xf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_terms(X[2 * i], X[2 * i + 1], xf[i]);
+      if constexpr (kLean) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          U[it] = zero4();
+#pragma unroll
+          for (int i = 0; i <= it >> 1; ++i)
+            U[it] = mul(row_op<NI>(sT + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), xf[i], U[it]);
+          reads_above<T>();
+        }
+      } else {
       U[0] = mul(inv[0], xf[0], zero4());
       U[1] = mul(inv[1], xf[0], zero4());
       U[2] = mul(inv[2], xf[0], zero4());
       U[3] = mul(inv[4], xf[0], zero4());
       U[2] = mul(inv[3], xf[1], U[2]);
       U[3] = mul(inv[5], xf[1], U[3]);
+      }
       float sick = 0.f;
 #pragma unroll
       for (int it = 0; it < 4; ++it)
@@ -287,7 +301,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
             if (16 * it + 4 * g + r >= ill) x[it][r] = 0.f;
       };
       look(X);
-      read_inv();
+      if constexpr (!kLean) read_inv();
       correct();
       look(U);
     }
@@ -301,18 +315,24 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       f32x4 u[4];
 #pragma unroll
       for (int it = 0; it < 4; ++it) u[it] = U[it] * *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
+      if constexpr (!kLean) {
       if constexpr (M > 2 || kOut) read_kt(0);
       read_kt(1);
       reads_above<T>();
+      }
+      forget();
       Op<T, NT> uf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_terms(u[2 * i], u[2 * i + 1], uf[i]);
 #pragma unroll
       for (int i = 0; i < NS; ++i) S[i] *= whole;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (kLean) read_kt(j);
 #pragma unroll
         for (int i = 0; i < NS; ++i) S[i] = mul(kt[j][i], uf[j], S[i]);
+        if constexpr (kLean) reads_above<T>();
+      }
       if (any_ill && ill < kC)
 #pragma unroll
         for (int i = 0; i < NS; ++i) S[i] = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
