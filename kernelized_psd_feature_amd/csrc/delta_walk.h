@@ -22,7 +22,7 @@ struct WalkTiles {
   static constexpr int kHead = 16 + kDeltaVec * 4;
   static constexpr int kTiles = kC * (LK * (kOut ? 2 : 1) + LV);
   static constexpr int kPO = kBf ? 2 : 1;           // terms of the outputs' operands
-  static constexpr int NI = kBf ? 2 : 1;            // terms of the inverse
+  static constexpr int NI = kBf ? (NT == 3 ? 3 : 2) : 1;               // terms of the inverse
   static constexpr int bytes = kHead + (kTiles + (NI + (kOut ? kPO : 0)) * kC * LP) * (int)sizeof(T);
   // waves a SIMD that the registers are held to (the launch bound counts workgroups a CU)
   static constexpr int occupancy = !kBf && DK == 128 ? 1 : kBf && !kOut && W == 8 && DK == 64 ? 4 : 8 / W;
