@@ -55,14 +55,14 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
   float* const sD = reinterpret_cast<float*>(lds + TL::kHead);
   float* const sA = reinterpret_cast<float*>(lds + TL::kHead + TL::kKeys);   // blocks [16][LD], row by row of them
-  auto block = [&](int i, int j) { return sA + (i * (i + 1) / 2 + j) * 16 * LD; };
+  auto block = [&](int i, int j) __attribute__((always_inline)) { return sA + (i * (i + 1) / 2 + j) * 16 * LD; };
 
   const DeltaMap& m = A.m;
   const unsigned unit = block_number();
   if (unit >= (unsigned)m.c_slots * (unsigned)m.H) return;
   const int slot = int(unit / (unsigned)m.H), h = int(unit - (unsigned)slot * (unsigned)m.H);
   DeltaPart s;
-  if (!find_part(m, slot, 1, m.n_chunks, m.c_slots, sh, s) || s.seq == m.n_seq) return;
+  if (!find_part(m, slot, 1, m.n_chunks, m.c_slots, sh, kThreads, s) || s.seq == m.n_seq) return;
   const int row0 = s.start + kC * s.part, n = min(kC, s.len - kC * s.part);
   if (n <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
@@ -102,6 +102,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
     vec[4 * kC + lane] = lo;
   }
   if (m.dk < DK) __syncthreads();
+  keep_rows(rk, n);
   rk.template put_split<LK>(sK);
   __syncthreads();
 
@@ -208,10 +209,10 @@ __device__ __forceinline__ void join(const DeltaArgs& A, int sub, int h, int seq
   float* const sums = kRev ? A.rsums : A.sums;
   const float* given = kRev ? A.dfin : A.init;
   const bool live = col < m.dv;
-  auto place = [&](int j) { return (long long)(slot + (kRev ? n - 1 - j : j)) * m.H + h; };
+  auto place = [&](int j) __attribute__((always_inline)) { return (long long)(slot + (kRev ? n - 1 - j : j)) * m.H + h; };
   f32x4 S[R], N[kAhead][R];
   f32x8 a[kAhead][R][M];
-  auto fetch = [&](int j, int to) {                 // `to`: known where this is unrolled
+  auto fetch = [&](int j, int to) __attribute__((always_inline)) {                 // `to`: known where this is unrolled
     if (j + 1 >= n) return;                         // the last segment's are not used
     const float* const here = sums + place(j) * SE;
     const float* const tr = A.trans + place(j) * ME;

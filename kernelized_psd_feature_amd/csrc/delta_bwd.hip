@@ -56,13 +56,24 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
   T* const sP = sT + NI * kC * LP;
 
   const DeltaMap& m = A.m;
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  // (locals: what lambdas read out of the arguments ended in scratch, whose loads wait for all others)
+  const float scale = A.scale;
+  const float* const at_vec = A.vec;
+  const int tid = threadIdx.x;
+  int lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  auto forget = [&]() __attribute__((always_inline)) {                 // (see the walk)
+    if constexpr (M > 2 && TL::kBf) {
+      asm volatile("" : "+v"(lane));
+      g = lane >> 4;
+      l16 = lane & 15;
+    }
+  };
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (unit >= (unsigned)m.n_slots * (unsigned)m.H) return;
   const int slot = int(unit / (unsigned)m.H), h = int(unit - (unsigned)slot * (unsigned)m.H);
   const int c0 = sub * DV;
   DeltaPart s;
-  if (!find_part(m, slot, m.L, m.n_seg, m.n_slots, sh, s) || s.seq == m.n_seq) return;
+  if (!find_part(m, slot, m.L, m.n_seg, m.n_slots, sh, kThr, s) || s.seq == m.n_seq) return;
   const int L = m.L, n_chunks = (s.len + kC - 1) / kC, n_seg = (n_chunks + L - 1) / L;
   const long long SE = (long long)m.dk * m.dv, st_off = ((long long)s.seq * m.H + h) * SE;
   if (s.part >= n_seg) {
@@ -88,7 +99,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
   StageInv<T, NI, LP, kThr> ri;
   uint4 vec_next;
   const long long chunk0 = (long long)s.c_slot * m.H + h;              // [c_slots][H]
-  auto fetch = [&](int c) {
+  auto fetch = [&](int c) __attribute__((always_inline)) {
     const int n = c == behind - 1 ? n_last : kC;
     fetch_rows(rk, A.sk[1], n);
     fetch_rows(rq, A.sq[1], n);
@@ -97,8 +108,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
     rq.p -= 2 * kC * A.sq[1];
     ro.p -= 2 * kC * A.sdo[1];
     ri.fetch(A.inv + (chunk0 + (long long)c * m.H) * kInvFloats);
-    if (tid < kDeltaVec / 4)
-      vec_next = reinterpret_cast<const uint4*>(A.vec + (chunk0 + (long long)c * m.H) * kDeltaVec)[tid];
+    vec_next = fetch_vec(at_vec + (chunk0 + (long long)c * m.H) * kDeltaVec);
   };
   fetch(behind - 1);
 
@@ -118,11 +128,15 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
 #pragma unroll 1
   for (int c = behind - 1; c >= first; --c) {
     __syncthreads();                                // the last chunk's tiles have been read
+    const int n = c == behind - 1 ? n_last : kC;
+    keep_rows(rk, n);
+    keep_rows(rq, n);
+    keep_rows(ro, n);
     rk.template put_split<LK>(sK);
     rq.template put_split<LK>(sQ);
     ro.template put<LV>(sO);
     ri.put(sT);
-    if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
+    put_vec(vec, vec_next);
     if (!kSums && live_tile) {
       float* dst = A.rstates + ((chunk0 + (long long)c * m.H) * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
 #pragma unroll
@@ -131,6 +145,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
     if (c > first) fetch(c - 1);
     __syncthreads();
     // reads in batches, as in the walk
+    forget();
     f32x4 Z[4], X[4];
     frag of[2];
     {
@@ -160,8 +175,9 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
       for (int i = 0; i < M; ++i)
 #pragma unroll
         for (int it = 0; it < 4; ++it) Z[it] = mul(kr[it][i], df[i], Z[it]);
-      put_weights<T, LP, J, NP>(sP, p, vec + 3 * kC, rt, j0, lane, A.scale);
+      put_weights<T, LP, J, NP>(sP, p, vec + 3 * kC, rt, j0, lane, scale);
     }
+    forget();
 #pragma unroll
     for (int i = 0; i < 2; ++i) of[i] = column_frag<LV>(sO + 32 * i * LV + wc, lane);
     Op<T, NI> inv[6];                               // (row tile, K step): (0, 0), (0, 1), (1, 0), (1, 1), (2, 1), (3, 1)
@@ -171,6 +187,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
 #pragma unroll
     for (int it = 0; it < 4; ++it) Z[it] *= *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
     __syncthreads();                                // P is there
+    forget();
     {
       Op<T, NP> pf[6];
 #pragma unroll
@@ -184,8 +201,9 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
       Z[0] = mul(pf[1], of[1], Z[0]);
       Z[1] = mul(pf[3], of[1], Z[1]);
     }
+    forget();
     frag qt[2][NS];                                 // Q transposed, 32 tokens each, then K
-    auto read_t = [&](const T* tile, int j) {
+    auto read_t = [&](const T* tile, int j) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) qt[j][i] = split_column_frag<LK>(tile + 32 * j * LK, i, lane);
     };
@@ -211,7 +229,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
       X[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
       if (!kSums && live_tile) *reinterpret_cast<f32x4*>(px + it * 256) = X[it];
       X[it] *= -yv;
-      Z[it] = half_of(of[it >> 1], it & 1) * yv * A.scale;
+      Z[it] = half_of(of[it >> 1], it & 1) * yv * scale;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -245,12 +263,11 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
 }
 
 // Both walks side by side.  kSums: sums and transitions of the segments.
-template <typename T, int DK, int W, bool kSums>
+template <typename T, int DK, int W>
 constexpr int kBothBytes = WalkTiles<T, DK, W, 3, false>::bytes > ReverseTiles<T, DK, W>::bytes ? WalkTiles<T, DK, W, 3, false>::bytes
                                                                                               : ReverseTiles<T, DK, W>::bytes;
 template <typename T, int DK, int W, bool kSums>
-__global__ __launch_bounds__(64 * W, sizeof(T) == 4 && DK == 128 ? 1 : 8 / W) void delta_both_kernel(DeltaArgs A, int blocks,
-                                                                                                  int forward) {
+__global__ __launch_bounds__(64 * W, (sizeof(T) == 4 && DK == 128 ? 1 : 2)) void delta_both_kernel(DeltaArgs A, int blocks, int forward) {
   extern __shared__ __align__(16) char lds[];
   const UnitBlock u = unit_block(blocks);
   if (u.sub < forward) delta_walk<T, DK, W, sizeof(T) == 2 ? 3 : 1, kSums ? Walk::sums : Walk::states>(A, u.unit, u.sub, 1, lds);
@@ -285,14 +302,19 @@ __device__ __forceinline__ Op<T, K> leading(const Op<T, N>& x) {
   return y;
 }
 
-// A row's operand over 32 value columns from memory, zeros from column `width` on, and the same order of columns of 32
-// rows of LD elements: bf16 straight (one load of 16 bytes), fp32 split (two).
-__device__ __forceinline__ bf16x8 value_row(const __bf16* p, int width, int g) {
-  return 8 * g < width ? row_frag(p + 8 * g) : bf16x8{};
+// A row's operand over 32 value columns from `col` on, of `width` columns at p (the last ones again behind them), and
+// the same order of columns of 32 rows of LD elements: bf16 straight (one load of 16 bytes), fp32 split (two).
+__device__ __forceinline__ bf16x8 value_row(const __bf16* p, int col, int width, int g) {
+  return row_frag(p + min(col + 8 * g, width - 8));
 }
-__device__ __forceinline__ f32x8 value_row(const float* p, int width, int g) {
-  const f32x4 a = 4 * g < width ? load4(p + 4 * g) : zero4(), b = 16 + 4 * g < width ? load4(p + 16 + 4 * g) : zero4();
-  return pack_frag(a, b, float());
+__device__ __forceinline__ f32x8 value_row(const float* p, int col, int width, int g) {
+  return pack_frag(load4(p + min(col + 4 * g, width - 4)), load4(p + min(col + 16 + 4 * g, width - 4)), float());
+}
+__device__ __forceinline__ void keep_columns(bf16x8& x, bool row, int width, int g) {
+  if (!row || 8 * g >= width) x = bf16x8{};
+}
+__device__ __forceinline__ void keep_columns(f32x8& x, bool row, int width, int g) {
+  x = pack_frag(row && 4 * g < width ? half_of(x, 0) : zero4(), row && 16 + 4 * g < width ? half_of(x, 1) : zero4(), float());
 }
 __device__ __forceinline__ void store_row(__bf16* p, int width, int g, const bf16x8& x) {
   if (8 * g < width) *reinterpret_cast<uint4*>(p + 8 * g) = __builtin_bit_cast(uint4, x);
@@ -352,7 +374,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   int lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   // The places in LDS that a phase uses are computed there: kept from phase to phase they would cost a hundred
   // registers, and scratch.
-  auto forget = [&] {
+  auto forget = [&]() __attribute__((always_inline)) {
     asm volatile("" : "+v"(lane));
     g = lane >> 4;
     l16 = lane & 15;
@@ -369,7 +391,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     DeltaPart s;
     long long row0;
   };
-  auto clear = [&](const Place& p, int from, int rows) {
+  auto clear = [&](const Place& p, int from, int rows) __attribute__((always_inline)) {
     const long long at_k = (long long)p.s.b * m.T * m.Hk + p.hk, lead = (long long)p.s.b * m.T * m.H + p.hk * share;
     for (long long i = tid; i < (long long)rows * (m.dk / 4); i += kThreads) {
       const long long at = (at_k + (from + i / (m.dk / 4)) * m.Hk) * m.dk + i % (m.dk / 4) * 4;
@@ -386,13 +408,13 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     }
   };
   // The first unit from p.unit on that has tokens; those before it are zeros' rows, or nothing.
-  auto find = [&](Place& p) {
+  auto find = [&](Place& p) __attribute__((always_inline)) {
     for (; p.unit < units; p.unit += gridDim.x) {
       p.slot = int(p.unit / (unsigned)m.Hk);
       p.hk = int(p.unit - (unsigned)p.slot * (unsigned)m.Hk);
       p.hh = p.vb = 0;
       if (m.packed) __syncthreads();                // the last answer has been read
-      if (!find_part(m, p.slot, 1, m.n_chunks, m.c_slots, sh, p.s)) continue;
+      if (!find_part(m, p.slot, 1, m.n_chunks, m.c_slots, sh, kThreads, p.s)) continue;
       p.n = min(kC, p.s.len - kC * p.s.part);
       p.row0 = p.s.start + (long long)kC * p.s.part;
       if (p.s.seq == m.n_seq) {                     // rows behind the last sequence
@@ -412,10 +434,11 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   frag od[2], vd;
   uint4 vec_next;
   float frob_next = 0.f;
-  auto load = [&](const Place& p) {
+  auto load = [&](const Place& p) __attribute__((always_inline)) {
     const int h = p.hk * share + p.hh, c0 = 64 * p.vb, row = 16 * w + l16;
-    const long long cs = (long long)p.slot * m.H + h, tile = cs * ct + 4 * p.vb + w;
     const bool last = kC * (p.s.part + 1) >= p.s.len, live_tile = 4 * p.vb + w < ct;   // uniform
+    const int block_tile = live_tile ? 4 * p.vb + w : ct - 1;
+    const long long cs = (long long)p.slot * m.H + h, tile = cs * ct + block_tile;
     if (p.hh == 0 && p.vb == 0) {
       rk = Stage<T, DK, kThreads>(reinterpret_cast<const T*>(A.k) + p.s.b * A.sk[0] + p.row0 * A.sk[1] + p.hk * A.sk[2], A.sk[1],
                                   m.dk, true);
@@ -424,12 +447,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       fetch_rows(rk, A.sk[1], p.n);
       fetch_rows(rq, A.sq[1], p.n);
     }
-    if (p.vb == 0 && tid < kDeltaVec / 4) vec_next = reinterpret_cast<const uint4*>(A.vec + cs * kDeltaVec)[tid];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = zero4();
-#pragma unroll
-    for (int i = 0; i < NS; ++i) S[i] = zero4();
-    if (live_tile) {
+    vec_next = fetch_vec(A.vec + cs * kDeltaVec);
+    {
       const float* const fx = (first_half ? A.u : A.x) + tile * 1024 + lane * 4;
       const float* const fs = (first_half ? A.cstates : A.rstates) + tile * (DK * 16) + lane * 4;
 #pragma unroll
@@ -437,25 +456,26 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) S[i] = load4(fs + i * 256);
     }
-    od[0] = od[1] = vd = frag{};
-    if (row < p.n) {
-      const T* const po = reinterpret_cast<const T*>(A.dO) + p.s.b * A.sdo[0] + (p.row0 + row) * A.sdo[1] + h * A.sdo[2] + c0;
-      const T* const pv = reinterpret_cast<const T*>(A.v) + p.s.b * A.sv[0] + (p.row0 + row) * A.sv[1] + h * A.sv[2] + c0;
+    {
+      const long long at = p.row0 + min(row, p.n - 1);
+      const T* const po = reinterpret_cast<const T*>(A.dO) + p.s.b * A.sdo[0] + at * A.sdo[1] + h * A.sdo[2];
+      const T* const pv = reinterpret_cast<const T*>(A.v) + p.s.b * A.sv[0] + at * A.sv[1] + h * A.sv[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) od[i] = value_row(po + 32 * i, m.dv - c0 - 32 * i, g);
-      const int half = first_half ? 0 : 32;
-      vd = value_row(pv + half, m.dv - c0 - half, g);
+      for (int i = 0; i < 2; ++i) od[i] = value_row(po, c0 + 32 * i, m.dv, g);
+      vd = value_row(pv, c0 + (first_half ? 0 : 32), m.dv, g);
     }
     // (behind the last chunk without a gradient D is zero)
-    const bool sum = live_tile && !first_half && !(last && !A.fstates);
-    const float* const next = last ? A.fstates + (((long long)p.s.seq * m.H + h) * ct + 4 * p.vb + w) * (DK * 16) + lane * 4
-                                   : A.cstates + (tile + (long long)m.H * ct) * (DK * 16) + lane * 4;
+    const bool given = !last || A.fstates;
+    const float* const next = first_half ? A.cstates + tile * (DK * 16) + lane * 4     // (not used)
+                              : !last ? A.cstates + (tile + (long long)m.H * ct) * (DK * 16) + lane * 4
+                              : given ? A.fstates + (((long long)p.s.seq * m.H + h) * ct + block_tile) * (DK * 16) + lane * 4
+                                      : A.rstates + tile * (DK * 16) + lane * 4;
     if constexpr (kAhead) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) Sn[i] = sum ? load4(next + i * 256) : zero4();
+      for (int i = 0; i < NS; ++i) Sn[i] = load4(next + i * 256);
     } else {
       frob_next = 0.f;
-      if (sum)
+      if (given && !first_half && live_tile)
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const f32x4 y = S[i] * load4(next + i * 256);
@@ -495,8 +515,19 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     }
     forget();
     __syncthreads();                                // the last block's tiles have been read
-    if (now.vb == 0 && tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
+    if (now.vb == 0) put_vec(vec, vec_next);
+    if (4 * now.vb + w >= ct) {                     // no such columns (uniform)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = zero4();
+#pragma unroll
+      for (int i = 0; i < NS; ++i) S[i] = zero4();
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) keep_columns(od[i], live_row, m.dv - c0 - 32 * i, g);
+    keep_columns(vd, live_row, m.dv - c0 - (first_half ? 0 : 32), g);
     if (now.hh == 0 && now.vb == 0) {
+      keep_rows(rk, now.n);
+      keep_rows(rq, now.n);
       rk.template put_split<LK>(sK);
       rq.template put_split<LK>(sQ);
     }
@@ -505,7 +536,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) put_terms<N>(at + 16 * i, PL, x[i]);
     }
-    auto put_d = [&] {
+    auto put_d = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) put_terms<N2>(sD + (16 * w + l16) * LS + 16 * i + 4 * g, PS, S[i]);
     };
@@ -514,11 +545,12 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       for (int i = 0; i < NS; ++i) put_terms<N>(sS + (16 * w + l16) * LS + 16 * i + 4 * g, PS, S[i]);
     } else if constexpr (kAhead) {
       put_d();
+      if (kC * (now.s.part + 1) < now.s.len || A.fstates)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const f32x4 y = S[i] * Sn[i];
-        frob += y[0] + y[1] + y[2] + y[3];
-      }
+        for (int i = 0; i < NS; ++i) {
+          const f32x4 y = S[i] * Sn[i];
+          frob += y[0] + y[1] + y[2] + y[3];
+        }
     }
     frob += frob_next;
     const frag oc[2] = {od[0], od[1]}, vc = vd;
@@ -683,14 +715,14 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 
 template <typename T, int DK, int W, bool kSums>
 hipError_t launch_both_t(const DeltaArgs& a, hipStream_t st) {
-  constexpr int bytes = kBothBytes<T, DK, W, kSums>;
+  constexpr int bytes = kBothBytes<T, DK, W>;
   const auto kernel = delta_both_kernel<T, DK, W, kSums>;
   hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes);
   if (e != hipSuccess) return e;
-  const int v = (a.m.dv + 16 * W - 1) / (16 * W);
-  const int forward = kSums ? ((a.m.dv + 15) / 16 + (a.m.dk + 15) / 16 + W - 1) / W : v;
+  const int reverse = (a.m.dv + 16 * W - 1) / (16 * W);
+  const int forward = ((a.m.dv + 15) / 16 + (kSums ? (a.m.dk + 15) / 16 : 0) + W - 1) / W;
   const long long units = (long long)a.m.n_slots * a.m.H;
-  launch_kernel(kernel, grid_rows((units + 7) / 8 * 8 * (forward + v)), 64 * W, bytes, st, a, forward + v, forward);
+  launch_kernel(kernel, grid_rows((units + 7) / 8 * 8 * (forward + reverse)), 64 * W, bytes, st, a, forward + reverse, forward);
   return hipGetLastError();
 }
 

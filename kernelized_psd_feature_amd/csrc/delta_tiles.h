@@ -134,11 +134,13 @@ template <typename T, int N, int LD, int kThr>
 struct StageInv {
   static constexpr int kVecs = kInvFloats / 4, R = (kVecs + kThr - 1) / kThr;
   f32x4 x[R];
+  template <bool kAlways = true>                    // (see fetch_rows)
   __device__ __forceinline__ void fetch(const float* p) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int v = threadIdx.x + i * kThr;
-      if (kVecs % kThr == 0 || v < kVecs) x[i] = reinterpret_cast<const f32x4*>(p)[v];
+      if constexpr (kAlways || kVecs % kThr == 0) x[i] = reinterpret_cast<const f32x4*>(p)[min(v, kVecs - 1)];
+      else if (v < kVecs) x[i] = reinterpret_cast<const f32x4*>(p)[v];
     }
   }
   __device__ __forceinline__ static void zeros(T* tile) {
@@ -220,9 +222,9 @@ struct DeltaPart {
 __device__ __forceinline__ int cu_at(const DeltaMap& m, int i) { return min(max(m.cu[i], 0), m.T); }
 
 // The part of `len` chunks in `slot`; false where there is none.  seq == n_seq: rows behind the last sequence.
-// sh: one int of LDS.  Every thread calls it.
+// sh: one int of LDS.  Each of the `threads` threads calls it.
 __device__ __forceinline__ bool find_part(const DeltaMap& m, int slot, int chunks, int per_seq, int n_slots, int* sh,
-                                          DeltaPart& s) {
+                                          int threads, DeltaPart& s) {
   if (!m.packed) {
     const int seq = slot / per_seq;
     s = DeltaPart{seq, seq, 0, m.T, slot - seq * per_seq, seq * m.n_chunks};
@@ -231,7 +233,7 @@ __device__ __forceinline__ bool find_part(const DeltaMap& m, int slot, int chunk
   const int SL = kC * chunks;
   if (threadIdx.x == 0) *sh = -1;
   __syncthreads();
-  for (int i = threadIdx.x; i <= m.n_seq; i += blockDim.x) {
+  for (int i = threadIdx.x; i <= m.n_seq; i += threads) {
     const int lo = decay_first_slot(cu_at(m, i), i, SL);
     const int hi = i < m.n_seq ? decay_first_slot(cu_at(m, i + 1), i + 1, SL) : n_slots;
     if (lo <= slot && slot < hi) *sh = i;
@@ -255,11 +257,38 @@ __device__ __forceinline__ UnitBlock unit_block(int blocks) {
   return UnitBlock{8 * y + x % 8, int(x / 8 - y * per)};
 }
 
-// A chunk's rows of an operand as they are staged (Stage in tiles.h), n of them.
-template <typename S>
+// A chunk's rows of an operand as they are staged (Stage in tiles.h), n >= 1 of them.  kAlways: the last one is read
+// for those behind it, which keep_rows() makes zeros before they are put, so that no load stands under a condition:
+// before the next one's zeros are written the compiler waits for it, and with it for all others.  That serves a
+// workgroup alone on its CU (the backward walks of 8 x 4096: 384 us, 320 so); two share the wait, and lack the
+// registers (131072 tokens: sums 407 us, 515 so; outputs 490 and 537).
+template <bool kAlways = true, typename S>
 __device__ __forceinline__ void fetch_rows(S& s, long long st, int n) {
-  if (n < kC) s.fetch(st, n);
-  else s.template fetch<false>(st);
+  if (kAlways && n < kC) {                          // uniform
+    const int row = threadIdx.x / S::PER;
+#pragma unroll
+    for (int i = 0; i < S::N; ++i)
+      s.x[i] = *reinterpret_cast<const uint4*>(s.p + (min(row + i * S::kRows, n - 1) - row) * st);
+    s.p += kC * st;
+  } else if (n < kC) {
+    s.fetch(st, n);
+  } else {
+    s.template fetch<false>(st);
+  }
+}
+template <typename S>
+__device__ __forceinline__ void keep_rows(S& s, int n) {
+  if (n < kC)                                       // uniform
+#pragma unroll
+    for (int i = 0; i < S::N; ++i)
+      if (int(threadIdx.x / S::PER) + i * S::kRows >= n) s.x[i] = uint4{0u, 0u, 0u, 0u};
+}
+// The vectors of a chunk: a thread's four of them, and into LDS.
+__device__ __forceinline__ uint4 fetch_vec(const float* p) {
+  return reinterpret_cast<const uint4*>(p)[min((int)threadIdx.x, kDeltaVec / 4 - 1)];
+}
+__device__ __forceinline__ void put_vec(float* vec, const uint4& x) {
+  if (threadIdx.x < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[threadIdx.x] = x;
 }
 
 }  // namespace kata

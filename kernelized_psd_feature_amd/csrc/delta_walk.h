@@ -38,6 +38,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   using frag = typename Elem<T>::frag;
   constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
   constexpr int NI = TL::NI, PO = TL::kPO, J = 16 / W;            // J: key tiles of a wave's part of P
+  constexpr bool kAlways = kWhat == Walk::states;   // fetch_rows
   constexpr bool kLean = sizeof(T) == 2 && kSums && W == 8 && DK == 64;
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
@@ -48,11 +49,12 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   T* const sP = sT + NI * kC * LP;
 
   const DeltaMap& m = A.m;
+  const float scale = A.scale;
   const int tid = threadIdx.x;
   int lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   // Wide heads: the places in LDS that a phase uses are computed there; kept from chunk to chunk they would cost
   // registers that are not there (a reload from scratch waits for the loads on their way, too).
-  auto forget = [&] {
+  auto forget = [&]() __attribute__((always_inline)) {
     if constexpr ((kOut && M > 2) || kLean) {
       asm volatile("" : "+v"(lane));
       g = lane >> 4;
@@ -69,12 +71,12 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   const bool unit_matrix = kSums && sub * W + w >= ct;
 
   DeltaPart s;
-  if (!find_part(m, slot, m.L, m.n_seg, m.n_slots, sh, s)) return;
+  if (!find_part(m, slot, m.L, m.n_seg, m.n_slots, sh, kThr, s)) return;
   const int L = m.L;
   T* const out = kOut ? reinterpret_cast<T*>(A.o) + s.b * A.so[0] + h * A.so[2] + c0 : nullptr;
   if constexpr (kOut) {
     const int per_row = min(DV, m.dv - c0) / 4;
-    auto clear = [&](int from, int rows) {          // the block's columns of `rows` output rows
+    auto clear = [&](int from, int rows) __attribute__((always_inline)) {          // the block's columns of `rows` output rows
       for (long long i = tid; i < (long long)rows * per_row; i += kThr)
         store4(out + (from + i / per_row) * A.so[1] + i % per_row * 4, zero4());
     };
@@ -116,13 +118,14 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   const long long chunk0 = (long long)(s.c_slot + first) * m.H + h;    // [c_slots][H]
   const float* p_inv = A.inv + chunk0 * kInvFloats;
   const float* p_vec = A.vec + chunk0 * kDeltaVec;
-  auto fetch = [&](int c) {
+  auto fetch = [&](int c) __attribute__((always_inline)) {
     const int n = c == behind - 1 ? n_last : kC;
-    fetch_rows(rk, A.sk[1], n);
-    if constexpr (kOut) fetch_rows(rq, A.sq[1], n);
-    if (!kSums || values) fetch_rows(rv, A.sv[1], n);
-    ri.fetch(p_inv);
-    if (tid < kDeltaVec / 4) vec_next = reinterpret_cast<const uint4*>(p_vec)[tid];
+    fetch_rows<kAlways>(rk, A.sk[1], n);
+    if constexpr (kOut) fetch_rows<kAlways>(rq, A.sq[1], n);
+    if (!kSums || values) fetch_rows<kAlways>(rv, A.sv[1], n);
+    ri.template fetch<kAlways>(p_inv);
+    if constexpr (kAlways) vec_next = fetch_vec(p_vec);
+    else if (tid < kDeltaVec / 4) vec_next = reinterpret_cast<const uint4*>(p_vec)[tid];
     p_inv += (long long)m.H * kInvFloats;
     p_vec += (long long)m.H * kDeltaVec;
   };
@@ -154,23 +157,35 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   }
 
   Quad<T> O[4];                                     // outputs of the last chunk
-  auto store = [&](int rows) {
+  auto store = [&](int rows) __attribute__((always_inline)) {
     if (kOut && live_col)
 #pragma unroll
       for (int it = 0; it < 4; ++it)
         if (16 * it + l16 < rows) *reinterpret_cast<Quad<T>*>(po + 16 * it * A.so[1]) = O[it];
     po += kC * A.so[1];
   };
+  f32x4 U[4];
+  auto store_u = [&]() __attribute__((always_inline)) {                              // of the last chunk
+#pragma unroll
+    for (int it = 0; it < 4; ++it) *reinterpret_cast<f32x4*>(p_u + it * 256) = U[it];
+    p_u += (long long)m.H * ct * 1024;
+  };
 #pragma unroll 1
   for (int c = first; c < behind; ++c) {
     __syncthreads();                                // the last chunk's tiles have been read
+    if constexpr (kAlways) {
+      const int n = c == behind - 1 ? n_last : kC;
+      keep_rows(rk, n);
+      keep_rows(rv, n);
+    }
     rk.template put_split<LK>(sK);
     if constexpr (kOut) rq.template put_split<LK>(sQ);
     if (!kSums || values) rv.template put<LV>(sV);
     ri.put(sT);
-    if (tid < kDeltaVec / 4) reinterpret_cast<uint4*>(vec)[tid] = vec_next;
+    put_vec(vec, vec_next);
     // (stores before the next loads: the wait for these then does not wait for stores just issued)
     if (kWhat == Walk::states && p_state) {         // uniform
+      if (c > first) store_u();
 #pragma unroll
       for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(p_state + i * 256) = S[i];
       p_state += (long long)m.H * ct * (DK * 16);
@@ -181,9 +196,9 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
 
     // LDS reads are issued in batches, ahead of the work that hides them (reads_above): left alone, the compiler
     // waits for nearly every read before its product.
-    f32x4 X[4], U[4], o[4];
+    f32x4 X[4], o[4];
     Op<T, NI> inv[6];                               // (row tile, K step): (0, 0), (1, 0), (2, 0), (2, 1), (3, 0), (3, 1)
-    auto read_inv = [&] {
+    auto read_inv = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int f = 0; f < 6; ++f)
         inv[f] = row_op<NI>(sT + (16 * (f < 2 ? f : 1 + f / 2) + l16) * LP + (f < 2 ? 0 : 32 * (f & 1)) + 8 * g, kC * LP);
@@ -205,11 +220,11 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
 #pragma unroll
           for (int t = PO - 1; t >= 0; --t) o[it] = mma(sf[i].t[t], q, o[it]);
         }
-        o[it] *= vec[16 * it + l16] * A.scale;
+        o[it] *= vec[16 * it + l16] * scale;
       }
       reads_above<T>();
       forget();
-      put_scores<T, DK, LK, LP, J, PO>(sP, sQ, sK, vec + 3 * kC, rt, j0, lane, A.scale);
+      put_scores<T, DK, LK, LP, J, PO>(sP, sQ, sK, vec + 3 * kC, rt, j0, lane, scale);
       reads_above<T>();
 #pragma unroll
       for (int i = 0; i < 2; ++i) vf[i] = column_frag<LV>(sV + 32 * i * LV + wc, lane);
@@ -246,13 +261,13 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       X[it] = bv * (half_of(vf[it >> 1], it & 1) - yv * X[it]);
     }
     frag kt[2][NS];                                 // K transposed, 32 keys each
-    auto read_kt = [&](int j) {
+    auto read_kt = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) kt[j][i] = split_column_frag<LK>(sK + 32 * j * LK, i, lane);
     };
     if constexpr (M <= 2 && !kOut && !kLean) read_kt(0);
     reads_above<T>();
-    auto correct = [&] {
+    auto correct = [&]() __attribute__((always_inline)) {
       Op<T, NT> xf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_terms(X[2 * i], X[2 * i + 1], xf[i]);
@@ -304,11 +319,6 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       if constexpr (!kLean) read_inv();
       correct();
       look(U);
-    }
-    if (kWhat == Walk::states && p_u) {             // uniform
-#pragma unroll
-      for (int it = 0; it < 4; ++it) *reinterpret_cast<f32x4*>(p_u + it * 256) = U[it];
-      p_u += (long long)m.H * ct * 1024;
     }
     {
       const float whole = vec[kC - 1];
@@ -362,6 +372,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   }
 
   if constexpr (kOut) store(n_last);
+  if (kWhat == Walk::states && p_state) store_u();
 
   if (kWhat == Walk::states && last_seg && A.fstates && p_state) {     // the state behind the last chunk
     float* at = A.fstates + (((long long)s.seq * m.H + h) * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
