@@ -33,6 +33,7 @@ struct DeltaArgs {
   float* rsums;                           // backward: [n_slots][H][dk][dv], the same of the gradient of the state
   float* cstates;                         // backward: [c_slots][H][DK][DV] entry states of the chunks, in registers' order
   float* rstates;                         // backward: the gradient of the state behind each chunk
+  float *pq, *pk;                         // backward, or null: [b][t][H][dk], dq and dk by value heads
   float *u, *x;                           // backward: [c_slots][H][DV][64] U of the chunks, and dv, in registers' order
   float* fstates;                         // backward with dfin: [n_seq][H], as cstates, the final states
   // states

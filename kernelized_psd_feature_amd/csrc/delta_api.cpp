@@ -197,6 +197,10 @@ kata_status kata_bwd_delta(const kata_delta_problem* pr, const void* q, const vo
   a.dfin = dfinal_state;
   a.dinit = dinitial_state;
   if (!dfinal_state) a.fstates = nullptr;
+  if (p.by_heads) {
+    a.pq = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.pq);
+    a.pk = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.pk);
+  }
   a.dq = dq; a.dk = dk; a.dv = dv; a.dbeta = dbeta; a.dlog = dlog_decay;
   const bool bf16 = pr->dtype == KATA_BF16;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);

@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "delta.h"
+#include "delta_plan.h"
 #include "delta_tiles.h"
 #include "delta_walk.h"
 #include "device.h"
@@ -26,7 +27,6 @@ namespace kata {
 namespace {
 
 constexpr int kThreads = 512;             // of the gradients' kernel
-constexpr int kGradBlocks = 256;          // its workgroups, one a CU
 
 // ---- the walk in reversed time ------------------------------------------------------------------
 template <typename T, int DK, int W>
@@ -381,23 +381,31 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   };
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   const bool first_half = wave < 4;
-  const int share = m.H / m.Hk, ct = (m.dv + 15) / 16, v_blocks = (m.dv + 63) / 64;
-  const unsigned units = (unsigned)m.c_slots * (unsigned)m.Hk;
+  // A.pq: a workgroup has one value head, and leaves its dq and dk there, in fp32 rows of H heads
+  const int shared = m.H / m.Hk, share = A.pq ? 1 : shared, heads = A.pq ? m.H : m.Hk;
+  const int ct = (m.dv + 15) / 16, v_blocks = (m.dv + 63) / 64;
+  const unsigned units = (unsigned)m.c_slots * (unsigned)heads;
 
-  // where the workgroup is: a chunk and head of q and k, its `hh`th value head, its `vb`th block of columns
+  // where the workgroup is: a chunk and its value head h0 + hh, its `vb`th block of columns
   struct Place {
     unsigned unit;
-    int slot, hk, hh, vb, n;
+    int slot, h0, hh, vb, n;
     DeltaPart s;
     long long row0;
   };
-  auto clear = [&](const Place& p, int from, int rows) __attribute__((always_inline)) {
-    const long long at_k = (long long)p.s.b * m.T * m.Hk + p.hk, lead = (long long)p.s.b * m.T * m.H + p.hk * share;
-    for (long long i = tid; i < (long long)rows * (m.dk / 4); i += kThreads) {
-      const long long at = (at_k + (from + i / (m.dk / 4)) * m.Hk) * m.dk + i % (m.dk / 4) * 4;
-      store4(reinterpret_cast<T*>(A.dq) + at, zero4());
-      store4(reinterpret_cast<T*>(A.dk) + at, zero4());
+  auto put_grads = [&](long long at, const f32x4& q, const f32x4& k) __attribute__((always_inline)) {
+    if (A.pq) {
+      store4(A.pq + at, q);
+      store4(A.pk + at, k);
+    } else {
+      store4(reinterpret_cast<T*>(A.dq) + at, q);
+      store4(reinterpret_cast<T*>(A.dk) + at, k);
     }
+  };
+  auto clear = [&](const Place& p, int from, int rows) __attribute__((always_inline)) {
+    const long long at_k = (long long)p.s.b * m.T * heads + p.h0 / share, lead = (long long)p.s.b * m.T * m.H + p.h0;
+    for (long long i = tid; i < (long long)rows * (m.dk / 4); i += kThreads)
+      put_grads((at_k + (from + i / (m.dk / 4)) * heads) * m.dk + i % (m.dk / 4) * 4, zero4(), zero4());
     const int per = share * m.dv / 4;
     for (long long i = tid; i < (long long)rows * per; i += kThreads)
       store4(reinterpret_cast<T*>(A.dv) + (lead + (from + i / per) * m.H) * m.dv + i % per * 4, zero4());
@@ -410,8 +418,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   // The first unit from p.unit on that has tokens; those before it are zeros' rows, or nothing.
   auto find = [&](Place& p) __attribute__((always_inline)) {
     for (; p.unit < units; p.unit += gridDim.x) {
-      p.slot = int(p.unit / (unsigned)m.Hk);
-      p.hk = int(p.unit - (unsigned)p.slot * (unsigned)m.Hk);
+      p.slot = int(p.unit / (unsigned)heads);
+      p.h0 = int(p.unit - (unsigned)p.slot * (unsigned)heads) * share;
       p.hh = p.vb = 0;
       if (m.packed) __syncthreads();                // the last answer has been read
       if (!find_part(m, p.slot, 1, m.n_chunks, m.c_slots, sh, kThreads, p.s)) continue;
@@ -435,14 +443,14 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   uint4 vec_next;
   float frob_next = 0.f;
   auto load = [&](const Place& p) __attribute__((always_inline)) {
-    const int h = p.hk * share + p.hh, c0 = 64 * p.vb, row = 16 * w + l16;
+    const int h = p.h0 + p.hh, hk = h / shared, c0 = 64 * p.vb, row = 16 * w + l16;
     const bool last = kC * (p.s.part + 1) >= p.s.len, live_tile = 4 * p.vb + w < ct;   // uniform
     const int block_tile = live_tile ? 4 * p.vb + w : ct - 1;
     const long long cs = (long long)p.slot * m.H + h, tile = cs * ct + block_tile;
     if (p.hh == 0 && p.vb == 0) {
-      rk = Stage<T, DK, kThreads>(reinterpret_cast<const T*>(A.k) + p.s.b * A.sk[0] + p.row0 * A.sk[1] + p.hk * A.sk[2], A.sk[1],
+      rk = Stage<T, DK, kThreads>(reinterpret_cast<const T*>(A.k) + p.s.b * A.sk[0] + p.row0 * A.sk[1] + hk * A.sk[2], A.sk[1],
                                   m.dk, true);
-      rq = Stage<T, DK, kThreads>(reinterpret_cast<const T*>(A.q) + p.s.b * A.sq[0] + p.row0 * A.sq[1] + p.hk * A.sq[2], A.sq[1],
+      rq = Stage<T, DK, kThreads>(reinterpret_cast<const T*>(A.q) + p.s.b * A.sq[0] + p.row0 * A.sq[1] + hk * A.sq[2], A.sq[1],
                                   m.dk, true);
       fetch_rows(rk, A.sk[1], p.n);
       fetch_rows(rq, A.sq[1], p.n);
@@ -500,7 +508,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 #pragma unroll 1
   while (more) {
     if constexpr (!kAhead) load(now);
-    const int h = now.hk * share + now.hh, c0 = 64 * now.vb, row = 16 * w + l16;
+    const int h = now.h0 + now.hh, c0 = 64 * now.vb, row = 16 * w + l16;
     const long long lead = ((long long)now.s.b * m.T + now.row0) * m.H + h;    // of [b][t][H]
     const bool live_row = row < now.n;
     if (now.vb == 0) {
@@ -701,16 +709,29 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       }
     }
     if (now.hh + 1 == share && live_row) {
-      const long long at = (((long long)now.s.b * m.T + now.row0 + row) * m.Hk + now.hk) * m.dk + 4 * g;
+      const long long at = (((long long)now.s.b * m.T + now.row0 + row) * heads + now.h0 / share) * m.dk + 4 * g;
 #pragma unroll
       for (int i = 0; i < NH; ++i)
-        if (16 * (i0 + i) + 4 * g < m.dk) {
-          store4(reinterpret_cast<T*>(A.dq) + at + 16 * (i0 + i), dqa[i]);
-          store4(reinterpret_cast<T*>(A.dk) + at + 16 * (i0 + i), dka[i]);
-        }
+        if (16 * (i0 + i) + 4 * g < m.dk) put_grads(at + 16 * (i0 + i), dqa[i], dka[i]);
     }
     now = next;
   }
+}
+
+// dq and dk of the heads of q and k: the sums over the value heads that share them, in their order.
+template <typename T>
+__global__ __launch_bounds__(256) void delta_share_kernel(const float* __restrict__ pq, const float* __restrict__ pk, T* __restrict__ dq,
+                                                          T* __restrict__ dk, long long quads, int width, int share) {
+  const long long i = (long long)block_number() * 256 + threadIdx.x;   // [row and head][width / 4]
+  if (i >= quads) return;
+  const long long head = i / (width / 4), from = head * share * width + i % (width / 4) * 4;
+  f32x4 q = load4(pq + from), k = load4(pk + from);
+  for (int j = 1; j < share; ++j) {
+    q += load4(pq + from + (long long)j * width);
+    k += load4(pk + from + (long long)j * width);
+  }
+  store4(dq + 4 * i, q);
+  store4(dk + 4 * i, k);
 }
 
 template <typename T, int DK, int W, bool kSums>
@@ -743,8 +764,14 @@ hipError_t launch_grads_t(const DeltaArgs& a, hipStream_t st) {
   const auto kernel = delta_grads_kernel<T, DK>;
   hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), TL::bytes);
   if (e != hipSuccess) return e;
-  const long long units = (long long)a.m.c_slots * a.m.Hk;
-  launch_kernel(kernel, dim3(unsigned(units < kGradBlocks ? units : kGradBlocks)), kThreads, TL::bytes, st, a);
+  const long long units = (long long)a.m.c_slots * (a.pq ? a.m.H : a.m.Hk);
+  launch_kernel(kernel, dim3(unsigned(units < kDeltaGradBlocks ? units : kDeltaGradBlocks)), kThreads, TL::bytes, st, a);
+  if (a.pq) {
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const long long quads = (a.m.packed ? 1ll : a.m.n_seq) * a.m.T * a.m.Hk * (a.m.dk / 4);
+    launch_kernel(delta_share_kernel<T>, grid_rows((quads + 255) / 256), 256, 0, st, a.pq, a.pk, (T*)a.dq, (T*)a.dk, quads, a.m.dk,
+                  a.m.H / a.m.Hk);
+  }
   return hipGetLastError();
 }
 

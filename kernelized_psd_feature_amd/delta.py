@@ -212,14 +212,16 @@ def _qk_norm_problem(q, k, wq, wk, eps, l2, rates, positions, offset, interleave
     if Hk and not H:
         raise ValueError("k without heads of q: pass it as q")
     w_dtype = None
-    for name, w in (("q_weight", wq), ("k_weight", wk)):
-        if w is None:
-            continue
-        if w.shape != (D,) or not w.is_contiguous() or w.device != device:
-            raise ValueError(f"{name} must be a contiguous vector of a head's width on {device}")
-        if w_dtype is not None and w.dtype != w_dtype:
+    if wq is not None:
+        if wq.shape != (D,) or not wq.is_contiguous() or wq.device != device:
+            raise ValueError(f"q_weight must be a contiguous vector of a head's width on {device}")
+        w_dtype = wq.dtype
+    if wk is not None:
+        if wk.shape != (D,) or not wk.is_contiguous() or wk.device != device:
+            raise ValueError(f"k_weight must be a contiguous vector of a head's width on {device}")
+        if w_dtype is not None and wk.dtype != w_dtype:
             raise ValueError("the weights must share their dtype")
-        w_dtype = w.dtype
+        w_dtype = wk.dtype
     n, at = 0, None
     pos64 = pos_a = pos_b = pos_t = 0
     n_axes = 1
@@ -232,16 +234,21 @@ def _qk_norm_problem(q, k, wq, wk, eps, l2, rates, positions, offset, interleave
         pos64, n_axes, pos_a, pos_b, pos_t, at = _l._positions(positions, axes, B, T, n, device)
     elif positions is not None or axes is not None:
         raise ValueError("positions need rates")
-    tight = [(T * h * D, h * D, D) for h in (H, Hk)]
-    strides = [x.stride()[:3] if x is not None else tight[1] for x in (q, k)]
-    for x in (q, k, *(outs or ()), *(grads or ())):
-        if x is not None:
-            _rows_ok(x, "q, k, their outputs and gradients")
-    for given in (outs, grads):
-        strides += [x.stride()[:3] if x is not None else t for x, t in zip(given or (None, None), tight)]
+    tight_q, tight_k = (T * H * D, H * D, D, 1), (T * Hk * D, Hk * D, D, 1)
+    sq, sk = q.stride(), tight_k if k is None else k.stride()
+    so = [tight_q, tight_k, tight_q, tight_k]        # of the outputs, of the gradients of q' and k'
+    for i, given in enumerate((outs, grads)):
+        if given is not None:
+            so[2 * i] = given[0].stride()
+            if k is not None:
+                so[2 * i + 1] = given[1].stride()
+    if not sq[3] == sk[3] == so[0][3] == so[1][3] == so[2][3] == so[3][3] == 1:
+        for x in (q, k, *(outs or ()), *(grads or ())):
+            if x is not None:
+                _rows_ok(x, "q, k, their outputs and gradients")
     return _QK_NORM.pack(B, T, H, Hk, D, 2 * n, _dtype(dtype), _l._k.KATA_F32 if w_dtype is None else _dtype(w_dtype),
                          1 if interleaved else 0, 1 if l2 else 0, pos64, n_axes, magnitude, eps, pos_a, pos_b, pos_t,
-                         offset, *(s for x in strides for s in x)), at
+                         offset, *sq[:3], *sk[:3], *so[0][:3], *so[1][:3], *so[2][:3], *so[3][:3]), at
 
 
 def fwd_qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, l2=False, rates=None, positions=None, offset=0,

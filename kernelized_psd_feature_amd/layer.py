@@ -344,8 +344,9 @@ def _positions(positions, axes, B, T, pairs, device):
         return pos64, 1, 0, *x.stride(), positions.data_ptr()
     if axes.shape != (pairs,) or axes.dtype != torch.int32 or not axes.is_contiguous() or axes.device != device:
         raise ValueError(f"axes must be a contiguous int32 vector of an axis for each rate on {device}")
+    shape = positions.shape
     try:
-        x = positions.expand(positions.shape[0], B, T) if positions.dim() == 3 and positions.shape[0] else None
+        x = None if len(shape) != 3 or not shape[0] else positions if shape[1:] == (B, T) else positions.expand(shape[0], B, T)
     except RuntimeError:
         x = None
     if x is None:

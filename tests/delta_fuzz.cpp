@@ -145,6 +145,8 @@ int main(int argc, char** argv) {
         parts.push_back({p.u, c * 4096 * ((pr.dv + 15) / 16)});
         parts.push_back({p.x, c * 4096 * ((pr.dv + 15) / 16)});
         parts.push_back({p.rstates, c * chunk});
+        if (p.by_heads)
+          for (const size_t at : {p.pq, p.pk}) parts.push_back({at, (wide)(pr.packed ? 1 : pr.n_seq) * pr.T * pr.H * pr.dk * 4});
         parts.push_back({p.fstates, (wide)pr.n_seq * pr.H * chunk});
       }
       std::sort(parts.begin(), parts.end(), [](const Part& a, const Part& b) { return a.at < b.at; });
