@@ -212,46 +212,44 @@ __device__ __forceinline__ void join(const DeltaArgs& A, int sub, int h, int seq
   auto place = [&](int j) __attribute__((always_inline)) { return (long long)(slot + (kRev ? n - 1 - j : j)) * m.H + h; };
   f32x4 S[R], N[kAhead][R];
   f32x8 a[kAhead][R][M];
-  auto fetch = [&](int j, int to) __attribute__((always_inline)) {                 // `to`: known where this is unrolled
-    if (j + 1 >= n) return;                         // the last segment's are not used
-    const float* const here = sums + place(j) * SE;
-    const float* const tr = A.trans + place(j) * ME;
-    const bool used = j > 0 || given;               // else the state is zero, and the transition is not there
+  // No load under a condition (see fetch_rows), so places behind the state's ends are others' again.
+  auto fetch = [&](int j, int to) __attribute__((always_inline)) {     // `to`: known where this is unrolled
+    const long long at = place(min(j, n - 2));      // the last segment's are not used
+    const float* const here = sums + at * SE + min(col, m.dv - 1);
+    const float* const tr = A.trans + at * ME;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int tile = w * R + i, row = 16 * tile + l16;
+      const int tile = w * R + i, row = min(16 * tile + l16, m.dk - 1);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int y = 16 * tile + 4 * g + r;
-        N[to][i][r] = live && y < m.dk ? here[y * m.dv + col] : 0.f;
-      }
+      for (int r = 0; r < 4; ++r) N[to][i][r] = here[min(16 * tile + 4 * g + r, m.dk - 1) * m.dv];
 #pragma unroll
       for (int k = 0; k < M; ++k)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int q = 32 * k + 16 * half + 4 * g; // widths are multiples of four
-          f32x4 x = zero4();
-          if (used && row < m.dk && q < m.dk) {
-            if constexpr (kRev)
+          const int q = min(32 * k + 16 * half + 4 * g, m.dk - 4);     // widths are multiples of four
+          f32x4 x;
+          if constexpr (kRev)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) x[r] = tr[(q + r) * m.dk + row];
-            else
-              x = *reinterpret_cast<const f32x4*>(tr + row * m.dk + q);
-          }
+            for (int r = 0; r < 4; ++r) x[r] = tr[(q + r) * m.dk + row];
+          else
+            x = *reinterpret_cast<const f32x4*>(tr + row * m.dk + q);
 #pragma unroll
           for (int r = 0; r < 4; ++r) a[to][i][k][4 * half + r] = x[r];
         }
     }
   };
+  const float* const entry = (given ? given + ((long long)seq * m.H + h) * SE : sums + place(0) * SE) + min(col, m.dv - 1);
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[i][r] = entry[min(16 * (w * R + i) + 4 * g + r, m.dk - 1) * m.dv];
 #pragma unroll
   for (int j = 0; j < kAhead; ++j) fetch(j, j);
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int y = 16 * (w * R + i) + 4 * g + r;
-      S[i][r] = given && live && y < m.dk ? given[((long long)seq * m.H + h) * SE + y * m.dv + col] : 0.f;
-    }
+    for (int r = 0; r < 4; ++r)
+      if (!given || !live || 16 * (w * R + i) + 4 * g + r >= m.dk) S[i][r] = 0.f;
   for (int j0 = 0; j0 < n; j0 += kAhead)
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
@@ -274,19 +272,26 @@ __device__ __forceinline__ void join(const DeltaArgs& A, int sub, int h, int seq
       f32x4 odd[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) odd[i] = zero4();
+      if (j > 0 || given)                           // else the state is zero, and the transition is not there
 #pragma unroll
-      for (int k = 0; k < M; ++k) {
-        const f32x8 b = row_frag(buf + l16 * LS + 32 * k + 8 * g);
+        for (int k = 0; k < M; ++k) {
+          const f32x8 b = row_frag(buf + l16 * LS + 32 * k + 8 * g);
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+          for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int r = 0; r < 8; r += 2) {
-            N[s][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s][i][k][r], b[r], N[s][i], 0, 0, 0);
-            odd[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s][i][k][r + 1], b[r + 1], odd[i], 0, 0, 0);
-          }
+            for (int r = 0; r < 8; r += 2) {
+              N[s][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s][i][k][r], b[r], N[s][i], 0, 0, 0);
+              odd[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s][i][k][r + 1], b[r + 1], odd[i], 0, 0, 0);
+            }
+        }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        S[i] = N[s][i] + odd[i];
+        if (m.dk < DK)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (16 * (w * R + i) + 4 * g + r >= m.dk) S[i][r] = 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < R; ++i) S[i] = N[s][i] + odd[i];
       fetch(j + kAhead, s);
     }
 }
