@@ -444,7 +444,9 @@ kata_status kata_bwd_layer_norm(const kata_norm_problem* pr, const void* dy, con
  * S_{-1} being the initial state (zero where none is given).  Keys of unit length (kata_qk_norm) and b_t in
  * [0, 2] keep it stable; other values are computed as they are.  Chunks of 64 tokens run on MFMA (fp32
  * problems on the fp32 MFMA).  Sums, inverses and states are fp32; in bf16 problems an operand that comes
- * out of them (state, inverse, correction, weight) is kept in two bf16 terms, hi + lo, which hold 2^-18 of it.
+ * out of them (state, inverse, correction, weight) is kept in two bf16 terms, hi + lo, which hold 2^-18 of it, or
+ * (where a final state is asked for, and in the backward pass) in three, 2^-27: outputs may differ by a rounding
+ * between calls with and without a final state.
  * A token reaches only later ones, infinities and NaN included: from one on, the columns that it
  * reaches are NaN.  Gradients of sequences with such values are not defined.
  *
@@ -465,7 +467,7 @@ typedef struct {
   int64_t sq[3], sk[3], sv[3], so[3], sdo[3], sbeta[3], sdecay[3];
 } kata_delta_problem;
 
-/* Bytes of device workspace kata_fwd_delta needs (0 for an invalid problem): 13.6 KB for a chunk of 64 tokens
+/* Bytes of device workspace kata_fwd_delta needs (0 for an invalid problem): 11.5 KB for a chunk of 64 tokens
  * and head, and where sequences are cut into segments, a state and a transition (dk x dk) a segment. */
 size_t kata_fwd_delta_workspace_size(const kata_delta_problem* pr);
 
@@ -476,6 +478,8 @@ kata_status kata_fwd_delta(const kata_delta_problem* pr, const void* q, const vo
                            const float* initial_state, void* o, float* final_state, void* workspace,
                            size_t ws_bytes, void* stream);
 
+/* For the backward pass: besides these, for a chunk and head two states (dk rounded up to 32, 64 or 128) and two
+ * 64 x dv arrays, fp32: 76 KB at dk = dv = 64. */
 size_t kata_bwd_delta_workspace_size(const kata_delta_problem* pr);
 
 /* Gradients of sum(dO * o) + sum(dfinal_state * final_state) in q, k [B][T][Hk][dk] (summed over the value

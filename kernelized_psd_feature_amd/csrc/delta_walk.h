@@ -28,6 +28,9 @@ struct WalkTiles {
   static constexpr int occupancy = !kBf && DK == 128 ? 1 : kBf && !kOut && W == 8 && DK == 64 ? 4 : 8 / W;
 };
 
+// A wave has 16 columns of the values (or of the transition), and a part of P; W waves share K, Q and the inverse in LDS.
+// With outputs a chunk takes 7.5 us where two workgroups share a CU (131072 tokens, width 64), without them and
+// alone on its CU 2.5.
 // kWhat: outputs and the final state; or (backward) the states before the chunks; or, of the segments,
 // sums and transitions (blocks of columns behind those of the values).  NT: terms of the recurrence's operands.
 // unit, sub: the segment and head, and which block of 16 W columns.
@@ -39,6 +42,9 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   constexpr int kThr = 64 * W, DV = TL::DV, M = DK / 32, NS = DK / 16, LK = TL::LK, LV = TL::LV, LP = TL::LP;
   constexpr int NI = TL::NI, PO = TL::kPO, J = 16 / W;            // J: key tiles of a wave's part of P
   constexpr bool kAlways = kWhat == Walk::states;   // fetch_rows
+  // Sums of bf16 heads of up to 64: values and transition are eight waves, two workgroups a CU if they keep to 128
+  // registers: LDS is read where it is used, without batches (131072 tokens: 407 us; four waves each for values
+  // and transition, with batches, 475).
   constexpr bool kLean = sizeof(T) == 2 && kSums && W == 8 && DK == 64;
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
@@ -232,10 +238,10 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       frag kr[4][M];
       if constexpr (!kLean) {
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+        for (int it = 0; it < 4; ++it)
 #pragma unroll
-        for (int i = 0; i < M; ++i) kr[it][i] = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
-      reads_above<T>();
+          for (int i = 0; i < M; ++i) kr[it][i] = row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g);
+        reads_above<T>();
       }
       Op<T, NT> sf[M];
 #pragma unroll
@@ -281,12 +287,12 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
           reads_above<T>();
         }
       } else {
-      U[0] = mul(inv[0], xf[0], zero4());
-      U[1] = mul(inv[1], xf[0], zero4());
-      U[2] = mul(inv[2], xf[0], zero4());
-      U[3] = mul(inv[4], xf[0], zero4());
-      U[2] = mul(inv[3], xf[1], U[2]);
-      U[3] = mul(inv[5], xf[1], U[3]);
+        U[0] = mul(inv[0], xf[0], zero4());
+        U[1] = mul(inv[1], xf[0], zero4());
+        U[2] = mul(inv[2], xf[0], zero4());
+        U[3] = mul(inv[4], xf[0], zero4());
+        U[2] = mul(inv[3], xf[1], U[2]);
+        U[3] = mul(inv[5], xf[1], U[3]);
       }
       float sick = 0.f;
 #pragma unroll
@@ -326,9 +332,9 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
 #pragma unroll
       for (int it = 0; it < 4; ++it) u[it] = U[it] * *reinterpret_cast<const f32x4*>(vec + kC + 16 * it + 4 * g);
       if constexpr (!kLean) {
-      if constexpr (M > 2 || kOut) read_kt(0);
-      read_kt(1);
-      reads_above<T>();
+        if constexpr (M > 2 || kOut) read_kt(0);
+        read_kt(1);
+        reads_above<T>();
       }
       forget();
       Op<T, NT> uf[2];

@@ -124,7 +124,8 @@ def fwd_delta(q, k, v, beta, log_decay=None, scale=1.0, initial_state=None, retu
     cu_seqlens: int32 (n + 1,) offsets of n sequences packed into B = 1; rows of no sequence are zero in a
     new output and left as they are in `out`, which must not overlap an input.
     initial_state, and the final state with return_state: fp32 (n, H, dk, dv).  Sums and states are fp32; bf16
-    operands that come out of them are kept in two terms (2^-18).
+    operands that come out of them are kept in two terms (2^-18), with return_state in three, so that outputs may
+    differ by a rounding from a call without it.
     workspace: uint8, delta_workspace_size() bytes (allocated here otherwise)."""
     o = _out_like(v, out)
     pr = _delta_problem(q, k, v, beta, log_decay, scale, cu_seqlens, o=o, zero_tail=1 if out is None else 0)
