@@ -323,10 +323,10 @@ class _QkNorm(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
-    def backward(ctx, dq, dk):
+    def backward(ctx, dq, dk=None):
         q, k, q_weight, k_weight, rates, positions, axes = ctx.saved_tensors
-        dq, dk, dwq, dwk = bwd_qk_norm(dq.contiguous(), dk.contiguous(), q, k, q_weight, k_weight, rates=rates,
-                                       positions=positions, axes=axes,
+        dq, dk, dwq, dwk = bwd_qk_norm(dq.contiguous(), None if dk is None else dk.contiguous(), q, k, q_weight, k_weight,
+                                       rates=rates, positions=positions, axes=axes,
                                        params=ctx.needs_input_grad[2] or ctx.needs_input_grad[3], **ctx.cfg)
         return (dq, dk, dwq if ctx.needs_input_grad[2] else None, dwk if ctx.needs_input_grad[3] else None,
                 *[None] * 8)
@@ -334,7 +334,7 @@ class _QkNorm(torch.autograd.Function):
 
 def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, l2=False, rates=None, positions=None, offset=0,
             interleaved=False, magnitude=1.0, axes=None):
-    """fwd_qk_norm of both q and k with bwd_qk_norm as its gradient under torch autograd."""
+    """fwd_qk_norm with bwd_qk_norm as its gradient under torch autograd."""
     return _QkNorm.apply(q, k, q_weight, k_weight, eps, l2, rates, positions, offset, interleaved, magnitude, axes)
 
 

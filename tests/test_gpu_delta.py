@@ -216,6 +216,39 @@ def test_delta_packed(dtype, lengths):
         assert not g[:, :lead].any() and not g[:, lead + n:].any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_delta_rows_of_no_sequence_are_not_looked_at(dtype):
+    lengths, lead, tail = [70, 0, 129, 64, 1], 5, 40
+    T = lead + sum(lengths) + tail
+    *args, S0 = _inputs(41, 1, T, 1, 2, 64, 64, dtype, N=len(lengths))
+    dO, cu = _randn(4, *args[2].shape, dtype=dtype), _cu(lengths, lead)
+    want = K.fwd_delta(*args, initial_state=S0, return_state=True, cu_seqlens=cu), K.bwd_delta(
+        *args[:4], dO, args[4], initial_state=S0, cu_seqlens=cu)
+    for x in (*args, dO):
+        x[:, :lead] = float("nan")
+        x[:, T - tail:] = float("inf")
+    got = K.fwd_delta(*args, initial_state=S0, return_state=True, cu_seqlens=cu), K.bwd_delta(
+        *args[:4], dO, args[4], initial_state=S0, cu_seqlens=cu)
+    assert all(torch.equal(x, y) for a, b in zip(got, want) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(BF, 64, 128), (BF, 40, 80), (BF, 128, 72), (F32, 32, 80), (F32, 64, 64)])
+def test_delta_backward_of_more_chunks_than_workgroups(dtype, dk, dv):
+    # 6 x 46 chunks: a workgroup of the gradients takes two, and value heads in turn; alone, a sequence's fit at once
+    B, T = 6, 2900
+    *args, S0 = _inputs(43, B, T, 1, 2, dk, dv, dtype)
+    dO = _randn(4, B, T, 2, dv, dtype=dtype)
+    got = K.bwd_delta(*args[:4], dO, args[4], initial_state=S0)
+    for i in (0, 3, 5):
+        one = K.bwd_delta(*[x[i:i + 1] for x in args[:4]], dO[i:i + 1], args[4][i:i + 1], initial_state=S0[i:i + 1])
+        for name, x, y, t in zip("dq dk dv dbeta dlog dstate".split(), got, one, (dtype,) * 4 + (F32,) * 2):
+            # both are off by what test_delta_errors_by_their_norm allows
+            few = 2.0 ** -17 if dtype == BF else 2.0 ** -18
+            tol = max(4 * U[BF], few) if t == BF else 2 * few * (16 if name == "dlog" else 2)
+            err = (x[i:i + 1].double() - y.double()).norm() / y.double().norm()
+            assert err <= tol, (name, float(err), tol)
+
+
 def test_delta_packed_offsets_outside_the_rows_are_clamped():
     *args, S0 = _inputs(1, 1, 100, 1, 1, 64, 64, BF, N=2)
     bad = torch.tensor([-5, 1 << 30, 90], dtype=torch.int32, device=DEV)
@@ -764,6 +797,39 @@ def test_autograd_of_a_layer(packed):
         # roundings of its largest entry.  (Keys of length 4 would grow by 4e26 along the 130 tokens, the largest
         # norm of the products of I - b k k^T: no digit of the gradient would be left, in any order of sums.)
         _inside(x, r.numpy(), 2048 * 2.0 ** -24 * float(r.abs().max()), name)
+
+
+def test_autograd_of_the_norm_of_one_tensor():
+    x, w = _randn(1, 2, 30, 3, 64).requires_grad_(), _randn(2, 64).requires_grad_()
+    g, rates = _randn(3, 2, 30, 3, 64), K.rotary_rates(64)[0]
+    got = torch.autograd.grad(K.qk_norm(x, None, w, rates=rates, offset=3), (x, w), g)
+    want = K.bwd_qk_norm(g, None, x.detach(), None, w.detach(), rates=rates, offset=3)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[2])
+
+
+def test_a_captured_training_step_of_the_layer():
+    q, k, v, b, ld, _ = _inputs(51, 2, 700, 1, 2, 64, 64, BF)
+    w, g, rates = _randn(6, 64), _randn(5, *v.shape, dtype=BF), K.rotary_rates(64)
+
+    def step():
+        leaves = [x.detach().requires_grad_() for x in (q, k, v, b, ld, w)]
+        o = K.parallel_delta_attn(*leaves[:5], qk_norm="l2", rotary=rates, norm=(leaves[5], None))
+        return (o, *torch.autograd.grad(o, leaves, g))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(3):
+        for j, x in enumerate((q, k, v, g)):
+            x.copy_(_randn(60 + 4 * i + j, *x.shape, dtype=BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.detach().clone() for x in out]
+        want = step()
+        assert all(torch.isfinite(x).all() for x in want)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 def test_one_layer_prompt_then_tokens():
