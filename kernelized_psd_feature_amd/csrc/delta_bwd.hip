@@ -179,7 +179,9 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
 #pragma unroll
       for (int i = 0; i < M; ++i)
 #pragma unroll
-        for (int it = 0; it < 4; ++it) Z[it] = mul(kr[it][i], df[i], Z[it]);
+        for (int t = NT - 1; t >= 0; --t)
+#pragma unroll
+          for (int it = 0; it < 4; ++it) Z[it] = mma(kr[it][i], df[i].t[t], Z[it]);
       put_weights<T, LP, J, NP>(sP, p, vec + 3 * kC, rt, j0, lane, scale);
     }
     forget();
@@ -199,12 +201,14 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
       for (int f = 0; f < 6; ++f)
         pf[f] = split_column_op<NP, LP>(sP + 32 * (f < 4 ? f & 1 : 1) * LP, kC * LP, f < 4 ? f >> 1 : f - 2, lane);
       reads_above<T>();
-      Z[0] = mul(pf[0], of[0], Z[0]);
-      Z[1] = mul(pf[2], of[0], Z[1]);
-      Z[2] = mul(pf[4], of[1], Z[2]);
-      Z[3] = mul(pf[5], of[1], Z[3]);
-      Z[0] = mul(pf[1], of[1], Z[0]);
-      Z[1] = mul(pf[3], of[1], Z[1]);
+#pragma unroll
+      for (int t = NP - 1; t >= 0; --t)
+#pragma unroll
+        for (int it = 0; it < 4; ++it) Z[it] = mma(pf[it < 2 ? 2 * it : it + 2].t[t], of[it >> 1], Z[it]);
+#pragma unroll
+      for (int t = NP - 1; t >= 0; --t)
+#pragma unroll
+        for (int it = 0; it < 2; ++it) Z[it] = mma(pf[2 * it + 1].t[t], of[1], Z[it]);
     }
     forget();
     frag qt[2][NS];                                 // Q transposed, 32 tokens each, then K
@@ -219,12 +223,16 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
       Op<T, NT> zf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_terms(Z[2 * i], Z[2 * i + 1], zf[i]);
-      X[0] = mul(inv[0], zf[0], zero4());
-      X[1] = mul(inv[2], zf[0], zero4());
-      X[2] = mul(inv[4], zf[1], zero4());
-      X[3] = mul(inv[5], zf[1], zero4());
-      X[0] = mul(inv[1], zf[1], X[0]);
-      X[1] = mul(inv[3], zf[1], X[1]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) X[it] = zero4();
+      each_term<NI, NT>([&](int n, int k) __attribute__((always_inline)) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) X[it] = mma(inv[it < 2 ? 2 * it : it + 2].t[n], zf[it >> 1].t[k], X[it]);
+      });
+      each_term<NI, NT>([&](int n, int k) __attribute__((always_inline)) {
+#pragma unroll
+        for (int it = 0; it < 2; ++it) X[it] = mma(inv[2 * it + 1].t[n], zf[1].t[k], X[it]);
+      });
     }
     Op<T, NT> kw[2], qw[2];
     float* const px = A.x + ((chunk0 + (long long)c * m.H) * ct + c0 / 16 + w) * 1024 + lane * 4;
@@ -249,14 +257,18 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
       if constexpr (M > 2) read_t(sQ, j);
       reads_above<T>();
 #pragma unroll
-      for (int i = 0; i < NS; ++i) D[i] = mul(qt[j][i], qw[j], D[i]);
+      for (int t = NT - 1; t >= 0; --t)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) D[i] = mma(qt[j][i], qw[j].t[t], D[i]);
       read_t(sK, j);
     }
     reads_above<T>();
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) D[i] = mul(qt[j][i], kw[j], D[i]);
+      for (int t = NT - 1; t >= 0; --t)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) D[i] = mma(qt[j][i], kw[j].t[t], D[i]);
   }
   float* dst = kSums ? A.rsums + ((long long)slot * m.H + h) * SE : first == 0 && A.dinit ? A.dinit + st_off : nullptr;
   if (!dst || col >= m.dv) return;

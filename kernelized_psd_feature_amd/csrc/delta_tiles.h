@@ -72,6 +72,18 @@ __device__ __forceinline__ f32x4 mul(const Op<T, N>& a, const Op<T, K>& b, f32x4
   return c;
 }
 
+// The pairs of terms (i, k) of a product of N by K of them, smallest first.  f adds that pair's product to several tiles
+// in turn: a product that waits for the one just issued costs its whole latency.
+template <int N, int K, typename F>
+__device__ __forceinline__ void each_term(F f) {
+  constexpr int most = N > K ? N : K;
+#pragma unroll
+  for (int order = most - 1; order >= 0; --order)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (order - i >= 0 && order - i < K) f(i, order - i);
+}
+
 // Four neighbouring elements of a row as N planes of them, `plane` elements apart.
 template <int N, typename T>
 __device__ __forceinline__ void put_terms(T* at, int plane, f32x4 x) {

@@ -46,6 +46,10 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
   // registers: LDS is read where it is used, without batches (131072 tokens: 407 us; four waves each for values
   // and transition, with batches, 475).
   constexpr bool kLean = sizeof(T) == 2 && kSums && W == 8 && DK == 64;
+  // Products of several tiles in turn, or a tile's one after the other.  In turn 4 x 16384 tokens of width 128 take
+  // 1284 us for 1332; outputs at width 64 and the sums above lack the registers (131072 tokens: 1075 for 1031).
+  constexpr bool kTurns = !kLean && (!kOut || M > 2);
+  constexpr int P = kTurns ? 2 : 1;                 // tiles of outputs
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
@@ -217,16 +221,27 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       for (int i = 0; i < M; ++i) split_terms(S[2 * i], S[2 * i + 1], sf[i]);
       // bf16: with two terms of the state, of P and of U an output has no error but its own rounding
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        X[it] = o[it] = zero4();
+      for (int i0 = 0; i0 < 4; i0 += P) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) X[i0 + p] = o[i0 + p] = zero4();
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-          X[it] = mul(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], X[it]);
-          const frag q = row_frag(sQ + (16 * it + l16) * LK + 32 * i + 8 * g);
+          frag kr[P], qr[P];
 #pragma unroll
-          for (int t = PO - 1; t >= 0; --t) o[it] = mma(sf[i].t[t], q, o[it]);
+          for (int p = 0; p < P; ++p) {
+            kr[p] = row_frag(sK + (16 * (i0 + p) + l16) * LK + 32 * i + 8 * g);
+            qr[p] = row_frag(sQ + (16 * (i0 + p) + l16) * LK + 32 * i + 8 * g);
+          }
+#pragma unroll
+          for (int t = NT - 1; t >= 0; --t)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              X[i0 + p] = mma(kr[p], sf[i].t[t], X[i0 + p]);
+              if (t < PO) o[i0 + p] = mma(sf[i].t[t], qr[p], o[i0 + p]);
+            }
         }
-        o[it] *= vec[16 * it + l16] * scale;
+#pragma unroll
+        for (int p = 0; p < P; ++p) o[i0 + p] *= vec[16 * (i0 + p) + l16] * scale;
       }
       reads_above<T>();
       forget();
@@ -254,9 +269,16 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
       for (int it = 0; it < 4; ++it) X[it] = zero4();
 #pragma unroll
       for (int i = 0; i < M; ++i)
+        if constexpr (kLean) {
 #pragma unroll
-        for (int it = 0; it < 4; ++it) X[it] = mul(kLean ? row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g) : kr[it][i], sf[i], X[it]);
-      if constexpr (kLean) reads_above<T>();
+          for (int it = 0; it < 4; ++it) X[it] = mul(row_frag(sK + (16 * it + l16) * LK + 32 * i + 8 * g), sf[i], X[it]);
+          reads_above<T>();
+        } else {
+#pragma unroll
+          for (int t = NT - 1; t >= 0; --t)
+#pragma unroll
+            for (int it = 0; it < 4; ++it) X[it] = mma(kr[it][i], sf[i].t[t], X[it]);
+        }
     }
     forget();
     if constexpr (M > 2 || kOut) read_inv();
@@ -286,13 +308,24 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
             U[it] = mul(row_op<NI>(sT + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), xf[i], U[it]);
           reads_above<T>();
         }
-      } else {
+      } else if constexpr (!kTurns) {
         U[0] = mul(inv[0], xf[0], zero4());
         U[1] = mul(inv[1], xf[0], zero4());
         U[2] = mul(inv[2], xf[0], zero4());
         U[3] = mul(inv[4], xf[0], zero4());
         U[2] = mul(inv[3], xf[1], U[2]);
         U[3] = mul(inv[5], xf[1], U[3]);
+      } else {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) U[it] = zero4();
+        each_term<NI, NT>([&](int n, int k) __attribute__((always_inline)) {
+#pragma unroll
+          for (int it = 0; it < 4; ++it) U[it] = mma(inv[it < 2 ? it : 2 * it - 2].t[n], xf[0].t[k], U[it]);
+        });
+        each_term<NI, NT>([&](int n, int k) __attribute__((always_inline)) {
+          U[2] = mma(inv[3].t[n], xf[1].t[k], U[2]);
+          U[3] = mma(inv[5].t[n], xf[1].t[k], U[3]);
+        });
       }
       float sick = 0.f;
 #pragma unroll
@@ -345,8 +378,15 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if constexpr (kLean) read_kt(j);
+        if constexpr (kTurns) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) S[i] = mul(kt[j][i], uf[j], S[i]);
+          for (int t = NT - 1; t >= 0; --t)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) S[i] = mma(kt[j][i], uf[j].t[t], S[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NS; ++i) S[i] = mul(kt[j][i], uf[j], S[i]);
+        }
         if constexpr (kLean) reads_above<T>();
       }
       if (any_ill && ill < kC)
@@ -360,10 +400,17 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& A, unsigned unit, in
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_terms(U[2 * i], U[2 * i + 1], uf[i]);
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+      for (int i0 = 0; i0 < 4; i0 += P)
 #pragma unroll
-        for (int i = 0; i <= it >> 1; ++i)
-          o[it] = mul(uf[i], row_op<PO>(sP + (16 * it + l16) * LP + 32 * i + 8 * g, kC * LP), o[it]);
+        for (int i = 0; i <= i0 >> 1; ++i) {
+          Op<T, PO> pf[P];
+#pragma unroll
+          for (int p = 0; p < P; ++p) pf[p] = row_op<PO>(sP + (16 * (i0 + p) + l16) * LP + 32 * i + 8 * g, kC * LP);
+          each_term<PO, PO>([&](int n, int k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) o[i0 + p] = mma(uf[i].t[n], pf[p].t[k], o[i0 + p]);
+          });
+        }
       if (any_ill)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
