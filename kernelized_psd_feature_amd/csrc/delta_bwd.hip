@@ -15,7 +15,7 @@
 // S and U, and D and dv, come from two walks like the forward pass's, one of them in reversed time, which keep
 // them for every chunk; all the rest is then computed for all chunks at once (delta_grads_kernel).
 //
-// 8 x 4096 tokens of 16 bf16 heads of 64: inverses 47 us, both walks 297, gradients 387; the bytes that the three
+// 8 x 4096 tokens of 16 bf16 heads of 64: inverses 47 us, both walks 297, gradients 370; the bytes that the three
 // exchange, 1.9 GB, are 380 us of HBM's time.  The walks are a chain as forward, 64 chunks of 4.6 us where 256
 // workgroups have a CU each (VALU 33 % of the cycles, LDS 34, MFMA 20).  Four waves more, forming P^T dO and
 // Q^T diag(y) dO a chunk ahead, did not shorten it (330 for 305): the waves share their SIMDs.
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(64 * W, (sizeof(T) == 4 && DK == 128 ? 1 : 2)) void
 // have left in tiles of 16 columns, go through LDS, [column][token] and [column][row of the state]; a wave has 16
 // tokens, four of the waves P's gradient and half of the columns of dq and dk, the others that of the system's
 // matrix and the other half.
-// 387 us for 8 x 4096 tokens of 16 heads of 64, 136 KB a chunk and head, 2.9 TB/s: a CU holds one workgroup (121 KB of
+// 370 us for 8 x 4096 tokens of 16 heads of 64, 136 KB a chunk and head, 3.0 TB/s: a CU holds one workgroup (121 KB of
 // LDS), its loads run a chunk ahead, and five barriers part phases of some hundred cycles of LDS and VALU each (VALU
 // 32 % of the cycles, LDS 30, MFMA 9; without any load 300 us).
 template <typename T, int DK>
@@ -377,6 +377,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   constexpr int NS = DK / 16, NH = NS / 2, LK = TL::LK, LP = TL::LP, LS = TL::LS, N = TL::N, N2 = TL::N2;
   constexpr int PL = TL::kPlane, PS = TL::kState;
   constexpr bool kAhead = TL::kAhead;
+  constexpr int G = NH < 2 || (sizeof(T) == 4 && DK > 64) ? 1 : 2;     // tiles of dq and dk in turn (each_term), by the registers
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
@@ -608,28 +609,53 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 #pragma unroll
     for (int t = 0; t < N; ++t) e -= first_half ? dot(z[0].t[t], vc) : dot(z[1].t[t], vc);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j <= w)                                   // uniform
+    for (int j0 = 0; j0 < 4; j0 += 2)
+      if (j0 <= w)                                  // uniform (a tile above the diagonal is not looked at)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const T* const at = sU + 32 * i * LP + 16 * j;
-          if (first_half) Wt[j] = mul(value_op<N, LP>(at, PL, lane), oc[i], Wt[j]);
-          else Wt[j] = mul(value_op<N2, LP>(at, PL, lane), leading<N2>(z[i]), Wt[j]);
+          const T* const at = sU + 32 * i * LP + 16 * j0;
+          if (first_half) {
+            const Op<T, N> ua = value_op<N, LP>(at, PL, lane), ub = value_op<N, LP>(at + 16, PL, lane);
+#pragma unroll
+            for (int t = N - 1; t >= 0; --t) {
+              Wt[j0] = mma(ua.t[t], oc[i], Wt[j0]);
+              Wt[j0 + 1] = mma(ub.t[t], oc[i], Wt[j0 + 1]);
+            }
+          } else {
+            const Op<T, N2> ua = value_op<N2, LP>(at, PL, lane), ub = value_op<N2, LP>(at + 16, PL, lane);
+            each_term<N2, N2>([&](int n, int k) __attribute__((always_inline)) {
+              Wt[j0] = mma(ua.t[n], z[i].t[k], Wt[j0]);
+              Wt[j0 + 1] = mma(ub.t[n], z[i].t[k], Wt[j0 + 1]);
+            });
+          }
         }
     forget();
     {
       const float yr = vec[16 * w + l16], yo = yr * A.scale;
 #pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        f32x4 a = zero4(), b = zero4();
+      for (int ia = 0; ia < NH; ia += G) {
+        f32x4 a[G], b[G];
+#pragma unroll
+        for (int p = 0; p < G; ++p) a[p] = b[p] = zero4();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const Op<T, N> st = value_op<N, LS>(sS + 32 * j * LS + 16 * (i0 + i), PS, lane);
-          a = mul(st, oc[j], a);
-          b = mul(leading<N2>(st), leading<N2>(z[j]), b);
+          Op<T, N> st[G];
+#pragma unroll
+          for (int p = 0; p < G; ++p) st[p] = value_op<N, LS>(sS + 32 * j * LS + 16 * (i0 + ia + p), PS, lane);
+#pragma unroll
+          for (int t = N - 1; t >= 0; --t)
+#pragma unroll
+            for (int p = 0; p < G; ++p) a[p] = mma(st[p].t[t], oc[j], a[p]);
+          each_term<N2, N2>([&](int n, int k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int p = 0; p < G; ++p) b[p] = mma(st[p].t[n], z[j].t[k], b[p]);
+          });
         }
-        dqh[i] += a * yo;
-        dka[i] -= b * yr;
+#pragma unroll
+        for (int p = 0; p < G; ++p) {
+          dqh[ia + p] += a[p] * yo;
+          dka[ia + p] -= b[p] * yr;
+        }
       }
     }
     Op<T, N2> u[2];
@@ -643,11 +669,22 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     forget();
     const float left = vec[kC + 16 * w + l16];
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      f32x4 a = zero4();
+    for (int ia = 0; ia < NH; ia += G) {
+      f32x4 a[G];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) a = mul(value_op<N2, LS>(sD + 32 * j * LS + 16 * (i0 + i), PS, lane), u[j], a);
-      dka[i] += a * left;
+      for (int p = 0; p < G; ++p) a[p] = zero4();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        Op<T, N2> st[G];
+#pragma unroll
+        for (int p = 0; p < G; ++p) st[p] = value_op<N2, LS>(sD + 32 * j * LS + 16 * (i0 + ia + p), PS, lane);
+        each_term<N2, N2>([&](int n, int k) __attribute__((always_inline)) {
+#pragma unroll
+          for (int p = 0; p < G; ++p) a[p] = mma(st[p].t[n], u[j].t[k], a[p]);
+        });
+      }
+#pragma unroll
+      for (int p = 0; p < G; ++p) dka[ia + p] += a[p] * left;
     }
     if (now.vb + 1 < v_blocks) {
       now = next;
@@ -687,18 +724,36 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NH; ++i)
+    for (int ia = 0; ia < NH; ia += G)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const frag kt = split_column_frag<LK>(sK + 32 * j * LK, i0 + i, lane);
+        frag kt[G];
+#pragma unroll
+        for (int p = 0; p < G; ++p) kt[p] = split_column_frag<LK>(sK + 32 * j * LK, i0 + ia + p, lane);
         if (j <= w >> 1) {                          // uniform
-          dqh[i] = mul(kt, row_op<N>(sU + (16 * w + l16) * LP + 32 * j + 8 * g, PL), dqh[i]);
-          dka[i] = mul(kt, row_op<N2>(sZ + (16 * w + l16) * LP + 32 * j + 8 * g, PL), dka[i]);
+          const Op<T, N> po = row_op<N>(sU + (16 * w + l16) * LP + 32 * j + 8 * g, PL);
+          const Op<T, N2> pv = row_op<N2>(sZ + (16 * w + l16) * LP + 32 * j + 8 * g, PL);
+#pragma unroll
+          for (int t = N - 1; t >= 0; --t)
+#pragma unroll
+            for (int p = 0; p < G; ++p) {
+              dqh[ia + p] = mma(kt[p], po.t[t], dqh[ia + p]);
+              if (t < N2) dka[ia + p] = mma(kt[p], pv.t[t], dka[ia + p]);
+            }
         }
         if (j >= w >> 1) {
-          dka[i] = mul(split_column_frag<LK>(sQ + 32 * j * LK, i0 + i, lane),
-                       split_column_op<N2, LP>(sU + 32 * j * LP, PL, w, lane), dka[i]);
-          dka[i] = mul(kt, split_column_op<N2, LP>(sZ + 32 * j * LP, PL, w, lane), dka[i]);
+          const Op<T, N2> po = split_column_op<N2, LP>(sU + 32 * j * LP, PL, w, lane);
+          const Op<T, N2> pv = split_column_op<N2, LP>(sZ + 32 * j * LP, PL, w, lane);
+          frag qt[G];
+#pragma unroll
+          for (int p = 0; p < G; ++p) qt[p] = split_column_frag<LK>(sQ + 32 * j * LK, i0 + ia + p, lane);
+#pragma unroll
+          for (int t = N2 - 1; t >= 0; --t) {
+#pragma unroll
+            for (int p = 0; p < G; ++p) dka[ia + p] = mma(qt[p], po.t[t], dka[ia + p]);
+#pragma unroll
+            for (int p = 0; p < G; ++p) dka[ia + p] = mma(kt[p], pv.t[t], dka[ia + p]);
+          }
         }
       }
     // dO . o = q . dq of this head
