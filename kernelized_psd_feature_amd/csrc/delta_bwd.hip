@@ -603,8 +603,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     for (int i = 0; i < 2; ++i) z[i] = value_op<N, LP>(sZ + 32 * i * LP + 16 * w, PL, lane);
     if (live_row) {                                 // dv, half of the columns each
       T* const dst = reinterpret_cast<T*>(A.dv) + (lead + (long long)row * m.H) * m.dv + c0;
-      if (first_half) store_row(dst, m.dv - c0, g, z[0].t[0]);
-      else store_row(dst + 32, m.dv - c0 - 32, g, z[1].t[0]);
+      frag dv = first_half ? z[0].t[0] : z[1].t[0];
+      if (fabsf(vec[2 * kC + row]) <= 1e-15f) dv = frag{};             // beta was nothing (delta_prep_kernel)
+      store_row(dst + (first_half ? 0 : 32), m.dv - c0 - (first_half ? 0 : 32), g, dv);
     }
 #pragma unroll
     for (int t = 0; t < N; ++t) e -= first_half ? dot(z[0].t[t], vc) : dot(z[1].t[t], vc);
@@ -770,7 +771,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     if (wave == 0) {
       const long long at = lead + (long long)lane * m.H;
       const float b = vec[2 * kC + lane];
-      if (lane < now.n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[2 * kC + lane] / (b * b));
+      if (lane < now.n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[2 * kC + lane] / b / b);
       if (A.dlog) {
         double y = (double)sE[lane] + sE[kC + lane];
 #pragma unroll

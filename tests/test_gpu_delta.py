@@ -166,6 +166,44 @@ def test_delta_beta_at_its_ends(dtype, beta):
         assert not K.fwd_delta(*args).any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_delta_tokens_without_a_step(dtype):
+    # padding by beta = 0: nothing is written there, and v has no gradient
+    *args, S0 = _inputs(61, 1, 200, 1, 2, 64, 40, dtype)
+    args[3][:, 50:90] = 0.0
+    args[3][:, 128] = 0.0
+    dO = _randn(9, *args[2].shape, dtype=dtype)
+    _, _, dv, db, _, _ = _check_backward(args, _rows(1, 200), 1.0, S0, dO, None, dtype)
+    assert not dv[:, 50:90].any() and not dv[:, 128].any() and dv[:, 49].any() and db[:, 50:90].any()
+    # and steps of any size
+    args[3][:, 50:90], args[3][:, 128] = 1e-12, 3e4
+    args[1][:, 128] = 0.0
+    _, S = K.fwd_delta(*args, initial_state=S0, return_state=True)
+    _check_forward(args, _rows(1, 200), 1.0, S0, None, S, dtype)
+    db = K.bwd_delta(*args[:4], dO, args[4], initial_state=S0)[3]
+    assert torch.isfinite(db).all() and db[:, 50:90].any()
+
+
+@pytest.mark.parametrize("at", [130, 511, 640, 999])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_delta_non_finite_tokens_in_segments(dtype, at):
+    *args, S0 = _inputs(62, 1, 1000, 2, 2, 64, 64, dtype)
+    clean, cleanS = K.fwd_delta(*args, initial_state=S0, return_state=True)
+    for which, value in (("v", float("nan")), ("v", float("inf")), ("k", float("nan")), ("beta", float("inf")), ("ld", float("nan"))):
+        bad = [x.clone() for x in args]
+        i = "q k v beta ld".split().index(which)
+        bad[i][(0, at, 0) + ((5,) if i < 3 else ())] = value
+        o, S = K.fwd_delta(*bad, initial_state=S0, return_state=True)
+        assert torch.equal(o[:, :at], clean[:, :at]), which
+        assert torch.equal(o[:, :, 1], clean[:, :, 1]) and torch.equal(S[:, 1], cleanS[:, 1]), which
+        if which == "v":
+            cols = [c for c in range(64) if c != 5]
+            assert torch.isnan(o[0, at:, 0, 5]).all() and torch.isnan(S[0, 0, :, 5]).all()
+            assert torch.equal(o[0, :, 0][:, cols], clean[0, :, 0][:, cols]) and torch.equal(S[0, 0][:, cols], cleanS[0, 0][:, cols])
+        else:
+            assert not torch.isfinite(o[0, at:, 0]).any() and not torch.isfinite(S[0, 0]).any(), which
+
+
 def test_delta_keys_that_repeat():
     # one key over and over: the system is as far from the unit matrix as it gets
     q, k, v, b, ld, S0 = _inputs(12, 1, 200, 1, 1, 64, 64, F32, gated=False)
