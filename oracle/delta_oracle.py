@@ -10,8 +10,8 @@ Per head (T, d) arrays, b = beta (T,), ld = log decays (T,), g = exp(ld):
 
 import numpy as np
 
-__all__ = ["delta_recurrent", "delta_backward", "delta_chunked", "delta_sizes", "delta_gradient_sizes", "turn", "qk_norm",
-           "qk_norm_backward"]
+__all__ = ["delta_recurrent", "delta_backward", "delta_chunked", "delta_sizes", "delta_gradient_sizes", "delta_token_sizes",
+           "delta_chunked_backward", "turn", "qk_norm", "qk_norm_backward"]
 
 
 def _decay(ld):
@@ -110,6 +110,70 @@ def delta_gradient_sizes(q, k, v, b, ld, dO, scale=1.0, S0=None, dS=None, C=64):
         terms = (G * np.abs(o[t:e])).sum(1) + (dV * np.abs(v[t:e])).sum(1)
         Bl[t:e] = np.cumsum(terms[::-1])[::-1] + (np.abs(D) * np.abs(states[e - 1])).sum()
     return Bq, Bk, Bl
+
+
+def delta_token_sizes(q, k, v, b, ld, dO, scale=1.0, S0=None, dS=None):
+    """What the roundings of a token's factors are relative to, by token (T,): products of the norms of what is
+    multiplied there, for o, dq, dk, dv, db, dld, and for the whole sequence of the final state and dS0.  The state
+    and its gradient enter as they are at the token, so the sizes fade with the decays."""
+    T, norm = len(q), lambda x: np.sqrt((x * x).sum(-1))  # noqa: E731
+    _, S, states = delta_recurrent(q, k, v, b, ld, scale, S0, keep=True)
+    g = _decay(ld)
+    first = np.zeros((q.shape[1], v.shape[1])) if S0 is None else S0.astype(float)
+    D = np.zeros_like(first) if dS is None else dS.astype(float).copy()
+    at, before = np.empty(T), np.empty(T)
+    for t in range(T - 1, -1, -1):
+        D = D + scale * np.outer(q[t], dO[t])
+        at[t] = np.linalg.norm(D)
+        before[t] = np.linalg.norm(g[t] * (states[t - 1] if t else first))
+        D = g[t] * (D - b[t] * np.outer(k[t], k[t] @ D))
+    b, nk, nq, s = np.abs(b), norm(k), norm(q), abs(scale)
+    err = norm(v) + nk * before
+    behind = before * (1 + b * nk * nk) + b * nk * err
+    last = np.linalg.norm(S) + (max(behind[-1], np.linalg.norm(first) * g[0] if T == 1 else 0.0) if T else 0.0)
+    return dict(o=s * nq * behind, dq=s * norm(dO) * behind, dk=at * b * err + before * b * nk * at, dv=b * nk * at, db=nk * at * err,
+                dld=at * before * (1 + b * nk * nk), state=last,
+                dS0=np.linalg.norm(D) + (g[0] * at[0] * (1 + b[0] * nk[0] ** 2) if T else 0.0))
+
+
+def delta_chunked_backward(q, k, v, b, ld, dO, scale=1.0, S0=None, dS=None, C=64, without=""):
+    """(dq, dk, dv, db, dld, dS0) by the chunked formulas, without one of their terms where `without` names it:
+    dq "state" "pairs"; dk "correction", "state", "scores", "keys", "rows"; dld "state", "read", "write", "pairs"; db
+    and dv "inverse" (as if the chunk's tokens had no pairs)."""
+    T, names = len(q), [(t, min(t + C, len(q))) for t in range(0, len(q), C)]
+    first = np.zeros((q.shape[1], v.shape[1])) if S0 is None else S0.astype(float)
+    D = np.zeros_like(first) if dS is None else dS.astype(float).copy()
+    entries, S = [], first
+    for t, e in names:
+        entries.append(S)
+        S = delta_recurrent(q[t:e], k[t:e], v[t:e], b[t:e], ld[t:e], scale, S)[1]
+    out = [np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape), np.zeros(T), np.zeros(T)]
+    keep = lambda name: 0.0 if name == without else 1.0  # noqa: E731
+    for (t, e), S in zip(names[::-1], entries[::-1]):
+        Q, K, V, B, G = q[t:e], k[t:e], v[t:e], b[t:e, None], dO[t:e]
+        n, c = e - t, np.cumsum(ld[t:e])
+        r = np.exp(np.minimum(c[:, None] - c, 0.0)) * np.tri(n)
+        y, left = np.exp(c)[:, None], np.exp(c[-1] - c)[:, None]
+        A = np.tril(r, -1) * (K @ K.T)
+        E = np.linalg.solve(np.eye(n) + A * B.T, V - y * (K @ S))          # U = B E
+        U = B * E
+        P = scale * r * (Q @ K.T)
+        Z = P.T @ G + left * (K @ D)
+        X = Z if without == "db inverse" else np.linalg.solve((np.eye(n) + B * A).T, Z)
+        dV = B * X
+        PO, PV = scale * r * (G @ U.T), -np.tril(r, -1) * (dV @ U.T)
+        out[0][t:e] = keep("dq state") * scale * y * (G @ S.T) + keep("dq pairs") * PO @ K
+        out[1][t:e] = (keep("dk correction") * left * (U @ D.T) - keep("dk state") * y * (dV @ S.T) + keep("dk scores") * PO.T @ Q
+                       + keep("dk keys") * PV.T @ K + keep("dk rows") * PV @ K)
+        out[2][t:e], out[3][t:e] = dV, (X * E).sum(1)
+        # by token: what reaches over its decay, from the tokens before it (and the state) to it and those behind (and D)
+        F = keep("dld pairs") * (PO * (Q @ K.T) + PV * (K @ K.T))
+        read = keep("dld read") * (y * (scale * (G * (Q @ S)) - dV * (K @ S))).sum(1)
+        write = keep("dld write") * left[:, 0] * (U * (K @ D)).sum(1)
+        for i in range(n):
+            out[4][t + i] = F[i:, :i].sum() + read[i:].sum() + write[:i].sum() + keep("dld state") * y[-1, 0] * (D * S).sum()
+        D = y[-1] * D + scale * (y * Q).T @ G - (y * K).T @ dV
+    return (*out, D)
 
 
 def turn(x, angles, interleaved=False, magnitude=1.0, inverse=False):
