@@ -485,7 +485,7 @@ size_t kata_bwd_delta_workspace_size(const kata_delta_problem* pr);
 /* Gradients of sum(dO * o) + sum(dfinal_state * final_state) in q, k [B][T][Hk][dk] (summed over the value
  * heads that share them), v [B][T][H][dv], beta [B][T][H] of dtype, and log_decay fp32 [B][T][H]
  * (dlog_decay NULL: not wanted), all contiguous, and where dinitial_state is not NULL, the initial state.
- * Rows of no sequence get zeros.  A |beta| below 1e-15 counts as zero.  initial_state and dfinal_state: nullable (zero); dinitial_state overlaps
+ * Rows of no sequence get zeros.  initial_state and dfinal_state: nullable (zero); dinitial_state overlaps
  * neither. */
 kata_status kata_bwd_delta(const kata_delta_problem* pr, const void* q, const void* k, const void* v,
                            const void* beta, const float* log_decay, const void* dO, const int32_t* cu_seqlens,

@@ -34,7 +34,7 @@ struct DeltaArgs {
   float* cstates;                         // backward: [c_slots][H][DK][DV] entry states of the chunks, in registers' order
   float* rstates;                         // backward: the gradient of the state behind each chunk
   float *pq, *pk;                         // backward, or null: [b][t][H][dk], dq and dk by value heads
-  float *u, *x;                           // backward: [c_slots][H][DV][64] U of the chunks, and dv, in registers' order
+  float *u, *x;                           // backward: [c_slots][H][DV][64] U of the chunks, and X (dv = b X), in registers' order
   float* fstates;                         // backward with dfin: [n_seq][H], as cstates, the final states
   // states
   const float *init, *dfin;               // [n_seq][H][dk][dv] or null
@@ -44,7 +44,7 @@ struct DeltaArgs {
   float* dlog;
 };
 
-hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st);
+hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, hipStream_t st);
 // The segments' sums and transitions; their sums become entry states; the outputs.
 hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, hipStream_t st);
 hipError_t launch_delta_join(const DeltaArgs& a, bool backward, hipStream_t st);

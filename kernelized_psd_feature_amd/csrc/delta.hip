@@ -53,7 +53,7 @@ struct PrepTiles {
 };
 
 template <typename T, int DK>
-__global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int backward) {
+__global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
   using TL = PrepTiles<T, DK>;
   using frag = typename Elem<T>::frag;
   constexpr int M = DK / 32, LK = TL::LK, LD = TL::LD;
@@ -90,8 +90,6 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A, int b
       b = to_f32(reinterpret_cast<const T*>(A.beta)[row_off(A.sb, s.b, row0 + lane, h)]);
       if (A.log_decay) ld = A.log_decay[row_off(A.sl, s.b, row0 + lane, h)];
       if (ld < -256.f) ld = -256.f;                 // exp of it is zero in fp32; sums of 64 stay finite
-      // X U / b^2 is wanted there: a factor of 1e-15 is as good as none, and can be taken out again
-      if (backward && fabsf(b) < 1e-15f) b = copysignf(1e-15f, b);
     }
     double c = ld * 1.4426950408889634;
 #pragma unroll
@@ -412,12 +410,11 @@ hipError_t with_lds(F kernel, int bytes) {
 }
 
 template <typename T, int DK>
-hipError_t launch_prep_t(const DeltaArgs& a, bool backward, hipStream_t st) {
+hipError_t launch_prep_t(const DeltaArgs& a, hipStream_t st) {
   using TL = PrepTiles<T, DK>;
   hipError_t e = with_lds(delta_prep_kernel<T, DK>, TL::bytes);
   if (e != hipSuccess) return e;
-  launch_kernel(delta_prep_kernel<T, DK>, grid_rows((long long)a.m.c_slots * a.m.H), kThreads, TL::bytes, st, a,
-                backward ? 1 : 0);
+  launch_kernel(delta_prep_kernel<T, DK>, grid_rows((long long)a.m.c_slots * a.m.H), kThreads, TL::bytes, st, a);
   return hipGetLastError();
 }
 
@@ -458,12 +455,12 @@ hipError_t launch_walk_d(const DeltaArgs& a, bool bf16, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, bool backward, hipStream_t st) {
+hipError_t launch_delta_prep(const DeltaArgs& a, bool bf16, hipStream_t st) {
   const int dk = a.m.dk;
-  if (bf16) return dk <= 32 ? launch_prep_t<__bf16, 32>(a, backward, st)
-                 : dk <= 64 ? launch_prep_t<__bf16, 64>(a, backward, st) : launch_prep_t<__bf16, 128>(a, backward, st);
-  return dk <= 32 ? launch_prep_t<float, 32>(a, backward, st)
-         : dk <= 64 ? launch_prep_t<float, 64>(a, backward, st) : launch_prep_t<float, 128>(a, backward, st);
+  if (bf16) return dk <= 32 ? launch_prep_t<__bf16, 32>(a, st)
+                 : dk <= 64 ? launch_prep_t<__bf16, 64>(a, st) : launch_prep_t<__bf16, 128>(a, st);
+  return dk <= 32 ? launch_prep_t<float, 32>(a, st)
+         : dk <= 64 ? launch_prep_t<float, 64>(a, st) : launch_prep_t<float, 128>(a, st);
 }
 
 hipError_t launch_delta_segments(const DeltaArgs& a, bool bf16, hipStream_t st) {

@@ -112,7 +112,7 @@ void place(kata::DeltaArgs& a, const kata::DeltaPlan& p, void* workspace) {
 kata_status run_before(const kata::DeltaArgs& a, bool bf16, bool backward, hipStream_t st, const char* what) {
   {
     Timed t(KATA_K_CHUNK_STATE, st);
-    hipError_t e = kata::launch_delta_prep(a, bf16, backward, st);
+    hipError_t e = kata::launch_delta_prep(a, bf16, st);
     if (e == hipSuccess && a.m.n_seg > 1)
       e = backward ? kata::launch_delta_bwd_walk(a, bf16, true, st) : kata::launch_delta_segments(a, bf16, st);
     if (e != hipSuccess) return launch_status(e, what);

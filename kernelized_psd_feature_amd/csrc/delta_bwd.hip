@@ -4,7 +4,7 @@
 //   Z = P^T dO scale + diag(exp(c_63 - c)) K D          (the gradient of U)
 //   X = (I + A)^-T Z,  dv = diag(b) X
 //   the gradient of S:  y_63 D + scale (diag(y) Q)^T dO - (diag(y) K)^T dv
-//   dbeta_i = X_i . U_i / b_i
+//   dbeta_i = X_i . (v_i - y_i S^T k_i - sum_{j < i} exp(c_i - c_j) (k_i . k_j) u_j), which needs no division by b
 //   dlog_t = sum_{i >= t in the chunk} (dO_i . o_i - dv_i . v_i) + <D, S'>,  S' the state behind the chunk
 //   PO_ij = scale exp(c_i - c_j) (dO_i . u_j) for j <= i,  PV_ij = -exp(c_i - c_j) (dv_i . u_j) for j < i
 //   dq = scale diag(y) dO S^T + PO K
@@ -12,7 +12,7 @@
 // (dlog: what <D, S> changes by at a token is known from its products with the gradients, dv . v - dO . o; and
 // dO . o is q . dq, a head's part of it.)
 //
-// S and U, and D and dv, come from two walks like the forward pass's, one of them in reversed time, which keep
+// S and U, and D and X, come from two walks like the forward pass's, one of them in reversed time, which keep
 // them for every chunk; all the rest is then computed for all chunks at once (delta_grads_kernel).
 //
 // 8 x 4096 tokens of 16 bf16 heads of 64: inverses 47 us, both walks 297, gradients 370; the bytes that the three
@@ -64,6 +64,9 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
   // (locals: what lambdas read out of the arguments ended in scratch, whose loads wait for all others)
   const float scale = A.scale;
   const float* const at_vec = A.vec;
+  const float* const at_inv = A.inv;
+  float* const at_x = A.x;
+  float* const at_states = A.rstates;
   const int tid = threadIdx.x;
   int lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   auto forget = [&]() __attribute__((always_inline)) {                 // (see the walk)
@@ -112,7 +115,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
     rk.p -= 2 * kC * A.sk[1];
     rq.p -= 2 * kC * A.sq[1];
     ro.p -= 2 * kC * A.sdo[1];
-    ri.fetch(A.inv + (chunk0 + (long long)c * m.H) * kInvFloats);
+    ri.fetch(at_inv + (chunk0 + (long long)c * m.H) * kInvFloats);
     vec_next = fetch_vec(at_vec + (chunk0 + (long long)c * m.H) * kDeltaVec);
   };
   fetch(behind - 1);
@@ -143,7 +146,7 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
     ri.put(sT);
     put_vec(vec, vec_next);
     if (!kSums && live_tile) {
-      float* dst = A.rstates + ((chunk0 + (long long)c * m.H) * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
+      float* dst = at_states + ((chunk0 + (long long)c * m.H) * ct + c0 / 16 + w) * (DK * 16) + lane * 4;
 #pragma unroll
       for (int i = 0; i < NS; ++i) *reinterpret_cast<f32x4*>(dst + i * 256) = D[i];
     }
@@ -235,13 +238,15 @@ __device__ __forceinline__ void delta_reverse(const DeltaArgs& A, unsigned unit,
       });
     }
     Op<T, NT> kw[2], qw[2];
-    float* const px = A.x + ((chunk0 + (long long)c * m.H) * ct + c0 / 16 + w) * 1024 + lane * 4;
+    if (!kSums && live_tile) {
+      float* const px = at_x + ((chunk0 + (long long)c * m.H) * ct + c0 / 16 + w) * 1024 + lane * 4;
+#pragma unroll
+      for (int it = 0; it < 4; ++it) *reinterpret_cast<f32x4*>(px + it * 256) = X[it];
+    }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const f32x4 yv = *reinterpret_cast<const f32x4*>(vec + 16 * it + 4 * g);
-      X[it] *= *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);      // dv
-      if (!kSums && live_tile) *reinterpret_cast<f32x4*>(px + it * 256) = X[it];
-      X[it] *= -yv;
+      X[it] *= -yv * *reinterpret_cast<const f32x4*>(vec + 2 * kC + 16 * it + 4 * g);
       Z[it] = half_of(of[it >> 1], it & 1) * yv * scale;
     }
 #pragma unroll
@@ -293,7 +298,7 @@ __global__ __launch_bounds__(64 * W, (sizeof(T) == 4 && DK == 128 ? 1 : 2)) void
 
 // ---- the gradients ------------------------------------------------------------------------------
 // One workgroup of eight waves for a chunk and a head of q and k, over the value heads that share it (few chunks: for
-// each value head) and blocks of 64 value columns, then for another chunk.  U, dv and the states, which the walks
+// each value head) and blocks of 64 value columns, then for another chunk.  U, X and the states, which the walks
 // have left in tiles of 16 columns, go through LDS, [column][token] and [column][row of the state]; a wave has 16
 // tokens, four of the waves P's gradient and half of the columns of dq and dk, the others that of the system's
 // matrix and the other half.
@@ -305,14 +310,14 @@ struct GradTiles {
   static constexpr bool kBf = sizeof(T) == 2;
   static constexpr int PAD = 16 / (int)sizeof(T);
   static constexpr int LK = DK + PAD, LP = kC + PAD, LS = DK + PAD;
-  static constexpr int kHead = 16 + kDeltaVec * 4 + 3 * kC * 4 + 16;   // an int, vec, dots and sums of the waves
-  // Terms of U, dv, S and PO, and how many of them enter dk, as of D and PV.  The dots dO . o and dv . v cancel in
+  static constexpr int kHead = 16 + kDeltaVec * 4 + 4 * kC * 4 + 16;   // an int, vec, dots and sums of the waves
+  // Terms of U, X, S and PO, and how many of them enter dk, as of D and PV.  The dots dO . o and dv . v cancel in
   // dlog: with two terms it was off by 2e-6 to 1e-5 of its norm, with three by 5e-7 to 1.6e-6.
   static constexpr int N = kBf ? 3 : 1, N2 = kBf ? 2 : 1;
   static constexpr int kPlane = 64 * LP, kState = 64 * LS;
   // The next chunk's operands are loaded ahead, and D has a place of its own, where registers and LDS are there.
   static constexpr bool kAhead = DK <= 64;
-  // K and Q; U and dv, then PO and PV; S (and D)
+  // K and Q; U and X, then PO and PV; S (and D)
   static constexpr int bytes = kHead + (2 * kC * LK + 2 * N * kPlane + (N + (kAhead ? N2 : 0)) * kState) * (int)sizeof(T);
 };
 template <int K, typename T, int N>
@@ -382,11 +387,12 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   int* const sh = reinterpret_cast<int*>(lds);
   float* const vec = reinterpret_cast<float*>(lds + 16);
   const float* const sc = vec + 3 * kC;
-  float* const sE = vec + kDeltaVec;                // [2][64] q . dq - dv . v in parts; then [64] dv . U
-  float* const sF = sE + 3 * kC;                    // [4] <D, S'>
+  const float* const sb = vec + 2 * kC;
+  float* const sE = vec + kDeltaVec;                // [2][64] each of q . dq - dv . v and of dbeta in parts
+  float* const sF = sE + 4 * kC;                    // [4] <D, S'>
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
   T* const sQ = sK + kC * LK;
-  T* const sU = sQ + kC * LK;                       // N planes each of U and dv, then of PO and (N2) PV
+  T* const sU = sQ + kC * LK;                       // N planes each of U and X, then of PO and (N2) PV
   T* const sZ = sU + N * PL;
   T* const sS = sZ + N * PL;                        // N planes of S, N2 of D
   T* const sD = kAhead ? sS + N * PS : sS;
@@ -457,7 +463,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     return false;
   };
 
-  // What is loaded for a place: a wave's 16 columns of U and S, or of dv, D and S' (the state behind the chunk); its 16
+  // What is loaded for a place: a wave's 16 columns of U and S, or of X, D and S' (the state behind the chunk); its 16
   // tokens' dO and (half of the columns) v; all together the chunk's rows and vectors.
   Stage<T, DK, kThreads> rk(nullptr, 0, m.dk, true), rq(nullptr, 0, m.dk, true);
   f32x4 x[4], S[NS], Sn[kAhead ? NS : 1];
@@ -524,8 +530,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   if constexpr (kAhead) load(now);
 
   f32x4 dqa[NH], dka[NH];                           // [row 16 (i0 + i) + 4 g + r][token 16 w + l16]
-  f32x4 Wt[4], dqh[NH];                             // the strip of dO U^T (second half: dv U^T), transposed; the head's dq
-  float frob = 0.f, e = 0.f;
+  f32x4 Wt[4], dqh[NH];                             // the strip of dO U^T (second half: X U^T), transposed; the head's dq
+  float frob = 0.f, xv = 0.f, xe = 0.f;             // X . v, and dbeta without it, in parts
   const int i0 = first_half ? 0 : NH;
 #pragma unroll 1
   while (more) {
@@ -534,7 +540,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     const long long lead = ((long long)now.s.b * m.T + now.row0) * m.H + h;    // of [b][t][H]
     const bool live_row = row < now.n;
     if (now.vb == 0) {
-      frob = e = 0.f;
+      frob = xv = xe = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) Wt[i] = zero4();
 #pragma unroll
@@ -603,12 +609,20 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     for (int i = 0; i < 2; ++i) z[i] = value_op<N, LP>(sZ + 32 * i * LP + 16 * w, PL, lane);
     if (live_row) {                                 // dv, half of the columns each
       T* const dst = reinterpret_cast<T*>(A.dv) + (lead + (long long)row * m.H) * m.dv + c0;
-      frag dv = first_half ? z[0].t[0] : z[1].t[0];
-      if (fabsf(vec[2 * kC + row]) <= 1e-15f) dv = frag{};             // beta was nothing (delta_prep_kernel)
-      store_row(dst + (first_half ? 0 : 32), m.dv - c0 - (first_half ? 0 : 32), g, dv);
+      auto store = [&](const Op<T, N>& x, int to) __attribute__((always_inline)) {
+        f32x4 lo = zero4(), hi = zero4();
+#pragma unroll
+        for (int t = N - 1; t >= 0; --t) {
+          lo += half_of(x.t[t], 0);
+          hi += half_of(x.t[t], 1);
+        }
+        store_row(dst + to, m.dv - c0 - to, g, pack_frag(sb[row] * lo, sb[row] * hi, T()));
+      };
+      if (first_half) store(z[0], 0);
+      else store(z[1], 32);
     }
 #pragma unroll
-    for (int t = 0; t < N; ++t) e -= first_half ? dot(z[0].t[t], vc) : dot(z[1].t[t], vc);
+    for (int t = 0; t < N; ++t) xv += first_half ? dot(z[0].t[t], vc) : dot(z[1].t[t], vc);
 #pragma unroll
     for (int j0 = 0; j0 < 4; j0 += 2)
       if (j0 <= w)                                  // uniform (a tile above the diagonal is not looked at)
@@ -632,7 +646,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
         }
     forget();
     {
-      const float yr = vec[16 * w + l16], yo = yr * A.scale;
+      const float yr = vec[16 * w + l16], yo = yr * A.scale, yb = yr * sb[16 * w + l16];
 #pragma unroll
       for (int ia = 0; ia < NH; ia += G) {
         f32x4 a[G], b[G];
@@ -655,7 +669,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 #pragma unroll
         for (int p = 0; p < G; ++p) {
           dqh[ia + p] += a[p] * yo;
-          dka[ia + p] -= b[p] * yr;
+          dka[ia + p] -= b[p] * yb;
+          const f32x4 y = unquad(*reinterpret_cast<const Quad<T>*>(sK + (16 * w + l16) * LK + split_place(16 * (i0 + ia + p) + 4 * g))) * b[p];
+          xe -= yr * (y[0] + y[1] + y[2] + y[3]);
         }
       }
     }
@@ -691,7 +707,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       now = next;
       continue;
     }
-    if constexpr (kAhead) __syncthreads();          // U and dv have been read
+    if constexpr (kAhead) __syncthreads();          // U and X have been read
     // PO or PV, the wave's strip of rows
     forget();
     {
@@ -701,24 +717,27 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f32x4 p = zero4();
-        if (j <= w)
+        if (j <= w) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int key = 16 * j + 4 * g + r;
             p[r] = key >= end ? 0.f : Wt[j][r] * (exp2_diff(hi, lo, sc[key], sc[kC + key]) * factor);
           }
+          if (!first_half) {
+            f32x4 kk = zero4();
+#pragma unroll
+            for (int i = 0; i < DK / 32; ++i)
+              kk = mma(row_frag(sK + (16 * j + l16) * LK + 32 * i + 8 * g), row_frag(sK + (16 * w + l16) * LK + 32 * i + 8 * g), kk);
+            kk *= p;
+            xe += kk[0] + kk[1] + kk[2] + kk[3];
+            p *= sb[16 * w + l16];
+          }
+        }
         if (first_half) put_terms<N>(at + split_place(16 * j + 4 * g), PL, p);
         else put_terms<N2>(at + split_place(16 * j + 4 * g), PL, p);
       }
     }
-    if (!first_half) {                              // the diagonal of dv U^T
-      float d = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (j == w && 4 * g + r == l16) d = Wt[j][r];
-      if (l16 >> 2 == g) sE[2 * kC + 16 * w + l16] = d;
+    if (!first_half) {
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
       if (lane == 0) sF[w] = frob;
@@ -758,6 +777,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
         }
       }
     // dO . o = q . dq of this head
+    float e = -sb[row] * xv;
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       const f32x4 y = unquad(*reinterpret_cast<const Quad<T>*>(sQ + (16 * w + l16) * LK + split_place(16 * (i0 + i) + 4 * g))) * dqh[i];
@@ -766,12 +786,17 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     }
     e += __shfl_xor(e, 16);
     e += __shfl_xor(e, 32);
-    if (lane < 16) sE[(first_half ? 0 : kC) + 16 * w + lane] = e;
+    xe += xv;
+    xe += __shfl_xor(xe, 16);
+    xe += __shfl_xor(xe, 32);
+    if (lane < 16) {
+      sE[(first_half ? 0 : kC) + 16 * w + lane] = e;
+      sE[(first_half ? 2 : 3) * kC + 16 * w + lane] = xe;
+    }
     __syncthreads();
     if (wave == 0) {
       const long long at = lead + (long long)lane * m.H;
-      const float b = vec[2 * kC + lane];
-      if (lane < now.n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[2 * kC + lane] / b / b);
+      if (lane < now.n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[2 * kC + lane] + sE[3 * kC + lane]);
       if (A.dlog) {
         double y = (double)sE[lane] + sE[kC + lane];
 #pragma unroll

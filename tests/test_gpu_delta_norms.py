@@ -80,7 +80,7 @@ def test_many_packed_sequences(dtype):
 
 
 @pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("beta", [1.0, 2.0, "mixed"])
+@pytest.mark.parametrize("beta", [0.0, 1.0, 2.0, "mixed"])
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 def test_beta_over_its_range(dtype, beta, gated):
     args = N.inputs(8, 1, 260, 2, 2, 64, 64, dtype)
@@ -116,3 +116,32 @@ def test_steps_of_any_size(dtype, beta):
     if beta < 0:                                     # the state grows along a key: by a factor of 2.5 each time
         args[3][:, 10:] = 0.0
     _check(args, N.rows(1, 200), 1.0, dtype=dtype)
+
+
+@pytest.mark.parametrize("shape", [(1, 150, 2, 2, 64, 64), (1, 150, 1, 2, 128, 128), (2, 90, 1, 3, 32, 40)])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_gradients_scale_with_what_arrives(dtype, shape):
+    # linear in dO, down to 2^-66, about 1e-20, and where beta is zero, too.  A power of two changes no rounding; what it
+    # takes below fp32's range is less than 2^-126 2^66 of what it is added to.  Two results are a step apart at most.
+    args = N.inputs(31, *shape, dtype)
+    args[3][:, 20:60:3], args[3][:, 64:70], args[3][:, 80] = 0.0, 1e-9, 1e-12
+    args[7] = None
+    whole = _run(args, forward=False)
+    assert whole["db"][:, 20:60:3].any()
+    for power in (-10, -30, -66):
+        less = _run([*args[:5], (args[5].double() * 2.0 ** power).to(dtype), *args[6:]], forward=False)
+        for name, x in whole.items():
+            x = x.double()
+            half = N.HALF[F32 if name in N.IN_FP32 else dtype]
+            few = 2.0 ** -60 if power > -66 else 2.0 ** -24
+            off = (less[name].double() * 2.0 ** -power - x).abs() - 2 * half * x.abs() - few * x.norm() / x.numel() ** 0.5
+            assert off.max() <= 0, (name, power, float(off.max()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_tokens_that_write_nothing_leave_no_gradient(dtype):
+    # u is zero there: no gradient of v, and none of k but through the state that it would read and correct
+    args = N.inputs(8, 1, 150, 2, 2, 64, 64, dtype)
+    args[3].zero_()
+    got = _run(args, forward=False)
+    assert not got["dk"].any() and not got["dv"].any() and got["db"].any()
