@@ -295,6 +295,7 @@ __device__ __forceinline__ void join(const DeltaArgs& A, int sub, int h, int seq
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         S[i] = N[s][i] + odd[i];
+        before_branch(S[i]);
         if (m.dk < DK)
 #pragma unroll
           for (int r = 0; r < 4; ++r)

@@ -123,6 +123,15 @@ __device__ __forceinline__ float sum_xor32(float x) {
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
+// Keeps what x is computed from ahead of a branch.  The compiler counts the instructions between a matrix instruction and
+// the first reader of its result, and waits for what is missing, but looks at a block once: where a branch may skip one
+// that is long enough, readers behind it are taken to be late on the short way, too, and read what was there before.  x is
+// what an ordinary instruction made of the result, a sum or a product, not the result itself.
+template <typename X>
+__device__ __forceinline__ void before_branch(X& x) {
+  asm volatile("" : "+v"(x));
+}
+
 // ---- non-finite values and masked P.V products ------------------------------------------
 // Inside an MFMA P.V product a masked weight P_ts = 0 still meets the value v_s of every key of
 // the K step, and 0 * inf or 0 * nan is nan: a non-finite value of a later token would reach
