@@ -5,12 +5,20 @@
 //   X = (I + A)^-T Z,  dv = diag(b) X
 //   the gradient of S:  y_63 D + scale (diag(y) Q)^T dO - (diag(y) K)^T dv
 //   dbeta_i = X_i . (v_i - y_i S^T k_i - sum_{j < i} exp(c_i - c_j) (k_i . k_j) u_j), which needs no division by b
-//   dlog_t = sum_{i >= t in the chunk} (dO_i . o_i - dv_i . v_i) + <D, S'>,  S' the state behind the chunk
+//   dlog_t = sum_{i >= t in the chunk} (dO_i . o_i - dv_i . v_i) + <D, S'>,  S' the state behind the chunk; or
+//   dlog_t = sum_{i >= t > j} F_ij + sum_{i >= t} R_i + sum_{j < t} W_j + y_63 <D, S>,  where
+//     F_ij = PO_ij (q_i . k_j) + PV_ij (k_i . k_j),  R_i = y_i (scale dO_i . S^T q_i - dv_i . S^T k_i),
+//     W_j = exp(c_63 - c_j) (u_j . D^T k_j)
 //   PO_ij = scale exp(c_i - c_j) (dO_i . u_j) for j <= i,  PV_ij = -exp(c_i - c_j) (dv_i . u_j) for j < i
 //   dq = scale diag(y) dO S^T + PO K
 //   dk = diag(exp(c_63 - c)) U D^T - diag(y) dv S^T + PO^T Q + PV^T K + PV K
 // (dlog: what <D, S> changes by at a token is known from its products with the gradients, dv . v - dO . o; and
-// dO . o is q . dq, a head's part of it.)
+// dO . o is q . dq, a head's part of it.  The second form is what reaches over the token's decay, from the tokens and the state
+// before it to those behind, every term with that decay for a factor.  Of a strong decay the first one's terms, which have it
+// not, leave only their roundings: mean log decays of -1, -5, -10, -20 are off by 2e-6, 3e-5, 4e-4, 0.3 of the norm in bf16 (fp32 2e-6,
+// 6e-5, 1e-3, 0.4), by the second form by 4e-7 to 7e-7 (fp32 2e-7 to 4e-7).  Weak ones are as good by the first (-0.02: 9e-7,
+// by the second 3e-6, of operands in two terms), and for less work: 8 x 4096 tokens 718 us, 754 by the second.  So the second is
+// for chunks in which any token's decay is below exp(-1/2).)
 //
 // S and U, and D and X, come from two walks like the forward pass's, one of them in reversed time, which keep
 // them for every chunk; all the rest is then computed for all chunks at once (delta_grads_kernel).
@@ -310,7 +318,7 @@ struct GradTiles {
   static constexpr bool kBf = sizeof(T) == 2;
   static constexpr int PAD = 16 / (int)sizeof(T);
   static constexpr int LK = DK + PAD, LP = kC + PAD, LS = DK + PAD;
-  static constexpr int kHead = 16 + kDeltaVec * 4 + 4 * kC * 4 + 16;   // an int, vec, dots and sums of the waves
+  static constexpr int kHead = 16 + kDeltaVec * 4 + (6 + 8) * kC * 4 + 16;                     // an int, vec, sums of the waves
   // Terms of U, X, S and PO, and how many of them enter dk, as of D and PV.  The dots dO . o and dv . v cancel in
   // dlog: with two terms it was off by 2e-6 to 1e-5 of its norm, with three by 5e-7 to 1.6e-6.
   static constexpr int N = kBf ? 3 : 1, N2 = kBf ? 2 : 1;
@@ -368,6 +376,25 @@ __device__ __forceinline__ Op<T, N> value_op(const T* p, int plane, int lane) {
   for (int i = 0; i < N; ++i) x.t[i] = value_column<LD>(p + i * plane, lane);
   return x;
 }
+// x of the lane whose number differs in bit 4 (5)
+__device__ __forceinline__ float other_16(float x) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(threadIdx.x & 16 ? p[0] : p[1]);
+}
+__device__ __forceinline__ float other_32(float x) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(threadIdx.x & 32 ? p[0] : p[1]);
+}
+// the sum over the 16 lanes of a row of them
+__device__ __forceinline__ float sum_16(float x) {
+  const auto turned = [](float y, auto by) __attribute__((always_inline)) {              // row_ror
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, y), 0x120 + decltype(by)::value, 0xf, 0xf, true));
+  };
+  x += turned(x, std::integral_constant<int, 8>());
+  x += turned(x, std::integral_constant<int, 4>());
+  x += turned(x, std::integral_constant<int, 2>());
+  return x + turned(x, std::integral_constant<int, 1>());
+}
 // the sum of the products of two operands' elements
 template <typename F>
 __device__ __forceinline__ float dot(const F& a, const F& b) {
@@ -388,8 +415,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   float* const vec = reinterpret_cast<float*>(lds + 16);
   const float* const sc = vec + 3 * kC;
   const float* const sb = vec + 2 * kC;
-  float* const sE = vec + kDeltaVec;                // [2][64] each of q . dq - dv . v and of dbeta in parts
-  float* const sF = sE + 4 * kC;                    // [4] <D, S'>
+  float* const sE = vec + kDeltaVec;                // [2][64] each, in two parts: q . dq - dv . v (or R), dbeta, W
+  float* const sG = sE + 6 * kC;                    // [2][4][64] by the halves' waves: the sums of F
+  float* const sF = sG + 8 * kC;                    // [4] <D, S'> (or <D, S>)
   T* const sK = reinterpret_cast<T*>(lds + TL::kHead);
   T* const sQ = sK + kC * LK;
   T* const sU = sQ + kC * LK;                       // N planes each of U and X, then of PO and (N2) PV
@@ -442,6 +470,11 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       reinterpret_cast<T*>(A.dbeta)[at] = T(0.f);
       if (A.dlog) A.dlog[at] = 0.f;
     }
+  };
+  // a lane's part (of four) of its token's dot with a row of K or Q: 16 columns, x the four of them at 4 g
+  auto row_dot = [&](const T* tile, int columns, const f32x4& x) __attribute__((always_inline)) {
+    const f32x4 y = unquad(*reinterpret_cast<const Quad<T>*>(tile + (16 * w + l16) * LK + split_place(16 * columns + 4 * g))) * x;
+    return y[0] + y[1] + y[2] + y[3];
   };
   // The first unit from p.unit on that has tokens; those before it are zeros' rows, or nothing.
   auto find = [&](Place& p) __attribute__((always_inline)) {
@@ -532,6 +565,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   f32x4 dqa[NH], dka[NH];                           // [row 16 (i0 + i) + 4 g + r][token 16 w + l16]
   f32x4 Wt[4], dqh[NH];                             // the strip of dO U^T (second half: X U^T), transposed; the head's dq
   float frob = 0.f, xv = 0.f, xe = 0.f;             // X . v, and dbeta without it, in parts
+  float frob_in = 0.f, write = 0.f;                 // strong decays: <D, S> and W in parts
+  bool strong = false;
   const int i0 = first_half ? 0 : NH;
 #pragma unroll 1
   while (more) {
@@ -540,7 +575,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     const long long lead = ((long long)now.s.b * m.T + now.row0) * m.H + h;    // of [b][t][H]
     const bool live_row = row < now.n;
     if (now.vb == 0) {
-      frob = xv = xe = 0.f;
+      frob = xv = xe = frob_in = write = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) Wt[i] = zero4();
 #pragma unroll
@@ -604,6 +639,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 
     // a wave's 16 tokens
     forget();
+    const float log2_decay = sc[lane] - (lane ? sc[lane - 1] : 0.f);
     Op<T, N> z[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) z[i] = value_op<N, LP>(sZ + 32 * i * LP + 16 * w, PL, lane);
@@ -670,8 +706,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
         for (int p = 0; p < G; ++p) {
           dqh[ia + p] += a[p] * yo;
           dka[ia + p] -= b[p] * yb;
-          const f32x4 y = unquad(*reinterpret_cast<const Quad<T>*>(sK + (16 * w + l16) * LK + split_place(16 * (i0 + ia + p) + 4 * g))) * b[p];
-          xe -= yr * (y[0] + y[1] + y[2] + y[3]);
+          xe -= yr * row_dot(sK, i0 + ia + p, b[p]);
         }
       }
     }
@@ -684,6 +719,15 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       __syncthreads();
     }
     forget();
+    strong = A.dlog && __any(log2_decay < -0.72f);  // uniform: log2 of exp(-1/2)
+    if (strong && !first_half && 4 * now.vb + w < ct) {
+      const long long tile = (((long long)now.slot * m.H + h) * ct + 4 * now.vb + w) * (DK * 16) + lane * 4;
+#pragma unroll 1
+      for (int i = 0; i < NS; ++i) {
+        const f32x4 y = load4(A.cstates + tile + i * 256) * load4(A.rstates + tile + i * 256);
+        frob_in += y[0] + y[1] + y[2] + y[3];
+      }
+    }
     const float left = vec[kC + 16 * w + l16];
 #pragma unroll
     for (int ia = 0; ia < NH; ia += G) {
@@ -701,7 +745,14 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
         });
       }
 #pragma unroll
-      for (int p = 0; p < G; ++p) dka[ia + p] += a[p] * left;
+      for (int p = 0; p < G; ++p) {
+        a[p] *= left;
+        dka[ia + p] += a[p];
+        before_branch(a[p]);
+      }
+      if (strong)
+#pragma unroll
+        for (int p = 0; p < G; ++p) write += row_dot(sK, i0 + ia + p, a[p]);
     }
     if (now.vb + 1 < v_blocks) {
       now = next;
@@ -710,6 +761,13 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     if constexpr (kAhead) __syncthreads();          // U and X have been read
     // PO or PV, the wave's strip of rows
     forget();
+    const float b_row = first_half ? 1.f : sb[16 * w + l16];
+    float e = 0.f;
+    if (strong) {
+      e = sb[16 * w + l16] * xe;
+#pragma unroll
+      for (int i = 0; i < NH; ++i) e += row_dot(sQ, i0 + i, dqh[i]);
+    }
     {
       const float hi = sc[16 * w + l16], lo = sc[kC + 16 * w + l16], factor = first_half ? A.scale : -1.f;
       const int end = 16 * w + l16 + (first_half ? 1 : 0);             // the first key that it does not reach
@@ -723,26 +781,47 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
             const int key = 16 * j + 4 * g + r;
             p[r] = key >= end ? 0.f : Wt[j][r] * (exp2_diff(hi, lo, sc[key], sc[kC + key]) * factor);
           }
-          if (!first_half) {
-            f32x4 kk = zero4();
-#pragma unroll
-            for (int i = 0; i < DK / 32; ++i)
-              kk = mma(row_frag(sK + (16 * j + l16) * LK + 32 * i + 8 * g), row_frag(sK + (16 * w + l16) * LK + 32 * i + 8 * g), kk);
-            kk *= p;
-            xe += kk[0] + kk[1] + kk[2] + kk[3];
-            p *= sb[16 * w + l16];
-          }
         }
+        Wt[j] = p;
+        p *= b_row;
         if (first_half) put_terms<N>(at + split_place(16 * j + 4 * g), PL, p);
         else put_terms<N2>(at + split_place(16 * j + 4 * g), PL, p);
       }
     }
     if (!first_half) {
+      if (strong) frob = frob_in;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
       if (lane == 0) sF[w] = frob;
     }
     __syncthreads();
+    if (!first_half || strong) {                    // F, of which dbeta wants the sums over the keys
+      const T* const mine = (first_half ? sQ : sK) + (16 * w + l16) * LK + 8 * g;
+      float before = 0.f;                           // F of the row's keys before the tile
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j > w) break;                           // uniform
+        f32x4 f = zero4();
+#pragma unroll
+        for (int i = 0; i < DK / 32; ++i) f = mma(row_frag(sK + (16 * j + l16) * LK + 32 * i + 8 * g), row_frag(mine + 32 * i), f);
+        f *= Wt[j];
+        const float whole = f[0] + f[1] + f[2] + f[3];
+        if (!first_half) xe += whole;
+        if (strong) {
+          // the row's sums over the keys before each key, then for each key those over the rows from it on
+          const float near = other_16(whole), pair = whole + near, far = other_32(pair);
+          f32x4 sum;
+          sum[0] = before + (g & 1 ? near : 0.f) + (g & 2 ? far : 0.f);
+          sum[1] = sum[0] + f[0];
+          sum[2] = sum[1] + f[1];
+          sum[3] = sum[2] + f[2];
+          before += pair + far;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sum[r] = sum_16(j == w && l16 < 4 * g + r ? 0.f : sum[r] * b_row);
+          if (l16 == 0) *reinterpret_cast<f32x4*>(sG + (w + (first_half ? 0 : 4)) * kC + 16 * j + 4 * g) = sum;
+        }
+      }
+    }
 #pragma unroll
     for (int ia = 0; ia < NH; ia += G)
 #pragma unroll
@@ -776,28 +855,43 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
           }
         }
       }
-    // dO . o = q . dq of this head
-    float e = -sb[row] * xv;
-#pragma unroll
     for (int i = 0; i < NH; ++i) {
-      const f32x4 y = unquad(*reinterpret_cast<const Quad<T>*>(sQ + (16 * w + l16) * LK + split_place(16 * (i0 + i) + 4 * g))) * dqh[i];
-      e += y[0] + y[1] + y[2] + y[3];
       dqa[i] += dqh[i];
+      before_branch(dqa[i]);
     }
-    e += __shfl_xor(e, 16);
-    e += __shfl_xor(e, 32);
-    xe += xv;
-    xe += __shfl_xor(xe, 16);
-    xe += __shfl_xor(xe, 32);
+    if (!strong) {                                  // dO . o = q . dq of this head
+      e = -sb[row] * xv;
+#pragma unroll
+      for (int i = 0; i < NH; ++i) e += row_dot(sQ, i0 + i, dqh[i]);
+    }
+    e = sum_xor32(sum_xor16(e));
+    xe = sum_xor32(sum_xor16(xe + xv));
+    if (strong) write = sum_xor32(sum_xor16(write));
     if (lane < 16) {
-      sE[(first_half ? 0 : kC) + 16 * w + lane] = e;
-      sE[(first_half ? 2 : 3) * kC + 16 * w + lane] = xe;
+      float* const at = sE + (first_half ? 0 : kC) + 16 * w + lane;
+      at[0] = e;
+      at[2 * kC] = xe;
+      if (strong) at[4 * kC] = write;
     }
     __syncthreads();
     if (wave == 0) {
       const long long at = lead + (long long)lane * m.H;
       if (lane < now.n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[2 * kC + lane] + sE[3 * kC + lane]);
-      if (A.dlog) {
+      if (strong) {
+        float y = sE[lane] + sE[kC + lane], z = sE[4 * kC + lane] + sE[5 * kC + lane];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const float down = __shfl_down(y, d), up = __shfl_up(z, d);
+          if (lane + d < 64) y += down;
+          if (lane >= d) z += up;
+        }
+        z = __shfl_up(z, 1);                        // of the tokens before
+        y += (lane ? z : 0.f) + vec[kC - 1] * (sF[0] + sF[1] + sF[2] + sF[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i >= lane >> 4) y += sG[i * kC + lane] + sG[(4 + i) * kC + lane];
+        if (lane < now.n) A.dlog[at] = y;
+      } else if (A.dlog) {
         double y = (double)sE[lane] + sE[kC + lane];
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -805,8 +899,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
           if (lane + d < 64) y += up;
         }
         y += (double)sF[0] + sF[1] + sF[2] + sF[3];
-        // a decay of nothing, and one of zero (in fp32), have no gradient
-        const bool none = (now.s.part == 0 && lane == 0 && !A.init) || sc[lane] - (lane ? sc[lane - 1] : 0.f) < -150.f;
+        const bool none = now.s.part == 0 && lane == 0 && !A.init;     // a decay of nothing has no gradient
         if (lane < now.n) A.dlog[at] = none ? 0.f : (float)y;
       }
     }

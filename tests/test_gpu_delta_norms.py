@@ -118,6 +118,16 @@ def test_steps_of_any_size(dtype, beta):
     _check(args, N.rows(1, 200), 1.0, dtype=dtype)
 
 
+@pytest.mark.parametrize("ld", [-1.0, -5.0, -10.0, -20.0, -60.0])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_strong_decays(dtype, ld):
+    # the gradient of a strong decay is small, e^ld of what its neighbours' terms are, and has to be as good as theirs
+    for every in (1, 3):
+        args = N.inputs(23, 1, 256, 1, 2, 64, 64, dtype)
+        args[4][:, ::every] = ld * (0.5 + torch.rand(1, -(-256 // every), 2, generator=torch.Generator().manual_seed(1)))
+        _check(args, N.rows(1, 256), 1.0, dtype=dtype)
+
+
 @pytest.mark.parametrize("shape", [(1, 150, 2, 2, 64, 64), (1, 150, 1, 2, 128, 128), (2, 90, 1, 3, 32, 40)])
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 def test_gradients_scale_with_what_arrives(dtype, shape):
