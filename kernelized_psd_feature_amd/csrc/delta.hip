@@ -176,9 +176,18 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs A) {
         for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], t[k][r], acc, 0, 0, 0);
       }
       const f32x4 d = *reinterpret_cast<const f32x4*>(sD + (16 * bi + l16) * LD + 4 * g);
+      // (a sum that overflows would meet the zeros above D's diagonal: it enters its own row alone)
+      f32x4 over;
       t[i] = zero4();
 #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool fits = fabsf(acc[r]) < __builtin_huge_valf();
+        over[r] = fits ? 0.f : __builtin_nanf("");
+        acc[r] = fits ? acc[r] : 0.f;
+      }
+#pragma unroll
       for (int r = 0; r < 4; ++r) t[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(-d[r], acc[r], t[i], 0, 0, 0);
+      t[i] += over;
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) inv[(bi * (bi + 1) / 2 + w) * 256 + (4 * g + r) * 16 + l16] = t[i][r];

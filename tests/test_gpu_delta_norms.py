@@ -155,3 +155,16 @@ def test_tokens_that_write_nothing_leave_no_gradient(dtype):
     args[3].zero_()
     got = _run(args, forward=False)
     assert not got["dk"].any() and not got["dv"].any() and got["db"].any()
+
+
+@pytest.mark.parametrize("at", [17, 41, 63])
+def test_a_product_that_overflows_reaches_no_earlier_row(at):
+    # k_at . k_5 = 1e23 and k_5 . k_3 = 1e16 are numbers, their product in the inverse is not; the rows before it are as without
+    q, k, v, b, _, _, S0, _ = (x.to(DEV) for x in N.inputs(2, 1, 130, 1, 1, 64, 64, F32))
+    k[0, 5] = k[0, 3]
+    k[0, [3, 5]] *= 1e8
+    clean, _ = K.fwd_delta(q, k, v, b, initial_state=S0, return_state=True)
+    k[0, at] = k[0, 3] * 1e7
+    o, S = K.fwd_delta(q, k, v, b, initial_state=S0, return_state=True)
+    assert torch.isfinite(clean[:, :at]).all() and torch.equal(o[:, :at], clean[:, :at])
+    assert not torch.isfinite(o[:, at:]).any() and not torch.isfinite(S).any()
