@@ -478,8 +478,10 @@ kata_status kata_fwd_delta(const kata_delta_problem* pr, const void* q, const vo
                            const float* initial_state, void* o, float* final_state, void* workspace,
                            size_t ws_bytes, void* stream);
 
-/* For the backward pass: besides these, for a chunk and head two states (dk rounded up to 32, 64 or 128) and two
- * 64 x dv arrays, fp32: 76 KB at dk = dv = 64. */
+/* For the backward pass: besides these, for a chunk and head two states (dk rounded up to 32 (fp32 only), 64 or 128, dv to
+ * 16) and two 64 x dv arrays, fp32, with the 11.5 KB 76 KB at dk = dv = 64; one more such state for a sequence and head, and a
+ * second state for a segment; and where heads of q and k are shared and the chunks times their number fewer than 256, two fp32
+ * arrays [b][t][H][dk]. */
 size_t kata_bwd_delta_workspace_size(const kata_delta_problem* pr);
 
 /* Gradients of sum(dO * o) + sum(dfinal_state * final_state) in q, k [B][T][Hk][dk] (summed over the value

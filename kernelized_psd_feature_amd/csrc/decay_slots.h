@@ -24,4 +24,11 @@ KATA_HD int decay_slot_count(int T, int n_seq, int SL) { return T / SL + n_seq +
 // scores of a wider head.
 KATA_HD int decay_columns(bool bf16, int dv) { return bf16 && dv > 64 ? 128 : 64; }
 
+// What the gated delta rule's kernels (delta_tiles.h) keep of a chunk and head, in floats: five vectors of its 64 tokens,
+// and the ten 16 x 16 blocks of its inverse on and below the diagonal.
+constexpr int kDeltaChunk = 64, kDeltaVec = 5 * kDeltaChunk, kInvBlocks = 10, kInvFloats = kInvBlocks * 256;
+// Rows of a chunk's state as the backward walks keep it, in tiles of 16 columns: the kernels' width.
+KATA_HD int delta_state_rows(bool bf16, int dk) { return dk <= 32 && !bf16 ? 32 : dk <= 64 ? 64 : 128; }
+constexpr int kTileColumns = 16;
+
 }  // namespace kata

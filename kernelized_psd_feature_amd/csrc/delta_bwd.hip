@@ -931,6 +931,7 @@ __global__ __launch_bounds__(256) void delta_share_kernel(const float* __restric
 
 template <typename T, int DK, int W, bool kSums>
 hipError_t launch_both_t(const DeltaArgs& a, hipStream_t st) {
+  if (delta_state_rows(sizeof(T) == 2, a.m.dk) != DK) return hipErrorInvalidValue;   // the workspace is laid out for others
   constexpr int bytes = kBothBytes<T, DK, W>;
   const auto kernel = delta_both_kernel<T, DK, W, kSums>;
   hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), bytes);
@@ -956,6 +957,7 @@ hipError_t launch_both_d(const DeltaArgs& a, bool bf16, hipStream_t st) {
 template <typename T, int DK>
 hipError_t launch_grads_t(const DeltaArgs& a, hipStream_t st) {
   using TL = GradTiles<T, DK>;
+  if (delta_state_rows(sizeof(T) == 2, a.m.dk) != DK) return hipErrorInvalidValue;
   const auto kernel = delta_grads_kernel<T, DK>;
   hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(kernel), TL::bytes);
   if (e != hipSuccess) return e;

@@ -49,7 +49,8 @@ kata_status check_delta_problem(const kata_delta_problem* pr, int most, bool bac
   return check_strides("o", pr->so, sizes, pr->dv, true, why);
 }
 
-constexpr size_t kVecBytes = 1280, kInvBytes = 10240;   // of a chunk and head (delta_tiles.h)
+static_assert(kDecayChunk == kDeltaChunk, "one chunk for both layers' slots");
+constexpr size_t kVecBytes = kDeltaVec * 4, kInvBytes = kInvFloats * 4;   // of a chunk and head
 
 }  // namespace
 
@@ -108,9 +109,8 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
   }
   if (backward) {
     if (p.n_seg > 1) p.rsums = part(s * state);
-    // (the state walks' tile: 32 rows have no bf16 form of the gradients' kernel)
-    const size_t DK = pr->dk <= 32 && !bf16 ? 32 : pr->dk <= 64 ? 64 : 128;
-    const size_t tiles = (pr->dv + 15) / 16, chunk_state = DK * 16 * tiles * 4, chunk_u = 64 * 16 * tiles * 4;
+    const size_t rows = delta_state_rows(bf16, pr->dk), tiles = (pr->dv + kTileColumns - 1) / kTileColumns;
+    const size_t chunk_state = rows * kTileColumns * tiles * 4, chunk_u = kDeltaChunk * kTileColumns * tiles * 4;
     p.cstates = part(c * chunk_state);
     p.rstates = part(c * chunk_state);
     p.u = part(c * chunk_u);
@@ -119,9 +119,9 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
     // fp32 heads of 40 and 72 on one of q and k: 70 us, the heads by themselves 27 and 5 for the sums).
     p.by_heads = pr->H > pr->Hk && int64_t(p.c_slots) * pr->Hk < kDeltaGradBlocks;
     if (p.by_heads) {
-      const size_t rows = size_t(pr->packed ? 1 : pr->n_seq) * pr->T * H * pr->dk * 4;
-      p.pq = part(rows);
-      p.pk = part(rows);
+      const size_t heads = size_t(pr->packed ? 1 : pr->n_seq) * pr->T * H * pr->dk * 4;
+      p.pq = part(heads);
+      p.pk = part(heads);
     }
     p.fstates = part(size_t(pr->n_seq) * H * chunk_state);
   }

@@ -1,5 +1,5 @@
 // What the gated delta rule's kernels share: where a chunk lies, what the workspace holds of it, and
-// products whose operands are kept in two bf16 terms.
+// products whose operands are kept in two or three bf16 terms.
 #pragma once
 
 #include "decay_slots.h"
@@ -14,8 +14,9 @@ __device__ __forceinline__ f32x4 unquad(const f32x4& x) { return x; }
 
 // What a chunk and head keep in the workspace.  Vectors: exp(c), exp(c_63 - c), beta, and c log2(e) as the sum
 // of two floats, of every token, c being the sum of the log decays from the chunk's first token on.
-// Inverse: its 16 x 16 blocks on and below the diagonal, by rows of blocks.
-constexpr int kDeltaVec = 5 * kC, kInvBlocks = 10, kInvFloats = kInvBlocks * 256;
+// Inverse: its 16 x 16 blocks on and below the diagonal, by rows of blocks.  Their sizes: decay_slots.h, which the planner
+// lays the workspace out by, too.
+static_assert(kDeltaChunk == kC, "the planner's chunks are the kernels'");
 
 // 2^(hi + lo) of the difference of two such sums
 __device__ __forceinline__ float exp2_diff(float hi, float lo, float hj, float lj) {
