@@ -412,8 +412,8 @@ def parallel_kata_attn(q, k, v, num_groups=1, form="auto", chunk=64, eps=1e-6, r
     (flash-style O(T^2)), or "auto" (chunked where T is a multiple of chunk, else quadratic).
     Under autograd the backward runs bwd (chunked where T is a multiple of chunk, else flash);
     its fp32 gradients are handed back in the inputs' dtype.
-    rotary: (rates, magnitude) of rotary_rates: q and k are turned by their positions first (see
-    rotary(); positions and interleaved are its arguments)."""
+    rotary: (rates, magnitude) of rotary_rates, with positions of several axes (rates, magnitude, axes): q and k
+    are turned by their positions first (see rotary(); positions and interleaved are its arguments)."""
     if rotary is not None:
         q, k = layer.turn(q, k, rotary, positions, 0, interleaved)
     if form == "auto":

@@ -378,7 +378,7 @@ def parallel_delta_attn(q, k, v, beta, log_decay=None, scale=1.0, initial_state=
             wq, wk, eps = (*qk_norm, 1e-6)[:3]
         else:
             raise ValueError("qk_norm must be 'l2' or (q_weight, k_weight[, eps])")
-        rates, magnitude, axes = (None, 1.0, None) if rotary is None else (*rotary, None)[:3]
+        rates, magnitude, axes = (None, 1.0, None) if rotary is None else _l.rotary_table(rotary)
         q, k = _QkNorm.apply(q, k, wq, wk, eps, qk_norm == "l2", rates, positions if rotary is not None else None, 0,
                              interleaved, magnitude, axes)
     elif rotary is not None:

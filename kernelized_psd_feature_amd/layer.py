@@ -401,7 +401,7 @@ def rotary(q, k, rates, positions=None, offset=0, interleaved=False, magnitude=1
     if B * T * H * D:
         pr = _ROTARY.pack(B, T, H, Hk, D, 2 * n, _dtype(dtype), 1 if interleaved else 0, 1 if inverse else 0,
                           pos64, magnitude, pos_b, pos_t, offset, *sq[:3], *sk[:3], *soq[:3], *sok[:3])
-        if axes is None:
+        if axes is None or n == 0:                   # (no pairs: no axis is looked at, and axes has no address)
             _run("kata_rotary", device, pr, pq, pk, rates.data_ptr(), at, poq, pok)
         else:
             _run("kata_rotary_axes", device, pr, pq, pk, rates.data_ptr(), at, axes.data_ptr(), n_axes, pos_a, poq, pok)
@@ -582,10 +582,17 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
     return _LayerNorm.apply(x, weight, bias, eps)
 
 
-def turn(q, k, rotary_table, positions=None, offset=0, interleaved=False):
-    """rotary() under torch autograd; rotary_table: (rates, magnitude) as rotary_rates returns them, with
+def rotary_table(table):
+    """(rates, magnitude, axes) of a layer's rotary argument: (rates, magnitude) as rotary_rates returns them, with
     positions of several axes (rates, magnitude, axes)."""
-    rates, magnitude, axes = (*rotary_table, None)[:3]
+    if not isinstance(table, (tuple, list)) or len(table) not in (2, 3):
+        raise ValueError("rotary must be (rates, magnitude) or (rates, magnitude, axes)")
+    return (*table, None)[:3]
+
+
+def turn(q, k, table, positions=None, offset=0, interleaved=False):
+    """rotary() under torch autograd; table: see rotary_table()."""
+    rates, magnitude, axes = rotary_table(table)
     return _Rotary.apply(q, k, rates, positions, offset, interleaved, magnitude, axes)
 
 
@@ -605,8 +612,8 @@ def parallel_decay_attn(q, k, v, log_decay, scale=1.0, initial_state=None, retur
     """Linear attention with one decay per head as a differentiable op, (B, T, H, dk) -> (B, T, H, dv)
     (see fwd_decay), the output in the inputs' dtype.
 
-    rotary: (rates, magnitude) of rotary_rates: q and k are turned first, by `positions` (see rotary();
-    with cu_seqlens they must be given).  norm: (weight, bias[, eps]): the outputs go through a layer
+    rotary: (rates, magnitude) of rotary_rates, with positions of several axes (rates, magnitude, axes): q and k
+    are turned first, by `positions` (see rotary(); with cu_seqlens they must be given).  norm: (weight, bias[, eps]): the outputs go through a layer
     norm, over each head for a weight of dv elements, over all heads of a token for one of H dv.
     log_decay is a constant: it has no gradient, and a tensor that asks for one is refused."""
     if log_decay.requires_grad:
