@@ -489,8 +489,8 @@ size_t kata_bwd_delta_workspace_size(const kata_delta_problem* pr);
  * (dlog_decay NULL: not wanted), all contiguous, and where dinitial_state is not NULL, the initial state.
  * Rows of no sequence get zeros.  initial_state and dfinal_state: nullable (zero); dinitial_state overlaps
  * neither.  Every gradient scales with dO and dfinal_state, at beta = 0 too.  dlog_decay of a token is good to some 2^-17
- * (fp32 2^-21) of the product of the 2-norms of the state and of its gradient there, the decay taken in, or, in a chunk of 64
- * tokens without a decay below exp(-1/2), of the largest product of the norms of the state behind a token and of its gradient, from
+ * (fp32 2^-21) of the product of the 2-norms of the state and of its gradient there, the decay taken in, or, in a bf16 chunk of
+ * 64 tokens without a decay below exp(-1/2), of the largest product of the norms of the state behind a token and of its gradient, from
  * there to the chunk's end.  A sum of both signs over dk x dv terms, it may be much smaller than that. */
 kata_status kata_bwd_delta(const kata_delta_problem* pr, const void* q, const void* k, const void* v,
                            const void* beta, const float* log_decay, const void* dO, const int32_t* cu_seqlens,

@@ -16,9 +16,10 @@
 // dO . o is q . dq, a head's part of it.  The second form is what reaches over the token's decay, from the tokens and the state
 // before it to those behind, every term with that decay for a factor.  Of a strong decay the first one's terms, which have it
 // not, leave only their roundings: mean log decays of -1, -5, -10, -20 are off by 2e-6, 3e-5, 4e-4, 0.3 of the norm in bf16 (fp32 2e-6,
-// 6e-5, 1e-3, 0.4), by the second form by 4e-7 to 7e-7 (fp32 2e-7 to 4e-7).  Weak ones are as good by the first (-0.02: 9e-7,
-// by the second 3e-6, of operands in two terms), and for less work: 8 x 4096 tokens 718 us, 754 by the second.  So the second is
-// for chunks in which any token's decay is below exp(-1/2).)
+// 6e-5, 1e-3, 0.4), by the second form by 4e-7 to 7e-7 (fp32 2e-7 to 4e-7).  In bf16 weak ones are as good by the first (-0.02: 9e-7,
+// by the second 3e-6, of operands in two terms), and for less work: a training step of 8 x 4096 tokens 948 us, 1016 where all chunks take the second.
+// So in bf16 the second is for chunks in which any token's decay is below exp(-1/2); in fp32, where it is the better one of
+// all (-0.02: 3e-7 to 5e-7 for 6e-7 to 1e-6) and both together lack the registers (2 x 1001: 147 us, 152), for every chunk.)
 //
 // S and U, and D and X, come from two walks like the forward pass's, one of them in reversed time, which keep
 // them for every chunk; all the rest is then computed for all chunks at once (delta_grads_kernel).
@@ -566,7 +567,6 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   f32x4 Wt[4], dqh[NH];                             // the strip of dO U^T (second half: X U^T), transposed; the head's dq
   float frob = 0.f, xv = 0.f, xe = 0.f;             // X . v, and dbeta without it, in parts
   float frob_in = 0.f, write = 0.f;                 // strong decays: <D, S> and W in parts
-  bool strong = false;
   const int i0 = first_half ? 0 : NH;
 #pragma unroll 1
   while (more) {
@@ -639,7 +639,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
 
     // a wave's 16 tokens
     forget();
-    const float log2_decay = sc[lane] - (lane ? sc[lane - 1] : 0.f);
+    float log2_decay = 0.f;
+    if constexpr (TL::kBf) log2_decay = sc[lane] - (lane ? sc[lane - 1] : 0.f);
     Op<T, N> z[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) z[i] = value_op<N, LP>(sZ + 32 * i * LP + 16 * w, PL, lane);
@@ -719,195 +720,197 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       __syncthreads();
     }
     forget();
-    strong = A.dlog && __any(log2_decay < -0.72f);  // uniform: log2 of exp(-1/2)
-    if (strong && !first_half && 4 * now.vb + w < ct) {
-      const long long tile = (((long long)now.slot * m.H + h) * ct + 4 * now.vb + w) * (DK * 16) + lane * 4;
+    // the rest, by how dlog is formed
+    auto finish = [&](auto strong) __attribute__((always_inline)) {
+      constexpr bool kStrong = decltype(strong)::value;
+      if (kStrong && !first_half && 4 * now.vb + w < ct) {
+        const long long tile = (((long long)now.slot * m.H + h) * ct + 4 * now.vb + w) * (DK * 16) + lane * 4;
 #pragma unroll 1
-      for (int i = 0; i < NS; ++i) {
-        const f32x4 y = load4(A.cstates + tile + i * 256) * load4(A.rstates + tile + i * 256);
-        frob_in += y[0] + y[1] + y[2] + y[3];
-      }
-    }
-    const float left = vec[kC + 16 * w + l16];
-#pragma unroll
-    for (int ia = 0; ia < NH; ia += G) {
-      f32x4 a[G];
-#pragma unroll
-      for (int p = 0; p < G; ++p) a[p] = zero4();
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        Op<T, N2> st[G];
-#pragma unroll
-        for (int p = 0; p < G; ++p) st[p] = value_op<N2, LS>(sD + 32 * j * LS + 16 * (i0 + ia + p), PS, lane);
-        each_term<N2, N2>([&](int n, int k) __attribute__((always_inline)) {
-#pragma unroll
-          for (int p = 0; p < G; ++p) a[p] = mma(st[p].t[n], u[j].t[k], a[p]);
-        });
-      }
-#pragma unroll
-      for (int p = 0; p < G; ++p) {
-        a[p] *= left;
-        dka[ia + p] += a[p];
-        before_branch(a[p]);
-      }
-      if (strong)
-#pragma unroll
-        for (int p = 0; p < G; ++p) write += row_dot(sK, i0 + ia + p, a[p]);
-    }
-    if (now.vb + 1 < v_blocks) {
-      now = next;
-      continue;
-    }
-    if constexpr (kAhead) __syncthreads();          // U and X have been read
-    // PO or PV, the wave's strip of rows
-    forget();
-    const float b_row = first_half ? 1.f : sb[16 * w + l16];
-    float e = 0.f;
-    if (strong) {
-      e = sb[16 * w + l16] * xe;
-#pragma unroll
-      for (int i = 0; i < NH; ++i) e += row_dot(sQ, i0 + i, dqh[i]);
-    }
-    {
-      const float hi = sc[16 * w + l16], lo = sc[kC + 16 * w + l16], factor = first_half ? A.scale : -1.f;
-      const int end = 16 * w + l16 + (first_half ? 1 : 0);             // the first key that it does not reach
-      T* const at = (first_half ? sU : sZ) + (16 * w + l16) * LP;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f32x4 p = zero4();
-        if (j <= w) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int key = 16 * j + 4 * g + r;
-            p[r] = key >= end ? 0.f : Wt[j][r] * (exp2_diff(hi, lo, sc[key], sc[kC + key]) * factor);
-          }
-        }
-        Wt[j] = p;
-        p *= b_row;
-        if (first_half) put_terms<N>(at + split_place(16 * j + 4 * g), PL, p);
-        else put_terms<N2>(at + split_place(16 * j + 4 * g), PL, p);
-      }
-    }
-    if (!first_half) {
-      if (strong) frob = frob_in;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
-      if (lane == 0) sF[w] = frob;
-    }
-    __syncthreads();
-    if (!first_half || strong) {                    // F, of which dbeta wants the sums over the keys
-      const T* const mine = (first_half ? sQ : sK) + (16 * w + l16) * LK + 8 * g;
-      float before = 0.f;                           // F of the row's keys before the tile
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j > w) break;                           // uniform
-        f32x4 f = zero4();
-#pragma unroll
-        for (int i = 0; i < DK / 32; ++i) f = mma(row_frag(sK + (16 * j + l16) * LK + 32 * i + 8 * g), row_frag(mine + 32 * i), f);
-        f *= Wt[j];
-        const float whole = f[0] + f[1] + f[2] + f[3];
-        if (!first_half) xe += whole;
-        if (strong) {
-          // the row's sums over the keys before each key, then for each key those over the rows from it on
-          const float near = other_16(whole), pair = whole + near, far = other_32(pair);
-          f32x4 sum;
-          sum[0] = before + (g & 1 ? near : 0.f) + (g & 2 ? far : 0.f);
-          sum[1] = sum[0] + f[0];
-          sum[2] = sum[1] + f[1];
-          sum[3] = sum[2] + f[2];
-          before += pair + far;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) sum[r] = sum_16(j == w && l16 < 4 * g + r ? 0.f : sum[r] * b_row);
-          if (l16 == 0) *reinterpret_cast<f32x4*>(sG + (w + (first_half ? 0 : 4)) * kC + 16 * j + 4 * g) = sum;
+        for (int i = 0; i < NS; ++i) {
+          const f32x4 y = load4(A.cstates + tile + i * 256) * load4(A.rstates + tile + i * 256);
+          frob_in += y[0] + y[1] + y[2] + y[3];
         }
       }
-    }
+      const float left = vec[kC + 16 * w + l16];
 #pragma unroll
-    for (int ia = 0; ia < NH; ia += G)
+      for (int ia = 0; ia < NH; ia += G) {
+        f32x4 a[G];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        frag kt[G];
+        for (int p = 0; p < G; ++p) a[p] = zero4();
 #pragma unroll
-        for (int p = 0; p < G; ++p) kt[p] = split_column_frag<LK>(sK + 32 * j * LK, i0 + ia + p, lane);
-        if (j <= w >> 1) {                          // uniform
-          const Op<T, N> po = row_op<N>(sU + (16 * w + l16) * LP + 32 * j + 8 * g, PL);
-          const Op<T, N2> pv = row_op<N2>(sZ + (16 * w + l16) * LP + 32 * j + 8 * g, PL);
+        for (int j = 0; j < 2; ++j) {
+          Op<T, N2> st[G];
 #pragma unroll
-          for (int t = N - 1; t >= 0; --t)
+          for (int p = 0; p < G; ++p) st[p] = value_op<N2, LS>(sD + 32 * j * LS + 16 * (i0 + ia + p), PS, lane);
+          each_term<N2, N2>([&](int n, int k) __attribute__((always_inline)) {
 #pragma unroll
-            for (int p = 0; p < G; ++p) {
-              dqh[ia + p] = mma(kt[p], po.t[t], dqh[ia + p]);
-              if (t < N2) dka[ia + p] = mma(kt[p], pv.t[t], dka[ia + p]);
+            for (int p = 0; p < G; ++p) a[p] = mma(st[p].t[n], u[j].t[k], a[p]);
+          });
+        }
+#pragma unroll
+        for (int p = 0; p < G; ++p) {
+          a[p] *= left;
+          dka[ia + p] += a[p];
+          if (kStrong) write += row_dot(sK, i0 + ia + p, a[p]);
+        }
+      }
+      if (now.vb + 1 < v_blocks) return;
+      if constexpr (kAhead) __syncthreads();          // U and X have been read
+      // PO or PV, the wave's strip of rows
+      forget();
+      const float b_row = first_half ? 1.f : sb[16 * w + l16];
+      float e = 0.f;
+      if (kStrong) {
+        e = sb[16 * w + l16] * xe;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) e += row_dot(sQ, i0 + i, dqh[i]);
+      }
+      {
+        const float hi = sc[16 * w + l16], lo = sc[kC + 16 * w + l16], factor = first_half ? A.scale : -1.f;
+        const int end = 16 * w + l16 + (first_half ? 1 : 0);             // the first key that it does not reach
+        T* const at = (first_half ? sU : sZ) + (16 * w + l16) * LP;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x4 p = zero4();
+          if (j <= w) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int key = 16 * j + 4 * g + r;
+              p[r] = key >= end ? 0.f : Wt[j][r] * (exp2_diff(hi, lo, sc[key], sc[kC + key]) * factor);
             }
+          }
+          Wt[j] = p;
+          p *= b_row;
+          if (first_half) put_terms<N>(at + split_place(16 * j + 4 * g), PL, p);
+          else put_terms<N2>(at + split_place(16 * j + 4 * g), PL, p);
         }
-        if (j >= w >> 1) {
-          const Op<T, N2> po = split_column_op<N2, LP>(sU + 32 * j * LP, PL, w, lane);
-          const Op<T, N2> pv = split_column_op<N2, LP>(sZ + 32 * j * LP, PL, w, lane);
-          frag qt[G];
+      }
+      if (!first_half) {
+        if (kStrong) frob = frob_in;
 #pragma unroll
-          for (int p = 0; p < G; ++p) qt[p] = split_column_frag<LK>(sQ + 32 * j * LK, i0 + ia + p, lane);
+        for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
+        if (lane == 0) sF[w] = frob;
+      }
+      __syncthreads();
+      if (!first_half || kStrong) {                    // F, of which dbeta wants the sums over the keys
+        const T* const mine = (first_half ? sQ : sK) + (16 * w + l16) * LK + 8 * g;
+        float before = 0.f;                           // F of the row's keys before the tile
 #pragma unroll
-          for (int t = N2 - 1; t >= 0; --t) {
+        for (int j = 0; j < 4; ++j) {
+          if (j > w) break;                           // uniform
+          f32x4 f = zero4();
 #pragma unroll
-            for (int p = 0; p < G; ++p) dka[ia + p] = mma(qt[p], po.t[t], dka[ia + p]);
+          for (int i = 0; i < DK / 32; ++i) f = mma(row_frag(sK + (16 * j + l16) * LK + 32 * i + 8 * g), row_frag(mine + 32 * i), f);
+          f *= Wt[j];
+          const float whole = f[0] + f[1] + f[2] + f[3];
+          if (!first_half) xe += whole;
+          if (kStrong) {
+            // the row's sums over the keys before each key, then for each key those over the rows from it on
+            const float near = other_16(whole), pair = whole + near, far = other_32(pair);
+            f32x4 sum;
+            sum[0] = before + (g & 1 ? near : 0.f) + (g & 2 ? far : 0.f);
+            sum[1] = sum[0] + f[0];
+            sum[2] = sum[1] + f[1];
+            sum[3] = sum[2] + f[2];
+            before += pair + far;
 #pragma unroll
-            for (int p = 0; p < G; ++p) dka[ia + p] = mma(kt[p], pv.t[t], dka[ia + p]);
+            for (int r = 0; r < 4; ++r) sum[r] = sum_16(j == w && l16 < 4 * g + r ? 0.f : sum[r] * b_row);
+            if (l16 == 0) *reinterpret_cast<f32x4*>(sG + (w + (first_half ? 0 : 4)) * kC + 16 * j + 4 * g) = sum;
           }
         }
       }
-    for (int i = 0; i < NH; ++i) {
-      dqa[i] += dqh[i];
-      before_branch(dqa[i]);
-    }
-    if (!strong) {                                  // dO . o = q . dq of this head
-      e = -sb[row] * xv;
 #pragma unroll
-      for (int i = 0; i < NH; ++i) e += row_dot(sQ, i0 + i, dqh[i]);
-    }
-    e = sum_xor32(sum_xor16(e));
-    xe = sum_xor32(sum_xor16(xe + xv));
-    if (strong) write = sum_xor32(sum_xor16(write));
-    if (lane < 16) {
-      float* const at = sE + (first_half ? 0 : kC) + 16 * w + lane;
-      at[0] = e;
-      at[2 * kC] = xe;
-      if (strong) at[4 * kC] = write;
-    }
-    __syncthreads();
-    if (wave == 0) {
-      const long long at = lead + (long long)lane * m.H;
-      if (lane < now.n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[2 * kC + lane] + sE[3 * kC + lane]);
-      if (strong) {
-        float y = sE[lane] + sE[kC + lane], z = sE[4 * kC + lane] + sE[5 * kC + lane];
+      for (int ia = 0; ia < NH; ia += G)
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const float down = __shfl_down(y, d), up = __shfl_up(z, d);
-          if (lane + d < 64) y += down;
-          if (lane >= d) z += up;
+        for (int j = 0; j < 2; ++j) {
+          frag kt[G];
+#pragma unroll
+          for (int p = 0; p < G; ++p) kt[p] = split_column_frag<LK>(sK + 32 * j * LK, i0 + ia + p, lane);
+          if (j <= w >> 1) {                          // uniform
+            const Op<T, N> po = row_op<N>(sU + (16 * w + l16) * LP + 32 * j + 8 * g, PL);
+            const Op<T, N2> pv = row_op<N2>(sZ + (16 * w + l16) * LP + 32 * j + 8 * g, PL);
+#pragma unroll
+            for (int t = N - 1; t >= 0; --t)
+#pragma unroll
+              for (int p = 0; p < G; ++p) {
+                dqh[ia + p] = mma(kt[p], po.t[t], dqh[ia + p]);
+                if (t < N2) dka[ia + p] = mma(kt[p], pv.t[t], dka[ia + p]);
+              }
+          }
+          if (j >= w >> 1) {
+            const Op<T, N2> po = split_column_op<N2, LP>(sU + 32 * j * LP, PL, w, lane);
+            const Op<T, N2> pv = split_column_op<N2, LP>(sZ + 32 * j * LP, PL, w, lane);
+            frag qt[G];
+#pragma unroll
+            for (int p = 0; p < G; ++p) qt[p] = split_column_frag<LK>(sQ + 32 * j * LK, i0 + ia + p, lane);
+#pragma unroll
+            for (int t = N2 - 1; t >= 0; --t) {
+#pragma unroll
+              for (int p = 0; p < G; ++p) dka[ia + p] = mma(qt[p], po.t[t], dka[ia + p]);
+#pragma unroll
+              for (int p = 0; p < G; ++p) dka[ia + p] = mma(kt[p], pv.t[t], dka[ia + p]);
+            }
+          }
         }
-        z = __shfl_up(z, 1);                        // of the tokens before
-        y += (lane ? z : 0.f) + vec[kC - 1] * (sF[0] + sF[1] + sF[2] + sF[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i >= lane >> 4) y += sG[i * kC + lane] + sG[(4 + i) * kC + lane];
-        if (lane < now.n) A.dlog[at] = y;
-      } else if (A.dlog) {
-        double y = (double)sE[lane] + sE[kC + lane];
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const double up = __shfl_down(y, d);
-          if (lane + d < 64) y += up;
-        }
-        y += (double)sF[0] + sF[1] + sF[2] + sF[3];
-        const bool none = now.s.part == 0 && lane == 0 && !A.init;     // a decay of nothing has no gradient
-        if (lane < now.n) A.dlog[at] = none ? 0.f : (float)y;
+      for (int i = 0; i < NH; ++i) {
+        dqa[i] += dqh[i];
       }
-    }
-    if (now.hh + 1 == share && live_row) {
-      const long long at = (((long long)now.s.b * m.T + now.row0 + row) * heads + now.h0 / share) * m.dk + 4 * g;
+      if (!kStrong) {                                  // dO . o = q . dq of this head
+        e = -sb[row] * xv;
 #pragma unroll
-      for (int i = 0; i < NH; ++i)
-        if (16 * (i0 + i) + 4 * g < m.dk) put_grads(at + 16 * (i0 + i), dqa[i], dka[i]);
+        for (int i = 0; i < NH; ++i) e += row_dot(sQ, i0 + i, dqh[i]);
+      }
+      e = sum_xor32(sum_xor16(e));
+      xe = sum_xor32(sum_xor16(xe + xv));
+      if (kStrong) write = sum_xor32(sum_xor16(write));
+      if (lane < 16) {
+        float* const at = sE + (first_half ? 0 : kC) + 16 * w + lane;
+        at[0] = e;
+        at[2 * kC] = xe;
+        if (kStrong) at[4 * kC] = write;
+      }
+      __syncthreads();
+      if (wave == 0) {
+        const long long at = lead + (long long)lane * m.H;
+        if (lane < now.n) reinterpret_cast<T*>(A.dbeta)[at] = from_f32<T>(sE[2 * kC + lane] + sE[3 * kC + lane]);
+        if (kStrong) {
+          float y = sE[lane] + sE[kC + lane], z = sE[4 * kC + lane] + sE[5 * kC + lane];
+#pragma unroll
+          for (int d = 1; d < 64; d <<= 1) {
+            const float down = __shfl_down(y, d), up = __shfl_up(z, d);
+            if (lane + d < 64) y += down;
+            if (lane >= d) z += up;
+          }
+          z = __shfl_up(z, 1);                        // of the tokens before
+          y += (lane ? z : 0.f) + vec[kC - 1] * (sF[0] + sF[1] + sF[2] + sF[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i >= lane >> 4) y += sG[i * kC + lane] + sG[(4 + i) * kC + lane];
+          if (A.dlog && lane < now.n) A.dlog[at] = y;
+        } else if (A.dlog) {
+          double y = (double)sE[lane] + sE[kC + lane];
+#pragma unroll
+          for (int d = 1; d < 64; d <<= 1) {
+            const double up = __shfl_down(y, d);
+            if (lane + d < 64) y += up;
+          }
+          y += (double)sF[0] + sF[1] + sF[2] + sF[3];
+          const bool none = now.s.part == 0 && lane == 0 && !A.init;     // a decay of nothing has no gradient
+          if (lane < now.n) A.dlog[at] = none ? 0.f : (float)y;
+        }
+      }
+      if (now.hh + 1 == share && live_row) {
+        const long long at = (((long long)now.s.b * m.T + now.row0 + row) * heads + now.h0 / share) * m.dk + 4 * g;
+#pragma unroll
+        for (int i = 0; i < NH; ++i)
+          if (16 * (i0 + i) + 4 * g < m.dk) put_grads(at + 16 * (i0 + i), dqa[i], dka[i]);
+      }
+    };
+    if constexpr (TL::kBf) {
+      if (A.dlog && __any(log2_decay < -0.72f)) finish(std::true_type());       // uniform: log2 of exp(-1/2)
+      else finish(std::false_type());
+    } else {
+      finish(std::true_type());
     }
     now = next;
   }
