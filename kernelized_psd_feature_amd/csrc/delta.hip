@@ -18,10 +18,10 @@
 // M (the recurrence from the unit matrix, without values), delta_join_kernel turns them into entry states,
 // and the walk runs the segments side by side.
 //
-// Where the time goes (131072 tokens, 16 bf16 heads of 64): inverses 176 us, sums 389, joining 26, walk 480, for
+// Where the time goes (131072 tokens, 16 bf16 heads of 64): inverses 178 us, sums 393, joining 27, walk 476, for
 // 215 us of reading q, k, v and writing o once.  A chunk is a chain of products (K S, T X, K^T U), each of operands
 // that are split anew into bf16 terms out of the last one's fp32 sums, with LDS reads and two or three barriers
-// between; two workgroups a CU hide part of each other's (sums: VALU 70 % of the cycles, LDS 59, MFMA 44; walk 51, 47,
+// between; two workgroups a CU hide part of each other's (sums: VALU 70 % of the cycles, LDS 60, MFMA 44; walk 51, 46,
 // 27).  The terms are the price of a chain: one of them is 2^-8 of a value, which the recurrence would carry from chunk
 // to chunk; with three the final state is off by 1.6e-7 of its norm, plain fp32 by 2.1e-7.
 #include <type_traits>
@@ -38,7 +38,7 @@ namespace {
 constexpr int kThreads = 256;             // of the kernels other than the walk
 
 // ---- inverses --------------------------------------------------------------------------------
-// 176 us for 131072 tokens of 16 heads of 64 (reads k, writes 11.5 KB a chunk and head: 3.6 TB/s).  The
+// 178 us for 131072 tokens of 16 heads of 64 (reads k, writes 11.5 KB a chunk and head: 3.6 TB/s).  The
 // substitution is exact to rounding for keys of any length; powers of A, which MFMA could take, grow with them.
 // One workgroup for a chunk and head.  A wave forms a strip of 16 rows of A (fp32 sums on MFMA); the four
 // blocks on the diagonal are inverted by substitution, 16 lanes a block, a column each; below them
@@ -331,7 +331,8 @@ __global__ __launch_bounds__(kThreads) void delta_join_kernel(DeltaArgs A, int b
 // products with the state are taken of the one before the token, in one pass over the rows:
 //   a = S^T k, z = S^T q, u = b (v - g a), o = scale (g z + (q . k) u), S <- g S + k u^T.
 // Bound by the state's two ways through HBM: 512 sequences of 16 heads of 64 x 64, 54.5 us, 5.0 TB/s, what a copy
-// reaches.  One sequence: 4.2 us, a launch and one pass of loads.
+// reaches.  One sequence: 4.7 us, a launch and one pass of loads.  Of 128 x 128 the
+// state takes 192 registers a lane, which leaves too few waves to keep the loads going: 256 sequences 167 us, 3.2 TB/s.
 struct TokenArgs {
   int T, H, share, dk, dv;
   long long sq[3], sk[3], sv[3], so[3], sb[3], sl[3];

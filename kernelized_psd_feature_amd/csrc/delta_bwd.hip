@@ -24,7 +24,7 @@
 // S and U, and D and X, come from two walks like the forward pass's, one of them in reversed time, which keep
 // them for every chunk; all the rest is then computed for all chunks at once (delta_grads_kernel).
 //
-// 8 x 4096 tokens of 16 bf16 heads of 64: inverses 47 us, both walks 297, gradients 370; the bytes that the three
+// 8 x 4096 tokens of 16 bf16 heads of 64: inverses 48 us, both walks 304, gradients 390; the bytes that the three
 // exchange, 1.9 GB, are 380 us of HBM's time.  The walks are a chain as forward, 64 chunks of 4.6 us where 256
 // workgroups have a CU each (VALU 33 % of the cycles, LDS 34, MFMA 20).  Four waves more, forming P^T dO and
 // Q^T diag(y) dO a chunk ahead, did not shorten it (330 for 305): the waves share their SIMDs.
@@ -311,9 +311,9 @@ __global__ __launch_bounds__(64 * W, (sizeof(T) == 4 && DK == 128 ? 1 : 2)) void
 // have left in tiles of 16 columns, go through LDS, [column][token] and [column][row of the state]; a wave has 16
 // tokens, four of the waves P's gradient and half of the columns of dq and dk, the others that of the system's
 // matrix and the other half.
-// 370 us for 8 x 4096 tokens of 16 heads of 64, 136 KB a chunk and head, 3.0 TB/s: a CU holds one workgroup (121 KB of
+// 390 us for 8 x 4096 tokens of 16 heads of 64, 136 KB a chunk and head, 2.9 TB/s: a CU holds one workgroup (122 KB of
 // LDS), its loads run a chunk ahead, and five barriers part phases of some hundred cycles of LDS and VALU each (VALU
-// 32 % of the cycles, LDS 30, MFMA 9; without any load 300 us).
+// 38 % of the cycles, LDS 30, MFMA 10; without any load 290 us).
 template <typename T, int DK>
 struct GradTiles {
   static constexpr bool kBf = sizeof(T) == 2;

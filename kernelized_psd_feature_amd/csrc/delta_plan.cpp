@@ -116,7 +116,7 @@ DeltaPlan plan_delta(const kata_delta_problem* pr, bool backward) {
     p.u = part(c * chunk_u);
     p.x = part(c * chunk_u);
     // Few chunks and heads of q and k leave CUs idle: each value head by itself, then their sums (2 x 1001 tokens, three
-    // fp32 heads of 40 and 72 on one of q and k: 70 us, the heads by themselves 27 and 5 for the sums).
+    // fp32 heads of 40 and 72 on one of q and k: 78 us, the heads by themselves 31 and 5 for the sums).
     p.by_heads = pr->H > pr->Hk && int64_t(p.c_slots) * pr->Hk < kDeltaGradBlocks;
     if (p.by_heads) {
       const size_t heads = size_t(pr->packed ? 1 : pr->n_seq) * pr->T * H * pr->dk * 4;
