@@ -35,7 +35,7 @@ struct DeltaArgs {
   float* rstates;                         // backward: the gradient of the state behind each chunk
   float *pq, *pk;                         // backward, or null: [b][t][H][dk], dq and dk by value heads
   float *u, *x;                           // backward: [c_slots][H][DV][64] U of the chunks, and X (dv = b X), in registers' order
-  float* fstates;                         // backward with dfin: [n_seq][H], as cstates, the final states
+  float* fstates;                         // bf16 backward with dfin, or null: [n_seq][H], as cstates, the final states
   // states
   const float *init, *dfin;               // [n_seq][H][dk][dv] or null
   float *fin, *dinit;

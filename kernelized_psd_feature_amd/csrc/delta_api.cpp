@@ -196,7 +196,7 @@ kata_status kata_bwd_delta(const kata_delta_problem* pr, const void* q, const vo
   a.init = initial_state;
   a.dfin = dfinal_state;
   a.dinit = dinitial_state;
-  if (!dfinal_state) a.fstates = nullptr;
+  if (!dfinal_state || pr->dtype != KATA_BF16) a.fstates = nullptr;     // (fp32: the gradients do not read them)
   if (p.by_heads) {
     a.pq = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.pq);
     a.pk = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.pk);

@@ -17,8 +17,8 @@
 // before it to those behind, every term with that decay for a factor.  Of a strong decay the first one's terms, which have it
 // not, leave only their roundings: mean log decays of -1, -5, -10, -20 are off by 2e-6, 3e-5, 4e-4, 0.3 of the norm in bf16 (fp32 2e-6,
 // 6e-5, 1e-3, 0.4), by the second form by 4e-7 to 7e-7 (fp32 2e-7 to 4e-7).  In bf16 weak ones are as good by the first (-0.02: 9e-7,
-// by the second 3e-6, of operands in two terms), and for less work: a training step of 8 x 4096 tokens 948 us, 1016 where all chunks take the second.
-// So in bf16 the second is for chunks in which any token's decay is below exp(-1/2); in fp32, where it is the better one of
+// by the second 3e-6, of operands in two terms), and for less work: a training step of 8 x 4096 tokens 948 us, 1016 where
+// all chunks take the second.  So in bf16 the second is for chunks in which any token's decay is below exp(-1/2); in fp32, where it is the better one of
 // all (-0.02: 3e-7 to 5e-7 for 6e-7 to 1e-6) and both together lack the registers (2 x 1001: 147 us, 152), for every chunk.)
 //
 // S and U, and D and X, come from two walks like the forward pass's, one of them in reversed time, which keep
@@ -326,6 +326,8 @@ struct GradTiles {
   static constexpr int kPlane = 64 * LP, kState = 64 * LS;
   // The next chunk's operands are loaded ahead, and D has a place of its own, where registers and LDS are there.
   static constexpr bool kAhead = DK <= 64;
+  // dlog always by what is carried over the decays, with <D, S>; else with <D, S'> but for chunks of strong decays.
+  static constexpr bool kCarried = !kBf;
   // K and Q; U and X, then PO and PV; S (and D)
   static constexpr int bytes = kHead + (2 * kC * LK + 2 * N * kPlane + (N + (kAhead ? N2 : 0)) * kState) * (int)sizeof(T);
 };
@@ -389,7 +391,8 @@ __device__ __forceinline__ float other_32(float x) {
 // the sum over the 16 lanes of a row of them
 __device__ __forceinline__ float sum_16(float x) {
   const auto turned = [](float y, auto by) __attribute__((always_inline)) {              // row_ror
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, y), 0x120 + decltype(by)::value, 0xf, 0xf, true));
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, y), 0x120 + decltype(by)::value, 0xf, 0xf, true));
   };
   x += turned(x, std::integral_constant<int, 8>());
   x += turned(x, std::integral_constant<int, 4>());
@@ -409,7 +412,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
   using frag = typename Elem<T>::frag;
   constexpr int NS = DK / 16, NH = NS / 2, LK = TL::LK, LP = TL::LP, LS = TL::LS, N = TL::N, N2 = TL::N2;
   constexpr int PL = TL::kPlane, PS = TL::kState;
-  constexpr bool kAhead = TL::kAhead;
+  constexpr bool kAhead = TL::kAhead, kCarried = TL::kCarried;
   constexpr int G = NH < 2 || (sizeof(T) == 4 && DK > 64) ? 1 : 2;     // tiles of dq and dk in turn (each_term), by the registers
   extern __shared__ __align__(16) char lds[];
   int* const sh = reinterpret_cast<int*>(lds);
@@ -497,7 +500,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     return false;
   };
 
-  // What is loaded for a place: a wave's 16 columns of U and S, or of X, D and S' (the state behind the chunk); its 16
+  // What is loaded for a place: a wave's 16 columns of U and S, or of X, D and S' (the state behind the chunk; kCarried: S); its 16
   // tokens' dO and (half of the columns) v; all together the chunk's rows and vectors.
   Stage<T, DK, kThreads> rk(nullptr, 0, m.dk, true), rq(nullptr, 0, m.dk, true);
   f32x4 x[4], S[NS], Sn[kAhead ? NS : 1];
@@ -535,8 +538,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       vd = value_row(pv, c0 + (first_half ? 0 : 32), m.dv, g);
     }
     // (behind the last chunk without a gradient D is zero)
-    const bool given = !last || A.fstates;
-    const float* const next = first_half ? A.cstates + tile * (DK * 16) + lane * 4     // (not used)
+    const bool given = kCarried || !last || A.fstates;
+    const float* const next = first_half || kCarried ? A.cstates + tile * (DK * 16) + lane * 4     // (first half: not used)
                               : !last ? A.cstates + (tile + (long long)m.H * ct) * (DK * 16) + lane * 4
                               : given ? A.fstates + (((long long)p.s.seq * m.H + h) * ct + block_tile) * (DK * 16) + lane * 4
                                       : A.rstates + tile * (DK * 16) + lane * 4;
@@ -616,7 +619,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
       for (int i = 0; i < NS; ++i) put_terms<N>(sS + (16 * w + l16) * LS + 16 * i + 4 * g, PS, S[i]);
     } else if constexpr (kAhead) {
       put_d();
-      if (kC * (now.s.part + 1) < now.s.len || A.fstates)
+      if (kCarried || kC * (now.s.part + 1) < now.s.len || A.fstates)
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const f32x4 y = S[i] * Sn[i];
@@ -640,7 +643,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     // a wave's 16 tokens
     forget();
     float log2_decay = 0.f;
-    if constexpr (TL::kBf) log2_decay = sc[lane] - (lane ? sc[lane - 1] : 0.f);
+    if constexpr (!kCarried) log2_decay = sc[lane] - (lane ? sc[lane - 1] : 0.f);
     Op<T, N> z[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) z[i] = value_op<N, LP>(sZ + 32 * i * LP + 16 * w, PL, lane);
@@ -723,7 +726,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
     // the rest, by how dlog is formed
     auto finish = [&](auto strong) __attribute__((always_inline)) {
       constexpr bool kStrong = decltype(strong)::value;
-      if (kStrong && !first_half && 4 * now.vb + w < ct) {
+      if (kStrong && !kCarried && !first_half && 4 * now.vb + w < ct) {
         const long long tile = (((long long)now.slot * m.H + h) * ct + 4 * now.vb + w) * (DK * 16) + lane * 4;
 #pragma unroll 1
         for (int i = 0; i < NS; ++i) {
@@ -786,7 +789,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
         }
       }
       if (!first_half) {
-        if (kStrong) frob = frob_in;
+        if (kStrong && !kCarried) frob = frob_in;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) frob += __shfl_xor(frob, d);
         if (lane == 0) sF[w] = frob;
@@ -906,7 +909,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(DeltaArgs A) {
           if (16 * (i0 + i) + 4 * g < m.dk) put_grads(at + 16 * (i0 + i), dqa[i], dka[i]);
       }
     };
-    if constexpr (TL::kBf) {
+    if constexpr (!kCarried) {
       if (A.dlog && __any(log2_decay < -0.72f)) finish(std::true_type());       // uniform: log2 of exp(-1/2)
       else finish(std::false_type());
     } else {
